@@ -63,6 +63,7 @@ extern "C" {
 #define Q8_ERR_DEVICE_TIMEOUT 5  /* a bounded on-device wait ran out (reported by q8_check) */
 #define Q8_ERR_CUDA           6  /* another CUDA runtime error (stream sync, symbol copy) */
 #define Q8_ERR_TOO_BIG        7  /* the request needs more than the fixed scratch of q8_0_gemm_noalloc */
+#define Q8_ERR_DATA           8  /* a length, page, slot, parent or path read on the device is out of range (reported by q8_check) */
 
 /* Recommended number of plane rows for `rows` tokens: rows rounded up to a
  * multiple of 128 (the GEMM's token tile).  Any rows_pad >= rows is accepted
@@ -480,9 +481,175 @@ Q8_API int q8_0_gemm_mma(const void *w, int64_t n, int64_t k,
                          float *y, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Paged key/value cache and the attention that reads it: the step between the
+ * q/k/v projections and the o projection, for single tokens, for trees of
+ * drafted tokens that a batch-of-tokens step verifies, and for prompts.
+ *
+ * A sequence holds `cached` tokens from earlier steps and gets `fresh` new
+ * ones in this step.  Token `pos` of sequence b lives in page
+ * table[b][pos / page_size], at offset pos % page_size.  The fresh rows of all
+ * sequences lie one after another: those of sequence b are rows
+ * starts[b] .. starts[b + 1] - 1 of q, k, v, y, slots, masks and positions.
+ *
+ * The lengths, tables and masks are device data, so one captured graph serves
+ * every step of the same capacity.  The kernels check each value they read
+ * before it becomes an address: a sequence or slot that is out of range is
+ * skipped (its outputs keep what they held) and q8_check reports Q8_ERR_DATA.
+ * ---------------------------------------------------------------------------
+ */
+#define Q8_KV_F16  1   /* k, v hold f16 values */
+#define Q8_KV_INT8 2   /* k, v hold int8 codes; k_scale, v_scale one f32 per (token, head): value = code * scale */
+#define Q8_TREE_MAX_NODES 64   /* drafted tokens of a sequence with tree masks (one 64-bit word per token) */
+#define Q8_KV_MAX_BATCH 4096   /* sequences of one call */
+
+typedef struct q8_kv_cache {
+    void *k, *v;              /* [layers][n_pages][kv_heads][page_size][head_dim] */
+    float *k_scale, *v_scale; /* [layers][n_pages][kv_heads][page_size] for Q8_KV_INT8, else NULL */
+    int64_t layers, n_pages;
+    int32_t kv_heads;         /* 1 .. 1024 */
+    int32_t page_size;        /* tokens per page, a multiple of 16 */
+    int32_t head_dim;         /* 64 or 128 */
+    int32_t dtype;            /* Q8_KV_F16 or Q8_KV_INT8 */
+} q8_kv_cache;
+/* n_pages * kv_heads * page_size < 2^31.  A page's tokens of one head are
+ * contiguous, so attention streams whole 16-token rows of a head. */
+
+/*
+ * q8_kv_plan -- the integers of one step, from the request lengths.
+ *   cached, fresh : int32 [batch] (inputs)
+ *   held          : int32 [batch] (input) pages each table row holds already,
+ *                   or NULL for ceil(cached / page_size).  They differ after
+ *                   q8_kv_accept kept fewer tokens than the step had pages for.
+ *   free_pages    : int32 [n_free] page ids to hand out, in this order (input;
+ *                   may be NULL when n_free is 0)
+ *   table         : int32 [batch][max_pages] (in and out: the entries for the
+ *                   pages that the fresh tokens open are written, all others
+ *                   are left as they are)
+ *   parents       : int32 [tokens] or NULL.  With parents, sequence b's fresh
+ *                   tokens are the nodes of a draft tree: parents[starts[b]+i]
+ *                   is the parent's index j < i in the same sequence, or -1 for a
+ *                   node that follows the last cached token; fresh <=
+ *                   Q8_TREE_MAX_NODES.  Without, they are a chain.
+ *   tokens        : capacity of the per-token arrays (tokens >= the sum of
+ *                   fresh; a larger one is for graphs of a fixed size)
+ *   starts        : int32 [batch + 1] (output) exclusive sums of fresh
+ *   slots         : int32 [tokens] (output) page * page_size + offset of each
+ *                   fresh token; -1 where the free pages ran out, and for
+ *                   every row behind the last sequence
+ *   positions     : int32 [tokens] (output): cached + the node's depth (its
+ *                   place in the text); rows behind the last sequence are left
+ *   masks         : int64 [tokens] (output, required with parents and NULL
+ *                   without): bit j set when node j is the node itself or one of
+ *                   its ancestors; rows behind the last sequence are left
+ *   needed        : int32 [1] (output) pages this step opens.  Pages are
+ *                   handed out by sequence, then by position; needed > n_free
+ *                   says that the tokens from the first missing page on have
+ *                   slot -1.
+ *   held_out      : int32 [batch] (output) pages each row needs now, the next
+ *                   step's `held`; or NULL
+ * Sequence b opens pages held .. ceil((cached+fresh)/page_size) - 1.  Running
+ * the call again on the same inputs writes the same.
+ * Q8_ERR_DATA: a negative length, fewer pages held than cached tokens need, a page id outside [0, n_pages), a table
+ * narrower than cached + fresh, more fresh tokens than `tokens` or than
+ * Q8_TREE_MAX_NODES with parents, a parent outside [-1, i).  The slots of the
+ * tokens concerned are -1 and their masks 0.
+ * Q8_ERR_ARG: batch outside 1..Q8_KV_MAX_BATCH, tokens < 1, page_size not a
+ * positive multiple of 16, n_pages * page_size >= 2^31, masks without parents.
+ */
+Q8_API int q8_kv_plan(const int32_t *cached, const int32_t *fresh, int64_t batch, const int32_t *held,
+                      const int32_t *free_pages, int64_t n_free, int32_t *table, int64_t max_pages,
+                      int64_t page_size, int64_t n_pages, const int32_t *parents, int64_t tokens,
+                      int32_t *starts, int32_t *slots, int32_t *positions, int64_t *masks,
+                      int32_t *needed, int32_t *held_out, void *stream);
+
+/*
+ * q8_kv_append -- write the k and v rows of a step's tokens into the cache.
+ *   cache, layer : cache descriptor (read during the call) and the layer
+ *   k, v         : f32 [tokens][kv_heads * head_dim] (inputs, as the k and v
+ *                  projections write them)
+ *   slots        : int32 [tokens] (q8_kv_plan's); a token with a negative slot
+ *                  is skipped, one with a slot past the cache too
+ *                  (Q8_ERR_DATA).  Slots are distinct.
+ * Q8_KV_F16: each value rounded to f16 (nearest even; past 65504 to infinity).
+ * Q8_KV_INT8: per (token, head) row d = amax/127 in f32, code = rint(x * (1/d))
+ * clamped to +-127, as a q8_0 block of head_dim values but with its scale kept
+ * in f32.  One scale per row, not per 32 values: in the attention a k row's
+ * scale multiplies a score and a v row's scale a softmax weight, so the codes
+ * enter the tensor core as they are.  A row that holds a NaN or an infinity
+ * gets a scale that is one.  tokens * kv_heads < 2^29.
+ */
+Q8_API int q8_kv_append(const q8_kv_cache *cache, int64_t layer, const float *k, const float *v,
+                        const int32_t *slots, int64_t tokens, void *stream);
+
+/*
+ * q8_tree_attention -- attention of the fresh tokens over their sequences:
+ *     y[t][h] = sum_j softmax_j(scale * q[t][h] . k[j]) v[j]
+ * over the tokens j of t's sequence that t can see: every cached one, and of
+ * the fresh ones (already appended) those whose bit is set in masks[t], or,
+ * when masks is NULL, those not after t.  Query head h reads key/value head
+ * h / (heads / kv_heads).  A row that sees nothing gives 0.
+ *   q        : f32 [tokens][heads * head_dim] (input)
+ *   heads    : a multiple of kv_heads, at most 64 query heads per key/value head
+ *   scale    : f32, usually 1/sqrt(head_dim)
+ *   table, max_pages, cached, starts, batch : as q8_kv_plan wrote them
+ *   masks    : int64 [tokens] or NULL
+ *   tokens   : rows of q and y (rows at and past starts[batch] are neither read
+ *              nor written)
+ *   max_fresh, max_len : host bounds: the most fresh tokens of a sequence
+ *              (<= tokens; <= Q8_TREE_MAX_NODES with masks) and the most
+ *              cached + fresh.  A sequence past a bound is skipped (Q8_ERR_DATA).
+ *   y        : f32 [tokens][heads * head_dim] (output), or NULL
+ *   qs, ds   : q8_0 plane of y (rows at least `tokens`; rows past the last
+ *              fresh one are not written), or both NULL.  Exactly the encoding
+ *              of the f32 values y holds or would hold: the input of the o
+ *              projection, as rmsnorm_quant and swiglu_quant produce theirs.
+ *   workspace, workspace_bytes : device scratch of at least
+ *              q8_tree_attention_workspace_bytes(...) bytes, 16-byte aligned;
+ *              contents ignored on entry.  Two calls, or two captured graphs,
+ *              may share one only if they are ordered on one stream.
+ * Precision: q enters the tensor cores as the sum of two f16 parts of its row
+ * scaled by a power of two (22 bits of the row's largest value), softmax
+ * weights likewise, keys and values exactly as the cache holds them; products
+ * accumulate in f32, statistics in f32.  Results are run-to-run identical.
+ * A token that a row cannot see never enters its result, whatever it holds.  A
+ * NaN or an infinity in a row's q makes the row NaN; one in a value that the
+ * row sees makes what it enters non-finite (a score of -inf has weight 0).
+ * Q8_ERR_ARG: a NULL pointer, layer or size out of range, neither y nor a
+ * plane, one of qs and ds alone, a short workspace.
+ */
+Q8_API size_t q8_tree_attention_workspace_bytes(const q8_kv_cache *cache, int64_t heads, int64_t max_fresh);
+Q8_API int q8_tree_attention(const q8_kv_cache *cache, int64_t layer, const float *q, int64_t heads, float scale,
+                             const int32_t *table, int64_t max_pages, const int32_t *cached, const int32_t *starts,
+                             int64_t batch, const int64_t *masks, int64_t tokens, int64_t max_fresh,
+                             int64_t max_len, float *y, int8_t *qs, uint32_t *ds, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * q8_kv_accept -- keep the verified path of each sequence's draft tree: its
+ * tokens' k and v, in every layer, move to the slots right behind the cached
+ * tokens, in the order of the path.
+ *   table, max_pages, cached, fresh, batch : as for the step (inputs)
+ *   paths    : int32 [batch][width] indices of accepted fresh tokens, strictly
+ *              increasing in each row's first counts[b] entries (a path from the
+ *              root through a tree is)
+ *   counts   : int32 [batch], 0 .. min(width, fresh)
+ *   lens     : int32 [batch] (output) cached + counts: the next step's cached
+ * width 1..Q8_TREE_MAX_NODES.  k/v of token cached + paths[b][j] are copied to
+ * token cached + j; other slots are left.  The pages behind the new length stay
+ * in the table: give the next q8_kv_plan the step's held_out as `held`, and it
+ * does not open them again.  A sequence with a bad path, count or page is left
+ * as it is with lens = cached (Q8_ERR_DATA).
+ */
+Q8_API int q8_kv_accept(const q8_kv_cache *cache, const int32_t *table, int64_t max_pages, const int32_t *cached,
+                        const int32_t *fresh, int64_t batch, const int32_t *paths, const int32_t *counts,
+                        int64_t width, int32_t *lens, void *stream);
+
+/*
  * q8_check -- synchronise `stream`, then read and clear the library's device
  * error word.  Returns Q8_OK, Q8_ERR_DEVICE_TIMEOUT if a bounded on-device
- * wait ran out since the last check (the affected outputs are undefined), or
+ * wait ran out since the last check (the affected outputs are undefined),
+ * Q8_ERR_DATA if the key/value cache calls met a value out of range, or
  * Q8_ERR_CUDA if the synchronisation itself failed.
  */
 Q8_API int q8_check(void *stream);

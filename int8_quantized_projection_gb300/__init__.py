@@ -35,6 +35,15 @@ from ._binding import (  # noqa: F401
     q4a_gemv_batched,
     q4a_gemv_batched_grouped,
     GEMV_MAX_TOKENS,
+    KV_MAX_BATCH,
+    TREE_MAX_NODES,
+    KvCache,
+    empty_kv_cache,
+    q8_kv_accept,
+    q8_kv_append,
+    q8_kv_plan,
+    q8_tree_attention,
+    q8_tree_attention_workspace_bytes,
     q8_check,
     q8_num_sms,
     q8_plane_rows,

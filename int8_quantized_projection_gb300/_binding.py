@@ -18,7 +18,7 @@ _lock = threading.Lock()
 _lib = None
 
 STATUS_NAMES = {0: "Q8_OK", 1: "Q8_ERR_ARG", 2: "Q8_ERR_ALIGN", 3: "Q8_ERR_DEVICE", 4: "Q8_ERR_LAUNCH",
-                5: "Q8_ERR_DEVICE_TIMEOUT", 6: "Q8_ERR_CUDA", 7: "Q8_ERR_TOO_BIG"}
+                5: "Q8_ERR_DEVICE_TIMEOUT", 6: "Q8_ERR_CUDA", 7: "Q8_ERR_TOO_BIG", 8: "Q8_ERR_DATA"}
 
 # (name, restype, argtypes) of every symbol include/q8proj.h declares.
 _P = ctypes.c_void_p
@@ -48,12 +48,21 @@ SIGNATURES = {
     "q4a_gemv": (_INT, [_P, _I64, _I64, _P, _P, _P, _P]),
     "q4a_gemv_batched": (_INT, [_P, _I64, _I64, _P, _P, _I64, _P, _P]),
     "q4a_gemv_batched_grouped": (_INT, [_P, _INT, _I64, _P, _P, _I64, _P]),
+    "q8_kv_plan": (_INT, [_P, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P]),
+    "q8_kv_append": (_INT, [_P, _I64, _P, _P, _P, _I64, _P]),
+    "q8_tree_attention_workspace_bytes": (ctypes.c_size_t, [_P, _I64, _I64]),
+    "q8_tree_attention": (_INT, [_P, _I64, _P, _I64, ctypes.c_float, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _P,
+                                 _P, _P, ctypes.c_size_t, _P]),
+    "q8_kv_accept": (_INT, [_P, _P, _I64, _P, _P, _I64, _P, _P, _I64, _P, _P]),
     "q8_check": (_INT, [_P]),
     "q8_num_sms": (_INT, []),
 }
 
 
 MAX_GROUP = 8
+KV_F16, KV_INT8 = 1, 2
+TREE_MAX_NODES = 64
+KV_MAX_BATCH = 4096
 GEMV_MAX_TOKENS = 16
 PRODUCER_QUANT, PRODUCER_RMSNORM, PRODUCER_SWIGLU = 1, 2, 3
 
@@ -62,6 +71,46 @@ class GemvProj(ctypes.Structure):
     """C struct q8_gemv_proj: one projection of a grouped GEMV."""
 
     _fields_ = [("w", ctypes.c_void_p), ("n", ctypes.c_int64), ("y", ctypes.c_void_p)]
+
+
+class KvCacheDesc(ctypes.Structure):
+    """C struct q8_kv_cache."""
+
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("layers", _I64), ("n_pages", _I64),
+                ("kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class KvCache:
+    """A paged key/value cache: the caller's tensors and the descriptor the calls take.
+
+    ``k``, ``v``: f16, or int8 codes, [layers][n_pages][kv_heads][page_size][head_dim]; ``k_scale``,
+    ``v_scale``: f32 [layers][n_pages][kv_heads][page_size], with int8 only.  :func:`empty_kv_cache` makes one."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "desc", "ref")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+
+        if k.dim() != 5 or v.shape != k.shape:
+            raise ValueError("k, v: expected two [layers][n_pages][kv_heads][page_size][head_dim] tensors")
+        if k.dtype not in (torch.float16, torch.int8):
+            raise ValueError(f"k: expected float16 or int8, got {k.dtype}")
+        int8 = k.dtype == torch.int8
+        _need(k, k.dtype, "k"), _need(v, k.dtype, "v")
+        if v.device != k.device or int8 != (k_scale is not None) or int8 != (v_scale is not None):
+            raise ValueError("k and v on one device; k_scale and v_scale with int8 and only then")
+        if int8:
+            for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                _need(t, torch.float32, n)
+                if t.shape != k.shape[:-1] or t.device != k.device:
+                    raise ValueError(f"{n}: expected [layers][n_pages][kv_heads][page_size] beside k")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        layers, n_pages, kv_heads, page, dim = k.shape
+        self.desc = KvCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if int8 else None,
+                                v_scale.data_ptr() if int8 else None, layers, n_pages, kv_heads, page, dim,
+                                KV_INT8 if int8 else KV_F16)
+        self.ref = ctypes.cast(ctypes.pointer(self.desc), _P)
 
 
 class Q8Error(RuntimeError):
@@ -533,6 +582,151 @@ def q8_0_gemm_mma(w, n: int, k: int, qs, ds, t: int, y, stream=None, bind=False)
     if w.numel() != n * (k // 32) * 34 or y.numel() < t * n or qs.shape[-1] != k or ds.shape[0] != rows_pad:
         raise ValueError("shape mismatch")
     return _launch("q8_0_gemm_mma", (_ptr(w), n, k, _ptr(qs), _ptr(ds), t, rows_pad, _ptr(y), _stream(stream)), bind)
+
+
+def empty_kv_cache(layers: int, n_pages: int, kv_heads: int, page_size: int, head_dim: int, int8: bool = False,
+                   device="cuda") -> KvCache:
+    """Allocate (with PyTorch) an uninitialised paged cache, f16 or int8 with f32 scales."""
+    import torch
+
+    shape = (layers, n_pages, kv_heads, page_size, head_dim)
+    dt = torch.int8 if int8 else torch.float16
+    k, v = (torch.empty(shape, dtype=dt, device=device) for _ in range(2))
+    ks, vs = (torch.empty(shape[:-1], dtype=torch.float32, device=device) if int8 else None for _ in range(2))
+    return KvCache(k, v, ks, vs)
+
+
+def _opt(t):
+    return _ptr(t) if t is not None else ctypes.c_void_p(0)
+
+
+def _need_i32(device, **tensors):
+    """Contiguous int32 CUDA tensors on one device, the current one (None passes)."""
+    import torch
+
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, which is not the current device")
+    for name, t in tensors.items():
+        if t is not None:
+            _need(t, torch.int32, name)
+            if t.device != device:
+                raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _bind_or_call(name, args, bind, keep):
+    if bind:
+        b = Bound(name, args)
+        b._keep = keep
+        return b
+    _check(name, getattr(lib(), name)(*args))
+    return None
+
+
+def q8_kv_plan(cached, fresh, free_pages, table, page_size: int, n_pages: int, starts, slots, positions, needed,
+               parents=None, masks=None, held=None, held_out=None, stream=None, bind=False):
+    """The integers of one step over a paged cache, from the request lengths.
+
+    cached, fresh int32 [batch]; free_pages int32 [n_free] ids to hand out; table int32 [batch][max_pages] (the
+    entries for newly opened pages are written); starts int32 [batch + 1], slots and positions int32 [tokens],
+    needed int32 [1] are outputs.  ``parents`` int32 [tokens] with ``masks`` int64 [tokens] (output): draft trees.
+    ``held`` int32 [batch]: pages each row has already (default ceil(cached / page_size)); ``held_out``: after the step."""
+    import torch
+
+    dev = cached.device
+    _need_i32(dev, cached=cached, fresh=fresh, free_pages=free_pages, table=table, starts=starts, slots=slots,
+              positions=positions, needed=needed, parents=parents, held=held, held_out=held_out)
+    batch, tokens = cached.numel(), slots.numel()
+    if (table.dim() != 2 or table.shape[0] != batch or fresh.numel() != batch or starts.numel() != batch + 1
+            or positions.numel() != tokens or needed.numel() != 1 or (parents is not None and parents.numel() != tokens)
+            or (held is not None and held.numel() != batch) or (held_out is not None and held_out.numel() != batch)):
+        raise ValueError("shape mismatch")
+    if masks is not None:
+        _need(masks, torch.int64, "masks")
+        if masks.numel() != tokens or masks.device != dev:
+            raise ValueError("masks: expected one int64 per token")
+    n_free = free_pages.numel() if free_pages is not None else 0
+    args = (_ptr(cached), _ptr(fresh), batch, _opt(held), _opt(free_pages if n_free else None), n_free, _ptr(table),
+            table.shape[1], page_size, n_pages, _opt(parents), tokens, _ptr(starts), _ptr(slots), _ptr(positions),
+            _opt(masks), _ptr(needed), _opt(held_out), _stream(stream))
+    return _bind_or_call("q8_kv_plan", args, bind, (cached, fresh, held, free_pages, table, parents, starts, slots,
+                                                    positions, masks, needed, held_out))
+
+
+def q8_kv_append(cache: KvCache, layer: int, k, v, slots, stream=None, bind=False):
+    """Write k, v f32 [tokens][kv_heads * head_dim] to the cache slots of one layer (int32 [tokens], < 0: skipped)."""
+    import torch
+
+    _need(k, torch.float32, "k"), _need(v, torch.float32, "v")
+    dev = cache.k.device
+    _need_i32(dev, slots=slots)
+    tokens, d = slots.numel(), cache.desc
+    if (k.numel() != tokens * d.kv_heads * d.head_dim or v.numel() != k.numel() or k.device != dev or v.device != dev):
+        raise ValueError("k, v: expected [tokens][kv_heads * head_dim] beside the cache")
+    args = (cache.ref, layer, _ptr(k), _ptr(v), _ptr(slots), tokens, _stream(stream))
+    return _bind_or_call("q8_kv_append", args, bind, (cache, k, v, slots))
+
+
+def q8_tree_attention_workspace_bytes(cache: KvCache, heads: int, max_fresh: int) -> int:
+    return int(lib().q8_tree_attention_workspace_bytes(cache.ref, heads, max_fresh))
+
+
+def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, qs=None, ds=None, masks=None,
+                      max_fresh: int = 0, max_len: int = 0, scale: float | None = None, workspace=None, stream=None,
+                      bind=False):
+    """Attention of a step's fresh tokens over the paged cache.
+
+    q f32 [tokens][heads * head_dim]; table, cached, starts as :func:`q8_kv_plan` left them; ``masks`` int64
+    [tokens] of draft trees, or None for causal.  Writes ``y`` (f32, like q; None when dead) and, with ``qs``/``ds``,
+    its q8_0 plane.  ``max_fresh`` (default tokens) and ``max_len`` (default the table's width) bound the lengths of a
+    sequence.  ``scale`` defaults to 1/sqrt(head_dim).  ``workspace``: a uint8 CUDA tensor of at least
+    q8_tree_attention_workspace_bytes(...) bytes; when None one is allocated here with PyTorch."""
+    import torch
+
+    _need(q, torch.float32, "q")
+    dev, d = cache.k.device, cache.desc
+    _need_i32(dev, table=table, cached=cached, starts=starts)
+    batch = cached.numel()
+    if q.dim() != 2 or q.device != dev or q.shape[1] % d.head_dim:
+        raise ValueError("q: expected [tokens][heads * head_dim] beside the cache")
+    tokens, heads = q.shape[0], q.shape[1] // d.head_dim
+    if table.dim() != 2 or table.shape[0] != batch or starts.numel() != batch + 1:
+        raise ValueError("shape mismatch")
+    for t, dt, n, size in ((y, torch.float32, "y", q.numel()), (qs, torch.int8, "qs", q.numel()),
+                           (ds, torch.int32, "ds", q.numel() // 32), (masks, torch.int64, "masks", tokens)):
+        if t is not None:
+            _need(t, dt, n)
+            if t.device != dev or t.numel() < size:
+                raise ValueError(f"{n}: fewer than {size} elements, or not beside the cache")
+    max_fresh = max_fresh or tokens
+    max_len = max_len or table.shape[1] * d.page_size
+    if workspace is None:
+        nbytes = q8_tree_attention_workspace_bytes(cache, heads, max_fresh)
+        if stream is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        else:  # from the pool of the stream that uses it, so that it is not handed out again too early
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _need(workspace, torch.uint8, "workspace")
+    if workspace.device != dev:
+        raise ValueError("workspace: not beside the cache")
+    args = (cache.ref, layer, _ptr(q), heads, d.head_dim ** -0.5 if scale is None else scale, _ptr(table), table.shape[1],
+            _ptr(cached), _ptr(starts), batch, _opt(masks), tokens, max_fresh, max_len, _opt(y), _opt(qs), _opt(ds),
+            _ptr(workspace), workspace.numel(), _stream(stream))
+    return _bind_or_call("q8_tree_attention", args, bind, (cache, q, table, cached, starts, masks, y, qs, ds, workspace))
+
+
+def q8_kv_accept(cache: KvCache, table, cached, fresh, paths, counts, lens, stream=None, bind=False):
+    """Move each sequence's accepted path (paths int32 [batch][width], counts int32 [batch]) to the front of its
+    fresh tokens, in every layer; lens int32 [batch] (output) = cached + counts."""
+    dev = cache.k.device
+    _need_i32(dev, table=table, cached=cached, fresh=fresh, paths=paths, counts=counts, lens=lens)
+    batch = cached.numel()
+    if (table.dim() != 2 or table.shape[0] != batch or paths.dim() != 2 or paths.shape[0] != batch
+            or any(t.numel() != batch for t in (fresh, counts, lens))):
+        raise ValueError("shape mismatch")
+    args = (cache.ref, _ptr(table), table.shape[1], _ptr(cached), _ptr(fresh), batch, _ptr(paths), _ptr(counts),
+            paths.shape[1], _ptr(lens), _stream(stream))
+    return _bind_or_call("q8_kv_accept", args, bind, (cache, table, cached, fresh, paths, counts, lens))
 
 
 def empty_plane(rows_pad: int, k: int, device="cuda"):

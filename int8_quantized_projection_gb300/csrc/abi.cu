@@ -2,13 +2,13 @@
 // q8_check, and the GEMM dispatch by shape.
 #include <mutex>
 
-#include "q8_common.cuh"
+#include "kv_common.cuh"
 
 namespace q8 {
 
 namespace {
 constexpr int kMaxDevices = 64;
-constexpr int kMaxSlots = 20;
+constexpr int kMaxSlots = 40;
 int g_sms[kMaxDevices];        // 0 = not queried yet
 int g_is103[kMaxDevices];      // 0 = unknown, 1 = yes, 2 = no
 int g_smem_set[kMaxDevices][kMaxSlots];
@@ -145,6 +145,7 @@ extern "C" const char *q8_strerror(int status)
     case Q8_ERR_LAUNCH: return "kernel launch failed";
     case Q8_ERR_DEVICE_TIMEOUT: return "a bounded on-device wait ran out";
     case Q8_ERR_CUDA: return "CUDA runtime error";
+    case Q8_ERR_DATA: return "a length, page, slot, parent or path on the device is out of range";
     case Q8_ERR_TOO_BIG: return "request exceeds the fixed scratch of the no-allocation entry point";
     default: return "unknown status";
     }
@@ -159,10 +160,13 @@ extern "C" int q8_check(void *stream)
     const int a = q8::gemv_take_error(s);
     const int b = q8::gemm_take_error(s);
     const int c = q8::quant_take_error(s);
-    if (a == Q8_ERR_CUDA || b == Q8_ERR_CUDA || c == Q8_ERR_CUDA) return Q8_ERR_CUDA;
-    if (a != Q8_OK) return a;
-    if (b != Q8_OK) return b;
-    return c;
+    const int d = q8::attn_take_error(s);
+    const int e = q8::kv_take_error(s);
+    for (const int st : {a, b, c, d, e})
+        if (st == Q8_ERR_CUDA) return st;
+    for (const int st : {a, b, c, d, e})
+        if (st != Q8_OK) return st;
+    return Q8_OK;
 }
 
 namespace q8 {

@@ -1,0 +1,223 @@
+// attn_common.cuh -- what the kernels of q8_tree_attention share: the
+// arguments, the split of the work over CTAs, visibility and the epilogue.
+//
+// Rows.  The `group` query heads that read one key/value head are packed with
+// the fresh tokens of a sequence into one list of rows, row r = token r/group,
+// head r%group, so a key that is loaded serves all of them.  A unit is a tile
+// of kRows such rows of one (sequence, key/value head); its cost is the number
+// of kTile-key tiles the last row of the tile can see.
+//
+// Split.  All units' tiles lie on one line, in the order (sequence, head, row
+// tile), and each CTA takes an equal stretch of it: a long context is spread
+// over many CTAs and short ones share one, whatever the mix of lengths, and
+// no CTA has more than one tile above the mean.  Only the lengths on the device
+// decide, so a captured graph stays balanced as the contexts grow.  A unit
+// that crosses a boundary leaves one partial (m, l, O) per piece in the
+// workspace (a CTA has two at most: its first and its last) and
+// attn_combine_kernel joins them in the order of the line.
+#pragma once
+
+#include "kv_common.cuh"
+
+namespace q8 {
+
+struct AttnArgs {
+    const float *q;
+    const int32_t *table, *cached, *starts;
+    const long long *masks;
+    const float *ks, *vs;  // this layer's scales (int8)
+    const uint16_t *v16;   // this layer's v as f16 bits (the rare path for non-finite values)
+    float *y;
+    int8_t *qs;
+    uint32_t *ds;
+    float *part;           // [2 * grid][rows][D] partial numerators
+    float2 *ml;            // [2 * grid][rows] partial (m, l)
+    int4 *desc;            // [2 * grid] the first piece of each CTA
+    long long tokens;
+    int batch, heads, kv_heads, group, max_pages, page, n_pages, max_fresh, max_len;
+    float scale;           // softmax scale * log2(e)
+};
+
+struct Unit {
+    int b, kvh, rt;      // sequence, key/value head, row tile
+    int tiles;           // its cost
+    int start;           // its place on the line
+    int cached, fresh, first;  // the sequence's lengths and first row of q
+    bool masks;
+};
+
+// Keys that rows [0, r_end) of a sequence's packed rows can see at most.
+__device__ __forceinline__ int attn_visible(const AttnArgs &a, int cached, int fresh, int r_end)
+{
+    if (a.masks) return cached + fresh;
+    return cached + min(fresh, (r_end - 1) / a.group + 1);
+}
+
+// Lengths of sequence b; fresh = 0 (no work) when a value is out of range.
+__device__ __forceinline__ bool attn_sequence(const AttnArgs &a, int b, int &cached, int &fresh, int &first)
+{
+    cached = a.cached[b];
+    first = a.starts[b];
+    const long long f = static_cast<long long>(a.starts[b + 1]) - first;
+    const long long len = f + cached;
+    if (f < 0 || f > a.max_fresh || first < 0 || first + f > a.tokens || cached < 0 || len > a.max_len ||
+        (len + a.page - 1) / a.page > a.max_pages) {
+        fresh = 0;
+        return false;
+    }
+    fresh = static_cast<int>(f);
+    return true;
+}
+
+// The line: pre[b] = tiles of the sequences before b (pre[batch] = all).  All
+// threads of the CTA call it; ends with a barrier.  False when a sequence is
+// out of range.
+template <int kRows, int kTile, int kThreads>
+__device__ __forceinline__ bool attn_line(const AttnArgs &a, int *pre)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rts = (a.max_fresh * a.group + kRows - 1) / kRows;
+    bool ok = true;
+    if (rts <= 8) {  // a thread per sequence
+        for (int b = tid; b < a.batch; b += kThreads) {
+            int cached, fresh, first, sum = 0;
+            ok &= attn_sequence(a, b, cached, fresh, first);
+            for (int r = 0; r < fresh * a.group; r += kRows)
+                sum += (attn_visible(a, cached, fresh, min(r + kRows, fresh * a.group)) + kTile - 1) / kTile;
+            pre[b + 1] = sum * a.kv_heads;
+        }
+    } else {  // prompts: a warp per sequence
+        for (int b = warp; b < a.batch; b += kThreads / 32) {
+            int cached, fresh, first, sum = 0;
+            ok &= attn_sequence(a, b, cached, fresh, first);
+            for (int r = lane * kRows; r < fresh * a.group; r += 32 * kRows)
+                sum += (attn_visible(a, cached, fresh, min(r + kRows, fresh * a.group)) + kTile - 1) / kTile;
+            sum = __reduce_add_sync(Q8_FULL_MASK, sum);
+            if (lane == 0) pre[b + 1] = sum * a.kv_heads;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int run = 0;
+        for (int b0 = 0; b0 < a.batch; b0 += 32) {
+            int v = b0 + lane < a.batch ? pre[b0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(Q8_FULL_MASK, v, o);
+                if (lane >= o) v += x;
+            }
+            if (b0 + lane < a.batch) pre[b0 + lane + 1] = run + v;
+            run += __shfl_sync(Q8_FULL_MASK, v, 31);
+        }
+        if (lane == 0) pre[0] = 0;
+    }
+    __syncthreads();
+    return ok;
+}
+
+// The unit at place `pos` of the line.
+template <int kRows, int kTile>
+__device__ __forceinline__ Unit attn_unit(const AttnArgs &a, const int *pre, int pos)
+{
+    int lo = 0, hi = a.batch;  // pre[lo] <= pos < pre[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= pos) lo = mid; else hi = mid;
+    }
+    Unit u;
+    u.b = lo;
+    attn_sequence(a, lo, u.cached, u.fresh, u.first);
+    const int per_head = (pre[lo + 1] - pre[lo]) / a.kv_heads;
+    u.kvh = (pos - pre[lo]) / per_head;
+    u.start = pre[lo] + u.kvh * per_head;
+    const int rows = u.fresh * a.group;
+    u.rt = 0;
+    if (a.masks) {
+        u.tiles = (u.cached + u.fresh + kTile - 1) / kTile;
+        u.rt = (pos - u.start) / u.tiles;
+        u.start += u.rt * u.tiles;
+    } else {
+        for (;; ++u.rt) {
+            u.tiles = (attn_visible(a, u.cached, u.fresh, min((u.rt + 1) * kRows, rows)) + kTile - 1) / kTile;
+            if (pos < u.start + u.tiles || (u.rt + 1) * kRows >= rows) break;
+            u.start += u.tiles;
+        }
+    }
+    return u;
+}
+
+// What one packed row can see: keys below `all`, and of the fresh ones those
+// set in `mask`.
+struct RowSight {
+    int all;
+    unsigned long long mask;
+};
+
+__device__ __forceinline__ RowSight attn_sight(const AttnArgs &a, const Unit &u, int row)
+{
+    RowSight s;
+    const int tok = row / a.group;
+    if (tok >= u.fresh) {  // a row of the tile that does not exist
+        s.all = 0;
+        s.mask = 0;
+    } else if (a.masks) {
+        s.all = u.cached;
+        s.mask = static_cast<unsigned long long>(a.masks[u.first + tok]);
+        if (u.fresh < 64) s.mask &= (1ull << u.fresh) - 1;
+    } else {
+        s.all = u.cached + tok + 1;
+        s.mask = 0;
+    }
+    return s;
+}
+
+__device__ __forceinline__ bool attn_sees(const RowSight &s, int cached, int key)
+{
+    const unsigned f = static_cast<unsigned>(key - cached);
+    return key < s.all || (f < 64u && ((s.mask >> f) & 1));
+}
+
+// Four consecutive values of a finished row (the 8 lanes of an aligned group
+// of 8 hold 32 consecutive ones): y and the plane.  All lanes of the warp
+// call it; `valid` says whether this lane's row exists.
+template <int D>
+__device__ __forceinline__ void attn_store(const AttnArgs &a, const Unit &u, int row, int c, float4 o, float l,
+                                           bool valid)
+{
+    // a row that saw nothing has l = 0 and O = 0
+    const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
+    const float4 r = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    const int tok = row / a.group;
+    const long long at =
+        (static_cast<long long>(u.first + tok) * a.heads + u.kvh * a.group + (row - tok * a.group)) * D + c;
+    if (a.y && valid) *reinterpret_cast<float4 *>(a.y + at) = r;
+    if (a.qs) {
+        const Q8Enc e = q8_encode8(r);
+        if (valid) {
+            *reinterpret_cast<uint32_t *>(a.qs + at) = e.qword;
+            if ((c & 31) == 0) a.ds[at / 32] = e.dsword;
+        }
+    }
+}
+
+// A query value in two f16 parts: hi + lo is v to 22 bits (|v| < 2^15).
+__device__ __forceinline__ void split_f16(float a, float b, uint32_t &hi, uint32_t &lo)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 2^e for e in [-126, 127]
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+} // namespace q8

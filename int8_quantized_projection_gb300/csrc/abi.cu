@@ -2,7 +2,7 @@
 // q8_check, and the GEMM dispatch by shape.
 #include <mutex>
 
-#include "kv_common.cuh"
+#include "attn_common.cuh"
 
 namespace q8 {
 
@@ -160,11 +160,12 @@ extern "C" int q8_check(void *stream)
     const int a = q8::gemv_take_error(s);
     const int b = q8::gemm_take_error(s);
     const int c = q8::quant_take_error(s);
-    const int d = q8::attn_take_error(s);
-    const int e = q8::kv_take_error(s);
-    for (const int st : {a, b, c, d, e})
+    const int d = q8::attn_rows_take_error(s);
+    const int e = q8::attn_tiles_take_error(s);
+    const int f = q8::kv_take_error(s);
+    for (const int st : {a, b, c, d, e, f})
         if (st == Q8_ERR_CUDA) return st;
-    for (const int st : {a, b, c, d, e})
+    for (const int st : {a, b, c, d, e, f})
         if (st != Q8_OK) return st;
     return Q8_OK;
 }

@@ -43,7 +43,6 @@ struct Unit {
     int tiles;           // its cost
     int start;           // its place on the line
     int cached, fresh, first;  // the sequence's lengths and first row of q
-    bool masks;
 };
 
 // Keys that rows [0, r_end) of a sequence's packed rows can see at most.
@@ -115,7 +114,15 @@ __device__ __forceinline__ bool attn_line(const AttnArgs &a, int *pre)
     return ok;
 }
 
-// The unit at place `pos` of the line.
+// Tiles of row tile rt of a sequence.
+template <int kRows, int kTile>
+__device__ __forceinline__ int attn_tiles_of(const AttnArgs &a, int cached, int fresh, int rt)
+{
+    return (attn_visible(a, cached, fresh, min((rt + 1) * kRows, fresh * a.group)) + kTile - 1) / kTile;
+}
+
+// The unit at place `pos` of the line; all lanes of a warp call it and get it
+// (causal row tiles differ in cost: the lanes add up 32 of them at a time).
 template <int kRows, int kTile>
 __device__ __forceinline__ Unit attn_unit(const AttnArgs &a, const int *pre, int pos)
 {
@@ -130,20 +137,53 @@ __device__ __forceinline__ Unit attn_unit(const AttnArgs &a, const int *pre, int
     const int per_head = (pre[lo + 1] - pre[lo]) / a.kv_heads;
     u.kvh = (pos - pre[lo]) / per_head;
     u.start = pre[lo] + u.kvh * per_head;
-    const int rows = u.fresh * a.group;
+    const int rts = (u.fresh * a.group + kRows - 1) / kRows, lane = threadIdx.x & 31;
     u.rt = 0;
+    u.tiles = attn_tiles_of<kRows, kTile>(a, u.cached, u.fresh, 0);
     if (a.masks) {
-        u.tiles = (u.cached + u.fresh + kTile - 1) / kTile;
         u.rt = (pos - u.start) / u.tiles;
         u.start += u.rt * u.tiles;
-    } else {
-        for (;; ++u.rt) {
-            u.tiles = (attn_visible(a, u.cached, u.fresh, min((u.rt + 1) * kRows, rows)) + kTile - 1) / kTile;
-            if (pos < u.start + u.tiles || (u.rt + 1) * kRows >= rows) break;
-            u.start += u.tiles;
+    } else if (rts > 1) {
+        for (int r0 = 0; r0 < rts; r0 += 32) {
+            const int mine = r0 + lane < rts ? attn_tiles_of<kRows, kTile>(a, u.cached, u.fresh, r0 + lane) : 0;
+            int v = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(Q8_FULL_MASK, v, o);
+                if (lane >= o) v += x;
+            }
+            const unsigned past = __ballot_sync(Q8_FULL_MASK, pos < u.start + v);
+            const int at = past ? __ffs(past) - 1 : 31;
+            u.tiles = __shfl_sync(Q8_FULL_MASK, mine, at);
+            u.rt = r0 + at;
+            const int end = __shfl_sync(Q8_FULL_MASK, v, at);
+            if (past || r0 + 32 >= rts) {
+                u.start += end - u.tiles;
+                break;
+            }
+            u.start += end;
         }
     }
     return u;
+}
+
+// The unit behind u on the line (u is not the last).
+template <int kRows, int kTile>
+__device__ __forceinline__ void attn_next_unit(const AttnArgs &a, const int *pre, Unit &u)
+{
+    u.start += u.tiles;
+    if ((u.rt + 1) * kRows < u.fresh * a.group) {
+        ++u.rt;
+    } else {
+        u.rt = 0;
+        if (++u.kvh == a.kv_heads) {
+            u.kvh = 0;
+            do ++u.b;
+            while (u.b + 1 < a.batch && pre[u.b + 1] <= u.start);  // empty sequences take no place
+            attn_sequence(a, u.b, u.cached, u.fresh, u.first);
+        }
+    }
+    u.tiles = attn_tiles_of<kRows, kTile>(a, u.cached, u.fresh, u.rt);
 }
 
 // What one packed row can see: keys below `all`, and of the fresh ones those
@@ -219,5 +259,62 @@ __device__ __forceinline__ float exp2_approx(float x)
 
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+constexpr int kAttnCtas = 152;  // the split is over this many CTAs whatever the device's count: results do not depend on it
+
+// One call's attention as the launchers take it.
+struct AttnCall {
+    AttnArgs a;
+    const uint8_t *k, *v;  // this layer
+    int64_t layer_rows;
+    int dim;
+    bool int8;
+};
+
+// rows of a unit: 8 or 16 (attn_rows.cu), 128 (attn_tiles.cu)
+int attn_rows_launch(const AttnCall &c, int rows, cudaStream_t s);
+int attn_rows_take_error(cudaStream_t s);
+int attn_tiles_launch(const AttnCall &c, cudaStream_t s);
+int attn_tiles_take_error(cudaStream_t s);
+
+// Joins the pieces of every unit that crosses a boundary of the split: CTA c
+// takes the unit that lies across the start of c's stretch, unless an earlier
+// boundary lies in the same unit.  Pieces are added in the order of the line.
+template <int D, int kRows>
+static __global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant__ AttnArgs a)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int c = blockIdx.x + 1;
+    const int4 d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
+    if (d1.w == 0) return;
+    const int u0 = d0.x, u1 = d0.y, per = d0.z;
+    if (c * per <= u0 || (c - 1) * per > u0) return;
+    const int head = 2 * (c - 1) + ((c - 1) * per == u0 ? 0 : 1);
+    const int pieces = 1 + (u1 - 1) / per - c + 1;  // CTAs c .. (u1 - 1) / per, and c - 1
+    Unit u;
+    u.b = d1.x, u.kvh = d1.y, u.rt = d1.z;
+    attn_sequence(a, u.b, u.cached, u.fresh, u.first);
+    const int rows = u.fresh * a.group;
+    for (int i = blockIdx.y * 256 + threadIdx.x; i < kRows * D / 4; i += 256 * gridDim.y) {
+        const int r = i / (D / 4), col = (i % (D / 4)) * 4;
+        auto at = [&](int k) { return k == 0 ? head : 2 * (c + k - 1); };
+        float m = -INFINITY;
+#pragma unroll 8
+        for (int k = 0; k < pieces; ++k) m = fmaxf(m, a.ml[at(k) * kRows + r].x);
+        float l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int k = 0; k < pieces; ++k) {
+            const float2 ml = a.ml[at(k) * kRows + r];
+            const float4 x =
+                *reinterpret_cast<const float4 *>(a.part + (static_cast<long long>(at(k)) * kRows + r) * D + col);
+            const float f = ml.x == -INFINITY ? 0.0f : ml.x == m ? 1.0f : exp2_approx(ml.x - m);
+            l += f * ml.y;
+            o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+        }
+        attn_store<D>(a, u, u.rt * kRows + r, col, o, l, u.rt * kRows + r < rows);
+    }
+}
 
 } // namespace q8

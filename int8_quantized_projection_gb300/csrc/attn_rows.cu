@@ -28,11 +28,9 @@
 
 #include "attn_common.cuh"
 
-namespace q8 {
-__device__ unsigned int g_attn_err;
-}
-
 namespace {
+
+__device__ unsigned int g_rows_err;
 
 using q8::AttnArgs;
 using q8::Unit;
@@ -182,8 +180,10 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 
     int slot = 0, phase = 0, wslot = 0;  // the ring: next to read (and its parity), next to fill
     bool dead = false;
+    Unit u;
     for (int pos = s0; pos < s1;) {
-        const Unit u = q8::attn_unit<kRows, kTile>(a, pre, pos);
+        if (pos == s0) u = q8::attn_unit<kRows, kTile>(a, pre, pos);
+        else q8::attn_next_unit<kRows, kTile>(a, pre, u);
         const int t0 = pos - u.start, t1 = min(u.tiles, t0 + (s1 - pos));
         const int rows = u.fresh * a.group, row0 = u.rt * kRows;
         const int seen = q8::attn_visible(a, u.cached, u.fresh, min(row0 + kRows, rows));
@@ -287,7 +287,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     q8::mbar_wait_bounded(bars + sl, ph, Q8_DRAIN_LIMIT_NS);
                     if (++sl == R::kStages) sl = 0, ph ^= 1;
                 }
-                if (lane == 0) atomicOr(&q8::g_attn_err, q8::kKvErrTimeout);
+                if (lane == 0) atomicOr(&g_rows_err, q8::kKvErrTimeout);
                 dead = true;
                 break;
             }
@@ -509,67 +509,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             __syncthreads();
         }
     }
-    if (bad_data) atomicOr(&q8::g_attn_err, q8::kKvErrData);
+    if (bad_data) atomicOr(&g_rows_err, q8::kKvErrData);
 }
-
-// Joins the pieces of every unit that crosses a boundary of the split: CTA c
-// takes the unit that lies across the start of c's stretch, unless an earlier
-// boundary lies in the same unit.  Pieces are added in the order of the line.
-template <int D, int kRows>
-__global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant__ AttnArgs a)
-{
-    q8::griddep_launch_dependents();
-    q8::griddep_wait();
-    const int c = blockIdx.x + 1;
-    const int4 d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
-    if (d1.w == 0) return;
-    const int u0 = d0.x, u1 = d0.y, per = d0.z;
-    if (c * per <= u0 || (c - 1) * per > u0) return;
-    const int head = 2 * (c - 1) + ((c - 1) * per == u0 ? 0 : 1);
-    const int pieces = 1 + (u1 - 1) / per - c + 1;  // CTAs c .. (u1 - 1) / per, and c - 1
-    Unit u;
-    u.b = d1.x, u.kvh = d1.y, u.rt = d1.z;
-    q8::attn_sequence(a, u.b, u.cached, u.fresh, u.first);
-    const int rows = u.fresh * a.group;
-    for (int i = blockIdx.y * 256 + threadIdx.x; i < kRows * D / 4; i += 256 * gridDim.y) {
-        const int r = i / (D / 4), col = (i % (D / 4)) * 4;
-        auto at = [&](int k) { return k == 0 ? head : 2 * (c + k - 1); };
-        float m = -INFINITY;
-#pragma unroll 8
-        for (int k = 0; k < pieces; ++k) m = fmaxf(m, a.ml[at(k) * kRows + r].x);
-        float l = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int k = 0; k < pieces; ++k) {
-            const float2 ml = a.ml[at(k) * kRows + r];
-            const float4 x =
-                *reinterpret_cast<const float4 *>(a.part + (static_cast<long long>(at(k)) * kRows + r) * D + col);
-            const float f = ml.x == -INFINITY ? 0.0f : ml.x == m ? 1.0f : q8::exp2_approx(ml.x - m);
-            l += f * ml.y;
-            o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
-        }
-        q8::attn_store<D>(a, u, u.rt * kRows + r, col, o, l, u.rt * kRows + r < rows);
-    }
-}
-
-constexpr int kCtas = 152;  // the split is over this many CTAs whatever the device's count, so results do not depend on it
-
-inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-
-struct Workspace {
-    size_t ml, desc, bytes;
-};
-
-Workspace workspace(int rows, int d)
-{
-    Workspace w;
-    w.ml = up256(size_t(2) * kCtas * rows * d * 4);
-    w.desc = w.ml + up256(size_t(2) * kCtas * rows * 8);
-    w.bytes = w.desc + size_t(2) * kCtas * 16;
-    return w;
-}
-
-int rows_of(int64_t max_rows) { return max_rows <= 8 ? 8 : 16; }
 
 template <int D, bool kInt8, int RG>
 int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int slot, cudaStream_t s)
@@ -577,9 +518,9 @@ int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a,
     const int smem = Ring<D, kInt8>::smem(a.batch);
     const void *fn = reinterpret_cast<const void *>(attn_rows_kernel<D, kInt8, RG>);
     if (!q8::set_max_dynamic_smem(fn, kMaxDynamic, slot)) return Q8_ERR_LAUNCH;
-    const int st = q8::launch_pdl(attn_rows_kernel<D, kInt8, RG>, dim3(kCtas), dim3(kThreads), smem, s, mk, mv, a);
+    const int st = q8::launch_pdl(attn_rows_kernel<D, kInt8, RG>, dim3(q8::kAttnCtas), dim3(kThreads), smem, s, mk, mv, a);
     if (st != Q8_OK) return st;
-    return q8::launch_pdl(attn_combine_kernel<D, 8 * RG>, dim3(kCtas - 1, (8 * RG * D / 4 + 255) / 256), dim3(256), 0, s,
+    return q8::launch_pdl(q8::attn_combine_kernel<D, 8 * RG>, dim3(q8::kAttnCtas - 1, (8 * RG * D / 4 + 255) / 256), dim3(256), 0, s,
                           a);
 }
 
@@ -587,84 +528,35 @@ int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a,
 
 namespace q8 {
 
-int attn_take_error(cudaStream_t s)
+int attn_rows_launch(const AttnCall &c, int rows, cudaStream_t s)
+{
+    const int D = c.dim;
+    const CUtensorMapDataType dt = c.int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapSwizzle sw = c.int8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    const uint32_t box = c.int8 ? D : 64;
+    const uint64_t pitch = D * (c.int8 ? 1 : 2);
+    CUtensorMap mk, mv;
+    if (!make_map_2d(&mk, dt, c.k, D, c.layer_rows, pitch, box, 16, sw) ||
+        !make_map_2d(&mv, dt, c.v, D, c.layer_rows, pitch, box, 16, sw))
+        return Q8_ERR_CUDA;
+    if (D == 128) {
+        if (c.int8)
+            return rows == 8 ? launch_rows<128, true, 1>(mk, mv, c.a, 20, s) : launch_rows<128, true, 2>(mk, mv, c.a, 21, s);
+        return rows == 8 ? launch_rows<128, false, 1>(mk, mv, c.a, 22, s) : launch_rows<128, false, 2>(mk, mv, c.a, 23, s);
+    }
+    if (c.int8)
+        return rows == 8 ? launch_rows<64, true, 1>(mk, mv, c.a, 24, s) : launch_rows<64, true, 2>(mk, mv, c.a, 25, s);
+    return rows == 8 ? launch_rows<64, false, 1>(mk, mv, c.a, 26, s) : launch_rows<64, false, 2>(mk, mv, c.a, 27, s);
+}
+
+int attn_rows_take_error(cudaStream_t s)
 {
     unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_attn_err, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_attn_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+    if (cudaMemcpyFromSymbolAsync(&v, g_rows_err, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_rows_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
         return Q8_ERR_CUDA;
     return (v & kKvErrTimeout) ? Q8_ERR_DEVICE_TIMEOUT : v ? Q8_ERR_DATA : Q8_OK;
 }
 
 } // namespace q8
-
-static bool attn_shape_ok(const q8_kv_cache *c, int64_t heads, int64_t max_fresh)
-{
-    return heads >= 1 && heads % c->kv_heads == 0 && heads / c->kv_heads <= 64 && max_fresh >= 1 &&
-           max_fresh < (int64_t(1) << 24);
-}
-
-extern "C" size_t q8_tree_attention_workspace_bytes(const q8_kv_cache *cache, int64_t heads, int64_t max_fresh)
-{
-    if (q8::kv_cache_status(cache) == Q8_ERR_ARG || !attn_shape_ok(cache, heads, max_fresh)) return 0;
-    return workspace(rows_of(max_fresh * (heads / cache->kv_heads)), cache->head_dim).bytes;
-}
-
-extern "C" int q8_tree_attention(const q8_kv_cache *cache, int64_t layer, const float *q, int64_t heads, float scale,
-                                 const int32_t *table, int64_t max_pages, const int32_t *cached, const int32_t *starts,
-                                 int64_t batch, const int64_t *masks, int64_t tokens, int64_t max_fresh,
-                                 int64_t max_len, float *y, int8_t *qs, uint32_t *ds, void *workspace_,
-                                 size_t workspace_bytes, void *stream)
-{
-    if (!cache || !q || !table || !cached || !starts || (!y && !qs) || (qs == nullptr) != (ds == nullptr))
-        return Q8_ERR_ARG;
-    const int cst = q8::kv_cache_status(cache);
-    if (cst == Q8_ERR_ARG) return cst;
-    if (layer < 0 || layer >= cache->layers || !attn_shape_ok(cache, heads, max_fresh) || batch < 1 ||
-        batch > Q8_KV_MAX_BATCH || tokens < 1 || tokens >= (int64_t(1) << 31) || max_fresh > tokens ||
-        max_len < max_fresh || max_len >= (int64_t(1) << 31) - 4096 || max_pages < 1 ||
-        max_pages >= (int64_t(1) << 31) || (masks && max_fresh > Q8_TREE_MAX_NODES))
-        return Q8_ERR_ARG;
-    const int group = static_cast<int>(heads / cache->kv_heads);
-    const int rows = rows_of(max_fresh * group);
-    // the line of tiles is counted in 32 bits
-    const double line = double(batch) * cache->kv_heads * ((max_fresh * group + rows - 1) / rows) *
-                        ((max_len + kTile - 1) / kTile);
-    if (line > 2.0e9) return Q8_ERR_ARG;
-    const Workspace w = workspace(rows, cache->head_dim);
-    if (!workspace_ || workspace_bytes < w.bytes) return Q8_ERR_ARG;
-    if (cst != Q8_OK) return cst;
-    const void *all[] = {q, table, cached, starts, masks, y, qs, ds, workspace_};
-    for (const void *p : all)
-        if (!q8::aligned16(p)) return Q8_ERR_ALIGN;
-    if (!q8::device_is_sm103()) return Q8_ERR_DEVICE;
-
-    const int D = cache->head_dim;
-    const bool i8 = cache->dtype == Q8_KV_INT8;
-    const int64_t lr = q8::kv_layer_rows(*cache), eb = q8::kv_element_bytes(*cache);
-    const uint8_t *kp = static_cast<const uint8_t *>(cache->k) + layer * lr * D * eb;
-    const uint8_t *vp = static_cast<const uint8_t *>(cache->v) + layer * lr * D * eb;
-    CUtensorMap mk, mv;
-    const CUtensorMapDataType dt = i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    const CUtensorMapSwizzle sw = i8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-    const uint32_t box = i8 ? D : 64;
-    if (!q8::make_map_2d(&mk, dt, kp, D, lr, D * eb, box, 16, sw) ||
-        !q8::make_map_2d(&mv, dt, vp, D, lr, D * eb, box, 16, sw))
-        return Q8_ERR_CUDA;
-    uint8_t *ws = static_cast<uint8_t *>(workspace_);
-    AttnArgs a = {q, table, cached, starts, reinterpret_cast<const long long *>(masks),
-                  i8 ? cache->k_scale + layer * lr : nullptr, i8 ? cache->v_scale + layer * lr : nullptr,
-                  reinterpret_cast<const uint16_t *>(vp), y, qs, ds, reinterpret_cast<float *>(ws),
-                  reinterpret_cast<float2 *>(ws + w.ml), reinterpret_cast<int4 *>(ws + w.desc), tokens,
-                  static_cast<int>(batch), static_cast<int>(heads), cache->kv_heads, group, static_cast<int>(max_pages),
-                  cache->page_size, static_cast<int>(cache->n_pages), static_cast<int>(max_fresh),
-                  static_cast<int>(max_len), scale * 1.4426950408889634f};
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (D == 128) {
-        if (i8) return rows == 8 ? launch_rows<128, true, 1>(mk, mv, a, 20, s) : launch_rows<128, true, 2>(mk, mv, a, 21, s);
-        return rows == 8 ? launch_rows<128, false, 1>(mk, mv, a, 22, s) : launch_rows<128, false, 2>(mk, mv, a, 23, s);
-    }
-    if (i8) return rows == 8 ? launch_rows<64, true, 1>(mk, mv, a, 24, s) : launch_rows<64, true, 2>(mk, mv, a, 25, s);
-    return rows == 8 ? launch_rows<64, false, 1>(mk, mv, a, 26, s) : launch_rows<64, false, 2>(mk, mv, a, 27, s);
-}

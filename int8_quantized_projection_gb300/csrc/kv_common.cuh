@@ -39,7 +39,6 @@ inline int kv_cache_status(const q8_kv_cache *c)
 constexpr unsigned int kKvErrTimeout = 1u, kKvErrData = 2u;
 
 int kv_take_error(cudaStream_t s);
-int attn_take_error(cudaStream_t s);
 
 // max(a, b), NaN when either is.
 __device__ __forceinline__ float max_nan(float a, float b)

@@ -32,7 +32,7 @@ struct AttnArgs {
     uint32_t *ds;
     float *part;           // [2 * grid][rows][D] partial numerators
     float2 *ml;            // [2 * grid][rows] partial (m, l)
-    int4 *desc;            // [2 * grid] the first piece of each CTA
+    int4 *desc;            // [2 * grid] the first piece of each CTA, if it is a part of a unit
     long long tokens;
     int batch, heads, kv_heads, group, max_pages, page, n_pages, max_fresh, max_len;
     float scale;           // softmax scale * log2(e)
@@ -40,8 +40,8 @@ struct AttnArgs {
 
 struct Unit {
     int b, kvh, rt;      // sequence, key/value head, row tile
-    int tiles;           // its cost
-    int start;           // its place on the line
+    int tiles;           // key tiles; it costs kHead more
+    int start;           // its place on the line: kHead, then the tiles
     int cached, fresh, first;  // the sequence's lengths and first row of q
 };
 
@@ -68,10 +68,37 @@ __device__ __forceinline__ bool attn_sequence(const AttnArgs &a, int b, int &cac
     return true;
 }
 
-// The line: pre[b] = tiles of the sequences before b (pre[batch] = all).  All
+// Tiles of row tile rt of a sequence.
+template <int kRows, int kTile>
+__device__ __forceinline__ int attn_tiles_of(const AttnArgs &a, int cached, int fresh, int rt)
+{
+    return (attn_visible(a, cached, fresh, min((rt + 1) * kRows, fresh * a.group)) + kTile - 1) / kTile;
+}
+
+// Packed row -> token and head of the group, for rows of one unit: a product
+// instead of a division (exact below 1024 for groups up to 64).
+struct RowMap {
+    int row0, tok0, rem0;
+    unsigned magic;
+    int group;
+
+    __device__ __forceinline__ RowMap(const AttnArgs &a, int row0_)
+        : row0(row0_), tok0(row0_ / a.group), rem0(row0_ - tok0 * a.group), magic((65535u + a.group) / a.group), group(a.group)
+    {
+    }
+    __device__ __forceinline__ int token(int r) const { return tok0 + static_cast<int>(((rem0 + r) * magic) >> 16); }
+    // element offset of row row0 + r in q and y
+    __device__ __forceinline__ long long at(const AttnArgs &a, const Unit &u, int r, int dim) const
+    {
+        const int t = token(r);
+        return (static_cast<long long>(u.first + t) * a.heads + u.kvh * group + (row0 + r - t * group)) * dim;
+    }
+};
+
+// The line: pre[b] = cost of the sequences before b (pre[batch] = all).  All
 // threads of the CTA call it; ends with a barrier.  False when a sequence is
 // out of range.
-template <int kRows, int kTile, int kThreads>
+template <int kRows, int kTile, int kHead, int kThreads>
 __device__ __forceinline__ bool attn_line(const AttnArgs &a, int *pre)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -81,16 +108,15 @@ __device__ __forceinline__ bool attn_line(const AttnArgs &a, int *pre)
         for (int b = tid; b < a.batch; b += kThreads) {
             int cached, fresh, first, sum = 0;
             ok &= attn_sequence(a, b, cached, fresh, first);
-            for (int r = 0; r < fresh * a.group; r += kRows)
-                sum += (attn_visible(a, cached, fresh, min(r + kRows, fresh * a.group)) + kTile - 1) / kTile;
+            for (int r = 0; r * kRows < fresh * a.group; ++r) sum += attn_tiles_of<kRows, kTile>(a, cached, fresh, r) + kHead;
             pre[b + 1] = sum * a.kv_heads;
         }
     } else {  // prompts: a warp per sequence
         for (int b = warp; b < a.batch; b += kThreads / 32) {
             int cached, fresh, first, sum = 0;
             ok &= attn_sequence(a, b, cached, fresh, first);
-            for (int r = lane * kRows; r < fresh * a.group; r += 32 * kRows)
-                sum += (attn_visible(a, cached, fresh, min(r + kRows, fresh * a.group)) + kTile - 1) / kTile;
+            for (int r = lane; r * kRows < fresh * a.group; r += 32)
+                sum += attn_tiles_of<kRows, kTile>(a, cached, fresh, r) + kHead;
             sum = __reduce_add_sync(Q8_FULL_MASK, sum);
             if (lane == 0) pre[b + 1] = sum * a.kv_heads;
         }
@@ -114,16 +140,9 @@ __device__ __forceinline__ bool attn_line(const AttnArgs &a, int *pre)
     return ok;
 }
 
-// Tiles of row tile rt of a sequence.
-template <int kRows, int kTile>
-__device__ __forceinline__ int attn_tiles_of(const AttnArgs &a, int cached, int fresh, int rt)
-{
-    return (attn_visible(a, cached, fresh, min((rt + 1) * kRows, fresh * a.group)) + kTile - 1) / kTile;
-}
-
 // The unit at place `pos` of the line; all lanes of a warp call it and get it
 // (causal row tiles differ in cost: the lanes add up 32 of them at a time).
-template <int kRows, int kTile>
+template <int kRows, int kTile, int kHead>
 __device__ __forceinline__ Unit attn_unit(const AttnArgs &a, const int *pre, int pos)
 {
     int lo = 0, hi = a.batch;  // pre[lo] <= pos < pre[hi]
@@ -141,11 +160,11 @@ __device__ __forceinline__ Unit attn_unit(const AttnArgs &a, const int *pre, int
     u.rt = 0;
     u.tiles = attn_tiles_of<kRows, kTile>(a, u.cached, u.fresh, 0);
     if (a.masks) {
-        u.rt = (pos - u.start) / u.tiles;
-        u.start += u.rt * u.tiles;
+        u.rt = (pos - u.start) / (u.tiles + kHead);
+        u.start += u.rt * (u.tiles + kHead);
     } else if (rts > 1) {
         for (int r0 = 0; r0 < rts; r0 += 32) {
-            const int mine = r0 + lane < rts ? attn_tiles_of<kRows, kTile>(a, u.cached, u.fresh, r0 + lane) : 0;
+            const int mine = r0 + lane < rts ? attn_tiles_of<kRows, kTile>(a, u.cached, u.fresh, r0 + lane) + kHead : 0;
             int v = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -154,11 +173,11 @@ __device__ __forceinline__ Unit attn_unit(const AttnArgs &a, const int *pre, int
             }
             const unsigned past = __ballot_sync(Q8_FULL_MASK, pos < u.start + v);
             const int at = past ? __ffs(past) - 1 : 31;
-            u.tiles = __shfl_sync(Q8_FULL_MASK, mine, at);
+            u.tiles = __shfl_sync(Q8_FULL_MASK, mine, at) - kHead;
             u.rt = r0 + at;
             const int end = __shfl_sync(Q8_FULL_MASK, v, at);
             if (past || r0 + 32 >= rts) {
-                u.start += end - u.tiles;
+                u.start += end - u.tiles - kHead;
                 break;
             }
             u.start += end;
@@ -168,10 +187,10 @@ __device__ __forceinline__ Unit attn_unit(const AttnArgs &a, const int *pre, int
 }
 
 // The unit behind u on the line (u is not the last).
-template <int kRows, int kTile>
+template <int kRows, int kTile, int kHead>
 __device__ __forceinline__ void attn_next_unit(const AttnArgs &a, const int *pre, Unit &u)
 {
-    u.start += u.tiles;
+    u.start += u.tiles + kHead;
     if ((u.rt + 1) * kRows < u.fresh * a.group) {
         ++u.rt;
     } else {
@@ -288,9 +307,10 @@ static __global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_c
     const int c = blockIdx.x + 1;
     const int4 d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
     if (d1.w == 0) return;
-    const int u0 = d0.x, u1 = d0.y, per = d0.z;
-    if (c * per <= u0 || (c - 1) * per > u0) return;
-    const int head = 2 * (c - 1) + ((c - 1) * per == u0 ? 0 : 1);
+    // the unit's place, its end, and the place of its first tile
+    const int u0 = d0.x, u1 = d0.y, per = d0.z, f0 = d0.w;
+    if (c * per <= f0 || (c - 1) * per > f0) return;
+    const int head = 2 * (c - 1) + ((c - 1) * per >= u0 ? 0 : 1);
     const int pieces = 1 + (u1 - 1) / per - c + 1;  // CTAs c .. (u1 - 1) / per, and c - 1
     Unit u;
     u.b = d1.x, u.kvh = d1.y, u.rt = d1.z;

@@ -37,6 +37,7 @@ using q8::Unit;
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;   // keys of a tile: 16 per warp
+constexpr int kHead = 1;             // what a unit costs beside its tiles, in tiles
 constexpr float kWeightBits = 6.0f;  // weights are 2^(s - m + 6)
 constexpr float kRaise = 8.0f;       // m may lag the maximum by this
 
@@ -171,7 +172,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     q8::fence_mbar_init();
     q8::griddep_launch_dependents();
     q8::griddep_wait();
-    bool bad_data = !q8::attn_line<kRows, kTile, kThreads>(a, pre);
+    bool bad_data = !q8::attn_line<kRows, kTile, kHead, kThreads>(a, pre);
     const int total = pre[a.batch];
     const int per = max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
     const int cta = blockIdx.x;
@@ -182,9 +183,12 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     bool dead = false;
     Unit u;
     for (int pos = s0; pos < s1;) {
-        if (pos == s0) u = q8::attn_unit<kRows, kTile>(a, pre, pos);
-        else q8::attn_next_unit<kRows, kTile>(a, pre, u);
-        const int t0 = pos - u.start, t1 = min(u.tiles, t0 + (s1 - pos));
+        if (pos == s0) u = q8::attn_unit<kRows, kTile, kHead>(a, pre, pos);
+        else q8::attn_next_unit<kRows, kTile, kHead>(a, pre, u);
+        const int t0 = max(0, pos - u.start - kHead), t1 = max(0, min(u.tiles, s1 - u.start - kHead));
+        const bool first = pos == s0;
+        pos = u.start + kHead + u.tiles;
+        if (t0 >= t1) continue;  // only the unit's head: the next CTA has its tiles
         const int rows = u.fresh * a.group, row0 = u.rt * kRows;
         const int seen = q8::attn_visible(a, u.cached, u.fresh, min(row0 + kRows, rows));
         const int k0 = t0 * kTile + warp * 16, k1 = min(t1 * kTile, seen);
@@ -456,7 +460,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         }
         __syncthreads();
         const bool partial = t0 > 0 || t1 < u.tiles;
-        const int pslot = 2 * cta + (pos == s0 ? 0 : 1);
+        const int pslot = 2 * cta + (first ? 0 : 1);
         const int poison = s_poison;
         for (int i = tid; i < kRows * D / 4; i += kThreads) {
             const int r = i / (D / 4), c = (i % (D / 4)) * 4;
@@ -497,11 +501,10 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 q8::attn_store<D>(a, u, row0 + r, c, o, l, row0 + r < rows);
             }
         }
-        if (partial && pos == s0 && tid == 0) {
-            a.desc[2 * cta] = make_int4(u.start, u.start + u.tiles, per, 0);
+        if (partial && first && tid == 0) {
+            a.desc[2 * cta] = make_int4(u.start, u.start + kHead + u.tiles, per, u.start + kHead);
             a.desc[2 * cta + 1] = make_int4(u.b, u.kvh, u.rt, 1);
         }
-        pos = u.start + t1;
         if (pos < s1) {  // the ring's next copies come after these reads and writes
             q8::fence_proxy_async_smem();
             __syncthreads();

@@ -37,6 +37,7 @@ using q8::Unit;
 __device__ unsigned int g_tiles_err;
 
 constexpr int kRows = 128, kTile = 128;
+constexpr int kHead = 3;             // what a unit costs beside its tiles, in tiles
 constexpr float kWeightBits = 6.0f;  // weights are 2^(s - m + 6): below 2^14 while m may lag by 2^8
 constexpr float kRaise = 8.0f;
 constexpr int kScaleSlots = 4;
@@ -52,7 +53,10 @@ struct Lay {
     static constexpr int kMat = 128 * D * 2;            // a 128-row f16 tile
     static constexpr int kBufs = kInt8 ? 1 : 2;         // f16 tiles of K, and of V
     static constexpr int offQ = 0;                      // high parts, low parts
-    static constexpr int offK = offQ + 2 * kMat;
+    // at a piece's end the finished rows pass through here: D/2 values and 16 bytes of padding per row and warpgroup
+    static constexpr int kOutRow = D / 2 * 4 + 16;
+    static constexpr int offK = offQ + 2 * kMat + 4096;
+    static_assert(2 * 128 * kOutRow <= 2 * kMat + 4096, "rows out");
     static constexpr int offV = offK + kBufs * kMat;
     static constexpr int offRaw = offV + kBufs * kMat;  // int8: two stages of K codes, two of V codes
     static constexpr int kRaw = 128 * D;
@@ -82,23 +86,27 @@ __device__ __forceinline__ void tc_commit(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// The MMAs' operands are computed by the whole warp (they are uniform, and the
+// instruction wants them in uniform registers); `one` is set in the one lane
+// that issues.
+
 // D (tensor memory) (+)= A (shared memory) B (shared memory)
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t one)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
         : "memory");
 }
 
 // D (tensor memory) (+)= A (tensor memory) B (shared memory)
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t one)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
         : "memory");
 }
 
@@ -224,53 +232,48 @@ __device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.
 
 // One CTA's stretch of the line, piece by piece; every role walks it alike.
 struct Walk {
-    int pos, end;
-    Unit u;           // before the first piece: the unit at pos
-    int t0, n, kend;  // first tile, tiles, keys end
-    bool begun;
+    int pos, begin, end;  // next place; the stretch
+    Unit u;               // before the first piece: the unit at `begin`
+    int t0, n, kend;      // first tile, tiles, keys end
+    bool first;           // the stretch begins in this unit
 
     __device__ __forceinline__ bool next(const AttnArgs &a, const int *pre)
     {
-        if (pos >= end) return false;
-        if (begun) q8::attn_next_unit<kRows, kTile>(a, pre, u);
-        begun = true;
-        t0 = pos - u.start;
-        n = min(u.tiles - t0, end - pos);
-        kend = min((t0 + n) * kTile,
-                   q8::attn_visible(a, u.cached, u.fresh, min((u.rt + 1) * kRows, u.fresh * a.group)));
-        pos += n;
-        return true;
+        while (pos < end) {
+            first = pos == begin;
+            if (!first) q8::attn_next_unit<kRows, kTile, kHead>(a, pre, u);
+            t0 = max(0, pos - u.start - kHead);
+            n = min(u.tiles, end - u.start - kHead) - t0;
+            pos = u.start + kHead + u.tiles;
+            kend = min((t0 + n) * kTile,
+                       q8::attn_visible(a, u.cached, u.fresh, min((u.rt + 1) * kRows, u.fresh * a.group)));
+            if (n > 0) return true;  // else only the unit's head: the next CTA has its tiles
+        }
+        return false;
     }
 };
 
-// 32 consecutive values of a finished row held by one thread: y and the plane
-// (the block's encoding by the steps of q8_encode8, without its shuffles).
-__device__ __forceinline__ void store32(const AttnArgs &a, long long at, const float (&o)[32])
+// One block of the plane: 32 consecutive values of a finished row in one
+// thread, encoded by the steps of q8_encode8 without its shuffles.
+__device__ __forceinline__ void encode32(const AttnArgs &a, long long at, const float (&o)[32])
 {
-    if (a.y) {
+    float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4 *>(a.y + at + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(o[i]));
+    const float d = q8::q8_block_d(m), di = q8::q8_block_di(d);
+    int sum = 0;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int c0 = q8::q8_code(o[4 * i], di), c1 = q8::q8_code(o[4 * i + 1], di);
+        const int c2 = q8::q8_code(o[4 * i + 2], di), c3 = q8::q8_code(o[4 * i + 3], di);
+        sum += c0 + c1 + c2 + c3;
+        w[i] = q8::pack4(c0, c1, c2, c3);
     }
-    if (a.qs) {
-        float m = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(o[i]));
-        const float d = q8::q8_block_d(m), di = q8::q8_block_di(d);
-        int sum = 0;
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c0 = q8::q8_code(o[4 * i], di), c1 = q8::q8_code(o[4 * i + 1], di);
-            const int c2 = q8::q8_code(o[4 * i + 2], di), c3 = q8::q8_code(o[4 * i + 3], di);
-            sum += c0 + c1 + c2 + c3;
-            w[i] = q8::pack4(c0, c1, c2, c3);
-        }
-        uint4 *dst = reinterpret_cast<uint4 *>(a.qs + at);
-        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        a.ds[at / 32] = q8::q8_dsword(d, sum);
-    }
+    uint4 *dst = reinterpret_cast<uint4 *>(a.qs + at);
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    a.ds[at / 32] = q8::q8_dsword(d, sum);
 }
 
 template <int D, bool kInt8>
@@ -316,7 +319,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     }
     q8::griddep_launch_dependents();
     q8::griddep_wait();
-    bool bad_data = !q8::attn_line<kRows, kTile, L::kThreads>(a, pre);
+    bool bad_data = !q8::attn_line<kRows, kTile, kHead, L::kThreads>(a, pre);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -326,10 +329,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     const int cta = blockIdx.x;
     const int s0 = min(total, cta * per);
     Walk w;
-    w.pos = s0;
+    w.pos = w.begin = s0;
     w.end = min(total, s0 + per);
-    w.begun = false;
-    if (w.pos < w.end) w.u = q8::attn_unit<kRows, kTile>(a, pre, w.pos);
+    if (w.pos < w.end) w.u = q8::attn_unit<kRows, kTile, kHead>(a, pre, w.pos);
 
     if (warp < 4) {
         setmaxnreg_dec<L::kRegsCtl>();
@@ -407,60 +409,70 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 drain_bar(bar((kInt8 ? L::bRVf : L::bVf) + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u);
             for (int t = max(0, nc - kScaleSlots); t < nc; ++t)
                 drain_bar(bar(L::bCf + t % kScaleSlots), static_cast<uint32_t>(t / kScaleSlots) & 1u);
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             // -------------------------------------------------------- MMAs
             constexpr uint32_t iS = idesc_f16(kTile, false), iO = idesc_f16(D, true);
+            const uint32_t one = lane == 0;
+            const uint32_t tm = __shfl_sync(Q8_FULL_MASK, tmem, 0);
             int T = 0;
             uint32_t piece = 0, pph[2] = {0, 0};
             bool ok = true;
             auto scores = [&](int t, int b) {  // tile t of the CTA into score buffer b
                 const int st = t % L::kBufs;
-                if (!wait_bar(bar(L::bKf + st), static_cast<uint32_t>(t / L::kBufs) & 1u, abort_flag)) return false;
+                if (!warp_wait(bar(L::bKf + st), static_cast<uint32_t>(t / L::kBufs) & 1u, abort_flag)) return false;
                 tc_fence_after();
-                const uint32_t k = base + L::offK + st * L::kMat;
+                const uint64_t k = desc128(base + L::offK + st * L::kMat, 16, 1024);
 #pragma unroll
-                for (int part = 1; part >= 0; --part)  // low parts first: the accumulator is small while they are added
+                for (int part = 1; part >= 0; --part) {  // low parts first: the accumulator is small while they are added
+                    const uint64_t q = desc128(base + L::offQ + part * L::kMat, 16, 1024);
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s) {
-                        const uint32_t o = (s >> 2) * 16384 + (s & 3) * 32;
-                        mma_ss(tmem + 128u * b, desc128(base + L::offQ + part * L::kMat + o, 16, 1024), desc128(k + o, 16, 1024),
-                               iS, part == 0 || s > 0);
+                        const uint32_t o = ((s >> 2) * 16384 + (s & 3) * 32) >> 4;
+                        mma_ss(tm + 128u * b, q + o, k + o, iS, part == 0 || s > 0, one);
                     }
-                tc_commit(bar(L::bKe + st));
-                tc_commit(bar(L::bSf + b));
+                }
+                if (one) {
+                    tc_commit(bar(L::bKe + st));
+                    tc_commit(bar(L::bSf + b));
+                }
+                __syncwarp();
                 return true;
             };
             while (ok && w.next(a, pre)) {
-                ok = wait_bar(bar(L::bQf), piece & 1u, abort_flag);
+                ok = warp_wait(bar(L::bQf), piece & 1u, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 for (int i = 0; ok && i < min(2, w.n); ++i) ok = scores(T + i, i);
                 for (int i = 0; ok && i < w.n; ++i) {
                     const int t = T + i, b = i & 1, st = t % L::kBufs;
-                    ok = wait_bar(bar(L::bVf + st), static_cast<uint32_t>(t / L::kBufs) & 1u, abort_flag) &&
-                         wait_bar(bar(L::bPf + b), pph[b], abort_flag);
+                    ok = warp_wait(bar(L::bVf + st), static_cast<uint32_t>(t / L::kBufs) & 1u, abort_flag) &&
+                         warp_wait(bar(L::bPf + b), b ? pph[1] : pph[0], abort_flag);
                     if (!ok) break;
-                    pph[b] ^= 1u;
+                    if (b) pph[1] ^= 1u; else pph[0] ^= 1u;
                     tc_fence_after();
-                    const uint32_t v = base + L::offV + st * L::kMat;
+                    const uint64_t v = desc128(base + L::offV + st * L::kMat, 16384, 1024);
+                    const uint32_t d = tm + L::kColO + D * b, p = tm + 128u * b;
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                    for (int part = 1; part >= 0; --part)
 #pragma unroll
                         for (int s = 0; s < kTile / 16; ++s)
-                            mma_ts(tmem + L::kColO + D * b, tmem + 128u * b + 32u * (s >> 1) + 8u * (s & 1) + 16u * part,
-                                   desc128(v + 2048 * s, 16384, 1024),
-                                   iO, (i >= 2) | part | s);
-                    tc_commit(bar(L::bVe + st));
+                            mma_ts(d, p + 32u * (s >> 1) + 8u * (s & 1) + 16u * part, v + ((2048u * s) >> 4), iO,
+                                   part == 0 || s > 0 || i >= 2, one);
+                    if (one) tc_commit(bar(L::bVe + st));
+                    __syncwarp();
                     if (i + 2 < w.n) ok = scores(t + 2, b);
                 }
                 if (!ok) break;
-                tc_commit(bar(L::bOf));
+                if (one) tc_commit(bar(L::bOf));
+                __syncwarp();
                 T += w.n;
                 ++piece;
             }
             // every MMA issued must be complete before tensor memory is freed
-            tc_commit(bar(L::bDrain));
-            drain_bar(bar(L::bDrain), 0);
+            if (one) {
+                tc_commit(bar(L::bDrain));
+                drain_bar(bar(L::bDrain), 0);
+            }
         }
         __syncwarp();
     } else if (warp < 12) {
@@ -472,31 +484,41 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         int T = 0;
         uint32_t piece = 0, sph = 0;
         if (tid == 128) a.desc[2 * cta + 1].w = 0;  // no first piece yet
-        while (w.next(a, pre)) {
+        // Q: a warp per row (D = 128) or two rows (D = 64), eight warps.  A unit's rows are in registers before the unit
+        // before it is finished.
+        constexpr int kPer = D == 128 ? 1 : 2, kLanes = 32 / kPer, kLoads = 16 / kPer;
+        const int sub = lane % kLanes;
+        auto q_row = [&](int j) { return ((warp - 4) + 8 * j) * kPer + lane / kLanes; };
+        float4 x[kLoads];
+        auto load_q = [&](const Unit &u) {
+            const q8::RowMap map(a, u.rt * kRows);
+            const int rows = u.fresh * a.group - u.rt * kRows;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int rr = q_row(j);
+                x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (rr < rows) x[j] = __ldg(reinterpret_cast<const float4 *>(a.q + map.at(a, u, rr, D)) + sub);
+            }
+        };
+        bool more = w.next(a, pre);
+        if (more) load_q(w.u);
+        while (more) {
             const Unit &u = w.u;
             const int rows = u.fresh * a.group, row0 = u.rt * kRows;
             {
-                // Q: a warp per row (D = 128) or two rows (D = 64), eight warps; the row's largest value goes to
-                // [1, 2), the sign of the scale into q
-                constexpr int kPer = D == 128 ? 1 : 2, kLanes = 32 / kPer;
-                const int sub = lane % kLanes, half = lane / kLanes;
+                // the row's largest value goes to [1, 2), the sign of the scale into q
                 const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
-#pragma unroll 4
-                for (int j = 0; j < 16 / kPer; ++j) {
-                    const int rr = ((warp - 4) + 8 * j) * kPer + half, row = row0 + rr, tok = row / a.group;
-                    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (row < rows)
-                        x = *reinterpret_cast<const float4 *>(
-                            a.q + (static_cast<long long>(u.first + tok) * a.heads + u.kvh * a.group + (row - tok * a.group)) * D +
-                            4 * sub);
-                    float m = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) {
+                    const int rr = q_row(j);
+                    float m = fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)), fmaxf(fabsf(x[j].z), fabsf(x[j].w)));
 #pragma unroll
                     for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(Q8_FULL_MASK, m, o));
                     const int e = min(126, max(-126, static_cast<int>(__float_as_uint(m) >> 23) - 127));
                     const float down = q8::pow2(-e) * sign;
                     uint2 hi, lo;
-                    q8::split_f16(x.x * down, x.y * down, hi.x, lo.x);
-                    q8::split_f16(x.z * down, x.w * down, hi.y, lo.y);
+                    q8::split_f16(x[j].x * down, x[j].y * down, hi.x, lo.x);
+                    q8::split_f16(x[j].z * down, x[j].w * down, hi.y, lo.y);
                     const int off = (sub >> 4) * 16384 + rr * 128 + ((((sub & 15) >> 1) ^ (rr & 7)) << 4) + (sub & 1) * 8;
                     *reinterpret_cast<uint2 *>(sm + L::offQ + off) = hi;
                     *reinterpret_cast<uint2 *>(sm + L::offQ + L::kMat + off) = lo;
@@ -701,6 +723,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 arrive(bar(L::bPf + wg));
                 if (kInt8) arrive(bar(L::bCe + t % kScaleSlots));
             }
+            Walk nx = w;
+            more = nx.next(a, pre);
+            if (more) load_q(nx.u);
             ok = ok && warp_wait(bar(L::bOf), piece & 1u, abort_flag);
             tc_fence_after();
             s_row[128 * (1 + 3 * wg) + r] = m;
@@ -711,14 +736,23 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             const int poison = *s_poison;
             const float m0 = s_row[128 + r], m1 = s_row[128 * 4 + r];
             const float mm = fmaxf(m0, m1);
-            const float f0 = m0 == -INFINITY ? 0.0f : m0 == mm ? 1.0f : q8::exp2_approx(m0 - mm);
-            const float f1 = m1 == -INFINITY ? 0.0f : m1 == mm ? 1.0f : q8::exp2_approx(m1 - mm);
+            float f0 = m0 == -INFINITY ? 0.0f : m0 == mm ? 1.0f : q8::exp2_approx(m0 - mm);
+            float f1 = m1 == -INFINITY ? 0.0f : m1 == mm ? 1.0f : q8::exp2_approx(m1 - mm);
             const float ll = f0 * s_row[128 * 2 + r] + f1 * s_row[128 * 5 + r];
             const float g0 = s_row[128 * 3 + r], g1 = s_row[128 * 6 + r];
             const bool partial = w.t0 > 0 || w.n < u.tiles;
-            const int pslot = 2 * cta + (w.pos - w.n == s0 ? 0 : 1);
+            const int pslot = 2 * cta + (w.first ? 0 : 1);
             const bool valid = row0 + r < rows;
-            // warpgroup g finishes columns [g * D/2, (g + 1) * D/2) of every row
+            const long long at = q8::RowMap(a, row0).at(a, u, r, D);
+            float *out = partial ? a.part + (static_cast<long long>(pslot) * kRows + r) * D : a.y ? a.y + at : nullptr;
+            if (!partial) {  // the quotient; a row that saw nothing is 0
+                const float inv = ll == 0.0f ? 0.0f : __frcp_rn(ll);
+                f0 *= inv, f1 *= inv;
+            }
+            // Warpgroup g finishes columns [g * D/2, (g + 1) * D/2) of every row.  A thread puts its half row into
+            // shared memory (all scores are computed, so Q's place is free) and hands it to one bulk copy: stores
+            // from the registers would touch 32 rows each.
+            uint8_t *stage = sm + L::offQ + (wg * 128 + r) * L::kOutRow;
 #pragma unroll 1
             for (int c = wg * (D / 2); ok && c < (wg + 1) * (D / 2); c += 32) {
                 uint32_t x0[32], x1[32];
@@ -744,38 +778,39 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                                           (static_cast<long long>(pg * a.kv_heads + u.kvh) * a.page + (key - pi * a.page)) * D + c;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
-                            const float x = __half2float(v[j]);
-                            if (!(fabsf(x) <= 65504.0f)) o[j] += x;
+                            const float y = __half2float(v[j]);
+                            if (!(fabsf(y) <= 65504.0f)) o[j] += y;
                         }
                     }
                 }
-                if (valid && partial) {
-                    float4 *dst = reinterpret_cast<float4 *>(a.part + (static_cast<long long>(pslot) * kRows + r) * D + c);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                } else if (valid) {
-                    const float inv = ll == 0.0f ? 0.0f : __frcp_rn(ll);  // a row that saw nothing
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] *= inv;
-                    const int row = row0 + r, tok = row / a.group;
-                    store32(a,
-                            (static_cast<long long>(u.first + tok) * a.heads + u.kvh * a.group + (row - tok * a.group)) * D + c,
-                            o);
-                }
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<float4 *>(stage + (c - wg * (D / 2)) * 4 + 16 * j) =
+                        make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                if (valid && !partial && a.qs) encode32(a, at + c, o);
                 __syncwarp();
             }
+            if (ok && valid && out) {
+                q8::fence_proxy_async_smem();
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(out + wg * (D / 2)),
+                             "r"(q8::smem_u32(stage)), "r"(D / 2 * 4)
+                             : "memory");
+            }
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             if (partial && wg == 0) a.ml[pslot * kRows + r] = make_float2(mm, ll);
-            if (partial && w.pos - w.n == s0 && tid == 128) {
-                a.desc[2 * cta] = make_int4(u.start, u.start + u.tiles, per, 0);
+            if (partial && w.first && tid == 128) {
+                a.desc[2 * cta] = make_int4(u.start, u.start + kHead + u.tiles, per, u.start + kHead);
                 a.desc[2 * cta + 1] = make_int4(u.b, u.kvh, u.rt, 1);
             }
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // Q's place is free again
             soft_sync();  // s_stop is written, s_poison and the row words are read
             if (*s_stop) break;
             if (tid == 128) *s_poison = 0;  // set again after the next piece's first barrier at the earliest
             T += w.n;
             ++piece;
+            w = nx;
         }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the rows have left before the CTA does
     } else if (kInt8) {
         setmaxnreg_dec<L::kRegsConv>();
         // ------------------------------------------------------------ int8 codes -> f16 tiles in the MMA's layout

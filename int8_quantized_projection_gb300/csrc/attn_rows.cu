@@ -113,7 +113,7 @@ __device__ __forceinline__ void weights(RowState<D> &st, const float (&s)[4], co
     if (kInt8) {  // the largest scale among the keys this row sees
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (v[i] <= 3.4028235e38f) big = fmaxf(big, v[i]);
+            if (fabsf(v[i]) <= 3.4028235e38f) big = fmaxf(big, fabsf(v[i]));
         big = fmaxf(big, __shfl_xor_sync(Q8_FULL_MASK, big, 1));
         big = fmaxf(big, __shfl_xor_sync(Q8_FULL_MASK, big, 2));
     }

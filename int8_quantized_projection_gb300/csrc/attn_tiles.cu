@@ -9,15 +9,16 @@
 //
 // Two softmax warpgroups take the tiles in turn, each with a score buffer and
 // an accumulator of its own in tensor memory (S0, S1, O0, O1: 512 columns for
-// D = 128) and its own (m, l), joined once per piece: they never wait for each
-// other, and while one computes weights the tensor core works on the other's
-// scores or product.  A thread owns a row, so maxima and sums need no
-// shuffles; P overwrites S in place (per 32 keys 16 columns of high parts
-// and 16 of low parts) and is the second product's A operand from tensor memory.  V is used
+// D = 128), its own (m, l), joined once per piece, and its own MMA-issuing
+// warp: they never wait for each other, and while one computes weights the
+// tensor core works on the other's scores or product.  (With one issuing
+// warp the tensor core stood still for a third of the time: it queues only a
+// few MMAs ahead, and each wait of the issuing warp takes some 300 cycles.)  P overwrites S in place (64 columns of high parts, 64 of low
+// parts) and is the second product's A operand from tensor memory.  V is used
 // as it lies in the cache ([key][dim], N-major).
 //
 // Roles: warp 0 copies K and V tiles (one TMA box per run of keys that share
-// a page), warp 1 issues the MMAs, warps 4-11 are the softmax warpgroups; for
+// a page), warps 1 and 3 issue the MMAs, warps 4-11 are the softmax warpgroups; for
 // int8, warps 12-15 widen the codes to f16 tiles (exact), a key's scale
 // multiplies its score column and a value's scale its weight column.
 //
@@ -53,10 +54,7 @@ struct Lay {
     static constexpr int kMat = 128 * D * 2;            // a 128-row f16 tile
     static constexpr int kBufs = kInt8 ? 1 : 2;         // f16 tiles of K, and of V
     static constexpr int offQ = 0;                      // high parts, low parts
-    // at a piece's end the finished rows pass through here: D/2 values and 16 bytes of padding per row and warpgroup
-    static constexpr int kOutRow = D / 2 * 4 + 16;
-    static constexpr int offK = offQ + 2 * kMat + 4096;
-    static_assert(2 * 128 * kOutRow <= 2 * kMat + 4096, "rows out");
+    static constexpr int offK = offQ + 2 * kMat;
     static constexpr int offV = offK + kBufs * kMat;
     static constexpr int offRaw = offV + kBufs * kMat;  // int8: two stages of K codes, two of V codes
     static constexpr int kRaw = 128 * D;
@@ -65,10 +63,12 @@ struct Lay {
     // per row: q scale; m, l and 2^e of each warpgroup
     static constexpr int offBar = offRow + 128 * 4 * 7;
     // barriers, by index
-    static constexpr int bKf = 0, bKe = 2, bVf = 4, bVe = 6;      // f16 tiles: full, empty
+    // f16 tiles: full, empty; by the tile's parity, for int8 too (one buffer, but tiles in turn have issuing warps of
+    // their own, and a warp that sees every other phase of one barrier could not tell them apart)
+    static constexpr int bKf = 0, bKe = 2, bVf = 4, bVe = 6;
     static constexpr int bRKf = 8, bRKe = 10, bRVf = 12, bRVe = 14;  // int8 codes
     static constexpr int bCf = 16, bCe = 20;                      // int8 scales
-    static constexpr int bSf = 24, bPf = 26, bQf = 28, bOf = 29, bDrain = 30, kBars = 31;
+    static constexpr int bSf = 24, bPf = 26, bQf = 28, bOf = 29, bDrain = 30, kBars = 32;
     static constexpr int offMisc = offBar + kBars * 8 + 8;
     static constexpr int offPre = offMisc + 32;
     static int smem(int batch) { return offPre + (batch + 1) * 4 + 1024; }
@@ -110,11 +110,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
-// 32 columns of this thread's lane; valid after tc_wait_ld and tc_regs32.
-__device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t *r)
+// 16 lanes x 64 columns (16x256b, 8 repetitions): registers 4*rep + {0, 1} are
+// lane i/4, columns 8*rep + 2*(i%4) + {0, 1}; 4*rep + {2, 3} the same of lane
+// i/4 + 8.  Valid after tc_wait_ld and tc_regs32.
+__device__ __forceinline__ void tc_ld16x64(uint32_t taddr, uint32_t *r)
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
         "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
@@ -123,6 +125,31 @@ __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t *r)
         : "r"(taddr));
 }
 
+__device__ __forceinline__ void tc_st16x64(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// 16 lanes x 32 columns (16x128b, 8 repetitions): registers 2*rep are lane
+// i/4, column 4*rep + i%4; 2*rep + 1 the same of lane i/4 + 8.  What pairs of
+// values read by tc_ld16x64 become when they are packed into a word each.
+__device__ __forceinline__ void tc_st16x32(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// No use of the registers is scheduled before the wait that precedes this.
 __device__ __forceinline__ void tc_regs32(uint32_t *r)
 {
 #pragma unroll
@@ -131,16 +158,6 @@ __device__ __forceinline__ void tc_regs32(uint32_t *r)
                      : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                        "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
                        "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]));
-}
-
-__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t *r)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-            taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
 }
 
 // Shared-memory matrix descriptor, 128-byte swizzle: rows of 128 bytes in
@@ -253,27 +270,28 @@ struct Walk {
     }
 };
 
-// One block of the plane: 32 consecutive values of a finished row in one
-// thread, encoded by the steps of q8_encode8 without its shuffles.
-__device__ __forceinline__ void encode32(const AttnArgs &a, long long at, const float (&o)[32])
+// One block of the plane, held by the four lanes of a quad: v[2 * i] are
+// columns 8 * i + c2 + {0, 1} of the 32.  The steps of q8_encode8.
+__device__ __forceinline__ void encode_quad(const AttnArgs &a, long long at, const float2 *v, int c2, bool valid)
 {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(o[i]));
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(v[2 * i].x), fabsf(v[2 * i].y)));
+    m = fmaxf(m, __shfl_xor_sync(Q8_FULL_MASK, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(Q8_FULL_MASK, m, 2));
     const float d = q8::q8_block_d(m), di = q8::q8_block_di(d);
     int sum = 0;
-    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c0 = q8::q8_code(o[4 * i], di), c1 = q8::q8_code(o[4 * i + 1], di);
-        const int c2 = q8::q8_code(o[4 * i + 2], di), c3 = q8::q8_code(o[4 * i + 3], di);
-        sum += c0 + c1 + c2 + c3;
-        w[i] = q8::pack4(c0, c1, c2, c3);
+    for (int i = 0; i < 4; ++i) {
+        const int q0 = q8::q8_code(v[2 * i].x, di), q1 = q8::q8_code(v[2 * i].y, di);
+        sum += q0 + q1;
+        if (valid)
+            *reinterpret_cast<uint16_t *>(a.qs + at + 8 * i + c2) =
+                static_cast<uint16_t>((q0 & 0xff) | ((q1 & 0xff) << 8));
     }
-    uint4 *dst = reinterpret_cast<uint4 *>(a.qs + at);
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    a.ds[at / 32] = q8::q8_dsword(d, sum);
+    sum += __shfl_xor_sync(Q8_FULL_MASK, sum, 1);
+    sum += __shfl_xor_sync(Q8_FULL_MASK, sum, 2);
+    if (valid && c2 == 0) a.ds[at / 32] = q8::q8_dsword(d, sum);
 }
 
 template <int D, bool kInt8>
@@ -305,7 +323,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             if (i == L::bCe || (i > L::bCe && i < L::bCe + kScaleSlots)) count = 128;  // the tile's warpgroup
             if (i >= L::bPf && i < L::bPf + 2) count = 128;
             if (i == L::bQf) count = 256;
-            if (kInt8 && (i == L::bKf || i == L::bVf)) count = 128;  // written by the widening warps
+            if (i == L::bOf) count = 2;  // a commit of each issuing warp
+            if (kInt8 && ((i >= L::bKf && i < L::bKf + 2) || (i >= L::bVf && i < L::bVf + 2))) count = 128;  // widening warps
             if ((i >= L::bRKe && i < L::bRKe + 2) || (i >= L::bRVe && i < L::bRVe + 2)) count = 128;
             q8::mbar_init(bars + i, count);
         }
@@ -409,31 +428,32 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 drain_bar(bar((kInt8 ? L::bRVf : L::bVf) + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u);
             for (int t = max(0, nc - kScaleSlots); t < nc; ++t)
                 drain_bar(bar(L::bCf + t % kScaleSlots), static_cast<uint32_t>(t / kScaleSlots) & 1u);
-        } else if (warp == 1) {
-            // -------------------------------------------------------- MMAs
+        } else if (warp & 1) {
+            // -------------------------------------------------------- MMAs: warp 1 for warpgroup 0's tiles, warp 3 for 1's
             constexpr uint32_t iS = idesc_f16(kTile, false), iO = idesc_f16(D, true);
+            const int b = warp >> 1;
             const uint32_t one = lane == 0;
             const uint32_t tm = __shfl_sync(Q8_FULL_MASK, tmem, 0);
+            const uint32_t ts = tm + 128u * b, to = tm + L::kColO + D * b;
             int T = 0;
-            uint32_t piece = 0, pph[2] = {0, 0};
+            uint32_t piece = 0, pph = 0;
             bool ok = true;
-            auto scores = [&](int t, int b) {  // tile t of the CTA into score buffer b
-                const int st = t % L::kBufs;
-                if (!warp_wait(bar(L::bKf + st), static_cast<uint32_t>(t / L::kBufs) & 1u, abort_flag)) return false;
+            auto scores = [&](int t) {
+                if (!warp_wait(bar(L::bKf + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u, abort_flag)) return false;
                 tc_fence_after();
-                const uint64_t k = desc128(base + L::offK + st * L::kMat, 16, 1024);
+                const uint64_t k = desc128(base + L::offK + (t % L::kBufs) * L::kMat, 16, 1024);
 #pragma unroll
                 for (int part = 1; part >= 0; --part) {  // low parts first: the accumulator is small while they are added
                     const uint64_t q = desc128(base + L::offQ + part * L::kMat, 16, 1024);
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s) {
                         const uint32_t o = ((s >> 2) * 16384 + (s & 3) * 32) >> 4;
-                        mma_ss(tm + 128u * b, q + o, k + o, iS, part == 0 || s > 0, one);
+                        mma_ss(ts, q + o, k + o, iS, part == 0 || s > 0, one);
                     }
                 }
                 if (one) {
-                    tc_commit(bar(L::bKe + st));
                     tc_commit(bar(L::bSf + b));
+                    tc_commit(bar(L::bKe + (t & 1)));
                 }
                 __syncwarp();
                 return true;
@@ -442,25 +462,23 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 ok = warp_wait(bar(L::bQf), piece & 1u, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                for (int i = 0; ok && i < min(2, w.n); ++i) ok = scores(T + i, i);
-                for (int i = 0; ok && i < w.n; ++i) {
-                    const int t = T + i, b = i & 1, st = t % L::kBufs;
-                    ok = warp_wait(bar(L::bVf + st), static_cast<uint32_t>(t / L::kBufs) & 1u, abort_flag) &&
-                         warp_wait(bar(L::bPf + b), b ? pph[1] : pph[0], abort_flag);
+                if (b < w.n) ok = scores(T + b);
+                for (int i = b; ok && i < w.n; i += 2) {
+                    const int t = T + i;
+                    ok = warp_wait(bar(L::bVf + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u, abort_flag) &&
+                         warp_wait(bar(L::bPf + b), pph, abort_flag);
                     if (!ok) break;
-                    if (b) pph[1] ^= 1u; else pph[0] ^= 1u;
+                    pph ^= 1u;
                     tc_fence_after();
-                    const uint64_t v = desc128(base + L::offV + st * L::kMat, 16384, 1024);
-                    const uint32_t d = tm + L::kColO + D * b, p = tm + 128u * b;
+                    const uint64_t v = desc128(base + L::offV + (t % L::kBufs) * L::kMat, 16384, 1024);
 #pragma unroll
                     for (int part = 1; part >= 0; --part)
 #pragma unroll
                         for (int s = 0; s < kTile / 16; ++s)
-                            mma_ts(d, p + 32u * (s >> 1) + 8u * (s & 1) + 16u * part, v + ((2048u * s) >> 4), iO,
-                                   part == 0 || s > 0 || i >= 2, one);
-                    if (one) tc_commit(bar(L::bVe + st));
+                            mma_ts(to, ts + 64u * part + 8u * s, v + ((2048u * s) >> 4), iO, part == 0 || s > 0 || i >= 2, one);
+                    if (one) tc_commit(bar(L::bVe + (t & 1)));
                     __syncwarp();
-                    if (i + 2 < w.n) ok = scores(t + 2, b);
+                    if (i + 2 < w.n) ok = scores(t + 2);  // after the products that read P from the same columns
                 }
                 if (!ok) break;
                 if (one) tc_commit(bar(L::bOf));
@@ -470,8 +488,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             }
             // every MMA issued must be complete before tensor memory is freed
             if (one) {
-                tc_commit(bar(L::bDrain));
-                drain_bar(bar(L::bDrain), 0);
+                tc_commit(bar(L::bDrain + b));
+                drain_bar(bar(L::bDrain + b), 0);
             }
         }
         __syncwarp();
@@ -506,15 +524,21 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             const Unit &u = w.u;
             const int rows = u.fresh * a.group, row0 = u.rt * kRows;
             {
-                // the row's largest value goes to [1, 2), the sign of the scale into q
-                const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+                // the row's largest value goes to [1, 2), the sign of the scale (or a scale of 0) into q: hidden scores
+                // become -inf before they are scaled, so the scale of a row is never 0
+                const float sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
 #pragma unroll
                 for (int j = 0; j < kLoads; ++j) {
                     const int rr = q_row(j);
-                    float m = fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)), fmaxf(fabsf(x[j].z), fabsf(x[j].w)));
+                    // magnitudes order as their bits do; a NaN's exponent is clamped like an infinity's
+                    uint32_t top = __float_as_uint(fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)), fmaxf(fabsf(x[j].z), fabsf(x[j].w))));
+                    if (D == 128) {
+                        top = __reduce_max_sync(Q8_FULL_MASK, top);
+                    } else {
 #pragma unroll
-                    for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(Q8_FULL_MASK, m, o));
-                    const int e = min(126, max(-126, static_cast<int>(__float_as_uint(m) >> 23) - 127));
+                        for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(Q8_FULL_MASK, top, o));
+                    }
+                    const int e = min(126, max(-126, static_cast<int>(top >> 23) - 127));
                     const float down = q8::pow2(-e) * sign;
                     uint2 hi, lo;
                     q8::split_f16(x[j].x * down, x[j].y * down, hi.x, lo.x);
@@ -522,18 +546,25 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     const int off = (sub >> 4) * 16384 + rr * 128 + ((((sub & 15) >> 1) ^ (rr & 7)) << 4) + (sub & 1) * 8;
                     *reinterpret_cast<uint2 *>(sm + L::offQ + off) = hi;
                     *reinterpret_cast<uint2 *>(sm + L::offQ + L::kMat + off) = lo;
-                    if (sub == 0) s_row[rr] = q8::pow2(e) * fabsf(a.scale);
+                    if (sub == 0) s_row[rr] = fmaxf(q8::pow2(e) * fabsf(a.scale), 1.17549435e-38f);
                 }
                 q8::fence_proxy_async_smem();
                 tc_fence_before();  // the last piece's tensor-memory loads are done
                 arrive(bar(L::bQf));
                 soft_sync();
             }
-            const float qs = s_row[r];
-            const q8::RowSight sight = q8::attn_sight(a, u, row0 + r);
+            // Scores are read 16 rows at a time (16x256b): a thread has rows g and g + 8 of the 16 at 32 columns each, so
+            // 64 registers hold all it needs between the maximum and the weights, the keys' scales are read once for
+            // two rows, and the code runs twice a tile (a first pass through straight-line code costs its fetch).
+            const int g = lane >> 2, c2 = 2 * (lane & 3);
+            float qs[4], m[4], l[4], ie[4];
+            int e[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {  // row 16 * (x / 2) + g + 8 * (x % 2) of the warp's 32
+                qs[x] = s_row[(warp & 3) * 32 + 16 * (x >> 1) + g + 8 * (x & 1)];
+                m[x] = -INFINITY, l[x] = 0.0f, ie[x] = q8::pow2(126), e[x] = -126;
+            }
             const int all_see = u.cached + (a.masks ? 0 : row0 / a.group + 1);  // keys below are seen by every row
-            float m = -INFINITY, l = 0.0f, ie = 1.0f;
-            int e = 0;
             bool ok = true;
             for (int i = wg; i < w.n; i += 2) {
                 if (!warp_wait(bar(L::bSf + wg), sph, abort_flag)) {
@@ -549,149 +580,163 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     break;
                 }
                 tc_fence_after();
-                // Two passes over the scores, 32 columns at a time: the maximum, then the weights, which go back to
-                // the columns their scores came from (16 of high parts, 16 of low parts).  Holding all 128 scores
-                // between the passes would take 128 registers; reading tensor memory twice is cheaper.
-                auto weigh = [&](auto hidden) {
-                    constexpr bool kMasked = decltype(hidden)::value;
-                    uint32_t see[4];  // the keys this row sees, a bit each
-                    if constexpr (kMasked) {
+                float all_big = 0.0f;  // int8: the tile's largest value scale
+                bool odd = masked;     // some row sees not every key, or a value scale is not finite
+                if (kInt8) {
+                    const float4 v4 = *reinterpret_cast<const float4 *>(sc + 128 + 4 * lane);
+                    all_big = fmaxf(fmaxf(fabsf(v4.x), fabsf(v4.y)), fmaxf(fabsf(v4.z), fabsf(v4.w)));
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int k = key0 + 32 * c, below = max(0, min(32, sight.all - k));
-                            see[c] = below == 32 ? ~0u : (1u << below) - 1u;
-                            const int sh = u.cached - k;  // bit b of the mask is key k + sh + b
-                            if (sh >= 0 && sh < 32) see[c] |= static_cast<uint32_t>(sight.mask << sh);
-                            else if (sh < 0 && sh > -64) see[c] |= static_cast<uint32_t>(sight.mask >> -sh);
-                        }
-                    }
-                    uint32_t s[2][32];
-                    // int8: 32 scores times their keys' scales
-                    auto key_scales = [&](uint32_t *x, int c) {
+                    for (int o = 1; o < 32; o <<= 1) all_big = fmaxf(all_big, __shfl_xor_sync(Q8_FULL_MASK, all_big, o));
+                    const float sum = (v4.x + v4.y) + (v4.z + v4.w);
+                    odd |= __any_sync(Q8_FULL_MASK, !(fabsf(sum) <= 3.4028235e38f));
+                }
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t lanes = static_cast<uint32_t>(16 * half) << 16;
+                    uint32_t s[64];
+                    tc_ld16x64(ts + lanes, s);
+                    tc_ld16x64(ts + lanes + 64, s + 32);
+                    // this half's state
+                    float mm[2] = {half ? m[2] : m[0], half ? m[3] : m[1]};
+                    const float qq[2] = {half ? qs[2] : qs[0], half ? qs[3] : qs[1]};
+                    float ii[2] = {half ? ie[2] : ie[0], half ? ie[3] : ie[1]};
+                    float top[2] = {-INFINITY, -INFINITY}, big[2] = {all_big, all_big};
+                    tc_wait_ld();
+                    tc_regs32(s);
+                    tc_regs32(s + 32);
+                    if (kInt8) {  // scores by their keys' scales
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 k4 = *reinterpret_cast<const float4 *>(sc + 32 * c + 4 * j);
-                            const float2 y = __fmul2_rn(
-                                make_float2(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])), make_float2(k4.x, k4.y));
-                            const float2 z = __fmul2_rn(
-                                make_float2(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])), make_float2(k4.z, k4.w));
-                            x[4 * j] = __float_as_uint(y.x), x[4 * j + 1] = __float_as_uint(y.y);
-                            x[4 * j + 2] = __float_as_uint(z.x), x[4 * j + 3] = __float_as_uint(z.y);
-                        }
-                    };
-                    float mx[2] = {-INFINITY, -INFINITY};
+                        for (int rep = 0; rep < 16; ++rep) {
+                            const float2 k2 = *reinterpret_cast<const float2 *>(sc + 8 * rep + c2);
 #pragma unroll
-                    for (int c = 0; c < 4; c += 2) {
-                        tc_ld32(ts + 32 * c, s[0]);
-                        tc_ld32(ts + 32 * c + 32, s[1]);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            tc_regs32(s[h]);
-                            if (kInt8) key_scales(s[h], c + h);
-                            if constexpr (kMasked) {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    if ((see[c + h] >> j) & 1u) mx[h] = fmaxf(mx[h], __uint_as_float(s[h][j]));
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 32; j += 2)
-                                    mx[h] = fmaxf(fmaxf(mx[h], __uint_as_float(s[h][j])), __uint_as_float(s[h][j + 1]));
+                            for (int x = 0; x < 4; x += 2) {
+                                const float2 y = __fmul2_rn(
+                                    make_float2(__uint_as_float(s[4 * rep + x]), __uint_as_float(s[4 * rep + x + 1])), k2);
+                                s[4 * rep + x] = __float_as_uint(y.x);
+                                s[4 * rep + x + 1] = __float_as_uint(y.y);
                             }
                         }
                     }
-                    float big = 0.0f;  // int8: the largest value scale that the row sees
-                    if (kInt8) {
-                        if constexpr (!kMasked) {  // the same keys for every row: four a lane
-                            const float4 v4 = *reinterpret_cast<const float4 *>(sc + 128 + 4 * lane);
-                            const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
+                    if (odd) {
+                        // hidden keys get score -inf; int8: the largest scale is taken over what the row sees, and a
+                        // scale that is not finite makes the scores that see it NaN
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (vv[j] <= 3.4028235e38f) big = fmaxf(big, vv[j]);
+                        for (int x = 0; x < 2; ++x) {
+                            const q8::RowSight sight = q8::attn_sight(a, u, row0 + (warp & 3) * 32 + 16 * half + g + 8 * x);
+                            big[x] = 0.0f;
 #pragma unroll
-                            for (int o = 1; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(Q8_FULL_MASK, big, o));
-                        } else {
+                            for (int c = 0; c < 4; ++c) {
+                                const int k = key0 + 32 * c, below = max(0, min(32, sight.all - k));
+                                uint32_t see = below == 32 ? ~0u : (1u << below) - 1u;  // of keys k .. k + 31
+                                const int sh = u.cached - k;                            // bit b of the mask is key k + sh + b
+                                if (sh >= 0 && sh < 32) see |= static_cast<uint32_t>(sight.mask << sh);
+                                else if (sh < 0 && sh > -64) see |= static_cast<uint32_t>(sight.mask >> -sh);
+                                see >>= c2;
 #pragma unroll
-                            for (int c = 0; c < 4; ++c)
-#pragma unroll 8
-                                for (int j = 0; j < 32; ++j) {
-                                    const float x = sc[128 + 32 * c + j];
-                                    if (((see[c] >> j) & 1u) && x <= 3.4028235e38f) big = fmaxf(big, x);
+                                for (int j = 0; j < 8; ++j) {  // column 8 * (j / 2) + c2 + j % 2 of the 32
+                                    uint32_t &y = s[16 * c + 4 * (j >> 1) + 2 * x + (j & 1)];
+                                    const bool seen = (see >> (8 * (j >> 1) + (j & 1))) & 1u;
+                                    if (kInt8) {
+                                        const float v = sc[128 + 32 * c + 8 * (j >> 1) + c2 + (j & 1)];
+                                        if (!(fabsf(v) <= 3.4028235e38f)) y = 0x7fffffffu;
+                                        else if (seen) big[x] = fmaxf(big[x], fabsf(v));
+                                    }
+                                    if (!seen) y = 0xff800000u;
                                 }
+                            }
+                            if (kInt8) {
+                                big[x] = fmaxf(big[x], __shfl_xor_sync(Q8_FULL_MASK, big[x], 1));
+                                big[x] = fmaxf(big[x], __shfl_xor_sync(Q8_FULL_MASK, big[x], 2));
+                            }
                         }
                     }
-                    float top = fmaxf(mx[0], mx[1]);
-                    if (top != -INFINITY) top *= qs;
-                    bool raise = top > m + kRaise;
-                    if (kInt8) raise |= big * ie > 1.0f;
-                    if (i == wg) {  // the first tile: nothing accumulated yet
-                        m = top;
-                        if (kInt8) {
-                            e = min(126, max(-126, static_cast<int>(__float_as_uint(big) >> 23) - 126));
-                            ie = q8::pow2(-e);
-                        }
-                    } else if (__any_sync(Q8_FULL_MASK, raise)) {
-                        const float mn = fmaxf(m, top);
-                        float f = mn == m ? 1.0f : q8::exp2_approx(m - mn);
-                        l *= f;
-                        m = mn;
-                        if (kInt8) {
-                            const int en = min(126, max(e, static_cast<int>(__float_as_uint(big) >> 23) - 126));
-                            f = e - en < -126 ? 0.0f : f * q8::pow2(e - en);
-                            e = en;
-                            ie = q8::pow2(-e);
+#pragma unroll
+                    for (int j = 0; j < 64; j += 4) {
+                        top[0] = fmaxf(fmaxf(top[0], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
+                        top[1] = fmaxf(fmaxf(top[1], __uint_as_float(s[j + 2])), __uint_as_float(s[j + 3]));
+                    }
+                    bool raise = i == wg;  // the first tile sets the references
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        top[x] = fmaxf(top[x], __shfl_xor_sync(Q8_FULL_MASK, top[x], 1));
+                        top[x] = fmaxf(top[x], __shfl_xor_sync(Q8_FULL_MASK, top[x], 2));
+                        top[x] *= qq[x];
+                        raise |= top[x] > mm[x] + kRaise;
+                        if (kInt8) raise |= big[x] * ii[x] > 1.0f;
+                    }
+                    if (__any_sync(Q8_FULL_MASK, raise)) {
+                        float f[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float mn = fmaxf(mm[x], top[x]);
+                            f[x] = mn == mm[x] ? 1.0f : q8::exp2_approx(mm[x] - mn);
+                            const float lx = (half ? l[2 + x] : l[x]) * f[x];
+                            if (half) l[2 + x] = lx; else l[x] = lx;
+                            mm[x] = mn;
+                            if (kInt8) {
+                                int ee = half ? e[2 + x] : e[x];
+                                const int en = min(126, max(ee, static_cast<int>(__float_as_uint(big[x]) >> 23) - 126));
+                                f[x] = ee - en < -126 ? 0.0f : f[x] * q8::pow2(ee - en);
+                                if (half) e[2 + x] = en; else e[x] = en;
+                                ii[x] = q8::pow2(-en);
+                            }
                         }
                         // the products so far are complete: their MMAs came before this tile's scores
+                        if (i != wg) {
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            tc_ld32(to + c, s[0]);
-                            tc_wait_ld();
-                            tc_regs32(s[0]);
+                            for (int c = 0; c < D; c += 64) {
+                                uint32_t o[32];
+                                tc_ld16x64(to + lanes + c, o);
+                                tc_wait_ld();
+                                tc_regs32(o);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) s[0][j] = __float_as_uint(__uint_as_float(s[0][j]) * f);
-                            tc_st16(to + c, s[0]);
-                            tc_st16(to + c + 16, s[0] + 16);
+                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[(j >> 1) & 1]);
+                                tc_st16x64(to + lanes + c, o);
+                            }
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.0f : m - kWeightBits;
-                    const float2 q2 = make_float2(qs, qs), r2 = make_float2(-ref, -ref);
-                    float2 sum = make_float2(0.0f, 0.0f);
-                    tc_ld32(ts, s[0]);
-                    tc_wait_ld();
+                    float2 ref[2], sum[2];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t *x = s[c & 1];
-                        tc_regs32(x);
-                        if (c < 3) tc_ld32(ts + 32 * (c + 1), s[(c + 1) & 1]);  // lands while this one is worked on
-                        if (kInt8) key_scales(x, c);
+                    for (int x = 0; x < 2; ++x) {
+                        const float z = mm[x] == -INFINITY ? 0.0f : kWeightBits - mm[x];
+                        ref[x] = make_float2(z, z);
+                        sum[x] = make_float2(0.0f, 0.0f);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t hi[16], lo[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float2 p = __ffma2_rn(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), q2, r2);
-                            p.x = q8::exp2_approx(p.x);
-                            p.y = q8::exp2_approx(p.y);
-                            if constexpr (kMasked) {
-                                if (!((see[c] >> (2 * j)) & 1u)) p.x = 0.0f;
-                                if (!((see[c] >> (2 * j + 1)) & 1u)) p.y = 0.0f;
-                            }
-                            sum = __fadd2_rn(sum, p);
-                            if (kInt8) {
-                                float2 v = *reinterpret_cast<const float2 *>(sc + 128 + 32 * c + 2 * j);
-                                if constexpr (kMasked) {
-                                    if (!((see[c] >> (2 * j)) & 1u)) v.x = 0.0f;
-                                    if (!((see[c] >> (2 * j + 1)) & 1u)) v.y = 0.0f;
+                        for (int j = 0; j < 8; ++j) {
+                            const int rep = 8 * c + j;
+                            float2 v2 = make_float2(1.0f, 1.0f);
+                            if (kInt8) v2 = *reinterpret_cast<const float2 *>(sc + 128 + 8 * rep + c2);
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                float2 p = __ffma2_rn(
+                                    make_float2(__uint_as_float(s[4 * rep + 2 * x]), __uint_as_float(s[4 * rep + 2 * x + 1])),
+                                    make_float2(qq[x], qq[x]), ref[x]);
+                                p.x = q8::exp2_approx(p.x);
+                                p.y = q8::exp2_approx(p.y);
+                                sum[x] = __fadd2_rn(sum[x], p);
+                                if (kInt8) {
+                                    // at most 1 for what the row sees; a hidden key's may be anything, its weight is 0
+                                    float2 y = __fmul2_rn(v2, make_float2(ii[x], ii[x]));
+                                    y.x = fminf(fmaxf(y.x, -1.0f), 1.0f), y.y = fminf(fmaxf(y.y, -1.0f), 1.0f);
+                                    p = __fmul2_rn(p, y);
                                 }
-                                p = __fmul2_rn(p, __fmul2_rn(v, make_float2(ie, ie)));
+                                q8::split_f16(p.x, p.y, hi[2 * j + x], lo[2 * j + x]);
                             }
-                            q8::split_f16(p.x, p.y, hi[j], lo[j]);
                         }
-                        tc_st16(ts + 32 * c, hi);
-                        tc_st16(ts + 32 * c + 16, lo);
-                        if (c < 3) tc_wait_ld();
+                        tc_st16x32(ts + lanes + 32 * c, hi);
+                        tc_st16x32(ts + lanes + 64 + 32 * c, lo);
                     }
-                    l += sum.x + sum.y;
-                };
-                if (masked) weigh(std::true_type{}); else weigh(std::false_type{});
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float sx = sum[x].x + sum[x].y;
+                        if (half) m[2 + x] = mm[x], l[2 + x] += sx, ie[2 + x] = ii[x];
+                        else m[x] = mm[x], l[x] += sx, ie[x] = ii[x];
+                    }
+                }
                 if (!kInt8 && masked) {
                     // values that no row sees must not reach the MMA as 0 * NaN: non-finite ones in a tile with hidden
                     // keys become zero, and are added back at the end for the rows that see them
@@ -728,81 +773,122 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             if (more) load_q(nx.u);
             ok = ok && warp_wait(bar(L::bOf), piece & 1u, abort_flag);
             tc_fence_after();
-            s_row[128 * (1 + 3 * wg) + r] = m;
-            s_row[128 * (2 + 3 * wg) + r] = l;
-            s_row[128 * (3 + 3 * wg) + r] = kInt8 ? q8::pow2(e) : 1.0f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                l[x] += __shfl_xor_sync(Q8_FULL_MASK, l[x], 1);
+                l[x] += __shfl_xor_sync(Q8_FULL_MASK, l[x], 2);
+                if (c2 == 0) {
+                    float *row = s_row + 128 * (1 + 3 * wg) + (warp & 3) * 32 + 16 * (x >> 1) + g + 8 * (x & 1);
+                    row[0] = m[x];
+                    row[128] = l[x];
+                    row[256] = kInt8 ? q8::pow2(e[x]) : 1.0f;
+                }
+            }
             soft_sync();
             if (tid == 128) *s_stop = *abort_flag;
             const int poison = *s_poison;
-            const float m0 = s_row[128 + r], m1 = s_row[128 * 4 + r];
-            const float mm = fmaxf(m0, m1);
-            float f0 = m0 == -INFINITY ? 0.0f : m0 == mm ? 1.0f : q8::exp2_approx(m0 - mm);
-            float f1 = m1 == -INFINITY ? 0.0f : m1 == mm ? 1.0f : q8::exp2_approx(m1 - mm);
-            const float ll = f0 * s_row[128 * 2 + r] + f1 * s_row[128 * 5 + r];
-            const float g0 = s_row[128 * 3 + r], g1 = s_row[128 * 6 + r];
             const bool partial = w.t0 > 0 || w.n < u.tiles;
             const int pslot = 2 * cta + (w.first ? 0 : 1);
-            const bool valid = row0 + r < rows;
-            const long long at = q8::RowMap(a, row0).at(a, u, r, D);
-            float *out = partial ? a.part + (static_cast<long long>(pslot) * kRows + r) * D : a.y ? a.y + at : nullptr;
-            if (!partial) {  // the quotient; a row that saw nothing is 0
-                const float inv = ll == 0.0f ? 0.0f : __frcp_rn(ll);
-                f0 *= inv, f1 *= inv;
-            }
-            // Warpgroup g finishes columns [g * D/2, (g + 1) * D/2) of every row.  A thread puts its half row into
-            // shared memory (all scores are computed, so Q's place is free) and hands it to one bulk copy: stores
-            // from the registers would touch 32 rows each.
-            uint8_t *stage = sm + L::offQ + (wg * 128 + r) * L::kOutRow;
+            const q8::RowMap map(a, row0);
+            // Warpgroup g finishes columns [g * D/2, (g + 1) * D/2) of every row, 16 rows at a time: with this shape a
+            // store of the warp writes whole 32-byte sectors of eight rows.
 #pragma unroll 1
-            for (int c = wg * (D / 2); ok && c < (wg + 1) * (D / 2); c += 32) {
-                uint32_t x0[32], x1[32];
-                tc_ld32(tl + L::kColO + c, x0);
-                if (w.n > 1) tc_ld32(tl + L::kColO + D + c, x1);
-                tc_wait_ld();
-                tc_regs32(x0);
-                float o[32];
+            for (int half = 0; ok && half < 2; ++half) {
+                const uint32_t lanes = static_cast<uint32_t>(16 * half) << 16;
+                const int r0 = (warp & 3) * 32 + 16 * half + g;  // and r0 + 8
+                uint32_t o0[32], o1[32];
+                // D/2 columns: 32 registers hold 64
+                const uint32_t from = tl + lanes + L::kColO + wg * (D / 2);
+                tc_ld16x64(from, o0);
+                if (w.n > 1) tc_ld16x64(from + D, o1);
+                float f0[2], f1[2], mm[2], ll[2];
+                long long at[2];
+                bool valid[2];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = f0 * (g0 * __uint_as_float(x0[j]));
-                if (w.n > 1) {
-                    tc_regs32(x1);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] += f1 * (g1 * __uint_as_float(x1[j]));
+                for (int x = 0; x < 2; ++x) {
+                    const float *row = s_row + r0 + 8 * x;
+                    const float m0 = row[128], m1 = row[128 * 4];
+                    mm[x] = fmaxf(m0, m1);
+                    f0[x] = m0 == -INFINITY ? 0.0f : m0 == mm[x] ? 1.0f : q8::exp2_approx(m0 - mm[x]);
+                    f1[x] = m1 == -INFINITY ? 0.0f : m1 == mm[x] ? 1.0f : q8::exp2_approx(m1 - mm[x]);
+                    ll[x] = f0[x] * row[128 * 2] + f1[x] * row[128 * 5];
+                    if (!partial) {  // the quotient; a row that saw nothing is 0
+                        const float inv = ll[x] == 0.0f ? 0.0f : __frcp_rn(ll[x]);
+                        f0[x] *= inv, f1[x] *= inv;
+                    }
+                    valid[x] = row0 + r0 + 8 * x < rows;
+                    at[x] = map.at(a, u, r0 + 8 * x, D);
                 }
-                if (valid && !kInt8 && poison) {  // the non-finite values that were left out, if this row sees them
+                tc_wait_ld();
+                tc_regs32(o0);
+                float2 o[16];  // 2 * rep + x: row r0 + 8 x, columns wg * D/2 + 8 rep + c2 + {0, 1}
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int x = j & 1;
+                    const float g0 = kInt8 ? s_row[r0 + 8 * x + 128 * 3] : 1.0f;
+                    o[j] = make_float2(f0[x] * (g0 * __uint_as_float(o0[2 * j])), f0[x] * (g0 * __uint_as_float(o0[2 * j + 1])));
+                }
+                if (w.n > 1) {
+                    tc_regs32(o1);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int x = j & 1;
+                        const float g1 = kInt8 ? s_row[r0 + 8 * x + 128 * 6] : 1.0f;
+                        o[j].x += f1[x] * (g1 * __uint_as_float(o1[2 * j]));
+                        o[j].y += f1[x] * (g1 * __uint_as_float(o1[2 * j + 1]));
+                    }
+                }
+                constexpr int kReps = D / 16;  // 8-column groups of this warpgroup's half
+                if (!kInt8 && poison) {  // the non-finite values that were left out, for the rows that see them
                     for (int key = max(w.t0 * kTile, (u.cached & ~(kTile - 1)) - kTile); key < w.kend; ++key) {
-                        if (!q8::attn_sees(sight, u.cached, key)) continue;
                         const int pi = key / a.page;
                         const int pg = a.table[static_cast<long long>(u.b) * a.max_pages + pi];
                         if (pg < 0 || pg >= a.n_pages) continue;
                         const __half *v = reinterpret_cast<const __half *>(a.v16) +
-                                          (static_cast<long long>(pg * a.kv_heads + u.kvh) * a.page + (key - pi * a.page)) * D + c;
+                                          (static_cast<long long>(pg * a.kv_heads + u.kvh) * a.page + (key - pi * a.page)) * D +
+                                          wg * (D / 2) + c2;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float y = __half2float(v[j]);
-                            if (!(fabsf(y) <= 65504.0f)) o[j] += y;
+                        for (int x = 0; x < 2; ++x) {
+                            if (!q8::attn_sees(q8::attn_sight(a, u, row0 + r0 + 8 * x), u.cached, key)) continue;
+#pragma unroll
+                            for (int rep = 0; rep < kReps; ++rep) {
+                                const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(v + 8 * rep));
+                                if (!(fabsf(y.x) <= 65504.0f)) o[2 * rep + x].x += y.x;
+                                if (!(fabsf(y.y) <= 65504.0f)) o[2 * rep + x].y += y.y;
+                            }
                         }
                     }
+                    __syncwarp();
                 }
+                if (partial) {
+                    float *dst = a.part + (static_cast<long long>(pslot) * kRows + r0) * D + wg * (D / 2) + c2;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<float4 *>(stage + (c - wg * (D / 2)) * 4 + 16 * j) =
-                        make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                if (valid && !partial && a.qs) encode32(a, at + c, o);
-                __syncwarp();
+                    for (int j = 0; j < 2 * kReps; ++j)
+                        *reinterpret_cast<float2 *>(dst + (j & 1) * 8 * D + 8 * (j >> 1)) = o[j];
+                    if (wg == 0 && c2 == 0) {
+                        a.ml[pslot * kRows + r0] = make_float2(mm[0], ll[0]);
+                        a.ml[pslot * kRows + r0 + 8] = make_float2(mm[1], ll[1]);
+                    }
+                } else {
+                    if (a.y) {
+#pragma unroll
+                        for (int j = 0; j < 2 * kReps; ++j)
+                            if (valid[j & 1])
+                                *reinterpret_cast<float2 *>(a.y + at[j & 1] + wg * (D / 2) + 8 * (j >> 1) + c2) = o[j];
+                    }
+                    if (a.qs) {
+#pragma unroll
+                        for (int blk = 0; blk < kReps / 4; ++blk)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                encode_quad(a, at[x] + wg * (D / 2) + 32 * blk, o + 8 * blk + x, c2, valid[x]);
+                    }
+                }
             }
-            if (ok && valid && out) {
-                q8::fence_proxy_async_smem();
-                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(out + wg * (D / 2)),
-                             "r"(q8::smem_u32(stage)), "r"(D / 2 * 4)
-                             : "memory");
-            }
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            if (partial && wg == 0) a.ml[pslot * kRows + r] = make_float2(mm, ll);
             if (partial && w.first && tid == 128) {
                 a.desc[2 * cta] = make_int4(u.start, u.start + kHead + u.tiles, per, u.start + kHead);
                 a.desc[2 * cta + 1] = make_int4(u.b, u.kvh, u.rt, 1);
             }
-            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // Q's place is free again
             soft_sync();  // s_stop is written, s_poison and the row words are read
             if (*s_stop) break;
             if (tid == 128) *s_poison = 0;  // set again after the next piece's first barrier at the earliest
@@ -810,7 +896,6 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             ++piece;
             w = nx;
         }
-        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the rows have left before the CTA does
     } else if (kInt8) {
         setmaxnreg_dec<L::kRegsConv>();
         // ------------------------------------------------------------ int8 codes -> f16 tiles in the MMA's layout
@@ -850,16 +935,18 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         while (ok && w.next(a, pre)) {
             for (int i = 0; i < w.n; ++i, ++T) {
                 const int st = T & 1;
-                const uint32_t rpar = static_cast<uint32_t>(T >> 1) & 1u, par = static_cast<uint32_t>(T) & 1u;
-                ok = warp_wait(bar(L::bRKf + st), rpar, abort_flag) && warp_wait(bar(L::bKe), par ^ 1u, abort_flag);
+                const uint32_t par = static_cast<uint32_t>(T >> 1) & 1u, last = static_cast<uint32_t>((T - 1) >> 1) & 1u;
+                ok = warp_wait(bar(L::bRKf + st), par, abort_flag) &&
+                     (T == 0 || warp_wait(bar(L::bKe + (st ^ 1)), last, abort_flag));  // the last tile's scores are done
                 if (!ok) break;
                 widen(L::offRaw + st * L::kRaw, L::offK);
-                arrive(bar(L::bKf));
+                arrive(bar(L::bKf + st));
                 arrive(bar(L::bRKe + st));
-                ok = warp_wait(bar(L::bRVf + st), rpar, abort_flag) && warp_wait(bar(L::bVe), par ^ 1u, abort_flag);
+                ok = warp_wait(bar(L::bRVf + st), par, abort_flag) &&
+                     (T == 0 || warp_wait(bar(L::bVe + (st ^ 1)), last, abort_flag));
                 if (!ok) break;
                 widen(L::offRaw + (2 + st) * L::kRaw, L::offV);
-                arrive(bar(L::bVf));
+                arrive(bar(L::bVf + st));
                 arrive(bar(L::bRVe + st));
             }
         }

@@ -40,6 +40,11 @@ constexpr int kTile = 16 * kWarps;   // keys of a tile: 16 per warp
 constexpr int kHead = 1;             // what a unit costs beside its tiles, in tiles
 constexpr float kWeightBits = 6.0f;  // weights are 2^(s - m + 6)
 constexpr float kRaise = 8.0f;       // m may lag the maximum by this
+// The MMA's f32 accumulation truncates: with values of one sign O loses 1e-7 of
+// itself per MMA (measured: 2.5e-5 after 257).  After this many tiles, one MMA
+// per tile and value in each warp, a piece's result goes to the workspace,
+// rounded to nearest, and the next tiles start anew.
+constexpr int kChain = 64;
 
 template <int D, bool kInt8>
 struct Ring {
@@ -164,6 +169,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + R::offBars) + warp * R::kStages;
     int *pre = reinterpret_cast<int *>(sm + R::offPre);
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_f[kWarps][kRows];
+    __shared__ float2 s_sum[kRows], s_next[kRows];  // (m, l) of the chains before
     __shared__ int s_poison;
 
     if (lane == 0)
@@ -185,331 +191,349 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     for (int pos = s0; pos < s1;) {
         if (pos == s0) u = q8::attn_unit<kRows, kTile, kHead>(a, pre, pos);
         else q8::attn_next_unit<kRows, kTile, kHead>(a, pre, u);
-        const int t0 = max(0, pos - u.start - kHead), t1 = max(0, min(u.tiles, s1 - u.start - kHead));
+        const int ta = max(0, pos - u.start - kHead), tb = max(0, min(u.tiles, s1 - u.start - kHead));
         const bool first = pos == s0;
         pos = u.start + kHead + u.tiles;
-        if (t0 >= t1) continue;  // only the unit's head: the next CTA has its tiles
-        const int rows = u.fresh * a.group, row0 = u.rt * kRows;
-        const int seen = q8::attn_visible(a, u.cached, u.fresh, min(row0 + kRows, rows));
-        const int k0 = t0 * kTile + warp * 16, k1 = min(t1 * kTile, seen);
-        const int n = dead || k0 >= k1 ? 0 : (k1 - k0 + kTile - 1) / kTile;  // this warp's 16-key groups
+        // (no tiles: only the unit's head, the next CTA has them)
+        for (int t0 = ta; t0 < tb; t0 += kChain) {
+            const int t1 = min(tb, t0 + kChain);
+            const int rows = u.fresh * a.group, row0 = u.rt * kRows;
+            const int seen = q8::attn_visible(a, u.cached, u.fresh, min(row0 + kRows, rows));
+            const int k0 = t0 * kTile + warp * 16, k1 = min(t1 * kTile, seen);
+            const int n = dead || k0 >= k1 ? 0 : (k1 - k0 + kTile - 1) / kTile;  // this warp's 16-key groups
 
-        // cache rows of the groups, 32 at a time, a lane each
-        auto fetch = [&](int i) {
-            i += lane;
-            if (i >= n) return 0;
-            const int key = k0 + i * kTile, pi = key / a.page;
-            int pg = a.table[static_cast<long long>(u.b) * a.max_pages + pi];
-            if (pg < 0 || pg >= a.n_pages) {
-                bad_data = true;
-                pg = 0;
-            }
-            return (pg * a.kv_heads + u.kvh) * a.page + (key - pi * a.page);
-        };
-        int base = 0, rows_now = fetch(0), rows_next = fetch(32);
-        auto issue = [&](int i) {
-            if (i >= base + 32) {
-                base += 32;
-                rows_now = rows_next;
-                rows_next = fetch(base + 32);
-            }
-            const int row = __shfl_sync(Q8_FULL_MASK, rows_now, i - base);
-            if (lane == 0) {
-                uint8_t *dst = ring + wslot * R::kStage;
-                uint64_t *bar = bars + wslot;
-                q8::mbar_arrive_expect_tx(bar, R::kTx);
-                const uint32_t d = q8::smem_u32(dst), bb = q8::smem_u32(bar);
-                constexpr int kBox = kInt8 ? D : 64;  // elements of a box row
-                constexpr int kBoxBytes = 16 * kBox * (kInt8 ? 1 : 2);
-#pragma unroll
-                for (int h = 0; h < D / kBox; ++h) {
-                    q8::tma_load_2d(d + h * kBoxBytes, &mk, h * kBox, row, bb);
-                    q8::tma_load_2d(d + R::kMat + h * kBoxBytes, &mv, h * kBox, row, bb);
+            // cache rows of the groups, 32 at a time, a lane each
+            auto fetch = [&](int i) {
+                i += lane;
+                if (i >= n) return 0;
+                const int key = k0 + i * kTile, pi = key / a.page;
+                int pg = a.table[static_cast<long long>(u.b) * a.max_pages + pi];
+                if (pg < 0 || pg >= a.n_pages) {
+                    bad_data = true;
+                    pg = 0;
                 }
-                if (kInt8) {
-                    q8::bulk_g2s(ring_sc + wslot * R::kScales, a.ks + row, 64, bar);
-                    q8::bulk_g2s(ring_sc + wslot * R::kScales + 64, a.vs + row, 64, bar);
+                return (pg * a.kv_heads + u.kvh) * a.page + (key - pi * a.page);
+            };
+            int base = 0, rows_now = fetch(0), rows_next = fetch(32);
+            auto issue = [&](int i) {
+                if (i >= base + 32) {
+                    base += 32;
+                    rows_now = rows_next;
+                    rows_next = fetch(base + 32);
                 }
-            }
-            wslot = wslot + 1 == R::kStages ? 0 : wslot + 1;
-        };
-        for (int i = 0; i < min(n, R::kStages); ++i) issue(i);
-
-        // q of this thread's rows, in two f16 parts
-        uint32_t qa[RG][D / 16][4];
-        float qs[RG];
-        q8::RowSight sight[RG];
+                const int row = __shfl_sync(Q8_FULL_MASK, rows_now, i - base);
+                if (lane == 0) {
+                    uint8_t *dst = ring + wslot * R::kStage;
+                    uint64_t *bar = bars + wslot;
+                    q8::mbar_arrive_expect_tx(bar, R::kTx);
+                    const uint32_t d = q8::smem_u32(dst), bb = q8::smem_u32(bar);
+                    constexpr int kBox = kInt8 ? D : 64;  // elements of a box row
+                    constexpr int kBoxBytes = 16 * kBox * (kInt8 ? 1 : 2);
 #pragma unroll
-        for (int rg = 0; rg < RG; ++rg) {
-            const int row = row0 + rg * 8 + gid;
-            sight[rg] = q8::attn_sight(a, u, row);
-            float2 x[D / 8];
-            float amax = 0.0f;
-            const int tok = row / a.group;
-            const float *src =
-                a.q + (static_cast<long long>(u.first + tok) * a.heads + u.kvh * a.group + (row - tok * a.group)) * D;
-#pragma unroll
-            for (int s = 0; s < D / 8; ++s) {
-                // the contraction's order is free: for int8 a thread's keys come as 8 consecutive codes
-                const int c = kInt8 ? 32 * (s / 4) + 8 * tig + 2 * (s % 4) : 8 * s + 2 * tig;
-                x[s] = row < rows ? *reinterpret_cast<const float2 *>(src + c) : make_float2(0.0f, 0.0f);
-                amax = fmaxf(amax, fmaxf(fabsf(x[s].x), fabsf(x[s].y)));
-            }
-            amax = fmaxf(amax, __shfl_xor_sync(Q8_FULL_MASK, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(Q8_FULL_MASK, amax, 2));
-            // the row's largest value to [1, 2): the low parts keep 22 bits of it
-            const int e = min(126, max(-126, static_cast<int>(__float_as_uint(amax) >> 23) - 127));
-            const float down = q8::pow2(-e);
-            qs[rg] = q8::pow2(e) * a.scale;
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                q8::split_f16(x[2 * s].x * down, x[2 * s].y * down, qa[rg][s][0], qa[rg][s][1]);
-                q8::split_f16(x[2 * s + 1].x * down, x[2 * s + 1].y * down, qa[rg][s][2], qa[rg][s][3]);
-            }
-        }
-
-        RowState<D> st[RG];
-#pragma unroll
-        for (int rg = 0; rg < RG; ++rg) {
-            st[rg].m = -INFINITY;
-            st[rg].l = 0.0f;
-            st[rg].e = -126;
-            st[rg].ie = q8::pow2(126);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) st[rg].o[i][j] = 0.0f;
-        }
-        // keys that every row of the tile sees
-        const int all_see = u.cached + (a.masks ? 0 : row0 / a.group + 1);
-
-        for (int i = 0; i < n; ++i) {
-            if (!__all_sync(Q8_FULL_MASK, q8::mbar_wait_bounded(bars + slot, phase))) {
-                // let the copies in flight land, then go on without them
-                int sl = slot, ph = phase;
-                for (int j = i; j < min(n, i + R::kStages); ++j) {
-                    q8::mbar_wait_bounded(bars + sl, ph, Q8_DRAIN_LIMIT_NS);
-                    if (++sl == R::kStages) sl = 0, ph ^= 1;
-                }
-                if (lane == 0) atomicOr(&g_rows_err, q8::kKvErrTimeout);
-                dead = true;
-                break;
-            }
-            const int key0 = k0 + i * kTile;
-            const bool masked = key0 + 16 > all_see;
-            uint8_t *stage = ring + slot * R::kStage;
-            const uint32_t sk = q8::smem_u32(stage), sv = sk + R::kMat;
-            const float *sc = reinterpret_cast<const float *>(ring_sc + slot * R::kScales);
-
-            bool wrote = false;
-            if (!kInt8 && masked) {
-                // values that no row sees must not reach the MMA as 0 * NaN: rows past the sequence become
-                // zero, and so do non-finite values of keys that some row may not see (added back at the end)
-                for (int c = lane; c < 16 * D / 8; c += 32) {
-                    uint4 *p = reinterpret_cast<uint4 *>(stage + R::kMat) + c;
-                    uint4 w = *p;
-                    uint32_t *ww = reinterpret_cast<uint32_t *>(&w);
-                    bool hit = false;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if ((ww[j] & 0x7c00u) == 0x7c00u) ww[j] &= 0xffff0000u, hit = true;
-                        if ((ww[j] & 0x7c000000u) == 0x7c000000u) ww[j] &= 0x0000ffffu, hit = true;
+                    for (int h = 0; h < D / kBox; ++h) {
+                        q8::tma_load_2d(d + h * kBoxBytes, &mk, h * kBox, row, bb);
+                        q8::tma_load_2d(d + R::kMat + h * kBoxBytes, &mv, h * kBox, row, bb);
                     }
-                    if (hit) {
-                        *p = w;
-                        wrote = true;
-                        if (key0 + ((c >> 3) & 15) < k1) s_poison = 1;
+                    if (kInt8) {
+                        q8::bulk_g2s(ring_sc + wslot * R::kScales, a.ks + row, 64, bar);
+                        q8::bulk_g2s(ring_sc + wslot * R::kScales + 64, a.vs + row, 64, bar);
                     }
                 }
-                if (wrote) q8::fence_proxy_async_smem();  // before the ring's next copy into this stage
-                __syncwarp();
-            }
+                wslot = wslot + 1 == R::kStages ? 0 : wslot + 1;
+            };
+            for (int i = 0; i < min(n, R::kStages); ++i) issue(i);
 
-            float acc[RG][2][4];
-#pragma unroll
-            for (int rg = 0; rg < RG; ++rg)
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[rg][t][j] = 0.0f;
-            if (!kInt8) {
-                const int key = ((lane >> 4) << 3) + (lane & 7);
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const int c = (s & 3) * 2 + ((lane >> 3) & 1);
-                    uint32_t b[4];
-                    ldsm4(b, sk + (s >> 2) * 2048 + key * 128 + ((c ^ (key & 7)) << 4));
-#pragma unroll
-                    for (int rg = 0; rg < RG; ++rg) {
-                        mma(acc[rg][0], qa[rg][s], b[0], b[1]);
-                        mma(acc[rg][1], qa[rg][s], b[2], b[3]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int key = 8 * t + gid;
-                        const uint2 w = *reinterpret_cast<const uint2 *>(
-                            stage + code_chunk<D>(key, 2 * c + (tig >> 1)) + (tig & 1) * 8);
-                        uint32_t b0, b1, b2, b3;
-                        q8::i8x4_to_f16x4(w.x, b0, b1);
-                        q8::i8x4_to_f16x4(w.y, b2, b3);
-#pragma unroll
-                        for (int rg = 0; rg < RG; ++rg) {
-                            mma(acc[rg][t], qa[rg][2 * c], b0, b1);
-                            mma(acc[rg][t], qa[rg][2 * c + 1], b2, b3);
-                        }
-                    }
-            }
-            float vs[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-            float2 k01, k89;
-            if (kInt8) {
-                k01 = *reinterpret_cast<const float2 *>(sc + 2 * tig);
-                k89 = *reinterpret_cast<const float2 *>(sc + 8 + 2 * tig);
-                const float2 v01 = *reinterpret_cast<const float2 *>(sc + 16 + 2 * tig);
-                const float2 v89 = *reinterpret_cast<const float2 *>(sc + 24 + 2 * tig);
-                vs[0] = v01.x, vs[1] = v01.y, vs[2] = v89.x, vs[3] = v89.y;
-            }
-            uint32_t pa[RG][4];
+            // q of this thread's rows, in two f16 parts
+            uint32_t qa[RG][D / 16][4];
+            float qs[RG];
+            q8::RowSight sight[RG];
 #pragma unroll
             for (int rg = 0; rg < RG; ++rg) {
-                float s[4];
+                const int row = row0 + rg * 8 + gid;
+                sight[rg] = q8::attn_sight(a, u, row);
+                float2 x[D / 8];
+                float amax = 0.0f;
+                const int tok = row / a.group;
+                const float *src =
+                    a.q + (static_cast<long long>(u.first + tok) * a.heads + u.kvh * a.group + (row - tok * a.group)) * D;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s[j] = (acc[rg][j >> 1][j & 1] + acc[rg][j >> 1][2 + (j & 1)]) * qs[rg];
-                if (kInt8) s[0] *= k01.x, s[1] *= k01.y, s[2] *= k89.x, s[3] *= k89.y;
-                float v[4] = {vs[0], vs[1], vs[2], vs[3]};
-                if (masked) {
+                for (int s = 0; s < D / 8; ++s) {
+                    // the contraction's order is free: for int8 a thread's keys come as 8 consecutive codes
+                    const int c = kInt8 ? 32 * (s / 4) + 8 * tig + 2 * (s % 4) : 8 * s + 2 * tig;
+                    x[s] = row < rows ? *reinterpret_cast<const float2 *>(src + c) : make_float2(0.0f, 0.0f);
+                    amax = fmaxf(amax, fmaxf(fabsf(x[s].x), fabsf(x[s].y)));
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(Q8_FULL_MASK, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(Q8_FULL_MASK, amax, 2));
+                // the row's largest value to [1, 2): the low parts keep 22 bits of it
+                const int e = min(126, max(-126, static_cast<int>(__float_as_uint(amax) >> 23) - 127));
+                const float down = q8::pow2(-e);
+                qs[rg] = q8::pow2(e) * a.scale;
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    q8::split_f16(x[2 * s].x * down, x[2 * s].y * down, qa[rg][s][0], qa[rg][s][1]);
+                    q8::split_f16(x[2 * s + 1].x * down, x[2 * s + 1].y * down, qa[rg][s][2], qa[rg][s][3]);
+                }
+            }
+
+            RowState<D> st[RG];
+#pragma unroll
+            for (int rg = 0; rg < RG; ++rg) {
+                st[rg].m = -INFINITY;
+                st[rg].l = 0.0f;
+                st[rg].e = -126;
+                st[rg].ie = q8::pow2(126);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) st[rg].o[i][j] = 0.0f;
+            }
+            // keys that every row of the tile sees
+            const int all_see = u.cached + (a.masks ? 0 : row0 / a.group + 1);
+
+            for (int i = 0; i < n; ++i) {
+                if (!__all_sync(Q8_FULL_MASK, q8::mbar_wait_bounded(bars + slot, phase))) {
+                    // let the copies in flight land, then go on without them
+                    int sl = slot, ph = phase;
+                    for (int j = i; j < min(n, i + R::kStages); ++j) {
+                        q8::mbar_wait_bounded(bars + sl, ph, Q8_DRAIN_LIMIT_NS);
+                        if (++sl == R::kStages) sl = 0, ph ^= 1;
+                    }
+                    if (lane == 0) atomicOr(&g_rows_err, q8::kKvErrTimeout);
+                    dead = true;
+                    break;
+                }
+                const int key0 = k0 + i * kTile;
+                const bool masked = key0 + 16 > all_see;
+                uint8_t *stage = ring + slot * R::kStage;
+                const uint32_t sk = q8::smem_u32(stage), sv = sk + R::kMat;
+                const float *sc = reinterpret_cast<const float *>(ring_sc + slot * R::kScales);
+
+                bool wrote = false;
+                if (!kInt8 && masked) {
+                    // values that no row sees must not reach the MMA as 0 * NaN: rows past the sequence become
+                    // zero, and so do non-finite values of keys that some row may not see (added back at the end)
+                    for (int c = lane; c < 16 * D / 8; c += 32) {
+                        uint4 *p = reinterpret_cast<uint4 *>(stage + R::kMat) + c;
+                        uint4 w = *p;
+                        uint32_t *ww = reinterpret_cast<uint32_t *>(&w);
+                        bool hit = false;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if ((ww[j] & 0x7c00u) == 0x7c00u) ww[j] &= 0xffff0000u, hit = true;
+                            if ((ww[j] & 0x7c000000u) == 0x7c000000u) ww[j] &= 0x0000ffffu, hit = true;
+                        }
+                        if (hit) {
+                            *p = w;
+                            wrote = true;
+                            if (key0 + ((c >> 3) & 15) < k1) s_poison = 1;
+                        }
+                    }
+                    if (wrote) q8::fence_proxy_async_smem();  // before the ring's next copy into this stage
+                    __syncwarp();
+                }
+
+                float acc[RG][2][4];
+#pragma unroll
+                for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[rg][t][j] = 0.0f;
+                if (!kInt8) {
+                    const int key = ((lane >> 4) << 3) + (lane & 7);
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s) {
+                        const int c = (s & 3) * 2 + ((lane >> 3) & 1);
+                        uint32_t b[4];
+                        ldsm4(b, sk + (s >> 2) * 2048 + key * 128 + ((c ^ (key & 7)) << 4));
+#pragma unroll
+                        for (int rg = 0; rg < RG; ++rg) {
+                            mma(acc[rg][0], qa[rg][s], b[0], b[1]);
+                            mma(acc[rg][1], qa[rg][s], b[2], b[3]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const int key = 8 * t + gid;
+                            const uint2 w = *reinterpret_cast<const uint2 *>(
+                                stage + code_chunk<D>(key, 2 * c + (tig >> 1)) + (tig & 1) * 8);
+                            uint32_t b0, b1, b2, b3;
+                            q8::i8x4_to_f16x4(w.x, b0, b1);
+                            q8::i8x4_to_f16x4(w.y, b2, b3);
+#pragma unroll
+                            for (int rg = 0; rg < RG; ++rg) {
+                                mma(acc[rg][t], qa[rg][2 * c], b0, b1);
+                                mma(acc[rg][t], qa[rg][2 * c + 1], b2, b3);
+                            }
+                        }
+                }
+                float vs[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+                float2 k01, k89;
+                if (kInt8) {
+                    k01 = *reinterpret_cast<const float2 *>(sc + 2 * tig);
+                    k89 = *reinterpret_cast<const float2 *>(sc + 8 + 2 * tig);
+                    const float2 v01 = *reinterpret_cast<const float2 *>(sc + 16 + 2 * tig);
+                    const float2 v89 = *reinterpret_cast<const float2 *>(sc + 24 + 2 * tig);
+                    vs[0] = v01.x, vs[1] = v01.y, vs[2] = v89.x, vs[3] = v89.y;
+                }
+                uint32_t pa[RG][4];
+#pragma unroll
+                for (int rg = 0; rg < RG; ++rg) {
+                    float s[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (!q8::attn_sees(sight[rg], u.cached, key0 + 8 * (j >> 1) + 2 * tig + (j & 1)))
-                            s[j] = -INFINITY, v[j] = 0.0f;
-                }
-                weights<D, kInt8>(st[rg], s, v, pa[rg]);
-            }
-            if (!kInt8) {
-                const int key = (((lane >> 3) & 1) << 3) + (lane & 7);
+                        s[j] = (acc[rg][j >> 1][j & 1] + acc[rg][j >> 1][2 + (j & 1)]) * qs[rg];
+                    if (kInt8) s[0] *= k01.x, s[1] *= k01.y, s[2] *= k89.x, s[3] *= k89.y;
+                    float v[4] = {vs[0], vs[1], vs[2], vs[3]};
+                    if (masked) {
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    const int c = (j & 3) * 2 + (lane >> 4);
-                    uint32_t b[4];
-                    ldsm4t(b, sv + (j >> 2) * 2048 + key * 128 + ((c ^ (key & 7)) << 4));
-#pragma unroll
-                    for (int rg = 0; rg < RG; ++rg) {
-                        mma(st[rg].o[2 * j], pa[rg], b[0], b[1]);
-                        mma(st[rg].o[2 * j + 1], pa[rg], b[2], b[3]);
+                        for (int j = 0; j < 4; ++j)
+                            if (!q8::attn_sees(sight[rg], u.cached, key0 + 8 * (j >> 1) + 2 * tig + (j & 1)))
+                                s[j] = -INFINITY, v[j] = 0.0f;
                     }
+                    weights<D, kInt8>(st[rg], s, v, pa[rg]);
                 }
-            } else {
-                // output column gid of tile 4*j + x is value dimension 4*(gid + 8*j) + x: a thread's four
-                // codes of a key are then one word, and pairs of keys interleave by byte permutes
-                const uint8_t *vb = stage + R::kMat;
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                    const int wi = gid + 8 * j;
-                    uint32_t w[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int key = 2 * tig + (x & 1) + 8 * (x >> 1);
-                        w[x] = *reinterpret_cast<const uint32_t *>(vb + code_chunk<D>(key, wi >> 2) + (wi & 3) * 4);
-                    }
-                    uint32_t b[4][2];
-                    q8::i8x4_to_f16x4(__byte_perm(w[0], w[1], 0x5140), b[0][0], b[1][0]);
-                    q8::i8x4_to_f16x4(__byte_perm(w[0], w[1], 0x7362), b[2][0], b[3][0]);
-                    q8::i8x4_to_f16x4(__byte_perm(w[2], w[3], 0x5140), b[0][1], b[1][1]);
-                    q8::i8x4_to_f16x4(__byte_perm(w[2], w[3], 0x7362), b[2][1], b[3][1]);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-#pragma unroll
-                        for (int rg = 0; rg < RG; ++rg) mma(st[rg].o[4 * j + x], pa[rg], b[x][0], b[x][1]);
-                }
-            }
-            if (++slot == R::kStages) slot = 0, phase ^= 1;
-            __syncwarp();  // every lane has read the stage
-            if (i + R::kStages < n) issue(i + R::kStages);
-        }
-
-        // join the warps: numerators to shared memory (the rings are empty now), scaled by 2^e at the read
-        __syncthreads();
-        float *om = reinterpret_cast<float *>(sm);
-#pragma unroll
-        for (int rg = 0; rg < RG; ++rg) {
-            float l = st[rg].l;
-            l += __shfl_xor_sync(Q8_FULL_MASK, l, 1);
-            l += __shfl_xor_sync(Q8_FULL_MASK, l, 2);
-            const int r = rg * 8 + gid;
-            if (tig == 0) {
-                s_m[warp][r] = st[rg].m;
-                s_l[warp][r] = l;
-                s_f[warp][r] = kInt8 ? q8::pow2(st[rg].e) : 1.0f;
-            }
-            float *o = om + (warp * kRows + r) * D;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const float x = st[rg].o[i][0] + st[rg].o[i][2], y = st[rg].o[i][1] + st[rg].o[i][3];
                 if (!kInt8) {
-                    *reinterpret_cast<float2 *>(o + 8 * i + 2 * tig) = make_float2(x, y);
+                    const int key = (((lane >> 3) & 1) << 3) + (lane & 7);
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        const int c = (j & 3) * 2 + (lane >> 4);
+                        uint32_t b[4];
+                        ldsm4t(b, sv + (j >> 2) * 2048 + key * 128 + ((c ^ (key & 7)) << 4));
+#pragma unroll
+                        for (int rg = 0; rg < RG; ++rg) {
+                            mma(st[rg].o[2 * j], pa[rg], b[0], b[1]);
+                            mma(st[rg].o[2 * j + 1], pa[rg], b[2], b[3]);
+                        }
+                    }
                 } else {
-                    const int c = 4 * (2 * tig + 8 * (i >> 2)) + (i & 3);
-                    o[c] = x;
-                    o[c + 4] = y;
+                    // output column gid of tile 4*j + x is value dimension 4*(gid + 8*j) + x: a thread's four
+                    // codes of a key are then one word, and pairs of keys interleave by byte permutes
+                    const uint8_t *vb = stage + R::kMat;
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) {
+                        const int wi = gid + 8 * j;
+                        uint32_t w[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int key = 2 * tig + (x & 1) + 8 * (x >> 1);
+                            w[x] = *reinterpret_cast<const uint32_t *>(vb + code_chunk<D>(key, wi >> 2) + (wi & 3) * 4);
+                        }
+                        uint32_t b[4][2];
+                        q8::i8x4_to_f16x4(__byte_perm(w[0], w[1], 0x5140), b[0][0], b[1][0]);
+                        q8::i8x4_to_f16x4(__byte_perm(w[0], w[1], 0x7362), b[2][0], b[3][0]);
+                        q8::i8x4_to_f16x4(__byte_perm(w[2], w[3], 0x5140), b[0][1], b[1][1]);
+                        q8::i8x4_to_f16x4(__byte_perm(w[2], w[3], 0x7362), b[2][1], b[3][1]);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int rg = 0; rg < RG; ++rg) mma(st[rg].o[4 * j + x], pa[rg], b[x][0], b[x][1]);
+                    }
+                }
+                if (++slot == R::kStages) slot = 0, phase ^= 1;
+                __syncwarp();  // every lane has read the stage
+                if (i + R::kStages < n) issue(i + R::kStages);
+            }
+
+            // join the warps: numerators to shared memory (the rings are empty now), scaled by 2^e at the read
+            __syncthreads();
+            float *om = reinterpret_cast<float *>(sm);
+#pragma unroll
+            for (int rg = 0; rg < RG; ++rg) {
+                float l = st[rg].l;
+                l += __shfl_xor_sync(Q8_FULL_MASK, l, 1);
+                l += __shfl_xor_sync(Q8_FULL_MASK, l, 2);
+                const int r = rg * 8 + gid;
+                if (tig == 0) {
+                    s_m[warp][r] = st[rg].m;
+                    s_l[warp][r] = l;
+                    s_f[warp][r] = kInt8 ? q8::pow2(st[rg].e) : 1.0f;
+                }
+                float *o = om + (warp * kRows + r) * D;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const float x = st[rg].o[i][0] + st[rg].o[i][2], y = st[rg].o[i][1] + st[rg].o[i][3];
+                    if (!kInt8) {
+                        *reinterpret_cast<float2 *>(o + 8 * i + 2 * tig) = make_float2(x, y);
+                    } else {
+                        const int c = 4 * (2 * tig + 8 * (i >> 2)) + (i & 3);
+                        o[c] = x;
+                        o[c + 4] = y;
+                    }
                 }
             }
-        }
-        __syncthreads();
-        const bool partial = t0 > 0 || t1 < u.tiles;
-        const int pslot = 2 * cta + (first ? 0 : 1);
-        const int poison = s_poison;
-        for (int i = tid; i < kRows * D / 4; i += kThreads) {
-            const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-            float m = -INFINITY;
+            __syncthreads();
+            const bool partial = ta > 0 || tb < u.tiles, rows_out = t1 == tb && !partial;
+            const int pslot = 2 * cta + (first ? 0 : 1);
+            const int poison = s_poison;
+            for (int i = tid; i < kRows * D / 4; i += kThreads) {
+                const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+                float m = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w][r]);
-            float l = 0.0f;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w][r]);
+                float l = 0.0f;
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = s_m[w][r] == -INFINITY ? 0.0f : s_m[w][r] == m ? 1.0f : q8::exp2_approx(s_m[w][r] - m);
-                l += f * s_l[w][r];
-                const float4 x = *reinterpret_cast<const float4 *>(om + (w * kRows + r) * D + c);
-                const float g = s_f[w][r];
-                o.x += f * (g * x.x), o.y += f * (g * x.y), o.z += f * (g * x.z), o.w += f * (g * x.w);
-            }
-            if (!kInt8 && poison) {  // the non-finite values that were left out, for the rows that see them
-                const q8::RowSight sg = q8::attn_sight(a, u, row0 + r);
-                for (int key = max(t0 * kTile, (u.cached & ~15) - 16); key < k1; ++key) {
-                    if (!q8::attn_sees(sg, u.cached, key)) continue;
-                    const int pi = key / a.page;
-                    const int pg = a.table[static_cast<long long>(u.b) * a.max_pages + pi];
-                    if (pg < 0 || pg >= a.n_pages) continue;
-                    const long long row =
-                        static_cast<long long>(pg * a.kv_heads + u.kvh) * a.page + (key - pi * a.page);
-                    const __half *v = reinterpret_cast<const __half *>(a.v16) + row * D + c;
-                    const float x[4] = {__half2float(v[0]), __half2float(v[1]), __half2float(v[2]), __half2float(v[3])};
-                    if (!(fabsf(x[0]) <= 65504.0f)) o.x += x[0];
-                    if (!(fabsf(x[1]) <= 65504.0f)) o.y += x[1];
-                    if (!(fabsf(x[2]) <= 65504.0f)) o.z += x[2];
-                    if (!(fabsf(x[3]) <= 65504.0f)) o.w += x[3];
+                for (int w = 0; w < kWarps; ++w) {
+                    const float f = s_m[w][r] == -INFINITY ? 0.0f : s_m[w][r] == m ? 1.0f : q8::exp2_approx(s_m[w][r] - m);
+                    l += f * s_l[w][r];
+                    const float4 x = *reinterpret_cast<const float4 *>(om + (w * kRows + r) * D + c);
+                    const float g = s_f[w][r];
+                    o.x += f * (g * x.x), o.y += f * (g * x.y), o.z += f * (g * x.z), o.w += f * (g * x.w);
+                }
+                if (!kInt8 && poison) {  // the non-finite values that were left out, for the rows that see them
+                    const q8::RowSight sg = q8::attn_sight(a, u, row0 + r);
+                    for (int key = max(t0 * kTile, (u.cached & ~15) - 16); key < k1; ++key) {
+                        if (!q8::attn_sees(sg, u.cached, key)) continue;
+                        const int pi = key / a.page;
+                        const int pg = a.table[static_cast<long long>(u.b) * a.max_pages + pi];
+                        if (pg < 0 || pg >= a.n_pages) continue;
+                        const long long row =
+                            static_cast<long long>(pg * a.kv_heads + u.kvh) * a.page + (key - pi * a.page);
+                        const __half *v = reinterpret_cast<const __half *>(a.v16) + row * D + c;
+                        const float x[4] = {__half2float(v[0]), __half2float(v[1]), __half2float(v[2]), __half2float(v[3])};
+                        if (!(fabsf(x[0]) <= 65504.0f)) o.x += x[0];
+                        if (!(fabsf(x[1]) <= 65504.0f)) o.y += x[1];
+                        if (!(fabsf(x[2]) <= 65504.0f)) o.z += x[2];
+                        if (!(fabsf(x[3]) <= 65504.0f)) o.w += x[3];
+                    }
+                }
+                float4 *sum = reinterpret_cast<float4 *>(a.part + (static_cast<long long>(pslot) * kRows + r) * D + c);
+                if (t0 > ta) {  // the chains before, by the thread that wrote them
+                    const float2 ml = s_sum[r];
+                    const float4 x = *sum;
+                    const float mn = fmaxf(m, ml.x);
+                    const float f = m == -INFINITY ? 0.0f : m == mn ? 1.0f : q8::exp2_approx(m - mn);
+                    const float g = ml.x == -INFINITY ? 0.0f : ml.x == mn ? 1.0f : q8::exp2_approx(ml.x - mn);
+                    o = make_float4(f * o.x + g * x.x, f * o.y + g * x.y, f * o.z + g * x.z, f * o.w + g * x.w);
+                    l = f * l + g * ml.y;
+                    m = mn;
+                }
+                if (!rows_out) {
+                    *sum = o;
+                    if (c == 0) {
+                        s_next[r] = make_float2(m, l);
+                        if (partial && t1 == tb) a.ml[pslot * kRows + r] = make_float2(m, l);
+                    }
+                } else {
+                    q8::attn_store<D>(a, u, row0 + r, c, o, l, row0 + r < rows);
                 }
             }
-            if (partial) {
-                *reinterpret_cast<float4 *>(a.part + (static_cast<long long>(pslot) * kRows + r) * D + c) = o;
-                if (c == 0) a.ml[pslot * kRows + r] = make_float2(m, l);
-            } else {
-                q8::attn_store<D>(a, u, row0 + r, c, o, l, row0 + r < rows);
+            if (partial && first && t1 == tb && tid == 0) {
+                a.desc[2 * cta] = make_int4(u.start, u.start + kHead + u.tiles, per, u.start + kHead);
+                a.desc[2 * cta + 1] = make_int4(u.b, u.kvh, u.rt, 1);
             }
-        }
-        if (partial && first && tid == 0) {
-            a.desc[2 * cta] = make_int4(u.start, u.start + kHead + u.tiles, per, u.start + kHead);
-            a.desc[2 * cta + 1] = make_int4(u.b, u.kvh, u.rt, 1);
-        }
-        if (pos < s1) {  // the ring's next copies come after these reads and writes
-            q8::fence_proxy_async_smem();
-            __syncthreads();
-            if (tid == 0) s_poison = 0;
-            __syncthreads();
+            if (pos < s1 || t1 < tb) {  // the ring's next copies come after these reads and writes
+                q8::fence_proxy_async_smem();
+                __syncthreads();
+                if (tid == 0) s_poison = 0;
+                if (tid < kRows) s_sum[tid] = s_next[tid];
+                __syncthreads();
+            }
         }
     }
     if (bad_data) atomicOr(&g_rows_err, q8::kKvErrData);

@@ -7,20 +7,28 @@
 // (22 bits), both parts are multiplied with the same key or value tile into
 // the same f32 accumulator, so a tile costs 2 * (D/16 + 8) MMAs of K = 16.
 //
-// Two softmax warpgroups take the tiles in turn, each with a score buffer and
-// an accumulator of its own in tensor memory (S0, S1, O0, O1: 512 columns for
-// D = 128), its own (m, l), joined once per piece, and its own MMA-issuing
-// warp: they never wait for each other, and while one computes weights the
-// tensor core works on the other's scores or product.  (With one issuing
-// warp the tensor core stood still for a third of the time: it queues only a
-// few MMAs ahead, and each wait of the issuing warp takes some 300 cycles.)  P overwrites S in place (64 columns of high parts, 64 of low
-// parts) and is the second product's A operand from tensor memory.  V is used
-// as it lies in the cache ([key][dim], N-major).
+// Tensor memory (512 columns): two score buffers of 128 columns, O and the sum
+// of earlier Os (kChain, below).  P overwrites S in place (64 columns of high
+// parts, 64 of low parts) and is the second product's A operand; V is used as
+// it lies in the cache ([key][dim], N-major).  With two buffers the next
+// tile's scores are there before this tile's weights are done.
 //
-// Roles: warp 0 copies K and V tiles (one TMA box per run of keys that share
-// a page), warps 1 and 3 issue the MMAs, warps 4-11 are the softmax warpgroups; for
-// int8, warps 12-15 widen the codes to f16 tiles (exact), a key's scale
-// multiplies its score column and a value's scale its weight column.
+// Eight softmax warps work on every tile, 16 rows each (two warps per lane
+// quarter of tensor memory): a tile's weights take half the time that four
+// warps would need, and a row has one owner for the whole unit, so there is
+// one (m, l), one O and nothing to join at the end.  Scores are read in the
+// 16x256b shape: a thread has two rows at 32 columns each, 64 registers hold
+// all it needs between the maximum and the weights, and a key's scale is read
+// once for two rows.
+//
+// Roles: warp 0 copies K and V tiles (one TMA box per run of keys that share a
+// page); warp 1 issues the scores' MMAs and warp 3 the products' (one warp for
+// both left the tensor core idle a third of the time: it queues only a few
+// MMAs ahead, and every wait of the issuing warp is a gap); warps 4-11 are the
+// softmax warps; for int8, warps 12-15 widen the codes to f16 tiles (exact), a
+// key's scale multiplies its score column and a value's scale its weight
+// column.  At a unit's end the next unit's queries go to shared memory before
+// the rows go out, so its first scores are computed meanwhile.
 //
 // Every mbarrier wait is bounded; one that runs out raises the CTA's abort
 // flag and the error word, and all roles drain and exit.
@@ -42,13 +50,18 @@ constexpr int kHead = 3;             // what a unit costs beside its tiles, in t
 constexpr float kWeightBits = 6.0f;  // weights are 2^(s - m + 6): below 2^14 while m may lag by 2^8
 constexpr float kRaise = 8.0f;
 constexpr int kScaleSlots = 4;
+// The tensor core's f32 accumulation truncates: O loses about 1e-7 of itself
+// per MMA, always towards zero (measured: 2.8e-5 after 31 tiles of 16 MMAs
+// with values of one sign).  After kChain tiles O is therefore added to a sum
+// of its own, rounded to nearest, and starts again.
+constexpr int kChain = 4;
 
 template <int D, bool kInt8>
 struct Lay {
     static constexpr int kThreads = kInt8 ? 512 : 384;
     // registers per thread after setmaxnreg; their sum is the launch's
     static constexpr int kRegsLaunch = kInt8 ? 128 : 168;
-    static constexpr int kRegsSoft = kInt8 ? 176 : 208, kRegsCtl = kInt8 ? 56 : 88, kRegsConv = 104;
+    static constexpr int kRegsSoft = kInt8 ? 176 : 184, kRegsCtl = kInt8 ? 80 : 136, kRegsConv = 80;
     static_assert(256 * kRegsSoft + 128 * kRegsCtl + (kInt8 ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch, "registers");
 
     static constexpr int kMat = 128 * D * 2;            // a 128-row f16 tile
@@ -60,20 +73,19 @@ struct Lay {
     static constexpr int kRaw = 128 * D;
     static constexpr int offScale = offRaw + (kInt8 ? 4 * kRaw : 0);   // slots of 128 k scales, 128 v scales
     static constexpr int offRow = offScale + (kInt8 ? kScaleSlots * 1024 : 0);
-    // per row: q scale; m, l and 2^e of each warpgroup
-    static constexpr int offBar = offRow + 128 * 4 * 7;
+    static constexpr int offBar = offRow + 2 * 128 * 4;  // before it: q scales of this unit and the next
     // barriers, by index
-    // f16 tiles: full, empty; by the tile's parity, for int8 too (one buffer, but tiles in turn have issuing warps of
-    // their own, and a warp that sees every other phase of one barrier could not tell them apart)
+    // f16 tiles: full, empty, by the tile's parity (for int8 one buffer, still two barriers)
     static constexpr int bKf = 0, bKe = 2, bVf = 4, bVe = 6;
     static constexpr int bRKf = 8, bRKe = 10, bRVf = 12, bRVe = 14;  // int8 codes
-    static constexpr int bCf = 16, bCe = 20;                      // int8 scales
-    static constexpr int bSf = 24, bPf = 26, bQf = 28, bOf = 29, bDrain = 30, kBars = 32;
+    static constexpr int bCf = 16, bCe = 20;                         // int8 scales
+    // scores written; weights written; products done, so the score buffer is free again; queries written
+    static constexpr int bSf = 24, bPf = 26, bSe = 28, bQf = 30, bDrain = 31, kBars = 33;
     static constexpr int offMisc = offBar + kBars * 8 + 8;
     static constexpr int offPre = offMisc + 32;
     static int smem(int batch) { return offPre + (batch + 1) * 4 + 1024; }
     static_assert(offPre + (Q8_KV_MAX_BATCH + 1) * 4 + 1024 <= 227 * 1024, "shared memory");
-    static constexpr int kColO = 256;                   // S0, S1 at 0, 128; O0, O1 from here
+    static constexpr int kColO = 256, kColSum = 384;    // the score buffers lie before them
 };
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -125,15 +137,22 @@ __device__ __forceinline__ void tc_ld16x64(uint32_t taddr, uint32_t *r)
         : "r"(taddr));
 }
 
-__device__ __forceinline__ void tc_st16x64(uint32_t taddr, const uint32_t *r)
+// The same with 32 columns (16x256b, 4 repetitions).
+__device__ __forceinline__ void tc_ld16x32(uint32_t taddr, uint32_t *r)
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tc_st16x32w(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
@@ -150,14 +169,16 @@ __device__ __forceinline__ void tc_st16x32(uint32_t taddr, const uint32_t *r)
 }
 
 // No use of the registers is scheduled before the wait that precedes this.
+__device__ __forceinline__ void tc_regs16(uint32_t *r)
+{
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
 __device__ __forceinline__ void tc_regs32(uint32_t *r)
 {
-#pragma unroll
-    for (int i = 0; i < 32; i += 16)
-        asm volatile(""
-                     : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
-                       "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
-                       "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]));
+    tc_regs16(r);
+    tc_regs16(r + 16);
 }
 
 // Shared-memory matrix descriptor, 128-byte swizzle: rows of 128 bytes in
@@ -308,7 +329,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::offBar);
     const uint32_t bar0 = base + L::offBar;
     auto bar = [&](int i) { return bar0 + 8u * i; };
-    float *s_row = reinterpret_cast<float *>(sm + L::offRow);  // [0]: q scale, [1 + 3g ..]: m, l, 2^e of warpgroup g
+    float *s_row = reinterpret_cast<float *>(sm + L::offRow);  // the rows' q scales, of this unit and the next
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::offMisc);
     volatile int *s_stop = abort_flag + 1, *s_poison = abort_flag + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::offMisc + 16);
@@ -320,10 +341,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         *s_poison = 0;
         for (int i = 0; i < L::kBars; ++i) {
             int count = 1;  // TMA bytes or a commit
-            if (i == L::bCe || (i > L::bCe && i < L::bCe + kScaleSlots)) count = 128;  // the tile's warpgroup
-            if (i >= L::bPf && i < L::bPf + 2) count = 128;
-            if (i == L::bQf) count = 256;
-            if (i == L::bOf) count = 2;  // a commit of each issuing warp
+            if (i >= L::bCe && i < L::bCe + kScaleSlots) count = 8;  // softmax warps
+            if (i >= L::bPf && i < L::bPf + 2) count = 8;
+            if (i == L::bQf) count = 8;
             if (kInt8 && ((i >= L::bKf && i < L::bKf + 2) || (i >= L::bVf && i < L::bVf + 2))) count = 128;  // widening warps
             if ((i >= L::bRKe && i < L::bRKe + 2) || (i >= L::bRVe && i < L::bRVe + 2)) count = 128;
             q8::mbar_init(bars + i, count);
@@ -428,85 +448,92 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 drain_bar(bar((kInt8 ? L::bRVf : L::bVf) + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u);
             for (int t = max(0, nc - kScaleSlots); t < nc; ++t)
                 drain_bar(bar(L::bCf + t % kScaleSlots), static_cast<uint32_t>(t / kScaleSlots) & 1u);
-        } else if (warp & 1) {
-            // -------------------------------------------------------- MMAs: warp 1 for warpgroup 0's tiles, warp 3 for 1's
-            constexpr uint32_t iS = idesc_f16(kTile, false), iO = idesc_f16(D, true);
-            const int b = warp >> 1;
+        } else if (warp == 1) {
+            // -------------------------------------------------------- scores
+            constexpr uint32_t iS = idesc_f16(kTile, false);
             const uint32_t one = lane == 0;
             const uint32_t tm = __shfl_sync(Q8_FULL_MASK, tmem, 0);
-            const uint32_t ts = tm + 128u * b, to = tm + L::kColO + D * b;
             int T = 0;
-            uint32_t piece = 0, pph = 0;
+            uint32_t piece = 0;
             bool ok = true;
-            auto scores = [&](int t) {
-                if (!warp_wait(bar(L::bKf + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u, abort_flag)) return false;
-                tc_fence_after();
-                const uint64_t k = desc128(base + L::offK + (t % L::kBufs) * L::kMat, 16, 1024);
-#pragma unroll
-                for (int part = 1; part >= 0; --part) {  // low parts first: the accumulator is small while they are added
-                    const uint64_t q = desc128(base + L::offQ + part * L::kMat, 16, 1024);
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s) {
-                        const uint32_t o = ((s >> 2) * 16384 + (s & 3) * 32) >> 4;
-                        mma_ss(ts, q + o, k + o, iS, part == 0 || s > 0, one);
-                    }
-                }
-                if (one) {
-                    tc_commit(bar(L::bSf + b));
-                    tc_commit(bar(L::bKe + (t & 1)));
-                }
-                __syncwarp();
-                return true;
-            };
             while (ok && w.next(a, pre)) {
                 ok = warp_wait(bar(L::bQf), piece & 1u, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                if (b < w.n) ok = scores(T + b);
-                for (int i = b; ok && i < w.n; i += 2) {
-                    const int t = T + i;
-                    ok = warp_wait(bar(L::bVf + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u, abort_flag) &&
-                         warp_wait(bar(L::bPf + b), pph, abort_flag);
+                ++piece;
+                for (int i = 0; ok && i < w.n; ++i, ++T) {
+                    const int b = T & 1;
+                    ok = warp_wait(bar(L::bKf + (T & 1)), static_cast<uint32_t>(T >> 1) & 1u, abort_flag) &&
+                         warp_wait(bar(L::bSe + b), (static_cast<uint32_t>(T >> 1) & 1u) ^ 1u, abort_flag);
                     if (!ok) break;
-                    pph ^= 1u;
                     tc_fence_after();
-                    const uint64_t v = desc128(base + L::offV + (t % L::kBufs) * L::kMat, 16384, 1024);
+                    const uint64_t k = desc128(base + L::offK + (T % L::kBufs) * L::kMat, 16, 1024);
+#pragma unroll
+                    for (int part = 1; part >= 0; --part) {  // low parts first: the accumulator is small meanwhile
+                        const uint64_t q = desc128(base + L::offQ + part * L::kMat, 16, 1024);
+#pragma unroll
+                        for (int s = 0; s < D / 16; ++s) {
+                            const uint32_t o = ((s >> 2) * 16384 + (s & 3) * 32) >> 4;
+                            mma_ss(tm + 128u * b, q + o, k + o, iS, part == 0 || s > 0, one);
+                        }
+                    }
+                    if (one) {
+                        tc_commit(bar(L::bSf + b));
+                        tc_commit(bar(L::bKe + (T & 1)));
+                    }
+                    __syncwarp();
+                }
+            }
+            // every MMA issued must be complete before tensor memory is freed
+            if (one) {
+                tc_commit(bar(L::bDrain));
+                drain_bar(bar(L::bDrain), 0);
+            }
+        } else if (warp == 3) {
+            // -------------------------------------------------------- products
+            constexpr uint32_t iO = idesc_f16(D, true);
+            const uint32_t one = lane == 0;
+            const uint32_t tm = __shfl_sync(Q8_FULL_MASK, tmem, 0);
+            int T = 0;
+            bool ok = true;
+            while (ok && w.next(a, pre)) {
+                for (int i = 0; i < w.n; ++i, ++T) {
+                    const int b = T & 1;
+                    ok = warp_wait(bar(L::bVf + (T & 1)), static_cast<uint32_t>(T >> 1) & 1u, abort_flag) &&
+                         warp_wait(bar(L::bPf + b), static_cast<uint32_t>(T >> 1) & 1u, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t v = desc128(base + L::offV + (T % L::kBufs) * L::kMat, 16384, 1024);
 #pragma unroll
                     for (int part = 1; part >= 0; --part)
 #pragma unroll
                         for (int s = 0; s < kTile / 16; ++s)
-                            mma_ts(to, ts + 64u * part + 8u * s, v + ((2048u * s) >> 4), iO, part == 0 || s > 0 || i >= 2, one);
-                    if (one) tc_commit(bar(L::bVe + (t & 1)));
+                            mma_ts(tm + L::kColO, tm + 128u * b + 64u * part + 8u * s, v + ((2048u * s) >> 4), iO,
+                                   part == 0 || s > 0 || i % kChain > 0, one);
+                    if (one) {
+                        tc_commit(bar(L::bSe + b));
+                        tc_commit(bar(L::bVe + (T & 1)));
+                    }
                     __syncwarp();
-                    if (i + 2 < w.n) ok = scores(t + 2);  // after the products that read P from the same columns
                 }
-                if (!ok) break;
-                if (one) tc_commit(bar(L::bOf));
-                __syncwarp();
-                T += w.n;
-                ++piece;
             }
-            // every MMA issued must be complete before tensor memory is freed
             if (one) {
-                tc_commit(bar(L::bDrain + b));
-                drain_bar(bar(L::bDrain + b), 0);
+                tc_commit(bar(L::bDrain + 1));
+                drain_bar(bar(L::bDrain + 1), 0);
             }
         }
         __syncwarp();
     } else if (warp < 12) {
         setmaxnreg_inc<L::kRegsSoft>();
-        // ------------------------------------------------------------ softmax: a thread owns row r of the unit's tile
-        const int wg = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
-        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-        const uint32_t ts = tl + 128u * wg, to = tl + L::kColO + D * wg;
+        // ------------------------------------------------------------ softmax
+        const int sw = warp - 4, g = lane >> 2, c2 = 2 * (lane & 3);
+        const int r0 = (warp & 3) * 32 + 16 * (sw >> 2) + g;  // this thread's rows of the tile: r0 and r0 + 8
+        const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32 + 16 * (sw >> 2)) << 16);
         int T = 0;
-        uint32_t piece = 0, sph = 0;
+        uint32_t piece = 0;
         if (tid == 128) a.desc[2 * cta + 1].w = 0;  // no first piece yet
-        // Q: a warp per row (D = 128) or two rows (D = 64), eight warps.  A unit's rows are in registers before the unit
-        // before it is finished.
+        // Q: a warp per row (D = 128) or two rows (D = 64), eight warps
         constexpr int kPer = D == 128 ? 1 : 2, kLanes = 32 / kPer, kLoads = 16 / kPer;
         const int sub = lane % kLanes;
-        auto q_row = [&](int j) { return ((warp - 4) + 8 * j) * kPer + lane / kLanes; };
+        auto q_row = [&](int j) { return (sw + 8 * j) * kPer + lane / kLanes; };
         float4 x[kLoads];
         auto load_q = [&](const Unit &u) {
             const q8::RowMap map(a, u.rt * kRows);
@@ -518,380 +545,376 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 if (rr < rows) x[j] = __ldg(reinterpret_cast<const float4 *>(a.q + map.at(a, u, rr, D)) + sub);
             }
         };
+        auto write_q = [&](float *scales) {
+            // the row's largest value goes to [1, 2), the sign of the scale (or a scale of 0) into q: hidden scores
+            // become -inf before they are scaled, so the scale of a row is never 0
+            const float sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int rr = q_row(j);
+                // magnitudes order as their bits do; a NaN's exponent is clamped like an infinity's
+                uint32_t top = __float_as_uint(fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)), fmaxf(fabsf(x[j].z), fabsf(x[j].w))));
+                if (D == 128) {
+                    top = __reduce_max_sync(Q8_FULL_MASK, top);
+                } else {
+#pragma unroll
+                    for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(Q8_FULL_MASK, top, o));
+                }
+                const int e = min(126, max(-126, static_cast<int>(top >> 23) - 127));
+                const float down = q8::pow2(-e) * sign;
+                uint2 hi, lo;
+                q8::split_f16(x[j].x * down, x[j].y * down, hi.x, lo.x);
+                q8::split_f16(x[j].z * down, x[j].w * down, hi.y, lo.y);
+                const int off = (sub >> 4) * 16384 + rr * 128 + ((((sub & 15) >> 1) ^ (rr & 7)) << 4) + (sub & 1) * 8;
+                *reinterpret_cast<uint2 *>(sm + L::offQ + off) = hi;
+                *reinterpret_cast<uint2 *>(sm + L::offQ + L::kMat + off) = lo;
+                if (sub == 0) scales[rr] = fmaxf(q8::pow2(e) * fabsf(a.scale), 1.17549435e-38f);
+            }
+            q8::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(bar(L::bQf));
+        };
+        // Products of tiles up to t complete (those of t - 2 are, when the scores of t are there).
+        auto products_done = [&](int t) {
+            return warp_wait(bar(L::bSe + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u, abort_flag);
+        };
         bool more = w.next(a, pre);
-        if (more) load_q(w.u);
+        if (more) {
+            load_q(w.u);
+            write_q(s_row);
+            soft_sync();  // the scales
+        }
         while (more) {
             const Unit &u = w.u;
             const int rows = u.fresh * a.group, row0 = u.rt * kRows;
-            {
-                // the row's largest value goes to [1, 2), the sign of the scale (or a scale of 0) into q: hidden scores
-                // become -inf before they are scaled, so the scale of a row is never 0
-                const float sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
-#pragma unroll
-                for (int j = 0; j < kLoads; ++j) {
-                    const int rr = q_row(j);
-                    // magnitudes order as their bits do; a NaN's exponent is clamped like an infinity's
-                    uint32_t top = __float_as_uint(fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)), fmaxf(fabsf(x[j].z), fabsf(x[j].w))));
-                    if (D == 128) {
-                        top = __reduce_max_sync(Q8_FULL_MASK, top);
-                    } else {
-#pragma unroll
-                        for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(Q8_FULL_MASK, top, o));
-                    }
-                    const int e = min(126, max(-126, static_cast<int>(top >> 23) - 127));
-                    const float down = q8::pow2(-e) * sign;
-                    uint2 hi, lo;
-                    q8::split_f16(x[j].x * down, x[j].y * down, hi.x, lo.x);
-                    q8::split_f16(x[j].z * down, x[j].w * down, hi.y, lo.y);
-                    const int off = (sub >> 4) * 16384 + rr * 128 + ((((sub & 15) >> 1) ^ (rr & 7)) << 4) + (sub & 1) * 8;
-                    *reinterpret_cast<uint2 *>(sm + L::offQ + off) = hi;
-                    *reinterpret_cast<uint2 *>(sm + L::offQ + L::kMat + off) = lo;
-                    if (sub == 0) s_row[rr] = fmaxf(q8::pow2(e) * fabsf(a.scale), 1.17549435e-38f);
-                }
-                q8::fence_proxy_async_smem();
-                tc_fence_before();  // the last piece's tensor-memory loads are done
-                arrive(bar(L::bQf));
-                soft_sync();
-            }
-            // Scores are read 16 rows at a time (16x256b): a thread has rows g and g + 8 of the 16 at 32 columns each, so
-            // 64 registers hold all it needs between the maximum and the weights, the keys' scales are read once for
-            // two rows, and the code runs twice a tile (a first pass through straight-line code costs its fetch).
-            const int g = lane >> 2, c2 = 2 * (lane & 3);
-            float qs[4], m[4], l[4], ie[4];
-            int e[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {  // row 16 * (x / 2) + g + 8 * (x % 2) of the warp's 32
-                qs[x] = s_row[(warp & 3) * 32 + 16 * (x >> 1) + g + 8 * (x & 1)];
-                m[x] = -INFINITY, l[x] = 0.0f, ie[x] = q8::pow2(126), e[x] = -126;
-            }
             const int all_see = u.cached + (a.masks ? 0 : row0 / a.group + 1);  // keys below are seen by every row
+            float qq[2], m[2], l[2], ii[2];
+            int e[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                qq[y] = s_row[128 * (piece & 1) + r0 + 8 * y];
+                m[y] = -INFINITY, l[y] = 0.0f, ii[y] = q8::pow2(126), e[y] = -126;
+            }
             bool ok = true;
-            for (int i = wg; i < w.n; i += 2) {
-                if (!warp_wait(bar(L::bSf + wg), sph, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                sph ^= 1u;
-                const int t = T + i, key0 = (w.t0 + i) * kTile;
+            const bool partial = w.t0 > 0 || w.n < u.tiles;
+            const int pslot = 2 * cta + (w.first ? 0 : 1);
+            float msum[2] = {-INFINITY, -INFINITY};  // the reference of the sum of earlier Os
+            for (int i = 0; ok && i < w.n; ++i) {
+                const int t = T + i, key0 = (w.t0 + i) * kTile, b = t & 1;
+                const uint32_t ts = tl + 128u * b;
                 const bool masked = key0 + kTile > min(all_see, w.kend);
                 const float *sc = reinterpret_cast<const float *>(sm + L::offScale + (t % kScaleSlots) * 1024);
-                if (kInt8 && !warp_wait(bar(L::bCf + t % kScaleSlots), static_cast<uint32_t>(t / kScaleSlots) & 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
+                ok = warp_wait(bar(L::bSf + b), static_cast<uint32_t>(t >> 1) & 1u, abort_flag) &&
+                     (!kInt8 ||
+                      warp_wait(bar(L::bCf + t % kScaleSlots), static_cast<uint32_t>(t / kScaleSlots) & 1u, abort_flag));
+                if (!ok) break;
                 tc_fence_after();
+                uint32_t s[64];
+                tc_ld16x64(ts, s);
+                tc_ld16x64(ts + 64, s + 32);
                 float all_big = 0.0f;  // int8: the tile's largest value scale
                 bool odd = masked;     // some row sees not every key, or a value scale is not finite
                 if (kInt8) {
                     const float4 v4 = *reinterpret_cast<const float4 *>(sc + 128 + 4 * lane);
-                    all_big = fmaxf(fmaxf(fabsf(v4.x), fabsf(v4.y)), fmaxf(fabsf(v4.z), fabsf(v4.w)));
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) all_big = fmaxf(all_big, __shfl_xor_sync(Q8_FULL_MASK, all_big, o));
+                    all_big = __uint_as_float(__reduce_max_sync(
+                        Q8_FULL_MASK, __float_as_uint(fmaxf(fmaxf(fabsf(v4.x), fabsf(v4.y)), fmaxf(fabsf(v4.z), fabsf(v4.w))))));
                     const float sum = (v4.x + v4.y) + (v4.z + v4.w);
                     odd |= __any_sync(Q8_FULL_MASK, !(fabsf(sum) <= 3.4028235e38f));
                 }
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t lanes = static_cast<uint32_t>(16 * half) << 16;
-                    uint32_t s[64];
-                    tc_ld16x64(ts + lanes, s);
-                    tc_ld16x64(ts + lanes + 64, s + 32);
-                    // this half's state
-                    float mm[2] = {half ? m[2] : m[0], half ? m[3] : m[1]};
-                    const float qq[2] = {half ? qs[2] : qs[0], half ? qs[3] : qs[1]};
-                    float ii[2] = {half ? ie[2] : ie[0], half ? ie[3] : ie[1]};
-                    float top[2] = {-INFINITY, -INFINITY}, big[2] = {all_big, all_big};
-                    tc_wait_ld();
-                    tc_regs32(s);
-                    tc_regs32(s + 32);
-                    if (kInt8) {  // scores by their keys' scales
+                float top[2] = {-INFINITY, -INFINITY}, big[2] = {all_big, all_big};
+                tc_wait_ld();
+                tc_regs32(s);
+                tc_regs32(s + 32);
+                if (kInt8) {  // scores by their keys' scales
 #pragma unroll
-                        for (int rep = 0; rep < 16; ++rep) {
-                            const float2 k2 = *reinterpret_cast<const float2 *>(sc + 8 * rep + c2);
+                    for (int rep = 0; rep < 16; ++rep) {
+                        const float2 k2 = *reinterpret_cast<const float2 *>(sc + 8 * rep + c2);
 #pragma unroll
-                            for (int x = 0; x < 4; x += 2) {
-                                const float2 y = __fmul2_rn(
-                                    make_float2(__uint_as_float(s[4 * rep + x]), __uint_as_float(s[4 * rep + x + 1])), k2);
-                                s[4 * rep + x] = __float_as_uint(y.x);
-                                s[4 * rep + x + 1] = __float_as_uint(y.y);
-                            }
+                        for (int y = 0; y < 4; y += 2) {
+                            const float2 z = __fmul2_rn(
+                                make_float2(__uint_as_float(s[4 * rep + y]), __uint_as_float(s[4 * rep + y + 1])), k2);
+                            s[4 * rep + y] = __float_as_uint(z.x);
+                            s[4 * rep + y + 1] = __float_as_uint(z.y);
                         }
-                    }
-                    if (odd) {
-                        // hidden keys get score -inf; int8: the largest scale is taken over what the row sees, and a
-                        // scale that is not finite makes the scores that see it NaN
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const q8::RowSight sight = q8::attn_sight(a, u, row0 + (warp & 3) * 32 + 16 * half + g + 8 * x);
-                            big[x] = 0.0f;
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const int k = key0 + 32 * c, below = max(0, min(32, sight.all - k));
-                                uint32_t see = below == 32 ? ~0u : (1u << below) - 1u;  // of keys k .. k + 31
-                                const int sh = u.cached - k;                            // bit b of the mask is key k + sh + b
-                                if (sh >= 0 && sh < 32) see |= static_cast<uint32_t>(sight.mask << sh);
-                                else if (sh < 0 && sh > -64) see |= static_cast<uint32_t>(sight.mask >> -sh);
-                                see >>= c2;
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) {  // column 8 * (j / 2) + c2 + j % 2 of the 32
-                                    uint32_t &y = s[16 * c + 4 * (j >> 1) + 2 * x + (j & 1)];
-                                    const bool seen = (see >> (8 * (j >> 1) + (j & 1))) & 1u;
-                                    if (kInt8) {
-                                        const float v = sc[128 + 32 * c + 8 * (j >> 1) + c2 + (j & 1)];
-                                        if (!(fabsf(v) <= 3.4028235e38f)) y = 0x7fffffffu;
-                                        else if (seen) big[x] = fmaxf(big[x], fabsf(v));
-                                    }
-                                    if (!seen) y = 0xff800000u;
-                                }
-                            }
-                            if (kInt8) {
-                                big[x] = fmaxf(big[x], __shfl_xor_sync(Q8_FULL_MASK, big[x], 1));
-                                big[x] = fmaxf(big[x], __shfl_xor_sync(Q8_FULL_MASK, big[x], 2));
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 64; j += 4) {
-                        top[0] = fmaxf(fmaxf(top[0], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
-                        top[1] = fmaxf(fmaxf(top[1], __uint_as_float(s[j + 2])), __uint_as_float(s[j + 3]));
-                    }
-                    bool raise = i == wg;  // the first tile sets the references
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        top[x] = fmaxf(top[x], __shfl_xor_sync(Q8_FULL_MASK, top[x], 1));
-                        top[x] = fmaxf(top[x], __shfl_xor_sync(Q8_FULL_MASK, top[x], 2));
-                        top[x] *= qq[x];
-                        raise |= top[x] > mm[x] + kRaise;
-                        if (kInt8) raise |= big[x] * ii[x] > 1.0f;
-                    }
-                    if (__any_sync(Q8_FULL_MASK, raise)) {
-                        float f[2];
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float mn = fmaxf(mm[x], top[x]);
-                            f[x] = mn == mm[x] ? 1.0f : q8::exp2_approx(mm[x] - mn);
-                            const float lx = (half ? l[2 + x] : l[x]) * f[x];
-                            if (half) l[2 + x] = lx; else l[x] = lx;
-                            mm[x] = mn;
-                            if (kInt8) {
-                                int ee = half ? e[2 + x] : e[x];
-                                const int en = min(126, max(ee, static_cast<int>(__float_as_uint(big[x]) >> 23) - 126));
-                                f[x] = ee - en < -126 ? 0.0f : f[x] * q8::pow2(ee - en);
-                                if (half) e[2 + x] = en; else e[x] = en;
-                                ii[x] = q8::pow2(-en);
-                            }
-                        }
-                        // the products so far are complete: their MMAs came before this tile's scores
-                        if (i != wg) {
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 64) {
-                                uint32_t o[32];
-                                tc_ld16x64(to + lanes + c, o);
-                                tc_wait_ld();
-                                tc_regs32(o);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[(j >> 1) & 1]);
-                                tc_st16x64(to + lanes + c, o);
-                            }
-                        }
-                    }
-                    float2 ref[2], sum[2];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float z = mm[x] == -INFINITY ? 0.0f : kWeightBits - mm[x];
-                        ref[x] = make_float2(z, z);
-                        sum[x] = make_float2(0.0f, 0.0f);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t hi[16], lo[16];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int rep = 8 * c + j;
-                            float2 v2 = make_float2(1.0f, 1.0f);
-                            if (kInt8) v2 = *reinterpret_cast<const float2 *>(sc + 128 + 8 * rep + c2);
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                float2 p = __ffma2_rn(
-                                    make_float2(__uint_as_float(s[4 * rep + 2 * x]), __uint_as_float(s[4 * rep + 2 * x + 1])),
-                                    make_float2(qq[x], qq[x]), ref[x]);
-                                p.x = q8::exp2_approx(p.x);
-                                p.y = q8::exp2_approx(p.y);
-                                sum[x] = __fadd2_rn(sum[x], p);
-                                if (kInt8) {
-                                    // at most 1 for what the row sees; a hidden key's may be anything, its weight is 0
-                                    float2 y = __fmul2_rn(v2, make_float2(ii[x], ii[x]));
-                                    y.x = fminf(fmaxf(y.x, -1.0f), 1.0f), y.y = fminf(fmaxf(y.y, -1.0f), 1.0f);
-                                    p = __fmul2_rn(p, y);
-                                }
-                                q8::split_f16(p.x, p.y, hi[2 * j + x], lo[2 * j + x]);
-                            }
-                        }
-                        tc_st16x32(ts + lanes + 32 * c, hi);
-                        tc_st16x32(ts + lanes + 64 + 32 * c, lo);
-                    }
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float sx = sum[x].x + sum[x].y;
-                        if (half) m[2 + x] = mm[x], l[2 + x] += sx, ie[2 + x] = ii[x];
-                        else m[x] = mm[x], l[x] += sx, ie[x] = ii[x];
                     }
                 }
+                if (odd) {
+                    // hidden keys get score -inf; int8: the largest scale is taken over what the row sees, and a
+                    // scale that is not finite makes the scores that see it NaN
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const q8::RowSight sight = q8::attn_sight(a, u, row0 + r0 + 8 * y);
+                        big[y] = 0.0f;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int k = key0 + 32 * c, below = max(0, min(32, sight.all - k));
+                            uint32_t see = below == 32 ? ~0u : (1u << below) - 1u;  // of keys k .. k + 31
+                            const int sh = u.cached - k;                            // bit b of the mask is key k + sh + b
+                            if (sh >= 0 && sh < 32) see |= static_cast<uint32_t>(sight.mask << sh);
+                            else if (sh < 0 && sh > -64) see |= static_cast<uint32_t>(sight.mask >> -sh);
+                            see >>= c2;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {  // column 8 * (j / 2) + c2 + j % 2 of the 32
+                                uint32_t &z = s[16 * c + 4 * (j >> 1) + 2 * y + (j & 1)];
+                                const bool seen = (see >> (8 * (j >> 1) + (j & 1))) & 1u;
+                                if (kInt8) {
+                                    const float v = sc[128 + 32 * c + 8 * (j >> 1) + c2 + (j & 1)];
+                                    if (!(fabsf(v) <= 3.4028235e38f)) z = 0x7fffffffu;
+                                    else if (seen) big[y] = fmaxf(big[y], fabsf(v));
+                                }
+                                if (!seen) z = 0xff800000u;
+                            }
+                        }
+                        if (kInt8) {
+                            big[y] = fmaxf(big[y], __shfl_xor_sync(Q8_FULL_MASK, big[y], 1));
+                            big[y] = fmaxf(big[y], __shfl_xor_sync(Q8_FULL_MASK, big[y], 2));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 64; j += 4) {
+                    top[0] = fmaxf(fmaxf(top[0], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
+                    top[1] = fmaxf(fmaxf(top[1], __uint_as_float(s[j + 2])), __uint_as_float(s[j + 3]));
+                }
+                const float mo[2] = {m[0], m[1]};  // the references of O as it stands
+                const int eo[2] = {e[0], e[1]};
+                bool raise = i == 0;  // the first tile sets the references
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    top[y] = fmaxf(top[y], __shfl_xor_sync(Q8_FULL_MASK, top[y], 1));
+                    top[y] = fmaxf(top[y], __shfl_xor_sync(Q8_FULL_MASK, top[y], 2));
+                    top[y] *= qq[y];
+                    raise |= top[y] > m[y] + kRaise;
+                    if (kInt8) raise |= big[y] * ii[y] > 1.0f;
+                }
+                if (__any_sync(Q8_FULL_MASK, raise)) {
+                    float f[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float mn = fmaxf(m[y], top[y]);
+                        f[y] = mn == m[y] ? 1.0f : q8::exp2_approx(m[y] - mn);
+                        l[y] *= f[y];
+                        m[y] = mn;
+                        if (kInt8) {
+                            const int en = min(126, max(e[y], static_cast<int>(__float_as_uint(big[y]) >> 23) - 126));
+                            f[y] = e[y] - en < -126 ? 0.0f : f[y] * q8::pow2(e[y] - en);
+                            e[y] = en;
+                            ii[y] = q8::pow2(-en);
+                        }
+                    }
+                    if (i % kChain > 0) {  // O follows, once the products so far are complete
+                        ok = products_done(t - 1);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[16];
+                            tc_ld16x32(tl + L::kColO + c, o);
+                            tc_wait_ld();
+                            tc_regs16(o);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[(j >> 1) & 1]);
+                            tc_st16x32w(tl + L::kColO + c, o);
+                        }
+                    }
+                }
+                float2 ref[2], sum[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float z = m[y] == -INFINITY ? 0.0f : kWeightBits - m[y];
+                    ref[y] = make_float2(z, z);
+                    sum[y] = make_float2(0.0f, 0.0f);
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int rep = 8 * c + j;
+                        float2 v2 = make_float2(1.0f, 1.0f);
+                        if (kInt8) v2 = *reinterpret_cast<const float2 *>(sc + 128 + 8 * rep + c2);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            float2 p = __ffma2_rn(
+                                make_float2(__uint_as_float(s[4 * rep + 2 * y]), __uint_as_float(s[4 * rep + 2 * y + 1])),
+                                make_float2(qq[y], qq[y]), ref[y]);
+                            p.x = q8::exp2_approx(p.x);
+                            p.y = q8::exp2_approx(p.y);
+                            sum[y] = __fadd2_rn(sum[y], p);
+                            if (kInt8) {
+                                // within +-1 for what the row sees; a hidden key's may be anything, its weight is 0
+                                float2 z = __fmul2_rn(v2, make_float2(ii[y], ii[y]));
+                                z.x = fminf(fmaxf(z.x, -1.0f), 1.0f), z.y = fminf(fmaxf(z.y, -1.0f), 1.0f);
+                                p = __fmul2_rn(p, z);
+                            }
+                            q8::split_f16(p.x, p.y, hi[2 * j + y], lo[2 * j + y]);
+                        }
+                    }
+                    tc_st16x32(ts + 32 * c, hi);
+                    tc_st16x32(ts + 64 + 32 * c, lo);
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) l[y] += sum[y].x + sum[y].y;
                 if (!kInt8 && masked) {
                     // values that no row sees must not reach the MMA as 0 * NaN: non-finite ones in a tile with hidden
                     // keys become zero, and are added back at the end for the rows that see them
-                    const int st = t & 1;
-                    if (!warp_wait(bar(L::bVf + st), static_cast<uint32_t>(t >> 1) & 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *v = sm + L::offV + st * L::kMat;
-                    for (int c = r; c < L::kMat / 16; c += 128) {
-                        uint4 x = *reinterpret_cast<const uint4 *>(v + 16 * c);
-                        uint32_t *xx = reinterpret_cast<uint32_t *>(&x);
+                    ok = warp_wait(bar(L::bVf + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u, abort_flag);
+                    if (!ok) break;
+                    uint8_t *v = sm + L::offV + (t & 1) * L::kMat;
+                    for (int c = tid - 128; c < L::kMat / 16; c += 256) {
+                        uint4 z = *reinterpret_cast<const uint4 *>(v + 16 * c);
+                        uint32_t *zz = reinterpret_cast<uint32_t *>(&z);
                         bool hit = false;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            if ((xx[j] & 0x7c00u) == 0x7c00u) xx[j] &= 0xffff0000u, hit = true;
-                            if ((xx[j] & 0x7c000000u) == 0x7c000000u) xx[j] &= 0x0000ffffu, hit = true;
+                            if ((zz[j] & 0x7c00u) == 0x7c00u) zz[j] &= 0xffff0000u, hit = true;
+                            if ((zz[j] & 0x7c000000u) == 0x7c000000u) zz[j] &= 0x0000ffffu, hit = true;
                         }
                         if (hit) {
-                            *reinterpret_cast<uint4 *>(v + 16 * c) = x;
+                            *reinterpret_cast<uint4 *>(v + 16 * c) = z;
                             if (key0 + ((c >> 3) & 127) < w.kend) *s_poison = 1;
                         }
                     }
                     q8::fence_proxy_async_smem();
                     __syncwarp();
                 }
+                if (i > 0 && i % kChain == 0) {
+                    // this tile's products start O anew: what it holds goes to the sum (the products were done
+                    // while this tile's weights were computed)
+                    ok = products_done(t - 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    float two[2], keep[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        two[y] = kInt8 ? q8::pow2(eo[y]) : 1.0f;
+                        keep[y] = msum[y] == -INFINITY ? 0.0f : q8::exp2_approx(msum[y] - mo[y]);
+                        msum[y] = mo[y];
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[16], z[16];
+                        tc_ld16x32(tl + L::kColO + c, o);
+                        if (i > kChain) tc_ld16x32(tl + L::kColSum + c, z);
+                        tc_wait_ld();
+                        tc_regs16(o);
+                        if (i > kChain) tc_regs16(z);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const int y = (j >> 1) & 1;
+                            float v = two[y] * __uint_as_float(o[j]);
+                            if (i > kChain) v += keep[y] * __uint_as_float(z[j]);
+                            o[j] = __float_as_uint(v);
+                        }
+                        tc_st16x32w(tl + L::kColSum + c, o);
+                    }
+                }
                 tc_wait_st();
                 tc_fence_before();
-                arrive(bar(L::bPf + wg));
-                if (kInt8) arrive(bar(L::bCe + t % kScaleSlots));
+                __syncwarp();
+                if (lane == 0) {
+                    arrive(bar(L::bPf + b));
+                    if (kInt8) arrive(bar(L::bCe + t % kScaleSlots));
+                }
             }
             Walk nx = w;
             more = nx.next(a, pre);
             if (more) load_q(nx.u);
-            ok = ok && warp_wait(bar(L::bOf), piece & 1u, abort_flag);
+            ok = ok && products_done(T + w.n - 1);
             tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                l[x] += __shfl_xor_sync(Q8_FULL_MASK, l[x], 1);
-                l[x] += __shfl_xor_sync(Q8_FULL_MASK, l[x], 2);
-                if (c2 == 0) {
-                    float *row = s_row + 128 * (1 + 3 * wg) + (warp & 3) * 32 + 16 * (x >> 1) + g + 8 * (x & 1);
-                    row[0] = m[x];
-                    row[128] = l[x];
-                    row[256] = kInt8 ? q8::pow2(e[x]) : 1.0f;
-                }
-            }
-            soft_sync();
+            if (more && ok) write_q(s_row + 128 * ((piece & 1) ^ 1));  // every score of this unit is computed
+            soft_sync();  // s_poison is complete, the next unit's scales are written
             if (tid == 128) *s_stop = *abort_flag;
             const int poison = *s_poison;
-            const bool partial = w.t0 > 0 || w.n < u.tiles;
-            const int pslot = 2 * cta + (w.first ? 0 : 1);
             const q8::RowMap map(a, row0);
-            // Warpgroup g finishes columns [g * D/2, (g + 1) * D/2) of every row, 16 rows at a time: with this shape a
-            // store of the warp writes whole 32-byte sectors of eight rows.
-#pragma unroll 1
-            for (int half = 0; ok && half < 2; ++half) {
-                const uint32_t lanes = static_cast<uint32_t>(16 * half) << 16;
-                const int r0 = (warp & 3) * 32 + 16 * half + g;  // and r0 + 8
-                uint32_t o0[32], o1[32];
-                // D/2 columns: 32 registers hold 64
-                const uint32_t from = tl + lanes + L::kColO + wg * (D / 2);
-                tc_ld16x64(from, o0);
-                if (w.n > 1) tc_ld16x64(from + D, o1);
-                float f0[2], f1[2], mm[2], ll[2];
-                long long at[2];
-                bool valid[2];
+            float inv[2], keep[2];
+            long long at[2];
+            bool valid[2];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float *row = s_row + r0 + 8 * x;
-                    const float m0 = row[128], m1 = row[128 * 4];
-                    mm[x] = fmaxf(m0, m1);
-                    f0[x] = m0 == -INFINITY ? 0.0f : m0 == mm[x] ? 1.0f : q8::exp2_approx(m0 - mm[x]);
-                    f1[x] = m1 == -INFINITY ? 0.0f : m1 == mm[x] ? 1.0f : q8::exp2_approx(m1 - mm[x]);
-                    ll[x] = f0[x] * row[128 * 2] + f1[x] * row[128 * 5];
-                    if (!partial) {  // the quotient; a row that saw nothing is 0
-                        const float inv = ll[x] == 0.0f ? 0.0f : __frcp_rn(ll[x]);
-                        f0[x] *= inv, f1[x] *= inv;
-                    }
-                    valid[x] = row0 + r0 + 8 * x < rows;
-                    at[x] = map.at(a, u, r0 + 8 * x, D);
-                }
+            for (int y = 0; y < 2; ++y) {
+                l[y] += __shfl_xor_sync(Q8_FULL_MASK, l[y], 1);
+                l[y] += __shfl_xor_sync(Q8_FULL_MASK, l[y], 2);
+                // the quotient; a row that saw nothing is 0
+                inv[y] = partial ? 1.0f : l[y] == 0.0f ? 0.0f : __frcp_rn(l[y]);
+                keep[y] = msum[y] == -INFINITY ? 0.0f : q8::exp2_approx(msum[y] - m[y]) * inv[y];
+                valid[y] = row0 + r0 + 8 * y < rows;
+                at[y] = map.at(a, u, r0 + 8 * y, D);
+            }
+            // rows out, 64 columns at a time: a store of the warp writes whole 32-byte sectors of eight rows
+#pragma unroll 1
+            for (int c = 0; ok && c < D; c += 64) {
+                uint32_t o[32];
+                tc_ld16x64(tl + L::kColO + c, o);
                 tc_wait_ld();
-                tc_regs32(o0);
-                float2 o[16];  // 2 * rep + x: row r0 + 8 x, columns wg * D/2 + 8 rep + c2 + {0, 1}
+                tc_regs32(o);
+                float2 v[16];  // 2 * rep + y: row r0 + 8 y, columns c + 8 rep + c2 + {0, 1}
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const int x = j & 1;
-                    const float g0 = kInt8 ? s_row[r0 + 8 * x + 128 * 3] : 1.0f;
-                    o[j] = make_float2(f0[x] * (g0 * __uint_as_float(o0[2 * j])), f0[x] * (g0 * __uint_as_float(o0[2 * j + 1])));
+                    const float two = kInt8 ? q8::pow2(e[j & 1]) : 1.0f;
+                    v[j] = make_float2(two * __uint_as_float(o[2 * j]) * inv[j & 1], two * __uint_as_float(o[2 * j + 1]) * inv[j & 1]);
                 }
-                if (w.n > 1) {
-                    tc_regs32(o1);
+                if (w.n > kChain) {  // and the sum of the chains before
+                    tc_ld16x64(tl + L::kColSum + c, o);
+                    tc_wait_ld();
+                    tc_regs32(o);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const int x = j & 1;
-                        const float g1 = kInt8 ? s_row[r0 + 8 * x + 128 * 6] : 1.0f;
-                        o[j].x += f1[x] * (g1 * __uint_as_float(o1[2 * j]));
-                        o[j].y += f1[x] * (g1 * __uint_as_float(o1[2 * j + 1]));
+                        v[j].x += keep[j & 1] * __uint_as_float(o[2 * j]);
+                        v[j].y += keep[j & 1] * __uint_as_float(o[2 * j + 1]);
                     }
                 }
-                constexpr int kReps = D / 16;  // 8-column groups of this warpgroup's half
                 if (!kInt8 && poison) {  // the non-finite values that were left out, for the rows that see them
                     for (int key = max(w.t0 * kTile, (u.cached & ~(kTile - 1)) - kTile); key < w.kend; ++key) {
                         const int pi = key / a.page;
                         const int pg = a.table[static_cast<long long>(u.b) * a.max_pages + pi];
                         if (pg < 0 || pg >= a.n_pages) continue;
-                        const __half *v = reinterpret_cast<const __half *>(a.v16) +
-                                          (static_cast<long long>(pg * a.kv_heads + u.kvh) * a.page + (key - pi * a.page)) * D +
-                                          wg * (D / 2) + c2;
+                        const __half *val = reinterpret_cast<const __half *>(a.v16) +
+                                            (static_cast<long long>(pg * a.kv_heads + u.kvh) * a.page + (key - pi * a.page)) * D + c + c2;
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            if (!q8::attn_sees(q8::attn_sight(a, u, row0 + r0 + 8 * x), u.cached, key)) continue;
+                        for (int y = 0; y < 2; ++y) {
+                            if (!q8::attn_sees(q8::attn_sight(a, u, row0 + r0 + 8 * y), u.cached, key)) continue;
 #pragma unroll
-                            for (int rep = 0; rep < kReps; ++rep) {
-                                const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(v + 8 * rep));
-                                if (!(fabsf(y.x) <= 65504.0f)) o[2 * rep + x].x += y.x;
-                                if (!(fabsf(y.y) <= 65504.0f)) o[2 * rep + x].y += y.y;
+                            for (int rep = 0; rep < 8; ++rep) {
+                                const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(val + 8 * rep));
+                                if (!(fabsf(z.x) <= 65504.0f)) v[2 * rep + y].x += z.x;
+                                if (!(fabsf(z.y) <= 65504.0f)) v[2 * rep + y].y += z.y;
                             }
                         }
                     }
                     __syncwarp();
                 }
                 if (partial) {
-                    float *dst = a.part + (static_cast<long long>(pslot) * kRows + r0) * D + wg * (D / 2) + c2;
+                    float *dst = a.part + (static_cast<long long>(pslot) * kRows + r0) * D + c + c2;
 #pragma unroll
-                    for (int j = 0; j < 2 * kReps; ++j)
-                        *reinterpret_cast<float2 *>(dst + (j & 1) * 8 * D + 8 * (j >> 1)) = o[j];
-                    if (wg == 0 && c2 == 0) {
-                        a.ml[pslot * kRows + r0] = make_float2(mm[0], ll[0]);
-                        a.ml[pslot * kRows + r0 + 8] = make_float2(mm[1], ll[1]);
-                    }
+                    for (int j = 0; j < 16; ++j) *reinterpret_cast<float2 *>(dst + (j & 1) * 8 * D + 8 * (j >> 1)) = v[j];
                 } else {
                     if (a.y) {
 #pragma unroll
-                        for (int j = 0; j < 2 * kReps; ++j)
-                            if (valid[j & 1])
-                                *reinterpret_cast<float2 *>(a.y + at[j & 1] + wg * (D / 2) + 8 * (j >> 1) + c2) = o[j];
+                        for (int j = 0; j < 16; ++j)
+                            if (valid[j & 1]) *reinterpret_cast<float2 *>(a.y + at[j & 1] + c + 8 * (j >> 1) + c2) = v[j];
                     }
                     if (a.qs) {
 #pragma unroll
-                        for (int blk = 0; blk < kReps / 4; ++blk)
+                        for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-                            for (int x = 0; x < 2; ++x)
-                                encode_quad(a, at[x] + wg * (D / 2) + 32 * blk, o + 8 * blk + x, c2, valid[x]);
+                            for (int y = 0; y < 2; ++y)
+                                encode_quad(a, at[y] + c + 32 * blk, v + 8 * blk + y, c2, valid[y]);
                     }
                 }
+            }
+            tc_fence_before();  // O is read: the next unit's products come after its first weights
+            if (partial && c2 == 0) {
+                a.ml[pslot * kRows + r0] = make_float2(m[0], l[0]);
+                a.ml[pslot * kRows + r0 + 8] = make_float2(m[1], l[1]);
             }
             if (partial && w.first && tid == 128) {
                 a.desc[2 * cta] = make_int4(u.start, u.start + kHead + u.tiles, per, u.start + kHead);
                 a.desc[2 * cta + 1] = make_int4(u.b, u.kvh, u.rt, 1);
             }
-            soft_sync();  // s_stop is written, s_poison and the row words are read
+            soft_sync();  // s_stop is written, s_poison is read
             if (*s_stop) break;
-            if (tid == 128) *s_poison = 0;  // set again after the next piece's first barrier at the earliest
+            if (tid == 128) *s_poison = 0;
+            soft_sync();  // before a tile of the next unit sets it
             T += w.n;
             ++piece;
             w = nx;

@@ -301,3 +301,29 @@ def test_offsets_past_32_bits(q8):
     vd = vv.half().double().cpu().numpy().reshape(n, kv_heads, d).transpose(1, 0, 2)[None]
     want, lim = ref.attention(q.cpu().numpy(), kd, vd, n, np.zeros((1, 1), int), [n - 2], [2], 8, d ** -0.5)
     ref.assert_within(y.cpu().numpy(), want, lim)
+
+
+@pytest.mark.parametrize("heads,n", [(1, 10_300_000), (17, 800_000)])
+def test_a_stretch_of_keys_longer_than_an_accumulation_chain(q8, heads, n):
+    """All values near 1, so that a truncating accumulation over a CTA's whole stretch would show.  The tensor core
+    loses up to 2^-23 of the running sum per MMA; over chains of 64 MMAs whose sum grows steadily that is at most
+    64 / 2 * 2^-23 = 2^-18, and as much for scores, weights and the quotient."""
+    import torch
+
+    g = torch.Generator("cuda").manual_seed(3)
+    page, d = 256, 64
+    pages = ref.pages_of(n, page)
+    k = torch.empty(1, pages, 1, page, d, dtype=torch.float16, device="cuda").normal_(generator=g)
+    v = torch.empty_like(k).normal_(generator=g).mul_(0.25).add_(1.0)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32).view(1, -1)
+    q = torch.randn(1, heads * d, generator=g, device="cuda")
+    y = torch.empty_like(q)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    q8.q8_tree_attention(q8.KvCache(k, v), 0, q, table, i32([n - 1]), i32([0, 1]), y, max_fresh=1)
+    q8.q8_check()
+    kk, vv = (x[0, table[0].long(), 0].reshape(-1, d)[:n] for x in (k, v))
+    for h in range(heads):
+        p = torch.softmax(kk.double() @ q[0, h * d:(h + 1) * d].double() * d ** -0.5, 0)
+        want = p @ vv.double()
+        rel = ((y[0, h * d:(h + 1) * d].double() - want).abs() / want.abs()).max().item()
+        assert rel <= 2.0 ** -17, (h, rel)

@@ -7,11 +7,15 @@
 // (22 bits), both parts are multiplied with the same key or value tile into
 // the same f32 accumulator, so a tile costs 2 * (D/16 + 8) MMAs of K = 16.
 //
-// Tensor memory (512 columns): two score buffers of 128 columns, O and the sum
-// of earlier Os (kChain, below).  P overwrites S in place (64 columns of high
-// parts, 64 of low parts) and is the second product's A operand; V is used as
-// it lies in the cache ([key][dim], N-major).  With two buffers the next
-// tile's scores are there before this tile's weights are done.
+// Tensor memory (512 columns): S, P (64 columns of high parts, 64 of low
+// parts: the second product's A operand), O and the sum of earlier Os
+// (kChain, below), one each.  S is free as soon as the softmax warps have read
+// it, so the next tile's scores are computed while this tile's weights are,
+// and P is written when the last tile's products are done, while they were
+// being computed: neither product waits for the other's operands.  (With P
+// over S, in two or three buffers, a tile's scores had to wait for the
+// products two or three tiles back.)  V is used as it lies in the cache
+// ([key][dim], N-major).
 //
 // Eight softmax warps work on every tile, 16 rows each (two warps per lane
 // quarter of tensor memory): a tile's weights take half the time that four
@@ -61,7 +65,7 @@ struct Lay {
     static constexpr int kThreads = kInt8 ? 512 : 384;
     // registers per thread after setmaxnreg; their sum is the launch's
     static constexpr int kRegsLaunch = kInt8 ? 128 : 168;
-    static constexpr int kRegsSoft = kInt8 ? 176 : 184, kRegsCtl = kInt8 ? 80 : 136, kRegsConv = 80;
+    static constexpr int kRegsSoft = kInt8 ? 160 : 184, kRegsCtl = kInt8 ? 96 : 136, kRegsConv = 96;
     static_assert(256 * kRegsSoft + 128 * kRegsCtl + (kInt8 ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch, "registers");
 
     static constexpr int kMat = 128 * D * 2;            // a 128-row f16 tile
@@ -79,13 +83,13 @@ struct Lay {
     static constexpr int bKf = 0, bKe = 2, bVf = 4, bVe = 6;
     static constexpr int bRKf = 8, bRKe = 10, bRVf = 12, bRVe = 14;  // int8 codes
     static constexpr int bCf = 16, bCe = 20;                         // int8 scales
-    // scores written; weights written; products done, so the score buffer is free again; queries written
-    static constexpr int bSf = 24, bPf = 26, bSe = 28, bQf = 30, bDrain = 31, kBars = 33;
+    // scores written, scores read, weights written, products done; queries written
+    static constexpr int bSf = 24, bSr = 25, bPf = 26, bPd = 27, bQf = 28, bDrain = 29, kBars = 31;
     static constexpr int offMisc = offBar + kBars * 8 + 8;
     static constexpr int offPre = offMisc + 32;
     static int smem(int batch) { return offPre + (batch + 1) * 4 + 1024; }
     static_assert(offPre + (Q8_KV_MAX_BATCH + 1) * 4 + 1024 <= 227 * 1024, "shared memory");
-    static constexpr int kColO = 256, kColSum = 384;    // the score buffers lie before them
+    static constexpr int kColP = 128, kColO = 256, kColSum = 384;  // S lies at 0
 };
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -342,8 +346,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         for (int i = 0; i < L::kBars; ++i) {
             int count = 1;  // TMA bytes or a commit
             if (i >= L::bCe && i < L::bCe + kScaleSlots) count = 8;  // softmax warps
-            if (i >= L::bPf && i < L::bPf + 2) count = 8;
-            if (i == L::bQf) count = 8;
+            if (i == L::bSr || i == L::bPf || i == L::bQf) count = 8;
             if (kInt8 && ((i >= L::bKf && i < L::bKf + 2) || (i >= L::bVf && i < L::bVf + 2))) count = 128;  // widening warps
             if ((i >= L::bRKe && i < L::bRKe + 2) || (i >= L::bRVe && i < L::bRVe + 2)) count = 128;
             q8::mbar_init(bars + i, count);
@@ -460,9 +463,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 ok = warp_wait(bar(L::bQf), piece & 1u, abort_flag);
                 ++piece;
                 for (int i = 0; ok && i < w.n; ++i, ++T) {
-                    const int b = T & 1;
                     ok = warp_wait(bar(L::bKf + (T & 1)), static_cast<uint32_t>(T >> 1) & 1u, abort_flag) &&
-                         warp_wait(bar(L::bSe + b), (static_cast<uint32_t>(T >> 1) & 1u) ^ 1u, abort_flag);
+                         warp_wait(bar(L::bSr), (static_cast<uint32_t>(T) & 1u) ^ 1u, abort_flag);  // the tile before
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t k = desc128(base + L::offK + (T % L::kBufs) * L::kMat, 16, 1024);
@@ -472,11 +474,11 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 #pragma unroll
                         for (int s = 0; s < D / 16; ++s) {
                             const uint32_t o = ((s >> 2) * 16384 + (s & 3) * 32) >> 4;
-                            mma_ss(tm + 128u * b, q + o, k + o, iS, part == 0 || s > 0, one);
+                            mma_ss(tm, q + o, k + o, iS, part == 0 || s > 0, one);
                         }
                     }
                     if (one) {
-                        tc_commit(bar(L::bSf + b));
+                        tc_commit(bar(L::bSf));
                         tc_commit(bar(L::bKe + (T & 1)));
                     }
                     __syncwarp();
@@ -496,9 +498,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             bool ok = true;
             while (ok && w.next(a, pre)) {
                 for (int i = 0; i < w.n; ++i, ++T) {
-                    const int b = T & 1;
                     ok = warp_wait(bar(L::bVf + (T & 1)), static_cast<uint32_t>(T >> 1) & 1u, abort_flag) &&
-                         warp_wait(bar(L::bPf + b), static_cast<uint32_t>(T >> 1) & 1u, abort_flag);
+                         warp_wait(bar(L::bPf), static_cast<uint32_t>(T) & 1u, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t v = desc128(base + L::offV + (T % L::kBufs) * L::kMat, 16384, 1024);
@@ -506,10 +507,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     for (int part = 1; part >= 0; --part)
 #pragma unroll
                         for (int s = 0; s < kTile / 16; ++s)
-                            mma_ts(tm + L::kColO, tm + 128u * b + 64u * part + 8u * s, v + ((2048u * s) >> 4), iO,
+                            mma_ts(tm + L::kColO, tm + L::kColP + 64u * part + 8u * s, v + ((2048u * s) >> 4), iO,
                                    part == 0 || s > 0 || i % kChain > 0, one);
                     if (one) {
-                        tc_commit(bar(L::bSe + b));
+                        tc_commit(bar(L::bPd));
                         tc_commit(bar(L::bVe + (T & 1)));
                     }
                     __syncwarp();
@@ -530,58 +531,67 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         int T = 0;
         uint32_t piece = 0;
         if (tid == 128) a.desc[2 * cta + 1].w = 0;  // no first piece yet
-        // Q: a warp per row (D = 128) or two rows (D = 64), eight warps
+        // Q: a warp per row (D = 128) or two rows (D = 64), eight warps, four loads at a time in a loop (straight-line
+        // code that runs once costs more than its loads' latency); the rows are brought to L2 beforehand.
         constexpr int kPer = D == 128 ? 1 : 2, kLanes = 32 / kPer, kLoads = 16 / kPer;
         const int sub = lane % kLanes;
-        auto q_row = [&](int j) { return (sw + 8 * j) * kPer + lane / kLanes; };
-        float4 x[kLoads];
-        auto load_q = [&](const Unit &u) {
+        auto prefetch_q = [&](const Unit &u) {
             const q8::RowMap map(a, u.rt * kRows);
-            const int rows = u.fresh * a.group - u.rt * kRows;
+            const int rr = (tid - 128) >> 1;
+            if (rr < u.fresh * a.group - u.rt * kRows) {
+                const float *row = a.q + map.at(a, u, rr, D) + (tid & 1) * (D / 2);
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const int rr = q_row(j);
-                x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (rr < rows) x[j] = __ldg(reinterpret_cast<const float4 *>(a.q + map.at(a, u, rr, D)) + sub);
+                for (int c = 0; c < D / 2; c += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
             }
         };
-        auto write_q = [&](float *scales) {
+        auto write_q = [&](const Unit &u, float *scales) {
+            const q8::RowMap map(a, u.rt * kRows);
+            const int rows = u.fresh * a.group - u.rt * kRows;
             // the row's largest value goes to [1, 2), the sign of the scale (or a scale of 0) into q: hidden scores
             // become -inf before they are scaled, so the scale of a row is never 0
             const float sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
+#pragma unroll 1
+            for (int j0 = 0; j0 < kLoads; j0 += 4) {
+                float4 x[4];
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const int rr = q_row(j);
-                // magnitudes order as their bits do; a NaN's exponent is clamped like an infinity's
-                uint32_t top = __float_as_uint(fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)), fmaxf(fabsf(x[j].z), fabsf(x[j].w))));
-                if (D == 128) {
-                    top = __reduce_max_sync(Q8_FULL_MASK, top);
-                } else {
-#pragma unroll
-                    for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(Q8_FULL_MASK, top, o));
+                for (int j = 0; j < 4; ++j) {
+                    const int rr = (sw + 8 * (j0 + j)) * kPer + lane / kLanes;
+                    x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (rr < rows) x[j] = __ldg(reinterpret_cast<const float4 *>(a.q + map.at(a, u, rr, D)) + sub);
                 }
-                const int e = min(126, max(-126, static_cast<int>(top >> 23) - 127));
-                const float down = q8::pow2(-e) * sign;
-                uint2 hi, lo;
-                q8::split_f16(x[j].x * down, x[j].y * down, hi.x, lo.x);
-                q8::split_f16(x[j].z * down, x[j].w * down, hi.y, lo.y);
-                const int off = (sub >> 4) * 16384 + rr * 128 + ((((sub & 15) >> 1) ^ (rr & 7)) << 4) + (sub & 1) * 8;
-                *reinterpret_cast<uint2 *>(sm + L::offQ + off) = hi;
-                *reinterpret_cast<uint2 *>(sm + L::offQ + L::kMat + off) = lo;
-                if (sub == 0) scales[rr] = fmaxf(q8::pow2(e) * fabsf(a.scale), 1.17549435e-38f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int rr = (sw + 8 * (j0 + j)) * kPer + lane / kLanes;
+                    // magnitudes order as their bits do; a NaN's exponent is clamped like an infinity's
+                    uint32_t top =
+                        __float_as_uint(fmaxf(fmaxf(fabsf(x[j].x), fabsf(x[j].y)), fmaxf(fabsf(x[j].z), fabsf(x[j].w))));
+                    if (D == 128) {
+                        top = __reduce_max_sync(Q8_FULL_MASK, top);
+                    } else {
+#pragma unroll
+                        for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(Q8_FULL_MASK, top, o));
+                    }
+                    const int e = min(126, max(-126, static_cast<int>(top >> 23) - 127));
+                    const float down = q8::pow2(-e) * sign;
+                    uint2 hi, lo;
+                    q8::split_f16(x[j].x * down, x[j].y * down, hi.x, lo.x);
+                    q8::split_f16(x[j].z * down, x[j].w * down, hi.y, lo.y);
+                    const int off = (sub >> 4) * 16384 + rr * 128 + ((((sub & 15) >> 1) ^ (rr & 7)) << 4) + (sub & 1) * 8;
+                    *reinterpret_cast<uint2 *>(sm + L::offQ + off) = hi;
+                    *reinterpret_cast<uint2 *>(sm + L::offQ + L::kMat + off) = lo;
+                    if (sub == 0) scales[rr] = fmaxf(q8::pow2(e) * fabsf(a.scale), 1.17549435e-38f);
+                }
             }
             q8::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) arrive(bar(L::bQf));
         };
-        // Products of tiles up to t complete (those of t - 2 are, when the scores of t are there).
-        auto products_done = [&](int t) {
-            return warp_wait(bar(L::bSe + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u, abort_flag);
-        };
+        // Products of tiles up to t complete; asked for every tile in turn, before the next tile's weights are written.
+        auto products_done = [&](int t) { return warp_wait(bar(L::bPd), static_cast<uint32_t>(t) & 1u, abort_flag); };
         bool more = w.next(a, pre);
         if (more) {
-            load_q(w.u);
-            write_q(s_row);
+            prefetch_q(w.u);
+            write_q(w.u, s_row);
             soft_sync();  // the scales
         }
         while (more) {
@@ -599,19 +609,21 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             const bool partial = w.t0 > 0 || w.n < u.tiles;
             const int pslot = 2 * cta + (w.first ? 0 : 1);
             float msum[2] = {-INFINITY, -INFINITY};  // the reference of the sum of earlier Os
+            Walk nx = w;
+            more = nx.next(a, pre);
+            if (more) prefetch_q(nx.u);
             for (int i = 0; ok && i < w.n; ++i) {
-                const int t = T + i, key0 = (w.t0 + i) * kTile, b = t & 1;
-                const uint32_t ts = tl + 128u * b;
+                const int t = T + i, key0 = (w.t0 + i) * kTile;
                 const bool masked = key0 + kTile > min(all_see, w.kend);
                 const float *sc = reinterpret_cast<const float *>(sm + L::offScale + (t % kScaleSlots) * 1024);
-                ok = warp_wait(bar(L::bSf + b), static_cast<uint32_t>(t >> 1) & 1u, abort_flag) &&
+                ok = warp_wait(bar(L::bSf), static_cast<uint32_t>(t) & 1u, abort_flag) &&
                      (!kInt8 ||
                       warp_wait(bar(L::bCf + t % kScaleSlots), static_cast<uint32_t>(t / kScaleSlots) & 1u, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t s[64];
-                tc_ld16x64(ts, s);
-                tc_ld16x64(ts + 64, s + 32);
+                tc_ld16x64(tl, s);
+                tc_ld16x64(tl + 64, s + 32);
                 float all_big = 0.0f;  // int8: the tile's largest value scale
                 bool odd = masked;     // some row sees not every key, or a value scale is not finite
                 if (kInt8) {
@@ -625,6 +637,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 tc_wait_ld();
                 tc_regs32(s);
                 tc_regs32(s + 32);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(bar(L::bSr));  // the next tile's scores may come
                 if (kInt8) {  // scores by their keys' scales
 #pragma unroll
                     for (int rep = 0; rep < 16; ++rep) {
@@ -678,6 +693,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 }
                 const float mo[2] = {m[0], m[1]};  // the references of O as it stands
                 const int eo[2] = {e[0], e[1]};
+                float f[2] = {1.0f, 1.0f};
                 bool raise = i == 0;  // the first tile sets the references
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
@@ -687,8 +703,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     raise |= top[y] > m[y] + kRaise;
                     if (kInt8) raise |= big[y] * ii[y] > 1.0f;
                 }
-                if (__any_sync(Q8_FULL_MASK, raise)) {
-                    float f[2];
+                raise = __any_sync(Q8_FULL_MASK, raise);
+                if (raise) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const float mn = fmaxf(m[y], top[y]);
@@ -702,21 +718,6 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                             ii[y] = q8::pow2(-en);
                         }
                     }
-                    if (i % kChain > 0) {  // O follows, once the products so far are complete
-                        ok = products_done(t - 1);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[16];
-                            tc_ld16x32(tl + L::kColO + c, o);
-                            tc_wait_ld();
-                            tc_regs16(o);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[(j >> 1) & 1]);
-                            tc_st16x32w(tl + L::kColO + c, o);
-                        }
-                    }
                 }
                 float2 ref[2], sum[2];
 #pragma unroll
@@ -725,36 +726,56 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     ref[y] = make_float2(z, z);
                     sum[y] = make_float2(0.0f, 0.0f);
                 }
+                // the weights, as pairs of f16 parts over the scores' registers
+#pragma unroll
+                for (int rep = 0; rep < 16; ++rep) {
+                    float2 v2 = make_float2(1.0f, 1.0f);
+                    if (kInt8) v2 = *reinterpret_cast<const float2 *>(sc + 128 + 8 * rep + c2);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t *z = s + 4 * rep + 2 * y;
+                        float2 p = __ffma2_rn(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])),
+                                              make_float2(qq[y], qq[y]), ref[y]);
+                        p.x = q8::exp2_approx(p.x);
+                        p.y = q8::exp2_approx(p.y);
+                        sum[y] = __fadd2_rn(sum[y], p);
+                        if (kInt8) {
+                            // within +-1 for what the row sees; a hidden key's may be anything, its weight is 0
+                            float2 x = __fmul2_rn(v2, make_float2(ii[y], ii[y]));
+                            x.x = fminf(fmaxf(x.x, -1.0f), 1.0f), x.y = fminf(fmaxf(x.y, -1.0f), 1.0f);
+                            p = __fmul2_rn(p, x);
+                        }
+                        q8::split_f16(p.x, p.y, z[0], z[1]);
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) l[y] += sum[y].x + sum[y].y;
+                // P and O are free once the products of the tile before are done
+                if (t > 0) {
+                    ok = products_done(t - 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int rep = 8 * c + j;
-                        float2 v2 = make_float2(1.0f, 1.0f);
-                        if (kInt8) v2 = *reinterpret_cast<const float2 *>(sc + 128 + 8 * rep + c2);
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            float2 p = __ffma2_rn(
-                                make_float2(__uint_as_float(s[4 * rep + 2 * y]), __uint_as_float(s[4 * rep + 2 * y + 1])),
-                                make_float2(qq[y], qq[y]), ref[y]);
-                            p.x = q8::exp2_approx(p.x);
-                            p.y = q8::exp2_approx(p.y);
-                            sum[y] = __fadd2_rn(sum[y], p);
-                            if (kInt8) {
-                                // within +-1 for what the row sees; a hidden key's may be anything, its weight is 0
-                                float2 z = __fmul2_rn(v2, make_float2(ii[y], ii[y]));
-                                z.x = fminf(fmaxf(z.x, -1.0f), 1.0f), z.y = fminf(fmaxf(z.y, -1.0f), 1.0f);
-                                p = __fmul2_rn(p, z);
-                            }
-                            q8::split_f16(p.x, p.y, hi[2 * j + y], lo[2 * j + y]);
-                        }
-                    }
-                    tc_st16x32(ts + 32 * c, hi);
-                    tc_st16x32(ts + 64 + 32 * c, lo);
+                    for (int j = 0; j < 16; ++j) hi[j] = s[32 * c + 2 * j], lo[j] = s[32 * c + 2 * j + 1];
+                    tc_st16x32(tl + L::kColP + 32 * c, hi);
+                    tc_st16x32(tl + L::kColP + 64 + 32 * c, lo);
                 }
+                if (raise && i % kChain > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[16];
+                        tc_ld16x32(tl + L::kColO + c, o);
+                        tc_wait_ld();
+                        tc_regs16(o);
 #pragma unroll
-                for (int y = 0; y < 2; ++y) l[y] += sum[y].x + sum[y].y;
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[(j >> 1) & 1]);
+                        tc_st16x32w(tl + L::kColO + c, o);
+                    }
+                }
                 if (!kInt8 && masked) {
                     // values that no row sees must not reach the MMA as 0 * NaN: non-finite ones in a tile with hidden
                     // keys become zero, and are added back at the end for the rows that see them
@@ -779,11 +800,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     __syncwarp();
                 }
                 if (i > 0 && i % kChain == 0) {
-                    // this tile's products start O anew: what it holds goes to the sum (the products were done
-                    // while this tile's weights were computed)
-                    ok = products_done(t - 1);
-                    if (!ok) break;
-                    tc_fence_after();
+                    // this tile's products start O anew: what it holds goes to the sum
                     float two[2], keep[2];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
@@ -813,16 +830,13 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    arrive(bar(L::bPf + b));
+                    arrive(bar(L::bPf));
                     if (kInt8) arrive(bar(L::bCe + t % kScaleSlots));
                 }
             }
-            Walk nx = w;
-            more = nx.next(a, pre);
-            if (more) load_q(nx.u);
             ok = ok && products_done(T + w.n - 1);
             tc_fence_after();
-            if (more && ok) write_q(s_row + 128 * ((piece & 1) ^ 1));  // every score of this unit is computed
+            if (more && ok) write_q(nx.u, s_row + 128 * ((piece & 1) ^ 1));  // every score of this unit is computed
             soft_sync();  // s_poison is complete, the next unit's scales are written
             if (tid == 128) *s_stop = *abort_flag;
             const int poison = *s_poison;
@@ -929,8 +943,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         bool ok = true;
         auto widen = [&](uint32_t src_off, uint32_t dst_off) {
             constexpr int kChunks = D / 16;  // 16 codes each
-#pragma unroll
-            for (int j = 0; j < 128 * kChunks / 128; ++j) {
+#pragma unroll 4
+            for (int j = 0; j < kChunks; ++j) {
                 const int idx = c0 + 128 * j;
                 int rr, c;
                 if (D == 128) {

@@ -25,8 +25,8 @@
 // all it needs between the maximum and the weights, and a key's scale is read
 // once for two rows.
 //
-// Roles: warp 0 copies K and V tiles (one TMA box per run of keys that share a
-// page); warp 1 issues the scores' MMAs and warp 3 the products' (one warp for
+// Roles: warps 0 and 2 copy K and V tiles (one TMA box per run of keys that
+// share a page); warp 1 issues the scores' MMAs and warp 3 the products' (one warp for
 // both left the tensor core idle a third of the time: it queues only a few
 // MMAs ahead, and every wait of the issuing warp is a gap); warps 4-11 are the
 // softmax warps; for int8, warps 12-15 widen the codes to f16 tiles (exact), a
@@ -50,7 +50,7 @@ using q8::Unit;
 __device__ unsigned int g_tiles_err;
 
 constexpr int kRows = 128, kTile = 128;
-constexpr int kHead = 3;             // what a unit costs beside its tiles, in tiles
+constexpr int kHead = 5;             // what a unit costs beside its tiles, in tiles
 constexpr float kWeightBits = 6.0f;  // weights are 2^(s - m + 6): below 2^14 while m may lag by 2^8
 constexpr float kRaise = 8.0f;
 constexpr int kScaleSlots = 4;
@@ -346,6 +346,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         for (int i = 0; i < L::kBars; ++i) {
             int count = 1;  // TMA bytes or a commit
             if (i >= L::bCe && i < L::bCe + kScaleSlots) count = 8;  // softmax warps
+            if (i >= L::bCf && i < L::bCf + kScaleSlots) count = 2;  // the keys' scales and the values'
             if (i == L::bSr || i == L::bPf || i == L::bQf) count = 8;
             if (kInt8 && ((i >= L::bKf && i < L::bKf + 2) || (i >= L::bVf && i < L::bVf + 2))) count = 128;  // widening warps
             if ((i >= L::bRKe && i < L::bRKe + 2) || (i >= L::bRVe && i < L::bRVe + 2)) count = 128;
@@ -377,12 +378,22 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 
     if (warp < 4) {
         setmaxnreg_dec<L::kRegsCtl>();
-        if (warp == 0) {
-            // -------------------------------------------------------- copies: K and V tiles, key scales
-            int T = 0, nk = 0, nv = 0, nc = 0;  // tiles so far; copies issued of each kind
+        if (!(warp & 1)) {
+            // -------------------------------------------------------- copies: warp 0 K tiles, warp 2 V tiles; a scale with
+            // its values
+            const bool is_v = warp == 2;
+            const CUtensorMap *map = is_v ? &mv : &mk;
+            const float *scales = is_v ? a.vs : a.ks;
+            const int full = kInt8 ? (is_v ? L::bRVf : L::bRKf) : (is_v ? L::bVf : L::bKf);
+            const int empty = kInt8 ? (is_v ? L::bRVe : L::bRKe) : (is_v ? L::bVe : L::bKe);
+            const uint32_t ring = base + (kInt8 ? L::offRaw + (is_v ? 2 * L::kRaw : 0) : is_v ? L::offV : L::offK);
+            constexpr int kStage = kInt8 ? L::kRaw : L::kMat;
+            constexpr int kRowBytes = kInt8 ? D : 128;  // of a box row
+            constexpr int kHalves = kInt8 ? 1 : D / 64;
+            const int boxes = kTile / box;
+            int T = 0, n_tiles = 0, n_scales = 0;  // tiles so far; copies issued of each kind
             bool ok = true;
             while (ok && w.next(a, pre)) {
-                const int boxes = kTile / box;
                 auto fetch = [&](int i) {  // cache row of this lane's box of tile i
                     const int key = (w.t0 + i) * kTile + lane * box;
                     if (i >= w.n || lane >= boxes || key >= w.kend) return 0;
@@ -396,60 +407,39 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 };
                 int row = fetch(0);
                 for (int i = 0; i < w.n; ++i, ++T) {
-                    const int ahead = fetch(i + 1);
+                    const int next = fetch(i + 1);
                     const int key0 = (w.t0 + i) * kTile;
                     const int nb = min(boxes, (w.kend - key0 + box - 1) / box);
                     const int st = T & 1;
-                    const uint32_t par = static_cast<uint32_t>(T >> 1) & 1u;
-                    constexpr int kRowBytes = kInt8 ? D : 128;  // of a box row
-                    constexpr int kHalves = kInt8 ? 1 : D / 64;
-                    auto copy = [&](int full, int empty, const CUtensorMap *map, int off) {
-                        if (!warp_wait(bar(empty + st), par ^ 1u, abort_flag)) return false;
-                        if (lane == 0) q8::mbar_arrive_expect_tx(bars + full + st, nb * box * kRowBytes * kHalves);
-                        __syncwarp();
-                        if (lane < nb) {
-#pragma unroll
-                            for (int h = 0; h < kHalves; ++h)
-                                q8::tma_load_2d(base + off + h * 16384 + lane * box * kRowBytes, map, h * 64, row,
-                                                bar(full + st));
-                        }
-                        return true;
-                    };
                     if (kInt8) {
                         const int cs = T % kScaleSlots;
                         ok = warp_wait(bar(L::bCe + cs), (static_cast<uint32_t>(T / kScaleSlots) & 1u) ^ 1u, abort_flag);
                         if (!ok) break;
-                        if (lane == 0) q8::mbar_arrive_expect_tx(bars + L::bCf + cs, nb * box * 8);
+                        if (lane == 0) q8::mbar_arrive_expect_tx(bars + L::bCf + cs, nb * box * 4);
                         __syncwarp();
-                        if (lane < nb) {
-                            uint8_t *dst = sm + L::offScale + cs * 1024 + lane * box * 4;
-                            q8::bulk_g2s(dst, a.ks + row, box * 4, bars + L::bCf + cs);
-                            q8::bulk_g2s(dst + 512, a.vs + row, box * 4, bars + L::bCf + cs);
-                        }
-                        nc = T + 1;
-                        ok = copy(L::bRKf, L::bRKe, &mk, L::offRaw + st * L::kRaw);
-                        if (!ok) break;
-                        nk = T + 1;
-                        ok = copy(L::bRVf, L::bRVe, &mv, L::offRaw + (2 + st) * L::kRaw);
-                        if (!ok) break;
-                        nv = T + 1;
-                    } else {
-                        ok = copy(L::bKf, L::bKe, &mk, L::offK + st * L::kMat);
-                        if (!ok) break;
-                        nk = T + 1;
-                        ok = copy(L::bVf, L::bVe, &mv, L::offV + st * L::kMat);
-                        if (!ok) break;
-                        nv = T + 1;
+                        if (lane < nb)
+                            q8::bulk_g2s(sm + L::offScale + cs * 1024 + (is_v ? 512 : 0) + lane * box * 4, scales + row, box * 4,
+                                         bars + L::bCf + cs);
+                        n_scales = T + 1;
                     }
-                    row = ahead;
+                    ok = warp_wait(bar(empty + st), (static_cast<uint32_t>(T >> 1) & 1u) ^ 1u, abort_flag);
+                    if (!ok) break;
+                    if (lane == 0) q8::mbar_arrive_expect_tx(bars + full + st, nb * box * kRowBytes * kHalves);
+                    __syncwarp();
+                    if (lane < nb) {
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h)
+                            q8::tma_load_2d(ring + st * kStage + h * 16384 + lane * box * kRowBytes, map, h * 64, row,
+                                            bar(full + st));
+                    }
+                    n_tiles = T + 1;
+                    row = next;
                 }
             }
             // the last copies must have landed before the CTA exits
-            for (int t = max(0, nk - 2); t < nk; ++t)
-                drain_bar(bar((kInt8 ? L::bRKf : L::bKf) + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u);
-            for (int t = max(0, nv - 2); t < nv; ++t)
-                drain_bar(bar((kInt8 ? L::bRVf : L::bVf) + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u);
-            for (int t = max(0, nc - kScaleSlots); t < nc; ++t)
+            for (int t = max(0, n_tiles - 2); t < n_tiles; ++t)
+                drain_bar(bar(full + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u);
+            for (int t = max(0, n_scales - kScaleSlots); t < n_scales; ++t)
                 drain_bar(bar(L::bCf + t % kScaleSlots), static_cast<uint32_t>(t / kScaleSlots) & 1u);
         } else if (warp == 1) {
             // -------------------------------------------------------- scores
@@ -596,19 +586,18 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         }
         while (more) {
             const Unit &u = w.u;
-            const int rows = u.fresh * a.group, row0 = u.rt * kRows;
+            const int rows = u.fresh * a.group, row0 = u.rt * kRows, pslot = 2 * cta + (w.first ? 0 : 1);
             const int all_see = u.cached + (a.masks ? 0 : row0 / a.group + 1);  // keys below are seen by every row
-            float qq[2], m[2], l[2], ii[2];
+            const q8::RowSight sight0 = q8::attn_sight(a, u, row0 + r0), sight1 = q8::attn_sight(a, u, row0 + r0 + 8);
+            const bool partial = w.t0 > 0 || w.n < u.tiles;
+            float qq[2], m[2], l[2], ii[2], msum[2];
             int e[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 qq[y] = s_row[128 * (piece & 1) + r0 + 8 * y];
-                m[y] = -INFINITY, l[y] = 0.0f, ii[y] = q8::pow2(126), e[y] = -126;
+                m[y] = msum[y] = -INFINITY, l[y] = 0.0f, ii[y] = q8::pow2(126), e[y] = -126;
             }
             bool ok = true;
-            const bool partial = w.t0 > 0 || w.n < u.tiles;
-            const int pslot = 2 * cta + (w.first ? 0 : 1);
-            float msum[2] = {-INFINITY, -INFINITY};  // the reference of the sum of earlier Os
             Walk nx = w;
             more = nx.next(a, pre);
             if (more) prefetch_q(nx.u);
@@ -658,7 +647,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     // scale that is not finite makes the scores that see it NaN
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const q8::RowSight sight = q8::attn_sight(a, u, row0 + r0 + 8 * y);
+                        const q8::RowSight &sight = y ? sight1 : sight0;
                         big[y] = 0.0f;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
@@ -782,18 +771,28 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     ok = warp_wait(bar(L::bVf + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u, abort_flag);
                     if (!ok) break;
                     uint8_t *v = sm + L::offV + (t & 1) * L::kMat;
-                    for (int c = tid - 128; c < L::kMat / 16; c += 256) {
-                        uint4 z = *reinterpret_cast<const uint4 *>(v + 16 * c);
-                        uint32_t *zz = reinterpret_cast<uint32_t *>(&z);
-                        bool hit = false;
+                    __half2 nan = __float2half2_rn(0.0f);  // stays 0 over finite values
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if ((zz[j] & 0x7c00u) == 0x7c00u) zz[j] &= 0xffff0000u, hit = true;
-                            if ((zz[j] & 0x7c000000u) == 0x7c000000u) zz[j] &= 0x0000ffffu, hit = true;
-                        }
-                        if (hit) {
-                            *reinterpret_cast<uint4 *>(v + 16 * c) = z;
-                            if (key0 + ((c >> 3) & 127) < w.kend) *s_poison = 1;
+                    for (int c = 0; c < L::kMat / 16; c += 256) {
+                        const uint4 z = *reinterpret_cast<const uint4 *>(v + 16 * (c + tid - 128));
+                        const __half2 *h = reinterpret_cast<const __half2 *>(&z);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) nan = __hfma2(h[j], __float2half2_rn(0.0f), nan);
+                    }
+                    if (__any_sync(Q8_FULL_MASK, __hisnan(__low2half(nan)) || __hisnan(__high2half(nan)))) {
+                        for (int c = tid - 128; c < L::kMat / 16; c += 256) {
+                            uint4 z = *reinterpret_cast<const uint4 *>(v + 16 * c);
+                            uint32_t *zz = reinterpret_cast<uint32_t *>(&z);
+                            bool hit = false;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                if ((zz[j] & 0x7c00u) == 0x7c00u) zz[j] &= 0xffff0000u, hit = true;
+                                if ((zz[j] & 0x7c000000u) == 0x7c000000u) zz[j] &= 0x0000ffffu, hit = true;
+                            }
+                            if (hit) {
+                                *reinterpret_cast<uint4 *>(v + 16 * c) = z;
+                                if (key0 + ((c >> 3) & 127) < w.kend) *s_poison = 1;
+                            }
                         }
                     }
                     q8::fence_proxy_async_smem();
@@ -834,101 +833,101 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     if (kInt8) arrive(bar(L::bCe + t % kScaleSlots));
                 }
             }
-            ok = ok && products_done(T + w.n - 1);
-            tc_fence_after();
             if (more && ok) write_q(nx.u, s_row + 128 * ((piece & 1) ^ 1));  // every score of this unit is computed
-            soft_sync();  // s_poison is complete, the next unit's scales are written
-            if (tid == 128) *s_stop = *abort_flag;
-            const int poison = *s_poison;
-            const q8::RowMap map(a, row0);
-            float inv[2], keep[2];
-            long long at[2];
-            bool valid[2];
+                ok = ok && products_done(T + w.n - 1);
+                tc_fence_after();
+                soft_sync();  // s_poison is complete, the next unit's scales are written
+                if (tid == 128) *s_stop = *abort_flag;
+                const int poison = *s_poison;
+                const q8::RowMap map(a, row0);
+                float inv[2], keep[2];
+                long long at[2];
+                bool valid[2];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                l[y] += __shfl_xor_sync(Q8_FULL_MASK, l[y], 1);
-                l[y] += __shfl_xor_sync(Q8_FULL_MASK, l[y], 2);
-                // the quotient; a row that saw nothing is 0
-                inv[y] = partial ? 1.0f : l[y] == 0.0f ? 0.0f : __frcp_rn(l[y]);
-                keep[y] = msum[y] == -INFINITY ? 0.0f : q8::exp2_approx(msum[y] - m[y]) * inv[y];
-                valid[y] = row0 + r0 + 8 * y < rows;
-                at[y] = map.at(a, u, r0 + 8 * y, D);
-            }
-            // rows out, 64 columns at a time: a store of the warp writes whole 32-byte sectors of eight rows
-#pragma unroll 1
-            for (int c = 0; ok && c < D; c += 64) {
-                uint32_t o[32];
-                tc_ld16x64(tl + L::kColO + c, o);
-                tc_wait_ld();
-                tc_regs32(o);
-                float2 v[16];  // 2 * rep + y: row r0 + 8 y, columns c + 8 rep + c2 + {0, 1}
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float two = kInt8 ? q8::pow2(e[j & 1]) : 1.0f;
-                    v[j] = make_float2(two * __uint_as_float(o[2 * j]) * inv[j & 1], two * __uint_as_float(o[2 * j + 1]) * inv[j & 1]);
+                for (int y = 0; y < 2; ++y) {
+                    l[y] += __shfl_xor_sync(Q8_FULL_MASK, l[y], 1);
+                    l[y] += __shfl_xor_sync(Q8_FULL_MASK, l[y], 2);
+                    // the quotient; a row that saw nothing is 0
+                    inv[y] = partial ? 1.0f : l[y] == 0.0f ? 0.0f : __frcp_rn(l[y]);
+                    keep[y] = msum[y] == -INFINITY ? 0.0f : q8::exp2_approx(msum[y] - m[y]) * inv[y];
+                    valid[y] = row0 + r0 + 8 * y < rows;
+                    at[y] = map.at(a, u, r0 + 8 * y, D);
                 }
-                if (w.n > kChain) {  // and the sum of the chains before
-                    tc_ld16x64(tl + L::kColSum + c, o);
+                // rows out, 64 columns at a time: a store of the warp writes whole 32-byte sectors of eight rows
+#pragma unroll 1
+                for (int c = 0; ok && c < D; c += 64) {
+                    uint32_t o[32];
+                    tc_ld16x64(tl + L::kColO + c, o);
                     tc_wait_ld();
                     tc_regs32(o);
+                    float2 v[16];  // 2 * rep + y: row r0 + 8 y, columns c + 8 rep + c2 + {0, 1}
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        v[j].x += keep[j & 1] * __uint_as_float(o[2 * j]);
-                        v[j].y += keep[j & 1] * __uint_as_float(o[2 * j + 1]);
+                        const float two = kInt8 ? q8::pow2(e[j & 1]) : 1.0f;
+                        v[j] = make_float2(two * __uint_as_float(o[2 * j]) * inv[j & 1], two * __uint_as_float(o[2 * j + 1]) * inv[j & 1]);
                     }
-                }
-                if (!kInt8 && poison) {  // the non-finite values that were left out, for the rows that see them
-                    for (int key = max(w.t0 * kTile, (u.cached & ~(kTile - 1)) - kTile); key < w.kend; ++key) {
-                        const int pi = key / a.page;
-                        const int pg = a.table[static_cast<long long>(u.b) * a.max_pages + pi];
-                        if (pg < 0 || pg >= a.n_pages) continue;
-                        const __half *val = reinterpret_cast<const __half *>(a.v16) +
-                                            (static_cast<long long>(pg * a.kv_heads + u.kvh) * a.page + (key - pi * a.page)) * D + c + c2;
+                    if (w.n > kChain) {  // and the sum of the chains before
+                        tc_ld16x64(tl + L::kColSum + c, o);
+                        tc_wait_ld();
+                        tc_regs32(o);
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            if (!q8::attn_sees(q8::attn_sight(a, u, row0 + r0 + 8 * y), u.cached, key)) continue;
-#pragma unroll
-                            for (int rep = 0; rep < 8; ++rep) {
-                                const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(val + 8 * rep));
-                                if (!(fabsf(z.x) <= 65504.0f)) v[2 * rep + y].x += z.x;
-                                if (!(fabsf(z.y) <= 65504.0f)) v[2 * rep + y].y += z.y;
-                            }
+                        for (int j = 0; j < 16; ++j) {
+                            v[j].x += keep[j & 1] * __uint_as_float(o[2 * j]);
+                            v[j].y += keep[j & 1] * __uint_as_float(o[2 * j + 1]);
                         }
                     }
-                    __syncwarp();
-                }
-                if (partial) {
-                    float *dst = a.part + (static_cast<long long>(pslot) * kRows + r0) * D + c + c2;
+                    if (!kInt8 && poison) {  // the non-finite values that were left out, for the rows that see them
+                        for (int key = max(w.t0 * kTile, (u.cached & ~(kTile - 1)) - kTile); key < w.kend; ++key) {
+                            const int pi = key / a.page;
+                            const int pg = a.table[static_cast<long long>(u.b) * a.max_pages + pi];
+                            if (pg < 0 || pg >= a.n_pages) continue;
+                            const __half *val = reinterpret_cast<const __half *>(a.v16) +
+                                                (static_cast<long long>(pg * a.kv_heads + u.kvh) * a.page + (key - pi * a.page)) * D + c + c2;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) *reinterpret_cast<float2 *>(dst + (j & 1) * 8 * D + 8 * (j >> 1)) = v[j];
-                } else {
-                    if (a.y) {
+                            for (int y = 0; y < 2; ++y) {
+                                if (!q8::attn_sees(y ? sight1 : sight0, u.cached, key)) continue;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (valid[j & 1]) *reinterpret_cast<float2 *>(a.y + at[j & 1] + c + 8 * (j >> 1) + c2) = v[j];
+                                for (int rep = 0; rep < 8; ++rep) {
+                                    const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(val + 8 * rep));
+                                    if (!(fabsf(z.x) <= 65504.0f)) v[2 * rep + y].x += z.x;
+                                    if (!(fabsf(z.y) <= 65504.0f)) v[2 * rep + y].y += z.y;
+                                }
+                            }
+                        }
+                        __syncwarp();
                     }
-                    if (a.qs) {
+                    if (partial) {
+                        float *dst = a.part + (static_cast<long long>(pslot) * kRows + r0) * D + c + c2;
 #pragma unroll
-                        for (int blk = 0; blk < 2; ++blk)
+                        for (int j = 0; j < 16; ++j) *reinterpret_cast<float2 *>(dst + (j & 1) * 8 * D + 8 * (j >> 1)) = v[j];
+                    } else {
+                        if (a.y) {
 #pragma unroll
-                            for (int y = 0; y < 2; ++y)
-                                encode_quad(a, at[y] + c + 32 * blk, v + 8 * blk + y, c2, valid[y]);
+                            for (int j = 0; j < 16; ++j)
+                                if (valid[j & 1]) *reinterpret_cast<float2 *>(a.y + at[j & 1] + c + 8 * (j >> 1) + c2) = v[j];
+                        }
+                        if (a.qs) {
+#pragma unroll
+                            for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y)
+                                    encode_quad(a, at[y] + c + 32 * blk, v + 8 * blk + y, c2, valid[y]);
+                        }
                     }
                 }
-            }
-            tc_fence_before();  // O is read: the next unit's products come after its first weights
-            if (partial && c2 == 0) {
-                a.ml[pslot * kRows + r0] = make_float2(m[0], l[0]);
-                a.ml[pslot * kRows + r0 + 8] = make_float2(m[1], l[1]);
-            }
-            if (partial && w.first && tid == 128) {
-                a.desc[2 * cta] = make_int4(u.start, u.start + kHead + u.tiles, per, u.start + kHead);
-                a.desc[2 * cta + 1] = make_int4(u.b, u.kvh, u.rt, 1);
-            }
-            soft_sync();  // s_stop is written, s_poison is read
-            if (*s_stop) break;
-            if (tid == 128) *s_poison = 0;
-            soft_sync();  // before a tile of the next unit sets it
+                tc_fence_before();  // O is read: the next unit's products come after its first weights
+                if (partial && c2 == 0) {
+                    a.ml[pslot * kRows + r0] = make_float2(m[0], l[0]);
+                    a.ml[pslot * kRows + r0 + 8] = make_float2(m[1], l[1]);
+                }
+                if (partial && w.first && tid == 128) {
+                    a.desc[2 * cta] = make_int4(u.start, u.start + kHead + u.tiles, per, u.start + kHead);
+                    a.desc[2 * cta + 1] = make_int4(u.b, u.kvh, u.rt, 1);
+                }
+                soft_sync();  // s_stop is written, s_poison is read
+                if (*s_stop) break;
+                if (tid == 128) *s_poison = 0;
+                soft_sync();  // before a tile of the next unit sets it
             T += w.n;
             ++piece;
             w = nx;

@@ -87,30 +87,31 @@ class KvCache:
     ``k``, ``v``: f16, or int8 codes, [layers][n_pages][kv_heads][page_size][head_dim]; ``k_scale``,
     ``v_scale``: f32 [layers][n_pages][kv_heads][page_size], with int8 only.  :func:`empty_kv_cache` makes one."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "desc", "ref")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "desc", "ref", "dev")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
 
-        if k.dim() != 5 or v.shape != k.shape:
+        shape, dt = k.shape, k.dtype
+        if len(shape) != 5 or v.shape != shape:
             raise ValueError("k, v: expected two [layers][n_pages][kv_heads][page_size][head_dim] tensors")
-        if k.dtype not in (torch.float16, torch.int8):
-            raise ValueError(f"k: expected float16 or int8, got {k.dtype}")
-        int8 = k.dtype == torch.int8
-        _need(k, k.dtype, "k"), _need(v, k.dtype, "v")
-        if v.device != k.device or int8 != (k_scale is not None) or int8 != (v_scale is not None):
-            raise ValueError("k and v on one device; k_scale and v_scale with int8 and only then")
+        int8 = dt is torch.int8
+        if not int8 and dt is not torch.float16:
+            raise ValueError(f"k: expected float16 or int8, got {dt}")
+        if int8 != (k_scale is not None) or int8 != (v_scale is not None):
+            raise ValueError("k_scale and v_scale with int8, and only then")
+        dev = self.dev = k.get_device()
+        _beside(k, dt, dev, "k"), _beside(v, dt, dev, "v")
+        ks = vs = None
         if int8:
-            for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                _need(t, torch.float32, n)
-                if t.shape != k.shape[:-1] or t.device != k.device:
-                    raise ValueError(f"{n}: expected [layers][n_pages][kv_heads][page_size] beside k")
+            if k_scale.shape != shape[:-1] or v_scale.shape != shape[:-1]:
+                raise ValueError("k_scale, v_scale: expected [layers][n_pages][kv_heads][page_size]")
+            ks = _beside(k_scale, torch.float32, dev, "k_scale")
+            vs = _beside(v_scale, torch.float32, dev, "v_scale")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        layers, n_pages, kv_heads, page, dim = k.shape
-        self.desc = KvCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if int8 else None,
-                                v_scale.data_ptr() if int8 else None, layers, n_pages, kv_heads, page, dim,
+        self.desc = KvCacheDesc(k.data_ptr(), v.data_ptr(), ks, vs, shape[0], shape[1], shape[2], shape[3], shape[4],
                                 KV_INT8 if int8 else KV_F16)
-        self.ref = ctypes.cast(ctypes.pointer(self.desc), _P)
+        self.ref = ctypes.addressof(self.desc)
 
 
 class Q8Error(RuntimeError):
@@ -596,29 +597,37 @@ def empty_kv_cache(layers: int, n_pages: int, kv_heads: int, page_size: int, hea
     return KvCache(k, v, ks, vs)
 
 
-def _opt(t):
-    return _ptr(t) if t is not None else ctypes.c_void_p(0)
+def _beside(t, dtype, dev, name):
+    """The device pointer of a contiguous tensor of this type on CUDA device `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of {dtype} on cuda:{dev}, got {t.dtype} on {t.device}")
+    return t.data_ptr()
 
 
-def _need_i32(device, **tensors):
-    """Contiguous int32 CUDA tensors on one device, the current one (None passes)."""
+_kv_fns = {}  # entry points of the loaded library
+
+
+def _kv_call(name, args, dev, stream, bind, keep):
+    """Launch (or bind) a key/value cache call on `stream`, or on the current stream of the tensors' device."""
     import torch
 
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, which is not the current device")
-    for name, t in tensors.items():
-        if t is not None:
-            _need(t, torch.int32, name)
-            if t.device != device:
-                raise ValueError(f"{name}: on {t.device}, expected {device}")
-
-
-def _bind_or_call(name, args, bind, keep):
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: tensors on cuda:{dev}, which is not the current device")
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    args += (stream,)
     if bind:
         b = Bound(name, args)
         b._keep = keep
         return b
-    _check(name, getattr(lib(), name)(*args))
+    fn = _kv_fns.get(name)
+    if fn is None:
+        fn = _kv_fns[name] = getattr(lib(), name)
+    st = fn(*args)
+    if st != 0:
+        raise Q8Error(name, st)
     return None
 
 
@@ -632,38 +641,37 @@ def q8_kv_plan(cached, fresh, free_pages, table, page_size: int, n_pages: int, s
     ``held`` int32 [batch]: pages each row has already (default ceil(cached / page_size)); ``held_out``: after the step."""
     import torch
 
-    dev = cached.device
-    _need_i32(dev, cached=cached, fresh=fresh, free_pages=free_pages, table=table, starts=starts, slots=slots,
-              positions=positions, needed=needed, parents=parents, held=held, held_out=held_out)
-    batch, tokens = cached.numel(), slots.numel()
-    if (table.dim() != 2 or table.shape[0] != batch or fresh.numel() != batch or starts.numel() != batch + 1
-            or positions.numel() != tokens or needed.numel() != 1 or (parents is not None and parents.numel() != tokens)
-            or (held is not None and held.numel() != batch) or (held_out is not None and held_out.numel() != batch)):
-        raise ValueError("shape mismatch")
-    if masks is not None:
-        _need(masks, torch.int64, "masks")
-        if masks.numel() != tokens or masks.device != dev:
-            raise ValueError("masks: expected one int64 per token")
+    i32, dev = torch.int32, cached.get_device()
+    batch, tokens, shape = cached.numel(), slots.numel(), table.shape
     n_free = free_pages.numel() if free_pages is not None else 0
-    args = (_ptr(cached), _ptr(fresh), batch, _opt(held), _opt(free_pages if n_free else None), n_free, _ptr(table),
-            table.shape[1], page_size, n_pages, _opt(parents), tokens, _ptr(starts), _ptr(slots), _ptr(positions),
-            _opt(masks), _ptr(needed), _opt(held_out), _stream(stream))
-    return _bind_or_call("q8_kv_plan", args, bind, (cached, fresh, held, free_pages, table, parents, starts, slots,
-                                                    positions, masks, needed, held_out))
+    if (len(shape) != 2 or shape[0] != batch or fresh.numel() != batch or starts.numel() != batch + 1
+            or positions.numel() != tokens or needed.numel() != 1 or (parents is not None and parents.numel() != tokens)
+            or (masks is not None and masks.numel() != tokens) or (held is not None and held.numel() != batch)
+            or (held_out is not None and held_out.numel() != batch)):
+        raise ValueError("shape mismatch")
+    args = (_beside(cached, i32, dev, "cached"), _beside(fresh, i32, dev, "fresh"), batch,
+            _beside(held, i32, dev, "held") if held is not None else None,
+            _beside(free_pages, i32, dev, "free_pages") if n_free else None, n_free, _beside(table, i32, dev, "table"),
+            shape[1], page_size, n_pages, _beside(parents, i32, dev, "parents") if parents is not None else None, tokens,
+            _beside(starts, i32, dev, "starts"), _beside(slots, i32, dev, "slots"),
+            _beside(positions, i32, dev, "positions"),
+            _beside(masks, torch.int64, dev, "masks") if masks is not None else None,
+            _beside(needed, i32, dev, "needed"), _beside(held_out, i32, dev, "held_out") if held_out is not None else None)
+    return _kv_call("q8_kv_plan", args, dev, stream, bind, (cached, fresh, held, free_pages, table, parents, starts, slots,
+                                                            positions, masks, needed, held_out))
 
 
 def q8_kv_append(cache: KvCache, layer: int, k, v, slots, stream=None, bind=False):
     """Write k, v f32 [tokens][kv_heads * head_dim] to the cache slots of one layer (int32 [tokens], < 0: skipped)."""
     import torch
 
-    _need(k, torch.float32, "k"), _need(v, torch.float32, "v")
-    dev = cache.k.device
-    _need_i32(dev, slots=slots)
-    tokens, d = slots.numel(), cache.desc
-    if (k.numel() != tokens * d.kv_heads * d.head_dim or v.numel() != k.numel() or k.device != dev or v.device != dev):
-        raise ValueError("k, v: expected [tokens][kv_heads * head_dim] beside the cache")
-    args = (cache.ref, layer, _ptr(k), _ptr(v), _ptr(slots), tokens, _stream(stream))
-    return _bind_or_call("q8_kv_append", args, bind, (cache, k, v, slots))
+    dev, d, tokens = cache.dev, cache.desc, slots.numel()
+    size = tokens * d.kv_heads * d.head_dim
+    if k.numel() != size or v.numel() != size:
+        raise ValueError("k, v: expected [tokens][kv_heads * head_dim]")
+    args = (cache.ref, layer, _beside(k, torch.float32, dev, "k"), _beside(v, torch.float32, dev, "v"),
+            _beside(slots, torch.int32, dev, "slots"), tokens)
+    return _kv_call("q8_kv_append", args, dev, stream, bind, (cache, k, v, slots))
 
 
 def q8_tree_attention_workspace_bytes(cache: KvCache, heads: int, max_fresh: int) -> int:
@@ -682,51 +690,49 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
     q8_tree_attention_workspace_bytes(...) bytes; when None one is allocated here with PyTorch."""
     import torch
 
-    _need(q, torch.float32, "q")
-    dev, d = cache.k.device, cache.desc
-    _need_i32(dev, table=table, cached=cached, starts=starts)
+    dev, d, i32 = cache.dev, cache.desc, torch.int32
+    dim, size, shape, tshape = d.head_dim, q.numel(), q.shape, table.shape
     batch = cached.numel()
-    if q.dim() != 2 or q.device != dev or q.shape[1] % d.head_dim:
-        raise ValueError("q: expected [tokens][heads * head_dim] beside the cache")
-    tokens, heads = q.shape[0], q.shape[1] // d.head_dim
-    if table.dim() != 2 or table.shape[0] != batch or starts.numel() != batch + 1:
-        raise ValueError("shape mismatch")
-    for t, dt, n, size in ((y, torch.float32, "y", q.numel()), (qs, torch.int8, "qs", q.numel()),
-                           (ds, torch.int32, "ds", q.numel() // 32), (masks, torch.int64, "masks", tokens)):
-        if t is not None:
-            _need(t, dt, n)
-            if t.device != dev or t.numel() < size:
-                raise ValueError(f"{n}: fewer than {size} elements, or not beside the cache")
+    if len(shape) != 2 or shape[1] % dim or len(tshape) != 2 or tshape[0] != batch or starts.numel() != batch + 1:
+        raise ValueError("q: expected [tokens][heads * head_dim]; table [batch][max_pages], starts [batch + 1]")
+    tokens, heads = shape[0], shape[1] // dim
+    if ((y is not None and y.numel() < size) or (qs is not None and qs.numel() < size)
+            or (ds is not None and ds.numel() < size // 32) or (masks is not None and masks.numel() < tokens)):
+        raise ValueError("y, qs, ds or masks: fewer rows than q")
     max_fresh = max_fresh or tokens
-    max_len = max_len or table.shape[1] * d.page_size
     if workspace is None:
         nbytes = q8_tree_attention_workspace_bytes(cache, heads, max_fresh)
         if stream is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.k.device)
         else:  # from the pool of the stream that uses it, so that it is not handed out again too early
             with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _need(workspace, torch.uint8, "workspace")
-    if workspace.device != dev:
-        raise ValueError("workspace: not beside the cache")
-    args = (cache.ref, layer, _ptr(q), heads, d.head_dim ** -0.5 if scale is None else scale, _ptr(table), table.shape[1],
-            _ptr(cached), _ptr(starts), batch, _opt(masks), tokens, max_fresh, max_len, _opt(y), _opt(qs), _opt(ds),
-            _ptr(workspace), workspace.numel(), _stream(stream))
-    return _bind_or_call("q8_tree_attention", args, bind, (cache, q, table, cached, starts, masks, y, qs, ds, workspace))
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.k.device)
+    args = (cache.ref, layer, _beside(q, torch.float32, dev, "q"), heads, dim ** -0.5 if scale is None else scale,
+            _beside(table, i32, dev, "table"), tshape[1], _beside(cached, i32, dev, "cached"),
+            _beside(starts, i32, dev, "starts"), batch,
+            _beside(masks, torch.int64, dev, "masks") if masks is not None else None, tokens, max_fresh,
+            max_len or tshape[1] * d.page_size, _beside(y, torch.float32, dev, "y") if y is not None else None,
+            _beside(qs, torch.int8, dev, "qs") if qs is not None else None,
+            _beside(ds, i32, dev, "ds") if ds is not None else None, _beside(workspace, torch.uint8, dev, "workspace"),
+            workspace.numel())
+    return _kv_call("q8_tree_attention", args, dev, stream, bind, (cache, q, table, cached, starts, masks, y, qs, ds,
+                                                                   workspace))
 
 
 def q8_kv_accept(cache: KvCache, table, cached, fresh, paths, counts, lens, stream=None, bind=False):
     """Move each sequence's accepted path (paths int32 [batch][width], counts int32 [batch]) to the front of its
     fresh tokens, in every layer; lens int32 [batch] (output) = cached + counts."""
-    dev = cache.k.device
-    _need_i32(dev, table=table, cached=cached, fresh=fresh, paths=paths, counts=counts, lens=lens)
-    batch = cached.numel()
-    if (table.dim() != 2 or table.shape[0] != batch or paths.dim() != 2 or paths.shape[0] != batch
-            or any(t.numel() != batch for t in (fresh, counts, lens))):
+    import torch
+
+    dev, i32 = cache.dev, torch.int32
+    batch, tshape, pshape = cached.numel(), table.shape, paths.shape
+    if (len(tshape) != 2 or tshape[0] != batch or len(pshape) != 2 or pshape[0] != batch or fresh.numel() != batch
+            or counts.numel() != batch or lens.numel() != batch):
         raise ValueError("shape mismatch")
-    args = (cache.ref, _ptr(table), table.shape[1], _ptr(cached), _ptr(fresh), batch, _ptr(paths), _ptr(counts),
-            paths.shape[1], _ptr(lens), _stream(stream))
-    return _bind_or_call("q8_kv_accept", args, bind, (cache, table, cached, fresh, paths, counts, lens))
+    args = (cache.ref, _beside(table, i32, dev, "table"), tshape[1], _beside(cached, i32, dev, "cached"),
+            _beside(fresh, i32, dev, "fresh"), batch, _beside(paths, i32, dev, "paths"),
+            _beside(counts, i32, dev, "counts"), pshape[1], _beside(lens, i32, dev, "lens"))
+    return _kv_call("q8_kv_accept", args, dev, stream, bind, (cache, table, cached, fresh, paths, counts, lens))
 
 
 def empty_plane(rows_pad: int, k: int, device="cuda"):

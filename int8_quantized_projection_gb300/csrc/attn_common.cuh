@@ -296,15 +296,23 @@ int attn_rows_take_error(cudaStream_t s);
 int attn_tiles_launch(const AttnCall &c, cudaStream_t s);
 int attn_tiles_take_error(cudaStream_t s);
 
-// Joins the pieces of every unit that crosses a boundary of the split: CTA c
-// takes the unit that lies across the start of c's stretch, unless an earlier
-// boundary lies in the same unit.  Pieces are added in the order of the line.
+// Joins the pieces of every unit that crosses a boundary of the split: CTA
+// (c - 1, y) takes every gridDim.y-th group of rows of the unit that lies
+// across the start of c's stretch, unless an earlier boundary lies in the same
+// unit.  Bound by latency: the descriptor, the pieces' (m, l), their numerators,
+// each one round of loads; 256 threads are kGroup rows x D/4 columns x as many
+// parts of the pieces, whose sums are added in a fixed order.  Units of few
+// rows have many pieces (33 for one sequence of 4097 tokens), those of 128 rows
+// few.
 template <int D, int kRows>
 static __global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant__ AttnArgs a)
 {
+    constexpr int kCols = D / 4, kGroup = kRows == 128 ? 8 : 2, kParts = 256 / (kGroup * kCols);
+    __shared__ float s_f[kGroup][kAttnCtas], s_l[kGroup];
+    __shared__ float4 s_o[kParts][kGroup][kCols];
     griddep_launch_dependents();
     griddep_wait();
-    const int c = blockIdx.x + 1;
+    const int c = blockIdx.x + 1, tid = threadIdx.x;
     const int4 d0 = a.desc[2 * c], d1 = a.desc[2 * c + 1];
     if (d1.w == 0) return;
     // the unit's place, its end, and the place of its first tile
@@ -312,28 +320,68 @@ static __global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_c
     if (c * per <= f0 || (c - 1) * per > f0) return;
     const int head = 2 * (c - 1) + ((c - 1) * per >= u0 ? 0 : 1);
     const int pieces = 1 + (u1 - 1) / per - c + 1;  // CTAs c .. (u1 - 1) / per, and c - 1
+    auto at = [&](int k) { return k == 0 ? head : 2 * (c + k - 1); };
     Unit u;
     u.b = d1.x, u.kvh = d1.y, u.rt = d1.z;
     attn_sequence(a, u.b, u.cached, u.fresh, u.first);
-    const int rows = u.fresh * a.group;
-    for (int i = blockIdx.y * 256 + threadIdx.x; i < kRows * D / 4; i += 256 * gridDim.y) {
-        const int r = i / (D / 4), col = (i % (D / 4)) * 4;
-        auto at = [&](int k) { return k == 0 ? head : 2 * (c + k - 1); };
-        float m = -INFINITY;
-#pragma unroll 8
-        for (int k = 0; k < pieces; ++k) m = fmaxf(m, a.ml[at(k) * kRows + r].x);
-        float l = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int k = 0; k < pieces; ++k) {
-            const float2 ml = a.ml[at(k) * kRows + r];
-            const float4 x =
-                *reinterpret_cast<const float4 *>(a.part + (static_cast<long long>(at(k)) * kRows + r) * D + col);
-            const float f = ml.x == -INFINITY ? 0.0f : ml.x == m ? 1.0f : exp2_approx(ml.x - m);
-            l += f * ml.y;
-            o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+    const int rows = min(kRows, u.fresh * a.group - u.rt * kRows);
+    const int part = tid / (kGroup * kCols), y = (tid / kCols) % kGroup, col = (tid % kCols) * 4;
+    for (int r0 = kGroup * blockIdx.y; r0 < rows; r0 += kGroup * gridDim.y) {
+        // warp y: the row's (m, l) and each piece's factor
+        if (tid < 32 * kGroup) {
+            const int w = tid >> 5, lane = tid & 31;
+            float2 ml[(kAttnCtas + 31) / 32];
+            float m = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int j = 0; j < (kAttnCtas + 31) / 32; ++j) {
+                ml[j] = make_float2(-INFINITY, 0.0f);
+                if (lane + 32 * j < pieces && r0 + w < kRows) ml[j] = a.ml[at(lane + 32 * j) * kRows + r0 + w];
+                m = fmaxf(m, ml[j].x);
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(Q8_FULL_MASK, m, o));
+#pragma unroll
+            for (int j = 0; j < (kAttnCtas + 31) / 32; ++j) {
+                const float f = ml[j].x == -INFINITY ? 0.0f : ml[j].x == m ? 1.0f : exp2_approx(ml[j].x - m);
+                if (lane + 32 * j < pieces) s_f[w][lane + 32 * j] = f;
+                l += f * ml[j].y;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(Q8_FULL_MASK, l, o);
+            if (lane == 0) s_l[w] = l;
         }
-        attn_store<D>(a, u, u.rt * kRows + r, col, o, l, u.rt * kRows + r < rows);
+        // the numerators' loads do not wait for the factors
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        bool waited = false;
+        for (int k0 = part; k0 < pieces || !waited; k0 += 8 * kParts) {
+            float4 x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (k0 + j * kParts < pieces && r0 + y < kRows)
+                    x[j] = *reinterpret_cast<const float4 *>(
+                        a.part + (static_cast<long long>(at(k0 + j * kParts)) * kRows + r0 + y) * D + col);
+            if (!waited) {
+                __syncthreads();
+                waited = true;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (k0 + j * kParts < pieces && r0 + y < kRows) {
+                    const float f = s_f[y][k0 + j * kParts];
+                    o.x += f * x[j].x, o.y += f * x[j].y, o.z += f * x[j].z, o.w += f * x[j].w;
+                }
+        }
+        s_o[part][y][tid % kCols] = o;
+        __syncthreads();
+        if (tid < kGroup * kCols) {
+#pragma unroll
+            for (int p = 1; p < kParts; ++p) {
+                const float4 z = s_o[p][y][tid % kCols];
+                o.x += z.x, o.y += z.y, o.z += z.z, o.w += z.w;
+            }
+            attn_store<D>(a, u, u.rt * kRows + r0 + y, col, o, s_l[y], r0 + y < rows);
+        }
+        __syncthreads();
     }
 }
 

@@ -6,7 +6,7 @@
 // with the running maximum m per row.  Bound by the cache's bytes: a key and a
 // value are read once for all the rows of a unit, so at 8 rows 32 operations
 // fall on a byte of f16, far below what even the warp-level MMA does per byte
-// of HBM.  So the design is a stream: eight warps a CTA, each with a ring of
+// of HBM.  So the design is a stream: 12 or 8 warps a CTA, each with a ring of
 // its own into which one lane copies 16 keys and 16 values by TMA, with no
 // barrier between the warps until a piece ends.  192 KB of copies are in
 // flight per SM.
@@ -35,9 +35,7 @@ __device__ unsigned int g_rows_err;
 using q8::AttnArgs;
 using q8::Unit;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kTile = 16 * kWarps;   // keys of a tile: 16 per warp
-constexpr int kHead = 1;             // what a unit costs beside its tiles, in tiles
+constexpr int kHead = 4;             // what a unit costs beside its tiles, in tiles
 constexpr float kWeightBits = 6.0f;  // weights are 2^(s - m + 6)
 constexpr float kRaise = 8.0f;       // m may lag the maximum by this
 // The MMA's f32 accumulation truncates: with values of one sign O loses 1e-7 of
@@ -46,11 +44,15 @@ constexpr float kRaise = 8.0f;       // m may lag the maximum by this
 // rounded to nearest, and the next tiles start anew.
 constexpr int kChain = 64;
 
-template <int D, bool kInt8>
+template <int D, bool kInt8, int RG>
 struct Ring {
+    // Twelve warps where 8 rows leave them the registers: a group of 16 keys is a chain of dependent steps (copy, MMAs,
+    // maximum, exponentials, MMAs) of some 2000 cycles, so it takes three warps a scheduler to keep up with HBM.
+    static constexpr int kWarps = RG == 1 ? 12 : 8, kThreads = 32 * kWarps;
+    static constexpr int kTile = 16 * kWarps;              // keys of a tile: 16 per warp
     static constexpr int kMat = 16 * D * (kInt8 ? 1 : 2);  // 16 keys
     static constexpr int kStage = 2 * kMat;                // and 16 values
-    static constexpr int kStages = kInt8 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6);
+    static constexpr int kStages = 196608 / (kWarps * kStage) < 8 ? 196608 / (kWarps * kStage) : 8;
     static constexpr int kScales = kInt8 ? 128 : 0;        // 16 + 16 f32 a stage
     static constexpr int kTx = kStage + kScales;
     static constexpr int offScales = kWarps * kStages * kStage;
@@ -58,11 +60,13 @@ struct Ring {
     static constexpr int offPre = offBars + kWarps * kStages * 8;
     static int smem(int batch) { return offPre + (batch + 1) * 4 + 1024; }
 };
-// the largest ring leaves room for the prefix sums of the largest batch (and 2 KB of static arrays)
-constexpr int kMaxDynamic = 225 * 1024;
-template <int D, bool kInt8>
-constexpr bool ring_fits() { return Ring<D, kInt8>::offPre + (Q8_KV_MAX_BATCH + 1) * 4 + 1024 <= kMaxDynamic; }
-static_assert(ring_fits<128, false>() && ring_fits<128, true>() && ring_fits<64, false>() && ring_fits<64, true>(),
+// the largest ring leaves room for the prefix sums of the largest batch (and 3 KB of static arrays)
+constexpr int kMaxDynamic = 224 * 1024;
+template <int D, bool kInt8, int RG>
+constexpr bool ring_fits() { return Ring<D, kInt8, RG>::offPre + (Q8_KV_MAX_BATCH + 1) * 4 + 1024 <= kMaxDynamic; }
+static_assert(ring_fits<128, false, 1>() && ring_fits<128, true, 1>() && ring_fits<64, false, 1>() && ring_fits<64, true, 1>() &&
+                  ring_fits<128, false, 2>() && ring_fits<128, true, 2>() && ring_fits<64, false, 2>() &&
+                  ring_fits<64, true, 2>(),
               "shared memory");
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -154,12 +158,12 @@ __device__ __forceinline__ void weights(RowState<D> &st, const float (&s)[4], co
 }
 
 template <int D, bool kInt8, int RG>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Ring<D, kInt8, RG>::kThreads, 1)
 attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                  const __grid_constant__ AttnArgs a)
 {
-    using R = Ring<D, kInt8>;
-    constexpr int kRows = 8 * RG;
+    using R = Ring<D, kInt8, RG>;
+    constexpr int kRows = 8 * RG, kWarps = R::kWarps, kThreads = R::kThreads, kTile = R::kTile;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = q8::smem_u32(smem_raw);
     uint8_t *sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -201,6 +205,21 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             const int seen = q8::attn_visible(a, u.cached, u.fresh, min(row0 + kRows, rows));
             const int k0 = t0 * kTile + warp * 16, k1 = min(t1 * kTile, seen);
             const int n = dead || k0 >= k1 ? 0 : (k1 - k0 + kTile - 1) / kTile;  // this warp's 16-key groups
+
+            float2 x[RG][D / 8];  // the rows' q: asked for before the copies, so as not to queue behind them
+#pragma unroll
+            for (int rg = 0; rg < RG; ++rg) {
+                const int row = row0 + rg * 8 + gid, tok = row / a.group;
+                const float *src =
+                    a.q + (static_cast<long long>(u.first + tok) * a.heads + u.kvh * a.group + (row - tok * a.group)) * D;
+#pragma unroll
+                for (int s = 0; s < D / 8; ++s) {
+                    // the contraction's order is free: for int8 a thread's keys come as 8 consecutive codes
+                    const int c = kInt8 ? 32 * (s / 4) + 8 * tig + 2 * (s % 4) : 8 * s + 2 * tig;
+                    x[rg][s] = make_float2(0.0f, 0.0f);
+                    if (row < rows) x[rg][s] = __ldg(reinterpret_cast<const float2 *>(src + c));
+                }
+            }
 
             // cache rows of the groups, 32 at a time, a lane each
             auto fetch = [&](int i) {
@@ -249,20 +268,10 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             q8::RowSight sight[RG];
 #pragma unroll
             for (int rg = 0; rg < RG; ++rg) {
-                const int row = row0 + rg * 8 + gid;
-                sight[rg] = q8::attn_sight(a, u, row);
-                float2 x[D / 8];
+                sight[rg] = q8::attn_sight(a, u, row0 + rg * 8 + gid);
                 float amax = 0.0f;
-                const int tok = row / a.group;
-                const float *src =
-                    a.q + (static_cast<long long>(u.first + tok) * a.heads + u.kvh * a.group + (row - tok * a.group)) * D;
 #pragma unroll
-                for (int s = 0; s < D / 8; ++s) {
-                    // the contraction's order is free: for int8 a thread's keys come as 8 consecutive codes
-                    const int c = kInt8 ? 32 * (s / 4) + 8 * tig + 2 * (s % 4) : 8 * s + 2 * tig;
-                    x[s] = row < rows ? *reinterpret_cast<const float2 *>(src + c) : make_float2(0.0f, 0.0f);
-                    amax = fmaxf(amax, fmaxf(fabsf(x[s].x), fabsf(x[s].y)));
-                }
+                for (int s = 0; s < D / 8; ++s) amax = fmaxf(amax, fmaxf(fabsf(x[rg][s].x), fabsf(x[rg][s].y)));
                 amax = fmaxf(amax, __shfl_xor_sync(Q8_FULL_MASK, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(Q8_FULL_MASK, amax, 2));
                 // the row's largest value to [1, 2): the low parts keep 22 bits of it
@@ -271,8 +280,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 qs[rg] = q8::pow2(e) * a.scale;
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    q8::split_f16(x[2 * s].x * down, x[2 * s].y * down, qa[rg][s][0], qa[rg][s][1]);
-                    q8::split_f16(x[2 * s + 1].x * down, x[2 * s + 1].y * down, qa[rg][s][2], qa[rg][s][3]);
+                    q8::split_f16(x[rg][2 * s].x * down, x[rg][2 * s].y * down, qa[rg][s][0], qa[rg][s][1]);
+                    q8::split_f16(x[rg][2 * s + 1].x * down, x[rg][2 * s + 1].y * down, qa[rg][s][2], qa[rg][s][3]);
                 }
             }
 
@@ -542,12 +551,13 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 template <int D, bool kInt8, int RG>
 int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int slot, cudaStream_t s)
 {
-    const int smem = Ring<D, kInt8>::smem(a.batch);
+    using R = Ring<D, kInt8, RG>;
+    const int smem = R::smem(a.batch);
     const void *fn = reinterpret_cast<const void *>(attn_rows_kernel<D, kInt8, RG>);
     if (!q8::set_max_dynamic_smem(fn, kMaxDynamic, slot)) return Q8_ERR_LAUNCH;
-    const int st = q8::launch_pdl(attn_rows_kernel<D, kInt8, RG>, dim3(q8::kAttnCtas), dim3(kThreads), smem, s, mk, mv, a);
+    const int st = q8::launch_pdl(attn_rows_kernel<D, kInt8, RG>, dim3(q8::kAttnCtas), dim3(R::kThreads), smem, s, mk, mv, a);
     if (st != Q8_OK) return st;
-    return q8::launch_pdl(q8::attn_combine_kernel<D, 8 * RG>, dim3(q8::kAttnCtas - 1, (8 * RG * D / 4 + 255) / 256), dim3(256), 0, s,
+    return q8::launch_pdl(q8::attn_combine_kernel<D, 8 * RG>, dim3(q8::kAttnCtas - 1, 4 * RG), dim3(256), 0, s,
                           a);
 }
 

@@ -1006,7 +1006,7 @@ int launch_tiles(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a
     const int st = q8::launch_pdl(attn_tiles_kernel<D, kInt8>, dim3(q8::kAttnCtas), dim3(L::kThreads), L::smem(a.batch), s, mk,
                                   mv, a, box);
     if (st != Q8_OK) return st;
-    return q8::launch_pdl(q8::attn_combine_kernel<D, kRows>, dim3(q8::kAttnCtas - 1, kRows * D / 4 / 256), dim3(256), 0, s, a);
+    return q8::launch_pdl(q8::attn_combine_kernel<D, kRows>, dim3(q8::kAttnCtas - 1, 8), dim3(256), 0, s, a);
 }
 
 } // namespace

@@ -598,9 +598,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 m[y] = msum[y] = -INFINITY, l[y] = 0.0f, ii[y] = q8::pow2(126), e[y] = -126;
             }
             bool ok = true;
-            Walk nx = w;
-            more = nx.next(a, pre);
-            if (more) prefetch_q(nx.u);
+            {  // (the walk's next state is not kept: the tiles need the registers)
+                Walk ahead = w;
+                if (ahead.next(a, pre)) prefetch_q(ahead.u);
+            }
             for (int i = 0; ok && i < w.n; ++i) {
                 const int t = T + i, key0 = (w.t0 + i) * kTile;
                 const bool masked = key0 + kTile > min(all_see, w.kend);
@@ -642,6 +643,14 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                         }
                     }
                 }
+                // of keys k .. k + 31, those that a row sees, from this thread's first column on
+                auto seen_of = [&](const q8::RowSight &sight, int k) {
+                    const int below = max(0, min(32, sight.all - k)), sh = u.cached - k;  // bit b of the mask is key k + sh + b
+                    uint32_t see = below == 32 ? ~0u : (1u << below) - 1u;
+                    if (sh >= 0 && sh < 32) see |= static_cast<uint32_t>(sight.mask << sh);
+                    else if (sh < 0 && sh > -64) see |= static_cast<uint32_t>(sight.mask >> -sh);
+                    return see >> c2;
+                };
                 if (odd) {
                     // hidden keys get score -inf; int8: the largest scale is taken over what the row sees, and a
                     // scale that is not finite makes the scores that see it NaN
@@ -651,12 +660,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                         big[y] = 0.0f;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const int k = key0 + 32 * c, below = max(0, min(32, sight.all - k));
-                            uint32_t see = below == 32 ? ~0u : (1u << below) - 1u;  // of keys k .. k + 31
-                            const int sh = u.cached - k;                            // bit b of the mask is key k + sh + b
-                            if (sh >= 0 && sh < 32) see |= static_cast<uint32_t>(sight.mask << sh);
-                            else if (sh < 0 && sh > -64) see |= static_cast<uint32_t>(sight.mask >> -sh);
-                            see >>= c2;
+                            const uint32_t see = seen_of(sight, key0 + 32 * c);
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {  // column 8 * (j / 2) + c2 + j % 2 of the 32
                                 uint32_t &z = s[16 * c + 4 * (j >> 1) + 2 * y + (j & 1)];
@@ -728,17 +732,27 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                         p.x = q8::exp2_approx(p.x);
                         p.y = q8::exp2_approx(p.y);
                         sum[y] = __fadd2_rn(sum[y], p);
-                        if (kInt8) {
-                            // within +-1 for what the row sees; a hidden key's may be anything, its weight is 0
-                            float2 x = __fmul2_rn(v2, make_float2(ii[y], ii[y]));
-                            x.x = fminf(fmaxf(x.x, -1.0f), 1.0f), x.y = fminf(fmaxf(x.y, -1.0f), 1.0f);
-                            p = __fmul2_rn(p, x);
-                        }
+                        if (kInt8) p = __fmul2_rn(p, __fmul2_rn(v2, make_float2(ii[y], ii[y])));  // |v2 * ii| <= 1 if seen
                         q8::split_f16(p.x, p.y, z[0], z[1]);
                     }
                 }
 #pragma unroll
                 for (int y = 0; y < 2; ++y) l[y] += sum[y].x + sum[y].y;
+                if (kInt8 && odd) {  // a hidden key's scale may be anything: 0 * it is not the weight
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t see = seen_of(y ? sight1 : sight0, key0 + 32 * c);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t keep =
+                                    ((see >> (8 * j)) & 1u ? 0xffffu : 0u) | ((see >> (8 * j)) & 2u ? 0xffff0000u : 0u);
+                                s[16 * c + 4 * j + 2 * y] &= keep;
+                                s[16 * c + 4 * j + 2 * y + 1] &= keep;
+                            }
+                        }
+                }
                 // P and O are free once the products of the tile before are done
                 if (t > 0) {
                     ok = products_done(t - 1);
@@ -833,6 +847,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     if (kInt8) arrive(bar(L::bCe + t % kScaleSlots));
                 }
             }
+            Walk nx = w;
+            more = nx.next(a, pre);
             if (more && ok) write_q(nx.u, s_row + 128 * ((piece & 1) ^ 1));  // every score of this unit is computed
                 ok = ok && products_done(T + w.n - 1);
                 tc_fence_after();
@@ -938,8 +954,6 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         // Eight lanes take half a row each of two neighbouring rows: with the 128-byte swizzle their 16-byte
         // stores then fall into distinct banks.
         const int c0 = tid - 384;
-        int T = 0;
-        bool ok = true;
         auto widen = [&](uint32_t src_off, uint32_t dst_off) {
             constexpr int kChunks = D / 16;  // 16 codes each
 #pragma unroll 4
@@ -968,24 +982,32 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             }
             q8::fence_proxy_async_smem();
         };
-        while (ok && w.next(a, pre)) {
-            for (int i = 0; i < w.n; ++i, ++T) {
-                const int st = T & 1;
-                const uint32_t par = static_cast<uint32_t>(T >> 1) & 1u, last = static_cast<uint32_t>((T - 1) >> 1) & 1u;
-                ok = warp_wait(bar(L::bRKf + st), par, abort_flag) &&
-                     (T == 0 || warp_wait(bar(L::bKe + (st ^ 1)), last, abort_flag));  // the last tile's scores are done
-                if (!ok) break;
-                widen(L::offRaw + st * L::kRaw, L::offK);
-                arrive(bar(L::bKf + st));
-                arrive(bar(L::bRKe + st));
-                ok = warp_wait(bar(L::bRVf + st), par, abort_flag) &&
-                     (T == 0 || warp_wait(bar(L::bVe + (st ^ 1)), last, abort_flag));
-                if (!ok) break;
-                widen(L::offRaw + (2 + st) * L::kRaw, L::offV);
-                arrive(bar(L::bVf + st));
-                arrive(bar(L::bRVe + st));
-            }
-        }
+        // the codes of the CTA's tile t, once the tile before has been used
+        auto widen_k = [&](int t) {
+            const int st = t & 1;
+            if (!warp_wait(bar(L::bRKf + st), static_cast<uint32_t>(t >> 1) & 1u, abort_flag) ||
+                (t > 0 && !warp_wait(bar(L::bKe + (st ^ 1)), static_cast<uint32_t>((t - 1) >> 1) & 1u, abort_flag)))
+                return false;
+            widen(L::offRaw + st * L::kRaw, L::offK);
+            arrive(bar(L::bKf + st));
+            arrive(bar(L::bRKe + st));
+            return true;
+        };
+        auto widen_v = [&](int t) {
+            const int st = t & 1;
+            if (!warp_wait(bar(L::bRVf + st), static_cast<uint32_t>(t >> 1) & 1u, abort_flag) ||
+                (t > 0 && !warp_wait(bar(L::bVe + (st ^ 1)), static_cast<uint32_t>((t - 1) >> 1) & 1u, abort_flag)))
+                return false;
+            widen(L::offRaw + (2 + st) * L::kRaw, L::offV);
+            arrive(bar(L::bVf + st));
+            arrive(bar(L::bRVe + st));
+            return true;
+        };
+        int tiles = 0;
+        while (w.next(a, pre)) tiles += w.n;
+        // a tile's K before the last tile's V: the scores run ahead of the products
+        bool ok = tiles == 0 || widen_k(0);
+        for (int t = 0; ok && t < tiles; ++t) ok = (t + 1 == tiles || widen_k(t + 1)) && widen_v(t);
     }
     if (bad_data) atomicOr(&g_tiles_err, q8::kKvErrData);
 

@@ -611,9 +611,6 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                       warp_wait(bar(L::bCf + t % kScaleSlots), static_cast<uint32_t>(t / kScaleSlots) & 1u, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t s[64];
-                tc_ld16x64(tl, s);
-                tc_ld16x64(tl + 64, s + 32);
                 float all_big = 0.0f;  // int8: the tile's largest value scale
                 bool odd = masked;     // some row sees not every key, or a value scale is not finite
                 if (kInt8) {
@@ -623,26 +620,6 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     const float sum = (v4.x + v4.y) + (v4.z + v4.w);
                     odd |= __any_sync(Q8_FULL_MASK, !(fabsf(sum) <= 3.4028235e38f));
                 }
-                float top[2] = {-INFINITY, -INFINITY}, big[2] = {all_big, all_big};
-                tc_wait_ld();
-                tc_regs32(s);
-                tc_regs32(s + 32);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive(bar(L::bSr));  // the next tile's scores may come
-                if (kInt8) {  // scores by their keys' scales
-#pragma unroll
-                    for (int rep = 0; rep < 16; ++rep) {
-                        const float2 k2 = *reinterpret_cast<const float2 *>(sc + 8 * rep + c2);
-#pragma unroll
-                        for (int y = 0; y < 4; y += 2) {
-                            const float2 z = __fmul2_rn(
-                                make_float2(__uint_as_float(s[4 * rep + y]), __uint_as_float(s[4 * rep + y + 1])), k2);
-                            s[4 * rep + y] = __float_as_uint(z.x);
-                            s[4 * rep + y + 1] = __float_as_uint(z.y);
-                        }
-                    }
-                }
                 // of keys k .. k + 31, those that a row sees, from this thread's first column on
                 auto seen_of = [&](const q8::RowSight &sight, int k) {
                     const int below = max(0, min(32, sight.all - k)), sh = u.cached - k;  // bit b of the mask is key k + sh + b
@@ -651,38 +628,92 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     else if (sh < 0 && sh > -64) see |= static_cast<uint32_t>(sight.mask >> -sh);
                     return see >> c2;
                 };
-                if (odd) {
-                    // hidden keys get score -inf; int8: the largest scale is taken over what the row sees, and a
-                    // scale that is not finite makes the scores that see it NaN
+                float top[2] = {-INFINITY, -INFINITY}, big[2] = {all_big, all_big};
+                if (odd) big[0] = big[1] = 0.0f;
+                // f16: all scores in 64 registers, read once.  int8: in two passes of two loops of 64 columns, the scores read
+                // twice, because straight-line code for 64 columns' scales, with the MMA and widening codes running beside
+                // it, was bound by its own fetching and by spills (f16 in two passes: 150 -> 192 us for a prompt of 3325 tokens;
+                // int8 in one: 161 -> 186 us for 16 trees of 64 nodes).
+                uint32_t s[kInt8 ? 32 : 64];
+                if constexpr (!kInt8) {
+                    tc_ld16x64(tl, s);
+                    tc_ld16x64(tl + 64, s + 32);
+                    tc_wait_ld();
+                    tc_regs32(s);
+                    tc_regs32(s + 32);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(bar(L::bSr));  // the next tile's scores may come
+                    if (odd) {  // hidden keys get score -inf
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const q8::RowSight &sight = y ? sight1 : sight0;
-                        big[y] = 0.0f;
+                        for (int y = 0; y < 2; ++y)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t see = seen_of(sight, key0 + 32 * c);
+                            for (int c = 0; c < 4; ++c) {
+                                const uint32_t see = seen_of(y ? sight1 : sight0, key0 + 32 * c);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {  // column 8 * (j / 2) + c2 + j % 2 of the 32
-                                uint32_t &z = s[16 * c + 4 * (j >> 1) + 2 * y + (j & 1)];
-                                const bool seen = (see >> (8 * (j >> 1) + (j & 1))) & 1u;
-                                if (kInt8) {
-                                    const float v = sc[128 + 32 * c + 8 * (j >> 1) + c2 + (j & 1)];
-                                    if (!(fabsf(v) <= 3.4028235e38f)) z = 0x7fffffffu;
-                                    else if (seen) big[y] = fmaxf(big[y], fabsf(v));
-                                }
-                                if (!seen) z = 0xff800000u;
+                                for (int j = 0; j < 8; ++j)  // column 8 * (j / 2) + c2 + j % 2 of the 32
+                                    if (!((see >> (8 * (j >> 1) + (j & 1))) & 1u))
+                                        s[16 * c + 4 * (j >> 1) + 2 * y + (j & 1)] = 0xff800000u;
+                            }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 64; j += 4) {
+                        top[0] = fmaxf(fmaxf(top[0], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
+                        top[1] = fmaxf(fmaxf(top[1], __uint_as_float(s[j + 2])), __uint_as_float(s[j + 3]));
+                    }
+                } else {
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        tc_ld16x64(tl + 64 * h, s);
+                        tc_wait_ld();
+                        tc_regs32(s);
+                        // scores by their keys' scales
+#pragma unroll
+                        for (int rep = 0; rep < 8; ++rep) {
+                            const float2 k2 = *reinterpret_cast<const float2 *>(sc + 64 * h + 8 * rep + c2);
+#pragma unroll
+                            for (int y = 0; y < 4; y += 2) {
+                                const float2 z = __fmul2_rn(
+                                    make_float2(__uint_as_float(s[4 * rep + y]), __uint_as_float(s[4 * rep + y + 1])), k2);
+                                s[4 * rep + y] = __float_as_uint(z.x);
+                                s[4 * rep + y + 1] = __float_as_uint(z.y);
                             }
                         }
-                        if (kInt8) {
+                        if (odd) {
+                            // hidden keys get score -inf; the largest scale is taken over what the row sees, and a
+                            // scale that is not finite makes the scores that see it NaN
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    const uint32_t see = seen_of(y ? sight1 : sight0, key0 + 64 * h + 32 * c);
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) {  // column 8 * (j / 2) + c2 + j % 2 of the 32
+                                        uint32_t &z = s[16 * c + 4 * (j >> 1) + 2 * y + (j & 1)];
+                                        const bool seen = (see >> (8 * (j >> 1) + (j & 1))) & 1u;
+                                        const float v = sc[128 + 64 * h + 32 * c + 8 * (j >> 1) + c2 + (j & 1)];
+                                        if (!(fabsf(v) <= 3.4028235e38f)) z = 0x7fffffffu;
+                                        else if (seen) big[y] = fmaxf(big[y], fabsf(v));
+                                        if (!seen) z = 0xff800000u;
+                                    }
+                                }
+                        }
+                        tc_st16x32w(tl + 64 * h, s);
+                        tc_st16x32w(tl + 64 * h + 32, s + 16);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            top[0] = fmaxf(fmaxf(top[0], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
+                            top[1] = fmaxf(fmaxf(top[1], __uint_as_float(s[j + 2])), __uint_as_float(s[j + 3]));
+                        }
+                    }
+                    if (odd) {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
                             big[y] = fmaxf(big[y], __shfl_xor_sync(Q8_FULL_MASK, big[y], 1));
                             big[y] = fmaxf(big[y], __shfl_xor_sync(Q8_FULL_MASK, big[y], 2));
                         }
                     }
-                }
-#pragma unroll
-                for (int j = 0; j < 64; j += 4) {
-                    top[0] = fmaxf(fmaxf(top[0], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
-                    top[1] = fmaxf(fmaxf(top[1], __uint_as_float(s[j + 2])), __uint_as_float(s[j + 3]));
+                    tc_wait_st();
                 }
                 const float mo[2] = {m[0], m[1]};  // the references of O as it stands
                 const int eo[2] = {e[0], e[1]};
@@ -719,54 +750,89 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     ref[y] = make_float2(z, z);
                     sum[y] = make_float2(0.0f, 0.0f);
                 }
-                // the weights, as pairs of f16 parts over the scores' registers
+                if constexpr (!kInt8) {
+                    // the weights, as pairs of f16 parts over the scores' registers
 #pragma unroll
-                for (int rep = 0; rep < 16; ++rep) {
-                    float2 v2 = make_float2(1.0f, 1.0f);
-                    if (kInt8) v2 = *reinterpret_cast<const float2 *>(sc + 128 + 8 * rep + c2);
+                    for (int rep = 0; rep < 16; ++rep) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        uint32_t *z = s + 4 * rep + 2 * y;
-                        float2 p = __ffma2_rn(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])),
-                                              make_float2(qq[y], qq[y]), ref[y]);
-                        p.x = q8::exp2_approx(p.x);
-                        p.y = q8::exp2_approx(p.y);
-                        sum[y] = __fadd2_rn(sum[y], p);
-                        if (kInt8) p = __fmul2_rn(p, __fmul2_rn(v2, make_float2(ii[y], ii[y])));  // |v2 * ii| <= 1 if seen
-                        q8::split_f16(p.x, p.y, z[0], z[1]);
+                        for (int y = 0; y < 2; ++y) {
+                            uint32_t *z = s + 4 * rep + 2 * y;
+                            float2 p = __ffma2_rn(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])),
+                                                  make_float2(qq[y], qq[y]), ref[y]);
+                            p.x = q8::exp2_approx(p.x);
+                            p.y = q8::exp2_approx(p.y);
+                            sum[y] = __fadd2_rn(sum[y], p);
+                            q8::split_f16(p.x, p.y, z[0], z[1]);
+                        }
                     }
-                }
+                    // P and O are free once the products of the tile before are done
+                    if (t > 0) {
+                        ok = products_done(t - 1);
+                        tc_fence_after();
+                    }
 #pragma unroll
-                for (int y = 0; y < 2; ++y) l[y] += sum[y].x + sum[y].y;
-                if (kInt8 && odd) {  // a hidden key's scale may be anything: 0 * it is not the weight
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
+                        for (int j = 0; j < 16; ++j) hi[j] = s[32 * c + 2 * j], lo[j] = s[32 * c + 2 * j + 1];
+                        tc_st16x32(tl + L::kColP + 32 * c, hi);
+                        tc_st16x32(tl + L::kColP + 64 + 32 * c, lo);
+                    }
+                } else {
+                    // Second pass: the weights, in two f16 parts.  P and O are free once the products of the tile before are
+                    // done, and S for the next tile once it is read.
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t hi[16], lo[16];
+                        tc_ld16x64(tl + 64 * h, s);
+                        tc_wait_ld();
+                        tc_regs32(s);
+                        if (h) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive(bar(L::bSr));
+                        }
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t see = seen_of(y ? sight1 : sight0, key0 + 32 * c);
+                        for (int rep = 0; rep < 8; ++rep) {
+                            const float2 v2 = *reinterpret_cast<const float2 *>(sc + 128 + 64 * h + 8 * rep + c2);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t keep =
-                                    ((see >> (8 * j)) & 1u ? 0xffffu : 0u) | ((see >> (8 * j)) & 2u ? 0xffff0000u : 0u);
-                                s[16 * c + 4 * j + 2 * y] &= keep;
-                                s[16 * c + 4 * j + 2 * y + 1] &= keep;
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t *z = s + 4 * rep + 2 * y;
+                                float2 p = __ffma2_rn(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])),
+                                                      make_float2(qq[y], qq[y]), ref[y]);
+                                p.x = q8::exp2_approx(p.x);
+                                p.y = q8::exp2_approx(p.y);
+                                sum[y] = __fadd2_rn(sum[y], p);
+                                p = __fmul2_rn(p, __fmul2_rn(v2, make_float2(ii[y], ii[y])));  // |v2 * ii| <= 1 if seen
+                                q8::split_f16(p.x, p.y, hi[2 * rep + y], lo[2 * rep + y]);
                             }
                         }
-                }
-                // P and O are free once the products of the tile before are done
-                if (t > 0) {
-                    ok = products_done(t - 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
+                        if (odd) {  // a hidden key's scale may be anything: 0 * it is not the weight
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t hi[16], lo[16];
+                            for (int y = 0; y < 2; ++y)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) hi[j] = s[32 * c + 2 * j], lo[j] = s[32 * c + 2 * j + 1];
-                    tc_st16x32(tl + L::kColP + 32 * c, hi);
-                    tc_st16x32(tl + L::kColP + 64 + 32 * c, lo);
+                                for (int c = 0; c < 2; ++c) {
+                                    const uint32_t see = seen_of(y ? sight1 : sight0, key0 + 64 * h + 32 * c);
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) {
+                                        const uint32_t keep =
+                                            ((see >> (8 * j)) & 1u ? 0xffffu : 0u) | ((see >> (8 * j)) & 2u ? 0xffff0000u : 0u);
+                                        hi[8 * c + 2 * j + y] &= keep;
+                                        lo[8 * c + 2 * j + y] &= keep;
+                                    }
+                                }
+                        }
+                        if (h == 0 && t > 0) {
+                            ok = products_done(t - 1);
+                            tc_fence_after();
+                        }
+                        tc_st16x32(tl + L::kColP + 32 * h, hi);
+                        tc_st16x32(tl + L::kColP + 64 + 32 * h, lo);
+                    }
                 }
+                if (!ok) break;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) l[y] += sum[y].x + sum[y].y;
                 if (raise && i % kChain > 0) {
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {

@@ -76,7 +76,8 @@ struct Lay {
     static constexpr int offRaw = offV + kBufs * kMat;  // int8: two stages of K codes, two of V codes
     static constexpr int kRaw = 128 * D;
     static constexpr int offScale = offRaw + (kInt8 ? 4 * kRaw : 0);   // slots of 128 k scales, 128 v scales
-    static constexpr int offRow = offScale + (kInt8 ? kScaleSlots * 1024 : 0);
+    static constexpr int offOnes = offScale + (kInt8 ? kScaleSlots * 1024 : 0);  // int8: 128 scales of 1
+    static constexpr int offRow = offOnes + (kInt8 ? 512 : 0);
     static constexpr int offBar = offRow + 2 * 128 * 4;  // before it: q scales of this unit and the next
     // barriers, by index
     // f16 tiles: full, empty, by the tile's parity (for int8 one buffer, still two barriers)
@@ -170,6 +171,15 @@ __device__ __forceinline__ void tc_st16x32(uint32_t taddr, const uint32_t *r)
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+__device__ __forceinline__ void tc_ld16x32p(uint32_t taddr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
 
 // No use of the registers is scheduled before the wait that precedes this.
@@ -354,6 +364,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         }
         q8::fence_mbar_init();
     }
+    if (kInt8 && tid < 128) reinterpret_cast<float *>(sm + L::offOnes)[tid] = 1.0f;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(q8::smem_u32(tmem_slot)),
                      "r"(512)
@@ -630,83 +641,36 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 };
                 float top[2] = {-INFINITY, -INFINITY}, big[2] = {all_big, all_big};
                 if (odd) big[0] = big[1] = 0.0f;
-                // f16: all scores in 64 registers, read once.  int8: in two passes of two loops of 64 columns, the scores read
-                // twice, because straight-line code for 64 columns' scales, with the MMA and widening codes running beside
-                // it, was bound by its own fetching and by spills (f16 in two passes: 150 -> 192 us for a prompt of 3325 tokens;
-                // int8 in one: 161 -> 186 us for 16 trees of 64 nodes).
-                uint32_t s[kInt8 ? 32 : 64];
-                if constexpr (!kInt8) {
-                    tc_ld16x64(tl, s);
-                    tc_ld16x64(tl + 64, s + 32);
-                    tc_wait_ld();
-                    tc_regs32(s);
-                    tc_regs32(s + 32);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive(bar(L::bSr));  // the next tile's scores may come
-                    if (odd) {  // hidden keys get score -inf
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint32_t see = seen_of(y ? sight1 : sight0, key0 + 32 * c);
-#pragma unroll
-                                for (int j = 0; j < 8; ++j)  // column 8 * (j / 2) + c2 + j % 2 of the 32
-                                    if (!((see >> (8 * (j >> 1) + (j & 1))) & 1u))
-                                        s[16 * c + 4 * (j >> 1) + 2 * y + (j & 1)] = 0xff800000u;
-                            }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 64; j += 4) {
-                        top[0] = fmaxf(fmaxf(top[0], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
-                        top[1] = fmaxf(fmaxf(top[1], __uint_as_float(s[j + 2])), __uint_as_float(s[j + 3]));
-                    }
-                } else {
+                if (odd) {
+                    // Where a row sees not every key: scores go back with -inf for what it does not see.  int8: multiplied
+                    // with their keys' scales already; the largest value scale is taken over what the row sees, and a scale
+                    // that is not finite makes the scores that see it NaN.
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        tc_ld16x64(tl + 64 * h, s);
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t z[16];
+                        tc_ld16x32(tl + 32 * c, z);
                         tc_wait_ld();
-                        tc_regs32(s);
-                        // scores by their keys' scales
+                        tc_regs16(z);
 #pragma unroll
-                        for (int rep = 0; rep < 8; ++rep) {
-                            const float2 k2 = *reinterpret_cast<const float2 *>(sc + 64 * h + 8 * rep + c2);
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t see = seen_of(y ? sight1 : sight0, key0 + 32 * c);
 #pragma unroll
-                            for (int y = 0; y < 4; y += 2) {
-                                const float2 z = __fmul2_rn(
-                                    make_float2(__uint_as_float(s[4 * rep + y]), __uint_as_float(s[4 * rep + y + 1])), k2);
-                                s[4 * rep + y] = __float_as_uint(z.x);
-                                s[4 * rep + y + 1] = __float_as_uint(z.y);
+                            for (int j = 0; j < 8; ++j) {  // column 8 * (j / 2) + c2 + j % 2 of the 32
+                                uint32_t &x = z[4 * (j >> 1) + 2 * y + (j & 1)];
+                                const bool seen = (see >> (8 * (j >> 1) + (j & 1))) & 1u;
+                                if (kInt8) {
+                                    const int key = 32 * c + 8 * (j >> 1) + c2 + (j & 1);
+                                    const float v = sc[128 + key];
+                                    x = __float_as_uint(__uint_as_float(x) * sc[key]);
+                                    if (!(fabsf(v) <= 3.4028235e38f)) x = 0x7fffffffu;
+                                    else if (seen) big[y] = fmaxf(big[y], fabsf(v));
+                                }
+                                if (!seen) x = 0xff800000u;
                             }
                         }
-                        if (odd) {
-                            // hidden keys get score -inf; the largest scale is taken over what the row sees, and a
-                            // scale that is not finite makes the scores that see it NaN
-#pragma unroll
-                            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                                for (int c = 0; c < 2; ++c) {
-                                    const uint32_t see = seen_of(y ? sight1 : sight0, key0 + 64 * h + 32 * c);
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) {  // column 8 * (j / 2) + c2 + j % 2 of the 32
-                                        uint32_t &z = s[16 * c + 4 * (j >> 1) + 2 * y + (j & 1)];
-                                        const bool seen = (see >> (8 * (j >> 1) + (j & 1))) & 1u;
-                                        const float v = sc[128 + 64 * h + 32 * c + 8 * (j >> 1) + c2 + (j & 1)];
-                                        if (!(fabsf(v) <= 3.4028235e38f)) z = 0x7fffffffu;
-                                        else if (seen) big[y] = fmaxf(big[y], fabsf(v));
-                                        if (!seen) z = 0xff800000u;
-                                    }
-                                }
-                        }
-                        tc_st16x32w(tl + 64 * h, s);
-                        tc_st16x32w(tl + 64 * h + 32, s + 16);
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            top[0] = fmaxf(fmaxf(top[0], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
-                            top[1] = fmaxf(fmaxf(top[1], __uint_as_float(s[j + 2])), __uint_as_float(s[j + 3]));
-                        }
+                        tc_st16x32w(tl + 32 * c, z);
                     }
-                    if (odd) {
+                    if (kInt8) {
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
                             big[y] = fmaxf(big[y], __shfl_xor_sync(Q8_FULL_MASK, big[y], 1));
@@ -714,6 +678,47 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                         }
                     }
                     tc_wait_st();
+                }
+                // The maximum, 64 columns at a time (f16: at once, read once).
+                uint32_t s[kInt8 ? 32 : 64];
+                const float *kk = odd ? reinterpret_cast<const float *>(sm + L::offOnes) : sc;
+                auto read_scores = [&](int h) {  // int8: 64 columns from 64 * h on, multiplied with their keys' scales
+                    tc_ld16x64(tl + 64 * h, s);
+                    tc_wait_ld();
+                    tc_regs32(s);
+#pragma unroll
+                    for (int rep = 0; rep < 8; ++rep) {
+                        const float2 k2 = *reinterpret_cast<const float2 *>(kk + 64 * h + 8 * rep + c2);
+#pragma unroll
+                        for (int y = 0; y < 4; y += 2) {
+                            const float2 z = __fmul2_rn(
+                                make_float2(__uint_as_float(s[4 * rep + y]), __uint_as_float(s[4 * rep + y + 1])), k2);
+                            s[4 * rep + y] = __float_as_uint(z.x);
+                            s[4 * rep + y + 1] = __float_as_uint(z.y);
+                        }
+                    }
+                };
+                auto scores_read = [&]() {  // the next tile's may come
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(bar(L::bSr));
+                };
+                if constexpr (!kInt8) {
+                    tc_ld16x64(tl, s);
+                    tc_ld16x64(tl + 64, s + 32);
+                    tc_wait_ld();
+                    tc_regs32(s);
+                    tc_regs32(s + 32);
+                    scores_read();
+                }
+#pragma unroll 1
+                for (int h = 0; h < (kInt8 ? 2 : 1); ++h) {
+                    if (kInt8) read_scores(h);
+#pragma unroll
+                    for (int j = 0; j < (kInt8 ? 32 : 64); j += 4) {
+                        top[0] = fmaxf(fmaxf(top[0], __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
+                        top[1] = fmaxf(fmaxf(top[1], __uint_as_float(s[j + 2])), __uint_as_float(s[j + 3]));
+                    }
                 }
                 const float mo[2] = {m[0], m[1]};  // the references of O as it stands
                 const int eo[2] = {e[0], e[1]};
@@ -750,10 +755,15 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     ref[y] = make_float2(z, z);
                     sum[y] = make_float2(0.0f, 0.0f);
                 }
-                if constexpr (!kInt8) {
-                    // the weights, as pairs of f16 parts over the scores' registers
+                // the weights, as pairs of f16 parts over the scores' registers
+#pragma unroll 1
+                for (int h = 0; h < (kInt8 ? 2 : 1); ++h) {
+                    if (kInt8) read_scores(h);
+                    if (kInt8 && h) scores_read();
 #pragma unroll
-                    for (int rep = 0; rep < 16; ++rep) {
+                    for (int rep = 0; rep < (kInt8 ? 8 : 16); ++rep) {
+                        float2 v2 = make_float2(1.0f, 1.0f);
+                        if (kInt8) v2 = *reinterpret_cast<const float2 *>(sc + 128 + 64 * h + 8 * rep + c2);
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
                             uint32_t *z = s + 4 * rep + 2 * y;
@@ -762,72 +772,38 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                             p.x = q8::exp2_approx(p.x);
                             p.y = q8::exp2_approx(p.y);
                             sum[y] = __fadd2_rn(sum[y], p);
+                            if (kInt8) p = __fmul2_rn(p, __fmul2_rn(v2, make_float2(ii[y], ii[y])));  // |v2 * ii| <= 1 if seen
                             q8::split_f16(p.x, p.y, z[0], z[1]);
                         }
                     }
                     // P and O are free once the products of the tile before are done
-                    if (t > 0) {
+                    if (h == 0 && t > 0) {
                         ok = products_done(t - 1);
                         tc_fence_after();
                     }
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < (kInt8 ? 1 : 2); ++c) {
                         uint32_t hi[16], lo[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) hi[j] = s[32 * c + 2 * j], lo[j] = s[32 * c + 2 * j + 1];
-                        tc_st16x32(tl + L::kColP + 32 * c, hi);
-                        tc_st16x32(tl + L::kColP + 64 + 32 * c, lo);
+                        tc_st16x32(tl + L::kColP + 32 * (h + c), hi);
+                        tc_st16x32(tl + L::kColP + 64 + 32 * (h + c), lo);
                     }
-                } else {
-                    // Second pass: the weights, in two f16 parts.  P and O are free once the products of the tile before are
-                    // done, and S for the next tile once it is read.
+                }
+                if (kInt8 && odd) {  // a hidden key's scale may be anything: 0 * it is not the weight
+                    tc_wait_st();
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t hi[16], lo[16];
-                        tc_ld16x64(tl + 64 * h, s);
+                    for (int c = 0; c < 4; ++c) {  // high parts of 64 keys, and of the next 64; low parts
+                        uint32_t z[16];
+                        tc_ld16x32p(tl + L::kColP + 32 * c, z);
                         tc_wait_ld();
-                        tc_regs32(s);
-                        if (h) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) arrive(bar(L::bSr));
+                        tc_regs16(z);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const uint32_t see = seen_of(j & 1 ? sight1 : sight0, key0 + 64 * (c & 1) + 32 * (j >> 3)) >> (8 * ((j >> 1) & 3));
+                            z[j] &= (see & 1u ? 0xffffu : 0u) | (see & 2u ? 0xffff0000u : 0u);
                         }
-#pragma unroll
-                        for (int rep = 0; rep < 8; ++rep) {
-                            const float2 v2 = *reinterpret_cast<const float2 *>(sc + 128 + 64 * h + 8 * rep + c2);
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const uint32_t *z = s + 4 * rep + 2 * y;
-                                float2 p = __ffma2_rn(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])),
-                                                      make_float2(qq[y], qq[y]), ref[y]);
-                                p.x = q8::exp2_approx(p.x);
-                                p.y = q8::exp2_approx(p.y);
-                                sum[y] = __fadd2_rn(sum[y], p);
-                                p = __fmul2_rn(p, __fmul2_rn(v2, make_float2(ii[y], ii[y])));  // |v2 * ii| <= 1 if seen
-                                q8::split_f16(p.x, p.y, hi[2 * rep + y], lo[2 * rep + y]);
-                            }
-                        }
-                        if (odd) {  // a hidden key's scale may be anything: 0 * it is not the weight
-#pragma unroll
-                            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                                for (int c = 0; c < 2; ++c) {
-                                    const uint32_t see = seen_of(y ? sight1 : sight0, key0 + 64 * h + 32 * c);
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) {
-                                        const uint32_t keep =
-                                            ((see >> (8 * j)) & 1u ? 0xffffu : 0u) | ((see >> (8 * j)) & 2u ? 0xffff0000u : 0u);
-                                        hi[8 * c + 2 * j + y] &= keep;
-                                        lo[8 * c + 2 * j + y] &= keep;
-                                    }
-                                }
-                        }
-                        if (h == 0 && t > 0) {
-                            ok = products_done(t - 1);
-                            tc_fence_after();
-                        }
-                        tc_st16x32(tl + L::kColP + 32 * h, hi);
-                        tc_st16x32(tl + L::kColP + 64 + 32 * h, lo);
+                        tc_st16x32(tl + L::kColP + 32 * c, z);
                     }
                 }
                 if (!ok) break;

@@ -35,7 +35,7 @@ __device__ unsigned int g_rows_err;
 using q8::AttnArgs;
 using q8::Unit;
 
-constexpr int kHead = 4;             // what a unit costs beside its tiles, in tiles
+constexpr int kHead = 3;             // what a unit costs beside its tiles, in tiles
 constexpr float kWeightBits = 6.0f;  // weights are 2^(s - m + 6)
 constexpr float kRaise = 8.0f;       // m may lag the maximum by this
 // The MMA's f32 accumulation truncates: with values of one sign O loses 1e-7 of

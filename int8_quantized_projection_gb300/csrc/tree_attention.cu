@@ -22,7 +22,9 @@ Workspace workspace(int rows, int d)
     return w;
 }
 
-// Packed rows of a unit, by the most a sequence and head can have.
+// Packed rows of a unit, by the most a sequence and head can have.  Measured with 28 heads on 4, head_dim 128, 8 sequences
+// of up to 16001 keys, f16 / int8: for 7 rows 35 / 28 us with 8 rows a unit, 41 / 43 with 16, 41 / 67 with 128; for 14 rows
+// 30 / 31 us with 16 rows a unit, 30 / 48 with 128.
 int rows_of(int64_t max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 128; }
 
 } // namespace
@@ -56,9 +58,9 @@ extern "C" int q8_tree_attention(const q8_kv_cache *cache, int64_t layer, const 
         return Q8_ERR_ARG;
     const int group = static_cast<int>(heads / cache->kv_heads);
     const int rows = rows_of(max_fresh * group);
-    // the line of tiles is counted in 32 bits
+    // the line of tiles and units' heads is counted in 32 bits
     const double line = double(batch) * cache->kv_heads * ((max_fresh * group + rows - 1) / rows) *
-                        ((max_len + 127) / 128);
+                        ((max_len + 127) / 128 + 8);
     if (line > 2.0e9) return Q8_ERR_ARG;
     const Workspace w = workspace(rows, cache->head_dim);
     if (!workspace_ || workspace_bytes < w.bytes) return Q8_ERR_ARG;

@@ -35,6 +35,7 @@ struct AttnArgs {
     int4 *desc;            // [2 * grid] the first piece of each CTA, if it is a part of a unit
     long long tokens;
     int batch, heads, kv_heads, group, max_pages, page, n_pages, max_fresh, max_len;
+    unsigned group_inv;    // 2^32 / group, rounded up (group 1: 2^32 - 1)
     float scale;           // softmax scale * log2(e)
 };
 
@@ -45,11 +46,22 @@ struct Unit {
     int cached, fresh, first;  // the sequence's lengths and first row of q
 };
 
+// Token of a packed row below 2^30: row / group by a product (a division costs
+// some 150 cycles, and a unit's start is a chain of such steps).  The product
+// is off by at most one: rows below 2^30 times a reciprocal too large by less
+// than 64 / 2^32.
+__device__ __forceinline__ int attn_token(const AttnArgs &a, int row)
+{
+    int q = __umulhi(row, a.group_inv);
+    const int r = row - q * a.group;
+    return q + (r >= a.group) - (r < 0);
+}
+
 // Keys that rows [0, r_end) of a sequence's packed rows can see at most.
 __device__ __forceinline__ int attn_visible(const AttnArgs &a, int cached, int fresh, int r_end)
 {
     if (a.masks) return cached + fresh;
-    return cached + min(fresh, (r_end - 1) / a.group + 1);
+    return cached + min(fresh, attn_token(a, r_end - 1) + 1);
 }
 
 // Lengths of sequence b; fresh = 0 (no work) when a value is out of range.
@@ -83,7 +95,7 @@ struct RowMap {
     int group;
 
     __device__ __forceinline__ RowMap(const AttnArgs &a, int row0_)
-        : row0(row0_), tok0(row0_ / a.group), rem0(row0_ - tok0 * a.group), magic((65535u + a.group) / a.group), group(a.group)
+        : row0(row0_), tok0(attn_token(a, row0_)), rem0(row0_ - tok0 * a.group), magic((65535u + a.group) / a.group), group(a.group)
     {
     }
     __device__ __forceinline__ int token(int r) const { return tok0 + static_cast<int>(((rem0 + r) * magic) >> 16); }
@@ -215,7 +227,7 @@ struct RowSight {
 __device__ __forceinline__ RowSight attn_sight(const AttnArgs &a, const Unit &u, int row)
 {
     RowSight s;
-    const int tok = row / a.group;
+    const int tok = attn_token(a, row);
     if (tok >= u.fresh) {  // a row of the tile that does not exist
         s.all = 0;
         s.mask = 0;
@@ -246,7 +258,7 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const Unit &u, int
     // a row that saw nothing has l = 0 and O = 0
     const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
     const float4 r = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    const int tok = row / a.group;
+    const int tok = attn_token(a, row);
     const long long at =
         (static_cast<long long>(u.first + tok) * a.heads + u.kvh * a.group + (row - tok * a.group)) * D + c;
     if (a.y && valid) *reinterpret_cast<float4 *>(a.y + at) = r;

@@ -24,6 +24,15 @@
 // The maximum is raised only when it grows by more than 2^8: weights are
 // kept at 2^6 below the reference, so they stay under 2^14 in f16, and the 64
 // or 128 multiplications of a rescale are rare.
+//
+// Measured (head_dim 128, 28 heads on 4): one decode over 262139 keys, f16,
+// 86.5 us (537 MB, 6.2 TB/s, 0.92 of a copy's rate); 61 ragged ones of up to
+// 8191 keys, int8, 75 us (326 MB, 4.4 TB/s).  Some 10 us of each call are the
+// launches, the line, the first copies' latency, and the join (one sequence of
+// 4097 keys takes 10.4 us).  int8 is bound by the warps' instructions, some 520
+// for 16 keys, of which the widening is a fifth: 16 warps instead of 12 with q
+// in shared memory came to 78 us, the next unit's copies before the join to
+// 75.6, two chains of score MMAs to 78.6; none was kept.
 #include <cuda.h>
 
 #include "attn_common.cuh"
@@ -35,7 +44,8 @@ __device__ unsigned int g_rows_err;
 using q8::AttnArgs;
 using q8::Unit;
 
-constexpr int kHead = 3;             // what a unit costs beside its tiles, in tiles
+// What a unit costs beside its tiles, in tiles (61 ragged int8 decodes of up to 8191 keys with 1: 86 us, 2: 79, 3: 74, 6: 76).
+constexpr int kHead = 3;
 constexpr float kWeightBits = 6.0f;  // weights are 2^(s - m + 6)
 constexpr float kRaise = 8.0f;       // m may lag the maximum by this
 // The MMA's f32 accumulation truncates: with values of one sign O loses 1e-7 of
@@ -209,7 +219,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             float2 x[RG][D / 8];  // the rows' q: asked for before the copies, so as not to queue behind them
 #pragma unroll
             for (int rg = 0; rg < RG; ++rg) {
-                const int row = row0 + rg * 8 + gid, tok = row / a.group;
+                const int row = row0 + rg * 8 + gid, tok = q8::attn_token(a, row);
                 const float *src =
                     a.q + (static_cast<long long>(u.first + tok) * a.heads + u.kvh * a.group + (row - tok * a.group)) * D;
 #pragma unroll
@@ -298,7 +308,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     for (int j = 0; j < 4; ++j) st[rg].o[i][j] = 0.0f;
             }
             // keys that every row of the tile sees
-            const int all_see = u.cached + (a.masks ? 0 : row0 / a.group + 1);
+            const int all_see = u.cached + (a.masks ? 0 : q8::attn_token(a, row0) + 1);
 
             for (int i = 0; i < n; ++i) {
                 if (!__all_sync(Q8_FULL_MASK, q8::mbar_wait_bounded(bars + slot, phase))) {

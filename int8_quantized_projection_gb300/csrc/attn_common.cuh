@@ -35,7 +35,7 @@ struct AttnArgs {
     int4 *desc;            // [2 * grid] the first piece of each CTA, if it is a part of a unit
     long long tokens;
     int batch, heads, kv_heads, group, max_pages, page, n_pages, max_fresh, max_len;
-    unsigned group_inv;    // 2^32 / group, rounded up (group 1: 2^32 - 1)
+    unsigned group_inv;    // kv_inverse(group)
     float scale;           // softmax scale * log2(e)
 };
 
@@ -46,16 +46,9 @@ struct Unit {
     int cached, fresh, first;  // the sequence's lengths and first row of q
 };
 
-// Token of a packed row below 2^30: row / group by a product (a division costs
-// some 150 cycles, and a unit's start is a chain of such steps).  The product
-// is off by at most one: rows below 2^30 times a reciprocal too large by less
-// than 64 / 2^32.
-__device__ __forceinline__ int attn_token(const AttnArgs &a, int row)
-{
-    int q = __umulhi(row, a.group_inv);
-    const int r = row - q * a.group;
-    return q + (r >= a.group) - (r < 0);
-}
+// Token of a packed row (a division costs some 150 cycles, and a unit's start
+// is a chain of such steps).
+__device__ __forceinline__ int attn_token(const AttnArgs &a, int row) { return kv_divide(row, a.group, a.group_inv); }
 
 // Keys that rows [0, r_end) of a sequence's packed rows can see at most.
 __device__ __forceinline__ int attn_visible(const AttnArgs &a, int cached, int fresh, int r_end)

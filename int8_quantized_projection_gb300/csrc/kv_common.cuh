@@ -48,4 +48,14 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+// n / d by a product, for 0 <= n < 2^31 (a division takes some 40 instructions).  inv = kv_inverse(d) is 2^32 / d
+// rounded up, or 2^32 - 1 for d = 1: n * inv / 2^32 is off by at most one either way.  n < 0 gives some value.
+inline unsigned kv_inverse(int64_t d) { return d == 1 ? ~0u : ~0u / static_cast<unsigned>(d) + 1; }
+
+__device__ __forceinline__ int kv_divide(int n, int d, unsigned inv)
+{
+    const int q = __umulhi(n, inv), r = n - q * d;
+    return q + (r >= d) - (r < 0);
+}
+
 } // namespace q8

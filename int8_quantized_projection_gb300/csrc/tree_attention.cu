@@ -83,7 +83,7 @@ extern "C" int q8_tree_attention(const q8_kv_cache *cache, int64_t layer, const 
            reinterpret_cast<float2 *>(ws + w.ml), reinterpret_cast<int4 *>(ws + w.desc), tokens,
            static_cast<int>(batch), static_cast<int>(heads), cache->kv_heads, group, static_cast<int>(max_pages),
            cache->page_size, static_cast<int>(cache->n_pages), static_cast<int>(max_fresh),
-           static_cast<int>(max_len), group == 1 ? ~0u : ~0u / group + 1, scale * 1.4426950408889634f};
+           static_cast<int>(max_len), q8::kv_inverse(group), scale * 1.4426950408889634f};
     c.k = kp, c.v = vp, c.layer_rows = lr, c.dim = D, c.int8 = i8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return rows == 128 ? q8::attn_tiles_launch(c, s) : q8::attn_rows_launch(c, rows, s);

@@ -1,5 +1,5 @@
 // kv_common.cuh -- what the paged key/value cache's kernels share: the checks
-// of a cache descriptor and the split of a step's attention over the CTAs.
+// of a cache descriptor, the error bits, and division by a product.
 #pragma once
 
 #include "q8_common.cuh"

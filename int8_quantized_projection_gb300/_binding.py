@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from array import array
 
 from . import build as _build
 
@@ -87,7 +88,7 @@ class KvCache:
     ``k``, ``v``: f16, or int8 codes, [layers][n_pages][kv_heads][page_size][head_dim]; ``k_scale``,
     ``v_scale``: f32 [layers][n_pages][kv_heads][page_size], with int8 only.  :func:`empty_kv_cache` makes one."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "desc", "ref", "dev")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "kv_heads", "page_size", "head_dim", "dev", "ref", "_words")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
@@ -101,17 +102,21 @@ class KvCache:
         if int8 != (k_scale is not None) or int8 != (v_scale is not None):
             raise ValueError("k_scale and v_scale with int8, and only then")
         dev = self.dev = k.get_device()
-        _beside(k, dt, dev, "k"), _beside(v, dt, dev, "v")
-        ks = vs = None
+        kp, vp = _beside(k, dt, dev, "k"), _beside(v, dt, dev, "v")
+        ks = vs = 0
         if int8:
             if k_scale.shape != shape[:-1] or v_scale.shape != shape[:-1]:
                 raise ValueError("k_scale, v_scale: expected [layers][n_pages][kv_heads][page_size]")
             ks = _beside(k_scale, torch.float32, dev, "k_scale")
             vs = _beside(v_scale, torch.float32, dev, "v_scale")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.desc = KvCacheDesc(k.data_ptr(), v.data_ptr(), ks, vs, shape[0], shape[1], shape[2], shape[3], shape[4],
-                                KV_INT8 if int8 else KV_F16)
-        self.ref = ctypes.addressof(self.desc)
+        layers, n_pages, self.kv_heads, self.page_size, self.head_dim = shape
+        # a KvCacheDesc's bytes (a Structure takes several times as long to make); sizes past 32 bits are refused below
+        if max(shape[2:]) >= 1 << 31:
+            raise ValueError("k: kv_heads, page_size and head_dim have 32 bits")
+        self._words = array("q", (kp, vp, ks, vs, layers, n_pages, shape[2] | shape[3] << 32,
+                                  shape[4] | (KV_INT8 if int8 else KV_F16) << 32))
+        self.ref = self._words.buffer_info()[0]
 
 
 class Q8Error(RuntimeError):
@@ -605,16 +610,17 @@ def _beside(t, dtype, dev, name):
 
 
 _kv_fns = {}  # entry points of the loaded library
+_workspace_sizes = {}  # of q8_tree_attention, by the sizes they depend on
 
 
 def _kv_call(name, args, dev, stream, bind, keep):
     """Launch (or bind) a key/value cache call on `stream`, or on the current stream of the tensors' device."""
-    import torch
+    from torch import _C
 
-    if dev != torch._C._cuda_getDevice():
+    if dev != _C._cuda_getDevice():
         raise ValueError(f"{name}: tensors on cuda:{dev}, which is not the current device")
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
+        stream = _C._cuda_getCurrentRawStream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     args += (stream,)
@@ -665,8 +671,8 @@ def q8_kv_append(cache: KvCache, layer: int, k, v, slots, stream=None, bind=Fals
     """Write k, v f32 [tokens][kv_heads * head_dim] to the cache slots of one layer (int32 [tokens], < 0: skipped)."""
     import torch
 
-    dev, d, tokens = cache.dev, cache.desc, slots.numel()
-    size = tokens * d.kv_heads * d.head_dim
+    dev, tokens = cache.dev, slots.numel()
+    size = tokens * cache.kv_heads * cache.head_dim
     if k.numel() != size or v.numel() != size:
         raise ValueError("k, v: expected [tokens][kv_heads * head_dim]")
     args = (cache.ref, layer, _beside(k, torch.float32, dev, "k"), _beside(v, torch.float32, dev, "v"),
@@ -690,8 +696,8 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
     q8_tree_attention_workspace_bytes(...) bytes; when None one is allocated here with PyTorch."""
     import torch
 
-    dev, d, i32 = cache.dev, cache.desc, torch.int32
-    dim, size, shape, tshape = d.head_dim, q.numel(), q.shape, table.shape
+    dev, dim, i32 = cache.dev, cache.head_dim, torch.int32
+    size, shape, tshape = q.numel(), q.shape, table.shape
     batch = cached.numel()
     if len(shape) != 2 or shape[1] % dim or len(tshape) != 2 or tshape[0] != batch or starts.numel() != batch + 1:
         raise ValueError("q: expected [tokens][heads * head_dim]; table [batch][max_pages], starts [batch + 1]")
@@ -701,7 +707,12 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
         raise ValueError("y, qs, ds or masks: fewer rows than q")
     max_fresh = max_fresh or tokens
     if workspace is None:
-        nbytes = q8_tree_attention_workspace_bytes(cache, heads, max_fresh)
+        key = cache.kv_heads, dim, heads, max_fresh
+        nbytes = _workspace_sizes.get(key)
+        if nbytes is None:
+            nbytes = q8_tree_attention_workspace_bytes(cache, heads, max_fresh)
+            if len(_workspace_sizes) < 1024:
+                _workspace_sizes[key] = nbytes
         if stream is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.k.device)
         else:  # from the pool of the stream that uses it, so that it is not handed out again too early
@@ -711,7 +722,7 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
             _beside(table, i32, dev, "table"), tshape[1], _beside(cached, i32, dev, "cached"),
             _beside(starts, i32, dev, "starts"), batch,
             _beside(masks, torch.int64, dev, "masks") if masks is not None else None, tokens, max_fresh,
-            max_len or tshape[1] * d.page_size, _beside(y, torch.float32, dev, "y") if y is not None else None,
+            max_len or tshape[1] * cache.page_size, _beside(y, torch.float32, dev, "y") if y is not None else None,
             _beside(qs, torch.int8, dev, "qs") if qs is not None else None,
             _beside(ds, i32, dev, "ds") if ds is not None else None, _beside(workspace, torch.uint8, dev, "workspace"),
             workspace.numel())

@@ -607,7 +607,10 @@ Q8_API int q8_kv_append(const q8_kv_cache *cache, int64_t layer, const float *k,
  *   workspace, workspace_bytes : device scratch of at least
  *              q8_tree_attention_workspace_bytes(...) bytes, 16-byte aligned;
  *              contents ignored on entry.  Two calls, or two captured graphs,
- *              may share one only if they are ordered on one stream.
+ *              may share one only if they are ordered on one stream.  NULL
+ *              and 0 where q8_tree_attention_needs_workspace(...) is 0 for the
+ *              call's heads, batch, max_fresh and max_len (a few rows over short
+ *              contexts, which join in shared memory).
  * Precision: q enters the tensor cores as the sum of two f16 parts of its row
  * scaled by a power of two (22 bits of the row's largest value), softmax
  * weights likewise, keys and values exactly as the cache holds them; products
@@ -616,9 +619,11 @@ Q8_API int q8_kv_append(const q8_kv_cache *cache, int64_t layer, const float *k,
  * NaN or an infinity in a row's q makes the row NaN; one in a value that the
  * row sees makes what it enters non-finite (a score of -inf has weight 0).
  * Q8_ERR_ARG: a NULL pointer, layer or size out of range, neither y nor a
- * plane, one of qs and ds alone, a short workspace.
+ * plane, one of qs and ds alone, a short workspace where one is needed.
  */
 Q8_API size_t q8_tree_attention_workspace_bytes(const q8_kv_cache *cache, int64_t heads, int64_t max_fresh);
+Q8_API int q8_tree_attention_needs_workspace(const q8_kv_cache *cache, int64_t heads, int64_t batch, int64_t max_fresh,
+                                             int64_t max_len);
 Q8_API int q8_tree_attention(const q8_kv_cache *cache, int64_t layer, const float *q, int64_t heads, float scale,
                              const int32_t *table, int64_t max_pages, const int32_t *cached, const int32_t *starts,
                              int64_t batch, const int64_t *masks, int64_t tokens, int64_t max_fresh,

@@ -43,6 +43,7 @@ from ._binding import (  # noqa: F401
     q8_kv_append,
     q8_kv_plan,
     q8_tree_attention,
+    q8_tree_attention_needs_workspace,
     q8_tree_attention_workspace_bytes,
     q8_check,
     q8_num_sms,

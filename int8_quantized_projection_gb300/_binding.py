@@ -52,6 +52,7 @@ SIGNATURES = {
     "q8_kv_plan": (_INT, [_P, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P]),
     "q8_kv_append": (_INT, [_P, _I64, _P, _P, _P, _I64, _P]),
     "q8_tree_attention_workspace_bytes": (ctypes.c_size_t, [_P, _I64, _I64]),
+    "q8_tree_attention_needs_workspace": (_INT, [_P, _I64, _I64, _I64, _I64]),
     "q8_tree_attention": (_INT, [_P, _I64, _P, _I64, ctypes.c_float, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _P,
                                  _P, _P, ctypes.c_size_t, _P]),
     "q8_kv_accept": (_INT, [_P, _P, _I64, _P, _P, _I64, _P, _P, _I64, _P, _P]),
@@ -684,6 +685,10 @@ def q8_tree_attention_workspace_bytes(cache: KvCache, heads: int, max_fresh: int
     return int(lib().q8_tree_attention_workspace_bytes(cache.ref, heads, max_fresh))
 
 
+def q8_tree_attention_needs_workspace(cache: KvCache, heads: int, batch: int, max_fresh: int, max_len: int) -> bool:
+    return bool(lib().q8_tree_attention_needs_workspace(cache.ref, heads, batch, max_fresh, max_len))
+
+
 def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, qs=None, ds=None, masks=None,
                       max_fresh: int = 0, max_len: int = 0, scale: float | None = None, workspace=None, stream=None,
                       bind=False):
@@ -693,7 +698,7 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
     [tokens] of draft trees, or None for causal.  Writes ``y`` (f32, like q; None when dead) and, with ``qs``/``ds``,
     its q8_0 plane.  ``max_fresh`` (default tokens) and ``max_len`` (default the table's width) bound the lengths of a
     sequence.  ``scale`` defaults to 1/sqrt(head_dim).  ``workspace``: a uint8 CUDA tensor of at least
-    q8_tree_attention_workspace_bytes(...) bytes; when None one is allocated here with PyTorch."""
+    q8_tree_attention_workspace_bytes(...) bytes; when None, and the call needs one, it is allocated here with PyTorch."""
     import torch
 
     dev, dim, i32 = cache.dev, cache.head_dim, torch.int32
@@ -705,15 +710,19 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
     if ((y is not None and y.numel() < size) or (qs is not None and qs.numel() < size)
             or (ds is not None and ds.numel() < size // 32) or (masks is not None and masks.numel() < tokens)):
         raise ValueError("y, qs, ds or masks: fewer rows than q")
-    max_fresh = max_fresh or tokens
+    max_fresh, max_len = max_fresh or tokens, max_len or tshape[1] * cache.page_size
     if workspace is None:
-        key = cache.kv_heads, dim, heads, max_fresh
+        key = cache.kv_heads, dim, heads, batch, max_fresh, max_len
         nbytes = _workspace_sizes.get(key)
         if nbytes is None:
-            nbytes = q8_tree_attention_workspace_bytes(cache, heads, max_fresh)
+            nbytes = 0
+            if q8_tree_attention_needs_workspace(cache, heads, batch, max_fresh, max_len):
+                nbytes = q8_tree_attention_workspace_bytes(cache, heads, max_fresh)
             if len(_workspace_sizes) < 1024:
                 _workspace_sizes[key] = nbytes
-        if stream is None:
+        if nbytes == 0:
+            pass
+        elif stream is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.k.device)
         else:  # from the pool of the stream that uses it, so that it is not handed out again too early
             with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
@@ -722,10 +731,11 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
             _beside(table, i32, dev, "table"), tshape[1], _beside(cached, i32, dev, "cached"),
             _beside(starts, i32, dev, "starts"), batch,
             _beside(masks, torch.int64, dev, "masks") if masks is not None else None, tokens, max_fresh,
-            max_len or tshape[1] * cache.page_size, _beside(y, torch.float32, dev, "y") if y is not None else None,
+            max_len, _beside(y, torch.float32, dev, "y") if y is not None else None,
             _beside(qs, torch.int8, dev, "qs") if qs is not None else None,
-            _beside(ds, i32, dev, "ds") if ds is not None else None, _beside(workspace, torch.uint8, dev, "workspace"),
-            workspace.numel())
+            _beside(ds, i32, dev, "ds") if ds is not None else None,
+            _beside(workspace, torch.uint8, dev, "workspace") if workspace is not None else None,
+            workspace.numel() if workspace is not None else 0)
     return _kv_call("q8_tree_attention", args, dev, stream, bind, (cache, q, table, cached, starts, masks, y, qs, ds,
                                                                    workspace))
 

@@ -28,11 +28,12 @@
 // Measured (head_dim 128, 28 heads on 4): one decode over 262139 keys, f16,
 // 86.5 us (537 MB, 6.2 TB/s, 0.92 of a copy's rate); 61 ragged ones of up to
 // 8191 keys, int8, 75 us (326 MB, 4.4 TB/s).  Some 10 us of each call are the
-// launches, the line, the first copies' latency, and the join (one sequence of
-// 4097 keys takes 10.4 us).  int8 is bound by the warps' instructions, some 520
-// for 16 keys, of which the widening is a fifth: 16 warps instead of 12 with q
-// in shared memory came to 78 us, the next unit's copies before the join to
-// 75.6, two chains of score MMAs to 78.6; none was kept.
+// launches, the line, the first copies' latency, and the join.  int8 is bound
+// by the warps' instructions, some 520 for 16 keys, of which the widening is a
+// fifth: 16 warps instead of 12 with q in shared memory came to 78 us, the next
+// unit's copies before the join to 75.6, two chains of score MMAs to 78.6; none
+// was kept.
+#include <cooperative_groups.h>
 #include <cuda.h>
 
 #include "attn_common.cuh"
@@ -43,9 +44,12 @@ __device__ unsigned int g_rows_err;
 
 using q8::AttnArgs;
 using q8::Unit;
+namespace cg = cooperative_groups;
 
 // What a unit costs beside its tiles, in tiles (61 ragged int8 decodes of up to 8191 keys with 1: 86 us, 2: 79, 3: 74, 6: 76).
 constexpr int kHead = 3;
+constexpr int kClusterTiles = 8;     // of a CTA of a cluster, however many units there are: lengths may be ragged
+static_assert(kClusterTiles <= 64, "a CTA of a cluster keeps one chain");
 constexpr float kWeightBits = 6.0f;  // weights are 2^(s - m + 6)
 constexpr float kRaise = 8.0f;       // m may lag the maximum by this
 // The MMA's f32 accumulation truncates: with values of one sign O loses 1e-7 of
@@ -167,7 +171,8 @@ __device__ __forceinline__ void weights(RowState<D> &st, const float (&s)[4], co
     q8::split_f16(p[2], p[3], a[2], a[3]);
 }
 
-template <int D, bool kInt8, int RG>
+// kCluster: a unit is a cluster's, whose CTAs join in shared memory; else the CTAs share the line.
+template <int D, bool kInt8, int RG, bool kCluster>
 __global__ void __launch_bounds__(Ring<D, kInt8, RG>::kThreads, 1)
 attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                  const __grid_constant__ AttnArgs a)
@@ -192,22 +197,45 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     q8::fence_mbar_init();
     q8::griddep_launch_dependents();
     q8::griddep_wait();
-    bool bad_data = !q8::attn_line<kRows, kTile, kHead, kThreads>(a, pre);
-    const int total = pre[a.batch];
-    const int per = max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
     const int cta = blockIdx.x;
-    const int s0 = min(total, cta * per), s1 = min(total, s0 + per);
-    if (tid == 0) a.desc[2 * cta + 1].w = 0;  // no first piece yet
+    bool bad_data = false;
+    int s0 = 0, s1 = 1, per = 1, rank = 0;
+    Unit u;
+    if constexpr (kCluster) {  // one unit for this CTA's cluster
+        const int unit = cta / a.cluster;
+        rank = cta - unit * a.cluster;
+        u.b = unit / a.kv_heads, u.kvh = unit - u.b * a.kv_heads, u.rt = u.start = 0;
+        bad_data = !q8::attn_sequence(a, u.b, u.cached, u.fresh, u.first);
+        if (u.fresh == 0) s1 = 0;
+        else u.tiles = q8::attn_tiles_of<kRows, kTile>(a, u.cached, u.fresh, 0);
+    } else {
+        bad_data = !q8::attn_line<kRows, kTile, kHead, kThreads>(a, pre);
+        const int total = pre[a.batch];
+        per = max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+        s0 = min(total, cta * per), s1 = min(total, s0 + per);
+        if (tid == 0) a.desc[2 * cta + 1].w = 0;  // no first piece yet
+    }
 
     int slot = 0, phase = 0, wslot = 0;  // the ring: next to read (and its parity), next to fill
     bool dead = false;
-    Unit u;
+    float4 *const shared_o = reinterpret_cast<float4 *>(sm + kWarps * kRows * D * 4);  // a.cluster: this CTA's part of the unit
+    if (kCluster && s1 > 0 && rank * u.tiles / a.cluster == (rank + 1) * u.tiles / a.cluster)  // no tile falls to this CTA
+        for (int i = tid; i < kRows * D / 4; i += kThreads) {
+            shared_o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i < kRows) s_sum[i] = make_float2(-INFINITY, 0.0f);
+        }
     for (int pos = s0; pos < s1;) {
-        if (pos == s0) u = q8::attn_unit<kRows, kTile, kHead>(a, pre, pos);
-        else q8::attn_next_unit<kRows, kTile, kHead>(a, pre, u);
-        const int ta = max(0, pos - u.start - kHead), tb = max(0, min(u.tiles, s1 - u.start - kHead));
+        int ta, tb;
         const bool first = pos == s0;
-        pos = u.start + kHead + u.tiles;
+        if constexpr (kCluster) {
+            ta = rank * u.tiles / a.cluster, tb = (rank + 1) * u.tiles / a.cluster;
+            pos = s1;
+        } else {
+            if (first) u = q8::attn_unit<kRows, kTile, kHead>(a, pre, pos);
+            else q8::attn_next_unit<kRows, kTile, kHead>(a, pre, u);
+            ta = max(0, pos - u.start - kHead), tb = max(0, min(u.tiles, s1 - u.start - kHead));
+            pos = u.start + kHead + u.tiles;
+        }
         // (no tiles: only the unit's head, the next CTA has them)
         for (int t0 = ta; t0 < tb; t0 += kChain) {
             const int t1 = min(tb, t0 + kChain);
@@ -532,7 +560,10 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     l = f * l + g * ml.y;
                     m = mn;
                 }
-                if (!rows_out) {
+                if (kCluster && a.cluster > 1) {
+                    shared_o[i] = o;
+                    if (c == 0) s_sum[r] = make_float2(m, l);
+                } else if (!rows_out) {
                     *sum = o;
                     if (c == 0) {
                         s_next[r] = make_float2(m, l);
@@ -542,7 +573,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     q8::attn_store<D>(a, u, row0 + r, c, o, l, row0 + r < rows);
                 }
             }
-            if (partial && first && t1 == tb && tid == 0) {
+            if (!kCluster && partial && first && t1 == tb && tid == 0) {
                 a.desc[2 * cta] = make_int4(u.start, u.start + kHead + u.tiles, per, u.start + kHead);
                 a.desc[2 * cta + 1] = make_int4(u.b, u.kvh, u.rt, 1);
             }
@@ -556,6 +587,26 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         }
     }
     if (bad_data) atomicOr(&g_rows_err, q8::kKvErrData);
+    if (kCluster && a.cluster > 1 && s1 > 0) {
+        // join the CTAs, in the order of their tiles; a warp takes 32 columns' threads, so that a block of the plane is whole
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        for (int g = warp * a.cluster + rank; g < kRows * D / 128; g += kWarps * a.cluster) {
+            const int i = 32 * g + lane, r = i / (D / 4), c = (i % (D / 4)) * 4;
+            float m = -INFINITY, l = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int k = 0; k < a.cluster; ++k) m = fmaxf(m, cluster.map_shared_rank(s_sum, k)[r].x);
+            for (int k = 0; k < a.cluster; ++k) {
+                const float2 ml = cluster.map_shared_rank(s_sum, k)[r];
+                const float4 x = cluster.map_shared_rank(shared_o, k)[i];
+                const float f = ml.x == -INFINITY ? 0.0f : ml.x == m ? 1.0f : q8::exp2_approx(ml.x - m);
+                l += f * ml.y;
+                o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+            }
+            q8::attn_store<D>(a, u, r, c, o, l, r < u.fresh * a.group);
+        }
+        cluster.sync();  // every CTA keeps its shared memory until the others have read it
+    }
 }
 
 template <int D, bool kInt8, int RG>
@@ -563,9 +614,13 @@ int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a,
 {
     using R = Ring<D, kInt8, RG>;
     const int smem = R::smem(a.batch);
-    const void *fn = reinterpret_cast<const void *>(attn_rows_kernel<D, kInt8, RG>);
-    if (!q8::set_max_dynamic_smem(fn, kMaxDynamic, slot)) return Q8_ERR_LAUNCH;
-    const int st = q8::launch_pdl(attn_rows_kernel<D, kInt8, RG>, dim3(q8::kAttnCtas), dim3(R::kThreads), smem, s, mk, mv, a);
+    const void *fn = a.cluster ? reinterpret_cast<const void *>(attn_rows_kernel<D, kInt8, RG, true>)
+                               : reinterpret_cast<const void *>(attn_rows_kernel<D, kInt8, RG, false>);
+    if (!q8::set_max_dynamic_smem(fn, kMaxDynamic, slot + (a.cluster ? 12 : 0))) return Q8_ERR_LAUNCH;
+    if (a.cluster)
+        return q8::launch_pdl_cluster(attn_rows_kernel<D, kInt8, RG, true>, dim3(a.batch * a.kv_heads * a.cluster), dim3(R::kThreads),
+                                      R::smem(0), s, a.cluster, mk, mv, a);
+    const int st = q8::launch_pdl(attn_rows_kernel<D, kInt8, RG, false>, dim3(q8::kAttnCtas), dim3(R::kThreads), smem, s, mk, mv, a);
     if (st != Q8_OK) return st;
     return q8::launch_pdl(q8::attn_combine_kernel<D, 8 * RG>, dim3(q8::kAttnCtas - 1, 4 * RG), dim3(256), 0, s,
                           a);
@@ -574,6 +629,24 @@ int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a,
 } // namespace
 
 namespace q8 {
+
+// The CTAs of a unit that join in shared memory, or 0 for the line.  A cluster has no line to add up, no workspace and no
+// second launch, but a unit gets eight CTAs at most, and those of a short unit are idle.  In tiles: a CTA's own
+// and its start, against a stretch of the line with its start and the join, some three tiles more.  Measured in a graph, 28
+// heads on 4 of 128 f16 values, lengths ragged up to the one given, line / clusters: 1 sequence of 380 keys 10.3 / 8.5 us (8
+// CTAs), 4097 10.4 / 10.3, 12000 11.7 / 14.4; 5 sequences of 1500 11.8 / 9.4 (4 CTAs); 9 of 6000 20.3 / 17.8 (4); 38 of 380
+// 16.8 / 8.3 (1), of 1500 23.4 / 17.7 (1).
+int attn_rows_cluster(int rows, int64_t units, int64_t max_len)
+{
+    const int64_t tile = rows == 8 ? Ring<128, false, 1>::kTile : Ring<128, false, 2>::kTile, tiles = (max_len + tile - 1) / tile;
+    if (units > kAttnCtas) return 0;
+    // The GPU has room for 15 clusters of 8, 36 of 4, 76 of 2 at once (units of 1500 keys: 15 of 8 8.2 us, 16 14.9; 36 of 4
+    // 8.9, 37 14.4): a little less is used, since GPUs differ in which SMs they have.
+    int c = units <= 14 ? 8 : units <= 34 ? 4 : units <= 74 ? 2 : 1;
+    while (c > 1 && c >= 2 * tiles) c /= 2;
+    const int64_t mine = (tiles + c - 1) / c;
+    return mine <= kClusterTiles && mine <= units * (tiles + kHead) / kAttnCtas + 3 ? c : 0;
+}
 
 int attn_rows_launch(const AttnCall &c, int rows, cudaStream_t s)
 {

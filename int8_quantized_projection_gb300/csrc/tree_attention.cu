@@ -27,6 +27,12 @@ Workspace workspace(int rows, int d)
 // 30 / 31 us with 16 rows a unit, 30 / 48 with 128.
 int rows_of(int64_t max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 128; }
 
+// CTAs of a unit that join without the workspace, or 0.
+int cluster_of(int rows, const q8_kv_cache *c, int64_t batch, int64_t max_len)
+{
+    return rows == 128 ? 0 : q8::attn_rows_cluster(rows, batch * c->kv_heads, max_len);
+}
+
 } // namespace
 
 static bool attn_shape_ok(const q8_kv_cache *c, int64_t heads, int64_t max_fresh)
@@ -39,6 +45,15 @@ extern "C" size_t q8_tree_attention_workspace_bytes(const q8_kv_cache *cache, in
 {
     if (q8::kv_cache_status(cache) == Q8_ERR_ARG || !attn_shape_ok(cache, heads, max_fresh)) return 0;
     return workspace(rows_of(max_fresh * (heads / cache->kv_heads)), cache->head_dim).bytes;
+}
+
+extern "C" int q8_tree_attention_needs_workspace(const q8_kv_cache *cache, int64_t heads, int64_t batch, int64_t max_fresh,
+                                                 int64_t max_len)
+{
+    if (q8::kv_cache_status(cache) == Q8_ERR_ARG || !attn_shape_ok(cache, heads, max_fresh) || batch < 1 ||
+        batch > Q8_KV_MAX_BATCH || max_len < 1)
+        return 1;
+    return cluster_of(rows_of(max_fresh * (heads / cache->kv_heads)), cache, batch, max_len) == 0;
 }
 
 extern "C" int q8_tree_attention(const q8_kv_cache *cache, int64_t layer, const float *q, int64_t heads, float scale,
@@ -63,7 +78,8 @@ extern "C" int q8_tree_attention(const q8_kv_cache *cache, int64_t layer, const 
                         ((max_len + 127) / 128 + 8);
     if (line > 2.0e9) return Q8_ERR_ARG;
     const Workspace w = workspace(rows, cache->head_dim);
-    if (!workspace_ || workspace_bytes < w.bytes) return Q8_ERR_ARG;
+    const int cluster = cluster_of(rows, cache, batch, max_len);
+    if (!cluster && (!workspace_ || workspace_bytes < w.bytes)) return Q8_ERR_ARG;
     if (cst != Q8_OK) return cst;
     const void *all[] = {q, table, cached, starts, masks, y, qs, ds, workspace_};
     for (const void *p : all)
@@ -83,7 +99,7 @@ extern "C" int q8_tree_attention(const q8_kv_cache *cache, int64_t layer, const 
            reinterpret_cast<float2 *>(ws + w.ml), reinterpret_cast<int4 *>(ws + w.desc), tokens,
            static_cast<int>(batch), static_cast<int>(heads), cache->kv_heads, group, static_cast<int>(max_pages),
            cache->page_size, static_cast<int>(cache->n_pages), static_cast<int>(max_fresh),
-           static_cast<int>(max_len), q8::kv_inverse(group), scale * 1.4426950408889634f};
+           static_cast<int>(max_len), q8::kv_inverse(group), cluster, scale * 1.4426950408889634f};
     c.k = kp, c.v = vp, c.layer_rows = lr, c.dim = D, c.int8 = i8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return rows == 128 ? q8::attn_tiles_launch(c, s) : q8::attn_rows_launch(c, rows, s);

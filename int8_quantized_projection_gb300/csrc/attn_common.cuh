@@ -38,7 +38,7 @@ struct AttnArgs {
     long long tokens;
     int batch, heads, kv_heads, group, max_pages, page, n_pages, max_fresh, max_len;
     unsigned group_inv;    // kv_inverse(group)
-    int cluster;           // CTAs of a unit that join in shared memory (attn_rows.cu), or 0: the line
+    int cluster;           // CTAs of a unit, which join in shared memory, or 0: the line
     float scale;           // softmax scale * log2(e)
 };
 
@@ -301,6 +301,7 @@ struct AttnCall {
 // rows of a unit: 8 or 16 (attn_rows.cu), 128 (attn_tiles.cu)
 int attn_rows_launch(const AttnCall &c, int rows, cudaStream_t s);
 int attn_rows_cluster(int rows, int64_t units, int64_t max_len);  // AttnArgs::cluster
+int attn_tiles_cluster(int64_t units, int64_t max_len);
 int attn_rows_take_error(cudaStream_t s);
 int attn_tiles_launch(const AttnCall &c, cudaStream_t s);
 int attn_tiles_take_error(cudaStream_t s);

@@ -62,6 +62,7 @@ __device__ unsigned int g_tiles_err;
 constexpr int kRows = 128, kTile = 128;
 // What a unit costs beside its tiles, in tiles (12000 cycles of 2750; the prompt of 3325 tokens with 3: 162 us, 4: 145, 5: 141).
 constexpr int kHead = 5;
+constexpr int kWholeTiles = 16;  // of a unit that one CTA does, however many there are: lengths may be ragged
 constexpr float kWeightBits = 6.0f;  // weights are 2^(s - m + 6): below 2^14 while m may lag by 2^8
 constexpr float kRaise = 8.0f;
 constexpr int kScaleSlots = 4;
@@ -293,7 +294,8 @@ __device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.
 template <uint32_t N>
 __device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// One CTA's stretch of the line, piece by piece; every role walks it alike.
+// One CTA's stretch of the line, piece by piece; every role walks it alike.  kWhole: its one unit, whole.
+template <bool kWhole>
 struct Walk {
     int pos, begin, end;  // next place; the stretch
     Unit u;               // before the first piece: the unit at `begin`
@@ -302,6 +304,14 @@ struct Walk {
 
     __device__ __forceinline__ bool next(const AttnArgs &a, const int *pre)
     {
+        if constexpr (kWhole) {
+            if (pos == end) return false;
+            pos = end;
+            first = true;
+            t0 = 0, n = u.tiles;
+            kend = q8::attn_visible(a, u.cached, u.fresh, min((u.rt + 1) * kRows, u.fresh * a.group));
+            return true;
+        }
         while (pos < end) {
             first = pos == begin;
             if (!first) q8::attn_next_unit<kRows, kTile, kHead>(a, pre, u);
@@ -340,7 +350,7 @@ __device__ __forceinline__ void encode_quad(const AttnArgs &a, long long at, con
     if (valid && c2 == 0) a.ds[at / 32] = q8::q8_dsword(d, sum);
 }
 
-template <int D, bool kInt8>
+template <int D, bool kInt8, bool kWhole>
 __global__ void __launch_bounds__(Lay<D, kInt8>::kThreads, 1)
 attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                   const __grid_constant__ AttnArgs a, const int box)
@@ -384,19 +394,32 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     }
     q8::griddep_launch_dependents();
     q8::griddep_wait();
-    bool bad_data = !q8::attn_line<kRows, kTile, kHead, L::kThreads>(a, pre);
+    const int cta = blockIdx.x;
+    bool bad_data = false;
+    int per = 1;
+    Walk<kWhole> w;
+    if constexpr (kWhole) {
+        const int rts = (a.max_fresh * a.group + kRows - 1) / kRows, x = cta / rts;
+        w.u.rt = cta - x * rts, w.u.b = x / a.kv_heads, w.u.kvh = x - w.u.b * a.kv_heads, w.u.start = 0;
+        bad_data = !q8::attn_sequence(a, w.u.b, w.u.cached, w.u.fresh, w.u.first);
+        w.pos = w.begin = 0;
+        w.end = w.u.rt * kRows < w.u.fresh * a.group;
+        w.u.tiles = w.end ? q8::attn_tiles_of<kRows, kTile>(a, w.u.cached, w.u.fresh, w.u.rt) : 0;
+    } else {
+        bad_data = !q8::attn_line<kRows, kTile, kHead, L::kThreads>(a, pre);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int total = pre[a.batch];
-    const int per = max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
-    const int cta = blockIdx.x;
-    const int s0 = min(total, cta * per);
-    Walk w;
-    w.pos = w.begin = s0;
-    w.end = min(total, s0 + per);
-    if (w.pos < w.end) w.u = q8::attn_unit<kRows, kTile, kHead>(a, pre, w.pos);
+    if constexpr (!kWhole) {
+        const int total = pre[a.batch];
+        per = max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+        const int s0 = min(total, cta * per);
+        w.pos = w.begin = s0;
+        w.end = min(total, s0 + per);
+        if (w.pos < w.end) w.u = q8::attn_unit<kRows, kTile, kHead>(a, pre, w.pos);
+    }
 
     if (warp < 4) {
         setmaxnreg_dec<L::kRegsCtl>();
@@ -542,7 +565,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32 + 16 * (sw >> 2)) << 16);
         int T = 0;
         uint32_t piece = 0;
-        if (tid == 128) a.desc[2 * cta + 1].w = 0;  // no first piece yet
+        if (!kWhole && tid == 128) a.desc[2 * cta + 1].w = 0;  // no first piece yet
         // Q: a warp per row (D = 128) or two rows (D = 64), eight warps, four loads at a time in a loop (straight-line
         // code that runs once costs more than its loads' latency); the rows are brought to L2 beforehand.
         constexpr int kPer = D == 128 ? 1 : 2, kLanes = 32 / kPer, kLoads = 16 / kPer;
@@ -611,7 +634,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             const int rows = u.fresh * a.group, row0 = u.rt * kRows, pslot = 2 * cta + (w.first ? 0 : 1);
             const int all_see = u.cached + (a.masks ? 0 : q8::attn_token(a, row0) + 1);  // keys below are seen by every row
             const q8::RowSight sight0 = q8::attn_sight(a, u, row0 + r0), sight1 = q8::attn_sight(a, u, row0 + r0 + 8);
-            const bool partial = w.t0 > 0 || w.n < u.tiles;
+            const bool partial = !kWhole && (w.t0 > 0 || w.n < u.tiles);
             float qq[2], m[2], l[2], ii[2], msum[2];
             int e[2];
 #pragma unroll
@@ -621,8 +644,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             }
             bool ok = true;
             {  // (the walk's next state is not kept: the tiles need the registers)
-                Walk ahead = w;
-                if (ahead.next(a, pre)) prefetch_q(ahead.u);
+                Walk<kWhole> ahead = w;
+                if (!kWhole && ahead.next(a, pre)) prefetch_q(ahead.u);
             }
             for (int i = 0; ok && i < w.n; ++i) {
                 const int t = T + i, key0 = (w.t0 + i) * kTile;
@@ -900,8 +923,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     if (kInt8) arrive(bar(L::bCe + t % kScaleSlots));
                 }
             }
-            Walk nx = w;
-            more = nx.next(a, pre);
+            Walk<kWhole> nx = w;
+            more = !kWhole && nx.next(a, pre);
             if (more && ok) write_q(nx.u, s_row + 128 * ((piece & 1) ^ 1));  // every score of this unit is computed
             ok = ok && products_done(T + w.n - 1);
             tc_fence_after();
@@ -1076,9 +1099,14 @@ template <int D, bool kInt8>
 int launch_tiles(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a, int box, int slot, cudaStream_t s)
 {
     using L = Lay<D, kInt8>;
-    if (!q8::set_max_dynamic_smem(reinterpret_cast<const void *>(attn_tiles_kernel<D, kInt8>), 227 * 1024, slot))
-        return Q8_ERR_LAUNCH;
-    const int st = q8::launch_pdl(attn_tiles_kernel<D, kInt8>, dim3(q8::kAttnCtas), dim3(L::kThreads), L::smem(a.batch), s, mk,
+    const void *fn = a.cluster ? reinterpret_cast<const void *>(attn_tiles_kernel<D, kInt8, true>)
+                               : reinterpret_cast<const void *>(attn_tiles_kernel<D, kInt8, false>);
+    if (!q8::set_max_dynamic_smem(fn, 227 * 1024, slot + (a.cluster ? 12 : 0))) return Q8_ERR_LAUNCH;
+    if (a.cluster) {
+        const unsigned units = static_cast<unsigned>(a.batch) * a.kv_heads * ((a.max_fresh * a.group + kRows - 1) / kRows);
+        return q8::launch_pdl(attn_tiles_kernel<D, kInt8, true>, dim3(units), dim3(L::kThreads), L::smem(0), s, mk, mv, a, box);
+    }
+    const int st = q8::launch_pdl(attn_tiles_kernel<D, kInt8, false>, dim3(q8::kAttnCtas), dim3(L::kThreads), L::smem(a.batch), s, mk,
                                   mv, a, box);
     if (st != Q8_OK) return st;
     return q8::launch_pdl(q8::attn_combine_kernel<D, kRows>, dim3(q8::kAttnCtas - 1, 8), dim3(256), 0, s, a);
@@ -1087,6 +1115,16 @@ int launch_tiles(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a
 } // namespace
 
 namespace q8 {
+
+// 1: a CTA per unit, which it does whole, without line, workspace and second launch; 0: the line.  In tiles: a CTA's own,
+// against its stretch of the line and the join, some six tiles more.  Measured in a graph, 28 heads on 4 of 128 f16 values,
+// trees of up to 16 nodes, line / whole: 1 sequence of 380 keys 15.6 / 13.6 us, 1000 15.1 / 17.9; 9 of 1000 18.6 / 18.3; 38 of
+// 380 23.4 / 14.7, of 1000 31.9 / 21.8; a prompt of 520 tokens 21.2 / 14.4.
+int attn_tiles_cluster(int64_t units, int64_t max_len)
+{
+    const int64_t tiles = (max_len + kTile - 1) / kTile;
+    return units <= kAttnCtas && tiles <= kWholeTiles && tiles <= units * (tiles + kHead) / kAttnCtas + 6 ? 1 : 0;
+}
 
 int attn_tiles_launch(const AttnCall &c, cudaStream_t s)
 {

@@ -28,9 +28,11 @@ Workspace workspace(int rows, int d)
 int rows_of(int64_t max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 128; }
 
 // CTAs of a unit that join without the workspace, or 0.
-int cluster_of(int rows, const q8_kv_cache *c, int64_t batch, int64_t max_len)
+int cluster_of(int64_t max_rows, const q8_kv_cache *c, int64_t batch, int64_t max_len)
 {
-    return rows == 128 ? 0 : q8::attn_rows_cluster(rows, batch * c->kv_heads, max_len);
+    const int rows = rows_of(max_rows);
+    const int64_t units = batch * c->kv_heads * ((max_rows + rows - 1) / rows);
+    return rows == 128 ? q8::attn_tiles_cluster(units, max_len) : q8::attn_rows_cluster(rows, units, max_len);
 }
 
 } // namespace
@@ -53,7 +55,7 @@ extern "C" int q8_tree_attention_needs_workspace(const q8_kv_cache *cache, int64
     if (q8::kv_cache_status(cache) == Q8_ERR_ARG || !attn_shape_ok(cache, heads, max_fresh) || batch < 1 ||
         batch > Q8_KV_MAX_BATCH || max_len < 1)
         return 1;
-    return cluster_of(rows_of(max_fresh * (heads / cache->kv_heads)), cache, batch, max_len) == 0;
+    return cluster_of(max_fresh * (heads / cache->kv_heads), cache, batch, max_len) == 0;
 }
 
 extern "C" int q8_tree_attention(const q8_kv_cache *cache, int64_t layer, const float *q, int64_t heads, float scale,
@@ -78,7 +80,7 @@ extern "C" int q8_tree_attention(const q8_kv_cache *cache, int64_t layer, const 
                         ((max_len + 127) / 128 + 8);
     if (line > 2.0e9) return Q8_ERR_ARG;
     const Workspace w = workspace(rows, cache->head_dim);
-    const int cluster = cluster_of(rows, cache, batch, max_len);
+    const int cluster = cluster_of(max_fresh * group, cache, batch, max_len);
     if (!cluster && (!workspace_ || workspace_bytes < w.bytes)) return Q8_ERR_ARG;
     if (cst != Q8_OK) return cst;
     const void *all[] = {q, table, cached, starts, masks, y, qs, ds, workspace_};

@@ -9,6 +9,7 @@ from int8_quantized_projection_gb300 import _binding, build
 FAKE, MISALIGNED = 0x10000, 0x10004  # never dereferenced: every call below fails validation first
 P = ctypes.c_void_p
 ERR_ARG, ERR_ALIGN = 1, 2
+LONG = 1 << 20  # contexts whose attention needs a workspace
 
 
 @pytest.fixture(scope="module")
@@ -75,11 +76,12 @@ def test_attention_arguments(lib):
     for kw in (dict(q=0), dict(table=0), dict(cached=0), dict(starts=0), dict(y=0), dict(y=0, qs=FAKE), dict(y=0, ds=FAKE),
                dict(qs=FAKE), dict(layer=2), dict(layer=-1), dict(heads=0), dict(heads=30), dict(heads=4 * 65), dict(batch=0),
                dict(batch=4097), dict(tokens=0), dict(max_fresh=0), dict(max_fresh=7), dict(max_len=2), dict(max_len=1 << 31),
-               dict(max_pages=0), dict(masks=FAKE, tokens=99, max_fresh=65), dict(ws=0), dict(nbytes=0),
+               dict(max_pages=0), dict(masks=FAKE, tokens=99, max_fresh=65), dict(ws=0, max_len=LONG),
+               dict(nbytes=0, max_len=LONG),
                dict(batch=4096, tokens=1 << 23, max_fresh=1 << 23, max_len=1 << 30)):
         assert attend(lib, desc(), **kw) == ERR_ARG, kw
     need = lib.q8_tree_attention_workspace_bytes(ref(desc()), 28, 3)
-    assert need > 0 and attend(lib, desc(), nbytes=need - 1) == ERR_ARG
+    assert need > 0 and attend(lib, desc(), nbytes=need - 1, max_len=LONG) == ERR_ARG
     for name in ("q", "table", "cached", "starts", "masks", "y", "ws"):
         assert attend(lib, desc(), **{name: MISALIGNED}) == ERR_ALIGN, name
     assert attend(lib, desc(), qs=MISALIGNED, ds=FAKE) == ERR_ALIGN
@@ -93,6 +95,16 @@ def test_attention_workspace(lib):
     # two pieces a CTA of 8 rows: numerators, (m, l) and descriptors
     assert size(28, 1) == 2 * 152 * 8 * 128 * 4 + 2 * 152 * 8 * 8 + 2 * 152 * 16
     assert size(28, 1, dim=64) < size(28, 1)
+
+
+def test_attention_needs_a_workspace(lib):
+    needs = lambda heads, batch, fresh, most, **kw: lib.q8_tree_attention_needs_workspace(  # noqa: E731
+        ref(desc(**kw)), heads, batch, fresh, most)
+    for heads, fresh in ((28, 1), (28, 2), (28, 16)):  # 8, 16 and 128 rows a unit
+        assert needs(heads, 2, fresh, 300) == 0 and needs(heads, 2, fresh, LONG) == 1
+        assert needs(heads, 38, fresh, 300) == 0 and needs(heads, 39, fresh, 300) == 1  # more units than CTAs
+    assert needs(28, 1, 1, 4098) == 0 and needs(28, 1, 3325, 3325) == 1
+    assert needs(30, 2, 1, 300) == 1 and needs(28, 0, 1, 300) == 1 and needs(28, 2, 0, 300) == 1  # nothing a call would take
 
 
 def test_accept_arguments(lib):

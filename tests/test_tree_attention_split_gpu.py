@@ -1,5 +1,5 @@
-"""Both ways of sharing few rows among CTAs, a cluster per unit and the line of all units, on the same inputs: the host's
-bound on the lengths chooses (a large one the line)."""
+"""Both ways of sharing the units among CTAs, a cluster (128 rows: a CTA) per unit and the line of all units, on the same
+inputs: the host's bound on the lengths chooses (a large one the line)."""
 import numpy as np
 import pytest
 
@@ -48,6 +48,27 @@ def test_small_trees_and_chains(q8, int8, heads, fresh):
     both(c, m)
 
 
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("d,heads,kv_heads,cached,fresh", [
+    (128, 28, 4, [380], [16]), (128, 28, 4, [100, 0, 128], [3, 5, 0]), (64, 8, 2, [700, 0], [33, 64]), (64, 64, 1, [5], [1])])
+def test_units_of_128_rows(q8, int8, d, heads, kv_heads, cached, fresh):
+    c = ref.Case(107, cached, fresh, heads, kv_heads, d, 16, int8)
+    assert clusters(q8, c, max(a + b for a, b in zip(cached, fresh)))
+    both(c)
+    m = trees(c)
+    both(c, m)
+    m[0] = 0
+    both(c, m)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("cached,fresh", [([0], [300]), ([130, 0], [70, 129])])
+def test_prompts(q8, int8, cached, fresh):
+    c = ref.Case(108, cached, fresh, 14, 2, 128, 32, int8)
+    assert clusters(q8, c, 300)
+    both(c)
+
+
 @pytest.mark.parametrize("batch", [1, 14, 15, 34, 35, 74, 75, 152, 153])
 def test_any_number_of_units(q8, batch):
     """8, 4, 2 and 1 CTAs a unit, and the line."""
@@ -79,7 +100,7 @@ def test_plane_and_rows_that_see_nothing(q8, int8):
     q8.q8_check()
 
 
-@pytest.mark.parametrize("heads,fresh", [(4, 2), (2, 8)])
+@pytest.mark.parametrize("heads,fresh", [(4, 2), (2, 8), (16, 9)])
 @pytest.mark.parametrize("bad", [np.nan, np.inf])
 def test_what_a_row_cannot_see_does_not_reach_it(q8, heads, fresh, bad):
     """Non-finite values in a node that others do not see, in either form."""

@@ -15,8 +15,9 @@
 // that crosses a boundary leaves one partial (m, l, O) per piece in the
 // workspace (a CTA has two at most: its first and its last) and
 // attn_combine_kernel joins them in the order of the line.
-// Few units over short contexts take another form: a cluster of 1 to 8 CTAs
-// per unit, joined in shared memory (attn_rows.cu).
+// Units over short contexts take another form: a cluster of 1 to 8 CTAs per
+// unit, joined in shared memory (attn_rows_cluster), or a CTA
+// (attn_tiles_cluster).
 #pragma once
 
 #include "kv_common.cuh"

@@ -171,7 +171,8 @@ __device__ __forceinline__ void weights(RowState<D> &st, const float (&s)[4], co
     q8::split_f16(p[2], p[3], a[2], a[3]);
 }
 
-// kCluster: a unit is a cluster's, whose CTAs join in shared memory; else the CTAs share the line.
+// kCluster: a unit is a cluster's, whose CTAs join in shared memory (clusters of one CTA take units in turn); else the CTAs
+// share the line.
 template <int D, bool kInt8, int RG, bool kCluster>
 __global__ void __launch_bounds__(Ring<D, kInt8, RG>::kThreads, 1)
 attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -201,13 +202,11 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     bool bad_data = false;
     int s0 = 0, s1 = 1, per = 1, rank = 0;
     Unit u;
-    if constexpr (kCluster) {  // one unit for this CTA's cluster
-        const int unit = cta / a.cluster;
-        rank = cta - unit * a.cluster;
-        u.b = unit / a.kv_heads, u.kvh = unit - u.b * a.kv_heads, u.rt = u.start = 0;
-        bad_data = !q8::attn_sequence(a, u.b, u.cached, u.fresh, u.first);
-        if (u.fresh == 0) s1 = 0;
-        else u.tiles = q8::attn_tiles_of<kRows, kTile>(a, u.cached, u.fresh, 0);
+    const int step = kCluster ? static_cast<int>(gridDim.x) / a.cluster : 0;  // clusters: units that far apart are one's
+    if constexpr (kCluster) {
+        s0 = cta / a.cluster, s1 = a.batch * a.kv_heads;
+        rank = cta - s0 * a.cluster;
+        u.fresh = 0;
     } else {
         bad_data = !q8::attn_line<kRows, kTile, kHead, kThreads>(a, pre);
         const int total = pre[a.batch];
@@ -219,17 +218,21 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     int slot = 0, phase = 0, wslot = 0;  // the ring: next to read (and its parity), next to fill
     bool dead = false;
     float4 *const shared_o = reinterpret_cast<float4 *>(sm + kWarps * kRows * D * 4);  // a.cluster: this CTA's part of the unit
-    if (kCluster && s1 > 0 && rank * u.tiles / a.cluster == (rank + 1) * u.tiles / a.cluster)  // no tile falls to this CTA
-        for (int i = tid; i < kRows * D / 4; i += kThreads) {
-            shared_o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (i < kRows) s_sum[i] = make_float2(-INFINITY, 0.0f);
-        }
     for (int pos = s0; pos < s1;) {
         int ta, tb;
         const bool first = pos == s0;
         if constexpr (kCluster) {
+            u.b = pos / a.kv_heads, u.kvh = pos - u.b * a.kv_heads, u.rt = u.start = 0;
+            pos += step;
+            bad_data |= !q8::attn_sequence(a, u.b, u.cached, u.fresh, u.first);
+            if (u.fresh == 0) continue;
+            u.tiles = q8::attn_tiles_of<kRows, kTile>(a, u.cached, u.fresh, 0);
             ta = rank * u.tiles / a.cluster, tb = (rank + 1) * u.tiles / a.cluster;
-            pos = s1;
+            if (ta == tb)  // no tile falls to this CTA
+                for (int i = tid; i < kRows * D / 4; i += kThreads) {
+                    shared_o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i < kRows) s_sum[i] = make_float2(-INFINITY, 0.0f);
+                }
         } else {
             if (first) u = q8::attn_unit<kRows, kTile, kHead>(a, pre, pos);
             else q8::attn_next_unit<kRows, kTile, kHead>(a, pre, u);
@@ -587,8 +590,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         }
     }
     if (bad_data) atomicOr(&g_rows_err, q8::kKvErrData);
-    if (kCluster && a.cluster > 1 && s1 > 0) {
-        // join the CTAs, in the order of their tiles; a warp takes 32 columns' threads, so that a block of the plane is whole
+    if (kCluster && a.cluster > 1 && u.fresh > 0) {
+        // join the CTAs of the one unit, in the order of their tiles; a warp takes 32 columns' threads, so that a block of the plane is whole
         cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();
         for (int g = warp * a.cluster + rank; g < kRows * D / 128; g += kWarps * a.cluster) {
@@ -617,8 +620,10 @@ int launch_rows(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a,
     const void *fn = a.cluster ? reinterpret_cast<const void *>(attn_rows_kernel<D, kInt8, RG, true>)
                                : reinterpret_cast<const void *>(attn_rows_kernel<D, kInt8, RG, false>);
     if (!q8::set_max_dynamic_smem(fn, kMaxDynamic, slot + (a.cluster ? 12 : 0))) return Q8_ERR_LAUNCH;
+    const int units = a.batch * a.kv_heads;
     if (a.cluster)
-        return q8::launch_pdl_cluster(attn_rows_kernel<D, kInt8, RG, true>, dim3(a.batch * a.kv_heads * a.cluster), dim3(R::kThreads),
+        return q8::launch_pdl_cluster(attn_rows_kernel<D, kInt8, RG, true>,
+                                      dim3(min(units, q8::kAttnCtas / a.cluster) * a.cluster), dim3(R::kThreads),
                                       R::smem(0), s, a.cluster, mk, mv, a);
     const int st = q8::launch_pdl(attn_rows_kernel<D, kInt8, RG, false>, dim3(q8::kAttnCtas), dim3(R::kThreads), smem, s, mk, mv, a);
     if (st != Q8_OK) return st;
@@ -635,17 +640,18 @@ namespace q8 {
 // and its start, against a stretch of the line with its start and the join, some three tiles more.  Measured in a graph, 28
 // heads on 4 of 128 f16 values, lengths ragged up to the one given, line / clusters: 1 sequence of 380 keys 10.3 / 8.5 us (8
 // CTAs), 4097 10.4 / 10.3, 12000 11.7 / 14.4; 5 sequences of 1500 11.8 / 9.4 (4 CTAs); 9 of 6000 20.3 / 17.8 (4); 38 of 380
-// 16.8 / 8.3 (1), of 1500 23.4 / 17.7 (1).
+// 16.8 / 8.3 (1), of 1500 23.4 / 17.7 (1); 61, whose 244 units are dealt out to 152 CTAs, of 380 18.4 / 15.1, of 1500 31.7 /
+// 29.5.
 int attn_rows_cluster(int rows, int64_t units, int64_t max_len)
 {
     const int64_t tile = rows == 8 ? Ring<128, false, 1>::kTile : Ring<128, false, 2>::kTile, tiles = (max_len + tile - 1) / tile;
-    if (units > kAttnCtas) return 0;
     // The GPU has room for 15 clusters of 8, 36 of 4, 76 of 2 at once (units of 1500 keys: 15 of 8 8.2 us, 16 14.9; 36 of 4
     // 8.9, 37 14.4): a little less is used, since GPUs differ in which SMs they have.
     int c = units <= 14 ? 8 : units <= 34 ? 4 : units <= 74 ? 2 : 1;
     while (c > 1 && c >= 2 * tiles) c /= 2;
-    const int64_t mine = (tiles + c - 1) / c;
-    return mine <= kClusterTiles && mine <= units * (tiles + kHead) / kAttnCtas + 3 ? c : 0;
+    // more units than CTAs: each CTA takes every kAttnCtas-th
+    const int64_t mine = (tiles + c - 1) / c, turns = (units * c + kAttnCtas - 1) / kAttnCtas;
+    return mine <= kClusterTiles && turns * (mine + kHead) <= units * (tiles + kHead) / kAttnCtas + kHead + 3 ? c : 0;
 }
 
 int attn_rows_launch(const AttnCall &c, int rows, cudaStream_t s)

@@ -294,7 +294,7 @@ __device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.
 template <uint32_t N>
 __device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// One CTA's stretch of the line, piece by piece; every role walks it alike.  kWhole: its one unit, whole.
+// One CTA's stretch of the line, piece by piece; every role walks it alike.  kWhole: units gridDim.x apart, whole.
 template <bool kWhole>
 struct Walk {
     int pos, begin, end;  // next place; the stretch
@@ -305,12 +305,20 @@ struct Walk {
     __device__ __forceinline__ bool next(const AttnArgs &a, const int *pre)
     {
         if constexpr (kWhole) {
-            if (pos == end) return false;
-            pos = end;
-            first = true;
-            t0 = 0, n = u.tiles;
-            kend = q8::attn_visible(a, u.cached, u.fresh, min((u.rt + 1) * kRows, u.fresh * a.group));
-            return true;
+            const int rts = (a.max_fresh * a.group + kRows - 1) / kRows;
+            while (pos < end) {
+                const int x = pos / rts;
+                u.rt = pos - x * rts, u.b = x / a.kv_heads, u.kvh = x - u.b * a.kv_heads;
+                pos += gridDim.x;
+                q8::attn_sequence(a, u.b, u.cached, u.fresh, u.first);
+                if (u.rt * kRows >= u.fresh * a.group) continue;
+                u.tiles = q8::attn_tiles_of<kRows, kTile>(a, u.cached, u.fresh, u.rt);
+                first = true;
+                t0 = 0, n = u.tiles;
+                kend = q8::attn_visible(a, u.cached, u.fresh, min((u.rt + 1) * kRows, u.fresh * a.group));
+                return true;
+            }
+            return false;
         }
         while (pos < end) {
             first = pos == begin;
@@ -399,12 +407,14 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     int per = 1;
     Walk<kWhole> w;
     if constexpr (kWhole) {
-        const int rts = (a.max_fresh * a.group + kRows - 1) / kRows, x = cta / rts;
-        w.u.rt = cta - x * rts, w.u.b = x / a.kv_heads, w.u.kvh = x - w.u.b * a.kv_heads, w.u.start = 0;
-        bad_data = !q8::attn_sequence(a, w.u.b, w.u.cached, w.u.fresh, w.u.first);
-        w.pos = w.begin = 0;
-        w.end = w.u.rt * kRows < w.u.fresh * a.group;
-        w.u.tiles = w.end ? q8::attn_tiles_of<kRows, kTile>(a, w.u.cached, w.u.fresh, w.u.rt) : 0;
+        w.pos = w.begin = cta;
+        w.end = a.batch * a.kv_heads * ((a.max_fresh * a.group + kRows - 1) / kRows);
+        w.u.start = 0;
+        if (cta == 0)
+            for (int b = tid; b < a.batch; b += L::kThreads) {
+                int x, y, z;
+                bad_data |= !q8::attn_sequence(a, b, x, y, z);
+            }
     } else {
         bad_data = !q8::attn_line<kRows, kTile, kHead, L::kThreads>(a, pre);
     }
@@ -645,7 +655,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             bool ok = true;
             {  // (the walk's next state is not kept: the tiles need the registers)
                 Walk<kWhole> ahead = w;
-                if (!kWhole && ahead.next(a, pre)) prefetch_q(ahead.u);
+                if (ahead.next(a, pre)) prefetch_q(ahead.u);
             }
             for (int i = 0; ok && i < w.n; ++i) {
                 const int t = T + i, key0 = (w.t0 + i) * kTile;
@@ -924,7 +934,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 }
             }
             Walk<kWhole> nx = w;
-            more = !kWhole && nx.next(a, pre);
+            more = nx.next(a, pre);
             if (more && ok) write_q(nx.u, s_row + 128 * ((piece & 1) ^ 1));  // every score of this unit is computed
             ok = ok && products_done(T + w.n - 1);
             tc_fence_after();
@@ -1103,8 +1113,9 @@ int launch_tiles(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a
                                : reinterpret_cast<const void *>(attn_tiles_kernel<D, kInt8, false>);
     if (!q8::set_max_dynamic_smem(fn, 227 * 1024, slot + (a.cluster ? 12 : 0))) return Q8_ERR_LAUNCH;
     if (a.cluster) {
-        const unsigned units = static_cast<unsigned>(a.batch) * a.kv_heads * ((a.max_fresh * a.group + kRows - 1) / kRows);
-        return q8::launch_pdl(attn_tiles_kernel<D, kInt8, true>, dim3(units), dim3(L::kThreads), L::smem(0), s, mk, mv, a, box);
+        const int units = a.batch * a.kv_heads * ((a.max_fresh * a.group + kRows - 1) / kRows);
+        return q8::launch_pdl(attn_tiles_kernel<D, kInt8, true>, dim3(min(units, q8::kAttnCtas)), dim3(L::kThreads), L::smem(0), s,
+                              mk, mv, a, box);
     }
     const int st = q8::launch_pdl(attn_tiles_kernel<D, kInt8, false>, dim3(q8::kAttnCtas), dim3(L::kThreads), L::smem(a.batch), s, mk,
                                   mv, a, box);
@@ -1116,14 +1127,15 @@ int launch_tiles(const CUtensorMap &mk, const CUtensorMap &mv, const AttnArgs &a
 
 namespace q8 {
 
-// 1: a CTA per unit, which it does whole, without line, workspace and second launch; 0: the line.  In tiles: a CTA's own,
+// 1: units are dealt out to CTAs, which do them whole, without line, workspace and second launch; 0: the line.  In tiles: a CTA's own,
 // against its stretch of the line and the join, some six tiles more.  Measured in a graph, 28 heads on 4 of 128 f16 values,
 // trees of up to 16 nodes, line / whole: 1 sequence of 380 keys 15.6 / 13.6 us, 1000 15.1 / 17.9; 9 of 1000 18.6 / 18.3; 38 of
-// 380 23.4 / 14.7, of 1000 31.9 / 21.8; a prompt of 520 tokens 21.2 / 14.4.
+// 380 23.4 / 14.7, of 1000 31.9 / 21.8; 61 (244 units) of 380 32.2 / 25.4; a prompt of 520 tokens 21.2 / 14.4.
 int attn_tiles_cluster(int64_t units, int64_t max_len)
 {
     const int64_t tiles = (max_len + kTile - 1) / kTile;
-    return units <= kAttnCtas && tiles <= kWholeTiles && tiles <= units * (tiles + kHead) / kAttnCtas + 6 ? 1 : 0;
+    const int64_t turns = (units + kAttnCtas - 1) / kAttnCtas;
+    return tiles <= kWholeTiles && turns * (tiles + kHead) <= units * (tiles + kHead) / kAttnCtas + kHead + 6 ? 1 : 0;
 }
 
 int attn_tiles_launch(const AttnCall &c, cudaStream_t s)

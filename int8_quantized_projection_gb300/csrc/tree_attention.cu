@@ -32,6 +32,7 @@ int cluster_of(int64_t max_rows, const q8_kv_cache *c, int64_t batch, int64_t ma
 {
     const int rows = rows_of(max_rows);
     const int64_t units = batch * c->kv_heads * ((max_rows + rows - 1) / rows);
+    if (units > (1 << 20)) return 0;  // counted in 32 bits
     return rows == 128 ? q8::attn_tiles_cluster(units, max_len) : q8::attn_rows_cluster(rows, units, max_len);
 }
 

@@ -82,6 +82,34 @@ def test_any_number_of_units(q8, batch):
     both(c)
 
 
+@pytest.mark.parametrize("heads,fresh", [(4, 1), (16, 1), (20, 2)])
+def test_more_units_than_ctas(q8, heads, fresh):
+    """8, 16 and 128 rows a unit, dealt out to CTAs; empty sequences among them."""
+    rng = np.random.default_rng(heads)
+    f = rng.integers(0, fresh + 1, 400)
+    f[0] = fresh
+    c = ref.Case(109, rng.integers(0, 90, 400).tolist(), f.tolist(), heads, 1, 64, 16, False)
+    assert clusters(q8, c, 92)
+    both(c)
+    m = trees(c)
+    both(c, m)
+
+
+def test_sequences_out_of_range_among_clusters(q8):
+    """Skipped and reported, in either form; the others are computed."""
+    for heads in (4, 16, 40):
+        for most in (64, LINE):
+            c = ref.Case(110, [20, 30, 10], [1, 1, 1], heads, 1, 64, 16, False)
+            c.table = np.pad(c.table, ((0, 0), (0, most // 16)), constant_values=-1)
+            want, lim = c.reference()
+            c.cached[1] = -5
+            y = c.run(max_len=most).cpu().numpy()
+            with pytest.raises(q8.Q8Error):
+                q8.q8_check()
+            assert np.isnan(y[1]).all()
+            ref.assert_within(y[[0, 2]], want[[0, 2]], lim[[0, 2]])
+
+
 @pytest.mark.parametrize("int8", [False, True])
 def test_plane_and_rows_that_see_nothing(q8, int8):
     import torch

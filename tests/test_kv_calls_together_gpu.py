@@ -18,20 +18,20 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 class Prepared:
     """A case's tensors on the device and the call over them."""
 
-    def __init__(self, case, most=None):
+    def __init__(self, case, bound=None):
         import torch
 
         self.case = case
         self.cache, self.q, self.table = case.cache(), case.dev(case.q), case.dev(case.table)
         self.cached, self.starts = case.dev(np.array(case.cached, np.int32)), case.dev(case.starts)
         self.y = torch.full((case.total, case.heads * case.d), float("nan"), device="cuda")
-        self.most = most or max(case.fresh)
+        self.most, self.bound = max(case.fresh), bound or self.table.shape[1] * case.page
         self.ws = torch.empty(case.q8.q8_tree_attention_workspace_bytes(self.cache, case.heads, self.most),
                               dtype=torch.uint8, device="cuda")
 
     def run(self, stream=None, ws=None):
         self.case.q8.q8_tree_attention(self.cache, 0, self.q, self.table, self.cached, self.starts, self.y,
-                                       max_fresh=self.most, max_len=self.table.shape[1] * self.case.page,
+                                       max_fresh=self.most, max_len=self.bound,
                                        workspace=self.ws if ws is None else ws, stream=stream)
 
     def check(self):
@@ -40,9 +40,11 @@ class Prepared:
 
 
 def some(int8):
-    return [Prepared(ref.Case(90, [3000, 20], [1, 1], 28, 4, 128, 64, int8)),  # 8 rows a unit
-            Prepared(ref.Case(91, [2000, 900, 5], [2, 1, 2], 14, 2, 128, 32, int8)),  # 16
-            Prepared(ref.Case(92, [1500, 0], [40, 33], 8, 1, 128, 16, int8))]  # 128
+    return [Prepared(ref.Case(*c, int8), bound)
+            for bound in (None, 1 << 20)  # a cluster or a CTA per unit; the line
+            for c in ((90, [3000, 20], [1, 1], 28, 4, 128, 64),  # 8 rows a unit
+                      (91, [2000, 900, 5], [2, 1, 2], 14, 2, 128, 32),  # 16
+                      (92, [500, 0], [40, 33], 8, 1, 128, 16))]  # 128
 
 
 @pytest.mark.parametrize("int8", [False, True])
@@ -138,21 +140,23 @@ _CHILD = textwrap.dedent(
     build.LIB = LIB
     import int8_quantized_projection_gb300 as q8
     from tests import _kv_ref as ref
-    from tests.test_kv_calls_together_gpu import some
+    from tests.test_kv_calls_together_gpu import Prepared, some
     out = {}
     for int8 in (False, True):
-        for rows, c in zip((8, 16, 128), some(int8)):
+        long = [Prepared(ref.Case(96, [60000], [n], 14, 2, 128, 64, int8), 1 << 20) for n in (1, 2, 16)]
+        for n, c in enumerate(long + some(int8)):
             c.run()
             lib = q8.lib()
             st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-            out[int8, rows] = lib.q8_check(st), lib.q8_check(st)
+            out[int8, n] = lib.q8_check(st), lib.q8_check(st)
     print("RESULT", out)
     """
 )
 
 
 def test_waits_that_run_out_report_a_timeout(tmp_path):
-    """A build whose waits give up at once: every attention kernel records the timeout, lets its copies land and returns."""
+    """A build whose waits give up at once: every attention kernel records the timeout, lets its copies land and returns.
+    Over short contexts the copies may be there before the first wait: no report then, but never another."""
     from int8_quantized_projection_gb300 import build
 
     lib = build.build(extra=["-DQ8_WAIT_LIMIT_NS=0ull"], lib_path=str(tmp_path / "libq8proj_waits0.so"))
@@ -160,4 +164,5 @@ def test_waits_that_run_out_report_a_timeout(tmp_path):
     r = subprocess.run([sys.executable, "-c", prog], capture_output=True, text=True, timeout=180, cwd=ROOT)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
     got = eval([ln for ln in r.stdout.splitlines() if ln.startswith("RESULT")][-1].split(" ", 1)[1])
-    assert len(got) == 6 and all(v == (5, 0) for v in got.values()), got  # Q8_ERR_DEVICE_TIMEOUT, then cleared
+    assert len(got) == 18 and all(v in ((5, 0), (0, 0)) for v in got.values()), got  # Q8_ERR_DEVICE_TIMEOUT, then cleared
+    assert all(got[int8, n] == (5, 0) for int8 in (False, True) for n in range(3)), got

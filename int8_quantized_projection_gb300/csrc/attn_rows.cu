@@ -207,6 +207,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         s0 = cta / a.cluster, s1 = a.batch * a.kv_heads;
         rank = cta - s0 * a.cluster;
         u.fresh = 0;
+        __syncthreads();  // the barriers and s_poison are set
     } else {
         bad_data = !q8::attn_line<kRows, kTile, kHead, kThreads>(a, pre);
         const int total = pre[a.batch];
@@ -591,7 +592,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     }
     if (bad_data) atomicOr(&g_rows_err, q8::kKvErrData);
     if (kCluster && a.cluster > 1 && u.fresh > 0) {
-        // join the CTAs of the one unit, in the order of their tiles; a warp takes 32 columns' threads, so that a block of the plane is whole
+        // join the CTAs of the one unit, in the order of their tiles; a warp takes 32 times 4 columns, whole blocks of the
+        // plane
         cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();
         for (int g = warp * a.cluster + rank; g < kRows * D / 128; g += kWarps * a.cluster) {

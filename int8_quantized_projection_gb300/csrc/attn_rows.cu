@@ -27,7 +27,7 @@
 //
 // Measured (head_dim 128, 28 heads on 4): one decode over 262139 keys, f16,
 // 86.5 us (537 MB, 6.2 TB/s, 0.92 of a copy's rate); 61 ragged ones of up to
-// 8191 keys, int8, 75 us (326 MB, 4.4 TB/s).  Some 10 us of each call are the
+// 8191 keys, int8, 73 us (326 MB, 4.5 TB/s).  Some 10 us of each call are the
 // launches, the line, the first copies' latency, and the join.  int8 is bound
 // by the warps' instructions, some 520 for 16 keys, of which the widening is a
 // fifth: 16 warps instead of 12 with q in shared memory came to 78 us, the next
@@ -68,7 +68,6 @@ struct Ring {
     static constexpr int kStage = 2 * kMat;                // and 16 values
     static constexpr int kStages = 196608 / (kWarps * kStage) < 8 ? 196608 / (kWarps * kStage) : 8;
     static constexpr int kScales = kInt8 ? 128 : 0;        // 16 + 16 f32 a stage
-    static constexpr int kTx = kStage + kScales;
     static constexpr int offScales = kWarps * kStages * kStage;
     static constexpr int offBars = offScales + kWarps * kStages * kScales;
     static constexpr int offPre = offBars + kWarps * kStages * 8;
@@ -193,7 +192,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     __shared__ int s_poison;
 
     if (lane == 0)
-        for (int i = 0; i < R::kStages; ++i) q8::mbar_init(bars + i, 1);
+        for (int i = 0; i < R::kStages; ++i) q8::mbar_init(bars + i, kInt8 ? 33 : 1);  // the codes' bytes; int8: each lane's scale
     if (tid == 0) s_poison = 0;
     q8::fence_mbar_init();
     q8::griddep_launch_dependents();
@@ -286,7 +285,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 if (lane == 0) {
                     uint8_t *dst = ring + wslot * R::kStage;
                     uint64_t *bar = bars + wslot;
-                    q8::mbar_arrive_expect_tx(bar, R::kTx);
+                    q8::mbar_arrive_expect_tx(bar, R::kStage);
                     const uint32_t d = q8::smem_u32(dst), bb = q8::smem_u32(bar);
                     constexpr int kBox = kInt8 ? D : 64;  // elements of a box row
                     constexpr int kBoxBytes = 16 * kBox * (kInt8 ? 1 : 2);
@@ -295,10 +294,12 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         q8::tma_load_2d(d + h * kBoxBytes, &mk, h * kBox, row, bb);
                         q8::tma_load_2d(d + R::kMat + h * kBoxBytes, &mv, h * kBox, row, bb);
                     }
-                    if (kInt8) {
-                        q8::bulk_g2s(ring_sc + wslot * R::kScales, a.ks + row, 64, bar);
-                        q8::bulk_g2s(ring_sc + wslot * R::kScales + 64, a.vs + row, 64, bar);
-                    }
+                }
+                if (kInt8) {  // 16 scales of the keys, 16 of the values, a lane each: two bulk copies of 64 bytes took 4 % longer
+                    const float *src = (lane < 16 ? a.ks : a.vs) + row + (lane & 15);
+                    const uint32_t dst = q8::smem_u32(ring_sc + wslot * R::kScales + lane * 4), bb = q8::smem_u32(bars + wslot);
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bb) : "memory");
                 }
                 wslot = wslot + 1 == R::kStages ? 0 : wslot + 1;
             };

@@ -555,7 +555,9 @@ typedef struct q8_kv_cache {
  * Q8_TREE_MAX_NODES with parents, a parent outside [-1, i).  The slots of the
  * tokens concerned are -1 and their masks 0.
  * Q8_ERR_ARG: batch outside 1..Q8_KV_MAX_BATCH, tokens < 1, page_size not a
- * positive multiple of 16, n_pages * page_size >= 2^31, masks without parents.
+ * positive multiple of 16, n_pages * page_size >= 2^31, masks without parents,
+ * an output that overlaps an input or another output (held_out in held's
+ * place: other CTAs still read held when the first ones write).
  */
 Q8_API int q8_kv_plan(const int32_t *cached, const int32_t *fresh, int64_t batch, const int32_t *held,
                       const int32_t *free_pages, int64_t n_free, int32_t *table, int64_t max_pages,
@@ -644,7 +646,8 @@ Q8_API int q8_tree_attention(const q8_kv_cache *cache, int64_t layer, const floa
  * token cached + j; other slots are left.  The pages behind the new length stay
  * in the table: give the next q8_kv_plan the step's held_out as `held`, and it
  * does not open them again.  A sequence with a bad path, count or page is left
- * as it is with lens = cached (Q8_ERR_DATA).
+ * as it is with lens = cached (Q8_ERR_DATA).  lens overlaps no input
+ * (Q8_ERR_ARG): the layers read cached while it is written.
  */
 Q8_API int q8_kv_accept(const q8_kv_cache *cache, const int32_t *table, int64_t max_pages, const int32_t *cached,
                         const int32_t *fresh, int64_t batch, const int32_t *paths, const int32_t *counts,

@@ -645,7 +645,8 @@ def q8_kv_plan(cached, fresh, free_pages, table, page_size: int, n_pages: int, s
     cached, fresh int32 [batch]; free_pages int32 [n_free] ids to hand out; table int32 [batch][max_pages] (the
     entries for newly opened pages are written); starts int32 [batch + 1], slots and positions int32 [tokens],
     needed int32 [1] are outputs.  ``parents`` int32 [tokens] with ``masks`` int64 [tokens] (output): draft trees.
-    ``held`` int32 [batch]: pages each row has already (default ceil(cached / page_size)); ``held_out``: after the step."""
+    ``held`` int32 [batch]: pages each row has already (default ceil(cached / page_size)); ``held_out``: after the step,
+    a tensor of its own.  Outputs share no memory with inputs or one another (refused)."""
     import torch
 
     i32, dev = torch.int32, cached.get_device()
@@ -742,7 +743,7 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
 
 def q8_kv_accept(cache: KvCache, table, cached, fresh, paths, counts, lens, stream=None, bind=False):
     """Move each sequence's accepted path (paths int32 [batch][width], counts int32 [batch]) to the front of its
-    fresh tokens, in every layer; lens int32 [batch] (output) = cached + counts."""
+    fresh tokens, in every layer; lens int32 [batch] (output, not in the place of ``cached``) = cached + counts."""
     import torch
 
     dev, i32 = cache.dev, torch.int32

@@ -415,6 +415,11 @@ extern "C" int q8_kv_plan(const int32_t *cached, const int32_t *fresh, int64_t b
                          held_out};
     for (const void *p : all)
         if (!q8::aligned16(p)) return Q8_ERR_ALIGN;
+    const q8::Span spans[] = {{table, batch * max_pages * 4}, {starts, (batch + 1) * 4}, {slots, tokens * 4},
+                              {positions, tokens * 4}, {masks, tokens * 8}, {needed, 4}, {held_out, batch * 4},
+                              {cached, batch * 4}, {fresh, batch * 4}, {held, batch * 4}, {free_pages, n_free * 4},
+                              {parents, tokens * 4}};
+    if (q8::outputs_overlap(spans, 7, 12)) return Q8_ERR_ARG;
     if (!q8::device_is_sm103()) return Q8_ERR_DEVICE;
     PlanArgs a = {cached, fresh, held, free_pages, parents, table, starts, slots, positions, needed, held_out,
                   reinterpret_cast<long long *>(masks), n_free, max_pages, tokens, static_cast<int>(batch),
@@ -468,6 +473,9 @@ extern "C" int q8_kv_accept(const q8_kv_cache *cache, const int32_t *table, int6
     const void *all[] = {table, cached, fresh, paths, counts, lens};
     for (const void *p : all)
         if (!q8::aligned16(p)) return Q8_ERR_ALIGN;
+    const q8::Span spans[] = {{lens, batch * 4}, {table, batch * max_pages * 4}, {cached, batch * 4}, {fresh, batch * 4},
+                              {paths, batch * width * 4}, {counts, batch * 4}};
+    if (q8::outputs_overlap(spans, 1, 6)) return Q8_ERR_ARG;
     if (!q8::device_is_sm103()) return Q8_ERR_DEVICE;
     AcceptArgs a = {static_cast<uint8_t *>(cache->k), static_cast<uint8_t *>(cache->v), cache->k_scale, cache->v_scale,
                     table, cached, fresh, paths, counts, lens, max_pages, q8::kv_layer_rows(*cache),

@@ -35,6 +35,24 @@ inline int kv_cache_status(const q8_kv_cache *c)
     return Q8_OK;
 }
 
+// An array of a call; {nullptr, any} where it has none.
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+
+// Whether one of the first `outs` arrays shares a byte with any other of the n.  A CTA writes its part of an output while
+// others still read the inputs, so an output in an input's place would change what they compute.
+inline bool outputs_overlap(const Span *a, int outs, int n)
+{
+    for (int i = 0; i < outs; ++i)
+        for (int j = i + 1; j < n; ++j) {
+            const uintptr_t x = reinterpret_cast<uintptr_t>(a[i].p), y = reinterpret_cast<uintptr_t>(a[j].p);
+            if (x && y && x < y + a[j].bytes && y < x + a[i].bytes) return true;
+        }
+    return false;
+}
+
 // Bits of the error words of the key/value cache's kernels.
 constexpr unsigned int kKvErrTimeout = 1u, kKvErrData = 2u;
 

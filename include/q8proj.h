@@ -524,8 +524,8 @@ typedef struct q8_kv_cache {
  *   free_pages    : int32 [n_free] page ids to hand out, in this order (input;
  *                   may be NULL when n_free is 0)
  *   table         : int32 [batch][max_pages] (in and out: the entries for the
- *                   pages that the fresh tokens open are written, all others
- *                   are left as they are)
+ *                   pages that the fresh tokens open are written, -1 where the
+ *                   free pages ran out; all others are left as they are)
  *   parents       : int32 [tokens] or NULL.  With parents, sequence b's fresh
  *                   tokens are the nodes of a draft tree: parents[starts[b]+i]
  *                   is the parent's index j < i in the same sequence, or -1 for a
@@ -545,9 +545,13 @@ typedef struct q8_kv_cache {
  *   needed        : int32 [1] (output) pages this step opens.  Pages are
  *                   handed out by sequence, then by position; needed > n_free
  *                   says that the tokens from the first missing page on have
- *                   slot -1.
- *   held_out      : int32 [batch] (output) pages each row needs now, the next
- *                   step's `held`; or NULL
+ *                   slot -1: run the call again, with the same held, once there
+ *                   are pages enough (or with fewer sequences).
+ *   held_out      : int32 [batch] (output) pages each row needs now, or NULL.
+ *                   With needed <= n_free it has them: the next step's `held`.
+ *                   Else it counts missing ones; given as `held` all the same,
+ *                   their entries of -1 are reported (Q8_ERR_DATA) and their
+ *                   tokens get slot -1.
  * Sequence b opens pages held .. ceil((cached+fresh)/page_size) - 1.  Running
  * the call again on the same inputs writes the same.
  * Q8_ERR_DATA: a negative length, fewer pages held than cached tokens need, a page id outside [0, n_pages), a table

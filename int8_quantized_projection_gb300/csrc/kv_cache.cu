@@ -138,10 +138,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
 
     if (blockIdx.y == 0)
         for (int q = warp; q < nseq; q += kPlanThreads / 32)
-            for (int i = s_held[q] + lane; i < s_want[q]; i += 32) {
-                const int p = page_of(q, i);
-                if (p >= 0) a.table[static_cast<long long>(seg + q) * a.max_pages + i] = p;
-            }
+            // -1 where there is no page: a row used before holds ids in range that belong to other sequences by now
+            for (int i = s_held[q] + lane; i < s_want[q]; i += 32)
+                a.table[static_cast<long long>(seg + q) * a.max_pages + i] = page_of(q, i);
 
     const long long t1 = min(s_start[kPlanSeqs], a.tokens);
     for (long long t = s_start[0] + tid + static_cast<long long>(kPlanThreads) * blockIdx.y; t < t1;

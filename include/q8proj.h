@@ -556,8 +556,11 @@ typedef struct q8_kv_cache {
  * the call again on the same inputs writes the same.
  * Q8_ERR_DATA: a negative length, fewer pages held than cached tokens need, a page id outside [0, n_pages), a table
  * narrower than cached + fresh, more fresh tokens than `tokens` or than
- * Q8_TREE_MAX_NODES with parents, a parent outside [-1, i).  The slots of the
- * tokens concerned are -1 and their masks 0.
+ * Q8_TREE_MAX_NODES with parents, a parent outside [-1, i).  A sequence whose
+ * lengths, held pages or row width are wrong gets slots of -1 and masks of 0.
+ * One with a wrong parent gets masks of 0 (its nodes see the cached tokens only)
+ * and keeps its slots.  A page id out of range costs the slots in that page;
+ * fresh tokens past `tokens` have no place in the per-token arrays.
  * Q8_ERR_ARG: batch outside 1..Q8_KV_MAX_BATCH, tokens < 1, page_size not a
  * positive multiple of 16, n_pages * page_size >= 2^31, masks without parents,
  * an output that overlaps an input or another output (held_out in held's

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
             for (int e = 0; e < 2; ++e) {
                 const int i = lane + 32 * e;
                 if (i < n) {
-                    a.masks[s0 + i] = static_cast<long long>(anc[e]);
+                    a.masks[s0 + i] = s_bad[q] ? 0 : static_cast<long long>(anc[e]);  // refused: its tokens have no slots
                     a.positions[s0 + i] = s_cached[q] + max(0, __popcll(anc[e]) - 1);
                 }
             }

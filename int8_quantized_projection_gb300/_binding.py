@@ -690,6 +690,21 @@ def q8_tree_attention_needs_workspace(cache: KvCache, heads: int, batch: int, ma
     return bool(lib().q8_tree_attention_needs_workspace(cache.ref, heads, batch, max_fresh, max_len))
 
 
+def _workspace_size(cache, heads, batch, max_fresh, max_len):
+    """Bytes of the workspace that a call without one gets; remembered by what they depend on."""
+    key = cache.kv_heads, cache.head_dim, heads, batch, max_fresh, max_len
+    nbytes = _workspace_sizes.get(key)
+    if nbytes is None:
+        nbytes = 0
+        if q8_tree_attention_needs_workspace(cache, heads, batch, max_fresh, max_len):
+            nbytes = q8_tree_attention_workspace_bytes(cache, heads, max_fresh)
+            if nbytes == 0:  # sizes or a descriptor that the call refuses: another cache with these figures may be right
+                return 0
+        if len(_workspace_sizes) < 1024:
+            _workspace_sizes[key] = nbytes
+    return nbytes
+
+
 def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, qs=None, ds=None, masks=None,
                       max_fresh: int = 0, max_len: int = 0, scale: float | None = None, workspace=None, stream=None,
                       bind=False):
@@ -713,14 +728,7 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
         raise ValueError("y, qs, ds or masks: fewer rows than q")
     max_fresh, max_len = max_fresh or tokens, max_len or tshape[1] * cache.page_size
     if workspace is None:
-        key = cache.kv_heads, dim, heads, batch, max_fresh, max_len
-        nbytes = _workspace_sizes.get(key)
-        if nbytes is None:
-            nbytes = 0
-            if q8_tree_attention_needs_workspace(cache, heads, batch, max_fresh, max_len):
-                nbytes = q8_tree_attention_workspace_bytes(cache, heads, max_fresh)
-            if len(_workspace_sizes) < 1024:
-                _workspace_sizes[key] = nbytes
+        nbytes = _workspace_size(cache, heads, batch, max_fresh, max_len)
         if nbytes == 0:
             pass
         elif stream is None:

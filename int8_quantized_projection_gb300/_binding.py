@@ -712,8 +712,10 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
 
     q f32 [tokens][heads * head_dim]; table, cached, starts as :func:`q8_kv_plan` left them; ``masks`` int64
     [tokens] of draft trees, or None for causal.  Writes ``y`` (f32, like q; None when dead) and, with ``qs``/``ds``,
-    its q8_0 plane.  ``max_fresh`` (default tokens) and ``max_len`` (default the table's width) bound the lengths of a
-    sequence.  ``scale`` defaults to 1/sqrt(head_dim).  ``workspace``: a uint8 CUDA tensor of at least
+    its q8_0 plane.  ``max_fresh`` (default tokens; with masks at most TREE_MAX_NODES) and ``max_len`` (default the
+    table's width) bound the lengths of a sequence.  ``max_fresh`` decides how many rows a unit has: give it for a batch
+    of several sequences, or each of 61 single tokens is computed as one of up to 61 tokens (2.4 times the time).
+    ``scale`` defaults to 1/sqrt(head_dim).  ``workspace``: a uint8 CUDA tensor of at least
     q8_tree_attention_workspace_bytes(...) bytes; when None, and the call needs one, it is allocated here with PyTorch."""
     import torch
 
@@ -726,7 +728,9 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
     if ((y is not None and y.numel() < size) or (qs is not None and qs.numel() < size)
             or (ds is not None and ds.numel() < size // 32) or (masks is not None and masks.numel() < tokens)):
         raise ValueError("y, qs, ds or masks: fewer rows than q")
-    max_fresh, max_len = max_fresh or tokens, max_len or tshape[1] * cache.page_size
+    if not max_fresh:
+        max_fresh = tokens if masks is None else min(tokens, TREE_MAX_NODES)
+    max_len = max_len or tshape[1] * cache.page_size
     if workspace is None:
         nbytes = _workspace_size(cache, heads, batch, max_fresh, max_len)
         if nbytes == 0:

@@ -600,7 +600,7 @@ Q8_API int q8_kv_append(const q8_kv_cache *cache, int64_t layer, const float *k,
  * h / (heads / kv_heads).  A row that sees nothing gives 0.
  *   q        : f32 [tokens][heads * head_dim] (input)
  *   heads    : a multiple of kv_heads, at most 64 query heads per key/value head
- *   scale    : f32, usually 1/sqrt(head_dim)
+ *   scale    : f32, usually 1/sqrt(head_dim); finite, and so is 1.45 * scale
  *   table, max_pages, cached, starts, batch : as q8_kv_plan wrote them
  *   masks    : int64 [tokens] or NULL
  *   tokens   : rows of q and y (rows at and past starts[batch] are neither read
@@ -628,7 +628,8 @@ Q8_API int q8_kv_append(const q8_kv_cache *cache, int64_t layer, const float *k,
  * NaN or an infinity in a row's q makes the row NaN; one in a value that the
  * row sees makes what it enters non-finite (a score of -inf has weight 0).
  * Q8_ERR_ARG: a NULL pointer, layer or size out of range, neither y nor a
- * plane, one of qs and ds alone, a short workspace where one is needed.
+ * plane, one of qs and ds alone, a short workspace where one is needed, a scale
+ * that is not finite.
  */
 Q8_API size_t q8_tree_attention_workspace_bytes(const q8_kv_cache *cache, int64_t heads, int64_t max_fresh);
 Q8_API int q8_tree_attention_needs_workspace(const q8_kv_cache *cache, int64_t heads, int64_t batch, int64_t max_fresh,

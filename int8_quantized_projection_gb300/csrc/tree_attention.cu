@@ -1,5 +1,8 @@
 // tree_attention.cu -- the entry points of q8_tree_attention: checks, the
 // workspace's layout and the choice of the kernel.
+#include <cfloat>
+#include <cmath>
+
 #include "attn_common.cuh"
 
 namespace {
@@ -74,6 +77,8 @@ extern "C" int q8_tree_attention(const q8_kv_cache *cache, int64_t layer, const 
         max_len < max_fresh || max_len >= (int64_t(1) << 31) - 4096 || max_pages < 1 ||
         max_pages >= (int64_t(1) << 31) || (masks && max_fresh > Q8_TREE_MAX_NODES))
         return Q8_ERR_ARG;
+    const float scale2 = scale * 1.4426950408889634f;  // the weights are powers of two
+    if (!(fabsf(scale2) <= FLT_MAX)) return Q8_ERR_ARG;
     const int group = static_cast<int>(heads / cache->kv_heads);
     const int rows = rows_of(max_fresh * group);
     // the line of tiles and units' heads is counted in 32 bits
@@ -102,7 +107,7 @@ extern "C" int q8_tree_attention(const q8_kv_cache *cache, int64_t layer, const 
            reinterpret_cast<float2 *>(ws + w.ml), reinterpret_cast<int4 *>(ws + w.desc), tokens,
            static_cast<int>(batch), static_cast<int>(heads), cache->kv_heads, group, static_cast<int>(max_pages),
            cache->page_size, static_cast<int>(cache->n_pages), static_cast<int>(max_fresh),
-           static_cast<int>(max_len), q8::kv_inverse(group), cluster, scale * 1.4426950408889634f};
+           static_cast<int>(max_len), q8::kv_inverse(group), cluster, scale2};
     c.k = kp, c.v = vp, c.layer_rows = lr, c.dim = D, c.int8 = i8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return rows == 128 ? q8::attn_tiles_launch(c, s) : q8::attn_rows_launch(c, rows, s);

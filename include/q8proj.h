@@ -663,10 +663,10 @@ Q8_API int q8_kv_accept(const q8_kv_cache *cache, const int32_t *table, int64_t 
 
 /*
  * q8_check -- synchronise `stream`, then read and clear the library's device
- * error word.  Returns Q8_OK, Q8_ERR_DEVICE_TIMEOUT if a bounded on-device
- * wait ran out since the last check (the affected outputs are undefined),
- * Q8_ERR_DATA if the key/value cache calls met a value out of range, or
- * Q8_ERR_CUDA if the synchronisation itself failed.
+ * error words.  Returns Q8_OK, Q8_ERR_DEVICE_TIMEOUT if a bounded on-device
+ * wait ran out since the last check (the affected outputs are undefined; also
+ * when there is the next to report), Q8_ERR_DATA if the key/value cache calls met
+ * a value out of range, or Q8_ERR_CUDA if the synchronisation itself failed.
  */
 Q8_API int q8_check(void *stream);
 

@@ -1,8 +1,10 @@
 // abi.cu -- C ABI plumbing of libq8proj: device checks, status codes,
 // q8_check, and the GEMM dispatch by shape.
+#include <atomic>
 #include <mutex>
+#include <thread>
 
-#include "attn_common.cuh"
+#include "q8_common.cuh"
 
 namespace q8 {
 
@@ -153,21 +155,74 @@ extern "C" const char *q8_strerror(int status)
 
 extern "C" int q8_num_sms(void) { return q8::device_sm_count(); }
 
+namespace {
+
+constexpr int kErrorWords = 6;
+struct ErrorWords {
+    unsigned int *w[kErrorWords];
+};
+
+constexpr int kChecks = 64;               // calls of q8_check that may be under way at once
+__device__ unsigned int g_taken[kChecks]; // what each found
+std::atomic<unsigned long long> g_checks; // a bit per entry of g_taken in use
+
+// Reads and clears the error words: one warp, a lane each.
+__global__ void take_errors_kernel(const __grid_constant__ ErrorWords e, int slot)
+{
+    const unsigned int mine = threadIdx.x < kErrorWords ? atomicExch(e.w[threadIdx.x], 0u) : 0u;
+    const unsigned int all = __reduce_or_sync(Q8_FULL_MASK, mine);
+    if (threadIdx.x == 0) g_taken[slot] = all;
+}
+
+bool error_words(ErrorWords *out)
+{
+    static ErrorWords words[q8::kMaxDevices];  // by device; looked up once
+    const int dev = q8::current_device();
+    if (dev < 0) return false;
+    std::lock_guard<std::mutex> lk(q8::g_mu);
+    ErrorWords &e = words[dev];
+    if (!e.w[kErrorWords - 1]) {
+        const ErrorWords got = {{q8::gemv_error_word(), q8::gemm_error_word(), q8::quant_error_word(),
+                                 q8::attn_rows_error_word(), q8::attn_tiles_error_word(), q8::kv_error_word()}};
+        for (const unsigned int *p : got.w)
+            if (!p) return false;
+        e = got;
+    }
+    *out = e;
+    return true;
+}
+
+} // namespace
+
+// One launch and one copy whatever the number of error words: with a copy from
+// and to each of the six and a wait a check takes 109 us on an idle stream,
+// with three 56 us, like this 22 us.
 extern "C" int q8_check(void *stream)
 {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(s) != cudaSuccess) return Q8_ERR_CUDA;
-    const int a = q8::gemv_take_error(s);
-    const int b = q8::gemm_take_error(s);
-    const int c = q8::quant_take_error(s);
-    const int d = q8::attn_rows_take_error(s);
-    const int e = q8::attn_tiles_take_error(s);
-    const int f = q8::kv_take_error(s);
-    for (const int st : {a, b, c, d, e, f})
-        if (st == Q8_ERR_CUDA) return st;
-    for (const int st : {a, b, c, d, e, f})
-        if (st != Q8_OK) return st;
-    return Q8_OK;
+    ErrorWords e;
+    if (!error_words(&e)) return Q8_ERR_CUDA;
+    int slot = 0;
+    for (unsigned long long used = g_checks.load();;) {
+        if (used == ~0ull) {
+            std::this_thread::yield();
+            used = g_checks.load();
+            continue;
+        }
+        slot = __builtin_ctzll(~used);
+        if (g_checks.compare_exchange_weak(used, used | 1ull << slot)) break;
+    }
+    unsigned int found = 0;
+    void *args[] = {&e, &slot};
+    const bool ok = cudaLaunchKernel(reinterpret_cast<const void *>(take_errors_kernel), dim3(1), dim3(32), args, 0, s) ==
+                        cudaSuccess &&
+                    cudaMemcpyFromSymbolAsync(&found, g_taken, sizeof(found), slot * sizeof(found),
+                                              cudaMemcpyDeviceToHost, s) == cudaSuccess &&
+                    cudaStreamSynchronize(s) == cudaSuccess;
+    g_checks.fetch_and(~(1ull << slot));
+    if (!ok) return Q8_ERR_CUDA;
+    return (found & q8::kErrTimeout) ? Q8_ERR_DEVICE_TIMEOUT : (found & q8::kErrData) ? Q8_ERR_DATA : Q8_OK;
 }
 
 namespace q8 {

@@ -303,9 +303,7 @@ struct AttnCall {
 int attn_rows_launch(const AttnCall &c, int rows, cudaStream_t s);
 int attn_rows_cluster(int rows, int64_t units, int64_t max_len);  // AttnArgs::cluster
 int attn_tiles_cluster(int64_t units, int64_t max_len);
-int attn_rows_take_error(cudaStream_t s);
 int attn_tiles_launch(const AttnCall &c, cudaStream_t s);
-int attn_tiles_take_error(cudaStream_t s);
 
 // Joins the pieces of every unit that crosses a boundary of the split: CTA
 // (c - 1, y) takes every gridDim.y-th group of rows of the unit that lies

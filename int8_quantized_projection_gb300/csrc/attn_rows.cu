@@ -351,7 +351,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         q8::mbar_wait_bounded(bars + sl, ph, Q8_DRAIN_LIMIT_NS);
                         if (++sl == R::kStages) sl = 0, ph ^= 1;
                     }
-                    if (lane == 0) atomicOr(&g_rows_err, q8::kKvErrTimeout);
+                    if (lane == 0) atomicOr(&g_rows_err, q8::kErrTimeout);
                     dead = true;
                     break;
                 }
@@ -591,7 +591,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             }
         }
     }
-    if (bad_data) atomicOr(&g_rows_err, q8::kKvErrData);
+    if (bad_data) atomicOr(&g_rows_err, q8::kErrData);
     if (kCluster && a.cluster > 1 && u.fresh > 0) {
         // join the CTAs of the one unit, in the order of their tiles; a warp takes 32 times 4 columns, whole blocks of the
         // plane
@@ -678,14 +678,10 @@ int attn_rows_launch(const AttnCall &c, int rows, cudaStream_t s)
     return rows == 8 ? launch_rows<64, false, 1>(mk, mv, c.a, 26, s) : launch_rows<64, false, 2>(mk, mv, c.a, 27, s);
 }
 
-int attn_rows_take_error(cudaStream_t s)
+unsigned int *attn_rows_error_word()
 {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_rows_err, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_rows_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return Q8_ERR_CUDA;
-    return (v & kKvErrTimeout) ? Q8_ERR_DEVICE_TIMEOUT : v ? Q8_ERR_DATA : Q8_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_rows_err) == cudaSuccess ? static_cast<unsigned int *>(p) : nullptr;
 }
 
 } // namespace q8

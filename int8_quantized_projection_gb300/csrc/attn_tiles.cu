@@ -248,7 +248,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
             : "memory");
         if (ok) return true;
         *abort_flag = 1;
-        atomicOr(&g_tiles_err, q8::kKvErrTimeout);
+        atomicOr(&g_tiles_err, q8::kErrTimeout);
         return false;
     }
     if (try_wait(bar, parity)) return true;
@@ -260,7 +260,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
         if (*abort_flag) return false;
         if (q8::globaltimer_ns() - t0 > Q8_WAIT_LIMIT_NS) {
             *abort_flag = 1;
-            atomicOr(&g_tiles_err, q8::kKvErrTimeout);
+            atomicOr(&g_tiles_err, q8::kErrTimeout);
             return false;
         }
     }
@@ -277,7 +277,7 @@ __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity)
     const uint64_t t0 = q8::globaltimer_ns();
     while (!try_wait(bar, parity))
         if (q8::globaltimer_ns() - t0 > Q8_DRAIN_LIMIT_NS) {
-            atomicOr(&g_tiles_err, q8::kKvErrTimeout);
+            atomicOr(&g_tiles_err, q8::kErrTimeout);
             return;
         }
 }
@@ -1095,7 +1095,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         bool ok = tiles == 0 || widen_k(0);
         for (int t = 0; ok && t < tiles; ++t) ok = (t + 1 == tiles || widen_k(t + 1)) && widen_v(t);
     }
-    if (bad_data) atomicOr(&g_tiles_err, q8::kKvErrData);
+    if (bad_data) atomicOr(&g_tiles_err, q8::kErrData);
 
     tc_fence_before();
     __syncthreads();
@@ -1156,14 +1156,10 @@ int attn_tiles_launch(const AttnCall &c, cudaStream_t s)
     return c.int8 ? launch_tiles<64, true>(mk, mv, c.a, box, 30, s) : launch_tiles<64, false>(mk, mv, c.a, box, 31, s);
 }
 
-int attn_tiles_take_error(cudaStream_t s)
+unsigned int *attn_tiles_error_word()
 {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_tiles_err, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_tiles_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return Q8_ERR_CUDA;
-    return (v & kKvErrTimeout) ? Q8_ERR_DEVICE_TIMEOUT : v ? Q8_ERR_DATA : Q8_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_tiles_err) == cudaSuccess ? static_cast<unsigned int *>(p) : nullptr;
 }
 
 } // namespace q8

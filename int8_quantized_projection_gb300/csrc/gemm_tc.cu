@@ -194,7 +194,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
             : "memory");
         if (ok) return true;
         *abort_flag = 1;
-        atomicOr(&g_gemm_err, 1u);
+        atomicOr(&g_gemm_err, q8::kErrTimeout);
         return false;
     }
     if (try_wait(bar, parity)) return true;
@@ -204,7 +204,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
         if (*abort_flag) return false;
         if (q8::globaltimer_ns() - t0 > Q8_WAIT_LIMIT_NS) {
             *abort_flag = 1;
-            atomicOr(&g_gemm_err, 1u);
+            atomicOr(&g_gemm_err, q8::kErrTimeout);
             return false;
         }
     }
@@ -217,7 +217,7 @@ __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity)
     const uint64_t t0 = q8::globaltimer_ns();
     while (!try_wait(bar, parity)) {
         if (q8::globaltimer_ns() - t0 > Q8_DRAIN_LIMIT_NS) {
-            atomicOr(&g_gemm_err, 1u);
+            atomicOr(&g_gemm_err, q8::kErrTimeout);
             return;
         }
     }
@@ -798,14 +798,10 @@ int gemm_tc_core(const uint8_t *a16, const float *dwt, int64_t n, int64_t k, con
 
 namespace q8 {
 
-int gemm_take_error(cudaStream_t s)
+unsigned int *gemm_error_word()
 {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_gemm_err, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_gemm_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return Q8_ERR_CUDA;
-    return v ? Q8_ERR_DEVICE_TIMEOUT : Q8_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_gemm_err) == cudaSuccess ? static_cast<unsigned int *>(p) : nullptr;
 }
 
 size_t gemm_workspace_bytes(int64_t n, int64_t t, int64_t k) { return ws_layout(n, t, k).total; }

@@ -461,7 +461,7 @@ gemv_staged_kernel(const uint4 *__restrict__ qs_row, const uint32_t *__restrict_
         const uint32_t par = (i / kStages) & 1u;
         const bool ok = q8::mbar_wait_bounded(&mybar[s], par);
         if (!__all_sync(Q8_FULL_MASK, ok)) {
-            if (lane == 0) atomicOr(&g_gemv_err, 1u);
+            if (lane == 0) atomicOr(&g_gemv_err, q8::kErrTimeout);
             // before leaving, let this warp's copies in flight land (each
             // wait bounded): no copy may still write into shared memory once
             // the CTA has exited
@@ -1004,7 +1004,7 @@ gemv_small_kernel(const __grid_constant__ SbGroup grp, const __grid_constant__ C
             for (; i < ng; ++i) {
                 const int s = i % kSbStages;
                 if (!q8::mbar_wait_bounded(&empty[s], static_cast<uint32_t>(i / kSbStages - 1) & 1u)) {
-                    atomicOr(&g_gemv_err, 1u);
+                    atomicOr(&g_gemv_err, q8::kErrTimeout);
                     *bad = 1;
                     break;
                 }
@@ -1015,7 +1015,7 @@ gemv_small_kernel(const __grid_constant__ SbGroup grp, const __grid_constant__ C
             for (int j = (i > kSbStages ? i - kSbStages : 0); j < i; ++j)
                 if (!q8::mbar_wait_bounded(&full[j % kSbStages], static_cast<uint32_t>(j / kSbStages) & 1u,
                                            Q8_DRAIN_LIMIT_NS)) {
-                    atomicOr(&g_gemv_err, 1u);
+                    atomicOr(&g_gemv_err, q8::kErrTimeout);
                     *bad = 1;
                 }
         }
@@ -1039,7 +1039,7 @@ gemv_small_kernel(const __grid_constant__ SbGroup grp, const __grid_constant__ C
                 __syncwarp();  // the barrier below is warp-aligned; got may differ between lanes on a timeout
                 if (!bar_all(1, kSbWarps * 32, got)) {
                     if (lane == 0) {
-                        atomicOr(&g_gemv_err, 1u);
+                        atomicOr(&g_gemv_err, q8::kErrTimeout);
                         *bad = 1;
                     }
                     break;
@@ -1047,7 +1047,7 @@ gemv_small_kernel(const __grid_constant__ SbGroup grp, const __grid_constant__ C
             } else {
                 if (!__all_sync(Q8_FULL_MASK, got)) {
                     if (lane == 0) {
-                        atomicOr(&g_gemv_err, 1u);
+                        atomicOr(&g_gemv_err, q8::kErrTimeout);
                         *bad = 1;
                     }
                     break;
@@ -1142,14 +1142,10 @@ int ceil_log2(int v)
 
 namespace q8 {
 
-int gemv_take_error(cudaStream_t s)
+unsigned int *gemv_error_word()
 {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_gemv_err, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_gemv_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return Q8_ERR_CUDA;
-    return v ? Q8_ERR_DEVICE_TIMEOUT : Q8_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_gemv_err) == cudaSuccess ? static_cast<unsigned int *>(p) : nullptr;
 }
 
 // Launch the generic kernel for `tokens` plane rows (used by the GEMM too).

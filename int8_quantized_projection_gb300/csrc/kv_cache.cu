@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
         for (long long t = max(s_start[kPlanSeqs], 0ll) + tid + static_cast<long long>(kPlanThreads) * blockIdx.y;
              t < a.tokens; t += static_cast<long long>(kPlanThreads) * gridDim.y)
             a.slots[t] = -1;
-    if (err) atomicOr(&g_kv_err, q8::kKvErrData);
+    if (err) atomicOr(&g_kv_err, q8::kErrData);
 }
 
 // ---------------------------------------------------------------------------
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     for (int u = 0; u < kAppendRows; ++u) {
         const int r = r0 + u * kGroups;
         if (slot[u] >= a.n_slots) {
-            if (sub == 0) atomicOr(&g_kv_err, q8::kKvErrData);
+            if (sub == 0) atomicOr(&g_kv_err, q8::kErrData);
             slot[u] = -1;
         }
         const bool is_v = r >= a.rows;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kAcceptThreads, 9) kv_accept_kernel(const __gr
     bad = __syncthreads_or(bad);
     if (layer == 0 && tid == 0) {
         a.lens[b] = c0 + (bad ? 0 : n);
-        if (bad) atomicOr(&g_kv_err, q8::kKvErrData);
+        if (bad) atomicOr(&g_kv_err, q8::kErrData);
     }
     if (bad) return;
 
@@ -387,14 +387,10 @@ __global__ void __launch_bounds__(kAcceptThreads, 9) kv_accept_kernel(const __gr
 
 namespace q8 {
 
-int kv_take_error(cudaStream_t s)
+unsigned int *kv_error_word()
 {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_kv_err, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_kv_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return Q8_ERR_CUDA;
-    return v ? Q8_ERR_DATA : Q8_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_kv_err) == cudaSuccess ? static_cast<unsigned int *>(p) : nullptr;
 }
 
 } // namespace q8

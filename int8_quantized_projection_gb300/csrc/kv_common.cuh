@@ -53,11 +53,6 @@ inline bool outputs_overlap(const Span *a, int outs, int n)
     return false;
 }
 
-// Bits of the error words of the key/value cache's kernels.
-constexpr unsigned int kKvErrTimeout = 1u, kKvErrData = 2u;
-
-int kv_take_error(cudaStream_t s);
-
 // max(a, b), NaN when either is.
 __device__ __forceinline__ float max_nan(float a, float b)
 {

@@ -15,7 +15,7 @@
 #define Q8_FULL_MASK 0xffffffffu
 
 // A bounded on-device wait gives up after this many nanoseconds, records
-// Q8_ERR_DEVICE_TIMEOUT in the translation unit's error word and lets the
+// kErrTimeout in the translation unit's error word and lets the
 // kernel return instead of hanging the GPU.
 #ifndef Q8_WAIT_LIMIT_NS
 #define Q8_WAIT_LIMIT_NS 1000000000ull
@@ -96,9 +96,19 @@ bool make_map_3d(CUtensorMap *m, CUtensorMapDataType dt, const void *ptr, uint64
                  uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1, uint32_t b2,
                  CUtensorMapSwizzle sw);
 
-// Per-translation-unit device error words are read and cleared through these
-// (each .cu file that has bounded waits defines one).
-int gemv_take_error(cudaStream_t s);
+// Bits of the device error words.
+constexpr unsigned int kErrTimeout = 1u;  // a bounded wait ran out
+constexpr unsigned int kErrData = 2u;     // a value read on the device is out of range
+
+// The current device's address of a translation unit's error word (each .cu
+// file whose kernels report errors has one), or nullptr; q8_check reads and
+// clears them all.
+unsigned int *gemv_error_word();
+unsigned int *gemm_error_word();
+unsigned int *quant_error_word();
+unsigned int *attn_rows_error_word();
+unsigned int *attn_tiles_error_word();
+unsigned int *kv_error_word();
 int gemv_generic_launch(const void *w, int64_t n, int64_t k, const int8_t *qs, const uint32_t *ds, float *y,
                         int64_t tokens, cudaStream_t s);
 // small-batch kernel (gemv.cu): 1 <= tokens <= Q8_GEMV_MAX_TOKENS, (k/32) % 8 == 0
@@ -122,8 +132,6 @@ int gemv_small_q4a_grouped_launch(const q8_gemv_proj *projs, int count, int64_t 
 constexpr int kGemvStagedMaxChunks = 512;
 int gemv_staged_q4a_launch(const void *w, int64_t n, int64_t k, const int8_t *qs, const uint32_t *ds, float *y,
                            cudaStream_t s);
-int gemm_take_error(cudaStream_t s);
-int quant_take_error(cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // device-side PTX wrappers

@@ -285,7 +285,7 @@ __device__ __forceinline__ void rowgroup_body(const CUtensorMap *tmx, const floa
             if (issued >= kGrpSlots) {
                 // the row that used this slot before must be read by all four warps
                 if (!q8::mbar_wait_bounded(&myempty[s], static_cast<uint32_t>((issued - kGrpSlots) / kGrpSlots) & 1u)) {
-                    atomicOr(&g_quant_err, 1u);
+                    atomicOr(&g_quant_err, q8::kErrTimeout);
                     break;
                 }
                 q8::fence_proxy_async_smem();  // those reads come before the copy into the slot
@@ -342,7 +342,7 @@ __device__ __forceinline__ void rowgroup_body(const CUtensorMap *tmx, const floa
             all_ok = all_ok && okf[grp][rb][k] != 0;
         }
         if (!all_ok) {  // a load did not arrive in time: report, stop (the whole group alike)
-            if (gt == 0) atomicOr(&g_quant_err, 1u);
+            if (gt == 0) atomicOr(&g_quant_err, q8::kErrTimeout);
             break;
         }
         if (mine_blk) {
@@ -594,14 +594,10 @@ extern "C" int swiglu_quant(const float *gate, const float *up, float *y, int64_
 
 namespace q8 {
 
-int quant_take_error(cudaStream_t s)
+unsigned int *quant_error_word()
 {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_quant_err, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_quant_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return Q8_ERR_CUDA;
-    return v ? Q8_ERR_DEVICE_TIMEOUT : Q8_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_quant_err) == cudaSuccess ? static_cast<unsigned int *>(p) : nullptr;
 }
 
 } // namespace q8

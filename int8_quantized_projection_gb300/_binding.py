@@ -9,6 +9,7 @@ loudly; there is no CPU or PyTorch fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 from array import array
@@ -87,9 +88,13 @@ class KvCache:
     """A paged key/value cache: the caller's tensors and the descriptor the calls take.
 
     ``k``, ``v``: f16, or int8 codes, [layers][n_pages][kv_heads][page_size][head_dim]; ``k_scale``,
-    ``v_scale``: f32 [layers][n_pages][kv_heads][page_size], with int8 only.  :func:`empty_kv_cache` makes one."""
+    ``v_scale``: f32 [layers][n_pages][kv_heads][page_size], with int8 only.  :func:`empty_kv_cache` makes one.
+    The descriptor has the tensors' addresses and sizes as they were given, so none of them can be replaced."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "kv_heads", "page_size", "head_dim", "dev", "ref", "_words")
+    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_kv_heads", "_page_size", "_head_dim", "_dev", "_ref", "_words")
+    k, v, k_scale, v_scale, kv_heads, page_size, head_dim, dev, ref = (
+        property(operator.attrgetter("_" + name))
+        for name in ("k", "v", "k_scale", "v_scale", "kv_heads", "page_size", "head_dim", "dev", "ref"))
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
@@ -102,7 +107,7 @@ class KvCache:
             raise ValueError(f"k: expected float16 or int8, got {dt}")
         if int8 != (k_scale is not None) or int8 != (v_scale is not None):
             raise ValueError("k_scale and v_scale with int8, and only then")
-        dev = self.dev = k.get_device()
+        dev = self._dev = k.get_device()
         kp, vp = _beside(k, dt, dev, "k"), _beside(v, dt, dev, "v")
         ks = vs = 0
         if int8:
@@ -110,14 +115,14 @@ class KvCache:
                 raise ValueError("k_scale, v_scale: expected [layers][n_pages][kv_heads][page_size]")
             ks = _beside(k_scale, torch.float32, dev, "k_scale")
             vs = _beside(v_scale, torch.float32, dev, "v_scale")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        layers, n_pages, self.kv_heads, self.page_size, self.head_dim = shape
+        self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
+        layers, n_pages, self._kv_heads, self._page_size, self._head_dim = shape
         # a KvCacheDesc's bytes (a Structure takes several times as long to make); sizes past 32 bits are refused below
         if max(shape[2:]) >= 1 << 31:
             raise ValueError("k: kv_heads, page_size and head_dim have 32 bits")
         self._words = array("q", (kp, vp, ks, vs, layers, n_pages, shape[2] | shape[3] << 32,
                                   shape[4] | (KV_INT8 if int8 else KV_F16) << 32))
-        self.ref = self._words.buffer_info()[0]
+        self._ref = self._words.buffer_info()[0]
 
 
 class Q8Error(RuntimeError):
@@ -673,26 +678,26 @@ def q8_kv_append(cache: KvCache, layer: int, k, v, slots, stream=None, bind=Fals
     """Write k, v f32 [tokens][kv_heads * head_dim] to the cache slots of one layer (int32 [tokens], < 0: skipped)."""
     import torch
 
-    dev, tokens = cache.dev, slots.numel()
-    size = tokens * cache.kv_heads * cache.head_dim
+    dev, tokens = cache._dev, slots.numel()
+    size = tokens * cache._kv_heads * cache._head_dim
     if k.numel() != size or v.numel() != size:
         raise ValueError("k, v: expected [tokens][kv_heads * head_dim]")
-    args = (cache.ref, layer, _beside(k, torch.float32, dev, "k"), _beside(v, torch.float32, dev, "v"),
+    args = (cache._ref, layer, _beside(k, torch.float32, dev, "k"), _beside(v, torch.float32, dev, "v"),
             _beside(slots, torch.int32, dev, "slots"), tokens)
     return _kv_call("q8_kv_append", args, dev, stream, bind, (cache, k, v, slots))
 
 
 def q8_tree_attention_workspace_bytes(cache: KvCache, heads: int, max_fresh: int) -> int:
-    return int(lib().q8_tree_attention_workspace_bytes(cache.ref, heads, max_fresh))
+    return int(lib().q8_tree_attention_workspace_bytes(cache._ref, heads, max_fresh))
 
 
 def q8_tree_attention_needs_workspace(cache: KvCache, heads: int, batch: int, max_fresh: int, max_len: int) -> bool:
-    return bool(lib().q8_tree_attention_needs_workspace(cache.ref, heads, batch, max_fresh, max_len))
+    return bool(lib().q8_tree_attention_needs_workspace(cache._ref, heads, batch, max_fresh, max_len))
 
 
 def _workspace_size(cache, heads, batch, max_fresh, max_len):
     """Bytes of the workspace that a call without one gets; remembered by what they depend on."""
-    key = cache.kv_heads, cache.head_dim, heads, batch, max_fresh, max_len
+    key = cache._kv_heads, cache._head_dim, heads, batch, max_fresh, max_len
     nbytes = _workspace_sizes.get(key)
     if nbytes is None:
         nbytes = 0
@@ -719,7 +724,7 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
     q8_tree_attention_workspace_bytes(...) bytes; when None, and the call needs one, it is allocated here with PyTorch."""
     import torch
 
-    dev, dim, i32 = cache.dev, cache.head_dim, torch.int32
+    dev, dim, i32 = cache._dev, cache._head_dim, torch.int32
     size, shape, tshape = q.numel(), q.shape, table.shape
     batch = cached.numel()
     if len(shape) != 2 or shape[1] % dim or len(tshape) != 2 or tshape[0] != batch or starts.numel() != batch + 1:
@@ -730,17 +735,17 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
         raise ValueError("y, qs, ds or masks: fewer rows than q")
     if not max_fresh:
         max_fresh = tokens if masks is None else min(tokens, TREE_MAX_NODES)
-    max_len = max_len or tshape[1] * cache.page_size
+    max_len = max_len or tshape[1] * cache._page_size
     if workspace is None:
         nbytes = _workspace_size(cache, heads, batch, max_fresh, max_len)
         if nbytes == 0:
             pass
         elif stream is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.k.device)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache._k.device)
         else:  # from the pool of the stream that uses it, so that it is not handed out again too early
             with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.k.device)
-    args = (cache.ref, layer, _beside(q, torch.float32, dev, "q"), heads, dim ** -0.5 if scale is None else scale,
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache._k.device)
+    args = (cache._ref, layer, _beside(q, torch.float32, dev, "q"), heads, dim ** -0.5 if scale is None else scale,
             _beside(table, i32, dev, "table"), tshape[1], _beside(cached, i32, dev, "cached"),
             _beside(starts, i32, dev, "starts"), batch,
             _beside(masks, torch.int64, dev, "masks") if masks is not None else None, tokens, max_fresh,
@@ -758,12 +763,12 @@ def q8_kv_accept(cache: KvCache, table, cached, fresh, paths, counts, lens, stre
     fresh tokens, in every layer; lens int32 [batch] (output, not in the place of ``cached``) = cached + counts."""
     import torch
 
-    dev, i32 = cache.dev, torch.int32
+    dev, i32 = cache._dev, torch.int32
     batch, tshape, pshape = cached.numel(), table.shape, paths.shape
     if (len(tshape) != 2 or tshape[0] != batch or len(pshape) != 2 or pshape[0] != batch or fresh.numel() != batch
             or counts.numel() != batch or lens.numel() != batch):
         raise ValueError("shape mismatch")
-    args = (cache.ref, _beside(table, i32, dev, "table"), tshape[1], _beside(cached, i32, dev, "cached"),
+    args = (cache._ref, _beside(table, i32, dev, "table"), tshape[1], _beside(cached, i32, dev, "cached"),
             _beside(fresh, i32, dev, "fresh"), batch, _beside(paths, i32, dev, "paths"),
             _beside(counts, i32, dev, "counts"), pshape[1], _beside(lens, i32, dev, "lens"))
     return _kv_call("q8_kv_accept", args, dev, stream, bind, (cache, table, cached, fresh, paths, counts, lens))

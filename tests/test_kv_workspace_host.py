@@ -14,8 +14,8 @@ class Described:
 
     def __init__(self, **kw):
         self.desc = desc(**kw)
-        self.ref = ctypes.addressof(self.desc)
-        self.kv_heads, self.head_dim = self.desc.kv_heads, self.desc.head_dim
+        self._ref = ctypes.addressof(self.desc)
+        self._kv_heads, self._head_dim = self.desc.kv_heads, self.desc.head_dim
 
 
 @pytest.fixture(autouse=True)

@@ -719,7 +719,7 @@ def q8_tree_attention(cache: KvCache, layer: int, q, table, cached, starts, y, q
     [tokens] of draft trees, or None for causal.  Writes ``y`` (f32, like q; None when dead) and, with ``qs``/``ds``,
     its q8_0 plane.  ``max_fresh`` (default tokens; with masks at most TREE_MAX_NODES) and ``max_len`` (default the
     table's width) bound the lengths of a sequence.  ``max_fresh`` decides how many rows a unit has: give it for a batch
-    of several sequences, or each of 61 single tokens is computed as one of up to 61 tokens (2.4 times the time).
+    of several sequences (61 single tokens over up to 8191 keys take 219 us with the default, 76 with 1, int8).
     ``scale`` defaults to 1/sqrt(head_dim).  ``workspace``: a uint8 CUDA tensor of at least
     q8_tree_attention_workspace_bytes(...) bytes; when None, and the call needs one, it is allocated here with PyTorch."""
     import torch

@@ -29,8 +29,8 @@
 // 86.5 us (537 MB, 6.2 TB/s, 0.92 of a copy's rate); 61 ragged ones of up to
 // 8191 keys, int8, 73 us (326 MB, 4.5 TB/s).  Some 10 us of each call are the
 // launches, the line, the first copies' latency, and the join.  int8 is bound
-// by the warps' instructions, some 520 for 16 keys, of which the widening is a
-// fifth: 16 warps instead of 12 with q in shared memory came to 78 us, the next
+// by the warps' chains of dependent steps, some 520 instructions for 16 keys, of
+// which the widening is a fifth (52 % of the issue slots are used): 16 warps instead of 12 with q in shared memory came to 78 us, the next
 // unit's copies before the join to 75.6, two chains of score MMAs to 78.6; none
 // was kept.
 #include <cooperative_groups.h>
@@ -55,7 +55,9 @@ constexpr float kRaise = 8.0f;       // m may lag the maximum by this
 // The MMA's f32 accumulation truncates: with values of one sign O loses 1e-7 of
 // itself per MMA (measured: 2.5e-5 after 257).  After this many tiles, one MMA
 // per tile and value in each warp, a piece's result goes to the workspace,
-// rounded to nearest, and the next tiles start anew.
+// rounded to nearest, and the next tiles start anew: up to 6e-6 of a result whose
+// values have one sign is lost, and half of that with chains of 32, for one more
+// pass over the rows' O every 32 tiles.
 constexpr int kChain = 64;
 
 template <int D, bool kInt8, int RG>
@@ -641,10 +643,11 @@ namespace q8 {
 // The CTAs of a unit that join in shared memory, or 0 for the line.  A cluster has no line to add up, no workspace and no
 // second launch, but a unit gets eight CTAs at most, and those of a short unit are idle.  In tiles: a CTA's own
 // and its start, against a stretch of the line with its start and the join, some three tiles more.  Measured in a graph, 28
-// heads on 4 of 128 f16 values, lengths ragged up to the one given, line / clusters: 1 sequence of 380 keys 10.3 / 8.5 us (8
-// CTAs), 4097 10.4 / 10.3, 12000 11.7 / 14.4; 5 sequences of 1500 11.8 / 9.4 (4 CTAs); 9 of 6000 20.3 / 17.8 (4); 38 of 380
-// 16.8 / 8.3 (1), of 1500 23.4 / 17.7 (1); 61, whose 244 units are dealt out to 152 CTAs, of 380 18.4 / 15.1, of 1500 31.7 /
-// 29.5.
+// heads on 4 of 128 f16 values, lengths ragged up to the one given, line / clusters of the size that the rule takes: 1
+// sequence of 380 keys 9.9 / 7.9 us (2 CTAs), 4097 10.6 / 9.9 (8); 5 sequences of 1500 11.8 / 9.4 (4); 8 of 6000 17.6 / 15.7
+// (4); 16 of 1500 15.2 / 12.2 (2); 38 of 380 17.7 / 9.4 (1), of 1500 23.6 / 17.7 (1); 61, whose 244 units are dealt out to 152
+// CTAs, of 380 19.4 / 16.1, of 1500 30.8 / 28.9.  Left to the line: 1 of 12000, 13.1 us (14.4 in clusters of 8), and 9 of 6000,
+// whose 36 clusters of 4 may not all fit, 18.7.
 int attn_rows_cluster(int rows, int64_t units, int64_t max_len)
 {
     const int64_t tile = rows == 8 ? Ring<128, false, 1>::kTile : Ring<128, false, 2>::kTile, tiles = (max_len + tile - 1) / tile;

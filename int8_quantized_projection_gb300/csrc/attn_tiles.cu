@@ -39,10 +39,13 @@
 // them twice, in two parts: 1094 TFLOP/s); 8 trees of up to 16 nodes over up
 // to 16001 keys, f16, 50 us (198 MB, 3.9 TB/s); 4 trees of up to 64 nodes over
 // up to 30011 keys, int8, 158 us.  A tile's two products take 2048 cycles of
-// the tensor core; f16 tiles follow each other every 2750 cycles, bound by the
-// softmax warps' instructions (two warps a scheduler), int8 tiles every 5000:
-// their scores are read twice, and free the next scores' place only then.  A
-// unit's start and end cost 12000 more, some 5000 of them for q's two parts.
+// the tensor core; f16 tiles follow each other every 2750 cycles, int8 tiles
+// every 5000.  What bounds them is the softmax warps' chain of dependent steps
+// (scores, maximum, vote, weights, store), which all eight walk in step, two a
+// scheduler: 43 % (f16) and 51 % (int8) of the issue slots are used, and most
+// waits are for tensor memory.  int8 scores are read twice, and free the next
+// scores' place only then.  A unit's start and end cost 12000 more, some 5000
+// of them for q's two parts.
 //
 // Every mbarrier wait is bounded; one that runs out raises the CTA's abort
 // flag and the error word, and all roles drain and exit.

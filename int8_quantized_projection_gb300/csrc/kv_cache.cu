@@ -17,8 +17,9 @@ __device__ unsigned int g_kv_err;
 // and round) instead of waiting for a scan kernel or for its neighbours, so
 // the plan is one launch of independent CTAs and its time is one launch's
 // latency.  gridDim.y CTAs share a segment's tokens when a few sequences
-// bring many.  Measured on the device: 1 sequence 2.8 us, 509 trees of up to 64
-// nodes 6.4 us.
+// bring many; the ancestor sets are the work of the first of them, two trees a
+// warp, which is what many trees wait for.  Measured on the device: 1 sequence
+// 2.8 us, 509 trees of up to 64 nodes 6.4 us.
 // ---------------------------------------------------------------------------
 constexpr int kPlanSeqs = 32, kPlanThreads = 512;
 
@@ -221,10 +222,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
 // ---------------------------------------------------------------------------
 // q8_kv_append.  A row (one head of one token) is D/4 lanes with a float4
 // each, so a warp takes 1 (D = 128) or 2 (D = 64) rows at a time; the row's
-// amax is a shuffle over those lanes.  Bound by memory: 4 bytes read and 2 or
-// 1 written per value.  Four rows per lane group are loaded before the first
-// is encoded, so that a prompt's call keeps enough bytes in flight; the loads
-// do not depend on the slot, which is looked up meanwhile.
+// amax is a shuffle over those lanes.  4 bytes are read and 2 or 1 written per
+// value.  Four rows per lane group are loaded before the first is encoded, so
+// that a prompt's call keeps enough bytes in flight; the loads do not depend on
+// the slot, which is looked up meanwhile.  Not bound by memory: a prompt of 3325
+// tokens is one wave of CTAs that load, then encode (59 % of the issue slots
+// while an SM has work, most waits for the loads), and the launch is half the
+// time.
 // ---------------------------------------------------------------------------
 // Its places are found by products instead of divisions, of which a thread
 // would do twelve.  Measured: 3325 tokens of 4 heads of 128 values into an int8

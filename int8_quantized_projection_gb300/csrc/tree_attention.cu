@@ -26,8 +26,8 @@ Workspace workspace(int rows, int d)
 }
 
 // Packed rows of a unit, by the most a sequence and head can have.  Measured with 28 heads on 4, head_dim 128, 8 sequences
-// of up to 16001 keys, f16 / int8: for 7 rows 35 / 28 us with 8 rows a unit, 41 / 43 with 16, 41 / 67 with 128; for 14 rows
-// 30 / 31 us with 16 rows a unit, 30 / 48 with 128.
+// of up to 16001 keys (136 / 70 MB, 20 / 10 us of HBM), f16 / int8: for 7 rows 30.2 / 23.5 us with 8 rows a unit, 35.5 / 36.4
+// with 16, 36.5 / 56.5 with 128; for 14 rows 36.7 / 37.6 us with 16 rows a unit, 36.6 / 56.4 with 128.
 int rows_of(int64_t max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 128; }
 
 // CTAs of a unit that join without the workspace, or 0.

@@ -552,8 +552,9 @@ typedef struct q8_kv_cache {
  *                   are pages enough (or with fewer sequences).
  *   held_out      : int32 [batch] (output) pages each row needs now, or NULL.
  *                   With needed <= n_free it has them: the next step's `held`.
- *                   Else it counts missing ones; given as `held` all the same,
- *                   their entries of -1 are reported (Q8_ERR_DATA) and their
+ *                   Else it counts missing ones, whose entries of -1 are a row's
+ *                   last: a row has held_out less those.  With held_out as `held`
+ *                   all the same, they are reported (Q8_ERR_DATA) and their
  *                   tokens get slot -1.
  * Sequence b opens pages held .. ceil((cached+fresh)/page_size) - 1.  Running
  * the call again on the same inputs writes the same.

@@ -648,8 +648,9 @@ def q8_kv_plan(cached, fresh, free_pages, table, page_size: int, n_pages: int, s
     """The integers of one step over a paged cache, from the request lengths.
 
     cached, fresh int32 [batch]; free_pages int32 [n_free] ids to hand out; table int32 [batch][max_pages] (the
-    entries for newly opened pages are written); starts int32 [batch + 1], slots and positions int32 [tokens],
-    needed int32 [1] are outputs.  ``parents`` int32 [tokens] with ``masks`` int64 [tokens] (output): draft trees.
+    entries for newly opened pages are written, -1 where the list ran out); starts int32 [batch + 1], slots and
+    positions int32 [tokens], needed int32 [1] are outputs.  The list itself is left: the caller drops its first
+    ``needed`` ids after the step.  ``parents`` int32 [tokens] with ``masks`` int64 [tokens] (output): draft trees.
     ``held`` int32 [batch]: pages each row has already (default ceil(cached / page_size)); ``held_out``: after the step,
     a tensor of its own.  Outputs share no memory with inputs or one another (refused)."""
     import torch

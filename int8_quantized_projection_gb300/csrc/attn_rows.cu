@@ -30,9 +30,9 @@
 // 8191 keys, int8, 73 us (326 MB, 4.5 TB/s).  Some 10 us of each call are the
 // launches, the line, the first copies' latency, and the join.  int8 is bound
 // by the warps' chains of dependent steps, some 520 instructions for 16 keys, of
-// which the widening is a fifth (52 % of the issue slots are used): 16 warps instead of 12 with q in shared memory came to 78 us, the next
-// unit's copies before the join to 75.6, two chains of score MMAs to 78.6; none
-// was kept.
+// which the widening is a fifth (52 % of the issue slots are used): 16 warps
+// instead of 12 with q in shared memory came to 78 us, the next unit's copies
+// before the join to 75.6, two chains of score MMAs to 78.6; none was kept.
 #include <cooperative_groups.h>
 #include <cuda.h>
 

@@ -51,6 +51,22 @@ def test_an_entry_without_a_page_keeps_no_old_one(q8, n_free):
     assert wrong["slots"].tolist() == want[2].tolist()
 
 
+@pytest.mark.parametrize("n_free", [0, 1, 2, 3])
+def test_the_next_step_goes_on_with_the_pages_that_there_are(q8, n_free):
+    """What a row has is held_out less its entries of -1: with the tokens that got a slot, a step like any other."""
+    rng = np.random.default_rng(80 + n_free)
+    table, free, n_pages = used_table(rng)
+    got = run(q8, CACHED, FRESH, PAGE, free[:n_free], table, n_pages, sum(FRESH))
+    held = [int(h) - int((row[:h] == -1).sum()) for h, row in zip(got["held_out"], got["table"])]
+    assert sum(held) == sum(ref.pages_of(c, PAGE) for c in CACHED) + n_free
+    ends = np.cumsum(FRESH)
+    cached = [c + int((got["slots"][e - f:e] >= 0).sum()) for c, f, e in zip(CACHED, FRESH, ends)]
+    fresh, left = [20, 3, 1], free[n_free:]
+    again = run(q8, cached, fresh, PAGE, left, got["table"], n_pages, sum(fresh), held=held)
+    q8.q8_check()
+    check(again, ref.plan(cached, fresh, PAGE, left, got["table"], sum(fresh), held=held), sum(fresh), sum(fresh), None)
+
+
 def test_a_free_page_out_of_range_leaves_no_old_entry(q8):
     rng = np.random.default_rng(75)
     table, free, n_pages = used_table(rng)

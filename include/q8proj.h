@@ -643,9 +643,9 @@ Q8_API int q8_kv_append(const q8_kv_cache *cache, int64_t layer, const float *k,
  * identical.
  * A token that a row cannot see never enters its result, whatever it holds.  A
  * NaN or an infinity in a row's q makes the row NaN; one in a value that the
- * row sees makes what it enters non-finite.  An f16 key with a NaN or an infinity
- * makes the rows that see it NaN, also where the score would be -inf and the
- * weight 0: the products of q's two parts with an infinity cancel.
+ * row sees makes what it enters non-finite.  An infinite f16 key may make the
+ * rows that see it NaN also where its score would be -inf and its weight 0: q's
+ * two parts may differ in sign.
  * Q8_ERR_ARG: a NULL pointer, layer or size out of range, neither y nor a
  * plane, one of qs and ds alone, a short workspace where one is needed, a scale
  * that is not finite.

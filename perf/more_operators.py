@@ -210,7 +210,7 @@ def run_own(s):
                         mode=q8.ROUTE_CHOSEN if case["chosen"] else q8.ROUTE_ALL, valid=s["valid"])
         return {key: s[key] for key in ("ids", "weights", "offsets", "rows", "places")}
     if op == "norm":
-        q8.residual_rmsnorm_quant(s["x"], s["h"], b=s["b"], expert_rows=s["ye"], places=s["places"], weights=s["weights"],
+        q8.rmsnorm_residual_quant(s["x"], s["h"], b=s["b"], expert_rows=s["ye"], places=s["places"], weights=s["weights"],
                                   w_post=s["w_post"], eps_post=EPS, gate=s["gate"], residual_scale=0.75, w=s["w"], eps=EPS,
                                   y=s.get("y"), qs=s.get("qs"), ds=s.get("ds"))
         return {"h": s["h"], "y": values(s["qs"], s["ds"], case["rows"]) if case["plane"] else s["y"]}

@@ -63,7 +63,7 @@ extern "C" {
 #define Q8_ERR_DEVICE_TIMEOUT 5  /* a bounded on-device wait ran out (reported by q8_check) */
 #define Q8_ERR_CUDA           6  /* another CUDA runtime error (stream sync, symbol copy) */
 #define Q8_ERR_TOO_BIG        7  /* the request needs more than the fixed scratch of q8_0_gemm_noalloc */
-#define Q8_ERR_DATA           8  /* a length, page, slot, parent or path read on the device is out of range (reported by q8_check) */
+#define Q8_ERR_DATA           8  /* a length, page, slot, parent, path, offset, row or place read on the device is out of range (reported by q8_check) */
 
 /* Recommended number of plane rows for `rows` tokens: rows rounded up to a
  * multiple of 128 (the GEMM's token tile).  Any rows_pad >= rows is accepted
@@ -681,11 +681,143 @@ Q8_API int q8_kv_accept(const q8_kv_cache *cache, const int32_t *table, int64_t 
                         int64_t width, int32_t *lens, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * A mixture-of-experts block: each token's activation meets the matrices of a
+ * few experts that its router logits choose on the device.  A step is
+ *     router logits (any projection) -> q8_moe_route
+ *     -> q8_0_experts_gate_up -> q8_0_experts_gemm (down)
+ *     -> rmsnorm_residual_quant (the weighted sum, both norms, the next plane).
+ *
+ * A (token, expert) pair has number p = token * top_k + j, j < top_k.  Sorted by
+ * expert, and by p within one, the pairs are the rows 0 .. offsets[experts] - 1
+ * of the products: those of expert e are offsets[e] .. offsets[e + 1] - 1.  All
+ * of this is device data, so one captured graph serves steps of any routing.
+ * The kernels check each value before it becomes an address: an expert whose
+ * offsets are out of order or range has no rows, a row whose pair is out of
+ * range is left as it was, and q8_check reports Q8_ERR_DATA.  Workspaces: two
+ * calls, or two captured graphs, may share one only if they are ordered on one
+ * stream; contents are ignored on entry.  Outputs overlap neither inputs nor
+ * one another (Q8_ERR_ARG).
+ * ---------------------------------------------------------------------------
+ */
+#define Q8_MAX_EXPERTS 1024
+#define Q8_MAX_TOP_K   16
+#define Q8_EXPERTS_MAX_N (1 << 22)   /* rows of an expert's matrix */
+#define Q8_EXPERTS_MAX_K (1 << 20)   /* its columns */
+#define Q8_ROUTE_CHOSEN 1   /* weights: softmax over the chosen experts */
+#define Q8_ROUTE_ALL    2   /* weights: softmax over all experts */
+
+/*
+ * q8_moe_route -- the experts of each token, their weights, and the pairs
+ * sorted by expert.
+ *   logits : f32 [tokens][experts] (input)
+ *   mode, scale : weight_j = scale * exp(l_j - max) / sum, the sum over the
+ *            chosen experts (Q8_ROUTE_CHOSEN) or over all (Q8_ROUTE_ALL)
+ *   valid  : int32 [1] (input) tokens that count, 0 .. tokens (Q8_ERR_DATA
+ *            otherwise, and the nearest is taken), or NULL for all; the others,
+ *            which fill up a graph's capacity, get no expert
+ *   ids    : int32 [tokens][top_k] (output) experts by falling logit, of equal
+ *            logits (+0 and -0 are) the lower expert first.  A logit that is
+ *            -inf or NaN is never chosen: a token with too few others has -1 in
+ *            the last places.
+ *   weights: f32 [tokens][top_k] (output), 0 where ids is -1.  Logits of +inf
+ *            share the weight equally.
+ *   offsets: int32 [experts + 1] (output) first sorted row of each expert, and
+ *            the number of pairs with an expert
+ *   rows   : int32 [tokens * top_k] (output) pair of each sorted row; -1 behind
+ *            the last
+ *   places : int32 [tokens][top_k] (output) sorted row of each pair, -1 without
+ *   workspace, workspace_bytes : device scratch of at least
+ *            q8_moe_route_workspace_bytes(tokens, experts, top_k) bytes; NULL
+ *            and 0 where that is 0 (few tokens).
+ * experts 1..Q8_MAX_EXPERTS, top_k 1..Q8_MAX_TOP_K and <= experts, tokens >= 1,
+ * tokens * top_k < 2^31, scale finite (Q8_ERR_ARG).  Results are run-to-run
+ * identical.
+ */
+Q8_API size_t q8_moe_route_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k);
+Q8_API int q8_moe_route(const float *logits, int64_t tokens, int64_t experts, int64_t top_k, int mode, float scale,
+                        const int32_t *valid, int32_t *ids, float *weights, int32_t *offsets, int32_t *rows,
+                        int32_t *places, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * q8_0_experts_gemm -- Y[r][i] = sum_b d_w(e,i,b) * d_a(s,b) * isum for the
+ * sorted rows r of every expert e, s the plane row of r: the formula of
+ * q8_0_gemm with the matrix chosen per row.
+ *   w      : Q8_0 blocks [experts][n][k/32] (input)
+ *   qs, ds, plane_rows : plane with plane_rows rows (input)
+ *   offsets: int32 [experts + 1] (input, q8_moe_route's)
+ *   rows   : int32 [pairs] (input, q8_moe_route's): row r reads plane row
+ *            rows[r] / top_k; or NULL: it reads plane row r (an activation that
+ *            is in sorted order already)
+ *   pairs  : capacity of rows and y (>= offsets[experts])
+ *   y      : f32 [pairs][n] (output); rows behind offsets[experts] are left
+ *   workspace, workspace_bytes : at least q8_0_experts_gemm_workspace_bytes(...)
+ *            bytes of device scratch; NULL and 0 where that is 0
+ * k % 32 == 0, any n >= 1.  The integer dot product of a block is exact, the
+ * scale of a block is rounded once and blocks are added in f32; results are
+ * run-to-run identical.
+ */
+Q8_API size_t q8_0_experts_gemm_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t plane_rows,
+                                                int64_t top_k, int64_t pairs);
+Q8_API int q8_0_experts_gemm(const void *w, int64_t experts, int64_t n, int64_t k, const int8_t *qs, const uint32_t *ds,
+                             int64_t plane_rows, const int32_t *offsets, const int32_t *rows, int64_t top_k,
+                             int64_t pairs, float *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * q8_0_experts_gate_up -- the gate and up products of the sorted rows and the
+ * plane of silu(gate) * up, which is the input of the down product (rows NULL).
+ *   w_gate, w_up : Q8_0 blocks [experts][nf][k/32] each (inputs)
+ *   qs, ds, plane_rows, offsets, rows, top_k, pairs : as for q8_0_experts_gemm
+ *   qs_out, ds_out : int8 [pairs][nf], uint32 [pairs][nf/32] (outputs): the
+ *            plane's rows in sorted order; rows behind offsets[experts] are left
+ * nf % 32 == 0.  SwiGLU and its encoding are those of swiglu_quant on the two
+ * products.
+ */
+Q8_API size_t q8_0_experts_gate_up_workspace_bytes(int64_t experts, int64_t nf, int64_t k, int64_t plane_rows,
+                                                   int64_t top_k, int64_t pairs);
+Q8_API int q8_0_experts_gate_up(const void *w_gate, const void *w_up, int64_t experts, int64_t nf, int64_t k,
+                                const int8_t *qs, const uint32_t *ds, int64_t plane_rows, const int32_t *offsets,
+                                const int32_t *rows, int64_t top_k, int64_t pairs, int8_t *qs_out, uint32_t *ds_out,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * rmsnorm_residual_quant -- the end of a block and the start of the next in one
+ * pass over the rows:
+ *     b' = b + sum_j weights[t][j] * expert_rows[places[t][j]]   (either part may be absent)
+ *     p  = (b' * rsqrt(mean(b'^2) + eps_post)) * w_post          (b' itself without w_post)
+ *     h  = residual_scale * x + gate * p                         (gate 1 without)
+ *     y  = (h * rsqrt(mean(h^2) + eps)) * w, and its q8_0 plane.
+ *   x      : f32 [rows][d] (input) the residual stream
+ *   b      : f32 [rows][d] (input) a dense block's output, or NULL
+ *   expert_rows, expert_row_count : f32 [expert_row_count][d] (input,
+ *            q8_0_experts_gemm's y), or NULL with top_k 0
+ *   places, weights : [rows][top_k] (inputs, q8_moe_route's), or NULL with top_k
+ *            0.  A place of -1 adds nothing; one out of range neither
+ *            (Q8_ERR_DATA).
+ *   w_post : f32 [d], or NULL       eps_post : read with w_post only
+ *   gate   : f32 [gate_rows][d], gate_rows 1 or rows, or NULL
+ *   w      : f32 [d]; NULL when neither y nor a plane is written
+ *   h      : f32 [rows][d] (output), x itself allowed; or NULL
+ *   y      : f32 [rows][d] (output), or NULL
+ *   qs, ds, rows_pad : plane of y (output; rows rows .. rows_pad - 1 are zeros),
+ *            or NULL both; exactly the encoding of the f32 values y holds or
+ *            would hold
+ * d % 32 == 0, d <= 32768, rows >= 0, rows_pad >= max(rows, 1); at least one
+ * output; residual_scale finite, eps >= 0.  The sums run over j in order, b
+ * first; each mean is an f32 sum in a fixed order.
+ */
+Q8_API int rmsnorm_residual_quant(const float *x, float residual_scale, const float *b, const float *expert_rows,
+                                  int64_t expert_row_count, const int32_t *places, const float *weights, int64_t top_k,
+                                  const float *w_post, float eps_post, const float *gate, int64_t gate_rows,
+                                  const float *w, float eps, float *h, float *y, int64_t rows, int64_t d, int8_t *qs,
+                                  uint32_t *ds, int64_t rows_pad, void *stream);
+
+/*
  * q8_check -- synchronise `stream`, then read and clear the library's device
  * error words.  Returns Q8_OK, Q8_ERR_DEVICE_TIMEOUT if a bounded on-device
  * wait ran out since the last check (the affected outputs are undefined; also
- * when there is the next to report), Q8_ERR_DATA if the key/value cache calls met
- * a value out of range, or Q8_ERR_CUDA if the synchronisation itself failed.
+ * when there is the next to report), Q8_ERR_DATA if the key/value cache's or the
+ * experts' calls met a value out of range, or Q8_ERR_CUDA if the synchronisation itself failed.
  */
 Q8_API int q8_check(void *stream);
 

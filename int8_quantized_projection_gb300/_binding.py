@@ -57,6 +57,15 @@ SIGNATURES = {
     "q8_tree_attention": (_INT, [_P, _I64, _P, _I64, ctypes.c_float, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _P,
                                  _P, _P, ctypes.c_size_t, _P]),
     "q8_kv_accept": (_INT, [_P, _P, _I64, _P, _P, _I64, _P, _P, _I64, _P, _P]),
+    "q8_moe_route_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "q8_moe_route": (_INT, [_P, _I64, _I64, _I64, _INT, ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "q8_0_experts_gemm_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I64, _I64]),
+    "q8_0_experts_gemm": (_INT, [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _P, _P, ctypes.c_size_t, _P]),
+    "q8_0_experts_gate_up_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I64, _I64]),
+    "q8_0_experts_gate_up": (_INT, [_P, _P, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P, ctypes.c_size_t,
+                                    _P]),
+    "rmsnorm_residual_quant": (_INT, [_P, ctypes.c_float, _P, _P, _I64, _P, _P, _I64, _P, ctypes.c_float, _P, _I64, _P,
+                                      ctypes.c_float, _P, _P, _I64, _I64, _P, _P, _I64, _P]),
     "q8_check": (_INT, [_P]),
     "q8_num_sms": (_INT, []),
 }
@@ -67,6 +76,9 @@ KV_F16, KV_INT8 = 1, 2
 TREE_MAX_NODES = 64
 KV_MAX_BATCH = 4096
 GEMV_MAX_TOKENS = 16
+ROUTE_CHOSEN, ROUTE_ALL = 1, 2
+MAX_EXPERTS = 1024
+MAX_TOP_K = 16
 PRODUCER_QUANT, PRODUCER_RMSNORM, PRODUCER_SWIGLU = 1, 2, 3
 
 
@@ -773,6 +785,163 @@ def q8_kv_accept(cache: KvCache, table, cached, fresh, paths, counts, lens, stre
             _beside(fresh, i32, dev, "fresh"), batch, _beside(paths, i32, dev, "paths"),
             _beside(counts, i32, dev, "counts"), pshape[1], _beside(lens, i32, dev, "lens"))
     return _kv_call("q8_kv_accept", args, dev, stream, bind, (cache, table, cached, fresh, paths, counts, lens))
+
+
+def _scratch(workspace, nbytes, dev, stream):
+    """The caller's workspace, or one of `nbytes` from the pool of the stream that uses it; None where none is needed."""
+    import torch
+
+    if workspace is not None or not nbytes:
+        return workspace
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+
+
+def _opt(t, dtype, dev, name):
+    return _beside(t, dtype, dev, name) if t is not None else None
+
+
+def _scratch_args(workspace, dev):
+    return (_beside(workspace, workspace.dtype, dev, "workspace"), workspace.nbytes) if workspace is not None else (None, 0)
+
+
+def q8_moe_route_workspace_bytes(tokens: int, experts: int, top_k: int) -> int:
+    return int(lib().q8_moe_route_workspace_bytes(tokens, experts, top_k))
+
+
+def q8_moe_route(logits, ids, weights, offsets, rows, places, mode: int = ROUTE_CHOSEN, scale: float = 1.0, valid=None,
+                 workspace=None, stream=None, bind=False):
+    """The top_k experts of each token, their weights, and the (token, expert) pairs sorted by expert.
+
+    logits f32 [tokens][experts]; outputs ids int32 and weights f32 [tokens][top_k], offsets int32 [experts + 1], rows
+    int32 [tokens * top_k] (the pair of each sorted row), places int32 [tokens][top_k] (the sorted row of each pair).
+    ``mode``: ROUTE_CHOSEN or ROUTE_ALL, what the softmax of the weights runs over.  ``valid`` int32 [1]: how many tokens
+    count (default all).  ``workspace``: a uint8 CUDA tensor; allocated here with PyTorch when None and one is needed."""
+    import torch
+
+    i32, dev = torch.int32, logits.get_device()
+    shape, ishape = logits.shape, ids.shape
+    if len(shape) != 2 or len(ishape) != 2 or ishape[0] != shape[0]:
+        raise ValueError("logits: expected [tokens][experts]; ids [tokens][top_k]")
+    (tokens, experts), top_k = shape, ishape[1]
+    if (weights.shape != ishape or places.shape != ishape or offsets.numel() != experts + 1
+            or rows.numel() != tokens * top_k or (valid is not None and valid.numel() != 1)):
+        raise ValueError("shape mismatch")
+    args = (_beside(logits, torch.float32, dev, "logits"), tokens, experts, top_k, mode, scale,
+            _opt(valid, i32, dev, "valid"), _beside(ids, i32, dev, "ids"), _beside(weights, torch.float32, dev, "weights"),
+            _beside(offsets, i32, dev, "offsets"), _beside(rows, i32, dev, "rows"), _beside(places, i32, dev, "places"))
+    workspace = _scratch(workspace, q8_moe_route_workspace_bytes(tokens, experts, top_k), dev, stream)
+    return _kv_call("q8_moe_route", args + _scratch_args(workspace, dev), dev, stream, bind,
+                    (logits, valid, ids, weights, offsets, rows, places, workspace))
+
+
+def _experts_sizes(w, experts, n, k, qs, ds, offsets, rows, top_k, pairs):
+    if k % 32 or w.numel() != experts * n * (k // 32) * 34:
+        raise ValueError("w: expected experts * n rows of k/32 blocks of 34 bytes")
+    shape = qs.shape
+    if len(shape) != 2 or shape[1] != k or ds.shape != (shape[0], k // 32):
+        raise ValueError("plane shape mismatch")
+    if offsets.numel() != experts + 1 or (rows is not None and rows.numel() != pairs):
+        raise ValueError("offsets: expected [experts + 1]; rows [pairs]")
+    return (experts, n, k, shape[0], top_k, pairs)
+
+
+def q8_0_experts_gemm_workspace_bytes(experts: int, n: int, k: int, plane_rows: int, top_k: int, pairs: int) -> int:
+    return int(lib().q8_0_experts_gemm_workspace_bytes(experts, n, k, plane_rows, top_k, pairs))
+
+
+def q8_0_experts_gemm(w, experts: int, n: int, k: int, qs, ds, offsets, y, rows=None, top_k: int = 1, workspace=None,
+                      stream=None, bind=False):
+    """y f32 [pairs][n]: each sorted row's plane row times its expert's matrix.
+
+    w uint8 [experts][n][k/32 blocks of 34 bytes]; offsets int32 [experts + 1] and ``rows`` int32 [pairs] as
+    :func:`q8_moe_route` wrote them with this ``top_k`` (row r reads plane row rows[r] // top_k), or ``rows=None``: row r
+    reads plane row r.  Rows behind offsets[experts] are left.  ``workspace``: a uint8 CUDA tensor of at least
+    q8_0_experts_gemm_workspace_bytes(...) bytes; allocated here with PyTorch when None and one is needed."""
+    import torch
+
+    i32, dev, pairs = torch.int32, qs.get_device(), y.shape[0]
+    if y.numel() != pairs * n:
+        raise ValueError("y: expected [pairs][n]")
+    sizes = _experts_sizes(w, experts, n, k, qs, ds, offsets, rows, top_k, pairs)
+    workspace = _scratch(workspace, q8_0_experts_gemm_workspace_bytes(*sizes), dev, stream)
+    args = (_beside(w, torch.uint8, dev, "w"), experts, n, k, _beside(qs, torch.int8, dev, "qs"), _beside(ds, i32, dev, "ds"),
+            sizes[3], _beside(offsets, i32, dev, "offsets"), _opt(rows, i32, dev, "rows"), top_k, pairs,
+            _beside(y, torch.float32, dev, "y"))
+    return _kv_call("q8_0_experts_gemm", args + _scratch_args(workspace, dev), dev, stream, bind,
+                    (w, qs, ds, offsets, rows, y, workspace))
+
+
+def q8_0_experts_gate_up_workspace_bytes(experts: int, nf: int, k: int, plane_rows: int, top_k: int, pairs: int) -> int:
+    return int(lib().q8_0_experts_gate_up_workspace_bytes(experts, nf, k, plane_rows, top_k, pairs))
+
+
+def q8_0_experts_gate_up(w_gate, w_up, experts: int, nf: int, k: int, qs, ds, offsets, qs_out, ds_out, rows=None,
+                         top_k: int = 1, workspace=None, stream=None, bind=False):
+    """The plane (qs_out int8 [>= pairs][nf], ds_out int32 [>= pairs][nf/32]) of silu(gate) * up of the sorted rows.
+
+    w_gate, w_up and the other arguments as for :func:`q8_0_experts_gemm`; the plane's rows are in sorted order, ready for
+    the down product with ``rows=None``.  ``pairs`` is rows' length, or the output plane's rows without ``rows``."""
+    import torch
+
+    i32, dev = torch.int32, qs.get_device()
+    oshape = qs_out.shape
+    pairs = rows.numel() if rows is not None else oshape[0]
+    if len(oshape) != 2 or oshape[1] != nf or oshape[0] < pairs or ds_out.shape != (oshape[0], nf // 32):
+        raise ValueError("output plane shape mismatch")
+    sizes = _experts_sizes(w_gate, experts, nf, k, qs, ds, offsets, rows, top_k, pairs)
+    if w_up.numel() != w_gate.numel():
+        raise ValueError("w_up: expected the size of w_gate")
+    workspace = _scratch(workspace, q8_0_experts_gate_up_workspace_bytes(*sizes), dev, stream)
+    args = (_beside(w_gate, torch.uint8, dev, "w_gate"), _beside(w_up, torch.uint8, dev, "w_up"), experts, nf, k,
+            _beside(qs, torch.int8, dev, "qs"), _beside(ds, i32, dev, "ds"), sizes[3], _beside(offsets, i32, dev, "offsets"),
+            _opt(rows, i32, dev, "rows"), top_k, pairs, _beside(qs_out, torch.int8, dev, "qs_out"),
+            _beside(ds_out, i32, dev, "ds_out"))
+    return _kv_call("q8_0_experts_gate_up", args + _scratch_args(workspace, dev), dev, stream, bind,
+                    (w_gate, w_up, qs, ds, offsets, rows, qs_out, ds_out, workspace))
+
+
+def rmsnorm_residual_quant(x, h, b=None, expert_rows=None, places=None, weights=None, w_post=None, eps_post: float = 0.0,
+                           gate=None, residual_scale: float = 1.0, w=None, eps: float = 0.0, y=None, qs=None, ds=None,
+                           stream=None, bind=False):
+    """h = residual_scale * x + gate * norm(b + sum_j weights[:, j] * expert_rows[places[:, j]]), then y = rmsnorm(h) * w
+    and its plane, in one pass.
+
+    x, b, h (``x`` itself allowed; None when dead) and y f32 [rows][d]; expert_rows f32 [pairs][d], places int32 and
+    weights f32 [rows][top_k] (q8_moe_route's; -1 adds nothing); w_post (None: no norm behind the block) and w f32 [d]; gate
+    f32 [1][d] or [rows][d].  ``y`` and the plane (``qs``/``ds``, any padded rows) are optional and need ``w``."""
+    import torch
+
+    f32, i32, dev = torch.float32, torch.int32, x.get_device()
+    rows, d = x.shape
+    top_k = 0
+    if expert_rows is not None:
+        if places is None or weights is None or len(places.shape) != 2 or weights.shape != places.shape:
+            raise ValueError("places, weights: expected [rows][top_k] with expert_rows")
+        top_k = places.shape[1]
+        if places.shape[0] != rows or top_k < 1 or len(expert_rows.shape) != 2 or expert_rows.shape[1] != d:
+            raise ValueError("expert_rows: expected [pairs][d]; places [rows][top_k]")
+    elif places is not None or weights is not None:
+        raise ValueError("places and weights with expert_rows, and only then")
+    for t, name in ((b, "b"), (h, "h"), (y, "y")):
+        if t is not None and t.shape != x.shape:
+            raise ValueError(f"{name}: expected the shape of x")
+    if (w is not None and w.numel() != d) or (w_post is not None and w_post.numel() != d):
+        raise ValueError("w, w_post: expected [d]")
+    if gate is not None and (gate.numel() % d or gate.numel() // d not in (1, rows)):
+        raise ValueError("gate: expected [1][d] or [rows][d]")
+    rows_pad = qs.shape[0] if qs is not None else 0
+    if (qs is None) != (ds is None) or (qs is not None and (qs.shape != (rows_pad, d) or ds.shape != (rows_pad, d // 32))):
+        raise ValueError("plane shape mismatch")
+    args = (_beside(x, f32, dev, "x"), residual_scale, _opt(b, f32, dev, "b"), _opt(expert_rows, f32, dev, "expert_rows"),
+            expert_rows.shape[0] if top_k else 0, _opt(places, i32, dev, "places"), _opt(weights, f32, dev, "weights"), top_k,
+            _opt(w_post, f32, dev, "w_post"), eps_post, _opt(gate, f32, dev, "gate"), gate.numel() // d if gate is not None else 0,
+            _opt(w, f32, dev, "w"), eps, _opt(h, f32, dev, "h"), _opt(y, f32, dev, "y"), rows, d,
+            _opt(qs, torch.int8, dev, "qs"), _opt(ds, i32, dev, "ds"), rows_pad)
+    return _kv_call("rmsnorm_residual_quant", args, dev, stream, bind, (x, b, expert_rows, places, weights, w_post, gate, w, h, y,
+                                                                        qs, ds))
 
 
 def empty_plane(rows_pad: int, k: int, device="cuda"):

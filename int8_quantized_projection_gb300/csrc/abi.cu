@@ -147,7 +147,7 @@ extern "C" const char *q8_strerror(int status)
     case Q8_ERR_LAUNCH: return "kernel launch failed";
     case Q8_ERR_DEVICE_TIMEOUT: return "a bounded on-device wait ran out";
     case Q8_ERR_CUDA: return "CUDA runtime error";
-    case Q8_ERR_DATA: return "a length, page, slot, parent or path on the device is out of range";
+    case Q8_ERR_DATA: return "a length, page, slot, parent, path, offset, row or place on the device is out of range";
     case Q8_ERR_TOO_BIG: return "request exceeds the fixed scratch of the no-allocation entry point";
     default: return "unknown status";
     }
@@ -157,7 +157,7 @@ extern "C" int q8_num_sms(void) { return q8::device_sm_count(); }
 
 namespace {
 
-constexpr int kErrorWords = 6;
+constexpr int kErrorWords = 9;
 struct ErrorWords {
     unsigned int *w[kErrorWords];
 };
@@ -178,7 +178,8 @@ __global__ void take_errors_kernel(const __grid_constant__ ErrorWords e, int slo
 bool error_words(ErrorWords *e)
 {
     *e = {{q8::gemv_error_word(), q8::gemm_error_word(), q8::quant_error_word(), q8::attn_rows_error_word(),
-           q8::attn_tiles_error_word(), q8::kv_error_word()}};
+           q8::attn_tiles_error_word(), q8::kv_error_word(), q8::route_error_word(), q8::experts_error_word(),
+           q8::resnorm_error_word()}};
     for (const unsigned int *p : e->w)
         if (!p) return false;
     return true;
@@ -187,7 +188,7 @@ bool error_words(ErrorWords *e)
 } // namespace
 
 // One launch and one copy whatever the number of error words: with a copy from
-// and to each of the six and a wait a check takes 109 us on an idle stream,
+// and to each of six and a wait a check takes 109 us on an idle stream,
 // with three 56 us, like this 23 us.
 extern "C" int q8_check(void *stream)
 {

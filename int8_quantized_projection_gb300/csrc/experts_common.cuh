@@ -1,0 +1,47 @@
+// experts_common.cuh -- what the kernels of the experts' products share: the
+// arguments of a launch and the lookup of a sorted row's source.
+#pragma once
+
+#include "kv_common.cuh"
+
+namespace q8 {
+
+// One product over grouped rows: for the rows r of expert e, offsets[e] <= r < offsets[e + 1],
+//     out[r * ld + i] = w[e][i] . plane[source(r)],   i < n,
+// and with w2 the same for a second matrix into out[r * ld + n + i].
+struct ExpertsArgs {
+    const uint8_t *w, *w2;    // [experts][n] rows of nb Q8_0 blocks; w2 may be nullptr
+    const int8_t *qs;         // plane [plane_rows][32 nb]
+    const uint32_t *ds;       // [plane_rows][nb]
+    const int32_t *offsets;   // [experts + 1]
+    const int32_t *rows;      // pair of each sorted row, or nullptr: row r reads plane row r
+    float *out;
+    int64_t plane_rows, ld;
+    int experts, n, nb, top_k, pairs;
+};
+
+// The rows of expert e, checked: an expert whose offsets are out of range has none.
+struct ExpertRows {
+    int first, count;
+    bool bad;
+};
+
+__device__ __forceinline__ ExpertRows expert_rows_of(const ExpertsArgs &a, int e)
+{
+    const int lo = a.offsets[e], hi = a.offsets[e + 1];
+    const bool bad = lo < 0 || hi < lo || hi > a.pairs;
+    return {lo, bad ? 0 : hi - lo, bad};
+}
+
+// Plane row of sorted row r, or -1 where it is out of range.
+__device__ __forceinline__ int64_t source_row(const ExpertsArgs &a, int r)
+{
+    int64_t s = r;
+    if (a.rows) {
+        const int p = a.rows[r];
+        s = p < 0 ? -1 : p / a.top_k;
+    }
+    return s < a.plane_rows ? s : -1;
+}
+
+} // namespace q8

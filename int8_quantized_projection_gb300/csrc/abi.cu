@@ -10,7 +10,7 @@ namespace q8 {
 
 namespace {
 constexpr int kMaxDevices = 64;
-constexpr int kMaxSlots = 48;
+constexpr int kMaxSlots = 64;
 int g_sms[kMaxDevices];        // 0 = not queried yet
 int g_is103[kMaxDevices];      // 0 = unknown, 1 = yes, 2 = no
 int g_smem_set[kMaxDevices][kMaxSlots];
@@ -157,7 +157,7 @@ extern "C" int q8_num_sms(void) { return q8::device_sm_count(); }
 
 namespace {
 
-constexpr int kErrorWords = 9;
+constexpr int kErrorWords = 10;
 struct ErrorWords {
     unsigned int *w[kErrorWords];
 };
@@ -179,7 +179,7 @@ bool error_words(ErrorWords *e)
 {
     *e = {{q8::gemv_error_word(), q8::gemm_error_word(), q8::quant_error_word(), q8::attn_rows_error_word(),
            q8::attn_tiles_error_word(), q8::kv_error_word(), q8::route_error_word(), q8::experts_error_word(),
-           q8::resnorm_error_word()}};
+           q8::experts_tiles_error_word(), q8::resnorm_error_word()}};
     for (const unsigned int *p : e->w)
         if (!p) return false;
     return true;

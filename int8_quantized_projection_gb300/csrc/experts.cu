@@ -77,6 +77,8 @@ bool sizes_ok(int64_t experts, int64_t n, int64_t k, int64_t plane_rows, int64_t
            pairs >= 1 && pairs < most - 256;
 }
 
+bool many_rows(int64_t experts, int64_t pairs) { return pairs >= 32 * experts; }
+
 int64_t weight_bytes(int64_t experts, int64_t n, int64_t k) { return experts * n * (k / 32) * 34; }
 
 q8::ExpertsArgs args_of(const void *w, const void *w2, int64_t experts, int64_t n, int64_t k, const int8_t *qs,
@@ -97,7 +99,8 @@ q8::ExpertsArgs args_of(const void *w, const void *w2, int64_t experts, int64_t 
 extern "C" size_t q8_0_experts_gemm_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t plane_rows,
                                                     int64_t top_k, int64_t pairs)
 {
-    return 0;
+    if (!sizes_ok(experts, n, k, plane_rows, top_k, pairs) || !many_rows(experts, pairs)) return 0;
+    return q8::experts_tiles_workspace(k, plane_rows, true, pairs);
 }
 
 extern "C" int q8_0_experts_gemm(const void *w, int64_t experts, int64_t n, int64_t k, const int8_t *qs, const uint32_t *ds,
@@ -114,14 +117,16 @@ extern "C" int q8_0_experts_gemm(const void *w, int64_t experts, int64_t n, int6
     for (const q8::Span &p : spans)
         if (!q8::aligned16(p.p)) return Q8_ERR_ALIGN;
     if (!q8::device_is_sm103()) return Q8_ERR_DEVICE;
-    return experts_launch(args_of(w, nullptr, experts, n, k, qs, ds, plane_rows, offsets, rows, top_k, pairs, y),
-                          static_cast<cudaStream_t>(stream));
+    const q8::ExpertsArgs a = args_of(w, nullptr, experts, n, k, qs, ds, plane_rows, offsets, rows, top_k, pairs, y);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return many_rows(experts, pairs) ? q8::experts_tiles_launch(a, nullptr, nullptr, workspace, s) : experts_launch(a, s);
 }
 
 extern "C" size_t q8_0_experts_gate_up_workspace_bytes(int64_t experts, int64_t nf, int64_t k, int64_t plane_rows,
                                                        int64_t top_k, int64_t pairs)
 {
     if (!sizes_ok(experts, nf, k, plane_rows, top_k, pairs) || nf % 32 != 0) return 0;
+    if (many_rows(experts, pairs)) return q8::experts_tiles_workspace(k, plane_rows, true, pairs);
     return static_cast<size_t>(pairs) * nf * 8;
 }
 
@@ -145,8 +150,9 @@ extern "C" int q8_0_experts_gate_up(const void *w_gate, const void *w_up, int64_
     if (!q8::device_is_sm103()) return Q8_ERR_DEVICE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     float *gu = static_cast<float *>(workspace);
-    const int st = experts_launch(
-        args_of(w_gate, w_up, experts, nf, k, qs, ds, plane_rows, offsets, rows, top_k, pairs, gu), s);
+    const q8::ExpertsArgs a = args_of(w_gate, w_up, experts, nf, k, qs, ds, plane_rows, offsets, rows, top_k, pairs, gu);
+    if (many_rows(experts, pairs)) return q8::experts_tiles_launch(a, qs_out, ds_out, workspace, s);
+    const int st = experts_launch(a, s);
     if (st != Q8_OK) return st;
     const int64_t ctas = (pairs * nf / 4 + 255) / 256;
     return q8::launch_pdl(experts_swiglu_kernel, dim3(static_cast<unsigned>(ctas < 152 * 8 ? ctas : 152 * 8)), dim3(256), 0, s,

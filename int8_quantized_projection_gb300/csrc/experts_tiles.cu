@@ -9,29 +9,32 @@
 // weights first would cost as much as the products.
 //
 //   Tiles.  128 weight rows x 64 or 128 sorted rows of one expert.  An expert's
-//   rows are dealt to ceil(rows / 128) tiles in groups of 64.  All
-//   tiles lie on one line (expert, weight tile, row tile), which the offsets
-//   on the device make, and CTA c takes tiles c, c + grid, ...: those that run
-//   together share their weights in L2.  A CTA's pipelines run on from tile to
-//   tile; only the epilogue's stores lie between the last block of one and the
-//   first of the next.
-//   Weights go to shared memory as they are (34-byte blocks, TMA boxes of 16
+//   rows are dealt to ceil(rows / 128) tiles in groups of 64.  All tiles lie on
+//   one line (expert, weight tile, row tile), which the offsets on the device
+//   make, and CTA c takes tiles c, c + grid, ...: those that run together share
+//   their weights in L2.  A CTA's pipelines run on from tile to tile; only the
+//   epilogue's stores lie between the last block of one and the first of the
+//   next.
+//   Weights go to shared memory as they are (34-byte blocks, TMA boxes of 32
 //   rows x 8 blocks, or 4-byte copies where rows of blocks are not 16-byte
-//   aligned), and four warps widen them there, a row a thread.
-//   Activations: a pre-pass widens the plane's codes to f16 once per plane row;
-//   the rows of a tile are gathered from there four a copy (tile::gather4), so
-//   no sorted copy of them is written.
-//   Gate and up: the 128 rows of a tile are 64 rows of each, 16 by 16, so that
-//   the two products of a channel meet in one thread, and the epilogue writes
-//   the plane of silu(gate) * up.
+//   aligned), and four warps widen them there, a row a thread.  Four other
+//   warps load the plane rows of a tile, wherever they lie, and widen them into
+//   shared memory: a quarter of the bytes that a widened plane would take from
+//   L2, no pass before the product and no workspace.
+//   Scales.  d_w(i) * d_a(t) of a block is a product of two vectors: a third MMA
+//   computes it beside the integers, d_w and d_a in the first of its 16 columns
+//   and zeros in the others (a product of two f16 is exact in f32).  So the
+//   epilogue reads two numbers a value from tensor memory and does one fma,
+//   without scales from shared memory (16 bytes a lane and four values) and
+//   without products of them.
+//   Gate and up: the 128 rows of a tile are 64 rows of each, 32 by 32.  Two
+//   warps swap halves of their columns, then a warp has a block of 32 channels of
+//   32 rows, and writes the plane of silu(gate) * up.
 //
-// Warp roles (512 threads):
-//   warp 0      gathers activation tiles, 2 blocks a stage
-//   warp 1      MMA issuer (one thread), tensor memory
-//   warp 2      weight copies, 8 blocks a slot
-//   warp 3      activation scales, 4 blocks a slot, and which rows are in range
-//   warps 4-7   widen weights
-//   warps 8-15  epilogue: two warps per TMEM lane quarter, 32-column groups in turn
+// Warp roles (640 threads):
+//   warp 0       MMA issuer, tensor memory      warp 1   weight copies, 8 blocks a slot
+//   warps 4-7    widen weights                  warps 8-11   load and widen activations
+//   warps 12-19  epilogue: a TMEM lane quarter and 64 columns each
 // Every mbarrier wait is bounded; a wait that runs out sets the CTA abort flag
 // and the error word, and all roles drain and exit.
 #include "experts_common.cuh"
@@ -41,33 +44,30 @@ namespace {
 __device__ unsigned int g_tiles_err;
 
 constexpr int BM = 128, kGroup = 64, kMaxGroups = 2, BN = kGroup * kMaxGroups;
-constexpr int kStages = 3, kRawSlots = 2, kDwSlots = 2, kDaSlots = 3, kAcc = 4;
-constexpr int kTmemBuf = BN, kTmemCols = kAcc * kTmemBuf;
-constexpr int kThreads = 512, kWidenThreads = 128, kEpiWarps = 8, kEpiThreads = 256;
-constexpr int kRegsCtl = 72, kRegsWiden = 72, kRegsEpi = 184;
-static_assert(128 * kRegsCtl + kWidenThreads * kRegsWiden + kEpiThreads * kRegsEpi <= 128 * kThreads, "register split");
+constexpr int kStages = 3, kRawSlots = 2, kAcc = 2;
+constexpr int kTmemBuf = 2 * BN, kTmemCols = kAcc * kTmemBuf;  // integers, then scales
+constexpr int kThreads = 640, kWidenThreads = 128, kEpiWarps = 8, kEpiThreads = 256;
+constexpr int kRegsCtl = 48, kRegsWiden = 72, kRegsEpi = 144, kRegsLaunch = 96;  // 640 threads: 65536 / 640, in eights
+static_assert(128 * kRegsCtl + 2 * kWidenThreads * kRegsWiden + kEpiThreads * kRegsEpi <= kRegsLaunch * kThreads, "register split");
 
 constexpr int kPiece = 8;                      // blocks of a weight slot
 constexpr int kPitchTma = 34 * kPiece;         // 272: a row's piece
 constexpr int kPitchAny = kPitchTma + 4;       // 276: with the two bytes that a row may start late; 69 words, odd
 constexpr int kRawBytes = BM * kPitchAny;      // 35328
 constexpr int kABytes = BM * 128, kBBytes = BN * 128;
-constexpr int kDwBytes = kPiece * BM * 4, kDaBlocks = 4, kDaBytes = kDaBlocks * BN * 4 + 32;
+constexpr int kScBytes = 128 * 16;             // one block's scales: 128 rows of 8 f16, of which the first is used
 
-constexpr int OFF_A = 0;
-constexpr int OFF_B = OFF_A + kStages * kABytes;
-constexpr int OFF_RAW = OFF_B + kStages * kBBytes;
-constexpr int OFF_DW = OFF_RAW + kRawSlots * kRawBytes;
-constexpr int OFF_DA = OFF_DW + kDwSlots * kDwBytes;
-constexpr int OFF_AMAX = OFF_DA + kDaSlots * kDaBytes;  // [4][BN] f32
-constexpr int OFF_CODES = OFF_AMAX + 4 * BN * 4;        // [BN][64] int8
-constexpr int OFF_MASK = OFF_CODES + BN * 64;           // rows of the tile that are in range: 6 words
-constexpr int OFF_CUM = OFF_MASK + 32;                  // row tiles before each expert
-constexpr int kBars = 2 * kRawSlots + 3 * kStages + 2 * kDwSlots + 2 * kDaSlots + 2 * kAcc + 1;
+constexpr int kStageBytes = kABytes + kBBytes + 4 * kScBytes;  // two blocks: codes of both sides, d_w twice, d_a twice
+constexpr int OFF_B = kABytes, OFF_DW = OFF_B + kBBytes, OFF_DA = OFF_DW + 2 * kScBytes;  // in a stage
+constexpr int OFF_ZERO = kStages * kStageBytes;         // columns 8 .. 15 of every scale operand
+constexpr int OFF_RAW = OFF_ZERO + kScBytes;
+constexpr int OFF_SWAP = OFF_RAW + kRawSlots * kRawBytes;  // [8 warps][16 columns][32] f32
+constexpr int OFF_CUM = OFF_SWAP + kEpiWarps * 16 * 32 * 4;  // row tiles before each expert
+constexpr int kBars = 2 * kRawSlots + 3 * kStages + 2 * kAcc + 1;
 constexpr int OFF_BAR = OFF_CUM + (Q8_MAX_EXPERTS + 2) * 4;
 constexpr int OFF_MISC = OFF_BAR + kBars * 8;           // abort flag, TMEM address, sums of the scan
-constexpr int kSmemBytes = OFF_MISC + 16 + 64 + 1024;   // + alignment slack
-static_assert(OFF_BAR % 8 == 0 && OFF_DA % 16 == 0 && OFF_CODES % 16 == 0 && kSmemBytes <= 227 * 1024, "shared memory");
+constexpr int kSmemBytes = OFF_MISC + 16 + 96 + 1024;   // + alignment slack
+static_assert(OFF_BAR % 8 == 0 && kStageBytes % 1024 == 0 && OFF_RAW % 128 == 0 && kSmemBytes <= 227 * 1024, "shared memory");
 
 struct Bars {
     uint32_t b0;
@@ -77,11 +77,7 @@ struct Bars {
     __device__ uint32_t a_full(int s) const { return at(2 * kRawSlots + s); }
     __device__ uint32_t b_full(int s) const { return at(2 * kRawSlots + kStages + s); }
     __device__ uint32_t ab_empty(int s) const { return at(2 * kRawSlots + 2 * kStages + s); }
-    __device__ uint32_t dw_full(int s) const { return at(2 * kRawSlots + 3 * kStages + s); }
-    __device__ uint32_t dw_empty(int s) const { return dw_full(kDwSlots + s); }
-    __device__ uint32_t da_full(int s) const { return dw_full(2 * kDwSlots + s); }
-    __device__ uint32_t da_empty(int s) const { return da_full(kDaSlots + s); }
-    __device__ uint32_t acc_full(int s) const { return da_full(2 * kDaSlots + s); }
+    __device__ uint32_t acc_full(int s) const { return at(2 * kRawSlots + 3 * kStages + s); }
     __device__ uint32_t acc_empty(int s) const { return acc_full(kAcc + s); }
     __device__ uint32_t drain() const { return acc_full(2 * kAcc); }
 };
@@ -108,22 +104,39 @@ __device__ __forceinline__ void tc_commit(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// 16 lanes x 32 columns: thread 4g + m gets lanes g and g + 8 at columns 8 rep + 2 m + {0, 1} in registers 4 rep + {0, 1} and
-// 4 rep + {2, 3}.  Valid after tc_wait_ld; tc_regs16 keeps their uses behind it.
-__device__ __forceinline__ void tc_ld16x32(uint32_t taddr, uint32_t *r)
+// 32 columns of the thread's own lane (warp w has lanes 32 (w % 4) and on).  Valid after tc_wait_ld; tc_regs32 keeps their uses
+// behind it.  This shape gives 3.3 registers a cycle and scheduler; 16x256b, which spreads a row over eight lanes, one.
+__device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t *r)
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
 
-__device__ __forceinline__ void tc_regs16(uint32_t *r)
+__device__ __forceinline__ void tc_regs32(uint32_t *r)
 {
-    asm volatile(""
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+#pragma unroll
+    for (int i = 0; i < 32; i += 16)
+        asm volatile(""
+                     : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]),
+                       "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]), "+r"(r[i + 12]),
+                       "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]));
+}
+
+// The arithmetic behind 16 pairs is done before any later volatile statement: their operands' registers are free for the next load.
+__device__ __forceinline__ void order16(float2 *a)
+{
+#pragma unroll
+    for (int i = 0; i < 16; i += 8)
+        asm volatile(""
+                     : "+f"(a[i].x), "+f"(a[i].y), "+f"(a[i + 1].x), "+f"(a[i + 1].y), "+f"(a[i + 2].x), "+f"(a[i + 2].y),
+                       "+f"(a[i + 3].x), "+f"(a[i + 3].y), "+f"(a[i + 4].x), "+f"(a[i + 4].y), "+f"(a[i + 5].x), "+f"(a[i + 5].y),
+                       "+f"(a[i + 6].x), "+f"(a[i + 6].y), "+f"(a[i + 7].x), "+f"(a[i + 7].y));
 }
 
 // K-major operand, 128-byte swizzle: rows of 128 bytes in 1024-byte atoms of 8 rows.
@@ -133,20 +146,26 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr)
            (1ull << 46) | (2ull << 61);
 }
 
+// K-major operand of 16 columns without swizzle: rows of 16 bytes for columns 0 .. 7 at addr, the zeros for columns 8 .. 15.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr, uint32_t zeros)
+{
+    return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>(((zeros - addr) >> 4) & 0x3fffu) << 16) |
+           (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
+}
+
 // D f32, A and B f16, K-major, M = 128, N = columns.
 __device__ __forceinline__ uint32_t mma_desc(int columns)
 {
     return (1u << 4) | (static_cast<uint32_t>(columns >> 3) << 17) | (static_cast<uint32_t>(BM >> 4) << 24);
 }
 
-// Four rows of the f16 plane, 128 bytes of each from element x on, to 512 bytes at dst.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, int x, int4 rows, uint32_t bar)
+// One lane of a warp that goes on together.  What only one thread may do is done inside: with operands that are the same in all lanes
+// an MMA takes some 40 cycles to issue; from a thread that has left its warp, 110.
+__device__ __forceinline__ bool elect_one()
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
-        "%6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar)
-        : "memory");
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // 4 bytes to shared memory, of which the first `bytes` come from src and the rest are zeros.
@@ -248,9 +267,9 @@ __device__ __forceinline__ int groups_of(int rows) { return (rows + kGroup - 1) 
 __device__ __forceinline__ int row_tiles_of(int rows) { return (groups_of(rows) + kMaxGroups - 1) / kMaxGroups; }
 
 // cum[e]: row tiles of the experts before e.
-__device__ __forceinline__ Tile tile_at(const q8::ExpertsArgs &a, const int *cum, int weight_tiles, int64_t at)
+__device__ __forceinline__ Tile tile_at(const q8::ExpertsArgs &a, const int *cum, int weight_tiles, int at)
 {
-    const int q = static_cast<int>(at / weight_tiles);
+    const int q = at / weight_tiles;
     int lo = 0, hi = a.experts;  // cum[lo] <= q < cum[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -260,7 +279,7 @@ __device__ __forceinline__ Tile tile_at(const q8::ExpertsArgs &a, const int *cum
             hi = mid;
     }
     const int mine = cum[lo + 1] - cum[lo];
-    const int rest = static_cast<int>(at - static_cast<int64_t>(cum[lo]) * weight_tiles);
+    const int rest = at - cum[lo] * weight_tiles;
     Tile t;
     t.e = lo;
     t.nt = rest / mine;
@@ -274,128 +293,34 @@ __device__ __forceinline__ Tile tile_at(const q8::ExpertsArgs &a, const int *cum
     return t;
 }
 
-// Weight row (of all experts' rows) at position r of a tile; in a pair of matrices positions 16 .. 31 of each 32 are w2's.
+// Weight row (of an expert's) at position r of a tile; in a pair of matrices positions 32 .. 63 and 96 .. 127 are w2's.
 template <bool kPair>
 __device__ __forceinline__ int tile_row(int nt, int r)
 {
-    return kPair ? 64 * nt + 16 * (r >> 5) + (r & 15) : BM * nt + r;
+    return kPair ? 64 * nt + 32 * (r >> 6) + (r & 31) : BM * nt + r;
 }
 
-__device__ __forceinline__ int dw_slot(int r) { return (r >> 5) * 32 + (r & 7) * 4 + ((r >> 4) & 1) * 2 + ((r >> 3) & 1); }
-// column -> place of its scale: the eight columns of a thread in a group of 32 are neighbours
-__device__ __forceinline__ int da_slot(int c) { return (c & ~31) + ((c >> 1) & 3) * 8 + ((c >> 3) & 3) * 2 + (c & 1); }
-
-// acc += (d_w * d_a) * P for one 16-lane x 32-column load
-__device__ __forceinline__ void epi_math(float2 *acc, const uint32_t *p, const float *da, float dw_lo, float dw_hi)
+// acc += scale * integer over 32 columns.
+__device__ __forceinline__ void epi_half(uint32_t taddr, float2 *acc)
 {
-    const float2 w0 = make_float2(dw_lo, dw_lo), w1 = make_float2(dw_hi, dw_hi);
+    uint32_t p[32], s[32];
+    tc_ld32(taddr, p);
+    tc_ld32(taddr + BN, s);
+    tc_wait_ld();
+    tc_regs32(p);
+    tc_regs32(s);
 #pragma unroll
-    for (int rep = 0; rep < 4; ++rep) {
-        const float2 d2 = make_float2(da[2 * rep], da[2 * rep + 1]);
-        acc[2 * rep] = __ffma2_rn(__fmul2_rn(w0, d2), make_float2(__uint_as_float(p[4 * rep]), __uint_as_float(p[4 * rep + 1])),
-                                  acc[2 * rep]);
-        acc[2 * rep + 1] = __ffma2_rn(__fmul2_rn(w1, d2),
-                                      make_float2(__uint_as_float(p[4 * rep + 2]), __uint_as_float(p[4 * rep + 3])),
-                                      acc[2 * rep + 1]);
-    }
-}
-
-// What an epilogue warp carries from block to block.
-struct EpiState {
-    uint8_t *sm;
-    Bars B;
-    volatile int *abort_flag;
-    uint32_t taddr;      // this warp's lanes and first column group
-    int q, h, g, m;      // TMEM lane quarter, half of the groups, lane = 4 g + m
-    uint32_t blocks;     // blocks done before this tile
-    uint32_t dw, da;     // slots used before this tile
-};
-
-// The blocks of one tile: NG 32-column groups of this warp.  The loads of the next group are in flight while one is scaled, across
-// blocks too, and a block's buffer is free when its last group has landed.
-template <int NG>
-__device__ __forceinline__ bool epi_blocks(const EpiState &s, int nb, float2 *acc, uint32_t *mask)
-{
-    uint32_t p[2][32];
-    auto buffer = [&](int j) { return s.taddr + ((s.blocks + j) % kAcc) * kTmemBuf; };
-    auto full = [&](int j) {
-        const uint32_t n = s.blocks + j;
-        const bool ok = warp_wait(s.B.acc_full(n % kAcc), (n / kAcc) & 1u, s.abort_flag);
-        tc_fence_after();
-        return ok;
-    };
-    auto load = [&](uint32_t *r, int j, int c) {
-        const uint32_t t = buffer(j) + 64u * c;
-        tc_ld16x32(t, r);
-        tc_ld16x32(t + (16u << 16), r + 16);
-    };
-    const float *sw = nullptr, *sa = nullptr;
-    if (!full(0)) return false;
-    load(p[0], 0, 0);
-    for (int j0 = 0; j0 < nb; j0 += 2) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int j = j0 + u;
-            if (u == 1 && j >= nb) break;
-            if ((j & 3) == 0) {  // the next four blocks' scales
-                const uint32_t d = s.da + (j >> 2);
-                if (!warp_wait(s.B.da_full(d % kDaSlots), (d / kDaSlots) & 1u, s.abort_flag)) return false;
-                sa = reinterpret_cast<const float *>(s.sm + OFF_DA + (d % kDaSlots) * kDaBytes) + 32 * s.h + 8 * s.m;
-                if ((j & 7) == 0) {
-                    const uint32_t w = s.dw + (j >> 3);
-                    if (!warp_wait(s.B.dw_full(w % kDwSlots), (w / kDwSlots) & 1u, s.abort_flag)) return false;
-                    sw = reinterpret_cast<const float *>(s.sm + OFF_DW + (w % kDwSlots) * kDwBytes) + 32 * s.q + 4 * s.g;
-                }
-                if (j + 4 >= nb) {
-                    const uint32_t *bits =
-                        reinterpret_cast<const uint32_t *>(s.sm + OFF_DA + (d % kDaSlots) * kDaBytes + kDaBlocks * BN * 4);
-#pragma unroll
-                    for (int c = 0; c < NG; ++c) mask[c] = bits[2 * c + s.h];
-                }
-            }
-            const float4 w4 = *reinterpret_cast<const float4 *>(sw + (j & 7) * BM);
-#pragma unroll
-            for (int c = 0; c < NG; ++c) {
-                const int step = u * NG + c;
-                uint32_t *now = p[step & 1], *next = p[(step + 1) & 1];
-                tc_wait_ld();
-                tc_regs16(now);
-                tc_regs16(now + 16);
-                if (c + 1 < NG) {
-                    load(next, j, c + 1);
-                } else {
-                    tc_fence_before();
-                    if ((s.g | s.m) == 0) arrive(s.B.acc_empty((s.blocks + j) % kAcc));
-                    if (j + 1 < nb) {
-                        if (!full(j + 1)) return false;
-                        load(next, j + 1, 0);
-                    }
-                }
-                const float4 a0 = *reinterpret_cast<const float4 *>(sa + (j & 3) * BN + 64 * c);
-                const float4 a1 = *reinterpret_cast<const float4 *>(sa + (j & 3) * BN + 64 * c + 4);
-                const float da[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-                epi_math(acc + 16 * c, now, da, w4.x, w4.y);
-                epi_math(acc + 16 * c + 8, now + 16, da, w4.z, w4.w);
-            }
-            if ((j & 3) == 3 || j == nb - 1) {
-                __syncwarp();
-                const uint32_t d = s.da + (j >> 2), w = s.dw + (j >> 3);
-                if ((s.g | s.m) == 0) {
-                    arrive(s.B.da_empty(d % kDaSlots));
-                    if ((j & 7) == 7 || j == nb - 1) arrive(s.B.dw_empty(w % kDwSlots));
-                }
-            }
-        }  // two blocks are an even number of groups: the next pair starts in p[0] again
-    }
-    return true;
+    for (int i = 0; i < 16; ++i)
+        acc[i] = __ffma2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                            make_float2(__uint_as_float(p[2 * i]), __uint_as_float(p[2 * i + 1])), acc[i]);
+    order16(acc);
 }
 
 // kPair: w and w2, the plane of silu(w x) * (w2 x); else w and f32 rows.  kTma: nb % 8 == 0.
 template <bool kPair, bool kTma>
 __global__ void __launch_bounds__(kThreads, 1)
 experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_constant__ CUtensorMap tmW,
-                     const __grid_constant__ CUtensorMap tmW2, const __grid_constant__ CUtensorMap tmB, int8_t *qs_out,
-                     uint32_t *ds_out)
+                     const __grid_constant__ CUtensorMap tmW2, int8_t *qs_out, uint32_t *ds_out)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = q8::smem_u32(smem_raw);
@@ -415,28 +340,32 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
         auto init = [&](int n, uint32_t count) {
             for (int k = 0; k < n; ++k) q8::mbar_init(b + i++, count);
         };
-        init(kRawSlots, 1);                  // raw_full: copied bytes
-        init(kRawSlots, kWidenThreads);      // raw_empty
-        init(kStages, kWidenThreads);        // a_full
-        init(kStages, 1);                    // b_full: copied bytes
-        init(kStages, 1);                    // ab_empty: tcgen05.commit
-        init(kDwSlots, kWidenThreads);       // dw_full
-        init(kDwSlots, kEpiWarps);           // dw_empty
-        init(kDaSlots, 1);                   // da_full
-        init(kDaSlots, kEpiWarps);           // da_empty
-        init(kAcc, 1);                       // acc_full: tcgen05.commit
-        init(kAcc, kEpiWarps);               // acc_empty
-        init(1, 1);                          // drain
+        init(kRawSlots, 1);           // raw_full: copied bytes
+        init(kRawSlots, 4);           // raw_empty: a warp each
+        init(kStages, 4);             // a_full
+        init(kStages, 4);             // b_full
+        init(kStages, 1);             // ab_empty: tcgen05.commit
+        init(kAcc, 1);                // acc_full: tcgen05.commit
+        init(kAcc, kEpiWarps);        // acc_empty
+        init(1, 1);                   // drain
         q8::fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(q8::smem_u32(tmem_slot)),
                      "r"(kTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    // of a scale operand's eight columns only the first is ever written
+    for (int i = tid; i < kScBytes / 16; i += kThreads) {
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(sm + OFF_ZERO + 16 * i) = zero;
+        for (int k = 0; k < 4 * kStages; ++k)
+            *reinterpret_cast<uint4 *>(sm + (k >> 2) * kStageBytes + OFF_DW + (k & 3) * kScBytes + 16 * i) = zero;
+    }
+    q8::fence_proxy_async_smem();
     q8::griddep_launch_dependents();
-    q8::griddep_wait();  // the offsets and the widened plane come from earlier kernels
+    q8::griddep_wait();  // the offsets and the plane come from earlier kernels
     {                    // row tiles before each expert: two experts a thread
         int n[2];
 #pragma unroll
@@ -468,168 +397,92 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    const int nb = a.nb, stages = (nb + 1) / 2, pieces = (nb + kPiece - 1) / kPiece, scales = (nb + kDaBlocks - 1) / kDaBlocks;
+    const int nb = a.nb, stages = (nb + 1) / 2, pieces = (nb + kPiece - 1) / kPiece;
     const int weight_tiles = kPair ? (a.n + 63) / 64 : (a.n + BM - 1) / BM;
-    const int64_t total = static_cast<int64_t>(cum[a.experts]) * weight_tiles;
+    const int total = cum[a.experts] * weight_tiles;  // below 2^31: y would not fit otherwise
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsCtl>();
         if (warp == 0) {
-            // ------------------------------------------------------------ activations
-            uint32_t n = 0;  // stages issued
-            bool ok = true;
-            for (int64_t at = blockIdx.x; at < total && ok; at += gridDim.x) {
-                const Tile t = tile_at(a, cum, weight_tiles, at);
-                int4 src[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    int r[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = 4 * (lane + 32 * k) + i;
-                        const int64_t s = q8::source_row(a, t.row0 + min(c, t.rows - 1));
-                        r[i] = s < 0 ? 0 : static_cast<int>(s);  // a row out of range: any, it is not stored
-                    }
-                    src[k] = make_int4(r[0], r[1], r[2], r[3]);
-                }
-                for (int s = 0; s < stages; ++s, ++n) {
-                    const int slot = n % kStages;
-                    ok = warp_wait(B.ab_empty(slot), ((n / kStages) & 1u) ^ 1u, abort_flag);
-                    if (!ok) break;
-                    if (lane == 0) expect_tx(B.b_full(slot), t.groups * kGroup * 128);
-                    __syncwarp();
-                    const uint32_t dst = base + OFF_B + slot * kBBytes;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        if (lane + 32 * k < t.groups * (kGroup / 4))
-                            tma_gather4(dst + 512 * (lane + 32 * k), &tmB, 64 * s, src[k], B.b_full(slot));
-                }
-            }
-            if (lane == 0)  // the last stages issued must have landed before the CTA exits
-                for (uint32_t s = n < kStages ? 0 : n - kStages; s < n; ++s) drain_bar(B.b_full(s % kStages), (s / kStages) & 1u);
-        } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issuer
-            if (lane == 0) {
-                uint32_t n = 0, blk = 0;
-                bool ok = true;
-                for (int64_t at = blockIdx.x; at < total && ok; at += gridDim.x) {
-                    const Tile t = tile_at(a, cum, weight_tiles, at);
-                    const uint32_t idesc = mma_desc(t.groups * kGroup);
-                    for (int j = 0; j < nb; ++j, ++blk) {
-                        const int slot = n % kStages;
-                        if ((j & 1) == 0) {
-                            ok = wait_bar(B.b_full(slot), (n / kStages) & 1u, abort_flag) &&
-                                 wait_bar(B.a_full(slot), (n / kStages) & 1u, abort_flag);
-                            if (!ok) break;
-                        }
-                        ok = wait_bar(B.acc_empty(blk % kAcc), ((blk / kAcc) & 1u) ^ 1u, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t d = tmem + (blk % kAcc) * kTmemBuf;
-                        const uint32_t pa = base + OFF_A + slot * kABytes + 64 * (j & 1);
-                        const uint32_t pb = base + OFF_B + slot * kBBytes + 64 * (j & 1);
-                        tc_mma_f16(d, smem_desc(pa), smem_desc(pb), idesc, 0);
-                        tc_mma_f16(d, smem_desc(pa + 32), smem_desc(pb + 32), idesc, 1);
-                        tc_commit(B.acc_full(blk % kAcc));
-                        if ((j & 1) || j == nb - 1) {
-                            tc_commit(B.ab_empty(slot));
-                            ++n;
-                        }
-                    }
-                }
-                // every MMA must have completed before its operands and TMEM go
-                tc_commit(B.drain());
-                drain_bar(B.drain(), 0);
-            }
-        } else if (warp == 2) {
-            // ------------------------------------------------------------ weights
-            if (kTma) {
-                uint32_t n = 0;
-                bool ok = true;
-                for (int64_t at = blockIdx.x; at < total && ok; at += gridDim.x) {
-                    const Tile t = tile_at(a, cum, weight_tiles, at);
-                    const int row = t.e * a.n + tile_row<kPair>(t.nt, 16 * lane);
-                    for (int s = 0; s < pieces; ++s, ++n) {
-                        const int slot = n % kRawSlots;
-                        ok = warp_wait(B.raw_empty(slot), ((n / kRawSlots) & 1u) ^ 1u, abort_flag);
-                        if (!ok) break;
-                        if (lane == 0) expect_tx(B.raw_full(slot), BM * kPitchTma);
-                        __syncwarp();
-                        if (lane < 8)  // 16 rows each
-                            q8::tma_load_2d(base + OFF_RAW + slot * kRawBytes + lane * 16 * kPitchTma,
-                                            kPair && (lane & 1) ? &tmW2 : &tmW, kPitchTma / 2 * s, row, B.raw_full(slot));
-                    }
-                }
-                if (lane == 0)
-                    for (uint32_t s = n < kRawSlots ? 0 : n - kRawSlots; s < n; ++s)
-                        drain_bar(B.raw_full(s % kRawSlots), (s / kRawSlots) & 1u);
-            }
-        } else {
-            // ------------------------------------------------------------ activation scales
-            uint32_t n = 0;
-            bool ok = true, bad = false;
-            for (int64_t at = blockIdx.x; at < total && ok; at += gridDim.x) {
+            uint32_t n = 0, blk = 0;  // stages and blocks done
+            bool ok = true;
+            for (int at = blockIdx.x; at < total && ok; at += gridDim.x) {
                 const Tile t = tile_at(a, cum, weight_tiles, at);
-                const uint32_t *src[2 * kMaxGroups];
-                uint32_t valid[2 * kMaxGroups];
-#pragma unroll
-                for (int i = 0; i < 2 * kMaxGroups; ++i) {
-                    const int c = lane + 32 * i;
-                    const int64_t s = c < t.rows ? q8::source_row(a, t.row0 + c) : -1;
-                    bad |= c < t.rows && s < 0;
-                    valid[i] = __ballot_sync(Q8_FULL_MASK, s >= 0);
-                    src[i] = a.ds + (s < 0 ? 0 : s) * nb;
-                }
-                for (int s = 0; s < scales; ++s, ++n) {
-                    const int slot = n % kDaSlots;
-                    ok = warp_wait(B.da_empty(slot), ((n / kDaSlots) & 1u) ^ 1u, abort_flag);
+                const uint32_t idesc = mma_desc(t.groups * kGroup);
+                for (int j = 0; j < nb; ++j, ++blk) {
+                    const int slot = n % kStages, u = j & 1;
+                    if (u == 0) {
+                        ok = warp_wait(B.a_full(slot), (n / kStages) & 1u, abort_flag) &&
+                             warp_wait(B.b_full(slot), (n / kStages) & 1u, abort_flag);
+                        if (!ok) break;
+                    }
+                    ok = warp_wait(B.acc_empty(blk % kAcc), ((blk / kAcc) & 1u) ^ 1u, abort_flag);
                     if (!ok) break;
-                    float *dst = reinterpret_cast<float *>(sm + OFF_DA + slot * kDaBytes);
-#pragma unroll
-                    for (int i = 0; i < 2 * kMaxGroups; ++i)
-                        if (i < 2 * t.groups) {
-                            const int c = da_slot(lane + 32 * i);
-                            uint32_t w[kDaBlocks];
-                            if (nb % kDaBlocks == 0) {
-                                const uint4 v = *reinterpret_cast<const uint4 *>(src[i] + kDaBlocks * s);
-                                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < kDaBlocks; ++k) w[k] = kDaBlocks * s + k < nb ? src[i][kDaBlocks * s + k] : 0u;
-                            }
-#pragma unroll
-                            for (int k = 0; k < kDaBlocks; ++k)
-                                dst[k * BN + c] = __half2float(__ushort_as_half(static_cast<unsigned short>(w[k] & 0xffffu)));
-                        }
-                    if (lane < 2 * kMaxGroups) {
-                        uint32_t v = valid[0];
-#pragma unroll
-                        for (int i = 1; i < 2 * kMaxGroups; ++i) v = lane == i ? valid[i] : v;
-                        reinterpret_cast<uint32_t *>(dst + kDaBlocks * BN)[lane] = v;
+                    tc_fence_after();
+                    const uint32_t d = tmem + (blk % kAcc) * kTmemBuf, stage = base + slot * kStageBytes;
+                    const uint64_t pa = smem_desc(stage + 64 * u), pb = smem_desc(stage + OFF_B + 64 * u);
+                    const uint64_t sa = scale_desc(stage + OFF_DW + u * kScBytes, base + OFF_ZERO);
+                    const uint64_t sb = scale_desc(stage + OFF_DA + u * kScBytes, base + OFF_ZERO);
+                    const bool last = u || j == nb - 1;
+                    if (elect_one()) {
+                        tc_mma_f16(d, pa, pb, idesc, 0);
+                        tc_mma_f16(d, pa + 2, pb + 2, idesc, 1);  // 32 bytes on
+                        tc_mma_f16(d + BN, sa, sb, idesc, 0);
+                        tc_commit(B.acc_full(blk % kAcc));
+                        if (last) tc_commit(B.ab_empty(slot));
                     }
                     __syncwarp();
-                    if (lane == 0) arrive(B.da_full(slot));
+                    n += last;
                 }
             }
-            if (bad) atomicOr(&g_tiles_err, q8::kErrData);
+            // every MMA must have completed before its operands and TMEM go
+            if (elect_one()) tc_commit(B.drain());
+            __syncwarp();
+            drain_bar(B.drain(), 0);
+        } else if (warp == 1 && kTma) {
+            // ------------------------------------------------------------ weights
+            uint32_t n = 0;
+            bool ok = true;
+            for (int at = blockIdx.x; at < total && ok; at += gridDim.x) {
+                const Tile t = tile_at(a, cum, weight_tiles, at);
+                const int row = t.e * a.n + tile_row<kPair>(t.nt, 0);
+                for (int s = 0; s < pieces; ++s, ++n) {
+                    const int slot = n % kRawSlots;
+                    ok = warp_wait(B.raw_empty(slot), ((n / kRawSlots) & 1u) ^ 1u, abort_flag);
+                    if (!ok) break;
+                    const uint32_t dst = base + OFF_RAW + slot * kRawBytes;
+                    if (elect_one()) {
+                        expect_tx(B.raw_full(slot), BM * kPitchTma);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)  // 32 rows each
+                            q8::tma_load_2d(dst + i * 32 * kPitchTma, kPair && (i & 1) ? &tmW2 : &tmW, kPitchTma / 2 * s,
+                                            row + (kPair ? 32 * (i >> 1) : 32 * i), B.raw_full(slot));
+                    }
+                    __syncwarp();
+                }
+            }
+            // the last copies must have landed before the CTA exits
+            for (uint32_t s = n < kRawSlots ? 0 : n - kRawSlots; s < n; ++s)
+                drain_bar(B.raw_full(s % kRawSlots), (s / kRawSlots) & 1u);
         }
     } else if (warp < 8) {
         setmaxnreg_dec<kRegsWiden>();
         // ---------------------------------------------------------------- widen weights: a row a thread
         const int r = tid - 128;
-        const int sw = r & 7, dslot = dw_slot(r);
+        const int sw = r & 7;
         uint32_t n = 0, p = 0;  // stages and pieces done
         bool ok = true;
         // the part of piece s of a tile's rows that this warp widens, 4 bytes a copy (rows of blocks that are not 16-byte aligned)
         auto copy = [&](const Tile &t, int s, uint32_t to) {
             if (kTma) return;
             const int cb = min(kPiece, nb - s * kPiece);
+            const uint8_t *w = kPair && (warp & 1) ? a.w2 : a.w;
+            const int64_t most = static_cast<int64_t>(a.experts) * a.n * nb * 34;
             for (int k = 0; k < 32; ++k) {
                 const int pos = 32 * (warp - 4) + k;
                 const int64_t row = static_cast<int64_t>(t.e) * a.n + min(tile_row<kPair>(t.nt, pos), a.n - 1);
-                const uint8_t *w = kPair && (pos & 16) ? a.w2 : a.w;
                 const int64_t from = (row * nb + s * kPiece) * 34, end = from + cb * 34;
-                const int64_t most = static_cast<int64_t>(a.experts) * a.n * nb * 34;
                 for (int64_t o = (from & ~int64_t(3)) + 4 * lane; o < end; o += 128)
                     cp_async4(base + OFF_RAW + (to % kRawSlots) * kRawBytes + pos * kPitchAny +
                                   static_cast<uint32_t>(o - (from & ~int64_t(3))),
@@ -637,21 +490,24 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
             }
             cp_async_commit();
         };
-        int64_t at = blockIdx.x;
+        int at = blockIdx.x;
         Tile t = {}, tn = {};
-        if (at < total) {
+        if (!kTma && at < total) {
             tn = tile_at(a, cum, weight_tiles, at);
             copy(tn, 0, 0);
         }
         for (; at < total && ok; at += gridDim.x) {
-            t = tn;
-            if (at + gridDim.x < total) tn = tile_at(a, cum, weight_tiles, at + gridDim.x);
+            if (!kTma) {
+                t = tn;
+                if (at + gridDim.x < total) tn = tile_at(a, cum, weight_tiles, at + gridDim.x);
+            }
             const int64_t row = static_cast<int64_t>(t.e) * a.n + min(tile_row<kPair>(t.nt, r), a.n - 1);
             for (int s = 0; s < pieces && ok; ++s, ++p) {
-                const int slot = p % kRawSlots, dws = p % kDwSlots;
+                const int slot = p % kRawSlots;
                 const uint8_t *raw = sm + OFF_RAW + slot * kRawBytes;
                 if (kTma) {
-                    ok = wait_bar(B.raw_full(slot), (p / kRawSlots) & 1u, abort_flag);
+                    ok = warp_wait(B.raw_full(slot), (p / kRawSlots) & 1u, abort_flag);
+                    if (!ok) break;
                 } else {
                     // the next piece's copies in flight while this one is widened
                     if (s + 1 < pieces)
@@ -663,17 +519,15 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     cp_async_wait<1>();
                     __syncwarp();
                 }
-                ok = ok && wait_bar(B.dw_empty(dws), ((p / kDwSlots) & 1u) ^ 1u, abort_flag);
-                if (!ok) break;
-                float *dw = reinterpret_cast<float *>(sm + OFF_DW + dws * kDwBytes) + dslot;
                 const int cb = min(kPiece, nb - s * kPiece);
 #pragma unroll
                 for (int k = 0; k < kPiece / 2; ++k) {
                     if (!kTma && 2 * k >= cb) break;
                     const int st = n % kStages;
-                    ok = wait_bar(B.ab_empty(st), ((n / kStages) & 1u) ^ 1u, abort_flag);
+                    ok = warp_wait(B.ab_empty(st), ((n / kStages) & 1u) ^ 1u, abort_flag);
                     if (!ok) break;
-                    uint8_t *out = sm + OFF_A + st * kABytes + r * 128;
+                    uint8_t *out = sm + st * kStageBytes + r * 128;
+                    uint16_t *dw = reinterpret_cast<uint16_t *>(sm + st * kStageBytes + OFF_DW + r * 16);
                     if (kTma) {
                         uint32_t W[20];  // 68 bytes from word 17 k on
 #pragma unroll
@@ -681,8 +535,8 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                             const uint4 v = *reinterpret_cast<const uint4 *>(raw + r * kPitchTma + 64 * k + 16 * i);
                             W[4 * i] = v.x, W[4 * i + 1] = v.y, W[4 * i + 2] = v.z, W[4 * i + 3] = v.w;
                         }
-                        dw[(2 * k) * BM] = __half2float(__ushort_as_half(static_cast<unsigned short>(W[k] & 0xffffu)));
-                        dw[(2 * k + 1) * BM] = __half2float(__ushort_as_half(static_cast<unsigned short>(W[k + 8] >> 16)));
+                        dw[0] = static_cast<uint16_t>(W[k]);
+                        dw[kScBytes / 2] = static_cast<uint16_t>(W[k + 8] >> 16);
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
                             uint4 o;
@@ -708,8 +562,7 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                             uint32_t W[9];
 #pragma unroll
                             for (int i = 0; i < 9; ++i) W[i] = there ? src[i] : 0u;
-                            dw[(2 * k + b) * BM] =
-                                __half2float(__ushort_as_half(static_cast<unsigned short>(odd ? W[0] >> 16 : W[0] & 0xffffu)));
+                            dw[b * (kScBytes / 2)] = static_cast<uint16_t>(odd ? W[0] >> 16 : W[0]);
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
                                 uint4 o;
@@ -720,213 +573,234 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                         }
                     }
                     q8::fence_proxy_async_smem();
-                    arrive(B.a_full(st));
+                    __syncwarp();
+                    if (lane == 0) arrive(B.a_full(st));
                     ++n;
                 }
                 if (!ok) break;
-                arrive(B.dw_full(dws));
-                if (kTma)
-                    arrive(B.raw_empty(slot));
-                else
-                    __syncwarp();  // the warp's next copies overwrite what its lanes have read
+                __syncwarp();  // the slot may be written again: by the copies of this warp, or once all four are done
+                if (kTma && lane == 0) arrive(B.raw_empty(slot));
             }
         }
         if (!kTma) cp_async_wait<0>();
+    } else if (warp < 12) {
+        setmaxnreg_dec<kRegsWiden>();
+        // ---------------------------------------------------------------- activations
+        // lane 4 r + c has 16 codes (chunk c of two blocks) of the columns 32 w + r + 8 i, i < 4, and the scales of column
+        // 32 w + r + 8 c; the next stage's loads are in flight while one is widened
+        const int c = lane & 3, r = lane >> 2, col = 32 * (warp - 8) + r;
+        uint32_t n = 0;
+        bool ok = true, bad = false;
+        const uint4 *src[4];
+        const uint32_t *sds = nullptr;
+        int at = blockIdx.x;
+        int groups = 0;
+        auto locate = [&](int where) {
+            const Tile t = tile_at(a, cum, weight_tiles, where);
+            groups = t.groups;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                int64_t x = q8::source_row(a, t.row0 + min(col + 8 * i, t.rows - 1));
+                bad |= x < 0;
+                x = max(x, int64_t(0));  // a row out of range: any, it is not stored
+                src[i] = reinterpret_cast<const uint4 *>(a.qs) + x * (2 * nb) + c;
+                if (i == c) sds = a.ds + x * nb;
+            }
+        };
+        uint4 v[4];
+        uint32_t d0 = 0, d1 = 0;
+        auto load = [&](int s) {
+            const bool two = 2 * s + 1 < nb;
+            if (32 * (warp - 8) >= groups * kGroup) return;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = two || c < 2 ? __ldg(src[i] + 4 * s) : make_uint4(0u, 0u, 0u, 0u);
+            d0 = __ldg(sds + 2 * s);
+            d1 = two ? __ldg(sds + 2 * s + 1) : 0u;
+        };
+        if (at < total) {
+            locate(at);
+            load(0);
+        }
+        for (; at < total && ok; at += gridDim.x) {
+            for (int s = 0; s < stages; ++s, ++n) {
+                const int st = n % kStages;
+                ok = warp_wait(B.ab_empty(st), ((n / kStages) & 1u) ^ 1u, abort_flag);
+                if (!ok) break;
+                const uint4 w[4] = {v[0], v[1], v[2], v[3]};
+                const uint32_t e0 = d0, e1 = d1;
+                const bool mine = 32 * (warp - 8) < groups * kGroup;
+                if (s + 1 < stages) {
+                    load(s + 1);
+                } else if (at + gridDim.x < total) {
+                    locate(at + gridDim.x);
+                    load(0);
+                }
+                if (mine) {
+                    uint8_t *out = sm + st * kStageBytes + OFF_B;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = col + 8 * i;  // row % 8 == r
+                        uint4 o0, o1;
+                        q8::i8x4_to_f16x4(w[i].x, o0.x, o0.y);
+                        q8::i8x4_to_f16x4(w[i].y, o0.z, o0.w);
+                        q8::i8x4_to_f16x4(w[i].z, o1.x, o1.y);
+                        q8::i8x4_to_f16x4(w[i].w, o1.z, o1.w);
+                        *reinterpret_cast<uint4 *>(out + row * 128 + 16 * ((2 * c) ^ r)) = o0;
+                        *reinterpret_cast<uint4 *>(out + row * 128 + 16 * ((2 * c + 1) ^ r)) = o1;
+                    }
+                    uint16_t *da = reinterpret_cast<uint16_t *>(sm + st * kStageBytes + OFF_DA + (col + 8 * c) * 16);
+                    da[0] = static_cast<uint16_t>(e0);
+                    da[kScBytes / 2] = static_cast<uint16_t>(e1);
+                    q8::fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) arrive(B.b_full(st));
+            }
+        }
+        if (bad) atomicOr(&g_tiles_err, q8::kErrData);
     } else {
         setmaxnreg_inc<kRegsEpi>();
         // ---------------------------------------------------------------- epilogue
-        EpiState s;
-        s.sm = sm, s.B = B, s.abort_flag = abort_flag;
-        s.q = warp & 3, s.h = (warp - 8) >> 2, s.g = lane >> 2, s.m = lane & 3;
-        s.taddr = tmem + (static_cast<uint32_t>(32 * s.q) << 16) + 32u * s.h;
-        s.blocks = s.dw = s.da = 0;
-        bool ok = true;
-        for (int64_t at = blockIdx.x; at < total; at += gridDim.x) {
+        const int q = warp & 3, h = (warp - 12) >> 2;  // lanes 32 q .., columns 64 h ..
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + 64u * h;
+        uint32_t blk = 0;
+        for (int at = blockIdx.x; at < total; at += gridDim.x) {
             const Tile t = tile_at(a, cum, weight_tiles, at);
-            // values of this thread: rows 32 q + 16 sub + g + 8 e, columns 32 (2c + h) + 8 rep + 2 m + {0, 1}, in
-            // acc[16 c + 8 sub + 2 rep + e]
-            float2 acc[16 * kMaxGroups];
-            uint32_t mask[kMaxGroups];
+            const bool mine = h < t.groups;
+            float2 acc[32];  // columns 64 h + 2 i, + 1 of position 32 q + lane
+            bool ok = true;
 #pragma unroll
-            for (int i = 0; i < 16 * kMaxGroups; ++i) acc[i] = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < kMaxGroups; ++i) mask[i] = 0u;
-            if (t.groups == 2)
-                ok = epi_blocks<2>(s, nb, acc, mask);
-            else
-                ok = epi_blocks<1>(s, nb, acc, mask);
-            tc_wait_ld();  // none left, unless a wait ran out
-            s.blocks += nb, s.dw += pieces, s.da += scales;
+            for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+            for (int j = 0; j < nb; ++j, ++blk) {
+                ok = warp_wait(B.acc_full(blk % kAcc), (blk / kAcc) & 1u, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                if (mine) {
+                    const uint32_t buf = taddr + (blk % kAcc) * kTmemBuf;
+                    epi_half(buf, acc);
+                    epi_half(buf + 32, acc + 16);
+                }
+                tc_fence_before();
+                if (lane == 0) arrive(B.acc_empty(blk % kAcc));
+            }
             ok = __all_sync(Q8_FULL_MASK, ok && !*abort_flag);
+            auto valid = [&](int c0) {  // of the 32 columns from c0 on
+                return __ballot_sync(Q8_FULL_MASK, c0 + lane < t.rows && q8::source_row(a, t.row0 + c0 + lane) >= 0);
+            };
             if (!kPair) {
                 if (!ok) break;
+                if (!mine) continue;
+                const int row = BM * t.nt + 32 * q + lane;
+                const uint32_t m[2] = {valid(64 * h), valid(64 * h + 32)};
+                float *out = a.out + static_cast<int64_t>(t.row0 + 64 * h) * a.ld + row;
+                if (row < a.n) {
 #pragma unroll
-                for (int c = 0; c < kMaxGroups; ++c) {
-                    if (c >= t.groups) break;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int sub = i >> 3, rep = (i >> 1) & 3, e = i & 1;
-                        const int row = BM * t.nt + 32 * s.q + 16 * sub + s.g + 8 * e;
-                        if (row >= a.n) continue;
-                        const int bit = 8 * rep + 2 * s.m, col = 32 * (2 * c + s.h) + bit;
-                        float *out = a.out + static_cast<int64_t>(t.row0 + col) * a.ld + row;
-                        const float2 v = acc[16 * c + i];
-                        if ((mask[c] >> bit) & 1u) out[0] = v.x;
-                        if ((mask[c] >> (bit + 1)) & 1u) out[a.ld] = v.y;
+                    for (int i = 0; i < 32; ++i) {
+                        if ((m[i >> 4] >> (2 * i & 31)) & 1u) *out = acc[i].x;
+                        out += a.ld;
+                        if ((m[i >> 4] >> ((2 * i & 31) + 1)) & 1u) *out = acc[i].y;
+                        out += a.ld;
+                        asm volatile("" : "+l"(out));  // one address after the other: all at once would not fit beside acc
                     }
                 }
             } else {
-                float *amax = reinterpret_cast<float *>(sm + OFF_AMAX);
-                uint8_t *codes = sm + OFF_CODES;
-                uint32_t *smask = reinterpret_cast<uint32_t *>(sm + OFF_MASK);
                 if (epi_any(!ok)) break;  // all of them, so that none waits for another below
-                // silu(gate) * up into acc[16 c + 2 rep + e]; the block's largest value: over e, g, and the warp of the other 16
-                // channels through shared memory
+                // warp q even has 32 gate channels, q odd the same up channels, of 64 columns: even keeps the first 32 columns
+                const int up = q & 1;
+                float *box = reinterpret_cast<float *>(sm + OFF_SWAP) + (warp - 12) * 512 + lane;
+                const float *from = reinterpret_cast<float *>(sm + OFF_SWAP) + ((warp - 12) ^ 1) * 512 + lane;
+                float v[32];
 #pragma unroll
-                for (int c = 0; c < kMaxGroups; ++c) {
-                    if (c >= t.groups) break;
+                for (int x = 0; x < 2; ++x) {
+                    if (mine) {
 #pragma unroll
-                    for (int rep = 0; rep < 4; ++rep) {
-                        float2 most = make_float2(0.0f, 0.0f);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float2 &g = acc[16 * c + 2 * rep + e];
-                            const float2 u = acc[16 * c + 8 + 2 * rep + e];
-                            g.x = q8::silu_mul(g.x, u.x), g.y = q8::silu_mul(g.y, u.y);
-                            most.x = fmaxf(most.x, fabsf(g.x)), most.y = fmaxf(most.y, fabsf(g.y));
-                        }
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) {
-                            most.x = fmaxf(most.x, __shfl_xor_sync(Q8_FULL_MASK, most.x, o));
-                            most.y = fmaxf(most.y, __shfl_xor_sync(Q8_FULL_MASK, most.y, o));
-                        }
-                        if (s.g == 0)
-                            *reinterpret_cast<float2 *>(amax + s.q * BN + 32 * (2 * c + s.h) + 8 * rep + 2 * s.m) = most;
-                    }
-                    if (s.q == 0 && lane == 0) smask[2 * c + s.h] = mask[c];
-                }
-                epi_sync();
-#pragma unroll
-                for (int c = 0; c < kMaxGroups; ++c) {
-                    if (c >= t.groups) break;
-#pragma unroll
-                    for (int rep = 0; rep < 4; ++rep) {
-                        const int col = 32 * (2 * c + s.h) + 8 * rep + 2 * s.m;
-                        const float *other = amax + (s.q & ~1) * BN + col;
-                        const float2 m0 = *reinterpret_cast<const float2 *>(other), m1 = *reinterpret_cast<const float2 *>(other + BN);
-                        const float ix = q8::q8_block_di(q8::q8_block_d(fmaxf(m0.x, m1.x)));
-                        const float iy = q8::q8_block_di(q8::q8_block_d(fmaxf(m0.y, m1.y)));
-                        // channel 16 q + g + 8 e of column col: 16-byte chunks swizzled by (col / 2) % 4 = m
-                        uint8_t *o = codes + col * 64 + 16 * (s.q ^ s.m) + s.g;
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float2 v = acc[16 * c + 2 * rep + e];
-                            o[8 * e] = static_cast<uint8_t>(q8::q8_code(v.x, ix));
-                            o[64 + 8 * e] = static_cast<uint8_t>(q8::q8_code(v.y, iy));
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 g = acc[8 * x + i], u = acc[16 + 8 * x + i];  // this and the other half's columns
+                            box[32 * (2 * i)] = up ? g.x : u.x;
+                            box[32 * (2 * i + 1)] = up ? g.y : u.y;
                         }
                     }
+                    epi_sync();
+                    if (mine) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 g = acc[8 * x + (i >> 1)], u = acc[16 + 8 * x + (i >> 1)];
+                            const float own = up ? (i & 1 ? u.y : u.x) : (i & 1 ? g.y : g.x), other = from[32 * i];
+                            v[16 * x + i] = up ? q8::silu_mul(other, own) : q8::silu_mul(own, other);
+                        }
+                    }
+                    if (x == 0) epi_sync();
                 }
-                epi_sync();
-                // a thread per (row, block of 32 channels)
-                for (int i = tid - 256; i < 2 * t.rows; i += kEpiThreads) {
-                    const int col = i >> 1, blk = i & 1, ch = 64 * t.nt + 32 * blk;
-                    if (ch >= a.n || !((smask[col >> 5] >> (col & 31)) & 1u)) continue;
-                    const int sz = (col >> 1) & 3;
-                    const uint4 v0 = *reinterpret_cast<const uint4 *>(codes + col * 64 + 16 * ((2 * blk) ^ sz));
-                    const uint4 v1 = *reinterpret_cast<const uint4 *>(codes + col * 64 + 16 * ((2 * blk + 1) ^ sz));
-                    int sum = q8::dp4a(v0.x, 0x01010101u, 0);
-                    sum = q8::dp4a(v0.y, 0x01010101u, sum), sum = q8::dp4a(v0.z, 0x01010101u, sum);
-                    sum = q8::dp4a(v0.w, 0x01010101u, sum), sum = q8::dp4a(v1.x, 0x01010101u, sum);
-                    sum = q8::dp4a(v1.y, 0x01010101u, sum), sum = q8::dp4a(v1.z, 0x01010101u, sum);
-                    sum = q8::dp4a(v1.w, 0x01010101u, sum);
-                    const float d = q8::q8_block_d(fmaxf(amax[(2 * blk) * BN + col], amax[(2 * blk + 1) * BN + col]));
-                    const int64_t row = t.row0 + col;
-                    uint4 *o = reinterpret_cast<uint4 *>(qs_out + row * a.n + ch);
-                    o[0] = v0, o[1] = v1;
-                    ds_out[row * (a.n >> 5) + (ch >> 5)] = q8::q8_dsword(d, sum);
+                if (!mine) continue;
+                const int c0 = 64 * h + 32 * up, ch = 64 * t.nt + 32 * (q >> 1);
+                const uint32_t m = valid(c0);
+                if (ch >= a.n) continue;
+                // lane i encodes column c0 + i's block: its largest value (NaN does not count), then its scale
+                uint32_t most = 0u;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const uint32_t b = __float_as_uint(fabsf(v[i]));
+                    const uint32_t top = __reduce_max_sync(Q8_FULL_MASK, b > 0x7f800000u ? 0u : b);
+                    if (lane == i) most = top;
                 }
+                const float d = q8::q8_block_d(__uint_as_float(most)), di = q8::q8_block_di(d);
+                int sum = 0;
+                int8_t *out = qs_out + static_cast<int64_t>(t.row0 + c0) * a.n + ch + lane;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int code = q8::q8_code(v[i], __shfl_sync(Q8_FULL_MASK, di, i));
+                    const int total_i = __reduce_add_sync(Q8_FULL_MASK, code);
+                    if (lane == i) sum = total_i;
+                    if ((m >> i) & 1u) *out = static_cast<int8_t>(code);
+                    out += a.n;
+                    asm volatile("" : "+l"(out));
+                }
+                if ((m >> lane) & 1u)
+                    ds_out[static_cast<int64_t>(t.row0 + c0 + lane) * (a.n >> 5) + (ch >> 5)] = q8::q8_dsword(d, sum);
             }
         }
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == 0) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }
 }
 
-// The plane's codes as f16, 16 a thread and round.
-__global__ void __launch_bounds__(256)
-experts_widen_plane_kernel(const uint4 *__restrict__ qs, int64_t chunks, uint4 *__restrict__ out)
-{
-    q8::griddep_launch_dependents();
-    q8::griddep_wait();
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < chunks; i += stride) {
-        const uint4 v = __ldg(qs + i);
-        uint4 o0, o1;
-        q8::i8x4_to_f16x4(v.x, o0.x, o0.y);
-        q8::i8x4_to_f16x4(v.y, o0.z, o0.w);
-        q8::i8x4_to_f16x4(v.z, o1.x, o1.y);
-        q8::i8x4_to_f16x4(v.w, o1.z, o1.w);
-        out[2 * i] = o0;
-        out[2 * i + 1] = o1;
-    }
-}
-
 template <bool kPair, bool kTma>
-int launch(const q8::ExpertsArgs &a, const CUtensorMap &mw, const CUtensorMap &mw2, const CUtensorMap &mb, unsigned grid,
+int launch(const q8::ExpertsArgs &a, const CUtensorMap &mw, const CUtensorMap &mw2, unsigned grid,
            int8_t *qs_out, uint32_t *ds_out, int slot, cudaStream_t s)
 {
     if (!q8::set_max_dynamic_smem(reinterpret_cast<const void *>(experts_tiles_kernel<kPair, kTma>), kSmemBytes, slot))
         return Q8_ERR_LAUNCH;
-    return q8::launch_pdl(experts_tiles_kernel<kPair, kTma>, dim3(grid), dim3(kThreads), kSmemBytes, s, a, mw, mw2, mb, qs_out,
-                          ds_out);
+    return q8::launch_pdl(experts_tiles_kernel<kPair, kTma>, dim3(grid), dim3(kThreads), kSmemBytes, s, a, mw, mw2, qs_out, ds_out);
 }
 
 } // namespace
 
 namespace q8 {
 
-int64_t experts_tiles_rows(int64_t plane_rows, bool gather, int64_t pairs)
+int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out, cudaStream_t s)
 {
-    return gather || plane_rows < pairs ? plane_rows : pairs;
-}
-
-size_t experts_tiles_workspace(int64_t k, int64_t plane_rows, bool gather, int64_t pairs)
-{
-    return static_cast<size_t>(experts_tiles_rows(plane_rows, gather, pairs)) * k * 2;
-}
-
-int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out, void *workspace, cudaStream_t s)
-{
-    const int64_t k = 32 * static_cast<int64_t>(a.nb), rows = experts_tiles_rows(a.plane_rows, a.rows != nullptr, a.pairs);
     const bool pair = a.w2 != nullptr, tma = a.nb % kPiece == 0;
-    CUtensorMap mw = {}, mw2 = {}, mb = {};
+    CUtensorMap mw = {}, mw2 = {};
     const uint64_t wrows = static_cast<uint64_t>(a.experts) * a.n, pitch = static_cast<uint64_t>(a.nb) * 34;
-    if (tma && (!make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.w, pitch / 2, wrows, pitch, kPitchTma / 2, 16,
+    if (tma && (!make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.w, pitch / 2, wrows, pitch, kPitchTma / 2, 32,
                              CU_TENSOR_MAP_SWIZZLE_NONE) ||
-                (pair && !make_map_2d(&mw2, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.w2, pitch / 2, wrows, pitch, kPitchTma / 2, 16,
+                (pair && !make_map_2d(&mw2, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.w2, pitch / 2, wrows, pitch, kPitchTma / 2, 32,
                                       CU_TENSOR_MAP_SWIZZLE_NONE))))
         return Q8_ERR_LAUNCH;
-    if (!make_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT16, workspace, static_cast<uint64_t>(k), static_cast<uint64_t>(rows),
-                     static_cast<uint64_t>(k) * 2, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B))
-        return Q8_ERR_LAUNCH;
-    const int64_t chunks = rows * (k / 16), ctas = (chunks + 255) / 256;
     const int sms = device_sm_count();
-    const int64_t cap = static_cast<int64_t>(sms) * 8;
-    int st = launch_pdl(experts_widen_plane_kernel, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(256), 0, s,
-                        reinterpret_cast<const uint4 *>(a.qs), chunks, static_cast<uint4 *>(workspace));
-    if (st != Q8_OK) return st;
     const int64_t weight_tiles = pair ? (a.n + 63) / 64 : (a.n + BM - 1) / BM;
     const int64_t most = (a.pairs / BN + (a.experts < a.pairs ? a.experts : a.pairs)) * weight_tiles;
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
-    if (pair) return tma ? launch<true, true>(a, mw, mw2, mb, grid, qs_out, ds_out, 48, s)
-                         : launch<true, false>(a, mw, mw2, mb, grid, qs_out, ds_out, 49, s);
-    return tma ? launch<false, true>(a, mw, mw2, mb, grid, qs_out, ds_out, 50, s)
-               : launch<false, false>(a, mw, mw2, mb, grid, qs_out, ds_out, 51, s);
+    if (pair) return tma ? launch<true, true>(a, mw, mw2, grid, qs_out, ds_out, 48, s)
+                         : launch<true, false>(a, mw, mw2, grid, qs_out, ds_out, 49, s);
+    return tma ? launch<false, true>(a, mw, mw2, grid, qs_out, ds_out, 50, s)
+               : launch<false, false>(a, mw, mw2, grid, qs_out, ds_out, 51, s);
 }
 
 unsigned int *experts_tiles_error_word()

@@ -99,7 +99,8 @@ q8::ExpertsArgs args_of(const void *w, const void *w2, int64_t experts, int64_t 
 extern "C" size_t q8_0_experts_gemm_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t plane_rows,
                                                     int64_t top_k, int64_t pairs)
 {
-    return 0;
+    if (!sizes_ok(experts, n, k, plane_rows, top_k, pairs) || !many_rows(experts, pairs)) return 0;
+    return q8::experts_tiles_workspace(k, pairs);
 }
 
 extern "C" int q8_0_experts_gemm(const void *w, int64_t experts, int64_t n, int64_t k, const int8_t *qs, const uint32_t *ds,
@@ -118,14 +119,14 @@ extern "C" int q8_0_experts_gemm(const void *w, int64_t experts, int64_t n, int6
     if (!q8::device_is_sm103()) return Q8_ERR_DEVICE;
     const q8::ExpertsArgs a = args_of(w, nullptr, experts, n, k, qs, ds, plane_rows, offsets, rows, top_k, pairs, y);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return many_rows(experts, pairs) ? q8::experts_tiles_launch(a, nullptr, nullptr, s) : experts_launch(a, s);
+    return many_rows(experts, pairs) ? q8::experts_tiles_launch(a, nullptr, nullptr, workspace, s) : experts_launch(a, s);
 }
 
 extern "C" size_t q8_0_experts_gate_up_workspace_bytes(int64_t experts, int64_t nf, int64_t k, int64_t plane_rows,
                                                        int64_t top_k, int64_t pairs)
 {
     if (!sizes_ok(experts, nf, k, plane_rows, top_k, pairs) || nf % 32 != 0) return 0;
-    if (many_rows(experts, pairs)) return 0;
+    if (many_rows(experts, pairs)) return q8::experts_tiles_workspace(k, pairs);
     return static_cast<size_t>(pairs) * nf * 8;
 }
 
@@ -150,7 +151,7 @@ extern "C" int q8_0_experts_gate_up(const void *w_gate, const void *w_up, int64_
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     float *gu = static_cast<float *>(workspace);
     const q8::ExpertsArgs a = args_of(w_gate, w_up, experts, nf, k, qs, ds, plane_rows, offsets, rows, top_k, pairs, gu);
-    if (many_rows(experts, pairs)) return q8::experts_tiles_launch(a, qs_out, ds_out, s);
+    if (many_rows(experts, pairs)) return q8::experts_tiles_launch(a, qs_out, ds_out, workspace, s);
     const int st = experts_launch(a, s);
     if (st != Q8_OK) return st;
     const int64_t ctas = (pairs * nf / 4 + 255) / 256;

@@ -21,7 +21,8 @@ struct ExpertsArgs {
 };
 
 // Many rows an expert, on the tensor cores (experts_tiles.cu): the f32 rows, or with qs_out and w2 the plane of silu(w x) * (w2 x).
-int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out, cudaStream_t s);
+size_t experts_tiles_workspace(int64_t k, int64_t pairs);
+int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out, void *workspace, cudaStream_t s);
 
 // The rows of expert e, checked: an expert whose offsets are out of range has none.
 struct ExpertRows {

@@ -17,10 +17,9 @@
 //   next.
 //   Weights go to shared memory as they are (34-byte blocks, TMA boxes of 32
 //   rows x 8 blocks, or 4-byte copies where rows of blocks are not 16-byte
-//   aligned), and four warps widen them there, a row a thread.  Four other
-//   warps load the plane rows of a tile, wherever they lie, and widen them into
-//   shared memory: a quarter of the bytes that a widened plane would take from
-//   L2, no pass before the product and no workspace.
+//   aligned), and four warps widen them there, a row a thread.  The activations
+//   are widened once, by a pass that also puts the rows in order, since each
+//   meets all weight tiles of its expert.
 //   Scales.  d_w(i) * d_a(t) of a block is a product of two vectors: a third MMA
 //   computes it beside the integers, d_w and d_a in the first of its 16 columns
 //   and zeros in the others (a product of two f16 is exact in f32).  So the
@@ -31,10 +30,10 @@
 //   warps swap halves of their columns, then a warp has a block of 32 channels of
 //   32 rows, and writes the plane of silu(gate) * up.
 //
-// Warp roles (640 threads):
-//   warp 0       MMA issuer, tensor memory      warp 1   weight copies, 8 blocks a slot
-//   warps 4-7    widen weights                  warps 8-11   load and widen activations
-//   warps 12-19  epilogue: a TMEM lane quarter and 64 columns each
+// Warp roles (512 threads):
+//   warp 0     MMA issuer, tensor memory          warp 1      weight copies, 8 blocks a slot
+//   warp 2     activation copies, 2 blocks a stage    warp 3   their scales
+//   warps 4-7  widen weights                      warps 8-15  epilogue: a TMEM lane quarter and 64 columns each
 // Every mbarrier wait is bounded; a wait that runs out sets the CTA abort flag
 // and the error word, and all roles drain and exit.
 #include "experts_common.cuh"
@@ -46,9 +45,9 @@ __device__ unsigned int g_tiles_err;
 constexpr int BM = 128, kGroup = 64, kMaxGroups = 2, BN = kGroup * kMaxGroups;
 constexpr int kStages = 3, kRawSlots = 2, kAcc = 2;
 constexpr int kTmemBuf = 2 * BN, kTmemCols = kAcc * kTmemBuf;  // integers, then scales
-constexpr int kThreads = 640, kWidenThreads = 128, kEpiWarps = 8, kEpiThreads = 256;
-constexpr int kRegsCtl = 48, kRegsWiden = 72, kRegsEpi = 144, kRegsLaunch = 96;  // 640 threads: 65536 / 640, in eights
-static_assert(128 * kRegsCtl + 2 * kWidenThreads * kRegsWiden + kEpiThreads * kRegsEpi <= kRegsLaunch * kThreads, "register split");
+constexpr int kThreads = 512, kWidenThreads = 128, kEpiWarps = 8, kEpiThreads = 256;
+constexpr int kRegsCtl = 40, kRegsWiden = 56, kRegsEpi = 208;
+static_assert(128 * kRegsCtl + kWidenThreads * kRegsWiden + kEpiThreads * kRegsEpi <= 128 * kThreads, "register split");
 
 constexpr int kPiece = 8;                      // blocks of a weight slot
 constexpr int kPitchTma = 34 * kPiece;         // 272: a row's piece
@@ -63,7 +62,7 @@ constexpr int OFF_ZERO = kStages * kStageBytes;         // columns 8 .. 15 of ev
 constexpr int OFF_RAW = OFF_ZERO + kScBytes;
 constexpr int OFF_SWAP = OFF_RAW + kRawSlots * kRawBytes;  // [8 warps][16 columns][32] f32
 constexpr int OFF_CUM = OFF_SWAP + kEpiWarps * 16 * 32 * 4;  // row tiles before each expert
-constexpr int kBars = 2 * kRawSlots + 3 * kStages + 2 * kAcc + 1;
+constexpr int kBars = 2 * kRawSlots + 2 * kStages + kAcc + 1;
 constexpr int OFF_BAR = OFF_CUM + (Q8_MAX_EXPERTS + 2) * 4;
 constexpr int OFF_MISC = OFF_BAR + kBars * 8;           // abort flag, TMEM address, sums of the scan
 constexpr int kSmemBytes = OFF_MISC + 16 + 96 + 1024;   // + alignment slack
@@ -74,12 +73,10 @@ struct Bars {
     __device__ uint32_t at(int i) const { return b0 + 8u * i; }
     __device__ uint32_t raw_full(int s) const { return at(s); }
     __device__ uint32_t raw_empty(int s) const { return at(kRawSlots + s); }
-    __device__ uint32_t a_full(int s) const { return at(2 * kRawSlots + s); }
-    __device__ uint32_t b_full(int s) const { return at(2 * kRawSlots + kStages + s); }
-    __device__ uint32_t ab_empty(int s) const { return at(2 * kRawSlots + 2 * kStages + s); }
-    __device__ uint32_t acc_full(int s) const { return at(2 * kRawSlots + 3 * kStages + s); }
-    __device__ uint32_t acc_empty(int s) const { return acc_full(kAcc + s); }
-    __device__ uint32_t drain() const { return acc_full(2 * kAcc); }
+    __device__ uint32_t ab_full(int s) const { return at(2 * kRawSlots + s); }
+    __device__ uint32_t ab_empty(int s) const { return at(2 * kRawSlots + kStages + s); }
+    __device__ uint32_t acc_full(int s) const { return at(2 * kRawSlots + 2 * kStages + s); }
+    __device__ uint32_t drain() const { return acc_full(kAcc); }
 };
 
 // ---------------------------------------------------------------------------
@@ -188,6 +185,7 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
+// Bounded wait: false on the CTA's abort flag or past the limit (which raises it and the error word).
 __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag)
 {
     const uint64_t t0 = q8::globaltimer_ns();
@@ -200,17 +198,22 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatil
     return false;
 }
 
-// Bounded wait: false on the CTA's abort flag or past the limit (which raises it and the error word).
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag)
-{
-    if (Q8_WAIT_LIMIT_NS != 0 && try_wait(bar, parity)) return true;
-    return wait_slow(bar, parity, abort_flag);
-}
-
-// The same for a whole warp that goes on together.
+// For a whole warp that goes on together.  The producers wait like this: their waits have slack.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag)
 {
-    return __all_sync(Q8_FULL_MASK, wait_bar(bar, parity, abort_flag));
+    const bool ok = (Q8_WAIT_LIMIT_NS != 0 && try_wait(bar, parity)) || wait_slow(bar, parity, abort_flag);
+    return __all_sync(Q8_FULL_MASK, ok);
+}
+
+// The hand-over between MMAs and epilogue is a chain of such waits, so each is as short as it can be (60 cycles when the phase
+// is over already; 100 with a vote).  After an abort it returns at once: the warp goes on with what lies there, and ends its
+// tile, which is not stored.
+__device__ __forceinline__ void wait_go(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    if (Q8_WAIT_LIMIT_NS != 0)
+        for (int i = 0; i < 64; ++i)
+            if (try_wait(bar, parity)) return;
+    wait_slow(bar, parity, abort_flag);
 }
 
 // Wait for copies or MMAs in flight before the CTA exits, whatever the abort flag says; bounded.
@@ -233,6 +236,19 @@ __device__ __forceinline__ void arrive(uint32_t bar)
 __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// A buffer of tensor memory is handed back by a named barrier: the epilogue warps arrive, the MMA warp waits, some 25 cycles
+// for a wait where an mbarrier takes 100 and its arrival as long again.  Both sides pass each barrier once per block, whatever
+// the abort flag says, so neither is left waiting.
+constexpr int kHandOver = 2;  // barriers 2 and 3
+__device__ __forceinline__ void acc_release(int buf)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(kHandOver + buf), "n"(kEpiThreads + 32) : "memory");
+}
+__device__ __forceinline__ void acc_acquire(int buf)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(kHandOver + buf), "n"(kEpiThreads + 32) : "memory");
 }
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
@@ -300,27 +316,12 @@ __device__ __forceinline__ int tile_row(int nt, int r)
     return kPair ? 64 * nt + 32 * (r >> 6) + (r & 31) : BM * nt + r;
 }
 
-// acc += scale * integer over 32 columns.
-__device__ __forceinline__ void epi_half(uint32_t taddr, float2 *acc)
-{
-    uint32_t p[32], s[32];
-    tc_ld32(taddr, p);
-    tc_ld32(taddr + BN, s);
-    tc_wait_ld();
-    tc_regs32(p);
-    tc_regs32(s);
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        acc[i] = __ffma2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
-                            make_float2(__uint_as_float(p[2 * i]), __uint_as_float(p[2 * i + 1])), acc[i]);
-    order16(acc);
-}
-
 // kPair: w and w2, the plane of silu(w x) * (w2 x); else w and f32 rows.  kTma: nb % 8 == 0.
 template <bool kPair, bool kTma>
 __global__ void __launch_bounds__(kThreads, 1)
 experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_constant__ CUtensorMap tmW,
-                     const __grid_constant__ CUtensorMap tmW2, int8_t *qs_out, uint32_t *ds_out)
+                     const __grid_constant__ CUtensorMap tmW2, const __grid_constant__ CUtensorMap tmB, int8_t *qs_out,
+                     uint32_t *ds_out)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = q8::smem_u32(smem_raw);
@@ -342,11 +343,9 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
         };
         init(kRawSlots, 1);           // raw_full: copied bytes
         init(kRawSlots, 4);           // raw_empty: a warp each
-        init(kStages, 4);             // a_full
-        init(kStages, 4);             // b_full
+        init(kStages, 6);             // ab_full: four widening warps, the copied bytes, their scales
         init(kStages, 1);             // ab_empty: tcgen05.commit
         init(kAcc, 1);                // acc_full: tcgen05.commit
-        init(kAcc, kEpiWarps);        // acc_empty
         init(1, 1);                   // drain
         q8::fence_mbar_init();
     }
@@ -405,37 +404,37 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
         setmaxnreg_dec<kRegsCtl>();
         if (warp == 0) {
             // ------------------------------------------------------------ MMA issuer
-            uint32_t n = 0, blk = 0;  // stages and blocks done
-            bool ok = true;
-            for (int at = blockIdx.x; at < total && ok; at += gridDim.x) {
+            uint32_t blk = 0, slot = 0, phase = 0;  // blocks done, stage and its phase
+            for (int at = blockIdx.x; at < total; at += gridDim.x) {
                 const Tile t = tile_at(a, cum, weight_tiles, at);
                 const uint32_t idesc = mma_desc(t.groups * kGroup);
-                for (int j = 0; j < nb; ++j, ++blk) {
-                    const int slot = n % kStages, u = j & 1;
-                    if (u == 0) {
-                        ok = warp_wait(B.a_full(slot), (n / kStages) & 1u, abort_flag) &&
-                             warp_wait(B.b_full(slot), (n / kStages) & 1u, abort_flag);
-                        if (!ok) break;
+                for (int j = 0; j < nb; j += 2) {
+                    const uint32_t stage = base + slot * kStageBytes;
+                    const uint64_t pa = smem_desc(stage), pb = smem_desc(stage + OFF_B);
+                    const uint64_t sa = scale_desc(stage + OFF_DW, base + OFF_ZERO), sb = scale_desc(stage + OFF_DA, base + OFF_ZERO);
+                    wait_go(B.ab_full(slot), phase, abort_flag);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        if (u == 1 && j + 1 == nb) break;
+                        if (blk >= kAcc) acc_acquire(blk % kAcc);
+                        tc_fence_after();
+                        const uint32_t d = tmem + (blk % kAcc) * kTmemBuf;
+                        // a scale operand's next block: its columns 8 .. 15 lie that much nearer
+                        constexpr uint64_t next = (kScBytes >> 4) - (static_cast<uint64_t>(kScBytes >> 4) << 16);
+                        if (elect_one()) {
+                            tc_mma_f16(d, pa + 4 * u, pb + 4 * u, idesc, 0);
+                            tc_mma_f16(d, pa + 4 * u + 2, pb + 4 * u + 2, idesc, 1);  // 32 bytes on
+                            tc_mma_f16(d + BN, sa + u * next, sb + u * next, idesc, 0);
+                            tc_commit(B.acc_full(blk % kAcc));
+                            if (u == 1 || j + 1 == nb) tc_commit(B.ab_empty(slot));
+                        }
+                        __syncwarp();
+                        ++blk;
                     }
-                    ok = warp_wait(B.acc_empty(blk % kAcc), ((blk / kAcc) & 1u) ^ 1u, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t d = tmem + (blk % kAcc) * kTmemBuf, stage = base + slot * kStageBytes;
-                    const uint64_t pa = smem_desc(stage + 64 * u), pb = smem_desc(stage + OFF_B + 64 * u);
-                    const uint64_t sa = scale_desc(stage + OFF_DW + u * kScBytes, base + OFF_ZERO);
-                    const uint64_t sb = scale_desc(stage + OFF_DA + u * kScBytes, base + OFF_ZERO);
-                    const bool last = u || j == nb - 1;
-                    if (elect_one()) {
-                        tc_mma_f16(d, pa, pb, idesc, 0);
-                        tc_mma_f16(d, pa + 2, pb + 2, idesc, 1);  // 32 bytes on
-                        tc_mma_f16(d + BN, sa, sb, idesc, 0);
-                        tc_commit(B.acc_full(blk % kAcc));
-                        if (last) tc_commit(B.ab_empty(slot));
-                    }
-                    __syncwarp();
-                    n += last;
+                    if (++slot == kStages) slot = 0, phase ^= 1u;
                 }
             }
+            for (int k = 0; k < kAcc && k < static_cast<int>(blk); ++k) acc_acquire(k);  // the last blocks'
             // every MMA must have completed before its operands and TMEM go
             if (elect_one()) tc_commit(B.drain());
             __syncwarp();
@@ -465,6 +464,62 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
             // the last copies must have landed before the CTA exits
             for (uint32_t s = n < kRawSlots ? 0 : n - kRawSlots; s < n; ++s)
                 drain_bar(B.raw_full(s % kRawSlots), (s / kRawSlots) & 1u);
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ activations
+            uint32_t n = 0;
+            bool ok = true;
+            for (int at = blockIdx.x; at < total && ok; at += gridDim.x) {
+                const Tile t = tile_at(a, cum, weight_tiles, at);
+                for (int s = 0; s < stages; ++s, ++n) {
+                    const int slot = n % kStages;
+                    ok = warp_wait(B.ab_empty(slot), ((n / kStages) & 1u) ^ 1u, abort_flag);
+                    if (!ok) break;
+                    const uint32_t dst = base + slot * kStageBytes + OFF_B;
+                    if (elect_one()) {  // rows behind the expert's are the next one's, or stale: their columns are not stored
+                        expect_tx(B.ab_full(slot), t.groups * kGroup * 128);
+                        q8::tma_load_2d(dst, &tmB, 64 * s, t.row0, B.ab_full(slot));
+                        if (t.groups > 1) q8::tma_load_2d(dst + kGroup * 128, &tmB, 64 * s, t.row0 + kGroup, B.ab_full(slot));
+                    }
+                    __syncwarp();
+                }
+            }
+            for (uint32_t s = n < kStages ? 0 : n - kStages; s < n; ++s) drain_bar(B.ab_full(s % kStages), (s / kStages) & 1u);
+        } else if (warp == 3) {
+            // ------------------------------------------------------------ their scales: columns lane, lane + 32, ...
+            uint32_t n = 0;
+            bool ok = true, bad = false;
+            for (int at = blockIdx.x; at < total && ok; at += gridDim.x) {
+                const Tile t = tile_at(a, cum, weight_tiles, at);
+                const uint32_t *src[BN / 32];
+#pragma unroll
+                for (int i = 0; i < BN / 32; ++i) {
+                    const int64_t x = q8::source_row(a, t.row0 + min(lane + 32 * i, t.rows - 1));
+                    bad |= x < 0;
+                    src[i] = a.ds + max(x, int64_t(0)) * nb;  // a row out of range: any, it is not stored
+                }
+                for (int s = 0; s < stages; ++s, ++n) {
+                    const int slot = n % kStages;
+                    const bool two = 2 * s + 1 < nb;
+                    uint32_t d[BN / 32][2];
+#pragma unroll
+                    for (int i = 0; i < BN / 32; ++i) {
+                        d[i][0] = i < 2 * t.groups ? __ldg(src[i] + 2 * s) : 0u;
+                        d[i][1] = i < 2 * t.groups && two ? __ldg(src[i] + 2 * s + 1) : 0u;
+                    }
+                    ok = warp_wait(B.ab_empty(slot), ((n / kStages) & 1u) ^ 1u, abort_flag);
+                    if (!ok) break;
+                    uint16_t *da = reinterpret_cast<uint16_t *>(sm + slot * kStageBytes + OFF_DA + lane * 16);
+#pragma unroll
+                    for (int i = 0; i < BN / 32; ++i) {
+                        da[256 * i] = static_cast<uint16_t>(d[i][0]);
+                        da[256 * i + kScBytes / 2] = static_cast<uint16_t>(d[i][1]);
+                    }
+                    q8::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive(B.ab_full(slot));
+                }
+            }
+            if (bad) atomicOr(&g_tiles_err, q8::kErrData);
         }
     } else if (warp < 8) {
         setmaxnreg_dec<kRegsWiden>();
@@ -574,7 +629,7 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     }
                     q8::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) arrive(B.a_full(st));
+                    if (lane == 0) arrive(B.ab_full(st));
                     ++n;
                 }
                 if (!ok) break;
@@ -583,114 +638,68 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
             }
         }
         if (!kTma) cp_async_wait<0>();
-    } else if (warp < 12) {
-        setmaxnreg_dec<kRegsWiden>();
-        // ---------------------------------------------------------------- activations
-        // lane 4 r + c has 16 codes (chunk c of two blocks) of the columns 32 w + r + 8 i, i < 4, and the scales of column
-        // 32 w + r + 8 c; the next stage's loads are in flight while one is widened
-        const int c = lane & 3, r = lane >> 2, col = 32 * (warp - 8) + r;
-        uint32_t n = 0;
-        bool ok = true, bad = false;
-        const uint4 *src[4];
-        const uint32_t *sds = nullptr;
-        int at = blockIdx.x;
-        int groups = 0;
-        auto locate = [&](int where) {
-            const Tile t = tile_at(a, cum, weight_tiles, where);
-            groups = t.groups;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                int64_t x = q8::source_row(a, t.row0 + min(col + 8 * i, t.rows - 1));
-                bad |= x < 0;
-                x = max(x, int64_t(0));  // a row out of range: any, it is not stored
-                src[i] = reinterpret_cast<const uint4 *>(a.qs) + x * (2 * nb) + c;
-                if (i == c) sds = a.ds + x * nb;
-            }
-        };
-        uint4 v[4];
-        uint32_t d0 = 0, d1 = 0;
-        auto load = [&](int s) {
-            const bool two = 2 * s + 1 < nb;
-            if (32 * (warp - 8) >= groups * kGroup) return;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = two || c < 2 ? __ldg(src[i] + 4 * s) : make_uint4(0u, 0u, 0u, 0u);
-            d0 = __ldg(sds + 2 * s);
-            d1 = two ? __ldg(sds + 2 * s + 1) : 0u;
-        };
-        if (at < total) {
-            locate(at);
-            load(0);
-        }
-        for (; at < total && ok; at += gridDim.x) {
-            for (int s = 0; s < stages; ++s, ++n) {
-                const int st = n % kStages;
-                ok = warp_wait(B.ab_empty(st), ((n / kStages) & 1u) ^ 1u, abort_flag);
-                if (!ok) break;
-                const uint4 w[4] = {v[0], v[1], v[2], v[3]};
-                const uint32_t e0 = d0, e1 = d1;
-                const bool mine = 32 * (warp - 8) < groups * kGroup;
-                if (s + 1 < stages) {
-                    load(s + 1);
-                } else if (at + gridDim.x < total) {
-                    locate(at + gridDim.x);
-                    load(0);
-                }
-                if (mine) {
-                    uint8_t *out = sm + st * kStageBytes + OFF_B;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = col + 8 * i;  // row % 8 == r
-                        uint4 o0, o1;
-                        q8::i8x4_to_f16x4(w[i].x, o0.x, o0.y);
-                        q8::i8x4_to_f16x4(w[i].y, o0.z, o0.w);
-                        q8::i8x4_to_f16x4(w[i].z, o1.x, o1.y);
-                        q8::i8x4_to_f16x4(w[i].w, o1.z, o1.w);
-                        *reinterpret_cast<uint4 *>(out + row * 128 + 16 * ((2 * c) ^ r)) = o0;
-                        *reinterpret_cast<uint4 *>(out + row * 128 + 16 * ((2 * c + 1) ^ r)) = o1;
-                    }
-                    uint16_t *da = reinterpret_cast<uint16_t *>(sm + st * kStageBytes + OFF_DA + (col + 8 * c) * 16);
-                    da[0] = static_cast<uint16_t>(e0);
-                    da[kScBytes / 2] = static_cast<uint16_t>(e1);
-                    q8::fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) arrive(B.b_full(st));
-            }
-        }
-        if (bad) atomicOr(&g_tiles_err, q8::kErrData);
     } else {
         setmaxnreg_inc<kRegsEpi>();
         // ---------------------------------------------------------------- epilogue
-        const int q = warp & 3, h = (warp - 12) >> 2;  // lanes 32 q .., columns 64 h ..
+        const int q = warp & 3, h = (warp - 8) >> 2;  // lanes 32 q .., columns 64 h ..
         const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + 64u * h;
         uint32_t blk = 0;
         for (int at = blockIdx.x; at < total; at += gridDim.x) {
             const Tile t = tile_at(a, cum, weight_tiles, at);
             const bool mine = h < t.groups;
             float2 acc[32];  // columns 64 h + 2 i, + 1 of position 32 q + lane
-            bool ok = true;
 #pragma unroll
             for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
-#pragma unroll 1
-            for (int j = 0; j < nb; ++j, ++blk) {
-                ok = warp_wait(B.acc_full(blk % kAcc), (blk / kAcc) & 1u, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                if (mine) {
-                    const uint32_t buf = taddr + (blk % kAcc) * kTmemBuf;
-                    epi_half(buf, acc);
-                    epi_half(buf + 32, acc + 16);
+            if (!mine) {
+                for (int j = 0; j < nb; ++j, ++blk) {
+                    wait_go(B.acc_full(blk % kAcc), (blk / kAcc) & 1u, abort_flag);
+                    acc_release(blk % kAcc);
                 }
-                tc_fence_before();
-                if (lane == 0) arrive(B.acc_empty(blk % kAcc));
+            } else {
+                // 32 columns at a time: the next ones' loads are in flight while these are added up, and a block's buffer is
+                // handed back when its second half has landed
+                uint32_t p[2][32], c[2][32];
+                auto load = [&](int x) {
+                    const uint32_t buf = taddr + (blk % kAcc) * kTmemBuf + 32 * x;
+                    tc_ld32(buf, p[x]);
+                    tc_ld32(buf + BN, c[x]);
+                };
+                auto add = [&](int x) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        acc[16 * x + i] =
+                            __ffma2_rn(make_float2(__uint_as_float(c[x][2 * i]), __uint_as_float(c[x][2 * i + 1])),
+                                       make_float2(__uint_as_float(p[x][2 * i]), __uint_as_float(p[x][2 * i + 1])), acc[16 * x + i]);
+                    order16(acc + 16 * x);
+                };
+                wait_go(B.acc_full(blk % kAcc), (blk / kAcc) & 1u, abort_flag);
+                tc_fence_after();
+                load(0);
+#pragma unroll 1
+                for (int j = 0; j < nb; ++j) {
+                    tc_wait_ld();
+                    tc_regs32(p[0]), tc_regs32(c[0]);
+                    load(1);
+                    add(0);
+                    tc_wait_ld();
+                    tc_regs32(p[1]), tc_regs32(c[1]);
+                    tc_fence_before();
+                    acc_release(blk % kAcc);
+                    ++blk;
+                    if (j + 1 < nb) {
+                        wait_go(B.acc_full(blk % kAcc), (blk / kAcc) & 1u, abort_flag);
+                        tc_fence_after();
+                        load(0);
+                    }
+                    add(1);
+                }
             }
-            ok = __all_sync(Q8_FULL_MASK, ok && !*abort_flag);
+            const bool ok = __all_sync(Q8_FULL_MASK, !*abort_flag);
             auto valid = [&](int c0) {  // of the 32 columns from c0 on
                 return __ballot_sync(Q8_FULL_MASK, c0 + lane < t.rows && q8::source_row(a, t.row0 + c0 + lane) >= 0);
             };
             if (!kPair) {
-                if (!ok) break;
-                if (!mine) continue;
+                if (!ok || !mine) continue;  // after an abort the tiles are walked, not stored
                 const int row = BM * t.nt + 32 * q + lane;
                 const uint32_t m[2] = {valid(64 * h), valid(64 * h + 32)};
                 float *out = a.out + static_cast<int64_t>(t.row0 + 64 * h) * a.ld + row;
@@ -705,11 +714,11 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     }
                 }
             } else {
-                if (epi_any(!ok)) break;  // all of them, so that none waits for another below
+                if (epi_any(!ok)) continue;  // all of them, so that none waits for another below
                 // warp q even has 32 gate channels, q odd the same up channels, of 64 columns: even keeps the first 32 columns
                 const int up = q & 1;
-                float *box = reinterpret_cast<float *>(sm + OFF_SWAP) + (warp - 12) * 512 + lane;
-                const float *from = reinterpret_cast<float *>(sm + OFF_SWAP) + ((warp - 12) ^ 1) * 512 + lane;
+                float *box = reinterpret_cast<float *>(sm + OFF_SWAP) + (warp - 8) * 512 + lane;
+                const float *from = reinterpret_cast<float *>(sm + OFF_SWAP) + ((warp - 8) ^ 1) * 512 + lane;
                 float v[32];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -770,37 +779,75 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
     }
 }
 
+// The sorted rows' codes as f16: out [pairs][16 chunks], 16 codes a thread and round.
+__global__ void __launch_bounds__(256)
+experts_sort_plane_kernel(const __grid_constant__ q8::ExpertsArgs a, uint4 *__restrict__ out)
+{
+    q8::griddep_launch_dependents();
+    q8::griddep_wait();
+    const int chunks = 2 * a.nb, lane = threadIdx.x & 31;  // of a row
+    const int rows = min(max(a.offsets[a.experts], 0), a.pairs);
+    const int warps = gridDim.x * (blockDim.x / 32);
+    for (int r = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
+        const int64_t src = max(q8::source_row(a, r), int64_t(0));  // out of range: any, it is not stored
+        const uint4 *from = reinterpret_cast<const uint4 *>(a.qs) + src * chunks;
+        uint4 *to = out + static_cast<int64_t>(r) * 2 * chunks;
+#pragma unroll 4
+        for (int i = lane; i < chunks; i += 32) {
+            const uint4 v = __ldg(from + i);
+            uint4 o0, o1;
+            q8::i8x4_to_f16x4(v.x, o0.x, o0.y);
+            q8::i8x4_to_f16x4(v.y, o0.z, o0.w);
+            q8::i8x4_to_f16x4(v.z, o1.x, o1.y);
+            q8::i8x4_to_f16x4(v.w, o1.z, o1.w);
+            to[2 * i] = o0;
+            to[2 * i + 1] = o1;
+        }
+    }
+}
+
 template <bool kPair, bool kTma>
-int launch(const q8::ExpertsArgs &a, const CUtensorMap &mw, const CUtensorMap &mw2, unsigned grid,
+int launch(const q8::ExpertsArgs &a, const CUtensorMap &mw, const CUtensorMap &mw2, const CUtensorMap &mb, unsigned grid,
            int8_t *qs_out, uint32_t *ds_out, int slot, cudaStream_t s)
 {
     if (!q8::set_max_dynamic_smem(reinterpret_cast<const void *>(experts_tiles_kernel<kPair, kTma>), kSmemBytes, slot))
         return Q8_ERR_LAUNCH;
-    return q8::launch_pdl(experts_tiles_kernel<kPair, kTma>, dim3(grid), dim3(kThreads), kSmemBytes, s, a, mw, mw2, qs_out, ds_out);
+    return q8::launch_pdl(experts_tiles_kernel<kPair, kTma>, dim3(grid), dim3(kThreads), kSmemBytes, s, a, mw, mw2, mb, qs_out,
+                          ds_out);
 }
 
 } // namespace
 
 namespace q8 {
 
-int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out, cudaStream_t s)
+size_t experts_tiles_workspace(int64_t k, int64_t pairs) { return static_cast<size_t>(pairs) * k * 2; }
+
+int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out, void *workspace, cudaStream_t s)
 {
     const bool pair = a.w2 != nullptr, tma = a.nb % kPiece == 0;
-    CUtensorMap mw = {}, mw2 = {};
+    CUtensorMap mw = {}, mw2 = {}, mb = {};
     const uint64_t wrows = static_cast<uint64_t>(a.experts) * a.n, pitch = static_cast<uint64_t>(a.nb) * 34;
     if (tma && (!make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.w, pitch / 2, wrows, pitch, kPitchTma / 2, 32,
                              CU_TENSOR_MAP_SWIZZLE_NONE) ||
                 (pair && !make_map_2d(&mw2, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.w2, pitch / 2, wrows, pitch, kPitchTma / 2, 32,
                                       CU_TENSOR_MAP_SWIZZLE_NONE))))
         return Q8_ERR_LAUNCH;
+    const uint64_t row = static_cast<uint64_t>(a.nb) * 64;  // bytes of f16
+    if (!make_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT16, workspace, row / 2, static_cast<uint64_t>(a.pairs), row, 64, kGroup,
+                     CU_TENSOR_MAP_SWIZZLE_128B))
+        return Q8_ERR_LAUNCH;
     const int sms = device_sm_count();
+    const int64_t ctas = (a.pairs + 7) / 8, cap = static_cast<int64_t>(sms) * 8;
+    const int st = launch_pdl(experts_sort_plane_kernel, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(256), 0, s, a,
+                              static_cast<uint4 *>(workspace));
+    if (st != Q8_OK) return st;
     const int64_t weight_tiles = pair ? (a.n + 63) / 64 : (a.n + BM - 1) / BM;
     const int64_t most = (a.pairs / BN + (a.experts < a.pairs ? a.experts : a.pairs)) * weight_tiles;
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
-    if (pair) return tma ? launch<true, true>(a, mw, mw2, grid, qs_out, ds_out, 48, s)
-                         : launch<true, false>(a, mw, mw2, grid, qs_out, ds_out, 49, s);
-    return tma ? launch<false, true>(a, mw, mw2, grid, qs_out, ds_out, 50, s)
-               : launch<false, false>(a, mw, mw2, grid, qs_out, ds_out, 51, s);
+    if (pair) return tma ? launch<true, true>(a, mw, mw2, mb, grid, qs_out, ds_out, 48, s)
+                         : launch<true, false>(a, mw, mw2, mb, grid, qs_out, ds_out, 49, s);
+    return tma ? launch<false, true>(a, mw, mw2, mb, grid, qs_out, ds_out, 50, s)
+               : launch<false, false>(a, mw, mw2, mb, grid, qs_out, ds_out, 51, s);
 }
 
 unsigned int *experts_tiles_error_word()

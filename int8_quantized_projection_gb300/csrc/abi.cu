@@ -178,7 +178,7 @@ __global__ void take_errors_kernel(const __grid_constant__ ErrorWords e, int slo
 bool error_words(ErrorWords *e)
 {
     *e = {{q8::gemv_error_word(), q8::gemm_error_word(), q8::quant_error_word(), q8::attn_rows_error_word(),
-           q8::attn_tiles_error_word(), q8::kv_error_word(), q8::route_error_word(), q8::experts_error_word(),
+           q8::attn_tiles_error_word(), q8::kv_error_word(), q8::route_error_word(), q8::experts_rows_error_word(),
            q8::experts_tiles_error_word(), q8::resnorm_error_word()}};
     for (const unsigned int *p : e->w)
         if (!p) return false;

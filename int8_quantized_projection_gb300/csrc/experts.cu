@@ -4,52 +4,13 @@
 
 namespace {
 
-__device__ unsigned int g_experts_err;
+__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 
-// One warp, one weight row, the expert's rows one after another: lane l takes the blocks l, l + 32, ...
-__global__ void __launch_bounds__(256) experts_plain_kernel(const __grid_constant__ q8::ExpertsArgs a)
-{
-    q8::griddep_launch_dependents();
-    q8::griddep_wait();
-    const int lane = threadIdx.x & 31, i = blockIdx.x * 8 + (threadIdx.x >> 5), e = blockIdx.y;
-    const q8::ExpertRows x = q8::expert_rows_of(a, e);
-    if (x.bad && threadIdx.x == 0) atomicOr(&g_experts_err, q8::kErrData);
-    const int all = a.w2 ? 2 * a.n : a.n;
-    if (i >= all) return;
-    const uint8_t *w = i < a.n ? a.w + (static_cast<int64_t>(e) * a.n + i) * a.nb * 34
-                               : a.w2 + (static_cast<int64_t>(e) * a.n + i - a.n) * a.nb * 34;
-    for (int r = x.first; r < x.first + x.count; ++r) {
-        const int64_t src = q8::source_row(a, r);
-        if (src < 0) {
-            if (lane == 0) atomicOr(&g_experts_err, q8::kErrData);
-            continue;
-        }
-        float acc = 0.0f;
-        for (int b = lane; b < a.nb; b += 32) {
-            const uint16_t *p = reinterpret_cast<const uint16_t *>(w + static_cast<int64_t>(b) * 34);
-            const uint32_t *q = reinterpret_cast<const uint32_t *>(a.qs + (src * a.nb + b) * 32);
-            int sum = 0;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) sum = q8::dp4a(p[1 + 2 * u] | (static_cast<uint32_t>(p[2 + 2 * u]) << 16), q[u], sum);
-            const float dw = __half2float(__ushort_as_half(p[0]));
-            const float da = __half2float(__ushort_as_half(static_cast<unsigned short>(a.ds[src * a.nb + b] & 0xffffu)));
-            acc = fmaf(dw * da, static_cast<float>(sum), acc);
-        }
-        acc = q8::rms_warp_sum(acc);
-        if (lane == 0) a.out[r * a.ld + i] = acc;
-    }
-}
-
-int experts_launch(const q8::ExpertsArgs &a, cudaStream_t s)
-{
-    const int all = a.w2 ? 2 * a.n : a.n;
-    return q8::launch_pdl(experts_plain_kernel, dim3((all + 7) / 8, a.experts), dim3(256), 0, s, a);
-}
-
-// gu [pairs][2 nf] (gate, then up) -> the plane of silu(gate) * up, rows up to the last expert's end.
+// gu [slices][pairs][2 nf] (gate, then up; the slices of k are added up in order) -> the plane of silu(gate) * up, rows up to the
+// last expert's end.
 __global__ void __launch_bounds__(256)
-experts_swiglu_kernel(const float4 *__restrict__ gu, int F, const int32_t *__restrict__ offsets, int experts, int pairs,
-                      uint32_t *__restrict__ qs, uint32_t *__restrict__ ds)
+experts_swiglu_kernel(const float4 *__restrict__ gu, int slices, int F, const int32_t *__restrict__ offsets, int experts,
+                      int pairs, uint32_t *__restrict__ qs, uint32_t *__restrict__ ds)
 {
     q8::griddep_launch_dependents();
     q8::griddep_wait();
@@ -60,7 +21,15 @@ experts_swiglu_kernel(const float4 *__restrict__ gu, int F, const int32_t *__res
     for (int64_t base = warp * 32; base < total; base += warps * 32) {
         const int64_t i = base + lane, r = i / F;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < total) o = q8::silu_mul4(gu[r * F + i], gu[r * F + i + F]);
+        if (i < total) {
+            const float4 *p = gu + r * F + i;
+            float4 g = p[0], u = p[F];
+            for (int k = 1; k < slices; ++k) {
+                p += static_cast<int64_t>(pairs) * 2 * F;
+                g = add4(g, p[0]), u = add4(u, p[F]);
+            }
+            o = q8::silu_mul4(g, u);
+        }
         const q8::Q8Enc e = q8::q8_encode8(o);
         if (i < total) {
             qs[i] = e.qword;
@@ -99,8 +68,10 @@ q8::ExpertsArgs args_of(const void *w, const void *w2, int64_t experts, int64_t 
 extern "C" size_t q8_0_experts_gemm_workspace_bytes(int64_t experts, int64_t n, int64_t k, int64_t plane_rows,
                                                     int64_t top_k, int64_t pairs)
 {
-    if (!sizes_ok(experts, n, k, plane_rows, top_k, pairs) || !many_rows(experts, pairs)) return 0;
-    return q8::experts_tiles_workspace(k, pairs);
+    if (!sizes_ok(experts, n, k, plane_rows, top_k, pairs)) return 0;
+    if (many_rows(experts, pairs)) return q8::experts_tiles_workspace(k, pairs);
+    const int slices = q8::experts_rows_slices(experts, pairs, k / 32);
+    return slices > 1 ? static_cast<size_t>(slices) * pairs * n * 4 : 0;
 }
 
 extern "C" int q8_0_experts_gemm(const void *w, int64_t experts, int64_t n, int64_t k, const int8_t *qs, const uint32_t *ds,
@@ -119,7 +90,11 @@ extern "C" int q8_0_experts_gemm(const void *w, int64_t experts, int64_t n, int6
     if (!q8::device_is_sm103()) return Q8_ERR_DEVICE;
     const q8::ExpertsArgs a = args_of(w, nullptr, experts, n, k, qs, ds, plane_rows, offsets, rows, top_k, pairs, y);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return many_rows(experts, pairs) ? q8::experts_tiles_launch(a, nullptr, nullptr, workspace, s) : experts_launch(a, s);
+    if (many_rows(experts, pairs)) return q8::experts_tiles_launch(a, nullptr, nullptr, workspace, s);
+    if (!need) return q8::experts_rows_launch(a, y, s);
+    float *part = static_cast<float *>(workspace);
+    const int st = q8::experts_rows_launch(a, part, s);
+    return st != Q8_OK ? st : q8::experts_join_launch(part, q8::experts_rows_slices(experts, pairs, k / 32), a, s);
 }
 
 extern "C" size_t q8_0_experts_gate_up_workspace_bytes(int64_t experts, int64_t nf, int64_t k, int64_t plane_rows,
@@ -127,7 +102,7 @@ extern "C" size_t q8_0_experts_gate_up_workspace_bytes(int64_t experts, int64_t 
 {
     if (!sizes_ok(experts, nf, k, plane_rows, top_k, pairs) || nf % 32 != 0) return 0;
     if (many_rows(experts, pairs)) return q8::experts_tiles_workspace(k, pairs);
-    return static_cast<size_t>(pairs) * nf * 8;
+    return static_cast<size_t>(q8::experts_rows_slices(experts, pairs, k / 32)) * pairs * nf * 8;
 }
 
 extern "C" int q8_0_experts_gate_up(const void *w_gate, const void *w_up, int64_t experts, int64_t nf, int64_t k,
@@ -152,20 +127,11 @@ extern "C" int q8_0_experts_gate_up(const void *w_gate, const void *w_up, int64_
     float *gu = static_cast<float *>(workspace);
     const q8::ExpertsArgs a = args_of(w_gate, w_up, experts, nf, k, qs, ds, plane_rows, offsets, rows, top_k, pairs, gu);
     if (many_rows(experts, pairs)) return q8::experts_tiles_launch(a, qs_out, ds_out, workspace, s);
-    const int st = experts_launch(a, s);
+    const int st = q8::experts_rows_launch(a, gu, s);
     if (st != Q8_OK) return st;
     const int64_t ctas = (pairs * nf / 4 + 255) / 256;
     return q8::launch_pdl(experts_swiglu_kernel, dim3(static_cast<unsigned>(ctas < 152 * 8 ? ctas : 152 * 8)), dim3(256), 0, s,
-                          reinterpret_cast<const float4 *>(gu), static_cast<int>(nf / 4), offsets, static_cast<int>(experts),
+                          reinterpret_cast<const float4 *>(gu), q8::experts_rows_slices(experts, pairs, k / 32),
+                          static_cast<int>(nf / 4), offsets, static_cast<int>(experts),
                           static_cast<int>(pairs), reinterpret_cast<uint32_t *>(qs_out), ds_out);
 }
-
-namespace q8 {
-
-unsigned int *experts_error_word()
-{
-    void *p = nullptr;
-    return cudaGetSymbolAddress(&p, g_experts_err) == cudaSuccess ? static_cast<unsigned int *>(p) : nullptr;
-}
-
-} // namespace q8

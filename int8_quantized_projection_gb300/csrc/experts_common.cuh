@@ -24,6 +24,12 @@ struct ExpertsArgs {
 size_t experts_tiles_workspace(int64_t k, int64_t pairs);
 int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out, void *workspace, cudaStream_t s);
 
+// A few rows an expert (experts_rows.cu): the f32 rows into out, or, where k is cut into several slices, their parts [slices][pairs][ld],
+// which the join adds up into a.out.
+int experts_rows_slices(int64_t experts, int64_t pairs, int64_t nb);
+int experts_rows_launch(const ExpertsArgs &a, float *out, cudaStream_t s);
+int experts_join_launch(const float *part, int slices, const ExpertsArgs &a, cudaStream_t s);
+
 // The rows of expert e, checked: an expert whose offsets are out of range has none.
 struct ExpertRows {
     int first, count;

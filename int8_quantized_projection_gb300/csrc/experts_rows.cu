@@ -1,0 +1,487 @@
+// experts_rows.cu -- products of a few sorted rows an expert with their experts'
+// Q8_0 matrices: a stream over the weights of the experts that have rows.
+//
+// The block dot products run on mma.sync m16n8k16 (16 weight rows x 8 sorted
+// rows), two MMAs a block, as in the small-batch kernel of gemv.cu: exact
+// integers, scaled by d_w * d_a and added in f32.  The weight codes enter as
+// 1152 + q (a byte permute makes that f16 from the code, a subtraction less per
+// two codes), and the accumulator starts at -1152 * ssum, which the plane has
+// for each block: |sum| < 2^24, so the integer is exact all the same.
+//
+//   The line.  A segment is up to 8 NT rows of one expert (and a slice of k where
+//   a row's activations would not fit shared memory); it has an item for every 16
+//   weight rows.  All segments' items lie on one line, from the offsets on the
+//   device, and CTA c takes an equal stretch of it.  Within one segment of its
+//   stretch the CTA's warps share the items' 8-block pieces equally: a warp
+//   takes a stretch of pieces, stores the items that are all its own and leaves
+//   the ends to be added up through shared memory, in warp order.
+//   Weights come through a ring of a warp's own, a TMA box of 16 rows x 8 blocks
+//   (272 bytes a row) a slot; its next pieces are asked for across items and
+//   segments.  Where rows of blocks are not 16-byte aligned the warp copies 4
+//   bytes at a time.
+//   Activations of a segment lie in shared memory in the order of the MMA's B
+//   fragments, widened to f16 once; rows that the segment does not have are not
+//   written: what lies there enters columns that are not stored.
+#include "experts_common.cuh"
+
+namespace {
+
+__device__ unsigned int g_rows_err;
+
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
+constexpr int kPiece = 8;                    // blocks
+constexpr int kPitchTma = 34 * kPiece;       // 272
+constexpr int kPitchAny = kPitchTma + 4;     // 276
+constexpr int kSlotBytes = 16 * kPitchAny + 64;  // 4480, a multiple of 128
+static_assert(kSlotBytes % 128 == 0, "TMA destination");
+
+struct RowsArgs {
+    q8::ExpertsArgs x;
+    int groups, slices, slice_blocks;  // items of a segment, slices of k, their blocks (the last may have fewer)
+    int slots;                         // of a warp's ring
+    int64_t part;                      // floats from one slice's output to the next's
+};
+
+// shared memory: ring [kWarps][slots] | B fragments [blocks][NT][32] uint4 | scales [blocks][NT][4] float4 |
+// partial items [kWarps][2][NT][32] float4 | row tables | barriers
+template <int NT>
+struct Layout {
+    int act, scale, part, cum, bar, total;
+    __host__ __device__ Layout(int slots, int blocks)
+    {
+        act = kWarps * slots * kSlotBytes;
+        scale = act + blocks * NT * 512;
+        part = scale + blocks * NT * 64;
+        cum = part + kWarps * 2 * NT * 512;
+        bar = cum + (Q8_MAX_EXPERTS + 2) * 4;
+        total = bar + kWarps * 8 * slots + 128 + 64;
+    }
+};
+
+struct Segment {
+    int e, first, rows, slice;  // expert, its sorted rows, slice of k
+    int b0, blocks;             // blocks of the slice
+    int i0, i1;                 // items of this CTA's stretch, from the segment's own start
+    int next;                   // place on the line behind them
+};
+
+// The segment at place i of the line, cut to the stretch that ends at `end`.  cum[e]: items of the experts before e.
+template <int NT>
+__device__ __forceinline__ Segment segment_at(const RowsArgs &a, const int *cum, int i, int end)
+{
+    int lo = 0, hi = a.x.experts;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid] <= i)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const q8::ExpertRows x = q8::expert_rows_of(a.x, lo);
+    const int at = i - cum[lo], seg = at / a.groups;
+    const int chunk = seg / a.slices;
+    Segment s;
+    s.e = lo;
+    s.slice = seg - chunk * a.slices;
+    s.first = x.first + chunk * 8 * NT;
+    s.rows = min(8 * NT, x.count - chunk * 8 * NT);
+    s.b0 = s.slice * a.slice_blocks;
+    s.blocks = min(a.slice_blocks, a.x.nb - s.b0);
+    s.i0 = at - seg * a.groups;
+    s.i1 = min(a.groups, s.i0 + end - i);
+    s.next = i + s.i1 - s.i0;
+    return s;
+}
+
+// The pieces that warp w takes of a segment's items: units u .. end - 1, unit = item * pieces + piece.
+__device__ __forceinline__ int share(int units, int w) { return static_cast<int>(static_cast<int64_t>(units) * w / kWarps); }
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four codes -> 1152 + q as two f16x2 words.
+__device__ __forceinline__ void biased_f16(uint32_t q, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t x = q ^ 0x80808080u;
+    lo = __byte_perm(x, 0x64646464u, 0x5140);
+    hi = __byte_perm(x, 0x64646464u, 0x5342);
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+template <int NT, bool kTma>
+__global__ void __launch_bounds__(kThreads, 1)
+experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2)
+{
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ int scan[kWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, m = lane & 3;
+    const Layout<NT> L(a.slots, a.slice_blocks);
+    int *cum = reinterpret_cast<int *>(sm + L.cum);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L.bar) + warp * a.slots;
+    uint8_t *ring = sm + warp * a.slots * kSlotBytes;
+    if (kTma && lane == 0) {
+        for (int i = 0; i < a.slots; ++i) q8::mbar_init(bars + i, 1);
+        q8::fence_mbar_init();
+    }
+    q8::griddep_launch_dependents();
+    q8::griddep_wait();
+    {  // items before each expert: two experts a thread
+        int n[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            n[k] = 0;
+            if (2 * tid + k < a.x.experts) {
+                const q8::ExpertRows x = q8::expert_rows_of(a.x, 2 * tid + k);
+                if (x.bad && blockIdx.x == 0) atomicOr(&g_rows_err, q8::kErrData);
+                n[k] = (x.count + 8 * NT - 1) / (8 * NT) * a.slices * a.groups;
+            }
+        }
+        int v = n[0] + n[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(Q8_FULL_MASK, v, o);
+            if (lane >= o) v += u;
+        }
+        if (lane == 31) scan[warp] = v;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) v += scan[w];
+        if (2 * tid < a.x.experts) cum[2 * tid + 1] = v - n[1];
+        if (2 * tid + 1 < a.x.experts) cum[2 * tid + 2] = v;
+        if (tid == 0) cum[0] = 0;
+        __syncthreads();
+    }
+    const int items = cum[a.x.experts];
+    const int end = static_cast<int>(static_cast<int64_t>(items) * (blockIdx.x + 1) / gridDim.x);
+    int at = static_cast<int>(static_cast<int64_t>(items) * blockIdx.x / gridDim.x);
+    const int n16 = (a.x.n + 15) / 16;
+
+    // what this warp asks for: its units of this and later segments
+    Segment fs = {};
+    int fu = 0, fend = 0, fpieces = 1, fnext = at;
+    uint32_t asked = 0, used = 0;
+    auto fetch = [&]() {  // the next unit into the next slot; every slot it goes to has been read
+        while (fu == fend) {
+            if (fnext >= end) {
+                if (!kTma) asm volatile("cp.async.commit_group;" ::: "memory");
+                return;
+            }
+            fs = segment_at<NT>(a, cum, fnext, end);
+            fnext = fs.next;
+            fpieces = (fs.blocks + kPiece - 1) / kPiece;
+            const int units = (fs.i1 - fs.i0) * fpieces;
+            fu = share(units, warp), fend = share(units, warp + 1);
+        }
+        const int item = fs.i0 + fu / fpieces, piece = fu % fpieces;
+        const bool second = item >= n16;
+        const int row = 16 * (second ? item - n16 : item), b = fs.b0 + piece * kPiece;
+        uint8_t *slot = ring + (asked % a.slots) * kSlotBytes;
+        if (kTma) {
+            if (lane == 0) {
+                uint64_t *bar = bars + asked % a.slots;
+                q8::mbar_arrive_expect_tx(bar, 16 * kPitchTma);
+                q8::tma_load_2d(q8::smem_u32(slot), second ? &tmW2 : &tmW, b * 17, fs.e * a.x.n + row, q8::smem_u32(bar));
+            }
+        } else {
+            const uint8_t *w = second ? a.x.w2 : a.x.w;
+            const int cb = min(kPiece, fs.b0 + fs.blocks - b);
+            const int64_t most = static_cast<int64_t>(a.x.experts) * a.x.n * a.x.nb * 34;
+            for (int r = 0; r < 16; ++r) {
+                const int64_t from = ((static_cast<int64_t>(fs.e) * a.x.n + min(row + r, a.x.n - 1)) * a.x.nb + b) * 34;
+                for (int64_t o = (from & ~int64_t(3)) + 4 * lane; o < from + cb * 34; o += 128)
+                    cp_async4(q8::smem_u32(slot) + r * kPitchAny + static_cast<uint32_t>(o - (from & ~int64_t(3))), w + o,
+                              static_cast<int>(min(int64_t(4), most - o)));
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        ++asked;
+        ++fu;
+    };
+    for (int i = 0; i < a.slots; ++i) fetch();
+
+    bool dead = false;  // a wait ran out
+    while (at < end) {
+        const Segment s = segment_at<NT>(a, cum, at, end);
+        const int pieces = (s.blocks + kPiece - 1) / kPiece, units = (s.i1 - s.i0) * pieces;
+        __syncthreads();  // the segment before is done with the activations and the partial items
+        // activations: lane (g, m) of a fragment has words m and m + 4 of row g's block
+        for (int i = tid; i < s.blocks * s.rows * 4; i += kThreads) {
+            const int mm = i & 3, rb = i >> 2, b = rb / s.rows, r = rb - b * s.rows;
+            const int64_t src = q8::source_row(a.x, s.first + r);
+            if (src < 0) {
+                atomicOr(&g_rows_err, q8::kErrData);
+                continue;  // not stored either
+            }
+            const uint32_t *q = reinterpret_cast<const uint32_t *>(a.x.qs) + (src * a.x.nb + s.b0 + b) * 8;
+            const uint32_t d = __ldg(a.x.ds + src * a.x.nb + s.b0 + b);
+            uint4 f;
+            q8::i8x4_to_f16x4(__ldg(q + mm), f.x, f.y);
+            q8::i8x4_to_f16x4(__ldg(q + mm + 4), f.z, f.w);
+            const int t = r >> 3, rr = r & 7;
+            reinterpret_cast<uint4 *>(sm + L.act)[(b * NT + t) * 32 + 4 * rr + mm] = f;
+            if (mm == 0) {  // row 2m + x of the tile: scale at 4m + x, start of the accumulator at 4m + 2 + x
+                float *sc = reinterpret_cast<float *>(sm + L.scale) + (b * NT + t) * 16 + 4 * (rr >> 1) + (rr & 1);
+                sc[0] = __half2float(__ushort_as_half(static_cast<unsigned short>(d & 0xffffu)));
+                sc[2] = -1152.0f * static_cast<float>(static_cast<int16_t>(d >> 16));
+            }
+        }
+        __syncthreads();
+        const int nt = (s.rows + 7) >> 3;  // tiles of 8 rows
+        const int u0 = share(units, warp), u1 = share(units, warp + 1);
+        float4 acc[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int u = u0; u < u1; ++u) {
+            const int item = u / pieces, piece = u - item * pieces;
+            const int slot_i = used % a.slots;
+            if (kTma) {
+                if (!dead && !__all_sync(Q8_FULL_MASK, q8::mbar_wait_bounded(bars + slot_i, (used / a.slots) & 1u))) {
+                    dead = true;
+                    if (lane == 0) atomicOr(&g_rows_err, q8::kErrTimeout);
+                }
+            } else {
+                if (a.slots == 2)
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                else
+                    asm volatile("cp.async.wait_group 2;" ::: "memory");
+                __syncwarp();
+            }
+            const uint8_t *slot = ring + slot_i * kSlotBytes;
+            const int cb = min(kPiece, s.blocks - piece * kPiece);
+            const int pitch = kTma ? kPitchTma / 4 : kPitchAny / 4;
+            const uint32_t *w0 = reinterpret_cast<const uint32_t *>(slot) + g * pitch, *w1 = w0 + 8 * pitch;
+            // two bytes later where the row's piece starts between words (rows g and g + 8 alike)
+            int late = 0;
+            if (!kTma) {
+                const int second = s.i0 + item >= n16;
+                const int row = 16 * (s.i0 + item - (second ? n16 : 0)) + g;
+                late = static_cast<int>(((static_cast<int64_t>(s.e) * a.x.n + min(row, a.x.n - 1)) * a.x.nb + s.b0 + piece * kPiece) * 34) & 2;
+            }
+            const uint4 *bf = reinterpret_cast<const uint4 *>(sm + L.act) + static_cast<int64_t>(piece) * kPiece * NT * 32 + lane;
+            const float4 *sc = reinterpret_cast<const float4 *>(sm + L.scale) + piece * kPiece * NT * 4 + m;
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) {
+                if (!kTma && j >= cb) break;
+                uint32_t q[4];  // words m of rows g and g + 8, then words m + 4
+                float dw0, dw1;
+                if (kTma) {
+                    const int w = (34 * j) >> 2;
+                    const uint32_t h0 = w0[w], h1 = w1[w];
+                    if (j & 1) {  // the scale in the upper half, codes in whole words
+                        dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(h0 >> 16)));
+                        dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(h1 >> 16)));
+                        q[0] = w0[w + 1 + m], q[1] = w1[w + 1 + m], q[2] = w0[w + 5 + m], q[3] = w1[w + 5 + m];
+                    } else {
+                        dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(h0 & 0xffffu)));
+                        dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(h1 & 0xffffu)));
+                        q[0] = __byte_perm(w0[w + m], w0[w + m + 1], 0x5432), q[1] = __byte_perm(w1[w + m], w1[w + m + 1], 0x5432);
+                        q[2] = __byte_perm(w0[w + m + 4], w0[w + m + 5], 0x5432);
+                        q[3] = __byte_perm(w1[w + m + 4], w1[w + m + 5], 0x5432);
+                    }
+                } else {
+                    const int byte = late + 34 * j, w = byte >> 2;
+                    const uint32_t sel = byte & 2 ? 0x7654u : 0x5432u;
+                    const int up = byte & 2 ? 16 : 0;
+                    dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(w0[w] >> up)));
+                    dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(w1[w] >> up)));
+                    q[0] = __byte_perm(w0[w + m], w0[w + m + 1], sel), q[1] = __byte_perm(w1[w + m], w1[w + m + 1], sel);
+                    q[2] = __byte_perm(w0[w + m + 4], w0[w + m + 5], sel), q[3] = __byte_perm(w1[w + m + 4], w1[w + m + 5], sel);
+                }
+                uint32_t f0[4], f1[4];
+                biased_f16(q[0], f0[0], f0[2]);
+                biased_f16(q[1], f0[1], f0[3]);
+                biased_f16(q[2], f1[0], f1[2]);
+                biased_f16(q[3], f1[1], f1[3]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (t > 0 && t >= nt) break;
+                    const uint4 b = bf[(j * NT + t) * 32];
+                    const float4 d = sc[(j * NT + t) * 4];
+                    float c[4] = {d.z, d.w, d.z, d.w};
+                    mma16816(c, f0, b.x, b.y);
+                    mma16816(c, f1, b.z, b.w);
+                    acc[t].x = fmaf(dw0 * d.x, c[0], acc[t].x);
+                    acc[t].y = fmaf(dw0 * d.y, c[1], acc[t].y);
+                    acc[t].z = fmaf(dw1 * d.x, c[2], acc[t].z);
+                    acc[t].w = fmaf(dw1 * d.y, c[3], acc[t].w);
+                }
+            }
+            __syncwarp();  // all lanes have read the slot
+            ++used;
+            fetch();
+            if (piece == pieces - 1 || u == u1 - 1) {
+                const int first_u = max(u0, item * pieces);
+                const bool whole = first_u == item * pieces && piece == pieces - 1;
+                if (whole && !dead) {
+                    const int i = s.i0 + item;
+                    const bool second = i >= n16;
+                    const int row = 16 * (second ? i - n16 : i) + g;
+                    float *out = a.x.out + s.slice * a.part + (second ? a.x.n : 0) + row;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const float v[4] = {acc[t].x, acc[t].y, acc[t].z, acc[t].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int r = 8 * t + 2 * m + (k & 1);
+                            if (r < s.rows && row + 8 * (k >> 1) < a.x.n && q8::source_row(a.x, s.first + r) >= 0)
+                                out[(s.first + r) * a.x.ld + 8 * (k >> 1)] = v[k];
+                        }
+                    }
+                } else if (!whole) {  // the first item's end, or the last one's start
+                    float4 *p = reinterpret_cast<float4 *>(sm + L.part) + ((warp * 2 + (item == u0 / pieces ? 0 : 1)) * NT) * 32 + lane;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) p[32 * t] = acc[t];
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+        const bool failed = __syncthreads_or(dead);
+        // items that several warps share: warp w adds up the one that starts among its pieces and ends among later ones'
+        if (u1 > u0 && u1 % pieces != 0 && !failed) {
+            const int item = u1 / pieces;
+            if (item * pieces >= u0) {
+                float4 sum[NT];
+                const float4 *p = reinterpret_cast<const float4 *>(sm + L.part) + lane;
+                const int mine = (warp * 2 + (item == u0 / pieces ? 0 : 1)) * NT;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) sum[t] = p[(mine + t) * 32];
+                for (int w = warp + 1; w < kWarps; ++w) {  // every later warp with pieces of it: its first item
+                    const int v0 = share(units, w), v1 = share(units, w + 1);
+                    if (v0 >= (item + 1) * pieces) break;
+                    if (v1 == v0) continue;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const float4 x = p[(w * 2 * NT + t) * 32];
+                        sum[t].x += x.x, sum[t].y += x.y, sum[t].z += x.z, sum[t].w += x.w;
+                    }
+                }
+                const int i = s.i0 + item;
+                const bool second = i >= n16;
+                const int row = 16 * (second ? i - n16 : i) + g;
+                float *out = a.x.out + s.slice * a.part + (second ? a.x.n : 0) + row;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const float v[4] = {sum[t].x, sum[t].y, sum[t].z, sum[t].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = 8 * t + 2 * m + (k & 1);
+                        if (r < s.rows && row + 8 * (k >> 1) < a.x.n && q8::source_row(a.x, s.first + r) >= 0)
+                            out[(s.first + r) * a.x.ld + 8 * (k >> 1)] = v[k];
+                    }
+                }
+            }
+        }
+        at = s.next;
+        if (failed) break;
+    }
+    // copies in flight land before the CTA exits (after a wait ran out; else there are none)
+    if (kTma) {
+        for (; used < asked; ++used)
+            if (!q8::mbar_wait_bounded(bars + used % a.slots, (used / a.slots) & 1u, Q8_DRAIN_LIMIT_NS) && lane == 0)
+                atomicOr(&g_rows_err, q8::kErrTimeout);
+    } else {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+}
+
+// y = sum of the slices' outputs, in order; rows up to the last expert's end.
+__global__ void __launch_bounds__(256)
+experts_join_kernel(const float *__restrict__ part, int slices, int64_t stride, int64_t ld, const int32_t *__restrict__ offsets,
+                    int experts, int pairs, float *__restrict__ y)
+{
+    q8::griddep_launch_dependents();
+    q8::griddep_wait();
+    const int64_t total = static_cast<int64_t>(min(max(offsets[experts], 0), pairs)) * ld;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        float v = part[i];
+        for (int k = 1; k < slices; ++k) v += part[k * stride + i];
+        y[i] = v;
+    }
+}
+
+constexpr int kMaxSmem = 227 * 1024 - 1024;
+
+// NT, slices of k and slots of a ring for a call: a pure function of its sizes.
+struct Plan {
+    int nt, slices, slice_blocks, slots, smem;
+};
+
+template <int NT>
+Plan plan_of(int nb)
+{
+    Plan p = {NT, 1, nb, 2, 0};
+    while (Layout<NT>(2, p.slice_blocks).total > kMaxSmem) {
+        ++p.slices;
+        p.slice_blocks = ((nb + p.slices - 1) / p.slices + kPiece - 1) / kPiece * kPiece;
+    }
+    p.slices = (nb + p.slice_blocks - 1) / p.slice_blocks;
+    if (Layout<NT>(3, p.slice_blocks).total <= kMaxSmem) p.slots = 3;
+    p.smem = Layout<NT>(p.slots, p.slice_blocks).total;
+    return p;
+}
+
+Plan plan_for(int64_t experts, int64_t pairs, int64_t nb)
+{
+    return pairs > 4 * experts ? plan_of<2>(static_cast<int>(nb)) : plan_of<1>(static_cast<int>(nb));
+}
+
+template <int NT, bool kTma>
+int launch(const RowsArgs &a, const CUtensorMap &mw, const CUtensorMap &mw2, int smem, unsigned grid, int slot, cudaStream_t s)
+{
+    if (!q8::set_max_dynamic_smem(reinterpret_cast<const void *>(experts_rows_kernel<NT, kTma>), kMaxSmem, slot)) return Q8_ERR_LAUNCH;
+    return q8::launch_pdl(experts_rows_kernel<NT, kTma>, dim3(grid), dim3(kThreads), smem, s, a, mw, mw2);
+}
+
+} // namespace
+
+namespace q8 {
+
+int experts_rows_slices(int64_t experts, int64_t pairs, int64_t nb) { return plan_for(experts, pairs, nb).slices; }
+
+// out: slices x pairs x ld floats where there are several, else the rows themselves.
+int experts_rows_launch(const ExpertsArgs &x, float *out, cudaStream_t s)
+{
+    const Plan p = plan_for(x.experts, x.pairs, x.nb);
+    RowsArgs a = {};
+    a.x = x;
+    a.x.out = out;
+    a.groups = (x.n + 15) / 16 * (x.w2 ? 2 : 1);
+    a.slices = p.slices, a.slice_blocks = p.slice_blocks, a.slots = p.slots;
+    a.part = static_cast<int64_t>(x.pairs) * x.ld;
+    const bool tma = x.nb % kPiece == 0;
+    CUtensorMap mw = {}, mw2 = {};
+    const uint64_t rows = static_cast<uint64_t>(x.experts) * x.n, pitch = static_cast<uint64_t>(x.nb) * 34;
+    if (tma && (!make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT16, x.w, pitch / 2, rows, pitch, kPitchTma / 2, 16,
+                             CU_TENSOR_MAP_SWIZZLE_NONE) ||
+                (x.w2 && !make_map_2d(&mw2, CU_TENSOR_MAP_DATA_TYPE_UINT16, x.w2, pitch / 2, rows, pitch, kPitchTma / 2, 16,
+                                      CU_TENSOR_MAP_SWIZZLE_NONE))))
+        return Q8_ERR_LAUNCH;
+    const unsigned grid = static_cast<unsigned>(device_sm_count());
+    if (p.nt == 1)
+        return tma ? launch<1, true>(a, mw, mw2, p.smem, grid, 52, s) : launch<1, false>(a, mw, mw2, p.smem, grid, 53, s);
+    return tma ? launch<2, true>(a, mw, mw2, p.smem, grid, 54, s) : launch<2, false>(a, mw, mw2, p.smem, grid, 55, s);
+}
+
+int experts_join_launch(const float *part, int slices, const ExpertsArgs &x, cudaStream_t s)
+{
+    const int64_t total = static_cast<int64_t>(x.pairs) * x.ld, ctas = (total + 255) / 256, cap = static_cast<int64_t>(device_sm_count()) * 8;
+    return launch_pdl(experts_join_kernel, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(256), 0, s, part, slices, total,
+                      x.ld, x.offsets, x.experts, x.pairs, x.out);
+}
+
+unsigned int *experts_rows_error_word()
+{
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_rows_err) == cudaSuccess ? static_cast<unsigned int *>(p) : nullptr;
+}
+
+} // namespace q8

@@ -110,7 +110,7 @@ unsigned int *attn_rows_error_word();
 unsigned int *attn_tiles_error_word();
 unsigned int *kv_error_word();
 unsigned int *route_error_word();
-unsigned int *experts_error_word();
+unsigned int *experts_rows_error_word();
 unsigned int *experts_tiles_error_word();
 unsigned int *resnorm_error_word();
 int gemv_generic_launch(const void *w, int64_t n, int64_t k, const int8_t *qs, const uint32_t *ds, float *y,

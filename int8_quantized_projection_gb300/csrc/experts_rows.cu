@@ -8,8 +8,8 @@
 // two codes), and the accumulator starts at -1152 * ssum, which the plane has
 // for each block: |sum| < 2^24, so the integer is exact all the same.
 //
-//   The line.  A segment is up to 8 NT rows of one expert (and a slice of k where
-//   a row's activations would not fit shared memory); it has an item for every 16
+//   The line.  A segment is up to 8 rows of one expert (and a slice of k where a
+//   row's activations would not fit shared memory); it has an item for every 16
 //   weight rows.  All segments' items lie on one line, from the offsets on the
 //   device, and CTA c takes an equal stretch of it.  Within one segment of its
 //   stretch the CTA's warps share the items' 8-block pieces equally: a warp
@@ -17,8 +17,8 @@
 //   the ends to be added up through shared memory, in warp order.
 //   Weights come through a ring of a warp's own, a TMA box of 16 rows x 8 blocks
 //   (272 bytes a row) a slot; its next pieces are asked for across items and
-//   segments.  Where rows of blocks are not 16-byte aligned the warp copies 4
-//   bytes at a time.
+//   segments.  Where rows of blocks are not 16-byte aligned each row's piece is a
+//   bulk copy of its own, from the 16-byte boundary before it to the one behind.
 //   Activations of a segment lie in shared memory in the order of the MMA's B
 //   fragments, widened to f16 once; rows that the segment does not have are not
 //   written: what lies there enters columns that are not stored.
@@ -31,30 +31,28 @@ __device__ unsigned int g_rows_err;
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kPiece = 8;                    // blocks
 constexpr int kPitchTma = 34 * kPiece;       // 272
-constexpr int kPitchAny = kPitchTma + 4;     // 276
-constexpr int kSlotBytes = 16 * kPitchAny + 64;  // 4480, a multiple of 128
-static_assert(kSlotBytes % 128 == 0, "TMA destination");
+constexpr int kPitchAny = kPitchTma + 32;    // 304: a row may start up to 14 bytes late; 76 words, so rows g and words m fall on 32 banks
+constexpr int kSlots = 2;                    // of a warp's ring
+__host__ __device__ constexpr int slot_bytes(bool tma) { return 16 * (tma ? kPitchTma : kPitchAny); }
+static_assert(slot_bytes(true) % 128 == 0 && slot_bytes(false) % 128 == 0, "TMA destination");
 
 struct RowsArgs {
     q8::ExpertsArgs x;
     int groups, slices, slice_blocks;  // items of a segment, slices of k, their blocks (the last may have fewer)
-    int slots;                         // of a warp's ring
     int64_t part;                      // floats from one slice's output to the next's
 };
 
-// shared memory: ring [kWarps][slots] | B fragments [blocks][NT][32] uint4 | scales [blocks][NT][4] float4 |
-// partial items [kWarps][2][NT][32] float4 | row tables | barriers
-template <int NT>
+// shared memory: ring [kWarps][kSlots] | B fragments [blocks][32] uint4 | scales [blocks][4] float4 | items before each expert |
+// barriers; the partial items [kWarps][2][32] float4 take the fragments' place
 struct Layout {
-    int act, scale, part, cum, bar, total;
-    __host__ __device__ Layout(int slots, int blocks)
+    int act, scale, cum, bar, total;
+    __host__ __device__ Layout(bool tma, int blocks)
     {
-        act = kWarps * slots * kSlotBytes;
-        scale = act + blocks * NT * 512;
-        part = scale + blocks * NT * 64;
-        cum = part + kWarps * 2 * NT * 512;
+        act = kWarps * kSlots * slot_bytes(tma);
+        scale = act + (blocks > 2 * kWarps ? blocks : 2 * kWarps) * 512;
+        cum = scale + blocks * 64;
         bar = cum + (Q8_MAX_EXPERTS + 2) * 4;
-        total = bar + kWarps * 8 * slots + 128 + 64;
+        total = bar + kWarps * 8 * kSlots + 128;
     }
 };
 
@@ -66,7 +64,6 @@ struct Segment {
 };
 
 // The segment at place i of the line, cut to the stretch that ends at `end`.  cum[e]: items of the experts before e.
-template <int NT>
 __device__ __forceinline__ Segment segment_at(const RowsArgs &a, const int *cum, int i, int end)
 {
     int lo = 0, hi = a.x.experts;
@@ -83,8 +80,8 @@ __device__ __forceinline__ Segment segment_at(const RowsArgs &a, const int *cum,
     Segment s;
     s.e = lo;
     s.slice = seg - chunk * a.slices;
-    s.first = x.first + chunk * 8 * NT;
-    s.rows = min(8 * NT, x.count - chunk * 8 * NT);
+    s.first = x.first + chunk * 8;
+    s.rows = min(8, x.count - chunk * 8);
     s.b0 = s.slice * a.slice_blocks;
     s.blocks = min(a.slice_blocks, a.x.nb - s.b0);
     s.i0 = at - seg * a.groups;
@@ -98,7 +95,7 @@ __device__ __forceinline__ int share(int units, int w) { return static_cast<int>
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -111,24 +108,37 @@ __device__ __forceinline__ void biased_f16(uint32_t q, uint32_t &lo, uint32_t &h
     hi = __byte_perm(x, 0x64646464u, 0x5342);
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes)
+// A 16 x 8 item's values: this lane's rows g and g + 8 of the weights, sorted rows 2m and 2m + 1.
+__device__ __forceinline__ void store_item(const RowsArgs &a, const Segment &s, int item, int n16, int g, int m, float4 v)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    const int i = s.i0 + item;
+    const bool second = i >= n16;
+    const int row = 16 * (second ? i - n16 : i) + g;
+    float *out = a.x.out + s.slice * a.part + (second ? a.x.n : 0) + row;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int r = 2 * m + k;
+        if (r < s.rows && q8::source_row(a.x, s.first + r) >= 0) {
+            float *o = out + (s.first + r) * a.x.ld;
+            if (row < a.x.n) o[0] = k ? v.y : v.x;
+            if (row + 8 < a.x.n) o[8] = k ? v.w : v.z;
+        }
+    }
 }
 
-template <int NT, bool kTma>
+template <bool kTma>
 __global__ void __launch_bounds__(kThreads, 1)
 experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2)
 {
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ int scan[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, m = lane & 3;
-    const Layout<NT> L(a.slots, a.slice_blocks);
+    const Layout L(kTma, a.slice_blocks);
     int *cum = reinterpret_cast<int *>(sm + L.cum);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L.bar) + warp * a.slots;
-    uint8_t *ring = sm + warp * a.slots * kSlotBytes;
-    if (kTma && lane == 0) {
-        for (int i = 0; i < a.slots; ++i) q8::mbar_init(bars + i, 1);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L.bar) + warp * kSlots;
+    uint8_t *ring = sm + warp * kSlots * slot_bytes(kTma);
+    if (lane == 0) {
+        for (int i = 0; i < kSlots; ++i) q8::mbar_init(bars + i, 1);
         q8::fence_mbar_init();
     }
     q8::griddep_launch_dependents();
@@ -141,7 +151,7 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
             if (2 * tid + k < a.x.experts) {
                 const q8::ExpertRows x = q8::expert_rows_of(a.x, 2 * tid + k);
                 if (x.bad && blockIdx.x == 0) atomicOr(&g_rows_err, q8::kErrData);
-                n[k] = (x.count + 8 * NT - 1) / (8 * NT) * a.slices * a.groups;
+                n[k] = (x.count + 7) / 8 * a.slices * a.groups;
             }
         }
         int v = n[0] + n[1];
@@ -169,11 +179,8 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
     uint32_t asked = 0, used = 0;
     auto fetch = [&]() {  // the next unit into the next slot; every slot it goes to has been read
         while (fu == fend) {
-            if (fnext >= end) {
-                if (!kTma) asm volatile("cp.async.commit_group;" ::: "memory");
-                return;
-            }
-            fs = segment_at<NT>(a, cum, fnext, end);
+            if (fnext >= end) return;
+            fs = segment_at(a, cum, fnext, end);
             fnext = fs.next;
             fpieces = (fs.blocks + kPiece - 1) / kPiece;
             const int units = (fs.i1 - fs.i0) * fpieces;
@@ -182,33 +189,38 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
         const int item = fs.i0 + fu / fpieces, piece = fu % fpieces;
         const bool second = item >= n16;
         const int row = 16 * (second ? item - n16 : item), b = fs.b0 + piece * kPiece;
-        uint8_t *slot = ring + (asked % a.slots) * kSlotBytes;
+        uint8_t *slot = ring + (asked % kSlots) * slot_bytes(kTma);
+        uint64_t *bar = bars + asked % kSlots;
         if (kTma) {
             if (lane == 0) {
-                uint64_t *bar = bars + asked % a.slots;
                 q8::mbar_arrive_expect_tx(bar, 16 * kPitchTma);
                 q8::tma_load_2d(q8::smem_u32(slot), second ? &tmW2 : &tmW, b * 17, fs.e * a.x.n + row, q8::smem_u32(bar));
             }
         } else {
             const uint8_t *w = second ? a.x.w2 : a.x.w;
             const int cb = min(kPiece, fs.b0 + fs.blocks - b);
-            const int64_t most = static_cast<int64_t>(a.x.experts) * a.x.n * a.x.nb * 34;
-            for (int r = 0; r < 16; ++r) {
-                const int64_t from = ((static_cast<int64_t>(fs.e) * a.x.n + min(row + r, a.x.n - 1)) * a.x.nb + b) * 34;
-                for (int64_t o = (from & ~int64_t(3)) + 4 * lane; o < from + cb * 34; o += 128)
-                    cp_async4(q8::smem_u32(slot) + r * kPitchAny + static_cast<uint32_t>(o - (from & ~int64_t(3))), w + o,
-                              static_cast<int>(min(int64_t(4), most - o)));
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            const int64_t most = static_cast<int64_t>(a.x.experts) * a.x.n * a.x.nb * 34, whole = most & ~int64_t(15);
+            const int64_t from =
+                ((static_cast<int64_t>(fs.e) * a.x.n + min(row + (lane & 15), a.x.n - 1)) * a.x.nb + b) * 34;
+            const int64_t start = from & ~int64_t(15), stop = (from + cb * 34 + 15) & ~int64_t(15);
+            const int bytes = lane < 16 ? static_cast<int>(max(min(stop, whole) - start, int64_t(0))) : 0;
+            uint8_t *dst = slot + (lane & 15) * kPitchAny;
+            const int all = __reduce_add_sync(Q8_FULL_MASK, bytes);
+            if (lane == 0) q8::mbar_arrive_expect_tx(bar, all);
+            __syncwarp();
+            if (bytes) q8::bulk_g2s(dst, w + start, bytes, bar);
+            if (lane < 16 && stop > whole)  // the last bytes of the last matrix, where they do not fill 16
+                for (int64_t o = max(whole, start); o < most; o += 2)
+                    *reinterpret_cast<uint16_t *>(dst + (o - start)) = *reinterpret_cast<const uint16_t *>(w + o);
         }
         ++asked;
         ++fu;
     };
-    for (int i = 0; i < a.slots; ++i) fetch();
+    for (int i = 0; i < kSlots; ++i) fetch();
 
     bool dead = false;  // a wait ran out
     while (at < end) {
-        const Segment s = segment_at<NT>(a, cum, at, end);
+        const Segment s = segment_at(a, cum, at, end);
         const int pieces = (s.blocks + kPiece - 1) / kPiece, units = (s.i1 - s.i0) * pieces;
         __syncthreads();  // the segment before is done with the activations and the partial items
         // activations: lane (g, m) of a fragment has words m and m + 4 of row g's block
@@ -224,48 +236,38 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
             uint4 f;
             q8::i8x4_to_f16x4(__ldg(q + mm), f.x, f.y);
             q8::i8x4_to_f16x4(__ldg(q + mm + 4), f.z, f.w);
-            const int t = r >> 3, rr = r & 7;
-            reinterpret_cast<uint4 *>(sm + L.act)[(b * NT + t) * 32 + 4 * rr + mm] = f;
-            if (mm == 0) {  // row 2m + x of the tile: scale at 4m + x, start of the accumulator at 4m + 2 + x
-                float *sc = reinterpret_cast<float *>(sm + L.scale) + (b * NT + t) * 16 + 4 * (rr >> 1) + (rr & 1);
+            reinterpret_cast<uint4 *>(sm + L.act)[b * 32 + 4 * r + mm] = f;
+            if (mm == 0) {  // row 2m + x: scale at 4m + x, start of the accumulator at 4m + 2 + x
+                float *sc = reinterpret_cast<float *>(sm + L.scale) + b * 16 + 4 * (r >> 1) + (r & 1);
                 sc[0] = __half2float(__ushort_as_half(static_cast<unsigned short>(d & 0xffffu)));
                 sc[2] = -1152.0f * static_cast<float>(static_cast<int16_t>(d >> 16));
             }
         }
         __syncthreads();
-        const int nt = (s.rows + 7) >> 3;  // tiles of 8 rows
         const int u0 = share(units, warp), u1 = share(units, warp + 1);
-        float4 acc[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;  // rows g and g + 8
+        float4 part[2];  // the parts of the first and the last item that other warps have pieces of
+        part[0] = part[1] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int u = u0; u < u1; ++u) {
             const int item = u / pieces, piece = u - item * pieces;
-            const int slot_i = used % a.slots;
-            if (kTma) {
-                if (!dead && !__all_sync(Q8_FULL_MASK, q8::mbar_wait_bounded(bars + slot_i, (used / a.slots) & 1u))) {
-                    dead = true;
-                    if (lane == 0) atomicOr(&g_rows_err, q8::kErrTimeout);
-                }
-            } else {
-                if (a.slots == 2)
-                    asm volatile("cp.async.wait_group 1;" ::: "memory");
-                else
-                    asm volatile("cp.async.wait_group 2;" ::: "memory");
-                __syncwarp();
+            const int slot_i = used % kSlots;
+            if (!dead && !__all_sync(Q8_FULL_MASK, q8::mbar_wait_bounded(bars + slot_i, (used / kSlots) & 1u))) {
+                dead = true;
+                if (lane == 0) atomicOr(&g_rows_err, q8::kErrTimeout);
             }
-            const uint8_t *slot = ring + slot_i * kSlotBytes;
+            const uint8_t *slot = ring + slot_i * slot_bytes(kTma);
             const int cb = min(kPiece, s.blocks - piece * kPiece);
             const int pitch = kTma ? kPitchTma / 4 : kPitchAny / 4;
             const uint32_t *w0 = reinterpret_cast<const uint32_t *>(slot) + g * pitch, *w1 = w0 + 8 * pitch;
-            // two bytes later where the row's piece starts between words (rows g and g + 8 alike)
-            int late = 0;
+            int late = 0;  // where the row's piece starts in its slot (rows g and g + 8 alike: 8 rows are a multiple of 16 bytes)
             if (!kTma) {
                 const int second = s.i0 + item >= n16;
+                // rows behind the matrix are copies of its last one, whose piece starts elsewhere: they are not stored
                 const int row = 16 * (s.i0 + item - (second ? n16 : 0)) + g;
-                late = static_cast<int>(((static_cast<int64_t>(s.e) * a.x.n + min(row, a.x.n - 1)) * a.x.nb + s.b0 + piece * kPiece) * 34) & 2;
+                late = static_cast<int>(((static_cast<int64_t>(s.e) * a.x.n + min(row, a.x.n - 1)) * a.x.nb + s.b0 + piece * kPiece) * 34) & 15;
             }
-            const uint4 *bf = reinterpret_cast<const uint4 *>(sm + L.act) + static_cast<int64_t>(piece) * kPiece * NT * 32 + lane;
-            const float4 *sc = reinterpret_cast<const float4 *>(sm + L.scale) + piece * kPiece * NT * 4 + m;
+            const uint4 *bf = reinterpret_cast<const uint4 *>(sm + L.act) + piece * kPiece * 32 + lane;
+            const float4 *sc = reinterpret_cast<const float4 *>(sm + L.scale) + piece * kPiece * 4 + m;
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) {
                 if (!kTma && j >= cb) break;
@@ -299,19 +301,14 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
                 biased_f16(q[1], f0[1], f0[3]);
                 biased_f16(q[2], f1[0], f1[2]);
                 biased_f16(q[3], f1[1], f1[3]);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (t > 0 && t >= nt) break;
-                    const uint4 b = bf[(j * NT + t) * 32];
-                    const float4 d = sc[(j * NT + t) * 4];
-                    float c[4] = {d.z, d.w, d.z, d.w};
-                    mma16816(c, f0, b.x, b.y);
-                    mma16816(c, f1, b.z, b.w);
-                    acc[t].x = fmaf(dw0 * d.x, c[0], acc[t].x);
-                    acc[t].y = fmaf(dw0 * d.y, c[1], acc[t].y);
-                    acc[t].z = fmaf(dw1 * d.x, c[2], acc[t].z);
-                    acc[t].w = fmaf(dw1 * d.y, c[3], acc[t].w);
-                }
+                const uint4 b = bf[j * 32];
+                const float4 d = sc[j * 4];
+                float c[4] = {d.z, d.w, d.z, d.w};
+                mma16816(c, f0, b.x, b.y);
+                mma16816(c, f1, b.z, b.w);
+                const float2 da = make_float2(d.x, d.y);
+                acc0 = __ffma2_rn(__fmul2_rn(make_float2(dw0, dw0), da), make_float2(c[0], c[1]), acc0);
+                acc1 = __ffma2_rn(__fmul2_rn(make_float2(dw1, dw1), da), make_float2(c[2], c[3]), acc1);
             }
             __syncwarp();  // all lanes have read the slot
             ++used;
@@ -319,77 +316,40 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
             if (piece == pieces - 1 || u == u1 - 1) {
                 const int first_u = max(u0, item * pieces);
                 const bool whole = first_u == item * pieces && piece == pieces - 1;
-                if (whole && !dead) {
-                    const int i = s.i0 + item;
-                    const bool second = i >= n16;
-                    const int row = 16 * (second ? i - n16 : i) + g;
-                    float *out = a.x.out + s.slice * a.part + (second ? a.x.n : 0) + row;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const float v[4] = {acc[t].x, acc[t].y, acc[t].z, acc[t].w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int r = 8 * t + 2 * m + (k & 1);
-                            if (r < s.rows && row + 8 * (k >> 1) < a.x.n && q8::source_row(a.x, s.first + r) >= 0)
-                                out[(s.first + r) * a.x.ld + 8 * (k >> 1)] = v[k];
-                        }
-                    }
-                } else if (!whole) {  // the first item's end, or the last one's start
-                    float4 *p = reinterpret_cast<float4 *>(sm + L.part) + ((warp * 2 + (item == u0 / pieces ? 0 : 1)) * NT) * 32 + lane;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) p[32 * t] = acc[t];
-                }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 v = make_float4(acc0.x, acc0.y, acc1.x, acc1.y);
+                if (!whole)
+                    part[item == u0 / pieces ? 0 : 1] = v;
+                else if (!dead)
+                    store_item(a, s, item, n16, g, m, v);
+                acc0 = acc1 = make_float2(0.f, 0.f);
             }
         }
-        const bool failed = __syncthreads_or(dead);
+        const bool failed = __syncthreads_or(dead);  // the fragments have been read: the partial items take their place
+        float4 *parts = reinterpret_cast<float4 *>(sm + L.act) + lane;
+        parts[(2 * warp) * 32] = part[0], parts[(2 * warp + 1) * 32] = part[1];
+        __syncthreads();
         // items that several warps share: warp w adds up the one that starts among its pieces and ends among later ones'
         if (u1 > u0 && u1 % pieces != 0 && !failed) {
             const int item = u1 / pieces;
             if (item * pieces >= u0) {
-                float4 sum[NT];
-                const float4 *p = reinterpret_cast<const float4 *>(sm + L.part) + lane;
-                const int mine = (warp * 2 + (item == u0 / pieces ? 0 : 1)) * NT;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) sum[t] = p[(mine + t) * 32];
+                float4 sum = part[item == u0 / pieces ? 0 : 1];
                 for (int w = warp + 1; w < kWarps; ++w) {  // every later warp with pieces of it: its first item
                     const int v0 = share(units, w), v1 = share(units, w + 1);
                     if (v0 >= (item + 1) * pieces) break;
                     if (v1 == v0) continue;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const float4 x = p[(w * 2 * NT + t) * 32];
-                        sum[t].x += x.x, sum[t].y += x.y, sum[t].z += x.z, sum[t].w += x.w;
-                    }
+                    const float4 x = parts[2 * w * 32];
+                    sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
                 }
-                const int i = s.i0 + item;
-                const bool second = i >= n16;
-                const int row = 16 * (second ? i - n16 : i) + g;
-                float *out = a.x.out + s.slice * a.part + (second ? a.x.n : 0) + row;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const float v[4] = {sum[t].x, sum[t].y, sum[t].z, sum[t].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int r = 8 * t + 2 * m + (k & 1);
-                        if (r < s.rows && row + 8 * (k >> 1) < a.x.n && q8::source_row(a.x, s.first + r) >= 0)
-                            out[(s.first + r) * a.x.ld + 8 * (k >> 1)] = v[k];
-                    }
-                }
+                store_item(a, s, item, n16, g, m, sum);
             }
         }
         at = s.next;
         if (failed) break;
     }
     // copies in flight land before the CTA exits (after a wait ran out; else there are none)
-    if (kTma) {
-        for (; used < asked; ++used)
-            if (!q8::mbar_wait_bounded(bars + used % a.slots, (used / a.slots) & 1u, Q8_DRAIN_LIMIT_NS) && lane == 0)
-                atomicOr(&g_rows_err, q8::kErrTimeout);
-    } else {
-        asm volatile("cp.async.wait_all;" ::: "memory");
-    }
+    for (; used < asked; ++used)
+        if (!q8::mbar_wait_bounded(bars + used % kSlots, (used / kSlots) & 1u, Q8_DRAIN_LIMIT_NS) && lane == 0)
+            atomicOr(&g_rows_err, q8::kErrTimeout);
 }
 
 // y = sum of the slices' outputs, in order; rows up to the last expert's end.
@@ -410,52 +370,46 @@ experts_join_kernel(const float *__restrict__ part, int slices, int64_t stride, 
 
 constexpr int kMaxSmem = 227 * 1024 - 1024;
 
-// NT, slices of k and slots of a ring for a call: a pure function of its sizes.
+// The slices of k: as few as fit the activations of 8 rows beside the ring, of whole pieces.
 struct Plan {
-    int nt, slices, slice_blocks, slots, smem;
+    int slices, slice_blocks, smem;
 };
 
-template <int NT>
 Plan plan_of(int nb)
 {
-    Plan p = {NT, 1, nb, 2, 0};
-    while (Layout<NT>(2, p.slice_blocks).total > kMaxSmem) {
+    const bool tma = nb % kPiece == 0;
+    Plan p = {1, nb, 0};
+    while (Layout(tma, p.slice_blocks).total > kMaxSmem) {
         ++p.slices;
         p.slice_blocks = ((nb + p.slices - 1) / p.slices + kPiece - 1) / kPiece * kPiece;
     }
     p.slices = (nb + p.slice_blocks - 1) / p.slice_blocks;
-    if (Layout<NT>(3, p.slice_blocks).total <= kMaxSmem) p.slots = 3;
-    p.smem = Layout<NT>(p.slots, p.slice_blocks).total;
+    p.smem = Layout(tma, p.slice_blocks).total;
     return p;
 }
 
-Plan plan_for(int64_t experts, int64_t pairs, int64_t nb)
-{
-    return pairs > 4 * experts ? plan_of<2>(static_cast<int>(nb)) : plan_of<1>(static_cast<int>(nb));
-}
-
-template <int NT, bool kTma>
+template <bool kTma>
 int launch(const RowsArgs &a, const CUtensorMap &mw, const CUtensorMap &mw2, int smem, unsigned grid, int slot, cudaStream_t s)
 {
-    if (!q8::set_max_dynamic_smem(reinterpret_cast<const void *>(experts_rows_kernel<NT, kTma>), kMaxSmem, slot)) return Q8_ERR_LAUNCH;
-    return q8::launch_pdl(experts_rows_kernel<NT, kTma>, dim3(grid), dim3(kThreads), smem, s, a, mw, mw2);
+    if (!q8::set_max_dynamic_smem(reinterpret_cast<const void *>(experts_rows_kernel<kTma>), kMaxSmem, slot)) return Q8_ERR_LAUNCH;
+    return q8::launch_pdl(experts_rows_kernel<kTma>, dim3(grid), dim3(kThreads), smem, s, a, mw, mw2);
 }
 
 } // namespace
 
 namespace q8 {
 
-int experts_rows_slices(int64_t experts, int64_t pairs, int64_t nb) { return plan_for(experts, pairs, nb).slices; }
+int experts_rows_slices(int64_t nb) { return plan_of(static_cast<int>(nb)).slices; }
 
 // out: slices x pairs x ld floats where there are several, else the rows themselves.
 int experts_rows_launch(const ExpertsArgs &x, float *out, cudaStream_t s)
 {
-    const Plan p = plan_for(x.experts, x.pairs, x.nb);
+    const Plan p = plan_of(x.nb);
     RowsArgs a = {};
     a.x = x;
     a.x.out = out;
     a.groups = (x.n + 15) / 16 * (x.w2 ? 2 : 1);
-    a.slices = p.slices, a.slice_blocks = p.slice_blocks, a.slots = p.slots;
+    a.slices = p.slices, a.slice_blocks = p.slice_blocks;
     a.part = static_cast<int64_t>(x.pairs) * x.ld;
     const bool tma = x.nb % kPiece == 0;
     CUtensorMap mw = {}, mw2 = {};
@@ -466,9 +420,7 @@ int experts_rows_launch(const ExpertsArgs &x, float *out, cudaStream_t s)
                                       CU_TENSOR_MAP_SWIZZLE_NONE))))
         return Q8_ERR_LAUNCH;
     const unsigned grid = static_cast<unsigned>(device_sm_count());
-    if (p.nt == 1)
-        return tma ? launch<1, true>(a, mw, mw2, p.smem, grid, 52, s) : launch<1, false>(a, mw, mw2, p.smem, grid, 53, s);
-    return tma ? launch<2, true>(a, mw, mw2, p.smem, grid, 54, s) : launch<2, false>(a, mw, mw2, p.smem, grid, 55, s);
+    return tma ? launch<true>(a, mw, mw2, p.smem, grid, 52, s) : launch<false>(a, mw, mw2, p.smem, grid, 53, s);
 }
 
 int experts_join_launch(const float *part, int slices, const ExpertsArgs &x, cudaStream_t s)

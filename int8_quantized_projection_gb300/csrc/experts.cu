@@ -70,7 +70,7 @@ extern "C" size_t q8_0_experts_gemm_workspace_bytes(int64_t experts, int64_t n, 
 {
     if (!sizes_ok(experts, n, k, plane_rows, top_k, pairs)) return 0;
     if (many_rows(experts, pairs)) return q8::experts_tiles_workspace(k, pairs);
-    const int slices = q8::experts_rows_slices(k / 32);
+    const int slices = q8::experts_rows_slices(experts, pairs, k / 32);
     return slices > 1 ? static_cast<size_t>(slices) * pairs * n * 4 : 0;
 }
 
@@ -94,7 +94,7 @@ extern "C" int q8_0_experts_gemm(const void *w, int64_t experts, int64_t n, int6
     if (!need) return q8::experts_rows_launch(a, y, s);
     float *part = static_cast<float *>(workspace);
     const int st = q8::experts_rows_launch(a, part, s);
-    return st != Q8_OK ? st : q8::experts_join_launch(part, q8::experts_rows_slices(k / 32), a, s);
+    return st != Q8_OK ? st : q8::experts_join_launch(part, q8::experts_rows_slices(experts, pairs, k / 32), a, s);
 }
 
 extern "C" size_t q8_0_experts_gate_up_workspace_bytes(int64_t experts, int64_t nf, int64_t k, int64_t plane_rows,
@@ -102,7 +102,7 @@ extern "C" size_t q8_0_experts_gate_up_workspace_bytes(int64_t experts, int64_t 
 {
     if (!sizes_ok(experts, nf, k, plane_rows, top_k, pairs) || nf % 32 != 0) return 0;
     if (many_rows(experts, pairs)) return q8::experts_tiles_workspace(k, pairs);
-    return static_cast<size_t>(q8::experts_rows_slices(k / 32)) * pairs * nf * 8;
+    return static_cast<size_t>(q8::experts_rows_slices(experts, pairs, k / 32)) * pairs * nf * 8;
 }
 
 extern "C" int q8_0_experts_gate_up(const void *w_gate, const void *w_up, int64_t experts, int64_t nf, int64_t k,
@@ -131,7 +131,7 @@ extern "C" int q8_0_experts_gate_up(const void *w_gate, const void *w_up, int64_
     if (st != Q8_OK) return st;
     const int64_t ctas = (pairs * nf / 4 + 255) / 256;
     return q8::launch_pdl(experts_swiglu_kernel, dim3(static_cast<unsigned>(ctas < 152 * 8 ? ctas : 152 * 8)), dim3(256), 0, s,
-                          reinterpret_cast<const float4 *>(gu), q8::experts_rows_slices(k / 32),
+                          reinterpret_cast<const float4 *>(gu), q8::experts_rows_slices(experts, pairs, k / 32),
                           static_cast<int>(nf / 4), offsets, static_cast<int>(experts),
                           static_cast<int>(pairs), reinterpret_cast<uint32_t *>(qs_out), ds_out);
 }

@@ -26,7 +26,7 @@ int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out,
 
 // A few rows an expert (experts_rows.cu): the f32 rows into out, or, where k is cut into several slices, their parts [slices][pairs][ld],
 // which the join adds up into a.out.
-int experts_rows_slices(int64_t nb);
+int experts_rows_slices(int64_t experts, int64_t pairs, int64_t nb);
 int experts_rows_launch(const ExpertsArgs &a, float *out, cudaStream_t s);
 int experts_join_launch(const float *part, int slices, const ExpertsArgs &a, cudaStream_t s);
 

@@ -8,7 +8,7 @@
 // two codes), and the accumulator starts at -1152 * ssum, which the plane has
 // for each block: |sum| < 2^24, so the integer is exact all the same.
 //
-//   The line.  A segment is up to 8 rows of one expert (and a slice of k where a
+//   The line.  A segment is up to 8 or 16 rows of one expert (and a slice of k where a
 //   row's activations would not fit shared memory); it has an item for every 16
 //   weight rows.  All segments' items lie on one line, from the offsets on the
 //   device, and CTA c takes an equal stretch of it.  Within one segment of its
@@ -42,15 +42,15 @@ struct RowsArgs {
     int64_t part;                      // floats from one slice's output to the next's
 };
 
-// shared memory: ring [kWarps][kSlots] | B fragments [blocks][32] uint4 | scales [blocks][4] float4 | items before each expert |
-// barriers; the partial items [kWarps][2][32] float4 take the fragments' place
+// shared memory: ring [kWarps][kSlots] | B fragments [blocks][NT][32] uint4 | scales [blocks][NT][4] float4 | items before each
+// expert | barriers; the partial items [kWarps][2][NT][32] float4 take the fragments' place.  nt: tiles of 8 rows a segment has.
 struct Layout {
     int act, scale, cum, bar, total;
-    __host__ __device__ Layout(bool tma, int blocks)
+    __host__ __device__ Layout(bool tma, int nt, int blocks)
     {
         act = kWarps * kSlots * slot_bytes(tma);
-        scale = act + (blocks > 2 * kWarps ? blocks : 2 * kWarps) * 512;
-        cum = scale + blocks * 64;
+        scale = act + (blocks > 2 * kWarps ? blocks : 2 * kWarps) * 512 * nt;
+        cum = scale + blocks * 64 * nt;
         bar = cum + (Q8_MAX_EXPERTS + 2) * 4;
         total = bar + kWarps * 8 * kSlots + 128;
     }
@@ -64,6 +64,7 @@ struct Segment {
 };
 
 // The segment at place i of the line, cut to the stretch that ends at `end`.  cum[e]: items of the experts before e.
+template <int NT>
 __device__ __forceinline__ Segment segment_at(const RowsArgs &a, const int *cum, int i, int end)
 {
     int lo = 0, hi = a.x.experts;
@@ -80,8 +81,8 @@ __device__ __forceinline__ Segment segment_at(const RowsArgs &a, const int *cum,
     Segment s;
     s.e = lo;
     s.slice = seg - chunk * a.slices;
-    s.first = x.first + chunk * 8;
-    s.rows = min(8, x.count - chunk * 8);
+    s.first = x.first + chunk * 8 * NT;
+    s.rows = min(8 * NT, x.count - chunk * 8 * NT);
     s.b0 = s.slice * a.slice_blocks;
     s.blocks = min(a.slice_blocks, a.x.nb - s.b0);
     s.i0 = at - seg * a.groups;
@@ -108,8 +109,8 @@ __device__ __forceinline__ void biased_f16(uint32_t q, uint32_t &lo, uint32_t &h
     hi = __byte_perm(x, 0x64646464u, 0x5342);
 }
 
-// A 16 x 8 item's values: this lane's rows g and g + 8 of the weights, sorted rows 2m and 2m + 1.
-__device__ __forceinline__ void store_item(const RowsArgs &a, const Segment &s, int item, int n16, int g, int m, float4 v)
+// A 16 x 8 tile's values: this lane's rows g and g + 8 of the weights, sorted rows 8t + 2m and 8t + 2m + 1.
+__device__ __forceinline__ void store_item(const RowsArgs &a, const Segment &s, int item, int n16, int g, int m, int t, float4 v)
 {
     const int i = s.i0 + item;
     const bool second = i >= n16;
@@ -117,7 +118,7 @@ __device__ __forceinline__ void store_item(const RowsArgs &a, const Segment &s, 
     float *out = a.x.out + s.slice * a.part + (second ? a.x.n : 0) + row;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int r = 2 * m + k;
+        const int r = 8 * t + 2 * m + k;
         if (r < s.rows && q8::source_row(a.x, s.first + r) >= 0) {
             float *o = out + (s.first + r) * a.x.ld;
             if (row < a.x.n) o[0] = k ? v.y : v.x;
@@ -126,14 +127,68 @@ __device__ __forceinline__ void store_item(const RowsArgs &a, const Segment &s, 
     }
 }
 
-template <bool kTma>
+// One unit: 16 weight rows x up to 8 blocks against T tiles of 8 rows.  late: byte of the slot's rows where the pieces start.
+template <bool kTma, int NT, int T>
+__device__ __forceinline__ void unit(const uint8_t *slot, int late, int cb, const uint4 *bf, const float4 *sc, int g, int m,
+                                     float2 (&acc)[NT][2])
+{
+    const int pitch = kTma ? kPitchTma / 4 : kPitchAny / 4;
+    const uint32_t *w0 = reinterpret_cast<const uint32_t *>(slot) + g * pitch, *w1 = w0 + 8 * pitch;
+#pragma unroll
+                for (int j = 0; j < kPiece; ++j) {
+                    if (!kTma && j >= cb) break;
+                    uint32_t q[4];  // words m of rows g and g + 8, then words m + 4
+                    float dw0, dw1;
+                    if (kTma) {
+                        const int w = (34 * j) >> 2;
+                        const uint32_t h0 = w0[w], h1 = w1[w];
+                        if (j & 1) {  // the scale in the upper half, codes in whole words
+                            dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(h0 >> 16)));
+                            dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(h1 >> 16)));
+                            q[0] = w0[w + 1 + m], q[1] = w1[w + 1 + m], q[2] = w0[w + 5 + m], q[3] = w1[w + 5 + m];
+                        } else {
+                            dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(h0 & 0xffffu)));
+                            dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(h1 & 0xffffu)));
+                            q[0] = __byte_perm(w0[w + m], w0[w + m + 1], 0x5432), q[1] = __byte_perm(w1[w + m], w1[w + m + 1], 0x5432);
+                            q[2] = __byte_perm(w0[w + m + 4], w0[w + m + 5], 0x5432);
+                            q[3] = __byte_perm(w1[w + m + 4], w1[w + m + 5], 0x5432);
+                        }
+                    } else {
+                        const int byte = late + 34 * j, w = byte >> 2;
+                        const uint32_t sel = byte & 2 ? 0x7654u : 0x5432u;
+                        const int up = byte & 2 ? 16 : 0;
+                        dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(w0[w] >> up)));
+                        dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(w1[w] >> up)));
+                        q[0] = __byte_perm(w0[w + m], w0[w + m + 1], sel), q[1] = __byte_perm(w1[w + m], w1[w + m + 1], sel);
+                        q[2] = __byte_perm(w0[w + m + 4], w0[w + m + 5], sel), q[3] = __byte_perm(w1[w + m + 4], w1[w + m + 5], sel);
+                    }
+                    uint32_t f0[4], f1[4];
+                    biased_f16(q[0], f0[0], f0[2]);
+                    biased_f16(q[1], f0[1], f0[3]);
+                    biased_f16(q[2], f1[0], f1[2]);
+                    biased_f16(q[3], f1[1], f1[3]);
+            #pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const uint4 b = bf[(j * NT + t) * 32];
+            const float4 d = sc[(j * NT + t) * 4];
+            float c[4] = {d.z, d.w, d.z, d.w};
+            mma16816(c, f0, b.x, b.y);
+            mma16816(c, f1, b.z, b.w);
+            const float2 da = make_float2(d.x, d.y);
+            acc[t][0] = __ffma2_rn(__fmul2_rn(make_float2(dw0, dw0), da), make_float2(c[0], c[1]), acc[t][0]);
+            acc[t][1] = __ffma2_rn(__fmul2_rn(make_float2(dw1, dw1), da), make_float2(c[2], c[3]), acc[t][1]);
+        }
+    }
+}
+
+template <bool kTma, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
 experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2)
 {
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ int scan[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, m = lane & 3;
-    const Layout L(kTma, a.slice_blocks);
+    const Layout L(kTma, NT, a.slice_blocks);
     int *cum = reinterpret_cast<int *>(sm + L.cum);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L.bar) + warp * kSlots;
     uint8_t *ring = sm + warp * kSlots * slot_bytes(kTma);
@@ -151,7 +206,7 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
             if (2 * tid + k < a.x.experts) {
                 const q8::ExpertRows x = q8::expert_rows_of(a.x, 2 * tid + k);
                 if (x.bad && blockIdx.x == 0) atomicOr(&g_rows_err, q8::kErrData);
-                n[k] = (x.count + 7) / 8 * a.slices * a.groups;
+                n[k] = (x.count + 8 * NT - 1) / (8 * NT) * a.slices * a.groups;
             }
         }
         int v = n[0] + n[1];
@@ -175,18 +230,20 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
 
     // what this warp asks for: its units of this and later segments
     Segment fs = {};
-    int fu = 0, fend = 0, fpieces = 1, fnext = at;
+    int fu = 0, fend = 0, fpieces = 1, fnext = at, fitem = 0, fpiece = 0;
     uint32_t asked = 0, used = 0;
     auto fetch = [&]() {  // the next unit into the next slot; every slot it goes to has been read
         while (fu == fend) {
             if (fnext >= end) return;
-            fs = segment_at(a, cum, fnext, end);
+            fs = segment_at<NT>(a, cum, fnext, end);
             fnext = fs.next;
             fpieces = (fs.blocks + kPiece - 1) / kPiece;
             const int units = (fs.i1 - fs.i0) * fpieces;
             fu = share(units, warp), fend = share(units, warp + 1);
+            fitem = fu / fpieces, fpiece = fu - fitem * fpieces;
         }
-        const int item = fs.i0 + fu / fpieces, piece = fu % fpieces;
+        const int item = fs.i0 + fitem, piece = fpiece;
+        if (++fpiece == fpieces) fpiece = 0, ++fitem;
         const bool second = item >= n16;
         const int row = 16 * (second ? item - n16 : item), b = fs.b0 + piece * kPiece;
         uint8_t *slot = ring + (asked % kSlots) * slot_bytes(kTma);
@@ -220,7 +277,7 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
 
     bool dead = false;  // a wait ran out
     while (at < end) {
-        const Segment s = segment_at(a, cum, at, end);
+        const Segment s = segment_at<NT>(a, cum, at, end);
         const int pieces = (s.blocks + kPiece - 1) / kPiece, units = (s.i1 - s.i0) * pieces;
         __syncthreads();  // the segment before is done with the activations and the partial items
         // activations: lane (g, m) of a fragment has words m and m + 4 of row g's block
@@ -236,20 +293,25 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
             uint4 f;
             q8::i8x4_to_f16x4(__ldg(q + mm), f.x, f.y);
             q8::i8x4_to_f16x4(__ldg(q + mm + 4), f.z, f.w);
-            reinterpret_cast<uint4 *>(sm + L.act)[b * 32 + 4 * r + mm] = f;
-            if (mm == 0) {  // row 2m + x: scale at 4m + x, start of the accumulator at 4m + 2 + x
-                float *sc = reinterpret_cast<float *>(sm + L.scale) + b * 16 + 4 * (r >> 1) + (r & 1);
+            reinterpret_cast<uint4 *>(sm + L.act)[(b * NT + (r >> 3)) * 32 + 4 * (r & 7) + mm] = f;
+            if (mm == 0) {  // row 2m + x of a tile: scale at 4m + x, start of the accumulator at 4m + 2 + x
+                float *sc = reinterpret_cast<float *>(sm + L.scale) + (b * NT + (r >> 3)) * 16 + 4 * ((r & 7) >> 1) + (r & 1);
                 sc[0] = __half2float(__ushort_as_half(static_cast<unsigned short>(d & 0xffffu)));
                 sc[2] = -1152.0f * static_cast<float>(static_cast<int16_t>(d >> 16));
             }
         }
         __syncthreads();
         const int u0 = share(units, warp), u1 = share(units, warp + 1);
-        float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;  // rows g and g + 8
-        float4 part[2];  // the parts of the first and the last item that other warps have pieces of
-        part[0] = part[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float2 acc[NT][2];               // rows g and g + 8 of the weights
+        float4 head[NT], tail[NT];       // the parts of the first and the last item that other warps have pieces of
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            acc[t][0] = acc[t][1] = make_float2(0.f, 0.f);
+            head[t] = tail[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        int item = u0 / pieces, piece = u0 - item * pieces;
+        const int item0 = item;
         for (int u = u0; u < u1; ++u) {
-            const int item = u / pieces, piece = u - item * pieces;
             const int slot_i = used % kSlots;
             if (!dead && !__all_sync(Q8_FULL_MASK, q8::mbar_wait_bounded(bars + slot_i, (used / kSlots) & 1u))) {
                 dead = true;
@@ -257,8 +319,6 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
             }
             const uint8_t *slot = ring + slot_i * slot_bytes(kTma);
             const int cb = min(kPiece, s.blocks - piece * kPiece);
-            const int pitch = kTma ? kPitchTma / 4 : kPitchAny / 4;
-            const uint32_t *w0 = reinterpret_cast<const uint32_t *>(slot) + g * pitch, *w1 = w0 + 8 * pitch;
             int late = 0;  // where the row's piece starts in its slot (rows g and g + 8 alike: 8 rows are a multiple of 16 bytes)
             if (!kTma) {
                 const int second = s.i0 + item >= n16;
@@ -266,81 +326,52 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
                 const int row = 16 * (s.i0 + item - (second ? n16 : 0)) + g;
                 late = static_cast<int>(((static_cast<int64_t>(s.e) * a.x.n + min(row, a.x.n - 1)) * a.x.nb + s.b0 + piece * kPiece) * 34) & 15;
             }
-            const uint4 *bf = reinterpret_cast<const uint4 *>(sm + L.act) + piece * kPiece * 32 + lane;
-            const float4 *sc = reinterpret_cast<const float4 *>(sm + L.scale) + piece * kPiece * 4 + m;
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j) {
-                if (!kTma && j >= cb) break;
-                uint32_t q[4];  // words m of rows g and g + 8, then words m + 4
-                float dw0, dw1;
-                if (kTma) {
-                    const int w = (34 * j) >> 2;
-                    const uint32_t h0 = w0[w], h1 = w1[w];
-                    if (j & 1) {  // the scale in the upper half, codes in whole words
-                        dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(h0 >> 16)));
-                        dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(h1 >> 16)));
-                        q[0] = w0[w + 1 + m], q[1] = w1[w + 1 + m], q[2] = w0[w + 5 + m], q[3] = w1[w + 5 + m];
-                    } else {
-                        dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(h0 & 0xffffu)));
-                        dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(h1 & 0xffffu)));
-                        q[0] = __byte_perm(w0[w + m], w0[w + m + 1], 0x5432), q[1] = __byte_perm(w1[w + m], w1[w + m + 1], 0x5432);
-                        q[2] = __byte_perm(w0[w + m + 4], w0[w + m + 5], 0x5432);
-                        q[3] = __byte_perm(w1[w + m + 4], w1[w + m + 5], 0x5432);
-                    }
-                } else {
-                    const int byte = late + 34 * j, w = byte >> 2;
-                    const uint32_t sel = byte & 2 ? 0x7654u : 0x5432u;
-                    const int up = byte & 2 ? 16 : 0;
-                    dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(w0[w] >> up)));
-                    dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(w1[w] >> up)));
-                    q[0] = __byte_perm(w0[w + m], w0[w + m + 1], sel), q[1] = __byte_perm(w1[w + m], w1[w + m + 1], sel);
-                    q[2] = __byte_perm(w0[w + m + 4], w0[w + m + 5], sel), q[3] = __byte_perm(w1[w + m + 4], w1[w + m + 5], sel);
-                }
-                uint32_t f0[4], f1[4];
-                biased_f16(q[0], f0[0], f0[2]);
-                biased_f16(q[1], f0[1], f0[3]);
-                biased_f16(q[2], f1[0], f1[2]);
-                biased_f16(q[3], f1[1], f1[3]);
-                const uint4 b = bf[j * 32];
-                const float4 d = sc[j * 4];
-                float c[4] = {d.z, d.w, d.z, d.w};
-                mma16816(c, f0, b.x, b.y);
-                mma16816(c, f1, b.z, b.w);
-                const float2 da = make_float2(d.x, d.y);
-                acc0 = __ffma2_rn(__fmul2_rn(make_float2(dw0, dw0), da), make_float2(c[0], c[1]), acc0);
-                acc1 = __ffma2_rn(__fmul2_rn(make_float2(dw1, dw1), da), make_float2(c[2], c[3]), acc1);
-            }
+            const uint4 *bf = reinterpret_cast<const uint4 *>(sm + L.act) + piece * kPiece * NT * 32 + lane;
+            const float4 *sc = reinterpret_cast<const float4 *>(sm + L.scale) + piece * kPiece * NT * 4 + m;
+            if (NT == 1 || s.rows <= 8)
+                unit<kTma, NT, 1>(slot, late, cb, bf, sc, g, m, acc);
+            else
+                unit<kTma, NT, NT>(slot, late, cb, bf, sc, g, m, acc);
             __syncwarp();  // all lanes have read the slot
             ++used;
             fetch();
             if (piece == pieces - 1 || u == u1 - 1) {
                 const int first_u = max(u0, item * pieces);
                 const bool whole = first_u == item * pieces && piece == pieces - 1;
-                const float4 v = make_float4(acc0.x, acc0.y, acc1.x, acc1.y);
-                if (!whole)
-                    part[item == u0 / pieces ? 0 : 1] = v;
-                else if (!dead)
-                    store_item(a, s, item, n16, g, m, v);
-                acc0 = acc1 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const float4 v = make_float4(acc[t][0].x, acc[t][0].y, acc[t][1].x, acc[t][1].y);
+                    if (whole) {
+                        if (!dead && 8 * t < s.rows) store_item(a, s, item, n16, g, m, t, v);
+                    } else if (item == item0) {
+                        head[t] = v;
+                    } else {
+                        tail[t] = v;
+                    }
+                    acc[t][0] = acc[t][1] = make_float2(0.f, 0.f);
+                }
             }
+            if (++piece == pieces) piece = 0, ++item;
         }
         const bool failed = __syncthreads_or(dead);  // the fragments have been read: the partial items take their place
         float4 *parts = reinterpret_cast<float4 *>(sm + L.act) + lane;
-        parts[(2 * warp) * 32] = part[0], parts[(2 * warp + 1) * 32] = part[1];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) parts[(2 * warp * NT + t) * 32] = head[t], parts[((2 * warp + 1) * NT + t) * 32] = tail[t];
         __syncthreads();
         // items that several warps share: warp w adds up the one that starts among its pieces and ends among later ones'
-        if (u1 > u0 && u1 % pieces != 0 && !failed) {
-            const int item = u1 / pieces;
-            if (item * pieces >= u0) {
-                float4 sum = part[item == u0 / pieces ? 0 : 1];
+        if (u1 > u0 && piece != 0 && !failed && item * pieces >= u0) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (8 * t >= s.rows) break;
+                float4 sum = item == item0 ? head[t] : tail[t];
                 for (int w = warp + 1; w < kWarps; ++w) {  // every later warp with pieces of it: its first item
                     const int v0 = share(units, w), v1 = share(units, w + 1);
                     if (v0 >= (item + 1) * pieces) break;
                     if (v1 == v0) continue;
-                    const float4 x = parts[2 * w * 32];
+                    const float4 x = parts[(2 * w * NT + t) * 32];
                     sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
                 }
-                store_item(a, s, item, n16, g, m, sum);
+                store_item(a, s, item, n16, g, m, t, sum);
             }
         }
         at = s.next;
@@ -370,41 +401,45 @@ experts_join_kernel(const float *__restrict__ part, int slices, int64_t stride, 
 
 constexpr int kMaxSmem = 227 * 1024 - 1024;
 
-// The slices of k: as few as fit the activations of 8 rows beside the ring, of whole pieces.
+// Tiles of 8 rows a segment has, and the slices of k: as few as fit its activations beside the ring, of whole pieces.
 struct Plan {
-    int slices, slice_blocks, smem;
+    int nt, slices, slice_blocks, smem;
 };
 
-Plan plan_of(int nb)
+Plan plan_of(int64_t experts, int64_t pairs, int nb)
 {
     const bool tma = nb % kPiece == 0;
-    Plan p = {1, nb, 0};
-    while (Layout(tma, p.slice_blocks).total > kMaxSmem) {
+    Plan p = {pairs > 4 * experts ? 2 : 1, 1, nb, 0};
+    while (Layout(tma, p.nt, p.slice_blocks).total > kMaxSmem) {
         ++p.slices;
         p.slice_blocks = ((nb + p.slices - 1) / p.slices + kPiece - 1) / kPiece * kPiece;
     }
     p.slices = (nb + p.slice_blocks - 1) / p.slice_blocks;
-    p.smem = Layout(tma, p.slice_blocks).total;
+    p.smem = Layout(tma, p.nt, p.slice_blocks).total;
     return p;
 }
 
-template <bool kTma>
+template <bool kTma, int NT>
 int launch(const RowsArgs &a, const CUtensorMap &mw, const CUtensorMap &mw2, int smem, unsigned grid, int slot, cudaStream_t s)
 {
-    if (!q8::set_max_dynamic_smem(reinterpret_cast<const void *>(experts_rows_kernel<kTma>), kMaxSmem, slot)) return Q8_ERR_LAUNCH;
-    return q8::launch_pdl(experts_rows_kernel<kTma>, dim3(grid), dim3(kThreads), smem, s, a, mw, mw2);
+    if (!q8::set_max_dynamic_smem(reinterpret_cast<const void *>(experts_rows_kernel<kTma, NT>), kMaxSmem, slot))
+        return Q8_ERR_LAUNCH;
+    return q8::launch_pdl(experts_rows_kernel<kTma, NT>, dim3(grid), dim3(kThreads), smem, s, a, mw, mw2);
 }
 
 } // namespace
 
 namespace q8 {
 
-int experts_rows_slices(int64_t nb) { return plan_of(static_cast<int>(nb)).slices; }
+int experts_rows_slices(int64_t experts, int64_t pairs, int64_t nb)
+{
+    return plan_of(experts, pairs, static_cast<int>(nb)).slices;
+}
 
 // out: slices x pairs x ld floats where there are several, else the rows themselves.
 int experts_rows_launch(const ExpertsArgs &x, float *out, cudaStream_t s)
 {
-    const Plan p = plan_of(x.nb);
+    const Plan p = plan_of(x.experts, x.pairs, x.nb);
     RowsArgs a = {};
     a.x = x;
     a.x.out = out;
@@ -420,7 +455,9 @@ int experts_rows_launch(const ExpertsArgs &x, float *out, cudaStream_t s)
                                       CU_TENSOR_MAP_SWIZZLE_NONE))))
         return Q8_ERR_LAUNCH;
     const unsigned grid = static_cast<unsigned>(device_sm_count());
-    return tma ? launch<true>(a, mw, mw2, p.smem, grid, 52, s) : launch<false>(a, mw, mw2, p.smem, grid, 53, s);
+    if (p.nt == 1)
+        return tma ? launch<true, 1>(a, mw, mw2, p.smem, grid, 52, s) : launch<false, 1>(a, mw, mw2, p.smem, grid, 53, s);
+    return tma ? launch<true, 2>(a, mw, mw2, p.smem, grid, 54, s) : launch<false, 2>(a, mw, mw2, p.smem, grid, 55, s);
 }
 
 int experts_join_launch(const float *part, int slices, const ExpertsArgs &x, cudaStream_t s)

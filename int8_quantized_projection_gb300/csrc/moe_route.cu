@@ -20,9 +20,9 @@ __device__ unsigned int g_route_err;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kMaxChunk = 1024;            // tokens of a CTA at most
-constexpr int kOneLaunch = 128;            // tokens that one CTA routes by itself
+constexpr int kOneLaunch = 64;             // tokens that one CTA routes by itself (two rounds of its warps; 128 take 13 us, in two launches 7)
 constexpr int kBitBytes = 40 * 1024;       // shared memory of the bit sets
-static_assert(kThreads >= Q8_MAX_EXPERTS && kBitBytes >= 4 * Q8_MAX_EXPERTS, "a thread and a word of bits per expert");
+static_assert(kThreads == Q8_MAX_EXPERTS && kBitBytes >= 4 * Q8_MAX_EXPERTS, "a thread and a word of bits per expert");
 
 struct RouteArgs {
     const float *logits;
@@ -196,30 +196,38 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const __grid_con
         a.counts[static_cast<int64_t>(blockIdx.x) * a.experts + e] = n;
 }
 
-// The places, from the counts of all chunks: every CTA adds them up for itself (chunks x experts integers from L2).
+// The places, from the counts of all chunks: every CTA adds them up for itself (chunks x experts integers from L2), all threads
+// taking part (a thread per expert alone: 13 us for 3325 tokens and 128 experts, so 8).
 __global__ void __launch_bounds__(kThreads) route_place_kernel(const __grid_constant__ RouteArgs a)
 {
     extern __shared__ uint32_t bits[];
-    __shared__ int s_base[Q8_MAX_EXPERTS], s_scan[kWarps];
+    __shared__ int s_base[Q8_MAX_EXPERTS], s_all[Q8_MAX_EXPERTS], s_before[Q8_MAX_EXPERTS], s_scan[kWarps];
     q8::griddep_launch_dependents();
     q8::griddep_wait();
     const int e = threadIdx.x, words = (a.chunk + 31) >> 5;
     const int t0 = blockIdx.x * a.chunk, t1 = min(a.tokens, t0 + a.chunk);
     for (int i = threadIdx.x; i < a.experts * words; i += kThreads) bits[i] = 0u;
-    int all = 0, before = 0;
-    if (e < a.experts)
-        for (int c = 0; c < a.chunks; ++c) {
-            const int n = a.counts[static_cast<int64_t>(c) * a.experts + e];
-            all += n;
-            if (c < static_cast<int>(blockIdx.x)) before += n;
-        }
+    s_all[e] = s_before[e] = 0;
     __syncthreads();
+    const int parts = kThreads / a.experts, part = e / a.experts, mine = e - part * a.experts;
+    if (part < parts) {
+        int all = 0, before = 0;
+#pragma unroll 8
+        for (int c = part; c < a.chunks; c += parts) {
+            const int n = a.counts[static_cast<int64_t>(c) * a.experts + mine];
+            all += n;
+            before += c < static_cast<int>(blockIdx.x) ? n : 0;
+        }
+        atomicAdd(&s_all[mine], all);
+        atomicAdd(&s_before[mine], before);
+    }
     const int64_t p0 = static_cast<int64_t>(t0) * a.top_k;
     for (int i = threadIdx.x; i < (t1 - t0) * a.top_k; i += kThreads) {
         const int id = a.ids[p0 + i], t = i / a.top_k;
         if (id >= 0) atomicOr(&bits[id * words + (t >> 5)], 1u << (t & 31));
     }
-    place_pairs(a, bits, words, t0, t1, all, before, s_base, s_scan);  // its barriers come before it reads the bits
+    __syncthreads();
+    place_pairs(a, bits, words, t0, t1, s_all[e], s_before[e], s_base, s_scan);
 }
 
 // Tokens of a CTA: all of them up to kOneLaunch, else an SM's share in whole words of bits, which have to fit kBitBytes.

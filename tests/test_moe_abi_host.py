@@ -68,7 +68,7 @@ def test_route_arguments(lib):
 
 def test_route_workspace(lib):
     size = lib.q8_moe_route_workspace_bytes
-    assert size(1, 64, 8) == 0 and size(128, 64, 8) == 0 and size(129, 64, 8) > 0
+    assert size(1, 64, 8) == 0 and size(64, 64, 8) == 0 and size(65, 64, 8) > 0
     assert size(0, 64, 8) == 0 and size(500, 64, 65) == 0 and size(500, 2000, 8) == 0
     assert size(3325, 128, 8) == 104 * 128 * 4  # chunks of 32 tokens
 

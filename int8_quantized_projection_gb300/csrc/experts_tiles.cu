@@ -31,9 +31,11 @@
 //   32 rows, and writes the plane of silu(gate) * up.
 //
 // Warp roles (512 threads):
-//   warp 0     MMA issuer, tensor memory          warp 1      weight copies, 8 blocks a slot
-//   warp 2     activation copies, 2 blocks a stage    warp 3   their scales
-//   warps 4-7  widen weights                      warps 8-15  epilogue: a TMEM lane quarter and 64 columns each
+//   warps 0, 1   MMA issuers, 64 columns each (warp 0: tensor memory)
+//   warp 2       weight copies, 8 blocks a slot     warp 3   activation copies and scales, 2 blocks a stage
+//   warps 4-7    widen weights                      warps 8-15   epilogue: a TMEM lane quarter and 64 columns each
+// The 64-column halves of a tile have accumulators and hand-overs of their own, two buffers each, so that one half loads from
+// tensor memory while the other adds up.
 // Every mbarrier wait is bounded; a wait that runs out sets the CTA abort flag
 // and the error word, and all roles drain and exit.
 #include "experts_common.cuh"
@@ -44,7 +46,7 @@ __device__ unsigned int g_tiles_err;
 
 constexpr int BM = 128, kGroup = 64, kMaxGroups = 2, BN = kGroup * kMaxGroups;
 constexpr int kStages = 3, kRawSlots = 2, kAcc = 2;
-constexpr int kTmemBuf = 2 * BN, kTmemCols = kAcc * kTmemBuf;  // integers, then scales
+constexpr int kTmemBuf = 2 * kGroup, kTmemCols = kMaxGroups * kAcc * kTmemBuf;  // integers, then scales
 constexpr int kThreads = 512, kWidenThreads = 128, kEpiWarps = 8, kEpiThreads = 256;
 constexpr int kRegsCtl = 40, kRegsWiden = 56, kRegsEpi = 208;
 static_assert(128 * kRegsCtl + kWidenThreads * kRegsWiden + kEpiThreads * kRegsEpi <= 128 * kThreads, "register split");
@@ -62,8 +64,10 @@ constexpr int OFF_ZERO = kStages * kStageBytes;         // columns 8 .. 15 of ev
 constexpr int OFF_RAW = OFF_ZERO + kScBytes;
 constexpr int OFF_SWAP = OFF_RAW + kRawSlots * kRawBytes;  // [8 warps][16 columns][32] f32
 constexpr int OFF_CUM = OFF_SWAP + kEpiWarps * 16 * 32 * 4;  // row tiles before each expert
-constexpr int kBars = 2 * kRawSlots + 2 * kStages + kAcc + 1;
-constexpr int OFF_BAR = OFF_CUM + (Q8_MAX_EXPERTS + 2) * 4;
+constexpr int kTable = 96;                              // tiles of this CTA that are looked up once
+constexpr int OFF_TABLE = (OFF_CUM + (Q8_MAX_EXPERTS + 2) * 4 + 15) / 16 * 16;
+constexpr int kBars = 2 * kRawSlots + 2 * kStages + 2 * kAcc + 2;
+constexpr int OFF_BAR = OFF_TABLE + kTable * 16;
 constexpr int OFF_MISC = OFF_BAR + kBars * 8;           // abort flag, TMEM address, sums of the scan
 constexpr int kSmemBytes = OFF_MISC + 16 + 96 + 1024;   // + alignment slack
 static_assert(OFF_BAR % 8 == 0 && kStageBytes % 1024 == 0 && OFF_RAW % 128 == 0 && kSmemBytes <= 227 * 1024, "shared memory");
@@ -75,8 +79,8 @@ struct Bars {
     __device__ uint32_t raw_empty(int s) const { return at(kRawSlots + s); }
     __device__ uint32_t ab_full(int s) const { return at(2 * kRawSlots + s); }
     __device__ uint32_t ab_empty(int s) const { return at(2 * kRawSlots + kStages + s); }
-    __device__ uint32_t acc_full(int s) const { return at(2 * kRawSlots + 2 * kStages + s); }
-    __device__ uint32_t drain() const { return acc_full(kAcc); }
+    __device__ uint32_t acc_full(int half, int s) const { return at(2 * kRawSlots + 2 * kStages + half * kAcc + s); }
+    __device__ uint32_t drain(int half) const { return acc_full(2, half); }
 };
 
 // ---------------------------------------------------------------------------
@@ -241,14 +245,14 @@ __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes)
 // A buffer of tensor memory is handed back by a named barrier: the epilogue warps arrive, the MMA warp waits, some 25 cycles
 // for a wait where an mbarrier takes 100 and its arrival as long again.  Both sides pass each barrier once per block, whatever
 // the abort flag says, so neither is left waiting.
-constexpr int kHandOver = 2;  // barriers 2 and 3
-__device__ __forceinline__ void acc_release(int buf)
+constexpr int kHandOver = 2;  // barriers 2 .. 5
+__device__ __forceinline__ void acc_release(int half, int buf)
 {
-    asm volatile("bar.arrive %0, %1;" ::"r"(kHandOver + buf), "n"(kEpiThreads + 32) : "memory");
+    asm volatile("bar.arrive %0, %1;" ::"r"(kHandOver + half * kAcc + buf), "n"(kEpiThreads / 2 + 32) : "memory");
 }
-__device__ __forceinline__ void acc_acquire(int buf)
+__device__ __forceinline__ void acc_acquire(int half, int buf)
 {
-    asm volatile("bar.sync %0, %1;" ::"r"(kHandOver + buf), "n"(kEpiThreads + 32) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(kHandOver + half * kAcc + buf), "n"(kEpiThreads / 2 + 32) : "memory");
 }
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
@@ -309,11 +313,35 @@ __device__ __forceinline__ Tile tile_at(const q8::ExpertsArgs &a, const int *cum
     return t;
 }
 
+// Tile i of this CTA, from the table where it is there.
+__device__ __forceinline__ Tile tile_of(const q8::ExpertsArgs &a, const int *cum, const int4 *table, int weight_tiles, int i)
+{
+    if (i >= kTable) return tile_at(a, cum, weight_tiles, blockIdx.x + i * gridDim.x);
+    const int4 v = table[i];
+    return {v.x & 0xffff, v.y, v.z, v.w, v.x >> 16};
+}
+
 // Weight row (of an expert's) at position r of a tile; in a pair of matrices positions 32 .. 63 and 96 .. 127 are w2's.
 template <bool kPair>
 __device__ __forceinline__ int tile_row(int nt, int r)
 {
     return kPair ? 64 * nt + 32 * (r >> 6) + (r & 31) : BM * nt + r;
+}
+
+// v[i] of all lanes joined into lane i: each step halves the columns that a lane still has and doubles the lanes they stand for.
+template <typename T, typename F>
+__device__ __forceinline__ T lane_columns(T (&v)[32], int lane, F join)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const T keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
+            v[i] = join(keep, __shfl_xor_sync(Q8_FULL_MASK, send, o));
+        }
+    }
+    return v[0];
 }
 
 // kPair: w and w2, the plane of silu(w x) * (w2 x); else w and f32 rows.  kTma: nb % 8 == 0.
@@ -344,9 +372,9 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
         init(kRawSlots, 1);           // raw_full: copied bytes
         init(kRawSlots, 4);           // raw_empty: a warp each
         init(kStages, 6);             // ab_full: four widening warps, the copied bytes, their scales
-        init(kStages, 1);             // ab_empty: tcgen05.commit
-        init(kAcc, 1);                // acc_full: tcgen05.commit
-        init(1, 1);                   // drain
+        init(kStages, 2);             // ab_empty: tcgen05.commit of both issuers
+        init(2 * kAcc, 1);            // acc_full: tcgen05.commit
+        init(2, 1);                   // drain
         q8::fence_mbar_init();
     }
     if (warp == 0) {
@@ -391,60 +419,74 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
         if (2 * tid + 1 < a.experts) cum[2 * tid + 2] = v;
         if (tid == 0) cum[0] = 0;
     }
+    __syncthreads();
+    const int weight_tiles = kPair ? (a.n + 63) / 64 : (a.n + BM - 1) / BM;
+    const int total = cum[a.experts] * weight_tiles;  // below 2^31: y would not fit otherwise
+    const int tiles = (total - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    int4 *table = reinterpret_cast<int4 *>(sm + OFF_TABLE);
+    if (tid < kTable && tid < tiles) {
+        const Tile t = tile_at(a, cum, weight_tiles, blockIdx.x + tid * gridDim.x);
+        table[tid] = make_int4(t.e | t.groups << 16, t.nt, t.row0, t.rows);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
     const int nb = a.nb, stages = (nb + 1) / 2, pieces = (nb + kPiece - 1) / kPiece;
-    const int weight_tiles = kPair ? (a.n + 63) / 64 : (a.n + BM - 1) / BM;
-    const int total = cum[a.experts] * weight_tiles;  // below 2^31: y would not fit otherwise
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsCtl>();
-        if (warp == 0) {
-            // ------------------------------------------------------------ MMA issuer
+        if (warp < 2) {
+            // ------------------------------------------------------------ MMA issuers
+            const int half = warp;
+            const uint32_t idesc = mma_desc(kGroup);
             uint32_t blk = 0, slot = 0, phase = 0;  // blocks done, stage and its phase
-            for (int at = blockIdx.x; at < total; at += gridDim.x) {
-                const Tile t = tile_at(a, cum, weight_tiles, at);
-                const uint32_t idesc = mma_desc(t.groups * kGroup);
+            for (int i = 0; i < tiles; ++i) {
+                const bool mine = half < tile_of(a, cum, table, weight_tiles, i).groups;
                 for (int j = 0; j < nb; j += 2) {
                     const uint32_t stage = base + slot * kStageBytes;
-                    const uint64_t pa = smem_desc(stage), pb = smem_desc(stage + OFF_B);
-                    const uint64_t sa = scale_desc(stage + OFF_DW, base + OFF_ZERO), sb = scale_desc(stage + OFF_DA, base + OFF_ZERO);
+                    const uint64_t pa = smem_desc(stage), pb = smem_desc(stage + OFF_B + half * (kBBytes / 2));
+                    const uint64_t sa = scale_desc(stage + OFF_DW, base + OFF_ZERO);
+                    const uint64_t sb = scale_desc(stage + OFF_DA + half * (kScBytes / 2), base + OFF_ZERO);
                     wait_go(B.ab_full(slot), phase, abort_flag);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        if (u == 1 && j + 1 == nb) break;
-                        if (blk >= kAcc) acc_acquire(blk % kAcc);
-                        tc_fence_after();
-                        const uint32_t d = tmem + (blk % kAcc) * kTmemBuf;
-                        // a scale operand's next block: its columns 8 .. 15 lie that much nearer
-                        constexpr uint64_t next = (kScBytes >> 4) - (static_cast<uint64_t>(kScBytes >> 4) << 16);
-                        if (elect_one()) {
-                            tc_mma_f16(d, pa + 4 * u, pb + 4 * u, idesc, 0);
-                            tc_mma_f16(d, pa + 4 * u + 2, pb + 4 * u + 2, idesc, 1);  // 32 bytes on
-                            tc_mma_f16(d + BN, sa + u * next, sb + u * next, idesc, 0);
-                            tc_commit(B.acc_full(blk % kAcc));
-                            if (u == 1 || j + 1 == nb) tc_commit(B.ab_empty(slot));
-                        }
+                    if (!mine) {
+                        if (lane == 0) arrive(B.ab_empty(slot));
                         __syncwarp();
-                        ++blk;
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            if (u == 1 && j + 1 == nb) break;
+                            if (blk >= kAcc) acc_acquire(half, blk % kAcc);
+                            tc_fence_after();
+                            const uint32_t d = tmem + (half * kAcc + blk % kAcc) * kTmemBuf;
+                            // a scale operand's next block: its columns 8 .. 15 lie that much nearer
+                            constexpr uint64_t next = (kScBytes >> 4) - (static_cast<uint64_t>(kScBytes >> 4) << 16);
+                            if (elect_one()) {
+                                tc_mma_f16(d, pa + 4 * u, pb + 4 * u, idesc, 0);
+                                tc_mma_f16(d, pa + 4 * u + 2, pb + 4 * u + 2, idesc, 1);  // 32 bytes on
+                                tc_mma_f16(d + kGroup, sa + u * next, sb + u * next, idesc, 0);
+                                tc_commit(B.acc_full(half, blk % kAcc));
+                                if (u == 1 || j + 1 == nb) tc_commit(B.ab_empty(slot));
+                            }
+                            __syncwarp();
+                            ++blk;
+                        }
                     }
                     if (++slot == kStages) slot = 0, phase ^= 1u;
                 }
             }
-            for (int k = 0; k < kAcc && k < static_cast<int>(blk); ++k) acc_acquire(k);  // the last blocks'
+            for (int k = 0; k < kAcc && k < static_cast<int>(blk); ++k) acc_acquire(half, k);  // the last blocks'
             // every MMA must have completed before its operands and TMEM go
-            if (elect_one()) tc_commit(B.drain());
+            if (elect_one()) tc_commit(B.drain(half));
             __syncwarp();
-            drain_bar(B.drain(), 0);
-        } else if (warp == 1 && kTma) {
+            drain_bar(B.drain(half), 0);
+        } else if (warp == 2 && kTma) {
             // ------------------------------------------------------------ weights
             uint32_t n = 0;
             bool ok = true;
-            for (int at = blockIdx.x; at < total && ok; at += gridDim.x) {
-                const Tile t = tile_at(a, cum, weight_tiles, at);
+            for (int i = 0; i < tiles && ok; ++i) {
+                const Tile t = tile_of(a, cum, table, weight_tiles, i);
                 const int row = t.e * a.n + tile_row<kPair>(t.nt, 0);
                 for (int s = 0; s < pieces; ++s, ++n) {
                     const int slot = n % kRawSlots;
@@ -454,9 +496,9 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     if (elect_one()) {
                         expect_tx(B.raw_full(slot), BM * kPitchTma);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)  // 32 rows each
-                            q8::tma_load_2d(dst + i * 32 * kPitchTma, kPair && (i & 1) ? &tmW2 : &tmW, kPitchTma / 2 * s,
-                                            row + (kPair ? 32 * (i >> 1) : 32 * i), B.raw_full(slot));
+                        for (int k = 0; k < 4; ++k)  // 32 rows each
+                            q8::tma_load_2d(dst + k * 32 * kPitchTma, kPair && (k & 1) ? &tmW2 : &tmW, kPitchTma / 2 * s,
+                                            row + (kPair ? 32 * (k >> 1) : 32 * k), B.raw_full(slot));
                     }
                     __syncwarp();
                 }
@@ -464,32 +506,12 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
             // the last copies must have landed before the CTA exits
             for (uint32_t s = n < kRawSlots ? 0 : n - kRawSlots; s < n; ++s)
                 drain_bar(B.raw_full(s % kRawSlots), (s / kRawSlots) & 1u);
-        } else if (warp == 2) {
-            // ------------------------------------------------------------ activations
-            uint32_t n = 0;
-            bool ok = true;
-            for (int at = blockIdx.x; at < total && ok; at += gridDim.x) {
-                const Tile t = tile_at(a, cum, weight_tiles, at);
-                for (int s = 0; s < stages; ++s, ++n) {
-                    const int slot = n % kStages;
-                    ok = warp_wait(B.ab_empty(slot), ((n / kStages) & 1u) ^ 1u, abort_flag);
-                    if (!ok) break;
-                    const uint32_t dst = base + slot * kStageBytes + OFF_B;
-                    if (elect_one()) {  // rows behind the expert's are the next one's, or stale: their columns are not stored
-                        expect_tx(B.ab_full(slot), t.groups * kGroup * 128);
-                        q8::tma_load_2d(dst, &tmB, 64 * s, t.row0, B.ab_full(slot));
-                        if (t.groups > 1) q8::tma_load_2d(dst + kGroup * 128, &tmB, 64 * s, t.row0 + kGroup, B.ab_full(slot));
-                    }
-                    __syncwarp();
-                }
-            }
-            for (uint32_t s = n < kStages ? 0 : n - kStages; s < n; ++s) drain_bar(B.ab_full(s % kStages), (s / kStages) & 1u);
         } else if (warp == 3) {
-            // ------------------------------------------------------------ their scales: columns lane, lane + 32, ...
+            // ------------------------------------------------------------ activations and their scales: columns lane, lane + 32, ...
             uint32_t n = 0;
             bool ok = true, bad = false;
-            for (int at = blockIdx.x; at < total && ok; at += gridDim.x) {
-                const Tile t = tile_at(a, cum, weight_tiles, at);
+            for (int at = 0; at < tiles && ok; ++at) {
+                const Tile t = tile_of(a, cum, table, weight_tiles, at);
                 const uint32_t *src[BN / 32];
 #pragma unroll
                 for (int i = 0; i < BN / 32; ++i) {
@@ -508,6 +530,13 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     }
                     ok = warp_wait(B.ab_empty(slot), ((n / kStages) & 1u) ^ 1u, abort_flag);
                     if (!ok) break;
+                    const uint32_t dst = base + slot * kStageBytes + OFF_B;
+                    if (elect_one()) {  // rows behind the expert's are the next one's, or stale: their columns are not stored
+                        expect_tx(B.ab_full(slot), t.groups * kGroup * 128);
+                        q8::tma_load_2d(dst, &tmB, 64 * s, t.row0, B.ab_full(slot));
+                        if (t.groups > 1) q8::tma_load_2d(dst + kGroup * 128, &tmB, 64 * s, t.row0 + kGroup, B.ab_full(slot));
+                    }
+                    __syncwarp();
                     uint16_t *da = reinterpret_cast<uint16_t *>(sm + slot * kStageBytes + OFF_DA + lane * 16);
 #pragma unroll
                     for (int i = 0; i < BN / 32; ++i) {
@@ -519,6 +548,7 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     if (lane == 0) arrive(B.ab_full(slot));
                 }
             }
+            for (uint32_t s = n < kStages ? 0 : n - kStages; s < n; ++s) drain_bar(B.ab_full(s % kStages), (s / kStages) & 1u);
             if (bad) atomicOr(&g_tiles_err, q8::kErrData);
         }
     } else if (warp < 8) {
@@ -545,16 +575,15 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
             }
             cp_async_commit();
         };
-        int at = blockIdx.x;
         Tile t = {}, tn = {};
-        if (!kTma && at < total) {
-            tn = tile_at(a, cum, weight_tiles, at);
+        if (!kTma && tiles > 0) {
+            tn = tile_of(a, cum, table, weight_tiles, 0);
             copy(tn, 0, 0);
         }
-        for (; at < total && ok; at += gridDim.x) {
+        for (int at = 0; at < tiles && ok; ++at) {
             if (!kTma) {
                 t = tn;
-                if (at + gridDim.x < total) tn = tile_at(a, cum, weight_tiles, at + gridDim.x);
+                if (at + 1 < tiles) tn = tile_of(a, cum, table, weight_tiles, at + 1);
             }
             const int64_t row = static_cast<int64_t>(t.e) * a.n + min(tile_row<kPair>(t.nt, r), a.n - 1);
             for (int s = 0; s < pieces && ok; ++s, ++p) {
@@ -567,7 +596,7 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     // the next piece's copies in flight while this one is widened
                     if (s + 1 < pieces)
                         copy(t, s + 1, p + 1);
-                    else if (at + gridDim.x < total)
+                    else if (at + 1 < tiles)
                         copy(tn, 0, p + 1);
                     else
                         cp_async_commit();
@@ -642,27 +671,22 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
         setmaxnreg_inc<kRegsEpi>();
         // ---------------------------------------------------------------- epilogue
         const int q = warp & 3, h = (warp - 8) >> 2;  // lanes 32 q .., columns 64 h ..
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + 64u * h;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + h * (kAcc * kTmemBuf);
         uint32_t blk = 0;
-        for (int at = blockIdx.x; at < total; at += gridDim.x) {
-            const Tile t = tile_at(a, cum, weight_tiles, at);
+        for (int at = 0; at < tiles; ++at) {
+            const Tile t = tile_of(a, cum, table, weight_tiles, at);
             const bool mine = h < t.groups;
             float2 acc[32];  // columns 64 h + 2 i, + 1 of position 32 q + lane
 #pragma unroll
             for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
-            if (!mine) {
-                for (int j = 0; j < nb; ++j, ++blk) {
-                    wait_go(B.acc_full(blk % kAcc), (blk / kAcc) & 1u, abort_flag);
-                    acc_release(blk % kAcc);
-                }
-            } else {
+            if (mine) {
                 // 32 columns at a time: the next ones' loads are in flight while these are added up, and a block's buffer is
                 // handed back when its second half has landed
                 uint32_t p[2][32], c[2][32];
                 auto load = [&](int x) {
                     const uint32_t buf = taddr + (blk % kAcc) * kTmemBuf + 32 * x;
                     tc_ld32(buf, p[x]);
-                    tc_ld32(buf + BN, c[x]);
+                    tc_ld32(buf + kGroup, c[x]);
                 };
                 auto add = [&](int x) {
 #pragma unroll
@@ -672,7 +696,7 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                                        make_float2(__uint_as_float(p[x][2 * i]), __uint_as_float(p[x][2 * i + 1])), acc[16 * x + i]);
                     order16(acc + 16 * x);
                 };
-                wait_go(B.acc_full(blk % kAcc), (blk / kAcc) & 1u, abort_flag);
+                wait_go(B.acc_full(h, blk % kAcc), (blk / kAcc) & 1u, abort_flag);
                 tc_fence_after();
                 load(0);
 #pragma unroll 1
@@ -684,10 +708,10 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     tc_wait_ld();
                     tc_regs32(p[1]), tc_regs32(c[1]);
                     tc_fence_before();
-                    acc_release(blk % kAcc);
+                    acc_release(h, blk % kAcc);
                     ++blk;
                     if (j + 1 < nb) {
-                        wait_go(B.acc_full(blk % kAcc), (blk / kAcc) & 1u, abort_flag);
+                        wait_go(B.acc_full(h, blk % kAcc), (blk / kAcc) & 1u, abort_flag);
                         tc_fence_after();
                         load(0);
                     }
@@ -745,26 +769,22 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                 const int c0 = 64 * h + 32 * up, ch = 64 * t.nt + 32 * (q >> 1);
                 const uint32_t m = valid(c0);
                 if (ch >= a.n) continue;
-                // lane i encodes column c0 + i's block: its largest value (NaN does not count), then its scale
-                uint32_t most = 0u;
+                // lane i gets column c0 + i's largest value (NaN does not count) and encodes its block's scale
+                float top[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const uint32_t b = __float_as_uint(fabsf(v[i]));
-                    const uint32_t top = __reduce_max_sync(Q8_FULL_MASK, b > 0x7f800000u ? 0u : b);
-                    if (lane == i) most = top;
-                }
-                const float d = q8::q8_block_d(__uint_as_float(most)), di = q8::q8_block_di(d);
-                int sum = 0;
+                for (int i = 0; i < 32; ++i) top[i] = fabsf(v[i]);
+                const float d = q8::q8_block_d(fmaxf(lane_columns(top, lane, [](float x, float y) { return fmaxf(x, y); }), 0.0f));
+                const float di = q8::q8_block_di(d);
+                int code[32];
                 int8_t *out = qs_out + static_cast<int64_t>(t.row0 + c0) * a.n + ch + lane;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    const int code = q8::q8_code(v[i], __shfl_sync(Q8_FULL_MASK, di, i));
-                    const int total_i = __reduce_add_sync(Q8_FULL_MASK, code);
-                    if (lane == i) sum = total_i;
-                    if ((m >> i) & 1u) *out = static_cast<int8_t>(code);
+                    code[i] = q8::q8_code(v[i], __shfl_sync(Q8_FULL_MASK, di, i));
+                    if ((m >> i) & 1u) *out = static_cast<int8_t>(code[i]);
                     out += a.n;
                     asm volatile("" : "+l"(out));
                 }
+                const int sum = lane_columns(code, lane, [](int x, int y) { return x + y; });
                 if ((m >> lane) & 1u)
                     ds_out[static_cast<int64_t>(t.row0 + c0 + lane) * (a.n >> 5) + (ch >> 5)] = q8::q8_dsword(d, sum);
             }

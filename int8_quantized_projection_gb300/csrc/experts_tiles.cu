@@ -16,7 +16,7 @@
 //   epilogue's stores lie between the last block of one and the first of the
 //   next.
 //   Weights go to shared memory as they are (34-byte blocks, TMA boxes of 32
-//   rows x 8 blocks, or 4-byte copies where rows of blocks are not 16-byte
+//   rows x 8 blocks, or a bulk copy a row where rows of blocks are not 16-byte
 //   aligned), and four warps widen them there, a row a thread.  The activations
 //   are widened once, by a pass that also puts the rows in order, since each
 //   meets all weight tiles of its expert.
@@ -53,8 +53,8 @@ static_assert(128 * kRegsCtl + kWidenThreads * kRegsWiden + kEpiThreads * kRegsE
 
 constexpr int kPiece = 8;                      // blocks of a weight slot
 constexpr int kPitchTma = 34 * kPiece;         // 272: a row's piece
-constexpr int kPitchAny = kPitchTma + 4;       // 276: with the two bytes that a row may start late; 69 words, odd
-constexpr int kRawBytes = BM * kPitchAny;      // 35328
+constexpr int kPitchAny = kPitchTma + 32;      // 304: a row may start up to 14 bytes late
+constexpr int kRawBytes = BM * kPitchAny;      // 38912
 constexpr int kABytes = BM * 128, kBBytes = BN * 128;
 constexpr int kScBytes = 128 * 16;             // one block's scales: 128 rows of 8 f16, of which the first is used
 
@@ -168,15 +168,6 @@ __device__ __forceinline__ bool elect_one()
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
     return p != 0;
 }
-
-// 4 bytes to shared memory, of which the first `bytes` come from src and the rest are zeros.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
 {
@@ -369,8 +360,8 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
         auto init = [&](int n, uint32_t count) {
             for (int k = 0; k < n; ++k) q8::mbar_init(b + i++, count);
         };
-        init(kRawSlots, 1);           // raw_full: copied bytes
-        init(kRawSlots, 4);           // raw_empty: a warp each
+        init(kRawSlots, kTma ? 1 : 4);  // raw_full: copied bytes, of each warp where the widening warps copy
+        init(kRawSlots, 4);             // raw_empty: a warp each
         init(kStages, 6);             // ab_full: four widening warps, the copied bytes, their scales
         init(kStages, 2);             // ab_empty: tcgen05.commit of both issuers
         init(2 * kAcc, 1);            // acc_full: tcgen05.commit
@@ -558,27 +549,31 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
         const int sw = r & 7;
         uint32_t n = 0, p = 0;  // stages and pieces done
         bool ok = true;
-        // the part of piece s of a tile's rows that this warp widens, 4 bytes a copy (rows of blocks that are not 16-byte aligned)
-        auto copy = [&](const Tile &t, int s, uint32_t to) {
+        // piece s of this thread's row, as many 16-byte units as hold it, where no TMA box can have it
+        uint32_t copied = 0;
+        auto copy = [&](const Tile &t, int s) {
             if (kTma) return;
-            const int cb = min(kPiece, nb - s * kPiece);
+            const int slot = copied % kRawSlots, cb = min(kPiece, nb - s * kPiece);
             const uint8_t *w = kPair && (warp & 1) ? a.w2 : a.w;
-            const int64_t most = static_cast<int64_t>(a.experts) * a.n * nb * 34;
-            for (int k = 0; k < 32; ++k) {
-                const int pos = 32 * (warp - 4) + k;
-                const int64_t row = static_cast<int64_t>(t.e) * a.n + min(tile_row<kPair>(t.nt, pos), a.n - 1);
-                const int64_t from = (row * nb + s * kPiece) * 34, end = from + cb * 34;
-                for (int64_t o = (from & ~int64_t(3)) + 4 * lane; o < end; o += 128)
-                    cp_async4(base + OFF_RAW + (to % kRawSlots) * kRawBytes + pos * kPitchAny +
-                                  static_cast<uint32_t>(o - (from & ~int64_t(3))),
-                              w + o, static_cast<int>(min(int64_t(4), most - o)));
-            }
-            cp_async_commit();
+            const int64_t most = static_cast<int64_t>(a.experts) * a.n * nb * 34, whole = most & ~int64_t(15);
+            const int64_t from = ((static_cast<int64_t>(t.e) * a.n + min(tile_row<kPair>(t.nt, r), a.n - 1)) * nb + s * kPiece) * 34;
+            const int64_t start = from & ~int64_t(15), stop = (from + cb * 34 + 15) & ~int64_t(15);
+            const int bytes = static_cast<int>(max(min(stop, whole) - start, int64_t(0)));
+            uint8_t *dst = sm + OFF_RAW + slot * kRawBytes + r * kPitchAny;
+            const int all = __reduce_add_sync(Q8_FULL_MASK, bytes);
+            q8::fence_proxy_async_smem();  // this warp has read what lies there
+            if (lane == 0) expect_tx(B.raw_full(slot), all);
+            __syncwarp();
+            if (bytes) q8::bulk_g2s(dst, w + start, bytes, reinterpret_cast<uint64_t *>(sm + OFF_BAR) + slot);
+            if (stop > whole)  // the last bytes of the last matrix, where they do not fill 16
+                for (int64_t o = max(whole, start); o < most; o += 2)
+                    *reinterpret_cast<uint16_t *>(dst + (o - start)) = *reinterpret_cast<const uint16_t *>(w + o);
+            ++copied;
         };
         Tile t = {}, tn = {};
         if (!kTma && tiles > 0) {
             tn = tile_of(a, cum, table, weight_tiles, 0);
-            copy(tn, 0, 0);
+            copy(tn, 0);
         }
         for (int at = 0; at < tiles && ok; ++at) {
             if (!kTma) {
@@ -589,20 +584,12 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
             for (int s = 0; s < pieces && ok; ++s, ++p) {
                 const int slot = p % kRawSlots;
                 const uint8_t *raw = sm + OFF_RAW + slot * kRawBytes;
-                if (kTma) {
-                    ok = warp_wait(B.raw_full(slot), (p / kRawSlots) & 1u, abort_flag);
-                    if (!ok) break;
-                } else {
-                    // the next piece's copies in flight while this one is widened
-                    if (s + 1 < pieces)
-                        copy(t, s + 1, p + 1);
-                    else if (at + 1 < tiles)
-                        copy(tn, 0, p + 1);
-                    else
-                        cp_async_commit();
-                    cp_async_wait<1>();
-                    __syncwarp();
-                }
+                if (s + 1 < pieces)  // the next piece's copies are in flight while this one is widened
+                    copy(t, s + 1);
+                else if (at + 1 < tiles)
+                    copy(tn, 0);
+                ok = warp_wait(B.raw_full(slot), (p / kRawSlots) & 1u, abort_flag);
+                if (!ok) break;
                 const int cb = min(kPiece, nb - s * kPiece);
 #pragma unroll
                 for (int k = 0; k < kPiece / 2; ++k) {
@@ -639,7 +626,7 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             const int64_t from = (row * nb + s * kPiece) * 34;
-                            const int at_byte = static_cast<int>(from & 2) + 34 * (2 * k + b);
+                            const int at_byte = static_cast<int>(from & 15) + 34 * (2 * k + b);
                             const uint32_t *src = reinterpret_cast<const uint32_t *>(raw + r * kPitchAny) + (at_byte >> 2);
                             const bool odd = at_byte & 2, there = 2 * k + b < cb;  // an odd last block: the other half is not used
                             const uint32_t sel = odd ? 0x7654u : 0x5432u;
@@ -666,7 +653,9 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                 if (kTma && lane == 0) arrive(B.raw_empty(slot));
             }
         }
-        if (!kTma) cp_async_wait<0>();
+        // the last copies must have landed before the CTA exits
+        for (uint32_t i = copied < kRawSlots ? 0 : copied - kRawSlots; i < copied; ++i)
+            drain_bar(B.raw_full(i % kRawSlots), (i / kRawSlots) & 1u);
     } else {
         setmaxnreg_inc<kRegsEpi>();
         // ---------------------------------------------------------------- epilogue

@@ -5,8 +5,8 @@
 // rows), two MMAs a block, as in the small-batch kernel of gemv.cu: exact
 // integers, scaled by d_w * d_a and added in f32.  The weight codes enter as
 // 1152 + q (a byte permute makes that f16 from the code, a subtraction less per
-// two codes), and the accumulator starts at -1152 * ssum, which the plane has
-// for each block: |sum| < 2^24, so the integer is exact all the same.
+// two codes), and the accumulator starts at -1152 times the sum of the row's
+// codes in the block: |sum| < 2^24, so the integer is exact all the same.
 //
 //   The line.  A segment is up to 8 or 16 rows of one expert (and a slice of k where a
 //   row's activations would not fit shared memory); it has an item for every 16
@@ -306,9 +306,9 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
         // activations: lane (g, m) of a fragment has words m and m + 4 of row g's block.  A thread takes half a block (words 4 h ..
         // 4 h + 3), four of them in flight, since under the stream a load takes some 2 us
         const int tasks = s.blocks * s.rows * 2;
-        for (int i0 = tid; i0 < tasks; i0 += 4 * kThreads) {
-            uint4 w[4];
-            uint32_t d[4];
+        for (int i0 = tid; i0 - lane < tasks; i0 += 4 * kThreads) {  // whole warps
+            uint4 w[4] = {};
+            uint32_t d[4] = {};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int i = i0 + k * kThreads, h = i & 1, rb = i >> 1, b = rb / s.rows, r = rb - b * s.rows;
@@ -321,8 +321,12 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int i = i0 + k * kThreads, h = i & 1, rb = i >> 1, b = rb / s.rows, r = rb - b * s.rows;
-                if (i >= tasks) break;
                 const uint32_t q[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                int sum = 0;
+#pragma unroll
+                for (int mm = 0; mm < 4; ++mm) sum = q8::dp4a(q[mm], 0x01010101u, sum);
+                sum += __shfl_xor_sync(Q8_FULL_MASK, sum, 1);  // the block's other half
+                if (i >= tasks) continue;
                 uint2 *f = reinterpret_cast<uint2 *>(sm + L.act) + ((b * NT + (r >> 3)) * 32 + 4 * (r & 7)) * 2 + h;
 #pragma unroll
                 for (int mm = 0; mm < 4; ++mm) {
@@ -332,7 +336,7 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
                 }
                 // row 2m + x of a tile: scale at 4m + x, start of the accumulator at 4m + 2 + x
                 float *sc = reinterpret_cast<float *>(sm + L.scale) + (b * NT + (r >> 3)) * 16 + 4 * ((r & 7) >> 1) + (r & 1);
-                sc[2 * h] = h ? -1152.0f * static_cast<float>(static_cast<int16_t>(d[k] >> 16))
+                sc[2 * h] = h ? -1152.0f * static_cast<float>(sum)
                               : __half2float(__ushort_as_half(static_cast<unsigned short>(d[k] & 0xffffu)));
             }
         }
@@ -349,9 +353,10 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
         const int item0 = item;
         for (int u = u0; u < u1; ++u) {
             const int slot_i = used % kSlots;
-            if (!dead && !__all_sync(Q8_FULL_MASK, q8::mbar_wait_bounded(bars + slot_i, (used / kSlots) & 1u))) {
+            if (!__all_sync(Q8_FULL_MASK, q8::mbar_wait_bounded(bars + slot_i, (used / kSlots) & 1u))) {
                 dead = true;
                 if (lane == 0) atomicOr(&g_rows_err, q8::kErrTimeout);
+                break;  // no slot is asked for again; the CTA leaves at the segment's end
             }
             const uint8_t *slot = ring + slot_i * slot_bytes(kTma);
             const int cb = min(kPiece, s.blocks - piece * kPiece);
@@ -378,7 +383,7 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
                 for (int t = 0; t < NT; ++t) {
                     const float4 v = make_float4(acc[t][0].x, acc[t][0].y, acc[t][1].x, acc[t][1].y);
                     if (whole) {
-                        if (!dead && 8 * t < s.rows) store_item(a, s, item, n16, g, m, t, v);
+                        if (8 * t < s.rows) store_item(a, s, item, n16, g, m, t, v);
                     } else if (item == item0) {
                         head[t] = v;
                     } else {

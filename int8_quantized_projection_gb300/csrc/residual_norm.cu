@@ -194,12 +194,14 @@ __global__ void __launch_bounds__(544, J <= 2 ? 2 : 1) residual_rmsnorm_stream_k
     __shared__ float weight[kMaxSlots];  // of the slot's expert row
     __shared__ int there[kMaxSlots];     // 0: no such row
     __shared__ float red[2][2][16];
+    __shared__ volatile int stop;        // a wait for a row ran out: no slot is filled again
     const int tid = threadIdx.x, P = blockDim.x - 32, F = a.F, d = 4 * F, lane = tid & 31;
     const bool own_gate = a.gate && a.gate_stride;
     const int vectors = (a.b ? 1 : 0) + a.top_k + (own_gate ? 1 : 0) + 1;
     const int64_t bytes = static_cast<int64_t>(d) * 4;
     if (tid == 0) {
         for (int i = 0; i < slots; ++i) q8::mbar_init(full + i, 1), q8::mbar_init(empty + i, P / 32);
+        stop = 0;
         q8::fence_mbar_init();
     }
     __syncthreads();
@@ -237,10 +239,9 @@ __global__ void __launch_bounds__(544, J <= 2 ? 2 : 1) residual_rmsnorm_stream_k
                 src = a.x + t * F;
             for (int k = 0; k < vectors; ++k) {
                 ok = __all_sync(Q8_FULL_MASK, q8::mbar_wait_bounded(empty + slot, phase ^ 1u));
-                if (!ok) {
-                    if (lane == 0) atomicOr(&g_resnorm_err, q8::kErrTimeout);
-                    break;
-                }
+                if (!ok && lane == 0) atomicOr(&g_resnorm_err, q8::kErrTimeout);
+                ok = __all_sync(Q8_FULL_MASK, ok && !stop);  // who gave a slot back unread set it before
+                if (!ok) break;
                 if (lane == k) {
                     weight[slot] = w;
                     there[slot] = src != nullptr;
@@ -277,6 +278,7 @@ __global__ void __launch_bounds__(544, J <= 2 ? 2 : 1) residual_rmsnorm_stream_k
     auto take = [&]() {
         if (!dead && !q8::mbar_wait_bounded(full + slot, phase)) {
             dead = true;
+            stop = 1;
             atomicOr(&g_resnorm_err, q8::kErrTimeout);
         }
         return reinterpret_cast<const float4 *>(ring + slot * bytes) + tid;

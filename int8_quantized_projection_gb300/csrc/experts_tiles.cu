@@ -169,6 +169,18 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// (A build without a limit, whose waits give up at once, asks without waiting.)
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
@@ -185,7 +197,7 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatil
 {
     const uint64_t t0 = q8::globaltimer_ns();
     do {
-        if (try_wait(bar, parity)) return true;
+        if (Q8_WAIT_LIMIT_NS == 0 ? test_wait(bar, parity) : try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
     } while (Q8_WAIT_LIMIT_NS != 0 && q8::globaltimer_ns() - t0 <= Q8_WAIT_LIMIT_NS);
     *abort_flag = 1;
@@ -200,21 +212,48 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return __all_sync(Q8_FULL_MASK, ok);
 }
 
-// The hand-over between MMAs and epilogue is a chain of such waits, so each is as short as it can be (60 cycles when the phase
-// is over already; 100 with a vote).  After an abort it returns at once: the warp goes on with what lies there, and ends its
-// tile, which is not stored.
-__device__ __forceinline__ void wait_go(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+// The hand-over between MMAs and epilogue is a chain of waits, so each is as short as it can be (60 cycles when the phase is over
+// already; 100 with a vote).  The issuers' for a stage: a lane whose wait ran out is not live from then on.  It issues no MMA and
+// frees no stage, so that nobody fills one that is still being copied into, but goes through all its blocks.
+__device__ __forceinline__ void wait_live(bool &live, uint32_t bar, uint32_t parity, volatile int *abort_flag)
 {
+    if (!live) return;
     if (Q8_WAIT_LIMIT_NS != 0)
         for (int i = 0; i < 64; ++i)
             if (try_wait(bar, parity)) return;
-    wait_slow(bar, parity, abort_flag);
+    live = wait_slow(bar, parity, abort_flag);
 }
 
-// Wait for copies or MMAs in flight before the CTA exits, whatever the abort flag says; bounded.
-__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity)
+// The epilogue's for a block's accumulators, whatever the abort flag says: the issuer commits every block, if need be without
+// MMAs, after waits that are bounded.  The limit is behind all of those, in time and in tries.
+__device__ __forceinline__ void wait_acc(uint32_t bar, uint32_t parity, volatile int *abort_flag)
 {
+    for (int i = 0; i < 64; ++i)
+        if (try_wait(bar, parity)) return;
     const uint64_t t0 = q8::globaltimer_ns();
+    for (uint32_t i = 0; i < (1u << 20) || q8::globaltimer_ns() - t0 <= 2 * (Q8_WAIT_LIMIT_NS + Q8_DRAIN_LIMIT_NS); ++i)
+        if (try_wait(bar, parity)) return;
+    *abort_flag = 1;
+    atomicOr(&g_tiles_err, q8::kErrTimeout);
+}
+
+// A buffer of tensor memory is handed back by a named barrier: the epilogue warps arrive, the MMA warp waits, some 25 cycles
+// for a wait where an mbarrier takes 100 and its arrival as long again (3325 rows of 1440 x 3584 pairs: 1375 us, with mbarriers
+// 1650).  Both sides pass each barrier once per block, in step: a warp arrives for block b + kAcc only behind that block's
+// commit, which the issuer makes behind the barrier of block b.
+constexpr int kHandOver = 2;  // barriers 2 .. 5
+__device__ __forceinline__ void acc_release(int half, int buf)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(kHandOver + half * kAcc + buf), "n"(kEpiThreads / 2 + 32) : "memory");
+}
+__device__ __forceinline__ void acc_acquire(int half, int buf)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(kHandOver + half * kAcc + buf), "n"(kEpiThreads / 2 + 32) : "memory");
+}
+
+// Wait for copies or MMAs in flight before the CTA exits, whatever the abort flag says; bounded, counted from t0.
+__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity, uint64_t t0)
+{
     while (!try_wait(bar, parity)) {
         if (q8::globaltimer_ns() - t0 > Q8_DRAIN_LIMIT_NS) {
             atomicOr(&g_tiles_err, q8::kErrTimeout);
@@ -231,19 +270,6 @@ __device__ __forceinline__ void arrive(uint32_t bar)
 __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-// A buffer of tensor memory is handed back by a named barrier: the epilogue warps arrive, the MMA warp waits, some 25 cycles
-// for a wait where an mbarrier takes 100 and its arrival as long again.  Both sides pass each barrier once per block, whatever
-// the abort flag says, so neither is left waiting.
-constexpr int kHandOver = 2;  // barriers 2 .. 5
-__device__ __forceinline__ void acc_release(int half, int buf)
-{
-    asm volatile("bar.arrive %0, %1;" ::"r"(kHandOver + half * kAcc + buf), "n"(kEpiThreads / 2 + 32) : "memory");
-}
-__device__ __forceinline__ void acc_acquire(int half, int buf)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(kHandOver + half * kAcc + buf), "n"(kEpiThreads / 2 + 32) : "memory");
 }
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
@@ -433,6 +459,7 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
             const int half = warp;
             const uint32_t idesc = mma_desc(kGroup);
             uint32_t blk = 0, slot = 0, phase = 0;  // blocks done, stage and its phase
+            bool live = true;
             for (int i = 0; i < tiles; ++i) {
                 const bool mine = half < tile_of(a, cum, table, weight_tiles, i).groups;
                 for (int j = 0; j < nb; j += 2) {
@@ -440,9 +467,9 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     const uint64_t pa = smem_desc(stage), pb = smem_desc(stage + OFF_B + half * (kBBytes / 2));
                     const uint64_t sa = scale_desc(stage + OFF_DW, base + OFF_ZERO);
                     const uint64_t sb = scale_desc(stage + OFF_DA + half * (kScBytes / 2), base + OFF_ZERO);
-                    wait_go(B.ab_full(slot), phase, abort_flag);
+                    wait_live(live, B.ab_full(slot), phase, abort_flag);
                     if (!mine) {
-                        if (lane == 0) arrive(B.ab_empty(slot));
+                        if (lane == 0 && live) arrive(B.ab_empty(slot));
                         __syncwarp();
                     } else {
 #pragma unroll
@@ -454,11 +481,13 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                             // a scale operand's next block: its columns 8 .. 15 lie that much nearer
                             constexpr uint64_t next = (kScBytes >> 4) - (static_cast<uint64_t>(kScBytes >> 4) << 16);
                             if (elect_one()) {
-                                tc_mma_f16(d, pa + 4 * u, pb + 4 * u, idesc, 0);
-                                tc_mma_f16(d, pa + 4 * u + 2, pb + 4 * u + 2, idesc, 1);  // 32 bytes on
-                                tc_mma_f16(d + kGroup, sa + u * next, sb + u * next, idesc, 0);
+                                if (live) {
+                                    tc_mma_f16(d, pa + 4 * u, pb + 4 * u, idesc, 0);
+                                    tc_mma_f16(d, pa + 4 * u + 2, pb + 4 * u + 2, idesc, 1);  // 32 bytes on
+                                    tc_mma_f16(d + kGroup, sa + u * next, sb + u * next, idesc, 0);
+                                    if (u == 1 || j + 1 == nb) tc_commit(B.ab_empty(slot));
+                                }
                                 tc_commit(B.acc_full(half, blk % kAcc));
-                                if (u == 1 || j + 1 == nb) tc_commit(B.ab_empty(slot));
                             }
                             __syncwarp();
                             ++blk;
@@ -467,11 +496,11 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     if (++slot == kStages) slot = 0, phase ^= 1u;
                 }
             }
-            for (int k = 0; k < kAcc && k < static_cast<int>(blk); ++k) acc_acquire(half, k);  // the last blocks'
             // every MMA must have completed before its operands and TMEM go
             if (elect_one()) tc_commit(B.drain(half));
             __syncwarp();
-            drain_bar(B.drain(half), 0);
+            for (int k = 0; k < kAcc && k < static_cast<int>(blk); ++k) acc_acquire(half, k);  // the last blocks'
+            drain_bar(B.drain(half), 0, q8::globaltimer_ns());
         } else if (warp == 2 && kTma) {
             // ------------------------------------------------------------ weights
             uint32_t n = 0;
@@ -495,8 +524,9 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                 }
             }
             // the last copies must have landed before the CTA exits
+            const uint64_t t0 = q8::globaltimer_ns();
             for (uint32_t s = n < kRawSlots ? 0 : n - kRawSlots; s < n; ++s)
-                drain_bar(B.raw_full(s % kRawSlots), (s / kRawSlots) & 1u);
+                drain_bar(B.raw_full(s % kRawSlots), (s / kRawSlots) & 1u, t0);
         } else if (warp == 3) {
             // ------------------------------------------------------------ activations and their scales: columns lane, lane + 32, ...
             uint32_t n = 0;
@@ -539,7 +569,8 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     if (lane == 0) arrive(B.ab_full(slot));
                 }
             }
-            for (uint32_t s = n < kStages ? 0 : n - kStages; s < n; ++s) drain_bar(B.ab_full(s % kStages), (s / kStages) & 1u);
+            const uint64_t t0 = q8::globaltimer_ns();
+            for (uint32_t s = n < kStages ? 0 : n - kStages; s < n; ++s) drain_bar(B.ab_full(s % kStages), (s / kStages) & 1u, t0);
             if (bad) atomicOr(&g_tiles_err, q8::kErrData);
         }
     } else if (warp < 8) {
@@ -654,8 +685,9 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
             }
         }
         // the last copies must have landed before the CTA exits
+        const uint64_t t0 = q8::globaltimer_ns();
         for (uint32_t i = copied < kRawSlots ? 0 : copied - kRawSlots; i < copied; ++i)
-            drain_bar(B.raw_full(i % kRawSlots), (i / kRawSlots) & 1u);
+            drain_bar(B.raw_full(i % kRawSlots), (i / kRawSlots) & 1u, t0);
     } else {
         setmaxnreg_inc<kRegsEpi>();
         // ---------------------------------------------------------------- epilogue
@@ -685,7 +717,8 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                                        make_float2(__uint_as_float(p[x][2 * i]), __uint_as_float(p[x][2 * i + 1])), acc[16 * x + i]);
                     order16(acc + 16 * x);
                 };
-                wait_go(B.acc_full(h, blk % kAcc), (blk / kAcc) & 1u, abort_flag);
+                wait_acc(B.acc_full(h, blk % kAcc), (blk / kAcc) & 1u, abort_flag);
+                __syncwarp();
                 tc_fence_after();
                 load(0);
 #pragma unroll 1
@@ -700,7 +733,8 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     acc_release(h, blk % kAcc);
                     ++blk;
                     if (j + 1 < nb) {
-                        wait_go(B.acc_full(h, blk % kAcc), (blk / kAcc) & 1u, abort_flag);
+                        wait_acc(B.acc_full(h, blk % kAcc), (blk / kAcc) & 1u, abort_flag);
+                        __syncwarp();
                         tc_fence_after();
                         load(0);
                     }

@@ -97,12 +97,12 @@ def swiglu(g, dg, u, du):
 def check_plane(qs, ds, y, lim):
     """The plane's rows encode values within lim of y: each code is the nearest of a scale amax / 127 stored as f16."""
     rows, k = y.shape
-    q = qs[:rows].reshape(rows, -1, 32).astype(np.float64)
+    q = qs[:rows].reshape(rows, k // 32, 32).astype(np.float64)
     word = ds[:rows].view(np.uint32)
     d = (word & 0xffff).astype(np.uint16).view(np.float16).astype(np.float64)
     ssum = (word >> 16).astype(np.uint16).view(np.int16)
     assert np.array_equal(ssum, q.sum(-1).astype(np.int64)), "block sums"
-    yb, lb = y.reshape(rows, -1, 32), lim.reshape(rows, -1, 32)
+    yb, lb = y.reshape(rows, k // 32, 32), lim.reshape(rows, k // 32, 32)
     amax, most = np.abs(yb).max(-1), lb.max(-1)
     step = amax / 127
     half = 2.0 ** -11 * step + 2.0 ** -25  # the scale's rounding to f16, normal or subnormal

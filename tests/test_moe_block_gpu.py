@@ -1,0 +1,294 @@
+"""A mixture-of-experts block as a step runs it: routing, products, norms, one after the other; captured, on other streams, beside
+one another, bound, and with waits that run out."""
+import os
+import subprocess
+import sys
+import textwrap
+
+import numpy as np
+import pytest
+
+from tests import _moe_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+class Block:
+    """One block's weights and buffers for up to `tokens` tokens, and its step."""
+
+    def __init__(self, q8, tokens, experts=8, top_k=2, d=512, nf=256, seed=0):
+        import torch
+
+        self.q8, self.tokens, self.experts, self.top_k, self.d, self.nf = q8, tokens, experts, top_k, d, nf
+        g = self.g = np.random.default_rng([seed, tokens, experts])
+        blobs = [ref.weights_of(g, experts, *s) for s in ((nf, d), (nf, d), (d, nf))]
+        self.w = [w for _, w in blobs]
+        dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+        self.wg, self.wu, self.wd = (dev(b) for b, _ in blobs)
+        self.post, self.pre = (1 + 0.1 * g.standard_normal(d).astype(np.float32) for _ in range(2))
+        self.post_d, self.pre_d = dev(self.post), dev(self.pre)
+        i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+        pairs = tokens * top_k
+        self.logits, self.x = torch.zeros(tokens, experts, device="cuda"), torch.zeros(tokens, d, device="cuda")
+        self.valid = i32(1)
+        self.qs, self.ds = q8.empty_plane(q8.q8_plane_rows(tokens), d)
+        self.ids, self.weights, self.places = i32(tokens, top_k), torch.zeros(tokens, top_k, device="cuda"), i32(tokens, top_k)
+        self.offsets, self.rows = i32(experts + 1), i32(pairs)
+        self.qh, self.dh = q8.empty_plane(pairs, nf)
+        self.ye = torch.zeros(pairs, d, device="cuda")
+        self.h, self.y = torch.zeros(tokens, d, device="cuda"), torch.zeros(tokens, d, device="cuda")
+        self.qn, self.dn = q8.empty_plane(q8.q8_plane_rows(tokens), d)
+        sizes = (experts, nf, d, self.qs.shape[0], top_k, pairs)
+        byte = lambda n: torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")  # noqa: E731
+        self.ws = [byte(q8.q8_moe_route_workspace_bytes(tokens, experts, top_k)),
+                   byte(q8.q8_0_experts_gate_up_workspace_bytes(*sizes)),
+                   byte(q8.q8_0_experts_gemm_workspace_bytes(experts, d, nf, pairs, top_k, pairs))]
+
+    def fill(self, real):
+        """New inputs of `real` tokens; the rest is padding that may hold anything."""
+        import torch
+
+        logits = self.g.standard_normal((self.tokens, self.experts)).astype(np.float32)
+        logits[real:] = np.nan
+        x = self.g.standard_normal((self.tokens, self.d)).astype(np.float32)
+        self.logits.copy_(torch.from_numpy(logits))
+        self.x.copy_(torch.from_numpy(x))
+        self.valid.fill_(real)
+        self.real = real
+
+    def step(self, stream=None, bind=False):
+        q8, kw = self.q8, dict(stream=stream, bind=bind)
+        return [
+            q8.quantize_q8_0(self.x, self.qs, self.ds, **kw),
+            q8.q8_moe_route(self.logits, self.ids, self.weights, self.offsets, self.rows, self.places, valid=self.valid,
+                            workspace=self.ws[0], **kw),
+            q8.q8_0_experts_gate_up(self.wg, self.wu, self.experts, self.nf, self.d, self.qs, self.ds, self.offsets, self.qh,
+                                    self.dh, rows=self.rows, top_k=self.top_k, workspace=self.ws[1], **kw),
+            q8.q8_0_experts_gemm(self.wd, self.experts, self.d, self.nf, self.qh, self.dh, self.offsets, self.ye,
+                                 top_k=self.top_k, workspace=self.ws[2], **kw),
+            q8.rmsnorm_residual_quant(self.x, self.h, expert_rows=self.ye, places=self.places, weights=self.weights,
+                                      w_post=self.post_d, eps_post=1e-6, residual_scale=0.5, w=self.pre_d, eps=1e-6, y=self.y,
+                                      qs=self.qn, ds=self.dn, **kw)]
+
+    def outputs(self):
+        return [t.clone() for t in (self.ids, self.weights, self.offsets, self.places, self.h, self.y, self.qn, self.dn)]
+
+    def check(self):
+        """Each call against its definition in 64 bits on what the one before it wrote."""
+        q8, pairs = self.q8, self.tokens * self.top_k
+        q8.q8_check()
+        n = lambda t: t.cpu().numpy()  # noqa: E731
+        ids, weights, offsets, rows, places = ref.route(n(self.logits), self.top_k, 1, valid=self.real)
+        assert np.array_equal(n(self.ids), ids) and np.array_equal(n(self.offsets), offsets)
+        assert np.array_equal(n(self.rows), rows) and np.array_equal(n(self.places), places)
+        assert np.all(np.abs(n(self.weights) - weights) <= 2.0 ** -18 * weights)
+        total = int(offsets[-1])
+
+        def values(qs, ds):
+            d16 = (n(ds).view(np.uint32) & 0xffff).astype(np.uint16).view(np.float16).astype(np.float64)
+            return n(qs).reshape(qs.shape[0], -1, 32) * d16[:, :, None]
+
+        x = values(self.qs, self.ds)
+        (gt, gl), (ut, ul) = (ref.product(w, x, offsets, rows // self.top_k) for w in self.w[:2])
+        ref.check_plane(n(self.qh), n(self.dh), *ref.swiglu(gt, gl, ut, ul))
+        yt, yl = ref.product(self.w[2], values(self.qh, self.dh), offsets, np.arange(pairs))
+        ye = n(self.ye)
+        assert np.all(np.abs(ye[:total] - yt) <= yl)
+        h, hl, y, ylim = ref.residual_norm(n(self.x), 0.5, None, ye, n(self.places), n(self.weights), self.post, 1e-6, None, self.pre,
+                                           1e-6)
+        assert np.all(np.abs(n(self.h) - h) <= hl + 1e-38) and np.all(np.abs(n(self.y) - y) <= ylim + 1e-38)
+        ref.check_plane(n(self.qn), n(self.dn), y, ylim)
+
+
+SIZES = [dict(tokens=1), dict(tokens=13, experts=16, top_k=4, d=1440, nf=96), dict(tokens=700), dict(tokens=90, experts=3, d=288)]
+
+
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_step(q8, size):
+    b = Block(q8, **size)
+    for real in (size["tokens"], size["tokens"] * 2 // 3, 0):
+        b.fill(real)
+        b.step()
+        b.check()
+
+
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_captured_steps_of_other_routings(q8, size):
+    import torch
+
+    b = Block(q8, **size)
+    b.fill(size["tokens"])
+    b.step()
+    b.check()
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        b.step(stream=stream)
+    for real in (size["tokens"], size["tokens"] // 2, size["tokens"]):
+        b.fill(real)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        b.check()
+        once = b.outputs()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(once, b.outputs()))  # run to run the same bits
+
+
+def test_graphs_that_share_a_workspace(q8):
+    """Two captured steps of one size over the same workspaces, replayed in turn on one stream."""
+    import torch
+
+    a, b = Block(q8, 700, seed=1), Block(q8, 700, seed=2)
+    b.ws = a.ws
+    graphs = []
+    for x in (a, b):
+        x.fill(700)
+        x.step()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            x.step()
+        graphs.append(g)
+    for _ in range(3):
+        for w in a.ws:
+            w.fill_(0xff)  # contents are ignored on entry
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    a.check(), b.check()
+
+
+def test_steps_in_flight_at_once(q8):
+    import torch
+
+    blocks = [Block(q8, **s, seed=3 + i) for i, s in enumerate(SIZES)]
+    want = []
+    for b in blocks:
+        b.fill(b.tokens)
+        b.step()
+        torch.cuda.synchronize()
+        want.append(b.outputs())
+    streams = [torch.cuda.Stream() for _ in blocks]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for b, s in zip(blocks, streams):
+            b.step(stream=s)
+    torch.cuda.synchronize()
+    for b, w in zip(blocks, want):
+        b.check()
+        assert all(torch.equal(x, y) for x, y in zip(w, b.outputs()))
+
+
+def test_bound_and_workspaces_of_the_call(q8):
+    """The bind form, and calls that allocate their own workspace on the stream that uses it."""
+    import torch
+
+    b = Block(q8, 700)
+    b.fill(700)
+    b.step()
+    want = b.outputs()
+    bound = b.step(bind=True)
+    b.h.zero_(), b.ye.zero_()
+    for call in bound:
+        call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, b.outputs()))
+    b.ws = [None, None, None]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        b.step(stream=side)
+        junk = torch.full((1 << 22,), float("nan"), device="cuda")  # from the current stream's pool meanwhile
+    side.synchronize()
+    assert junk.isnan().all() and all(torch.equal(x, y) for x, y in zip(want, b.outputs()))
+    b.check()
+
+
+def test_one_call_beside_another_kernels_writes(q8):
+    """The plane and the routing may come from the kernel right before the call: no input is read before it has finished."""
+    import torch
+
+    b = Block(q8, 40, experts=4)
+    for i in range(20):
+        b.fill(40 - i)
+        b.step()
+    b.check()
+
+
+def test_a_plane_without_block_sums(q8):
+    """The products read codes and scales; the sums beside the scales are another operator's."""
+    import torch
+
+    b = Block(q8, 9)
+    b.fill(9)
+    b.step()
+    want = b.ye.clone()
+    b.ds &= 0xffff
+    b.dh.zero_()
+    q8.q8_0_experts_gate_up(b.wg, b.wu, b.experts, b.nf, b.d, b.qs, b.ds, b.offsets, b.qh, b.dh, rows=b.rows, top_k=b.top_k)
+    b.dh &= 0xffff
+    q8.q8_0_experts_gemm(b.wd, b.experts, b.d, b.nf, b.qh, b.dh, b.offsets, b.ye, top_k=b.top_k)
+    q8.q8_check()
+    assert torch.equal(b.ye, want)
+
+
+_CHILD = textwrap.dedent(
+    """
+    import ctypes, sys
+    sys.path.insert(0, ROOT)
+    import numpy as np, torch
+    from int8_quantized_projection_gb300 import _binding as bd
+    lib = ctypes.CDLL(LIB)
+    for name, (res, args) in bd.SIGNATURES.items():
+        f = getattr(lib, name); f.restype = res; f.argtypes = args
+    st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    P = lambda t: ctypes.c_void_p(t.data_ptr())
+    out = {}
+    def run(name, k, rows, n=1024, experts=4):
+        pairs = experts * rows
+        w = torch.randint(0, 60, (experts * n * (k // 32) * 34,), dtype=torch.uint8, device="cuda")
+        qs = torch.randint(-127, 128, (pairs, k), dtype=torch.int8, device="cuda")
+        ds = torch.full((pairs, k // 32), 0x3C00, dtype=torch.int32, device="cuda")
+        off = torch.arange(0, pairs + 1, rows, dtype=torch.int32, device="cuda")
+        y = torch.empty(pairs, n, device="cuda")
+        qo, do = torch.empty(pairs, n, dtype=torch.int8, device="cuda"), torch.empty(pairs, n // 32, dtype=torch.int32, device="cuda")
+        need = max(lib.q8_0_experts_gemm_workspace_bytes(experts, n, k, pairs, 1, pairs),
+                   lib.q8_0_experts_gate_up_workspace_bytes(experts, n, k, pairs, 1, pairs), 16)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        assert lib.q8_0_experts_gemm(P(w), experts, n, k, P(qs), P(ds), pairs, P(off), None, 1, pairs, P(y), P(ws), need, st) == 0
+        out[name] = lib.q8_check(st)
+        assert lib.q8_0_experts_gate_up(P(w), P(w), experts, n, k, P(qs), P(ds), pairs, P(off), None, 1, pairs, P(qo), P(do), P(ws),
+                                        need, st) == 0
+        out[name + "_pair"] = lib.q8_check(st)
+        out[name + "_after"] = lib.q8_check(st)
+    # 13 units of weights for each warp of the stream, whose ring holds two: the later waits follow their copies at once
+    run("rows", 2048, 3, n=16384)
+    run("rows_unaligned", 2080, 12, n=16384)
+    run("tiles", 2048, 200)
+    run("tiles_unaligned", 2080, 200)
+    rows, d = 2000, 3584
+    x, b, h = (torch.randn(rows, d, device="cuda") for _ in range(3))
+    assert lib.rmsnorm_residual_quant(P(x), 1.0, P(b), None, 0, None, None, 0, None, 0.0, None, 0, None, 0.0, P(h), None, rows, d,
+                                      None, None, 0, st) == 0
+    out["norm"] = lib.q8_check(st)
+    out["norm_after"] = lib.q8_check(st)
+    print("RESULT", out)
+    """
+)
+
+
+def test_waits_that_run_out(tmp_path):
+    """A build whose waits give up at once: each kernel reports it, reaches its exit and leaves the GPU usable."""
+    from int8_quantized_projection_gb300 import build
+
+    lib = build.build(lib_path=str(tmp_path / "short" / "libq8proj_short.so"), extra=["-DQ8_WAIT_LIMIT_NS=0ull"])
+    r = subprocess.run([sys.executable, "-c", f"ROOT = {ROOT!r}\nLIB = {lib!r}\n" + _CHILD], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+    out = eval(r.stdout.split("RESULT", 1)[1])
+    # whether a wait finds its copy depends on the copy; in each kernel some do not
+    assert all(status == 0 if name.endswith("_after") else status in (0, 5) for name, status in out.items()), out
+    for kernel in ("rows", "rows_unaligned", "tiles", "tiles_unaligned", "norm"):
+        assert 5 in (out[kernel], out.get(kernel + "_pair")), out

@@ -266,7 +266,7 @@ _CHILD = textwrap.dedent(
         out[name + "_after"] = lib.q8_check(st)
     # 13 units of weights for each warp of the stream, whose ring holds two: the later waits follow their copies at once
     run("rows", 2048, 3, n=16384)
-    run("rows_unaligned", 2080, 12, n=16384)
+    run("rows_unaligned", 2080, 3, n=16384)
     run("tiles", 2048, 200)
     run("tiles_unaligned", 2080, 200)
     rows, d = 2000, 3584

@@ -42,15 +42,17 @@ struct RowsArgs {
     int64_t part;                      // floats from one slice's output to the next's
 };
 
-// shared memory: ring [kWarps][kSlots] | B fragments [blocks][NT][32] uint4 | scales [blocks][NT][4] float4 | items before each
-// expert | barriers; the partial items [kWarps][2][NT][32] float4 take the fragments' place.  nt: tiles of 8 rows a segment has.
+// shared memory: ring [kWarps][kSlots] | B fragments [blocks][NT][32] uint4 | scales [blocks][NT][4] float4 | rows of each expert
+// | cost before each | barriers; the partial items [kWarps][2][NT][32] float4 take the fragments' place.  nt: tiles of 8 rows a
+// segment has.
 struct Layout {
-    int act, scale, cum, bar, total;
+    int act, scale, rows, cum, bar, total;
     __host__ __device__ Layout(bool tma, int nt, int blocks)
     {
         act = kWarps * kSlots * slot_bytes(tma);
         scale = act + (blocks > 2 * kWarps ? blocks : 2 * kWarps) * 512 * nt;
-        cum = scale + blocks * 64 * nt;
+        rows = scale + blocks * 64 * nt;
+        cum = rows + Q8_MAX_EXPERTS * 8;
         bar = cum + (Q8_MAX_EXPERTS + 2) * 4;
         total = bar + kWarps * 8 * kSlots + 128;
     }
@@ -75,9 +77,9 @@ __device__ __forceinline__ int expert_cost(int count)
 }
 
 // The segment at place i of the line, cut to the stretch that ends at `end`: the items that start in it.  cum[e]: cost of the
-// experts before e.
+// experts before e; rows[e]: its first and their number.
 template <int NT>
-__device__ __forceinline__ Segment segment_at(const RowsArgs &a, const int *cum, int i, int end)
+__device__ __forceinline__ Segment segment_at(const RowsArgs &a, const int2 *rows, const int *cum, int i, int end)
 {
     int lo = 0, hi = a.x.experts;
     while (hi - lo > 1) {
@@ -87,13 +89,13 @@ __device__ __forceinline__ Segment segment_at(const RowsArgs &a, const int *cum,
         else
             hi = mid;
     }
-    const q8::ExpertRows x = q8::expert_rows_of(a.x, lo);
+    const int first = rows[lo].x, count = rows[lo].y;
     const int whole = item_cost(8 * NT) * a.groups * a.slices;
-    const int chunk = min((i - cum[lo]) / whole, (x.count - 1) / (8 * NT));
+    const int chunk = min((i - cum[lo]) / whole, (count - 1) / (8 * NT));
     Segment s;
     s.e = lo;
-    s.first = x.first + chunk * 8 * NT;
-    s.rows = min(8 * NT, x.count - chunk * 8 * NT);
+    s.first = first + chunk * 8 * NT;
+    s.rows = min(8 * NT, count - chunk * 8 * NT);
     const int cost = item_cost(s.rows);
     s.slice = (i - cum[lo] - chunk * whole) / (cost * a.groups);
     s.b0 = s.slice * a.slice_blocks;
@@ -204,6 +206,7 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, m = lane & 3;
     const Layout L(kTma, NT, a.slice_blocks);
     int *cum = reinterpret_cast<int *>(sm + L.cum);
+    int2 *rows = reinterpret_cast<int2 *>(sm + L.rows);  // first and number of each expert's
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L.bar) + warp * kSlots;
     uint8_t *ring = sm + warp * kSlots * slot_bytes(kTma);
     if (lane == 0) {
@@ -220,6 +223,7 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
             if (2 * tid + k < a.x.experts) {
                 const q8::ExpertRows x = q8::expert_rows_of(a.x, 2 * tid + k);
                 if (x.bad && blockIdx.x == 0) atomicOr(&g_rows_err, q8::kErrData);
+                rows[2 * tid + k] = make_int2(x.first, x.count);
                 n[k] = expert_cost<NT>(x.count) * a.slices * a.groups;
             }
         }
@@ -249,7 +253,7 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
     auto fetch = [&]() {  // the next unit into the next slot; every slot it goes to has been read
         while (fu == fend) {
             if (fnext >= end) return;
-            fs = segment_at<NT>(a, cum, fnext, end);
+            fs = segment_at<NT>(a, rows, cum, fnext, end);
             fnext = fs.next;
             fpieces = (fs.blocks + kPiece - 1) / kPiece;
             const int units = (fs.i1 - fs.i0) * fpieces;
@@ -291,7 +295,7 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
 
     bool dead = false;  // a wait ran out
     while (at < end) {
-        const Segment s = segment_at<NT>(a, cum, at, end);
+        const Segment s = segment_at<NT>(a, rows, cum, at, end);
         if (s.i0 == s.i1) {
             at = s.next;
             continue;

@@ -44,12 +44,14 @@ namespace {
 
 __device__ unsigned int g_tiles_err;
 
-constexpr int BM = 128, kGroup = 64, kMaxGroups = 2, BN = kGroup * kMaxGroups;
+constexpr int BM = 128, kGroup = 16, kMaxGroups = 8, BN = kGroup * kMaxGroups, kBox = 64;  // kBox: sorted rows of a copy
 constexpr int kStages = 3, kRawSlots = 2, kAcc = 2;
-constexpr int kTmemBuf = 2 * kGroup, kTmemCols = kMaxGroups * kAcc * kTmemBuf;  // integers, then scales
-constexpr int kThreads = 512, kWidenThreads = 128, kEpiWarps = 8, kEpiThreads = 256;
-constexpr int kRegsCtl = 40, kRegsWiden = 56, kRegsEpi = 208;
-static_assert(128 * kRegsCtl + kWidenThreads * kRegsWiden + kEpiThreads * kRegsEpi <= 128 * kThreads, "register split");
+constexpr int kTmemBuf = 2 * BN, kTmemCols = kAcc * kTmemBuf;  // integers, then scales
+constexpr int kThreads = 768, kWidenThreads = 128, kEpiWarps = 16, kEpiThreads = 512;
+constexpr int kWidenWarp = 4, kEpiWarp = 8;  // the first of them
+constexpr int kRegsLaunch = 80, kRegsCtl = 40, kRegsWiden = 56, kRegsEpi = 96;
+static_assert(128 * kRegsCtl + kWidenThreads * kRegsWiden + kEpiThreads * kRegsEpi <= kRegsLaunch * kThreads, "register split");
+static_assert(kRegsLaunch * kThreads <= 65536 && (kRegsLaunch + 8) * kThreads > 65536, "registers at launch");
 
 constexpr int kPiece = 8;                      // blocks of a weight slot
 constexpr int kPitchTma = 34 * kPiece;         // 272: a row's piece
@@ -62,14 +64,14 @@ constexpr int kStageBytes = kABytes + kBBytes + 4 * kScBytes;  // two blocks: co
 constexpr int OFF_B = kABytes, OFF_DW = OFF_B + kBBytes, OFF_DA = OFF_DW + 2 * kScBytes;  // in a stage
 constexpr int OFF_ZERO = kStages * kStageBytes;         // columns 8 .. 15 of every scale operand
 constexpr int OFF_RAW = OFF_ZERO + kScBytes;
-constexpr int OFF_SWAP = OFF_RAW + kRawSlots * kRawBytes;  // [8 warps][16 columns][32] f32
-constexpr int OFF_CUM = OFF_SWAP + kEpiWarps * 16 * 32 * 4;  // row tiles before each expert
+constexpr int OFF_SWAP = OFF_RAW + kRawSlots * kRawBytes;  // [16 warps][8 columns][32] f32
+constexpr int OFF_CUM = OFF_SWAP + kEpiWarps * 8 * 32 * 4;  // row tiles before each expert
 constexpr int kTable = 96;                              // tiles of this CTA that are looked up once
 constexpr int OFF_TABLE = (OFF_CUM + (Q8_MAX_EXPERTS + 2) * 4 + 15) / 16 * 16;
-constexpr int kBars = 2 * kRawSlots + 2 * kStages + 2 * kAcc + 2;
+constexpr int kBars = 2 * kRawSlots + 2 * kStages + 2 * kAcc;
 constexpr int OFF_BAR = OFF_TABLE + kTable * 16;
 constexpr int OFF_MISC = OFF_BAR + kBars * 8;           // abort flag, TMEM address, sums of the scan
-constexpr int kSmemBytes = OFF_MISC + 16 + 96 + 1024;   // + alignment slack
+constexpr int kSmemBytes = OFF_MISC + 16 + kThreads / 8 + 1024;   // + alignment slack
 static_assert(OFF_BAR % 8 == 0 && kStageBytes % 1024 == 0 && OFF_RAW % 128 == 0 && kSmemBytes <= 227 * 1024, "shared memory");
 
 struct Bars {
@@ -79,8 +81,8 @@ struct Bars {
     __device__ uint32_t raw_empty(int s) const { return at(kRawSlots + s); }
     __device__ uint32_t ab_full(int s) const { return at(2 * kRawSlots + s); }
     __device__ uint32_t ab_empty(int s) const { return at(2 * kRawSlots + kStages + s); }
-    __device__ uint32_t acc_full(int half, int s) const { return at(2 * kRawSlots + 2 * kStages + half * kAcc + s); }
-    __device__ uint32_t drain(int half) const { return acc_full(2, half); }
+    __device__ uint32_t acc_full(int s) const { return at(2 * kRawSlots + 2 * kStages + s); }
+    __device__ uint32_t drain(int s) const { return acc_full(kAcc + s); }
 };
 
 // ---------------------------------------------------------------------------
@@ -90,54 +92,56 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 __device__ __forceinline__ void tc_commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// 32 columns of the thread's own lane (warp w has lanes 32 (w % 4) and on).  Valid after tc_wait_ld; tc_regs32 keeps their uses
-// behind it.  This shape gives 3.3 registers a cycle and scheduler; 16x256b, which spreads a row over eight lanes, one.
-__device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t *r)
+// One block's MMAs and commits, by one lane of a warp that goes on together, in a row without branches: next to other roles' code a
+// branch costs some 100 cycles.  a, b: codes (the second MMA's are 32 bytes on); sa, sb: scales; `live` false: the commit to
+// `full` alone.
+__device__ __forceinline__ void tc_block(uint32_t d, uint64_t a, uint64_t b, uint64_t sa, uint64_t sb, uint32_t idesc, bool live,
+                                         uint32_t empty, uint32_t full)
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
-        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "{\n\t.reg .pred one, go, no, yes;\n\t"
+        "elect.sync _|one, 0xffffffff;\n\t"
+        "setp.ne.and.b32 go, %9, 0, one;\n\t"
+        "setp.ne.b32 no, 0, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
+        "@go tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %3, %8, no;\n\t"
+        "@go tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %5, %8, yes;\n\t"
+        "@go tcgen05.mma.cta_group::1.kind::f16 [%1], %6, %7, %8, no;\n\t"
+        "@go tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%10];\n\t"
+        "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%11];\n\t}" ::"r"(d),
+        "r"(d + BN), "l"(a), "l"(b), "l"(a + 2), "l"(b + 2), "l"(sa), "l"(sb), "r"(idesc), "r"(static_cast<uint32_t>(live)),
+        "r"(empty), "r"(full)
+        : "memory");
+}
+
+// 16 columns of the thread's own lane (warp w has lanes 32 (w % 4) and on).  Valid after tc_wait_ld; tc_regs16 keeps their uses
+// behind it.  This shape gives 3.3 registers a cycle and scheduler; 16x256b, which spreads a row over eight lanes, one.
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
 
-__device__ __forceinline__ void tc_regs32(uint32_t *r)
+__device__ __forceinline__ void tc_regs16(uint32_t *r)
 {
-#pragma unroll
-    for (int i = 0; i < 32; i += 16)
-        asm volatile(""
-                     : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]),
-                       "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]), "+r"(r[i + 12]),
-                       "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]));
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
-// The arithmetic behind 16 pairs is done before any later volatile statement: their operands' registers are free for the next load.
-__device__ __forceinline__ void order16(float2 *a)
+// The arithmetic behind 8 pairs is done before any later volatile statement: their operands' registers are free for the next load.
+__device__ __forceinline__ void order8(float2 *a)
 {
-#pragma unroll
-    for (int i = 0; i < 16; i += 8)
-        asm volatile(""
-                     : "+f"(a[i].x), "+f"(a[i].y), "+f"(a[i + 1].x), "+f"(a[i + 1].y), "+f"(a[i + 2].x), "+f"(a[i + 2].y),
-                       "+f"(a[i + 3].x), "+f"(a[i + 3].y), "+f"(a[i + 4].x), "+f"(a[i + 4].y), "+f"(a[i + 5].x), "+f"(a[i + 5].y),
-                       "+f"(a[i + 6].x), "+f"(a[i + 6].y), "+f"(a[i + 7].x), "+f"(a[i + 7].y));
+    asm volatile(""
+                 : "+f"(a[0].x), "+f"(a[0].y), "+f"(a[1].x), "+f"(a[1].y), "+f"(a[2].x), "+f"(a[2].y), "+f"(a[3].x), "+f"(a[3].y),
+                   "+f"(a[4].x), "+f"(a[4].y), "+f"(a[5].x), "+f"(a[5].y), "+f"(a[6].x), "+f"(a[6].y), "+f"(a[7].x), "+f"(a[7].y));
 }
 
 // K-major operand, 128-byte swizzle: rows of 128 bytes in 1024-byte atoms of 8 rows.
@@ -155,7 +159,7 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr, uint32_t zeros)
 }
 
 // D f32, A and B f16, K-major, M = 128, N = columns.
-__device__ __forceinline__ uint32_t mma_desc(int columns)
+__device__ __forceinline__ constexpr uint32_t mma_desc(int columns)
 {
     return (1u << 4) | (static_cast<uint32_t>(columns >> 3) << 17) | (static_cast<uint32_t>(BM >> 4) << 24);
 }
@@ -241,14 +245,14 @@ __device__ __forceinline__ void wait_acc(uint32_t bar, uint32_t parity, volatile
 // for a wait where an mbarrier takes 100 and its arrival as long again (3325 tokens, 8 of 64 experts of 2 x 1280 x 3584: 1370 us, with
 // mbarriers 1650).  Both sides pass each barrier once per block, in step: a warp arrives for block b + kAcc only behind its
 // commit, which the issuer makes behind the barrier of block b.
-constexpr int kHandOver = 2;  // barriers 2 .. 5
-__device__ __forceinline__ void acc_release(int half, int buf)
+constexpr int kHandOver = 2;  // barriers 2 and 3
+__device__ __forceinline__ void acc_release(int buf)
 {
-    asm volatile("bar.arrive %0, %1;" ::"r"(kHandOver + half * kAcc + buf), "n"(kEpiThreads / 2 + 32) : "memory");
+    asm volatile("bar.arrive %0, %1;" ::"r"(kHandOver + buf), "n"(kEpiThreads + 32) : "memory");
 }
-__device__ __forceinline__ void acc_acquire(int half, int buf)
+__device__ __forceinline__ void acc_acquire(int buf)
 {
-    asm volatile("bar.sync %0, %1;" ::"r"(kHandOver + half * kAcc + buf), "n"(kEpiThreads / 2 + 32) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(kHandOver + buf), "n"(kEpiThreads + 32) : "memory");
 }
 
 // Wait for copies or MMAs in flight before the CTA exits, whatever the abort flag says; bounded, counted from t0.
@@ -297,7 +301,7 @@ __device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.
 struct Tile {
     int e, nt;          // expert, weight tile
     int row0, rows;     // sorted rows
-    int groups;         // of 64 columns
+    int groups;         // of 16 columns
 };
 
 __device__ __forceinline__ int groups_of(int rows) { return (rows + kGroup - 1) / kGroup; }
@@ -345,12 +349,15 @@ __device__ __forceinline__ int tile_row(int nt, int r)
     return kPair ? 64 * nt + 32 * (r >> 6) + (r & 31) : BM * nt + r;
 }
 
-// v[i] of all lanes joined into lane i: each step halves the columns that a lane still has and doubles the lanes they stand for.
+// v[i] of all lanes joined into lanes i and i + 16: after a first step that joins the halves of a warp, each halves the columns
+// that a lane still has and doubles the lanes they stand for.
 template <typename T, typename F>
-__device__ __forceinline__ T lane_columns(T (&v)[32], int lane, F join)
+__device__ __forceinline__ T lane_columns(T (&v)[16], int lane, F join)
 {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
+    for (int i = 0; i < 16; ++i) v[i] = join(v[i], __shfl_xor_sync(Q8_FULL_MASK, v[i], 16));
+#pragma unroll
+    for (int o = 8; o; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -359,6 +366,48 @@ __device__ __forceinline__ T lane_columns(T (&v)[32], int lane, F join)
         }
     }
     return v[0];
+}
+
+// An MMA issuer: the blocks that go to one buffer of accumulators.  An MMA takes its operands from uniform registers; where the
+// compiler sees that all lanes have the same (constants, the loops' bounds by a reduction), it computes them there.
+template <int kBuf>
+__device__ __forceinline__ void issue(const q8::ExpertsArgs &a, const int *cum, const int4 *table, int weight_tiles, int tiles,
+                                      const Bars &B, uint32_t base, volatile int *abort_flag)
+{
+    const int lane = threadIdx.x & 31, nb = a.nb;
+    constexpr uint32_t d = kBuf * kTmemBuf;           // all of tensor memory is this CTA's: from 0 on
+    uint32_t blk = 0, done = 0, slot = 0, phase = 0;  // blocks, and this buffer's; stage and its phase
+    bool live = true;
+    const int n = __reduce_max_sync(Q8_FULL_MASK, tiles);
+    for (int i = 0; i < n; ++i) {
+        const uint32_t idesc = mma_desc(kGroup * __reduce_max_sync(Q8_FULL_MASK, tile_of(a, cum, table, weight_tiles, i).groups));
+        const int u = (kBuf ^ blk) & 1;  // blocks take the buffers in turn: of a stage this one's
+        for (int j = 0; j < nb; j += 2) {
+            const uint32_t stage = base + slot * kStageBytes;
+            const uint64_t pa = smem_desc(stage) + 4 * u, pb = smem_desc(stage + OFF_B) + 4 * u;
+            // the next block's columns 8 .. 15 lie that much nearer
+            constexpr uint64_t next = (kScBytes >> 4) - (static_cast<uint64_t>(kScBytes >> 4) << 16);
+            const uint64_t sa = scale_desc(stage + OFF_DW, base + OFF_ZERO) + u * next;
+            const uint64_t sb = scale_desc(stage + OFF_DA, base + OFF_ZERO) + u * next;
+            wait_live(live, B.ab_full(slot), phase, abort_flag);
+            if (j + u < nb) {
+                if (done) acc_acquire(kBuf);
+                tc_fence_after();
+                tc_block(d, pa, pb, sa, sb, idesc, live, B.ab_empty(slot), B.acc_full(kBuf));
+                ++done;
+            } else if (lane == 0 && live) {
+                arrive(B.ab_empty(slot));
+            }
+            __syncwarp();
+            if (++slot == kStages) slot = 0, phase ^= 1u;
+        }
+        blk += nb;
+    }
+    // every MMA must have completed before its operands and TMEM go
+    if (elect_one()) tc_commit(B.drain(kBuf));
+    __syncwarp();
+    if (done) acc_acquire(kBuf);  // the last block's
+    drain_bar(B.drain(kBuf), 0, q8::globaltimer_ns());
 }
 
 // kPair: w and w2, the plane of silu(w x) * (w2 x); else w and f32 rows.  kTma: nb % 8 == 0.
@@ -389,9 +438,9 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
         init(kRawSlots, kTma ? 1 : 4);  // raw_full: copied bytes, of each warp where the widening warps copy
         init(kRawSlots, 4);             // raw_empty: a warp each
         init(kStages, 6);             // ab_full: four widening warps, the copied bytes, their scales
-        init(kStages, 2);             // ab_empty: tcgen05.commit of both issuers
-        init(2 * kAcc, 1);            // acc_full: tcgen05.commit
-        init(2, 1);                   // drain
+        init(kStages, kAcc);          // ab_empty: tcgen05.commit of the issuers
+        init(kAcc, 1);                // acc_full: tcgen05.commit
+        init(kAcc, 1);                // drain
         q8::fence_mbar_init();
     }
     if (warp == 0) {
@@ -452,55 +501,12 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
 
     const int nb = a.nb, stages = (nb + 1) / 2, pieces = (nb + kPiece - 1) / kPiece;
 
-    if (warp < 4) {
+    if (warp < kWidenWarp) {
         setmaxnreg_dec<kRegsCtl>();
-        if (warp < 2) {
-            // ------------------------------------------------------------ MMA issuers
-            const int half = warp;
-            const uint32_t idesc = mma_desc(kGroup);
-            uint32_t blk = 0, slot = 0, phase = 0;  // blocks done, stage and its phase
-            bool live = true;
-            for (int i = 0; i < tiles; ++i) {
-                const bool mine = half < tile_of(a, cum, table, weight_tiles, i).groups;
-                for (int j = 0; j < nb; j += 2) {
-                    const uint32_t stage = base + slot * kStageBytes;
-                    const uint64_t pa = smem_desc(stage), pb = smem_desc(stage + OFF_B + half * (kBBytes / 2));
-                    const uint64_t sa = scale_desc(stage + OFF_DW, base + OFF_ZERO);
-                    const uint64_t sb = scale_desc(stage + OFF_DA + half * (kScBytes / 2), base + OFF_ZERO);
-                    wait_live(live, B.ab_full(slot), phase, abort_flag);
-                    if (!mine) {
-                        if (lane == 0 && live) arrive(B.ab_empty(slot));
-                        __syncwarp();
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            if (u == 1 && j + 1 == nb) break;
-                            if (blk >= kAcc) acc_acquire(half, blk % kAcc);
-                            tc_fence_after();
-                            const uint32_t d = tmem + (half * kAcc + blk % kAcc) * kTmemBuf;
-                            // a scale operand's next block: its columns 8 .. 15 lie that much nearer
-                            constexpr uint64_t next = (kScBytes >> 4) - (static_cast<uint64_t>(kScBytes >> 4) << 16);
-                            if (elect_one()) {
-                                if (live) {
-                                    tc_mma_f16(d, pa + 4 * u, pb + 4 * u, idesc, 0);
-                                    tc_mma_f16(d, pa + 4 * u + 2, pb + 4 * u + 2, idesc, 1);  // 32 bytes on
-                                    tc_mma_f16(d + kGroup, sa + u * next, sb + u * next, idesc, 0);
-                                    if (u == 1 || j + 1 == nb) tc_commit(B.ab_empty(slot));
-                                }
-                                tc_commit(B.acc_full(half, blk % kAcc));
-                            }
-                            __syncwarp();
-                            ++blk;
-                        }
-                    }
-                    if (++slot == kStages) slot = 0, phase ^= 1u;
-                }
-            }
-            // every MMA must have completed before its operands and TMEM go
-            if (elect_one()) tc_commit(B.drain(half));
-            __syncwarp();
-            for (int k = 0; k < kAcc && k < static_cast<int>(blk); ++k) acc_acquire(half, k);  // the last blocks'
-            drain_bar(B.drain(half), 0, q8::globaltimer_ns());
+        if (warp == 0) {
+            issue<0>(a, cum, table, weight_tiles, tiles, B, base, abort_flag);
+        } else if (warp == 1) {
+            issue<1>(a, cum, table, weight_tiles, tiles, B, base, abort_flag);
         } else if (warp == 2 && kTma) {
             // ------------------------------------------------------------ weights
             uint32_t n = 0;
@@ -546,16 +552,16 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     uint32_t d[BN / 32][2];
 #pragma unroll
                     for (int i = 0; i < BN / 32; ++i) {
-                        d[i][0] = i < 2 * t.groups ? __ldg(src[i] + 2 * s) : 0u;
-                        d[i][1] = i < 2 * t.groups && two ? __ldg(src[i] + 2 * s + 1) : 0u;
+                        d[i][0] = 32 * i < t.rows ? __ldg(src[i] + 2 * s) : 0u;
+                        d[i][1] = 32 * i < t.rows && two ? __ldg(src[i] + 2 * s + 1) : 0u;
                     }
                     ok = warp_wait(B.ab_empty(slot), ((n / kStages) & 1u) ^ 1u, abort_flag);
                     if (!ok) break;
                     const uint32_t dst = base + slot * kStageBytes + OFF_B;
                     if (elect_one()) {  // rows behind the expert's are the next one's, or stale: their columns are not stored
-                        expect_tx(B.ab_full(slot), t.groups * kGroup * 128);
+                        expect_tx(B.ab_full(slot), (t.rows > kBox ? 2 : 1) * kBox * 128);
                         q8::tma_load_2d(dst, &tmB, 64 * s, t.row0, B.ab_full(slot));
-                        if (t.groups > 1) q8::tma_load_2d(dst + kGroup * 128, &tmB, 64 * s, t.row0 + kGroup, B.ab_full(slot));
+                        if (t.rows > kBox) q8::tma_load_2d(dst + kBox * 128, &tmB, 64 * s, t.row0 + kBox, B.ab_full(slot));
                     }
                     __syncwarp();
                     uint16_t *da = reinterpret_cast<uint16_t *>(sm + slot * kStageBytes + OFF_DA + lane * 16);
@@ -573,10 +579,10 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
             for (uint32_t s = n < kStages ? 0 : n - kStages; s < n; ++s) drain_bar(B.ab_full(s % kStages), (s / kStages) & 1u, t0);
             if (bad) atomicOr(&g_tiles_err, q8::kErrData);
         }
-    } else if (warp < 8) {
+    } else if (warp < kEpiWarp) {
         setmaxnreg_dec<kRegsWiden>();
         // ---------------------------------------------------------------- widen weights: a row a thread
-        const int r = tid - 128;
+        const int r = tid - 32 * kWidenWarp;
         const int sw = r & 7;
         uint32_t n = 0, p = 0;  // stages and pieces done
         bool ok = true;
@@ -691,88 +697,82 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
     } else {
         setmaxnreg_inc<kRegsEpi>();
         // ---------------------------------------------------------------- epilogue
-        const int q = warp & 3, h = (warp - 8) >> 2;  // lanes 32 q .., columns 64 h ..
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + h * (kAcc * kTmemBuf);
+        const int q = warp & 3, col = 32 * ((warp - kEpiWarp) >> 2);  // lanes 32 q .., columns col ..
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + col;
         uint32_t blk = 0;
         for (int at = 0; at < tiles; ++at) {
             const Tile t = tile_of(a, cum, table, weight_tiles, at);
-            const bool mine = h < t.groups;
-            float2 acc[32];  // columns 64 h + 2 i, + 1 of position 32 q + lane
+            const bool mine = col < t.rows;
+            float2 acc[16];  // columns col + 2 i, + 1 of position 32 q + lane
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
-            if (mine) {
-                // 32 columns at a time: the next ones' loads are in flight while these are added up, and a block's buffer is
-                // handed back when its second half has landed
-                uint32_t p[2][32], c[2][32];
-                auto load = [&](int x) {
-                    const uint32_t buf = taddr + (blk % kAcc) * kTmemBuf + 32 * x;
-                    tc_ld32(buf, p[x]);
-                    tc_ld32(buf + kGroup, c[x]);
-                };
-                auto add = [&](int x) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        acc[16 * x + i] =
-                            __ffma2_rn(make_float2(__uint_as_float(c[x][2 * i]), __uint_as_float(c[x][2 * i + 1])),
-                                       make_float2(__uint_as_float(p[x][2 * i]), __uint_as_float(p[x][2 * i + 1])), acc[16 * x + i]);
-                    order16(acc + 16 * x);
-                };
-                wait_acc(B.acc_full(h, blk % kAcc), (blk / kAcc) & 1u, abort_flag);
-                __syncwarp();
-                tc_fence_after();
-                load(0);
+            for (int i = 0; i < 16; ++i) acc[i] = make_float2(0.0f, 0.0f);
+            if (!mine) {  // in step with the others
+                for (int j = 0; j < nb; ++j, ++blk) {
+                    wait_acc(B.acc_full(blk % kAcc), (blk / kAcc) & 1u, abort_flag);
+                    __syncwarp();
+                    acc_release(blk % kAcc);
+                }
+            } else {
 #pragma unroll 1
                 for (int j = 0; j < nb; ++j) {
-                    tc_wait_ld();
-                    tc_regs32(p[0]), tc_regs32(c[0]);
-                    load(1);
-                    add(0);
-                    tc_wait_ld();
-                    tc_regs32(p[1]), tc_regs32(c[1]);
-                    tc_fence_before();
-                    acc_release(h, blk % kAcc);
-                    ++blk;
-                    if (j + 1 < nb) {
-                        wait_acc(B.acc_full(h, blk % kAcc), (blk / kAcc) & 1u, abort_flag);
-                        __syncwarp();
-                        tc_fence_after();
-                        load(0);
+                    const uint32_t buf = taddr + (blk % kAcc) * kTmemBuf;
+                    wait_acc(B.acc_full(blk % kAcc), (blk / kAcc) & 1u, abort_flag);
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {  // 16 columns at a time: four warps a scheduler hide each other's loads
+                        uint32_t p[16], c[16];
+                        tc_ld16(buf + 16 * x, p);
+                        tc_ld16(buf + BN + 16 * x, c);
+                        tc_wait_ld();
+                        tc_regs16(p), tc_regs16(c);
+                        if (x == 1) {
+                            tc_fence_before();
+                            acc_release(blk % kAcc);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            acc[8 * x + i] =
+                                __ffma2_rn(make_float2(__uint_as_float(c[2 * i]), __uint_as_float(c[2 * i + 1])),
+                                           make_float2(__uint_as_float(p[2 * i]), __uint_as_float(p[2 * i + 1])), acc[8 * x + i]);
+                        order8(acc + 8 * x);
                     }
-                    add(1);
+                    ++blk;
                 }
             }
             const bool ok = __all_sync(Q8_FULL_MASK, !*abort_flag);
-            auto valid = [&](int c0) {  // of the 32 columns from c0 on
+            // of the 32 columns from c0 on
+            auto valid = [&](int c0) {
                 return __ballot_sync(Q8_FULL_MASK, c0 + lane < t.rows && q8::source_row(a, t.row0 + c0 + lane) >= 0);
             };
             if (!kPair) {
                 if (!ok || !mine) continue;  // after an abort the tiles are walked, not stored
                 const int row = BM * t.nt + 32 * q + lane;
-                const uint32_t m[2] = {valid(64 * h), valid(64 * h + 32)};
-                float *out = a.out + static_cast<int64_t>(t.row0 + 64 * h) * a.ld + row;
+                const uint32_t m = valid(col);
+                float *out = a.out + static_cast<int64_t>(t.row0 + col) * a.ld + row;
                 if (row < a.n) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if ((m[i >> 4] >> (2 * i & 31)) & 1u) *out = acc[i].x;
+                    for (int i = 0; i < 16; ++i) {
+                        if ((m >> (2 * i)) & 1u) *out = acc[i].x;
                         out += a.ld;
-                        if ((m[i >> 4] >> ((2 * i & 31) + 1)) & 1u) *out = acc[i].y;
+                        if ((m >> (2 * i + 1)) & 1u) *out = acc[i].y;
                         out += a.ld;
                         asm volatile("" : "+l"(out));  // one address after the other: all at once would not fit beside acc
                     }
                 }
             } else {
                 if (epi_any(!ok)) continue;  // all of them, so that none waits for another below
-                // warp q even has 32 gate channels, q odd the same up channels, of 64 columns: even keeps the first 32 columns
+                // warp q even has 32 gate channels, q odd the same up channels, of 32 columns: even keeps the first 16 columns
                 const int up = q & 1;
-                float *box = reinterpret_cast<float *>(sm + OFF_SWAP) + (warp - 8) * 512 + lane;
-                const float *from = reinterpret_cast<float *>(sm + OFF_SWAP) + ((warp - 8) ^ 1) * 512 + lane;
-                float v[32];
+                float *box = reinterpret_cast<float *>(sm + OFF_SWAP) + (warp - kEpiWarp) * 256 + lane;
+                const float *from = reinterpret_cast<float *>(sm + OFF_SWAP) + ((warp - kEpiWarp) ^ 1) * 256 + lane;
+                float v[16];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (mine) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 g = acc[8 * x + i], u = acc[16 + 8 * x + i];  // this and the other half's columns
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 g = acc[4 * x + i], u = acc[8 + 4 * x + i];  // this and the other half's columns
                             box[32 * (2 * i)] = up ? g.x : u.x;
                             box[32 * (2 * i + 1)] = up ? g.y : u.y;
                         }
@@ -780,35 +780,35 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     epi_sync();
                     if (mine) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 g = acc[8 * x + (i >> 1)], u = acc[16 + 8 * x + (i >> 1)];
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 g = acc[4 * x + (i >> 1)], u = acc[8 + 4 * x + (i >> 1)];
                             const float own = up ? (i & 1 ? u.y : u.x) : (i & 1 ? g.y : g.x), other = from[32 * i];
-                            v[16 * x + i] = up ? q8::silu_mul(other, own) : q8::silu_mul(own, other);
+                            v[8 * x + i] = up ? q8::silu_mul(other, own) : q8::silu_mul(own, other);
                         }
                     }
                     if (x == 0) epi_sync();
                 }
                 if (!mine) continue;
-                const int c0 = 64 * h + 32 * up, ch = 64 * t.nt + 32 * (q >> 1);
+                const int c0 = col + 16 * up, ch = 64 * t.nt + 32 * (q >> 1);
                 const uint32_t m = valid(c0);
                 if (ch >= a.n) continue;
-                // lane i gets column c0 + i's largest value (NaN does not count) and encodes its block's scale
-                float top[32];
+                // lanes i and i + 16 get column c0 + i's largest value (NaN does not count) and encode its block's scale
+                float top[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) top[i] = fabsf(v[i]);
+                for (int i = 0; i < 16; ++i) top[i] = fabsf(v[i]);
                 const float d = q8::q8_block_d(fmaxf(lane_columns(top, lane, [](float x, float y) { return fmaxf(x, y); }), 0.0f));
                 const float di = q8::q8_block_di(d);
-                int code[32];
+                int code[16];
                 int8_t *out = qs_out + static_cast<int64_t>(t.row0 + c0) * a.n + ch + lane;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
+                for (int i = 0; i < 16; ++i) {
                     code[i] = q8::q8_code(v[i], __shfl_sync(Q8_FULL_MASK, di, i));
                     if ((m >> i) & 1u) *out = static_cast<int8_t>(code[i]);
                     out += a.n;
                     asm volatile("" : "+l"(out));
                 }
                 const int sum = lane_columns(code, lane, [](int x, int y) { return x + y; });
-                if ((m >> lane) & 1u)
+                if (lane < 16 && ((m >> lane) & 1u))
                     ds_out[static_cast<int64_t>(t.row0 + c0 + lane) * (a.n >> 5) + (ch >> 5)] = q8::q8_dsword(d, sum);
             }
         }
@@ -876,7 +876,7 @@ int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out,
                                       CU_TENSOR_MAP_SWIZZLE_NONE))))
         return Q8_ERR_LAUNCH;
     const uint64_t row = static_cast<uint64_t>(a.nb) * 64;  // bytes of f16
-    if (!make_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT16, workspace, row / 2, static_cast<uint64_t>(a.pairs), row, 64, kGroup,
+    if (!make_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT16, workspace, row / 2, static_cast<uint64_t>(a.pairs), row, 64, kBox,
                      CU_TENSOR_MAP_SWIZZLE_128B))
         return Q8_ERR_LAUNCH;
     const int sms = device_sm_count();

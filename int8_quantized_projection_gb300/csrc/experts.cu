@@ -47,9 +47,9 @@ bool sizes_ok(int64_t experts, int64_t n, int64_t k, int64_t plane_rows, int64_t
 }
 
 // Whether the tensor cores' tiles or the stream over the weights take a call: by the rows an expert has on average, all that the
-// host knows.  64 experts of 3584 x 2 x 1280: 30 rows each 308 us streamed, 367 in tiles; 61 rows 559 and 397.  Eight of
-// 3584 x 18944: 32 rows 289 and 314, 63 rows 511 and 332.
-bool many_rows(int64_t experts, int64_t pairs) { return pairs >= 38 * experts; }
+// host knows.  64 experts of 2 x 1280 x 3584: 20 rows each 217 us streamed, 250 in tiles; 30 rows 288 and 256.  Eight of
+// 18944 x 3584: 16 rows 169 and 212, 32 rows 278 and 224.  128 of 3584 x 1440: 22 rows 391 and 455, 31 rows 510 and 463.
+bool many_rows(int64_t experts, int64_t pairs) { return pairs >= 25 * experts; }
 
 int64_t weight_bytes(int64_t experts, int64_t n, int64_t k) { return experts * n * (k / 32) * 34; }
 

@@ -8,8 +8,8 @@
 // and each matrix meets only a few tiles of rows, so a pass that widens all
 // weights first would cost as much as the products.
 //
-//   Tiles.  128 weight rows x 64 or 128 sorted rows of one expert.  An expert's
-//   rows are dealt to ceil(rows / 128) tiles in groups of 64.  All tiles lie on
+//   Tiles.  128 weight rows x 16 .. 128 sorted rows of one expert.  An expert's
+//   rows are dealt to ceil(rows / 128) tiles in steps of 16.  All tiles lie on
 //   one line (expert, weight tile, row tile), which the offsets on the device
 //   make, and CTA c takes tiles c, c + grid, ...: those that run together share
 //   their weights in L2.  A CTA's pipelines run on from tile to tile; only the
@@ -18,8 +18,8 @@
 //   Weights go to shared memory as they are (34-byte blocks, TMA boxes of 32
 //   rows x 8 blocks, or a bulk copy a row where rows of blocks are not 16-byte
 //   aligned), and four warps widen them there, a row a thread.  The activations
-//   are widened once, by a pass that also puts the rows in order, since each
-//   meets all weight tiles of its expert.
+//   are widened once, by a pass that also puts the rows and their scales in order,
+//   since each meets all weight tiles of its expert.
 //   Scales.  d_w(i) * d_a(t) of a block is a product of two vectors: a third MMA
 //   computes it beside the integers, d_w and d_a in the first of its 16 columns
 //   and zeros in the others (a product of two f16 is exact in f32).  So the
@@ -28,14 +28,16 @@
 //   without products of them.
 //   Gate and up: the 128 rows of a tile are 64 rows of each, 32 by 32.  Two
 //   warps swap halves of their columns, then a warp has a block of 32 channels of
-//   32 rows, and writes the plane of silu(gate) * up.
+//   16 rows, and writes the plane of silu(gate) * up.
+//   What bounds it: the round trip of a block between MMAs and epilogue, with two buffers of accumulators (256 columns each,
+//   all of tensor memory).  So each buffer has an issuer of its own, and 16 epilogue warps hold 32 columns each: four a scheduler
+//   hide one another's loads.  3325 tokens of 8 of 64 experts, 2 x 1280 x 3584: 1070 us, 457 TFLOP/s; with one issuer and eight
+//   warps 1430, with two halves of 64 columns that have buffers, issuers and four warps each 1370.
 //
-// Warp roles (512 threads):
-//   warps 0, 1   MMA issuers, 64 columns each (warp 0: tensor memory)
+// Warp roles (768 threads):
+//   warps 0, 1   MMA issuers, a buffer each (warp 0: tensor memory)
 //   warp 2       weight copies, 8 blocks a slot     warp 3   activation copies and scales, 2 blocks a stage
-//   warps 4-7    widen weights                      warps 8-15   epilogue: a TMEM lane quarter and 64 columns each
-// The 64-column halves of a tile have accumulators and hand-overs of their own, two buffers each, so that one half loads from
-// tensor memory while the other adds up.
+//   warps 4-7    widen weights                      warps 8-23   epilogue: a TMEM lane quarter and 32 columns each
 // Every mbarrier wait is bounded; a wait that runs out sets the CTA abort flag
 // and the error word, and all roles drain and exit.
 #include "experts_common.cuh"
@@ -232,8 +234,7 @@ __device__ __forceinline__ void wait_live(bool &live, uint32_t bar, uint32_t par
 // MMAs, after waits that are bounded.  The limit is behind all of those, in time and in tries.
 __device__ __forceinline__ void wait_acc(uint32_t bar, uint32_t parity, volatile int *abort_flag)
 {
-    for (int i = 0; i < 64; ++i)
-        if (try_wait(bar, parity)) return;
+    if (__builtin_expect(try_wait(bar, parity), 1)) return;
     const uint64_t t0 = q8::globaltimer_ns();
     for (uint32_t i = 0; i < (1u << 20) || q8::globaltimer_ns() - t0 <= 2 * (Q8_WAIT_LIMIT_NS + Q8_DRAIN_LIMIT_NS); ++i)
         if (try_wait(bar, parity)) return;
@@ -414,8 +415,8 @@ __device__ __forceinline__ void issue(const q8::ExpertsArgs &a, const int *cum, 
 template <bool kPair, bool kTma>
 __global__ void __launch_bounds__(kThreads, 1)
 experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_constant__ CUtensorMap tmW,
-                     const __grid_constant__ CUtensorMap tmW2, const __grid_constant__ CUtensorMap tmB, int8_t *qs_out,
-                     uint32_t *ds_out)
+                     const __grid_constant__ CUtensorMap tmW2, const __grid_constant__ CUtensorMap tmB,
+                     const uint32_t *__restrict__ scales, int8_t *qs_out, uint32_t *ds_out)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = q8::smem_u32(smem_raw);
@@ -536,25 +537,19 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
         } else if (warp == 3) {
             // ------------------------------------------------------------ activations and their scales: columns lane, lane + 32, ...
             uint32_t n = 0;
-            bool ok = true, bad = false;
+            bool ok = true;
             for (int at = 0; at < tiles && ok; ++at) {
                 const Tile t = tile_of(a, cum, table, weight_tiles, at);
-                const uint32_t *src[BN / 32];
+                const uint32_t *from = scales + static_cast<int64_t>(t.row0 + lane) * stages;
+                uint32_t ahead[BN / 32];  // the next stage's: a load takes half as long as a stage
+                auto load = [&]() {
 #pragma unroll
-                for (int i = 0; i < BN / 32; ++i) {
-                    const int64_t x = q8::source_row(a, t.row0 + min(lane + 32 * i, t.rows - 1));
-                    bad |= x < 0;
-                    src[i] = a.ds + max(x, int64_t(0)) * nb;  // a row out of range: any, it is not stored
-                }
+                    for (int i = 0; i < BN / 32; ++i) ahead[i] = lane + 32 * i < t.rows ? __ldg(from + 32 * i * stages) : 0u;
+                    ++from;
+                };
+                load();
                 for (int s = 0; s < stages; ++s, ++n) {
                     const int slot = n % kStages;
-                    const bool two = 2 * s + 1 < nb;
-                    uint32_t d[BN / 32][2];
-#pragma unroll
-                    for (int i = 0; i < BN / 32; ++i) {
-                        d[i][0] = 32 * i < t.rows ? __ldg(src[i] + 2 * s) : 0u;
-                        d[i][1] = 32 * i < t.rows && two ? __ldg(src[i] + 2 * s + 1) : 0u;
-                    }
                     ok = warp_wait(B.ab_empty(slot), ((n / kStages) & 1u) ^ 1u, abort_flag);
                     if (!ok) break;
                     const uint32_t dst = base + slot * kStageBytes + OFF_B;
@@ -567,9 +562,10 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     uint16_t *da = reinterpret_cast<uint16_t *>(sm + slot * kStageBytes + OFF_DA + lane * 16);
 #pragma unroll
                     for (int i = 0; i < BN / 32; ++i) {
-                        da[256 * i] = static_cast<uint16_t>(d[i][0]);
-                        da[256 * i + kScBytes / 2] = static_cast<uint16_t>(d[i][1]);
+                        da[256 * i] = static_cast<uint16_t>(ahead[i]);
+                        da[256 * i + kScBytes / 2] = static_cast<uint16_t>(ahead[i] >> 16);
                     }
+                    if (s + 1 < stages) load();
                     q8::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) arrive(B.ab_full(slot));
@@ -577,7 +573,6 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
             }
             const uint64_t t0 = q8::globaltimer_ns();
             for (uint32_t s = n < kStages ? 0 : n - kStages; s < n; ++s) drain_bar(B.ab_full(s % kStages), (s / kStages) & 1u, t0);
-            if (bad) atomicOr(&g_tiles_err, q8::kErrData);
         }
     } else if (warp < kEpiWarp) {
         setmaxnreg_dec<kRegsWiden>();
@@ -713,8 +708,11 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     acc_release(blk % kAcc);
                 }
             } else {
-#pragma unroll 1
+// a jump back costs some 130 cycles beside the other roles' code: 3325 tokens 1200 us with one block a round, 1070 with four,
+// 1110 with eight
+#pragma unroll 4
                 for (int j = 0; j < nb; ++j) {
+                    if (!kPair) asm volatile("" : "+r"(blk));  // else the buffers' addresses of all four blocks stay in registers
                     const uint32_t buf = taddr + (blk % kAcc) * kTmemBuf;
                     wait_acc(B.acc_full(blk % kAcc), (blk / kAcc) & 1u, abort_flag);
                     __syncwarp();
@@ -822,17 +820,26 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
     }
 }
 
-// The sorted rows' codes as f16: out [pairs][16 chunks], 16 codes a thread and round.
+// The sorted rows' codes as f16, out [pairs][16 chunks], 16 codes a thread and round; and their scales, two blocks a word.
 __global__ void __launch_bounds__(256)
-experts_sort_plane_kernel(const __grid_constant__ q8::ExpertsArgs a, uint4 *__restrict__ out)
+experts_sort_plane_kernel(const __grid_constant__ q8::ExpertsArgs a, uint4 *__restrict__ out, uint32_t *__restrict__ scales)
 {
     q8::griddep_launch_dependents();
     q8::griddep_wait();
-    const int chunks = 2 * a.nb, lane = threadIdx.x & 31;  // of a row
+    const int chunks = 2 * a.nb, words = (a.nb + 1) / 2, lane = threadIdx.x & 31;  // of a row
     const int rows = min(max(a.offsets[a.experts], 0), a.pairs);
     const int warps = gridDim.x * (blockDim.x / 32);
     for (int r = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
-        const int64_t src = max(q8::source_row(a, r), int64_t(0));  // out of range: any, it is not stored
+        int64_t src = q8::source_row(a, r);
+        if (src < 0) {  // out of range: any, it is not stored
+            src = 0;
+            if (lane == 0) atomicOr(&g_tiles_err, q8::kErrData);
+        }
+        const uint32_t *ds = a.ds + src * a.nb;
+        for (int i = lane; i < words; i += 32) {
+            const uint32_t d0 = __ldg(ds + 2 * i), d1 = 2 * i + 1 < a.nb ? __ldg(ds + 2 * i + 1) : 0u;
+            scales[static_cast<int64_t>(r) * words + i] = __byte_perm(d0, d1, 0x5410);
+        }
         const uint4 *from = reinterpret_cast<const uint4 *>(a.qs) + src * chunks;
         uint4 *to = out + static_cast<int64_t>(r) * 2 * chunks;
 #pragma unroll 4
@@ -850,20 +857,23 @@ experts_sort_plane_kernel(const __grid_constant__ q8::ExpertsArgs a, uint4 *__re
 }
 
 template <bool kPair, bool kTma>
-int launch(const q8::ExpertsArgs &a, const CUtensorMap &mw, const CUtensorMap &mw2, const CUtensorMap &mb, unsigned grid,
+int launch(const q8::ExpertsArgs &a, const CUtensorMap &mw, const CUtensorMap &mw2, const CUtensorMap &mb, const uint32_t *scales, unsigned grid,
            int8_t *qs_out, uint32_t *ds_out, int slot, cudaStream_t s)
 {
     if (!q8::set_max_dynamic_smem(reinterpret_cast<const void *>(experts_tiles_kernel<kPair, kTma>), kSmemBytes, slot))
         return Q8_ERR_LAUNCH;
-    return q8::launch_pdl(experts_tiles_kernel<kPair, kTma>, dim3(grid), dim3(kThreads), kSmemBytes, s, a, mw, mw2, mb, qs_out,
-                          ds_out);
+    return q8::launch_pdl(experts_tiles_kernel<kPair, kTma>, dim3(grid), dim3(kThreads), kSmemBytes, s, a, mw, mw2, mb, scales,
+                          qs_out, ds_out);
 }
 
 } // namespace
 
 namespace q8 {
 
-size_t experts_tiles_workspace(int64_t k, int64_t pairs) { return static_cast<size_t>(pairs) * k * 2; }
+size_t experts_tiles_workspace(int64_t k, int64_t pairs)
+{
+    return static_cast<size_t>(pairs) * k * 2 + static_cast<size_t>(pairs) * ((k / 32 + 1) / 2) * 4;  // codes, scales
+}
 
 int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out, void *workspace, cudaStream_t s)
 {
@@ -879,18 +889,19 @@ int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out,
     if (!make_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT16, workspace, row / 2, static_cast<uint64_t>(a.pairs), row, 64, kBox,
                      CU_TENSOR_MAP_SWIZZLE_128B))
         return Q8_ERR_LAUNCH;
+    uint32_t *scales = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + static_cast<int64_t>(a.pairs) * row);
     const int sms = device_sm_count();
     const int64_t ctas = (a.pairs + 7) / 8, cap = static_cast<int64_t>(sms) * 8;
     const int st = launch_pdl(experts_sort_plane_kernel, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(256), 0, s, a,
-                              static_cast<uint4 *>(workspace));
+                              static_cast<uint4 *>(workspace), scales);
     if (st != Q8_OK) return st;
     const int64_t weight_tiles = pair ? (a.n + 63) / 64 : (a.n + BM - 1) / BM;
     const int64_t most = (a.pairs / BN + (a.experts < a.pairs ? a.experts : a.pairs)) * weight_tiles;
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
-    if (pair) return tma ? launch<true, true>(a, mw, mw2, mb, grid, qs_out, ds_out, 48, s)
-                         : launch<true, false>(a, mw, mw2, mb, grid, qs_out, ds_out, 49, s);
-    return tma ? launch<false, true>(a, mw, mw2, mb, grid, qs_out, ds_out, 50, s)
-               : launch<false, false>(a, mw, mw2, mb, grid, qs_out, ds_out, 51, s);
+    if (pair) return tma ? launch<true, true>(a, mw, mw2, mb, scales, grid, qs_out, ds_out, 48, s)
+                         : launch<true, false>(a, mw, mw2, mb, scales, grid, qs_out, ds_out, 49, s);
+    return tma ? launch<false, true>(a, mw, mw2, mb, scales, grid, qs_out, ds_out, 50, s)
+               : launch<false, false>(a, mw, mw2, mb, scales, grid, qs_out, ds_out, 51, s);
 }
 
 unsigned int *experts_tiles_error_word()

@@ -31,7 +31,7 @@
 //   16 rows, and writes the plane of silu(gate) * up.
 //   What bounds it: the round trip of a block between MMAs and epilogue, with two buffers of accumulators (256 columns each,
 //   all of tensor memory).  So each buffer has an issuer of its own, and 16 epilogue warps hold 32 columns each: four a scheduler
-//   hide one another's loads.  3325 tokens of 8 of 64 experts, 2 x 1280 x 3584: 1070 us, 457 TFLOP/s; with one issuer and eight
+//   hide one another's loads.  3325 tokens of 8 of 64 experts, 2 x 1280 x 3584: 1060 us, 460 TFLOP/s; with one issuer and eight
 //   warps 1430, with two halves of 64 columns that have buffers, issuers and four warps each 1370.
 //
 // Warp roles (768 threads):
@@ -348,25 +348,6 @@ template <bool kPair>
 __device__ __forceinline__ int tile_row(int nt, int r)
 {
     return kPair ? 64 * nt + 32 * (r >> 6) + (r & 31) : BM * nt + r;
-}
-
-// v[i] of all lanes joined into lanes i and i + 16: after a first step that joins the halves of a warp, each halves the columns
-// that a lane still has and doubles the lanes they stand for.
-template <typename T, typename F>
-__device__ __forceinline__ T lane_columns(T (&v)[16], int lane, F join)
-{
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = join(v[i], __shfl_xor_sync(Q8_FULL_MASK, v[i], 16));
-#pragma unroll
-    for (int o = 8; o; o >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int i = 0; i < o; ++i) {
-            const T keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
-            v[i] = join(keep, __shfl_xor_sync(Q8_FULL_MASK, send, o));
-        }
-    }
-    return v[0];
 }
 
 // An MMA issuer: the blocks that go to one buffer of accumulators.  An MMA takes its operands from uniform registers; where the
@@ -791,21 +772,25 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                 const uint32_t m = valid(c0);
                 if (ch >= a.n) continue;
                 // lanes i and i + 16 get column c0 + i's largest value (NaN does not count) and encode its block's scale
-                float top[16];
+                float top = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top[i] = fabsf(v[i]);
-                const float d = q8::q8_block_d(fmaxf(lane_columns(top, lane, [](float x, float y) { return fmaxf(x, y); }), 0.0f));
+                for (int i = 0; i < 16; ++i) {
+                    float x;
+                    asm("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(x) : "f"(v[i]));
+                    if ((lane & 15) == i) top = x;
+                }
+                const float d = q8::q8_block_d(fmaxf(top, 0.0f));
                 const float di = q8::q8_block_di(d);
-                int code[16];
+                int sum = 0;
                 int8_t *out = qs_out + static_cast<int64_t>(t.row0 + c0) * a.n + ch + lane;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    code[i] = q8::q8_code(v[i], __shfl_sync(Q8_FULL_MASK, di, i));
-                    if ((m >> i) & 1u) *out = static_cast<int8_t>(code[i]);
+                    const int code = q8::q8_code(v[i], __shfl_sync(Q8_FULL_MASK, di, i)), all = __reduce_add_sync(Q8_FULL_MASK, code);
+                    if ((lane & 15) == i) sum = all;
+                    if ((m >> i) & 1u) *out = static_cast<int8_t>(code);
                     out += a.n;
                     asm volatile("" : "+l"(out));
                 }
-                const int sum = lane_columns(code, lane, [](int x, int y) { return x + y; });
                 if (lane < 16 && ((m >> lane) & 1u))
                     ds_out[static_cast<int64_t>(t.row0 + c0 + lane) * (a.n >> 5) + (ch >> 5)] = q8::q8_dsword(d, sum);
             }

@@ -692,9 +692,10 @@ Q8_API int q8_kv_accept(const q8_kv_cache *cache, const int32_t *table, int64_t 
  * expert, and by p within one, the pairs are the rows 0 .. offsets[experts] - 1
  * of the products: those of expert e are offsets[e] .. offsets[e + 1] - 1.  All
  * of this is device data, so one captured graph serves steps of any routing.
- * The kernels check each value before it becomes an address: an expert whose
- * offsets are out of order or range has no rows, a row whose pair is out of
- * range is left as it was, and q8_check reports Q8_ERR_DATA.  Workspaces: two
+ * The kernels check each value before it becomes an address, and q8_check
+ * reports Q8_ERR_DATA: an expert whose offsets are out of range or fall has no
+ * rows, and with offsets that fall the rows of the others are undefined; a row
+ * whose pair is out of range is left as it was.  Workspaces: two
  * calls, or two captured graphs, may share one only if they are ordered on one
  * stream; contents are ignored on entry.  Outputs overlap neither inputs nor
  * one another (Q8_ERR_ARG).

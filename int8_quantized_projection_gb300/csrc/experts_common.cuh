@@ -18,6 +18,7 @@ struct ExpertsArgs {
     float *out;
     int64_t plane_rows, ld;
     int experts, n, nb, top_k, pairs;
+    bool many;                // the work's numbers would pass 31 bits if every second expert had all rows
 };
 
 // Many rows an expert, on the tensor cores (experts_tiles.cu): the f32 rows, or with qs_out and w2 the plane of silu(w x) * (w2 x).

@@ -215,14 +215,16 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
     }
     q8::griddep_launch_dependents();
     q8::griddep_wait();
-    {  // cost of the experts before each: two experts a thread
-        int n[2];
+    bool many = false;  // a line that passes 31 bits: possible only where offsets fall, so that experts overlap; nothing is computed
+    {                   // cost of the experts before each: two experts a thread
+        int n[2], falls = 0;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             n[k] = 0;
             if (2 * tid + k < a.x.experts) {
                 const q8::ExpertRows x = q8::expert_rows_of(a.x, 2 * tid + k);
                 if (x.bad && blockIdx.x == 0) atomicOr(&g_rows_err, q8::kErrData);
+                falls |= x.bad;
                 rows[2 * tid + k] = make_int2(x.first, x.count);
                 n[k] = expert_cost<NT>(x.count) * a.slices * a.groups;
             }
@@ -234,14 +236,14 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
             if (lane >= o) v += u;
         }
         if (lane == 31) scan[warp] = v;
-        __syncthreads();
+        many = __syncthreads_or(falls) && a.x.many;
         for (int w = 0; w < warp; ++w) v += scan[w];
         if (2 * tid < a.x.experts) cum[2 * tid + 1] = v - n[1];
         if (2 * tid + 1 < a.x.experts) cum[2 * tid + 2] = v;
         if (tid == 0) cum[0] = 0;
         __syncthreads();
     }
-    const int line = cum[a.x.experts];
+    const int line = many ? 0 : cum[a.x.experts];
     const int end = static_cast<int>(static_cast<int64_t>(line) * (blockIdx.x + 1) / gridDim.x);
     int at = static_cast<int>(static_cast<int64_t>(line) * blockIdx.x / gridDim.x);
     const int n16 = (a.x.n + 15) / 16;
@@ -491,6 +493,7 @@ int experts_rows_launch(const ExpertsArgs &x, float *out, cudaStream_t s)
     a.groups = (x.n + 15) / 16 * (x.w2 ? 2 : 1);
     a.slices = p.slices, a.slice_blocks = p.slice_blocks;
     a.part = static_cast<int64_t>(x.pairs) * x.ld;
+    a.x.many = (x.experts / 2 + 1) * (static_cast<int64_t>(x.pairs) / 8 + 1) * item_cost(8) * a.slices * a.groups > INT32_MAX;
     const bool tma = x.nb % kPiece == 0;
     CUtensorMap mw = {}, mw2 = {};
     const uint64_t rows = static_cast<uint64_t>(x.experts) * x.n, pitch = static_cast<uint64_t>(x.nb) * 34;

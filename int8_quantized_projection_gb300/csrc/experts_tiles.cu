@@ -31,7 +31,7 @@
 //   16 rows, and writes the plane of silu(gate) * up.
 //   What bounds it: the round trip of a block between MMAs and epilogue, with two buffers of accumulators (256 columns each,
 //   all of tensor memory).  So each buffer has an issuer of its own, and 16 epilogue warps hold 32 columns each: four a scheduler
-//   hide one another's loads.  3325 tokens of 8 of 64 experts, 2 x 1280 x 3584: 1060 us, 460 TFLOP/s; with one issuer and eight
+//   hide one another's loads.  3325 tokens of 8 of 64 experts, 2 x 1280 x 3584: 1035 us, 472 TFLOP/s; with one issuer and eight
 //   warps 1430, with two halves of 64 columns that have buffers, issuers and four warps each 1370.
 //
 // Warp roles (768 threads):
@@ -441,14 +441,16 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
     q8::fence_proxy_async_smem();
     q8::griddep_launch_dependents();
     q8::griddep_wait();  // the offsets and the plane come from earlier kernels
-    {                    // row tiles before each expert: two experts a thread
-        int n[2];
+    bool many = false;  // more tiles than 31 bits number: possible only where offsets fall, so that experts overlap
+    {  // row tiles before each expert: two experts a thread
+        int n[2], falls = 0;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             n[k] = 0;
             if (2 * tid + k < a.experts) {
                 const q8::ExpertRows x = q8::expert_rows_of(a, 2 * tid + k);
                 if (x.bad && blockIdx.x == 0) atomicOr(&g_tiles_err, q8::kErrData);
+                falls |= x.bad;
                 n[k] = row_tiles_of(x.count);
             }
         }
@@ -459,17 +461,15 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
             if (lane >= o) v += u;
         }
         if (lane == 31) scan[warp] = v;
-        __syncthreads();
-        int before = 0;
-        for (int w = 0; w < warp; ++w) before += scan[w];
-        v += before;
+        many = __syncthreads_or(falls) && a.many;
+        for (int w = 0; w < warp; ++w) v += scan[w];
         if (2 * tid < a.experts) cum[2 * tid + 1] = v - n[1];
         if (2 * tid + 1 < a.experts) cum[2 * tid + 2] = v;
         if (tid == 0) cum[0] = 0;
     }
     __syncthreads();
     const int weight_tiles = kPair ? (a.n + 63) / 64 : (a.n + BM - 1) / BM;
-    const int total = cum[a.experts] * weight_tiles;  // below 2^31: y would not fit otherwise
+    const int total = many ? 0 : cum[a.experts] * weight_tiles;  // else below 2^31: y would not fit otherwise
     const int tiles = (total - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
     int4 *table = reinterpret_cast<int4 *>(sm + OFF_TABLE);
     if (tid < kTable && tid < tiles) {
@@ -604,7 +604,7 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                 ok = warp_wait(B.raw_full(slot), (p / kRawSlots) & 1u, abort_flag);
                 if (!ok) break;
                 const int cb = min(kPiece, nb - s * kPiece);
-#pragma unroll
+#pragma unroll (kTma ? kPiece / 2 : 1)  // unrolled only where words of the piece are named at compile time
                 for (int k = 0; k < kPiece / 2; ++k) {
                     if (!kTma && 2 * k >= cb) break;
                     const int st = n % kStages;
@@ -860,8 +860,9 @@ size_t experts_tiles_workspace(int64_t k, int64_t pairs)
     return static_cast<size_t>(pairs) * k * 2 + static_cast<size_t>(pairs) * ((k / 32 + 1) / 2) * 4;  // codes, scales
 }
 
-int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out, void *workspace, cudaStream_t s)
+int experts_tiles_launch(const ExpertsArgs &args, int8_t *qs_out, uint32_t *ds_out, void *workspace, cudaStream_t s)
 {
+    ExpertsArgs a = args;
     const bool pair = a.w2 != nullptr, tma = a.nb % kPiece == 0;
     CUtensorMap mw = {}, mw2 = {}, mb = {};
     const uint64_t wrows = static_cast<uint64_t>(a.experts) * a.n, pitch = static_cast<uint64_t>(a.nb) * 34;
@@ -881,6 +882,7 @@ int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out,
                               static_cast<uint4 *>(workspace), scales);
     if (st != Q8_OK) return st;
     const int64_t weight_tiles = pair ? (a.n + 63) / 64 : (a.n + BM - 1) / BM;
+    a.many = (a.experts / 2 + 1) * (static_cast<int64_t>(a.pairs) / BN + 1) * weight_tiles > INT32_MAX;
     const int64_t most = (a.pairs / BN + (a.experts < a.pairs ? a.experts : a.pairs)) * weight_tiles;
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
     if (pair) return tma ? launch<true, true>(a, mw, mw2, mb, scales, grid, qs_out, ds_out, 48, s)

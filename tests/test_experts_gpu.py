@@ -113,6 +113,46 @@ def test_bad_offsets_and_rows(q8, tokens):
     assert np.all(np.abs(got[keep] - want[keep]) <= lim[keep])
 
 
+def test_offsets_that_overlap_without_end(q8):
+    """Every second expert claims all rows: more items of the stream's line than 31 bits number.  Nothing is computed."""
+    import torch
+
+    experts, n, pairs = 1024, 32768, 25000
+    w = torch.zeros(experts * n * 34, dtype=torch.uint8, device="cuda")
+    qs, ds = q8.empty_plane(pairs, 32)
+    qs.zero_(), ds.zero_()
+    offsets = torch.zeros(experts + 1, dtype=torch.int32, device="cuda")
+    offsets[1::2] = pairs
+    y = torch.full((pairs, n), float("nan"), device="cuda")
+    q8.q8_0_experts_gemm(w, experts, n, 32, qs, ds, offsets, y)
+    with pytest.raises(q8.Q8Error, match="DATA"):
+        q8.q8_check()
+    assert y.isnan().all()
+
+
+@pytest.mark.parametrize("k,rows", [(10240, 3), (10272, 3), (10240, 40), (10272, 40)])
+def test_weights_past_32_bits(q8, k, rows):
+    """The last of 96 experts starts 5.3 GB into the blocks and is the only one with rows (with 40 an expert on average: tiles)."""
+    import torch
+
+    experts, n, pairs = 96, 5120, 96 * rows
+    blob, w = ref.weights_of(np.random.default_rng(3), 1, n, k)
+    wd = torch.zeros(experts * n * (k // 32) * 34, dtype=torch.uint8, device="cuda")
+    wd[-blob.size:] = torch.from_numpy(blob).cuda()
+    qs, ds, x = ref.plane_of(np.random.default_rng(4), 5, k)
+    source = np.arange(9) % 5
+    rows_ = np.full(pairs, -1, np.int64)
+    rows_[:9] = source
+    offsets = np.zeros(experts + 1, np.int64)
+    offsets[-1] = 9
+    dq, dd, do, dr = cuda(qs, ds, offsets.astype(np.int32), rows_.astype(np.int32))
+    y = torch.full((pairs, n), float("nan"), device="cuda")
+    q8.q8_0_experts_gemm(wd, experts, n, k, dq, dd, do, y, rows=dr, top_k=1)
+    q8.q8_check()
+    want, lim = ref.product(w, x, np.array([0, 9]), source)
+    assert np.all(np.abs(y[:9].cpu().numpy() - want) <= lim) and y[9:].isnan().all()
+
+
 def test_no_pairs_at_all(q8):
     import torch
 

@@ -153,6 +153,37 @@ def test_weights_past_32_bits(q8, k, rows):
     assert np.all(np.abs(y[:9].cpu().numpy() - want) <= lim) and y[9:].isnan().all()
 
 
+@pytest.mark.parametrize("k", [256, 288])
+@pytest.mark.parametrize("counts", [[0, 1, 15, 16, 17, 31, 33, 63, 64, 65, 0, 112, 113, 127, 128, 129, 143, 145, 255, 256, 257, 0],
+                                    [25], [24], [0, 0, 0, 100], [385, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0]])
+def test_rows_at_the_edges_of_tiles(q8, counts, k):
+    """Every number of rows at which a tile, a step of 16 columns or a copy of 64 rows ends."""
+    import torch
+
+    g = np.random.default_rng(len(counts))
+    experts, n, nf = len(counts), 160, 96
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    total = int(offsets[-1])
+    pairs = total + 3
+    source = g.integers(0, 50, total)
+    rows = np.concatenate([source, [-1, -1, -1]])
+    qs, ds, x = ref.plane_of(g, 50, k)
+    (blob, w), (bg, wg), (bu, wu) = ref.weights_of(g, experts, n, k), ref.weights_of(g, experts, nf, k), ref.weights_of(g, experts, nf, k)
+    dw, dg, du, dq, dd, do, dr = cuda(blob, bg, bu, qs, ds, offsets.astype(np.int32), rows.astype(np.int32))
+    y = torch.full((pairs, n), float("nan"), device="cuda")
+    q8.q8_0_experts_gemm(dw, experts, n, k, dq, dd, do, y, rows=dr, top_k=1)
+    qo = torch.full((pairs, nf), 77, dtype=torch.int8, device="cuda")
+    so = torch.full((pairs, nf // 32), 77, dtype=torch.int32, device="cuda")
+    q8.q8_0_experts_gate_up(dg, du, experts, nf, k, dq, dd, do, qo, so, rows=dr, top_k=1)
+    q8.q8_check()
+    want, lim = ref.product(w, x, offsets, source)
+    got = y.cpu().numpy()
+    assert np.all(np.abs(got[:total] - want) <= lim) and np.isnan(got[total:]).all()
+    v, vlim = ref.swiglu(*ref.product(wg, x, offsets, source), *ref.product(wu, x, offsets, source))
+    ref.check_plane(qo.cpu().numpy(), so.cpu().numpy(), v, vlim)
+    assert (qo[total:] == 77).all() and (so[total:] == 77).all()
+
+
 def test_no_pairs_at_all(q8):
     import torch
 

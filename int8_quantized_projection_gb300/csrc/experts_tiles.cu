@@ -845,7 +845,12 @@ template <bool kPair, bool kTma>
 int launch(const q8::ExpertsArgs &a, const CUtensorMap &mw, const CUtensorMap &mw2, const CUtensorMap &mb, const uint32_t *scales, unsigned grid,
            int8_t *qs_out, uint32_t *ds_out, int slot, cudaStream_t s)
 {
-    if (!q8::set_max_dynamic_smem(reinterpret_cast<const void *>(experts_tiles_kernel<kPair, kTma>), kSmemBytes, slot))
+    // the epilogue's registers come from those that the CTA is launched with: built with fewer, it would wait for them for ever
+    static const bool registers = [] {
+        cudaFuncAttributes f = {};
+        return cudaFuncGetAttributes(&f, experts_tiles_kernel<kPair, kTma>) == cudaSuccess && f.numRegs >= kRegsLaunch;
+    }();
+    if (!registers || !q8::set_max_dynamic_smem(reinterpret_cast<const void *>(experts_tiles_kernel<kPair, kTma>), kSmemBytes, slot))
         return Q8_ERR_LAUNCH;
     return q8::launch_pdl(experts_tiles_kernel<kPair, kTma>, dim3(grid), dim3(kThreads), kSmemBytes, s, a, mw, mw2, mb, scales,
                           qs_out, ds_out);

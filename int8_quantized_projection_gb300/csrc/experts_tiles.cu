@@ -243,9 +243,9 @@ __device__ __forceinline__ void wait_acc(uint32_t bar, uint32_t parity, volatile
 }
 
 // A buffer of tensor memory is handed back by a named barrier: the epilogue warps arrive, the MMA warp waits, some 25 cycles
-// for a wait where an mbarrier takes 100 and its arrival as long again (3325 tokens, 8 of 64 experts of 2 x 1280 x 3584: 1370 us, with
-// mbarriers 1650).  Both sides pass each barrier once per block, in step: a warp arrives for block b + kAcc only behind its
-// commit, which the issuer makes behind the barrier of block b.
+// for a wait where an mbarrier takes 100 and its arrival as long again (3325 tokens, with tiles in two halves of 64 columns: 1370
+// us, by mbarriers 1650).  Both sides pass each barrier once per block, in step: a warp arrives for block b + kAcc only behind
+// its commit, which the issuer makes behind the barrier of block b.
 constexpr int kHandOver = 2;  // barriers 2 and 3
 __device__ __forceinline__ void acc_release(int buf)
 {

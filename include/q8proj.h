@@ -695,7 +695,9 @@ Q8_API int q8_kv_accept(const q8_kv_cache *cache, const int32_t *table, int64_t 
  * The kernels check each value before it becomes an address, and q8_check
  * reports Q8_ERR_DATA: an expert whose offsets are out of range or fall has no
  * rows, and with offsets that fall the rows of the others are undefined; a row
- * whose pair is out of range is left as it was.  Workspaces: two
+ * whose pair is out of range is left as it was.  So are rows that no expert has:
+ * those before offsets[0] too, so that offsets + e0 and the matrices from expert
+ * e0 on run a part of the experts.  Workspaces: two
  * calls, or two captured graphs, may share one only if they are ordered on one
  * stream; contents are ignored on entry.  Outputs overlap neither inputs nor
  * one another (Q8_ERR_ARG).

@@ -6,36 +6,45 @@ namespace {
 
 __device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 
-// gu [slices][pairs][2 nf] (gate, then up; the slices of k are added up in order) -> the plane of silu(gate) * up, rows up to the
-// last expert's end.
+// gu [slices][pairs][2 nf] (gate, then up; the slices of k are added up in order) -> the plane of silu(gate) * up, of the rows
+// that have products.
 __global__ void __launch_bounds__(256)
-experts_swiglu_kernel(const float4 *__restrict__ gu, int slices, int F, const int32_t *__restrict__ offsets, int experts,
-                      int pairs, uint32_t *__restrict__ qs, uint32_t *__restrict__ ds)
+experts_swiglu_kernel(const __grid_constant__ q8::ExpertsArgs a, const float4 *__restrict__ gu, int slices,
+                      uint32_t *__restrict__ qs, uint32_t *__restrict__ ds)
 {
     q8::griddep_launch_dependents();
     q8::griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const int64_t warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-    const int64_t total = static_cast<int64_t>(min(max(offsets[experts], 0), pairs)) * F;
-    for (int64_t base = warp * 32; base < total; base += warps * 32) {
-        const int64_t i = base + lane, r = i / F;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int lane = threadIdx.x & 31, F = a.n / 4, first = a.offsets[0], last = a.offsets[a.experts];
+    const int seen = q8::bad_offsets(a);
+    const int64_t room = static_cast<int64_t>(a.pairs) * F, step = (static_cast<int64_t>(gridDim.x) * blockDim.x) / 32 * 32;
+    int64_t base = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / 32 * 32, total = room;
+    bool known = false, bad = false;
+    do {  // the first round's loads go out with those of the offsets, whatever these say
+        const int64_t i = base + lane;
+        const int r = static_cast<unsigned>(i >> 3) / static_cast<unsigned>(F >> 3);  // below 25 * 1024 rows of 2^17 blocks
+        float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+        int pair = 0;
         if (i < total) {
-            const float4 *p = gu + r * F + i;
-            float4 g = p[0], u = p[F];
+            const float4 *p = gu + static_cast<int64_t>(r) * F + i;
+            g = p[0], u = p[F];
+            if (a.rows) pair = a.rows[r];
             for (int k = 1; k < slices; ++k) {
-                p += static_cast<int64_t>(pairs) * 2 * F;
+                p += 2 * room;
                 g = add4(g, p[0]), u = add4(u, p[F]);
             }
-            o = q8::silu_mul4(g, u);
         }
-        const q8::Q8Enc e = q8::q8_encode8(o);
-        if (i < total) {
+        if (!known) {
+            bad = __syncthreads_or(seen);
+            known = true;
+            if (bad && a.many) return;  // nothing has been computed
+            total = static_cast<int64_t>(min(max(last, 0), a.pairs)) * F;
+        }
+        const q8::Q8Enc e = q8::q8_encode8(q8::silu_mul4(g, u));
+        if (i < total && r >= first && q8::source_ok(a, r, pair) && (!bad || q8::expert_has(a, r))) {
             qs[i] = e.qword;
             if ((lane & 7) == 0) ds[i >> 3] = e.dsword;
         }
-    }
+    } while ((base += step) < total);
 }
 
 bool sizes_ok(int64_t experts, int64_t n, int64_t k, int64_t plane_rows, int64_t top_k, int64_t pairs)
@@ -92,9 +101,10 @@ extern "C" int q8_0_experts_gemm(const void *w, int64_t experts, int64_t n, int6
     for (const q8::Span &p : spans)
         if (!q8::aligned16(p.p)) return Q8_ERR_ALIGN;
     if (!q8::device_is_sm103()) return Q8_ERR_DEVICE;
-    const q8::ExpertsArgs a = args_of(w, nullptr, experts, n, k, qs, ds, plane_rows, offsets, rows, top_k, pairs, y);
+    q8::ExpertsArgs a = args_of(w, nullptr, experts, n, k, qs, ds, plane_rows, offsets, rows, top_k, pairs, y);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (many_rows(experts, pairs)) return q8::experts_tiles_launch(a, nullptr, nullptr, workspace, s);
+    a.many = q8::experts_rows_many(a);
     if (!need) return q8::experts_rows_launch(a, y, s);
     float *part = static_cast<float *>(workspace);
     const int st = q8::experts_rows_launch(a, part, s);
@@ -129,13 +139,13 @@ extern "C" int q8_0_experts_gate_up(const void *w_gate, const void *w_up, int64_
     if (!q8::device_is_sm103()) return Q8_ERR_DEVICE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     float *gu = static_cast<float *>(workspace);
-    const q8::ExpertsArgs a = args_of(w_gate, w_up, experts, nf, k, qs, ds, plane_rows, offsets, rows, top_k, pairs, gu);
+    q8::ExpertsArgs a = args_of(w_gate, w_up, experts, nf, k, qs, ds, plane_rows, offsets, rows, top_k, pairs, gu);
     if (many_rows(experts, pairs)) return q8::experts_tiles_launch(a, qs_out, ds_out, workspace, s);
+    a.many = q8::experts_rows_many(a);
     const int st = q8::experts_rows_launch(a, gu, s);
     if (st != Q8_OK) return st;
     const int64_t ctas = (pairs * nf / 4 + 255) / 256;
     return q8::launch_pdl(experts_swiglu_kernel, dim3(static_cast<unsigned>(ctas < 152 * 8 ? ctas : 152 * 8)), dim3(256), 0, s,
-                          reinterpret_cast<const float4 *>(gu), q8::experts_rows_slices(experts, pairs, k / 32),
-                          static_cast<int>(nf / 4), offsets, static_cast<int>(experts),
-                          static_cast<int>(pairs), reinterpret_cast<uint32_t *>(qs_out), ds_out);
+                          a, reinterpret_cast<const float4 *>(gu), q8::experts_rows_slices(experts, pairs, k / 32),
+                          reinterpret_cast<uint32_t *>(qs_out), ds_out);
 }

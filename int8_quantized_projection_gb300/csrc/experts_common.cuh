@@ -26,8 +26,9 @@ size_t experts_tiles_workspace(int64_t k, int64_t pairs);
 int experts_tiles_launch(const ExpertsArgs &a, int8_t *qs_out, uint32_t *ds_out, void *workspace, cudaStream_t s);
 
 // A few rows an expert (experts_rows.cu): the f32 rows into out, or, where k is cut into several slices, their parts [slices][pairs][ld],
-// which the join adds up into a.out.
+// which the join adds up into a.out.  experts_rows_many: a.many, for all three.
 int experts_rows_slices(int64_t experts, int64_t pairs, int64_t nb);
+bool experts_rows_many(const ExpertsArgs &a);
 int experts_rows_launch(const ExpertsArgs &a, float *out, cudaStream_t s);
 int experts_join_launch(const float *part, int slices, const ExpertsArgs &a, cudaStream_t s);
 
@@ -53,6 +54,37 @@ __device__ __forceinline__ int64_t source_row(const ExpertsArgs &a, int r)
         s = p < 0 ? -1 : p / a.top_k;
     }
     return s < a.plane_rows ? s : -1;
+}
+
+// The same question of sorted row r whose pair is p = rows[r]: whether it is in range.
+__device__ __forceinline__ bool source_ok(const ExpertsArgs &a, int r, int p)
+{
+    return a.rows ? p >= 0 && p < a.plane_rows * a.top_k : r < a.plane_rows;
+}
+
+// The passes behind the stream read its products from a workspace, where rows that it stored nothing for hold anything: those that
+// no expert with right offsets has, and those whose pair is out of range.  While all offsets are right, an expert has every row
+// from offsets[0] to offsets[experts]; the CTA's threads look at all of them once, beside its first loads: this thread's share.
+__device__ __forceinline__ int bad_offsets(const ExpertsArgs &a)
+{
+    int bad = 0;
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) bad |= expert_rows_of(a, e).bad;
+    return bad;
+}
+
+// Where some are not: whether an expert has sorted row r, offsets[0] <= r < offsets[experts].
+__device__ __forceinline__ bool expert_has(const ExpertsArgs &a, int r)
+{
+    int lo = 0, hi = a.experts;  // the last expert that starts at r or before
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.offsets[mid] <= r)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const ExpertRows x = expert_rows_of(a, lo);
+    return !x.bad && r - x.first < x.count;
 }
 
 } // namespace q8

@@ -430,20 +430,41 @@ experts_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ 
             atomicOr(&g_rows_err, q8::kErrTimeout);
 }
 
-// y = sum of the slices' outputs, in order; rows up to the last expert's end.
-__global__ void __launch_bounds__(256)
-experts_join_kernel(const float *__restrict__ part, int slices, int64_t stride, int64_t ld, const int32_t *__restrict__ offsets,
-                    int experts, int pairs, float *__restrict__ y)
+// y = sum of the slices' outputs, in order, of the rows that have products; kJoin columns of a row at a time.
+constexpr int kJoin = 512;
+__global__ void __launch_bounds__(256) experts_join_kernel(const __grid_constant__ q8::ExpertsArgs a, const float *__restrict__ part, int slices)
 {
     q8::griddep_launch_dependents();
     q8::griddep_wait();
-    const int64_t total = static_cast<int64_t>(min(max(offsets[experts], 0), pairs)) * ld;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        float v = part[i];
-        for (int k = 1; k < slices; ++k) v += part[k * stride + i];
-        y[i] = v;
-    }
+    const int64_t stride = a.pairs * a.ld;
+    const int segs = static_cast<int>((a.ld + kJoin - 1) / kJoin), first = a.offsets[0], last = a.offsets[a.experts];
+    const int seen = q8::bad_offsets(a);
+    int at = blockIdx.x, total = a.pairs * segs;  // below 25 * 1024 rows of 2^22 / kJoin
+    bool known = false, bad = false;
+    do {  // the first round's loads go out with those of the offsets, whatever these say
+        const int r = at / segs;
+        const int64_t c0 = (at - r * segs) * kJoin + threadIdx.x, row = r * a.ld;
+        const int pair = at < total && a.rows ? a.rows[r] : 0;
+        float v[kJoin / 256];
+        for (int k = 0; k < slices; ++k) {
+            const float *p = part + k * stride + row + c0;
+#pragma unroll
+            for (int x = 0; x < kJoin / 256; ++x) {
+                const float add = at < total && c0 + 256 * x < a.ld ? p[256 * x] : 0.0f;
+                v[x] = k ? v[x] + add : add;
+            }
+        }
+        if (!known) {
+            bad = __syncthreads_or(seen);
+            known = true;
+            if (bad && a.many) return;  // nothing has been computed
+            total = min(max(last, 0), a.pairs) * segs;
+        }
+        if (at >= total || r < first || !q8::source_ok(a, r, pair) || (bad && !q8::expert_has(a, r))) continue;
+#pragma unroll
+        for (int x = 0; x < kJoin / 256; ++x)
+            if (c0 + 256 * x < a.ld) a.out[row + c0 + 256 * x] = v[x];
+    } while ((at += gridDim.x) < total);
 }
 
 constexpr int kMaxSmem = 227 * 1024 - 1024;
@@ -466,6 +487,8 @@ Plan plan_of(int64_t experts, int64_t pairs, int nb)
     return p;
 }
 
+int groups_of(const q8::ExpertsArgs &x) { return (x.n + 15) / 16 * (x.w2 ? 2 : 1); }
+
 template <bool kTma, int NT>
 int launch(const RowsArgs &a, const CUtensorMap &mw, const CUtensorMap &mw2, int smem, unsigned grid, int slot, cudaStream_t s)
 {
@@ -483,6 +506,12 @@ int experts_rows_slices(int64_t experts, int64_t pairs, int64_t nb)
     return plan_of(experts, pairs, static_cast<int>(nb)).slices;
 }
 
+bool experts_rows_many(const ExpertsArgs &x)
+{
+    const int64_t items = static_cast<int64_t>(experts_rows_slices(x.experts, x.pairs, x.nb)) * groups_of(x);
+    return (x.experts / 2 + 1) * (static_cast<int64_t>(x.pairs) / 8 + 1) * item_cost(8) * items > INT32_MAX;
+}
+
 // out: slices x pairs x ld floats where there are several, else the rows themselves.
 int experts_rows_launch(const ExpertsArgs &x, float *out, cudaStream_t s)
 {
@@ -490,10 +519,9 @@ int experts_rows_launch(const ExpertsArgs &x, float *out, cudaStream_t s)
     RowsArgs a = {};
     a.x = x;
     a.x.out = out;
-    a.groups = (x.n + 15) / 16 * (x.w2 ? 2 : 1);
+    a.groups = groups_of(x);
     a.slices = p.slices, a.slice_blocks = p.slice_blocks;
     a.part = static_cast<int64_t>(x.pairs) * x.ld;
-    a.x.many = (x.experts / 2 + 1) * (static_cast<int64_t>(x.pairs) / 8 + 1) * item_cost(8) * a.slices * a.groups > INT32_MAX;
     const bool tma = x.nb % kPiece == 0;
     CUtensorMap mw = {}, mw2 = {};
     const uint64_t rows = static_cast<uint64_t>(x.experts) * x.n, pitch = static_cast<uint64_t>(x.nb) * 34;
@@ -510,9 +538,8 @@ int experts_rows_launch(const ExpertsArgs &x, float *out, cudaStream_t s)
 
 int experts_join_launch(const float *part, int slices, const ExpertsArgs &x, cudaStream_t s)
 {
-    const int64_t total = static_cast<int64_t>(x.pairs) * x.ld, ctas = (total + 255) / 256, cap = static_cast<int64_t>(device_sm_count()) * 8;
-    return launch_pdl(experts_join_kernel, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(256), 0, s, part, slices, total,
-                      x.ld, x.offsets, x.experts, x.pairs, x.out);
+    const int64_t ctas = x.pairs * ((x.ld + kJoin - 1) / kJoin), cap = static_cast<int64_t>(device_sm_count()) * 8;
+    return launch_pdl(experts_join_kernel, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(256), 0, s, x, part, slices);
 }
 
 unsigned int *experts_rows_error_word()

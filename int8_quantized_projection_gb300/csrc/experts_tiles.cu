@@ -805,16 +805,16 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
     }
 }
 
-// The sorted rows' codes as f16, out [pairs][16 chunks], 16 codes a thread and round; and their scales, two blocks a word.
+// The experts' rows' codes as f16, out [pairs][16 chunks], 16 codes a thread and round; and their scales, two blocks a word.
 __global__ void __launch_bounds__(256)
 experts_sort_plane_kernel(const __grid_constant__ q8::ExpertsArgs a, uint4 *__restrict__ out, uint32_t *__restrict__ scales)
 {
     q8::griddep_launch_dependents();
     q8::griddep_wait();
     const int chunks = 2 * a.nb, words = (a.nb + 1) / 2, lane = threadIdx.x & 31;  // of a row
-    const int rows = min(max(a.offsets[a.experts], 0), a.pairs);
+    const int first = min(max(a.offsets[0], 0), a.pairs), rows = min(max(a.offsets[a.experts], 0), a.pairs);
     const int warps = gridDim.x * (blockDim.x / 32);
-    for (int r = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
+    for (int r = first + blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
         int64_t src = q8::source_row(a, r);
         if (src < 0) {  // out of range: any, it is not stored
             src = 0;

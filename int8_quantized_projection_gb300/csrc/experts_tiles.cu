@@ -771,7 +771,7 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                 const int c0 = col + 16 * up, ch = 64 * t.nt + 32 * (q >> 1);
                 const uint32_t m = valid(c0);
                 if (ch >= a.n) continue;
-                // lanes i and i + 16 get column c0 + i's largest value (NaN does not count) and encode its block's scale
+                // lanes i and i + 16 get column c0 + i's largest value (NaN counts where all are) and encode its block's scale
                 float top = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -779,17 +779,28 @@ experts_tiles_kernel(const __grid_constant__ q8::ExpertsArgs a, const __grid_con
                     asm("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(x) : "f"(v[i]));
                     if ((lane & 15) == i) top = x;
                 }
-                const float d = q8::q8_block_d(fmaxf(top, 0.0f));
+                const float d = q8::q8_block_d(top);
                 const float di = q8::q8_block_di(d);
+                // columns with rows whose scale is subnormal, infinite or NaN
+                const uint32_t odd = __ballot_sync(Q8_FULL_MASK, !q8::block_rounds_by_add(d)) & m & 0xffffu;
                 int sum = 0;
                 int8_t *out = qs_out + static_cast<int64_t>(t.row0 + c0) * a.n + ch + lane;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int code = q8::q8_code(v[i], __shfl_sync(Q8_FULL_MASK, di, i)), all = __reduce_add_sync(Q8_FULL_MASK, code);
+                    const int code = q8::q8_code_bits(v[i], __shfl_sync(Q8_FULL_MASK, di, i)), all = __reduce_add_sync(Q8_FULL_MASK, code);
                     if ((lane & 15) == i) sum = all;
                     if ((m >> i) & 1u) *out = static_cast<int8_t>(code);
                     out += a.n;
                     asm volatile("" : "+l"(out));
+                }
+                if (odd) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int code = q8::q8_code(v[i], __shfl_sync(Q8_FULL_MASK, di, i)), all = __reduce_add_sync(Q8_FULL_MASK, code);
+                        if (!((odd >> i) & 1u)) continue;
+                        if ((lane & 15) == i) sum = all;
+                        out[static_cast<int64_t>(i - 16) * a.n] = static_cast<int8_t>(code);
+                    }
                 }
                 if (lane < 16 && ((m >> lane) & 1u))
                     ds_out[static_cast<int64_t>(t.row0 + c0 + lane) * (a.n >> 5) + (ch >> 5)] = q8::q8_dsword(d, sum);

@@ -362,6 +362,13 @@ __device__ __forceinline__ bool block_rounds_by_add(float d)
     return d == 0.0f || (d >= 1.17549435e-38f && d <= 3.40282347e+38f);
 }
 
+// One value of a block that block_rounds_by_add: its low byte is the code, its low 16 bits add up to the block's ssum (the magic
+// number's are 0).  A NaN beside numbers gives what it gives in q8_encode8.
+__device__ __forceinline__ int q8_code_bits(float v, float di)
+{
+    return static_cast<int>(__float_as_uint(__fadd_rn(__fmaf_rn(v, di, 0.0f), kRoundMagic)));
+}
+
 // 8 adjacent lanes hold one 32-element block, a float4 each.
 __device__ __forceinline__ Q8Enc q8_encode8(float4 v)
 {

@@ -21,8 +21,10 @@ __device__ unsigned int g_route_err;
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kMaxChunk = 1024;            // tokens of a CTA at most
 constexpr int kOneLaunch = 64;             // tokens that one CTA routes by itself (two rounds of its warps; 128 take 13 us, in two launches 7)
-constexpr int kBitBytes = 40 * 1024;       // shared memory of the bit sets
+constexpr int kBitBytes = 35 * 1024;       // shared memory of the bit sets
+constexpr int kPlaceBytes = 4 * (3 * Q8_MAX_EXPERTS + kWarps);  // of the placing kernel's sums
 static_assert(kThreads == Q8_MAX_EXPERTS && kBitBytes >= 4 * Q8_MAX_EXPERTS, "a thread and a word of bits per expert");
+static_assert(kBitBytes + kPlaceBytes <= 48 * 1024, "shared memory of a launch that asks for no more");
 
 struct RouteArgs {
     const float *logits;
@@ -202,6 +204,7 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const __grid_cons
 {
     extern __shared__ uint32_t bits[];
     __shared__ int s_base[Q8_MAX_EXPERTS], s_all[Q8_MAX_EXPERTS], s_before[Q8_MAX_EXPERTS], s_scan[kWarps];
+    static_assert(sizeof s_base + sizeof s_all + sizeof s_before + sizeof s_scan == kPlaceBytes, "counted for kBitBytes");
     q8::griddep_launch_dependents();
     q8::griddep_wait();
     const int e = threadIdx.x, words = (a.chunk + 31) >> 5;

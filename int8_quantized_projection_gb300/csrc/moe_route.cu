@@ -123,10 +123,10 @@ __device__ __forceinline__ int scan_experts(int v, int *s_scan, int &total)
     return v + (warp ? s_scan[warp - 1] : 0);
 }
 
-// The second half: offsets, and each pair of this CTA's tokens [t0, t1) to its place.  `all`: this thread's expert's pairs,
+// The second half: offsets, and each pair of this CTA's `tokens` from t0 on to its place.  `all`: this thread's expert's pairs,
 // `before`: those of them in earlier chunks.  bits: [experts][words], bit t - t0 of an expert set where token t chose it.
-__device__ __forceinline__ void place_pairs(const RouteArgs &a, const uint32_t *bits, int words, int t0, int t1, int all,
-                                            int before, int *s_base, int *s_scan)
+__device__ __forceinline__ void place_pairs(const RouteArgs &a, const uint32_t *bits, int words, int t0, int tokens,
+                                            int all, int before, int *s_base, int *s_scan)
 {
     const int e = threadIdx.x;
     int total;
@@ -139,7 +139,7 @@ __device__ __forceinline__ void place_pairs(const RouteArgs &a, const uint32_t *
         }
     }
     __syncthreads();
-    const int pairs = (t1 - t0) * a.top_k;
+    const int pairs = tokens * a.top_k;
     const int64_t p0 = static_cast<int64_t>(t0) * a.top_k;
     for (int i = threadIdx.x; i < pairs; i += kThreads) {
         const int id = a.ids[p0 + i], t = i / a.top_k;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const __grid_con
     q8::griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int words = (a.chunk + 31) >> 5;
-    const int t0 = blockIdx.x * a.chunk, t1 = min(a.tokens, t0 + a.chunk);
+    const int t0 = blockIdx.x * a.chunk, tokens = min(a.chunk, a.tokens - t0);  // t0 + chunk may pass 31 bits
     int real = a.tokens;
     if (a.valid) {
         real = *a.valid;
@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const __grid_con
     }
     for (int i = threadIdx.x; i < a.experts * words; i += kThreads) bits[i] = 0u;
     __syncthreads();
-    for (int t = t0 + warp; t < t1; t += kWarps) {
+    for (int i = warp; i < tokens; i += kWarps) {
+        const int t = t0 + i;
         int id = -1;
         float weight = 0.0f;
         if (t < real) choose<EPL>(a, t, lane, id, weight);
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const __grid_con
             const int64_t p = static_cast<int64_t>(t) * a.top_k + lane;
             a.ids[p] = id;
             a.weights[p] = weight;
-            if (id >= 0) atomicOr(&bits[id * words + ((t - t0) >> 5)], 1u << ((t - t0) & 31));
+            if (id >= 0) atomicOr(&bits[id * words + (i >> 5)], 1u << (i & 31));
         }
     }
     __syncthreads();
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const __grid_con
     if (e < a.experts)
         for (int w = 0; w < words; ++w) n += __popc(bits[e * words + w]);
     if (kOne)
-        place_pairs(a, bits, words, t0, t1, n, 0, s_base, s_scan);
+        place_pairs(a, bits, words, t0, tokens, n, 0, s_base, s_scan);
     else if (e < a.experts)
         a.counts[static_cast<int64_t>(blockIdx.x) * a.experts + e] = n;
 }
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const __grid_cons
     q8::griddep_launch_dependents();
     q8::griddep_wait();
     const int e = threadIdx.x, words = (a.chunk + 31) >> 5;
-    const int t0 = blockIdx.x * a.chunk, t1 = min(a.tokens, t0 + a.chunk);
+    const int t0 = blockIdx.x * a.chunk, tokens = min(a.chunk, a.tokens - t0);
     for (int i = threadIdx.x; i < a.experts * words; i += kThreads) bits[i] = 0u;
     s_all[e] = s_before[e] = 0;
     __syncthreads();
@@ -225,12 +226,12 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const __grid_cons
         atomicAdd(&s_before[mine], before);
     }
     const int64_t p0 = static_cast<int64_t>(t0) * a.top_k;
-    for (int i = threadIdx.x; i < (t1 - t0) * a.top_k; i += kThreads) {
+    for (int i = threadIdx.x; i < tokens * a.top_k; i += kThreads) {
         const int id = a.ids[p0 + i], t = i / a.top_k;
         if (id >= 0) atomicOr(&bits[id * words + (t >> 5)], 1u << (t & 31));
     }
     __syncthreads();
-    place_pairs(a, bits, words, t0, t1, s_all[e], s_before[e], s_base, s_scan);
+    place_pairs(a, bits, words, t0, tokens, s_all[e], s_before[e], s_base, s_scan);
 }
 
 // Tokens of a CTA: all of them up to kOneLaunch, else an SM's share in whole words of bits, which have to fit kBitBytes.

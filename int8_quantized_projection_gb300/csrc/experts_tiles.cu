@@ -825,7 +825,9 @@ experts_sort_plane_kernel(const __grid_constant__ q8::ExpertsArgs a, uint4 *__re
     const int chunks = 2 * a.nb, words = (a.nb + 1) / 2, lane = threadIdx.x & 31;  // of a row
     const int first = min(max(a.offsets[0], 0), a.pairs), rows = min(max(a.offsets[a.experts], 0), a.pairs);
     const int warps = gridDim.x * (blockDim.x / 32);
-    for (int r = first + blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
+    // in 64 bits: a step behind the last row may pass 31
+    for (int64_t at = static_cast<int64_t>(first) + blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); at < rows; at += warps) {
+        const int r = static_cast<int>(at);
         int64_t src = q8::source_row(a, r);
         if (src < 0) {  // out of range: any, it is not stored
             src = 0;

@@ -372,6 +372,7 @@ __device__ __forceinline__ void issue(const q8::ExpertsArgs &a, const int *cum, 
             const uint64_t sa = scale_desc(stage + OFF_DW, base + OFF_ZERO) + u * next;
             const uint64_t sb = scale_desc(stage + OFF_DA, base + OFF_ZERO) + u * next;
             wait_live(live, B.ab_full(slot), phase, abort_flag);
+            __syncwarp();  // lanes may leave the wait one by one; the barrier below wants the whole warp (1035 -> 1041 us; only there 1046)
             if (j + u < nb) {
                 if (done) acc_acquire(kBuf);
                 tc_fence_after();

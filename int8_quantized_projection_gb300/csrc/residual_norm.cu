@@ -180,6 +180,7 @@ __device__ __forceinline__ float row_sum(float v, float *red, int P)
 {
     v = q8::rms_warp_sum(v);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncwarp();  // the barrier wants whole warps
     rows_sync(P);
     float tot = 0.0f;
     for (int i = 0; i < P >> 5; ++i) tot += red[i];

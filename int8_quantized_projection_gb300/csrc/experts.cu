@@ -58,7 +58,8 @@ bool sizes_ok(int64_t experts, int64_t n, int64_t k, int64_t plane_rows, int64_t
 // Whether the tensor cores' tiles or the stream over the weights take a call: by the rows an expert has on average, all that the
 // host knows.  64 experts of 2 x 1280 x 3584: 20 rows each 217 us streamed, 250 in tiles; 30 rows 288 and 256.  Eight of
 // 18944 x 3584: 16 rows 169 and 212, 32 rows 278 and 224.  128 of 3584 x 1440, whose rows are copied one by one: 22 rows 391
-// and 500, 31 rows 510 and 510.
+// and 500, 31 rows 510 and 510, so that such widths would like the stream a little longer.  The average is that of the capacity:
+// a call whose pairs are mostly padding takes the tiles all the same.
 bool many_rows(int64_t experts, int64_t pairs) { return pairs >= 25 * experts; }
 
 int64_t weight_bytes(int64_t experts, int64_t n, int64_t k) { return experts * n * (k / 32) * 34; }

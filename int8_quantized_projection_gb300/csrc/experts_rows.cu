@@ -151,39 +151,39 @@ __device__ __forceinline__ void unit(const uint8_t *slot, int late, int cb, cons
     const int pitch = kTma ? kPitchTma / 4 : kPitchAny / 4;
     const uint32_t *w0 = reinterpret_cast<const uint32_t *>(slot) + g * pitch, *w1 = w0 + 8 * pitch;
 #pragma unroll
-                for (int j = 0; j < kPiece; ++j) {
-                    if (!kTma && j >= cb) break;
-                    uint32_t q[4];  // words m of rows g and g + 8, then words m + 4
-                    float dw0, dw1;
-                    if (kTma) {
-                        const int w = (34 * j) >> 2;
-                        const uint32_t h0 = w0[w], h1 = w1[w];
-                        if (j & 1) {  // the scale in the upper half, codes in whole words
-                            dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(h0 >> 16)));
-                            dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(h1 >> 16)));
-                            q[0] = w0[w + 1 + m], q[1] = w1[w + 1 + m], q[2] = w0[w + 5 + m], q[3] = w1[w + 5 + m];
-                        } else {
-                            dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(h0 & 0xffffu)));
-                            dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(h1 & 0xffffu)));
-                            q[0] = __byte_perm(w0[w + m], w0[w + m + 1], 0x5432), q[1] = __byte_perm(w1[w + m], w1[w + m + 1], 0x5432);
-                            q[2] = __byte_perm(w0[w + m + 4], w0[w + m + 5], 0x5432);
-                            q[3] = __byte_perm(w1[w + m + 4], w1[w + m + 5], 0x5432);
-                        }
-                    } else {
-                        const int byte = late + 34 * j, w = byte >> 2;
-                        const uint32_t sel = byte & 2 ? 0x7654u : 0x5432u;
-                        const int up = byte & 2 ? 16 : 0;
-                        dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(w0[w] >> up)));
-                        dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(w1[w] >> up)));
-                        q[0] = __byte_perm(w0[w + m], w0[w + m + 1], sel), q[1] = __byte_perm(w1[w + m], w1[w + m + 1], sel);
-                        q[2] = __byte_perm(w0[w + m + 4], w0[w + m + 5], sel), q[3] = __byte_perm(w1[w + m + 4], w1[w + m + 5], sel);
-                    }
-                    uint32_t f0[4], f1[4];
-                    biased_f16(q[0], f0[0], f0[2]);
-                    biased_f16(q[1], f0[1], f0[3]);
-                    biased_f16(q[2], f1[0], f1[2]);
-                    biased_f16(q[3], f1[1], f1[3]);
-            #pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+        if (!kTma && j >= cb) break;
+        uint32_t q[4];  // words m of rows g and g + 8, then words m + 4
+        float dw0, dw1;
+        if (kTma) {
+            const int w = (34 * j) >> 2;
+            const uint32_t h0 = w0[w], h1 = w1[w];
+            if (j & 1) {  // the scale in the upper half, codes in whole words
+                dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(h0 >> 16)));
+                dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(h1 >> 16)));
+                q[0] = w0[w + 1 + m], q[1] = w1[w + 1 + m], q[2] = w0[w + 5 + m], q[3] = w1[w + 5 + m];
+            } else {
+                dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(h0 & 0xffffu)));
+                dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(h1 & 0xffffu)));
+                q[0] = __byte_perm(w0[w + m], w0[w + m + 1], 0x5432), q[1] = __byte_perm(w1[w + m], w1[w + m + 1], 0x5432);
+                q[2] = __byte_perm(w0[w + m + 4], w0[w + m + 5], 0x5432);
+                q[3] = __byte_perm(w1[w + m + 4], w1[w + m + 5], 0x5432);
+            }
+        } else {
+            const int byte = late + 34 * j, w = byte >> 2;
+            const uint32_t sel = byte & 2 ? 0x7654u : 0x5432u;
+            const int up = byte & 2 ? 16 : 0;
+            dw0 = __half2float(__ushort_as_half(static_cast<unsigned short>(w0[w] >> up)));
+            dw1 = __half2float(__ushort_as_half(static_cast<unsigned short>(w1[w] >> up)));
+            q[0] = __byte_perm(w0[w + m], w0[w + m + 1], sel), q[1] = __byte_perm(w1[w + m], w1[w + m + 1], sel);
+            q[2] = __byte_perm(w0[w + m + 4], w0[w + m + 5], sel), q[3] = __byte_perm(w1[w + m + 4], w1[w + m + 5], sel);
+        }
+        uint32_t f0[4], f1[4];
+        biased_f16(q[0], f0[0], f0[2]);
+        biased_f16(q[1], f0[1], f0[3]);
+        biased_f16(q[2], f1[0], f1[2]);
+        biased_f16(q[3], f1[1], f1[3]);
+#pragma unroll
         for (int t = 0; t < T; ++t) {
             const uint4 b = bf[(j * NT + t) * 32];
             const float4 d = sc[(j * NT + t) * 4];

@@ -31,7 +31,7 @@
 //   16 rows, and writes the plane of silu(gate) * up.
 //   What bounds it: the round trip of a block between MMAs and epilogue, with two buffers of accumulators (256 columns each,
 //   all of tensor memory).  So each buffer has an issuer of its own, and 16 epilogue warps hold 32 columns each: four a scheduler
-//   hide one another's loads.  3325 tokens of 8 of 64 experts, 2 x 1280 x 3584: 1035 us, 472 TFLOP/s; with one issuer and eight
+//   hide one another's loads.  3325 tokens of 8 of 64 experts, 2 x 1280 x 3584: 1039 us, 470 TFLOP/s; with one issuer and eight
 //   warps 1430, with two halves of 64 columns that have buffers, issuers and four warps each 1370.
 //
 // Warp roles (768 threads):

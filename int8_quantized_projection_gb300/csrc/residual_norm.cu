@@ -165,11 +165,11 @@ __global__ void __launch_bounds__(512) residual_rmsnorm_kernel(const __grid_cons
 
 // ---------------------------------------------------------------------------
 // Many rows.  A row's inputs (b, top_k expert rows, a gate of its own, x) come one after the other through a ring of shared-memory
-// slots, a bulk copy of d floats each, which a warp of its own keeps full across rows: some 190 KB are in flight on an SM whatever
-// the other warps wait for, where loads into registers leave the memory idle while a row is reduced (3325 rows of 3584 joined from
-// eight: 97 us with four CTAs an SM).  The vectors that all rows share stay in registers.
+// slots, a bulk copy of d floats each, which a warp of its own keeps full across rows: the rings of the CTAs that an SM holds are in
+// flight whatever the other warps wait for, where loads into registers leave the memory idle while a row is reduced (3325 rows of
+// 3584 joined from eight: 97 us with four CTAs an SM).  The vectors that all rows share stay in registers.
 // ---------------------------------------------------------------------------
-constexpr int kNarrow = 512, kStreamMaxD = 8192;  // six slots at the widest
+constexpr int kNarrow = 512, kStreamMaxD = 8192;  // at the widest six slots for joined rows, two for others
 constexpr int kStreamSmem = 200 * 1024;
 constexpr int kMaxSlots = 64;
 
@@ -376,7 +376,9 @@ template <int J>
 int launch_stream(const NormArgs &a, int64_t rows, int P, int slot, cudaStream_t s)
 {
     // several CTAs share an SM, so that one works while another is at its barriers: fewer where a row has many vectors and a deep
-    // ring tells (3325 rows of 3584: eight joined 88 us with two CTAs, 92 with four; none 34.8 and 33.8)
+    // ring tells (3325 rows of 3584: eight joined 88 us with rings for two CTAs, 92 for four; none 34.8 and 33.8).  How many an SM
+    // holds goes by their registers (52, 56 and 96 a thread) too: two of 3584, one above d = 4608, whatever `threads` would
+    // let it have, so that for top_k < 2 half of the shared memory or more stays unused there and at d = 7168 a ring has one slot
     const int threads = a.top_k >= 2 ? 1024 : 2048;
     const int bytes = 16 * a.F, want = threads / (P + 32) < 8 ? threads / (P + 32) : 8;
     const int ctas = want < 1 ? 1 : want, fit = kStreamSmem / ctas / bytes, slots = fit < kMaxSlots ? fit : kMaxSlots;
